@@ -13,9 +13,11 @@
 
 #include "cxa.h"
 #include "internal.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
-// Device-side status word: kernels OR in 1 when a bounded wait expires.
+// Device-side status word: kernels OR in 1 when a bounded wait expires, 2 for a page
+// number outside the pool (paged.cuh).
 static __device__ unsigned int g_cxa_status_word = 0;
 
 struct cxa_cache {
@@ -582,6 +584,7 @@ const char* cxa_strerror(int code) {
     case CXA_ENOTREADY: return "CXA_ENOTREADY: projection cache not populated";
     case CXA_ECUDA: return "CXA_ECUDA: CUDA runtime error";
     case CXA_ETIMEOUT: return "CXA_ETIMEOUT: a kernel's bounded wait expired";
+    case CXA_EPAGE: return "CXA_EPAGE: a page table entry lies outside the pool";
     default: return "unknown cxa status";
   }
 }
@@ -626,13 +629,13 @@ int cxa_device_status(int clear) {
   unsigned int word = 0;
   if ((e = cudaMemcpy(&word, dev.status_word, sizeof(word), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return fail_cuda(e, "cxa_device_status: read");
-  if (word) g_timeouts_seen.fetch_add(1, std::memory_order_acq_rel);
+  if (word & cxa::kStatusTimeout) g_timeouts_seen.fetch_add(1, std::memory_order_acq_rel);
   if (clear) {
     const unsigned int zero = 0;
     if ((e = cudaMemcpy(dev.status_word, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
       return fail_cuda(e, "cxa_device_status: clear");
   }
-  return word ? CXA_ETIMEOUT : CXA_OK;
+  return (word & cxa::kStatusTimeout) ? CXA_ETIMEOUT : (word & cxa::kStatusBadPage) ? CXA_EPAGE : CXA_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,103 @@
+// What the paged self-attention kernels share: the batch of new tokens, the pages of
+// a layer, and the look-up of a key's row (also run on the host by cxa_paged_check).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <string>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace cxa {
+
+constexpr int kMaxRotaryPairs = 64;
+
+// A rotation, passed by value as a kernel parameter. step[i] is the turn of pair i per
+// position in units of 2^-64 turns: position * step modulo 2^64 is the pair's phase with
+// whole turns dropped exactly, so a far position costs no precision (an error of at most
+// |position| * 2^-65 turns), where position * frequency in fp32 would lose it all.
+struct RotaryArg {
+  unsigned long long step[kMaxRotaryPairs];
+  float factor;       // multiplies the rotated values
+  int pairs;          // rotated pairs; 0: no rotation
+  int interleaved;    // pair i is (2i, 2i + 1); otherwise (i, i + pairs)
+};
+
+// The new tokens of a batch, packed: sequence b owns rows q_start[b] .. q_start[b + 1),
+// the last of them at position kv_len[b] - 1. All pointers are device pointers.
+struct PagedBatch {
+  const int* q_start;
+  const int* kv_len;
+  const int* table;      // [B][width] page numbers
+  int B, n_tokens, width;
+};
+
+// One layer of the pool: [num_pages][Hkv][1 << page_shift][dh].
+struct PagedLayer {
+  void* K;
+  void* V;
+  int num_pages, Hkv, page_shift;
+};
+
+struct PagedSeq {
+  int q0, n;     // first row and number of new tokens
+  int kv;        // keys after them
+};
+
+__host__ __device__ inline PagedSeq paged_seq(const int* q_start, const int* kv_len, int b, int n_tokens) {
+  PagedSeq s;
+  const int lo = q_start[b], hi = q_start[b + 1];
+  s.q0 = lo < 0 ? 0 : lo > n_tokens ? n_tokens : lo;
+  const int q1 = hi < 0 ? 0 : hi > n_tokens ? n_tokens : hi;
+  s.n = q1 > s.q0 ? q1 - s.q0 : 0;
+  s.kv = kv_len[b] > 0 ? kv_len[b] : 0;
+  return s;
+}
+
+// The page that holds position t of a sequence, or -1 if t lies outside the table's
+// row or the entry outside the pool.
+__host__ __device__ inline int paged_lookup(const int* table_row, int width, int page_shift, int num_pages, int t) {
+  if (t < 0 || (t >> page_shift) >= width) return -1;
+  const int page = table_row[t >> page_shift];
+  return page >= 0 && page < num_pages ? page : -1;
+}
+
+// Bits of the device status word.
+constexpr unsigned int kStatusTimeout = 1u, kStatusBadPage = 2u;
+
+struct NormRopeLaunch {
+  const void *q, *k, *v;            // k, v may be null; v only with pages
+  long long q_stride, k_stride, v_stride;      // elements from one token's row to the next
+  void *q_out, *k_out;              // k_out unused with pages
+  long long qo_stride, ko_stride;
+  int Hq, Hk, dh, n_tokens;
+  const int* pos;                   // [n_tokens], without pages
+  const float *wq, *wk;             // [dh] or NULL (1)
+  float eps;
+  bool norm;
+  bool act_bf16, pool_bf16;
+  RotaryArg rot;
+  bool append;                      // write k and v into the layer's pages
+  PagedBatch batch;
+  PagedLayer layer;
+};
+
+struct PagedAttnLaunch {
+  const void* q;
+  void* out;
+  long long q_stride, o_stride;     // elements
+  int Hq, dh, max_new;
+  float scale;
+  bool act_bf16, pool_bf16;
+  PagedBatch batch;
+  PagedLayer layer;
+  void* workspace;
+};
+
+cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+size_t paged_rows_workspace_bytes(int dh);
+cudaError_t launch_paged_rows(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+
+}  // namespace cxa

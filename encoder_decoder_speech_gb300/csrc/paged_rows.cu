@@ -1,0 +1,554 @@
+// Attention of new tokens over a paged K/V cache, for few query rows a K/V head: single
+// tokens, proposed tokens, short chunks, and every fp32 call.
+//
+//   out[r] = sum_j p_rj V_j / sum_j p_rj,  p_rj = 2^(s_rj - m_r),
+//   s_rj = scale * log2(e) * q_r . K_j  over the keys j that row r may see,
+//
+// in one pass with the running reference m_r. Bound by memory: K and V are read once for
+// the kRows = 16 query rows of a tile (query heads of one K/V head times new tokens).
+//
+// A warp takes 16 keys a step and multiplies on the tensor cores with m16n8k16 products,
+// whose operands come straight from global memory, 16 bytes a lane, with no staging in
+// shared memory: a product does not care which channel carries which index as long as
+// both operands agree, so lane (g, t) of the K operand takes 16 consecutive bytes of
+// key g and the query operand is laid out to match; for P.V, lane (g, t) takes 16
+// consecutive bytes of keys 2t and 2t + 1 and pairs them up by byte permutes. The K of
+// the next step is under way while a step is computed.
+//
+// Rounding: fp32 values enter the products as sums of three bf16 parts (8 + 8 + 8 bits,
+// by truncation, so exactly), of whose products the six largest are taken: what is left
+// out is below 2^-22 of a term. With bf16 tensors q, K and V are exact as they are and the
+// probabilities keep two parts (16 bits), which leaves the output's own rounding as the
+// only one that shows. Sums, references and accumulators are fp32.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "paged.cuh"
+#include "paged_work.cuh"
+#include "ptx.cuh"
+
+namespace cxa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;            // query rows a tile
+constexpr int kStep = 16;            // keys a warp takes at a time
+constexpr int kChunkShift = 6;       // 64 keys: one step of each warp
+constexpr int kStepsPerChunk = (1 << kChunkShift) / kStep;
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxBlocks = 160 * kBlocksPerSm;
+constexpr float kMoveLog2 = 8.f;     // a row's reference moves only past this margin
+
+struct RowsParams {
+  const void* q;
+  void* out;
+  long long q_stride, o_stride;
+  float qscale;                      // scale * log2(e)
+  unsigned int* counters;            // [grid], zero between calls
+  float* part;                       // [2 * grid][kRows][kDh + 2]
+  unsigned int* status;
+  PagedBatch batch;
+  PagedLayer layer;
+  WorkShape shape;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// The high halves of two words: (lo's, hi's) as a bf16 pair, that is, both truncated.
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+__device__ __forceinline__ uint32_t low_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
+
+// A pair of fp32 values as N bf16 pairs that add up to them (exactly, for N = 3).
+template <int N>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    w[i] = high_halves(ua, ub);
+    a -= __uint_as_float(ua & 0xFFFF0000u);
+    b -= __uint_as_float(ub & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ bool nonfinite(uint32_t w, bool bf16_pair) {
+  if (bf16_pair) return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+  return (w & 0x7F800000u) == 0x7F800000u;
+}
+
+template <typename TQ, typename TP, int kDh>
+struct Shape {
+  static constexpr bool q32 = sizeof(TQ) == 4, p32 = sizeof(TP) == 4;
+  static constexpr int QP = q32 ? 3 : 1;           // bf16 parts of a query value,
+  static constexpr int KP = p32 ? 3 : 1;           // of a K or V value
+  static constexpr int PP = q32 ? 3 : 2;           // and of a probability
+  static constexpr int KS = kDh / 16;              // products along a head
+  static constexpr int NB = kDh / 8;               // accumulator blocks of 8 channels
+  static constexpr int row_bytes = kDh * static_cast<int>(sizeof(TP));
+  static constexpr int KV = row_bytes / 64;        // 16-byte loads of a lane along a K row
+  static constexpr int VV = row_bytes / 128;       // and along a V row
+  static constexpr int PE = kDh + 4;               // floats of a row in the block's merge
+  static constexpr int q_bytes = QP * KS * 32 * 16;
+  static constexpr int merge_bytes = kWarps * kRows * PE * 4 + 2 * kWarps * kRows * 4;
+  static constexpr int smem = q_bytes + merge_bytes;
+};
+
+// B operand of product s along a head from a lane's K loads.
+template <typename S>
+__device__ __forceinline__ void k_operand(const uint4 (&k)[S::KV], int s, uint32_t (&b)[S::KP][2]) {
+  if constexpr (S::p32) {
+    uint32_t w[3];
+    split_pair<3>(__uint_as_float(k[s].x), __uint_as_float(k[s].y), w);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) b[i][0] = w[i];
+    split_pair<3>(__uint_as_float(k[s].z), __uint_as_float(k[s].w), w);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) b[i][1] = w[i];
+  } else {
+    const uint4& u = k[s >> 1];
+    b[0][0] = (s & 1) ? u.z : u.x;
+    b[0][1] = (s & 1) ? u.w : u.y;
+  }
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& u, int i) {
+  return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+}
+
+// B operand of accumulator block c from a lane's V loads of its four keys.
+template <typename S>
+__device__ __forceinline__ void v_operand(const uint4 (&v)[4][S::VV], int c, uint32_t (&b)[S::KP][2]) {
+  if constexpr (S::p32) {
+    const int p = c / 4, e = c % 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w[3];
+      split_pair<3>(__uint_as_float(word(v[2 * j][p], e)), __uint_as_float(word(v[2 * j + 1][p], e)), w);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) b[i][j] = w[i];
+    }
+  } else {
+    const int p = c / 8, e = c % 8;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = word(v[2 * j][p], e / 2), y = word(v[2 * j + 1][p], e / 2);
+      b[0][j] = (e & 1) ? high_halves(x, y) : low_halves(x, y);
+    }
+  }
+}
+
+template <typename TQ, typename TP, int kDh>
+__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ RowsParams p) {
+  using S = Shape<TQ, TP, kDh>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ WorkScratch s_work;
+  __shared__ int s_last;
+  uint4* s_q = reinterpret_cast<uint4*>(smem);                             // [QP][KS][32 lanes]
+  float* s_o = reinterpret_cast<float*>(smem + S::q_bytes);                // [kWarps][kRows][PE]
+  float* s_m = s_o + kWarps * kRows * S::PE;                               // [kWarps][kRows]
+  float* s_l = s_m + kWarps * kRows;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const PagedBatch& bt = p.batch;
+  const int Hkv = p.layer.Hkv, shift = p.layer.page_shift, G = p.shape.G;
+  WorkRange range;
+  WorkCursor cur;
+  if (!work_locate<kThreads>(bt, p.shape, Hkv, &s_work, &range, &cur)) return;
+
+  for (;;) {
+    // ---- the part of the item in this block's range
+    const long long end = min(range.g1, cur.first + cur.nc);
+    const int c0 = cur.c, c1 = static_cast<int>(end - cur.first);
+    const PagedSeq seq = cur.seq;
+    const int row0 = cur.rt * kRows;
+    const int rows = min(kRows, work_rows(seq, p.shape) - row0);
+    const int keys = tile_keys(seq, p.shape, cur.rt);
+
+    // ---- the queries as A operands: lane (g, t) holds rows g and g + 8, channels to match
+    // the K loads
+    for (int i = tid; i < S::KS * 32; i += kThreads) {
+      const int s = i >> 5, ql = i & 31, qg = ql >> 2, qt = ql & 3;
+      const int ch = S::p32 ? 16 * s + 4 * qt : 32 * (s >> 1) + 8 * qt + 4 * (s & 1);
+      uint32_t w[2][2][S::QP];     // [row][pair of channels]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = qg + 8 * r;
+        const bool ok = row < rows;
+        const int tok = (row0 + row) / G, hd = cur.h * G + (row0 + row) % G;
+        const TQ* src = static_cast<const TQ*>(p.q) + (ok ? (seq.q0 + tok) * p.q_stride + hd * kDh + ch : 0);
+        if constexpr (S::q32) {
+          const float4 f = ok ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+          split_pair<S::QP>(f.x, f.y, w[r][0]);
+          split_pair<S::QP>(f.z, f.w, w[r][1]);
+        } else {
+          const uint2 u = ok ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
+          w[r][0][0] = u.x;
+          w[r][1][0] = u.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < S::QP; ++j) s_q[j * S::KS * 32 + i] = make_uint4(w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j]);
+    }
+    // keys that this lane's two rows may see
+    int see[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r;
+      see[r] = row < rows ? visible_keys(seq, (row0 + row) / G, p.shape.cap) : 0;
+    }
+    const int see_all = visible_keys(seq, row0 / G, p.shape.cap);   // keys that every row may see
+    __syncthreads();
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[S::NB][4];
+#pragma unroll
+    for (int c = 0; c < S::NB; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+
+    const int* table_row = bt.table + static_cast<size_t>(cur.b) * bt.width;
+    const uint8_t* Kb = static_cast<const uint8_t*>(p.layer.K);
+    const uint8_t* Vb = static_cast<const uint8_t*>(p.layer.V);
+    const int s1 = min(c1 * kStepsPerChunk, (keys + kStep - 1) / kStep);
+    auto step_page = [&](int s) {
+      if (s >= s1) return 0;
+      const int page = paged_lookup(table_row, bt.width, shift, p.layer.num_pages, s * kStep);
+      if (page < 0 && lane == 0) atomicOr(p.status, kStatusBadPage);
+      return page;
+    };
+    // byte offset of the step's first row in the layer; a step lies in one page
+    auto step_row = [&](int s, int page) {
+      return ((((static_cast<size_t>(page) * Hkv + cur.h) << shift) + ((s * kStep) & ((1 << shift) - 1)))) *
+             S::row_bytes;
+    };
+    auto load_k = [&](int s, int page, uint4 (&k)[2][S::KV]) {
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const bool ok = s < s1 && page >= 0 && s * kStep + 8 * nb + g < keys;
+        const uint8_t* src = Kb + (ok ? step_row(s, page) + (8 * nb + g) * S::row_bytes + t * 16 : 0);
+#pragma unroll
+        for (int v = 0; v < S::KV; ++v)
+          k[nb][v] = ok ? __ldg(reinterpret_cast<const uint4*>(src + v * 64)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    int s = c0 * kStepsPerChunk + warp;
+    int page = step_page(s), page_next = step_page(s + kWarps);
+    uint4 kn[2][S::KV];
+    load_k(s, page, kn);
+    for (; s < s1; s += kWarps) {
+      uint4 k[2][S::KV], v[4][S::VV];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int i = 0; i < S::KV; ++i) k[nb][i] = kn[nb][i];
+      // V of this step, K of the next
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = 8 * (j >> 1) + 2 * t + (j & 1);
+        // a key that no row sees weighs 0, and its V may hold anything: read as 0
+        const bool ok = page >= 0 && s * kStep + key < keys;
+        const uint8_t* src = Vb + (ok ? step_row(s, page) + key * S::row_bytes + g * 16 : 0);
+#pragma unroll
+        for (int i = 0; i < S::VV; ++i)
+          v[j][i] = ok ? __ldg(reinterpret_cast<const uint4*>(src + i * 128)) : make_uint4(0, 0, 0, 0);
+      }
+      const int page_now = page;
+      page = page_next;
+      load_k(s + kWarps, page, kn);
+      page_next = step_page(s + 2 * kWarps);
+      if (page_now < 0) continue;      // a bad page: its keys are left out
+
+      // ---- scores
+      float sc[2][4];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) {
+        uint4 a[S::QP];
+#pragma unroll
+        for (int i = 0; i < S::QP; ++i) a[i] = s_q[(i * S::KS + ks) * 32 + lane];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          uint32_t b[S::KP][2];
+          k_operand<S>(k[nb], ks, b);
+#pragma unroll
+          for (int i = 0; i < S::QP; ++i)
+#pragma unroll
+            for (int j = 0; j < S::KP; ++j)
+              if (i + j <= 2) mma_16816(sc[nb], a[i], b[j][0], b[j][1]);
+        }
+      }
+      const bool masked = s * kStep + kStep > see_all;
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[nb][i] *= p.qscale;
+          if (masked && s * kStep + 8 * nb + 2 * t + (i & 1) >= see[i >> 1]) sc[nb][i] = -INFINITY;
+        }
+
+      // ---- running reference: moved for the whole tile when some row passes the margin
+      bool move = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        move |= fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1])) > m[r] + kMoveLog2;
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mx = fmaxf(mx, m[r]);
+          const float corr = m[r] == -INFINITY ? 0.f : ex2(m[r] - mx);
+          m[r] = mx;
+          l[r] *= corr;
+#pragma unroll
+          for (int c = 0; c < S::NB; ++c) {
+            o[c][2 * r] *= corr;
+            o[c][2 * r + 1] *= corr;
+          }
+        }
+      }
+      uint4 pa[S::PP];
+      {
+        float pr[2][4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ref = m[i >> 1] == -INFINITY ? 0.f : m[i >> 1];   // nothing visible yet
+            pr[nb][i] = ex2(sc[nb][i] - ref);
+            l[i >> 1] += pr[nb][i];
+          }
+        uint32_t w[4][S::PP];
+        split_pair<S::PP>(pr[0][0], pr[0][1], w[0]);
+        split_pair<S::PP>(pr[0][2], pr[0][3], w[1]);
+        split_pair<S::PP>(pr[1][0], pr[1][1], w[2]);
+        split_pair<S::PP>(pr[1][2], pr[1][3], w[3]);
+#pragma unroll
+        for (int i = 0; i < S::PP; ++i) pa[i] = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+      }
+
+      // ---- values. A row's weight for a key it may not see is 0, but 0 * inf is not: if a
+      // masked step holds such a value, each token's rows are taken by themselves.
+      bool wild = false;
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < S::VV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wild |= nonfinite(word(v[j][i], e), !S::p32);
+        wild = __any_sync(0xffffffffu, wild);
+      }
+      if (!wild) {
+#pragma unroll
+        for (int c = 0; c < S::NB; ++c) {
+          uint32_t b[S::KP][2];
+          v_operand<S>(v, c, b);
+#pragma unroll
+          for (int i = 0; i < S::PP; ++i)
+#pragma unroll
+            for (int j = 0; j < S::KP; ++j)
+              if (i + j <= 2) mma_16816(o[c], pa[i], b[j][0], b[j][1]);
+        }
+      } else {
+        for (int tok = row0 / G; tok <= (row0 + rows - 1) / G; ++tok) {
+          const int lim = visible_keys(seq, tok, p.shape.cap);
+          uint4 vm[4][S::VV];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < S::VV; ++i)
+              vm[j][i] = s * kStep + 8 * (j >> 1) + 2 * t + (j & 1) < lim ? v[j][i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < S::NB; ++c) {
+            uint32_t b[S::KP][2];
+            v_operand<S>(vm, c, b);
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < S::PP; ++i)
+#pragma unroll
+              for (int j = 0; j < S::KP; ++j)
+                if (i + j <= 2) mma_16816(d, pa[i], b[j][0], b[j][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((row0 + g + 8 * (i >> 1)) / G == tok) o[c][i] += d[i];
+          }
+        }
+      }
+    }
+
+    // ---- the warps' states become one
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t == 0) {
+        s_m[warp * kRows + g + 8 * r] = m[r];
+        s_l[warp * kRows + g + 8 * r] = l[r];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < S::NB; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 2 * t + (i & 1);     // the block's column: which lanes' 16 bytes
+        const int ch = S::p32 ? 32 * (c / 4) + 4 * n + c % 4 : 64 * (c / 8) + 8 * n + c % 8;
+        s_o[(warp * kRows + g + 8 * (i >> 1)) * S::PE + ch] = o[c][i];
+      }
+    __syncthreads();
+    const bool whole = c0 == 0 && c1 == cur.nc;
+    const long long owner0 = cur.first / range.per;       // blocks that hold a part of the item
+    const int parts = static_cast<int>((cur.first + cur.nc - 1) / range.per - owner0) + 1;
+    float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kRows * (kDh + 2);
+
+    auto write_out = [&](int r, int ch, float4 v, float sum) {
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      const int tok = (row0 + r) / G, hd = cur.h * G + (row0 + r) % G;
+      TQ* dst = static_cast<TQ*>(p.out) + (seq.q0 + tok) * p.o_stride + hd * kDh + ch;
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      if constexpr (S::q32) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {
+        __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+      }
+    };
+    for (int i = tid; i < rows * (kDh / 4); i += kThreads) {
+      const int r = i / (kDh / 4), ch = 4 * (i % (kDh / 4));
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w * kRows + r] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * S::PE + ch);
+        sum += f * s_l[w * kRows + r];
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+      if (whole) {
+        write_out(r, ch, acc, sum);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * kDh + ch) = acc;
+        if (ch == 0) {
+          slot[kRows * kDh + r] = M;
+          slot[kRows * (kDh + 1) + r] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      __syncthreads();      // the partial state is written
+      if (tid == 0) {
+        const unsigned int n = atomic_add_acq_rel_gpu(p.counters + owner0, 1u);
+        s_last = n == static_cast<unsigned int>(parts - 1);
+        if (s_last) p.counters[owner0] = 0u;
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int i = tid; i < rows * (kDh / 4); i += kThreads) {
+          const int r = i / (kDh / 4), ch = 4 * (i % (kDh / 4));
+          float M = -INFINITY, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < parts; ++k) {
+            const float* sl = p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kRows * (kDh + 2);
+            const float mk = __ldcg(sl + kRows * kDh + r), lk = __ldcg(sl + kRows * (kDh + 1) + r);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + r * kDh + ch));
+            const float mn = fmaxf(M, mk), ref = mn == -INFINITY ? 0.f : mn;
+            const float fo = ex2(M - ref), fk = ex2(mk - ref);
+            M = mn;
+            sum = sum * fo + lk * fk;
+            acc.x = acc.x * fo + x.x * fk;
+            acc.y = acc.y * fo + x.y * fk;
+            acc.z = acc.z * fo + x.z * fk;
+            acc.w = acc.w * fo + x.w * fk;
+          }
+          write_out(r, ch, acc, sum);
+        }
+      }
+    }
+    if (end >= range.g1) break;
+    work_next(bt, p.shape, Hkv, &cur);
+    __syncthreads();        // the queries and states of this item are done with
+  }
+}
+
+template <typename TQ, typename TP, int kDh>
+cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr int smem = Shape<TQ, TP, kDh>::smem;
+  cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<TQ, TP, kDh>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  int grid = dev.num_sms * kBlocksPerSm;
+  if (grid > kMaxBlocks) grid = kMaxBlocks;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_rows_kernel<TQ, TP, kDh>, prm);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+template <int kDh>
+cudaError_t launch_dh(const PagedAttnLaunch& a, const RowsParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  using bf = __nv_bfloat16;
+  if (a.act_bf16) return launch<bf, bf, kDh>(a, prm, dev, stream);
+  return a.pool_bf16 ? launch<float, bf, kDh>(a, prm, dev, stream) : launch<float, float, kDh>(a, prm, dev, stream);
+}
+
+constexpr size_t kCounterBytes = (kMaxBlocks * 4 + 255) / 256 * 256;
+
+}  // namespace
+
+size_t paged_rows_workspace_bytes(int dh) {
+  return kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4;
+}
+
+cudaError_t launch_paged_rows(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+  RowsParams prm;
+  prm.q = a.q;
+  prm.out = a.out;
+  prm.q_stride = a.q_stride;
+  prm.o_stride = a.o_stride;
+  prm.qscale = a.scale * 1.4426950408889634f;
+  prm.counters = static_cast<unsigned int*>(a.workspace);
+  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+  prm.status = dev.status_word;
+  prm.batch = a.batch;
+  prm.layer = a.layer;
+  prm.shape.G = a.Hq / a.layer.Hkv;
+  prm.shape.rows = kRows;
+  prm.shape.chunk_shift = kChunkShift;
+  prm.shape.cap = a.batch.width << a.layer.page_shift;
+  prm.shape.min_rows = 0;
+  prm.shape.max_rows = 0x7FFFFFFF;
+  return a.dh == 64 ? launch_dh<64>(a, prm, dev, stream) : launch_dh<128>(a, prm, dev, stream);
+}
+
+}  // namespace cxa

@@ -1,0 +1,157 @@
+// How the paged attention kernels share out their work.
+//
+// A work item is a tile of query rows of one (sequence, K/V head): the rows are the
+// sequence's new tokens times the G query heads of the K/V head, token by token. Its cost
+// is its number of 64- or 128-key chunks, the causal limit of its last token deciding how
+// many there are; an item without a visible key counts one chunk, in which its rows are
+// written as zeros. All chunks of all items are numbered densely, in the order (sequence,
+// head, tile, chunk), and block c of the grid takes the numbers [c * per, (c + 1) * per):
+// every block has the same number of chunks whatever the lengths, and blocks working on
+// one head's tiles run at the same time, so that its keys are read from L2.
+//
+// An item cut by a block boundary leaves one partial state per block that holds a part of
+// it, and the block that arrives last merges them in order of their chunks: the result
+// does not depend on who is last. A block has at most two cut items, one that began before
+// its range (its partial slot 2c) and one that goes on behind it (2c + 1); the arrival
+// counter of a cut item is that of the first block that holds a part of it.
+#pragma once
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace cxa {
+
+struct WorkShape {
+  int G;              // query heads a K/V head
+  int rows;           // rows a tile
+  int chunk_shift;    // log2 of the keys a chunk
+  int cap;            // keys the table's row can hold
+  int min_rows, max_rows;   // sequences with fewer or more query rows a head are another kernel's
+};
+
+// The rows of one K/V head of a sequence; 0 if the sequence is not this kernel's.
+__device__ __forceinline__ int work_rows(const PagedSeq& s, const WorkShape& w) {
+  const long long m = static_cast<long long>(s.n) * w.G;
+  return m < w.min_rows || m > w.max_rows ? 0 : static_cast<int>(m);
+}
+
+// Keys visible to token i of a sequence.
+__device__ __forceinline__ int visible_keys(const PagedSeq& s, int i, int cap) {
+  return max(0, min(cap, s.kv - s.n + i + 1));
+}
+
+__device__ __forceinline__ int tile_keys(const PagedSeq& s, const WorkShape& w, int rt) {
+  return visible_keys(s, min(s.n - 1, (rt * w.rows + w.rows - 1) / w.G), w.cap);
+}
+
+__device__ __forceinline__ int tile_chunks(const PagedSeq& s, const WorkShape& w, int rt) {
+  return max(1, (tile_keys(s, w, rt) + (1 << w.chunk_shift) - 1) >> w.chunk_shift);
+}
+
+// Chunks of one head of a sequence.
+__device__ __forceinline__ long long head_chunks(const PagedSeq& s, const WorkShape& w) {
+  const int m = work_rows(s, w);
+  long long u = 0;
+  for (int rt = 0; rt * w.rows < m; ++rt) u += tile_chunks(s, w, rt);
+  return u;
+}
+
+struct WorkCursor {
+  PagedSeq seq;
+  int b, h, rt, c;     // c: first chunk of the item in this block's range
+  int tiles;           // of a head of the sequence
+  int nc;              // chunks of the item
+  long long first;     // number of the item's first chunk
+};
+
+struct WorkRange {
+  long long g0, g1;    // this block's chunk numbers
+  long long per;
+};
+
+// Scratch in shared memory for work_locate.
+struct WorkScratch {
+  long long scan[33];
+  WorkCursor cur;
+};
+
+// Number the chunks and find this block's range and the item it starts in. Called by all
+// kThreads threads of the block; returns false if the block has nothing to do.
+template <int kThreads>
+__device__ bool work_locate(const PagedBatch& bt, const WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
+                            WorkCursor* cur) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kW = kThreads / 32;
+  // each thread counts a run of sequences
+  const int each = (bt.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * each, bt.B), b1 = min(b0 + each, bt.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += head_chunks(paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens), w) * Hkv;
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) sm->scan[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    if (i < warp) before += sm->scan[i];
+    total += sm->scan[i];
+  }
+  range->per = (total + gridDim.x - 1) / gridDim.x;
+  range->g0 = range->per * blockIdx.x;
+  range->g1 = min(total, range->g0 + range->per);
+  if (range->g0 >= range->g1) return false;     // the same in every thread
+  long long at = before + incl - mine;
+  if (range->g0 >= at && range->g0 < at + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
+      const long long u = head_chunks(s, w);
+      if (range->g0 < at + u * Hkv) {
+        WorkCursor c;
+        c.seq = s;
+        c.b = b;
+        c.h = static_cast<int>((range->g0 - at) / u);
+        at += u * c.h;
+        c.tiles = (work_rows(s, w) + w.rows - 1) / w.rows;
+        for (c.rt = 0;; ++c.rt) {
+          c.nc = tile_chunks(s, w, c.rt);
+          if (range->g0 < at + c.nc || c.rt + 1 >= c.tiles) break;
+          at += c.nc;
+        }
+        c.first = at;
+        c.c = static_cast<int>(range->g0 - at);
+        sm->cur = c;
+        break;
+      }
+      at += u * Hkv;
+    }
+  }
+  __syncthreads();
+  *cur = sm->cur;
+  return true;
+}
+
+// The item after the cursor's; only called while chunks remain in the block's range.
+__device__ __forceinline__ void work_next(const PagedBatch& bt, const WorkShape& w, int Hkv, WorkCursor* c) {
+  c->first += c->nc;
+  c->c = 0;
+  if (++c->rt == c->tiles) {
+    c->rt = 0;
+    if (++c->h == Hkv) {
+      c->h = 0;
+      do {
+        ++c->b;
+        if (c->b >= bt.B) return;
+        c->seq = paged_seq(bt.q_start, bt.kv_len, c->b, bt.n_tokens);
+        c->tiles = (work_rows(c->seq, w) + w.rows - 1) / w.rows;
+      } while (c->tiles == 0);
+    }
+  }
+  c->nc = tile_chunks(c->seq, w, c->rt);
+}
+
+}  // namespace cxa

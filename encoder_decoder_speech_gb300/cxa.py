@@ -15,10 +15,13 @@ import os
 
 from . import _build
 
-CXA_OK, CXA_EINVAL, CXA_ENOTREADY, CXA_ECUDA, CXA_ETIMEOUT = 0, -1, -2, -3, -4
+CXA_OK, CXA_EINVAL, CXA_ENOTREADY, CXA_ECUDA, CXA_ETIMEOUT, CXA_EPAGE = 0, -1, -2, -3, -4, -5
 CXA_F32, CXA_BF16 = 0, 1
 CXA_DECODE_AUTO, CXA_DECODE_STREAM, CXA_DECODE_ROWS = 0, 1, 2
 CXA_POPULATE_AUTO, CXA_POPULATE_PAIR, CXA_POPULATE_SINGLE = 0, 1, 2
+CXA_ROTARY_HALF, CXA_ROTARY_INTERLEAVED = 0, 1
+CXA_ROTARY_PLAIN, CXA_ROTARY_LINEAR, CXA_ROTARY_NTK, CXA_ROTARY_WAVELENGTH = 0, 1, 2, 3
+CXA_NORM_NONE, CXA_NORM_RMS = 0, 1
 
 # every symbol include/cxa.h declares: name -> (restype, argtypes)
 _c_void_pp = ctypes.POINTER(ctypes.c_void_p)
@@ -70,6 +73,33 @@ SIGNATURES = {
     "cxa_alignment_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
                                              ctypes.c_void_p]),
+    "cxa_rotary_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                              ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_void_p,
+                                              ctypes.c_void_p]),
+    "cxa_rotary_create": (ctypes.c_int, [_c_void_pp, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_double]),
+    "cxa_rotary_destroy": (None, [ctypes.c_void_p]),
+    "cxa_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p,
+                                        ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p]),
+    "cxa_pages_create": (ctypes.c_int, [_c_void_pp, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "cxa_pages_destroy": (None, [ctypes.c_void_p]),
+    "cxa_paged_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int]),
+    "cxa_paged_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p,
+                                        ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong,
+                                        ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
+    "cxa_paged_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "cxa_paged_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                           ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_longlong, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 # most query rows cxa_decode_shared takes per cache row (CXA_MAX_SHARED_QUERIES)
@@ -248,6 +278,71 @@ def cxa_decode_noalloc(handle, Q, key_len, out, scale, stream=None) -> int:
     """cxa_decode with its scratch in libcxa's fixed device array: for callers
     that cannot allocate device memory. Calls must be ordered on one stream."""
     return load().cxa_decode_noalloc(handle, _ptr(Q), _ptr(key_len), _ptr(out), float(scale), _stream(stream))
+
+
+def cxa_rotary_frequencies(rot_dim, base, scaling, factor=1.0, orig_len=0.0, alpha=1.0, beta=32.0):
+    """Returns (status, frequencies, attn_factor): radians a position of each rotated pair."""
+    freq, att = (ctypes.c_double * max(rot_dim // 2, 1))(), ctypes.c_double()
+    rc = load().cxa_rotary_frequencies(rot_dim, base, scaling, factor, orig_len, alpha, beta, freq, ctypes.byref(att))
+    return rc, list(freq), att.value
+
+
+def cxa_rotary_create(rot_dim, layout, freq, attn_factor=1.0):
+    """freq: host sequence of rot_dim / 2 numbers. Returns (status, handle)."""
+    h = ctypes.c_void_p()
+    arr = None if freq is None else (ctypes.c_double * max(len(freq), 1))(*freq)
+    rc = load().cxa_rotary_create(ctypes.byref(h), rot_dim, layout, arr, attn_factor)
+    return rc, (h.value if rc == CXA_OK else None)
+
+
+def cxa_rotary_destroy(handle) -> None:
+    load().cxa_rotary_destroy(handle)
+
+
+def cxa_qk_norm_rope(q, q_stride, Hq, k, k_stride, Hk, dh, n_tokens, pos, norm, eps, q_weight, k_weight, rot, q_out,
+                     qo_stride, k_out, ko_stride, dtype, stream=None) -> int:
+    return load().cxa_qk_norm_rope(_ptr(q), q_stride, Hq, _ptr(k), k_stride, Hk, dh, n_tokens, _ptr(pos), norm, eps,
+                                   _ptr(q_weight), _ptr(k_weight), rot, _ptr(q_out), qo_stride, _ptr(k_out), ko_stride,
+                                   dtype, _stream(stream))
+
+
+def cxa_pages_create(Kp, Vp, num_pages, page_size, L, Hkv, dh, cache_dtype):
+    """Returns (status, handle); handle is None unless status == CXA_OK."""
+    h = ctypes.c_void_p()
+    rc = load().cxa_pages_create(ctypes.byref(h), _ptr(Kp), _ptr(Vp), num_pages, page_size, L, Hkv, dh, cache_dtype)
+    return rc, (h.value if rc == CXA_OK else None)
+
+
+def cxa_pages_destroy(handle) -> None:
+    load().cxa_pages_destroy(handle)
+
+
+def cxa_paged_check(handle, B, n_tokens, q_start, kv_len, page_table, max_pages) -> int:
+    """q_start [B + 1], kv_len [B], page_table [B * max_pages]: host sequences of ints."""
+    def ints(x):
+        x = [int(v) for v in x]
+        return (ctypes.c_int * max(len(x), 1))(*x)
+    if len(q_start) != B + 1 or len(kv_len) != B or len(page_table) != B * max_pages:
+        raise ValueError("q_start, kv_len and page_table must have B + 1, B and B * max_pages entries")
+    return load().cxa_paged_check(handle, B, n_tokens, ints(q_start), ints(kv_len), ints(page_table), max_pages)
+
+
+def cxa_paged_append(handle, layer, B, n_tokens, q_start, kv_len, page_table, max_pages, k, k_stride, v, v_stride, q,
+                     q_stride, Hq, q_out, qo_stride, norm, eps, q_weight, k_weight, rot, dtype, stream=None) -> int:
+    return load().cxa_paged_append(handle, layer, B, n_tokens, _ptr(q_start), _ptr(kv_len), _ptr(page_table), max_pages,
+                                   _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride, Hq, _ptr(q_out), qo_stride,
+                                   norm, eps, _ptr(q_weight), _ptr(k_weight), rot, dtype, _stream(stream))
+
+
+def cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new) -> int:
+    return load().cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new)
+
+
+def cxa_paged_attention(handle, layer, B, n_tokens, max_new, q_start, kv_len, page_table, max_pages, q, q_stride, Hq,
+                        out, o_stride, scale, dtype, workspace, workspace_bytes, stream=None) -> int:
+    return load().cxa_paged_attention(handle, layer, B, n_tokens, max_new, _ptr(q_start), _ptr(kv_len),
+                                      _ptr(page_table), max_pages, _ptr(q), q_stride, Hq, _ptr(out), o_stride, scale,
+                                      dtype, _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def cxa_invalidate(handle, b=-1) -> int:
@@ -438,6 +533,240 @@ class CrossAttentionCache:
     def close(self) -> None:
         if getattr(self, "handle", None):
             cxa_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- paged self-attention
+def _rows(name, t, dh=None, dtype=None, device=None):
+    """Check a packed [tokens, heads, dh] tensor; returns (tokens, heads, dh, row stride)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head dim]")
+    n, H, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d != 1) or (s1 != d and H > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if n > 1 and s0 < H * d:
+        raise ValueError(f"{name}: the rows of different tokens must not overlap")
+    if dh is not None and d != dh:
+        raise ValueError(f"{name}: head dim {d}, expected {dh}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return n, H, d, s0 if n > 1 else H * d
+
+
+def _ints(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+
+
+def _weight(name, t, dh, device):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (dh,) or not t.is_contiguous()
+                          or t.device != device):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({dh},) on {device}")
+
+
+def _on(device):
+    """The device's context, entered only when another device is current."""
+    import contextlib
+    import torch
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+_LAYOUTS = {"half": CXA_ROTARY_HALF, "interleaved": CXA_ROTARY_INTERLEAVED}
+_SCALINGS = {"none": CXA_ROTARY_PLAIN, "linear": CXA_ROTARY_LINEAR, "ntk": CXA_ROTARY_NTK,
+             "wavelength": CXA_ROTARY_WAVELENGTH}
+
+
+class Rotary:
+    """A position rotation of the first ``rot_dim`` channels of a head (cxa_rotary): layout
+    "half" pairs channels (i, i + rot_dim / 2), "interleaved" (2i, 2i + 1); scaling "none",
+    "linear", "ntk" or "wavelength" for contexts longer than the trained one. ``freq``
+    (rot_dim / 2 radians a position) replaces the frequencies that base and scaling give,
+    ``attn_factor`` the factor of the rotated values."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, orig_len: float = 0.0, alpha: float = 1.0, beta: float = 32.0, freq=None,
+                 attn_factor: float | None = None):
+        self.handle = None
+        if layout not in _LAYOUTS or scaling not in _SCALINGS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, scaling one of {sorted(_SCALINGS)}")
+        if freq is None:
+            rc, freq, att = cxa_rotary_frequencies(rot_dim, base, _SCALINGS[scaling], factor, orig_len, alpha, beta)
+            check(rc, "cxa_rotary_frequencies")
+        else:
+            freq, att = [float(f) for f in freq], 1.0
+            if len(freq) * 2 != rot_dim:
+                raise ValueError("freq must have rot_dim / 2 entries")
+        self.rot_dim, self.freq = rot_dim, freq
+        self.attn_factor = att if attn_factor is None else attn_factor
+        rc, self.handle = cxa_rotary_create(rot_dim, _LAYOUTS[layout], freq, self.attn_factor)
+        check(rc, "cxa_rotary_create")
+
+    def __del__(self):
+        try:
+            if self.handle:
+                cxa_rotary_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
+
+
+def _norm(norm_eps):
+    return (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
+
+
+def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None = None, q_weight=None, k_weight=None,
+                 q_out=None, k_out=None, stream=None):
+    """Head norms (RMS, if norm_eps is given) and rotation of q [N, Hq, dh] and k [N, Hk, dh]
+    (or None), float32 or bfloat16, at positions pos [N] int32. Token rows may be strided
+    slices; q_out and k_out may be q and k. Returns (q_out, k_out)."""
+    import torch
+    n, Hq, dh, qs = _rows("q", q)
+    dev, dt = q.device, q.dtype
+    _ints("pos", pos, (n,), dev)
+    _weight("q_weight", q_weight, dh, dev)
+    _weight("k_weight", k_weight, dh, dev)
+    Hk = ks = kos = 0
+    if q_out is None:
+        q_out = torch.empty((n, Hq, dh), dtype=dt, device=dev)
+    no, Ho, _, qos = _rows("q_out", q_out, dh, dt, dev)
+    if no != n or Ho != Hq:
+        raise ValueError("q_out must have q's shape")
+    if k is not None:
+        nk, Hk, _, ks = _rows("k", k, dh, dt, dev)
+        if k_out is None:
+            k_out = torch.empty((n, Hk, dh), dtype=dt, device=dev)
+        no, Ho, _, kos = _rows("k_out", k_out, dh, dt, dev)
+        if nk != n or no != n or Ho != Hk:
+            raise ValueError("k must have q's tokens and k_out k's shape")
+    norm, eps = _norm(norm_eps)
+    with _on(dev):
+        check(cxa_qk_norm_rope(q, qs, Hq, k, ks, Hk, dh, n, pos, norm, eps, q_weight, k_weight,
+                               rotary.handle if rotary is not None else None, q_out, qos,
+                               k_out if k is not None else None, kos, _dtype_code(dt), stream), "cxa_qk_norm_rope")
+    return q_out, (k_out if k is not None else None)
+
+
+class PagedCache:
+    """Owns a [L][num_pages][Hkv][page_size][dh] pool of K/V pages (``Kp``, ``Vp``, zeroed),
+    its descriptor, and the attention's workspaces: one per stream, so that calls on
+    different streams do not share one. The batch of a call is q_start [B + 1], kv_len [B]
+    and page_table [B, max_pages], int32 on the device (see include/cxa.h)."""
+
+    def __init__(self, num_pages: int, page_size: int, L: int, Hkv: int, dh: int = 64, cache_dtype: str = "bf16",
+                 device="cuda"):
+        import torch
+        self.handle = None
+        self.num_pages, self.page_size, self.L, self.Hkv, self.dh = num_pages, page_size, L, Hkv, dh
+        self.cache_dtype = cache_dtype
+        tdt = torch.float32 if _DTYPES[cache_dtype] == CXA_F32 else torch.bfloat16
+        self.Kp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
+        self.Vp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
+        self._ws = {}
+        rc, self.handle = cxa_pages_create(self.Kp, self.Vp, num_pages, page_size, L, Hkv, dh, _DTYPES[cache_dtype])
+        check(rc, "cxa_pages_create")
+
+    def _batch(self, q_start, kv_len, page_table):
+        dev = self.Kp.device
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [sequences, pages]")
+        B, width = page_table.shape
+        _ints("q_start", q_start, (B + 1,), dev)
+        _ints("kv_len", kv_len, (B,), dev)
+        _ints("page_table", page_table, (B, width), dev)
+        return B, width
+
+    def workspace(self, Hq: int, max_new: int, stream=None):
+        """A zeroed attention workspace, kept per stream. While a graph is captured it is a
+        new one (cleared in the graph), as replays may run beside anything else."""
+        import torch
+        n = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
+        key = _stream(stream)
+        ws = self._ws.get(key)
+        capturing = torch.cuda.is_current_stream_capturing()
+        if ws is not None and ws.numel() >= n and not capturing:
+            return ws
+        if stream is None or key == torch.cuda.current_stream().cuda_stream:
+            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(key)):
+                ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
+        if not capturing:
+            self._ws[key] = ws
+        return ws
+
+    def append(self, layer: int, k, v, q_start, kv_len, page_table, q=None, q_out=None, rotary: Rotary | None = None,
+               norm_eps: float | None = None, q_weight=None, k_weight=None, stream=None):
+        """Write k, v [N, Hkv, dh] of the new tokens into their pages, k normalised (RMS, if
+        norm_eps is given) and rotated; with q [N, Hq, dh] also return q_out, the queries
+        normalised and rotated (rows behind the batch's last token are left as they are)."""
+        import torch
+        dev, dt = self.Kp.device, k.dtype
+        B, width = self._batch(q_start, kv_len, page_table)
+        n, Hk, _, ks = _rows("k", k, self.dh, None, dev)
+        nv, Hv, _, vs = _rows("v", v, self.dh, dt, dev)
+        if (Hk, nv, Hv) != (self.Hkv, n, self.Hkv):
+            raise ValueError(f"k and v must be [tokens, {self.Hkv}, {self.dh}]")
+        _weight("q_weight", q_weight, self.dh, dev)
+        _weight("k_weight", k_weight, self.dh, dev)
+        Hq = qs = qos = 0
+        if q is not None:
+            nq, Hq, _, qs = _rows("q", q, self.dh, dt, dev)
+            if q_out is None:
+                q_out = torch.empty((n, Hq, self.dh), dtype=dt, device=dev)
+            no, Ho, _, qos = _rows("q_out", q_out, self.dh, dt, dev)
+            if nq != n or no != n or Ho != Hq:
+                raise ValueError("q must have k's tokens and q_out q's shape")
+        norm, eps = _norm(norm_eps)
+        with _on(dev):
+            check(cxa_paged_append(self.handle, layer, B, n, q_start, kv_len, page_table, width, k, ks, v, vs, q, qs,
+                                   Hq, q_out if q is not None else None, qos, norm, eps, q_weight, k_weight,
+                                   rotary.handle if rotary is not None else None, _dtype_code(dt), stream),
+                  "cxa_paged_append")
+        return q_out if q is not None else None
+
+    def attend(self, layer: int, q, q_start, kv_len, page_table, max_new: int, out=None, scale: float = 0.0,
+               workspace=None, stream=None):
+        """Attention of the new tokens' queries q [N, Hq, dh] over their sequences' keys up to
+        each token's own. max_new: an upper bound of the new tokens of one sequence. Returns
+        out [N, Hq, dh] (rows behind the batch's last token are left as they are)."""
+        import torch
+        dev, dt = self.Kp.device, q.dtype
+        B, width = self._batch(q_start, kv_len, page_table)
+        n, Hq, _, qs = _rows("q", q, self.dh, None, dev)
+        if out is None:
+            out = torch.empty((n, Hq, self.dh), dtype=dt, device=dev)
+        no, Ho, _, os_ = _rows("out", out, self.dh, dt, dev)
+        if (no, Ho) != (n, Hq):
+            raise ValueError("out must have q's shape")
+        with _on(dev):
+            ws = workspace if workspace is not None else self.workspace(Hq, max_new, stream)
+            check(cxa_paged_attention(self.handle, layer, B, n, max_new, q_start, kv_len, page_table, width, q, qs, Hq,
+                                      out, os_, scale, _dtype_code(dt), ws, ws.numel(), stream), "cxa_paged_attention")
+        return out
+
+    def check(self, q_start, kv_len, page_table, n_tokens: int) -> None:
+        """Raise CxaError if the batch (host or device tensors) is not sound (cxa_paged_check)."""
+        check(cxa_paged_check(self.handle, page_table.shape[0], n_tokens, q_start.tolist(), kv_len.tolist(),
+                              page_table.reshape(-1).tolist(), page_table.shape[1]), "cxa_paged_check")
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            cxa_pages_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -55,6 +55,7 @@ extern "C" {
                                 until prefill repopulates the cache) */
 #define CXA_ECUDA      (-3)  /* a CUDA runtime error (launch failure, wrong device) */
 #define CXA_ETIMEOUT   (-4)  /* a kernel's bounded wait expired (see cxa_device_status) */
+#define CXA_EPAGE      (-5)  /* a kernel met a page number outside the pool (see cxa_device_status) */
 
 /* ---- element types ------------------------------------------------------- */
 #define CXA_F32   0   /* IEEE fp32 */
@@ -288,6 +289,172 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
                                     size_t workspace_bytes, void* stream);
 
 /*
+ * ---- Paged self-attention cache ---------------------------------------------
+ *
+ * The decoder's self-attention for batches of sequences of any lengths: keys and
+ * values live in a pool of pages that the caller hands out, a sequence's pages listed
+ * in its row of a page table. One decoder layer's step is cxa_paged_append (head norms,
+ * position rotation, the new rows into their pages) followed by cxa_paged_attention
+ * (every new token over the keys up to its own). New tokens come one a sequence
+ * (decoding), a few (proposals to check), or many (prompts), mixed in one batch. The
+ * contiguous cache of cxa_self_attention_step is its one-token form over
+ * fixed slots ("Recurrence as feeds", "What it opened": the cache is an explicit
+ * input that one run writes and the next reads).
+ *
+ * The batch, common to the calls below. The new tokens of all sequences are packed:
+ *   B          sequences, >= 1.
+ *   n_tokens   rows of the packed tensors (at least the batch's new tokens: rows from
+ *              q_start[B] on are padding, neither read nor written).
+ *   q_start    device int32 [B + 1]: sequence b owns rows q_start[b] .. q_start[b+1]
+ *              (none, if equal); q_start[0] = 0, not decreasing.
+ *   kv_len     device int32 [B]: keys of each sequence, its new tokens included; its
+ *              last new token has position kv_len[b] - 1. A new token of negative
+ *              position (kv_len less than the new tokens) is not appended and its
+ *              attention is zero.
+ *   page_table device int32 [B][max_pages]: position t lies in page
+ *              page_table[b][t / page_size], row t % page_size. Entries behind a
+ *              sequence's last key are not read.
+ *   max_pages  columns of page_table; max_pages * page_size <= 2^30.
+ * A needed entry that is no page of the pool (below 0, num_pages or more, or behind the
+ * table's row) is never dereferenced: an append leaves that row out, attention leaves
+ * the page's keys out, and cxa_device_status reports CXA_EPAGE. cxa_paged_check finds
+ * such entries beforehand on the host.
+ *
+ * Packed tensors hold a token's heads contiguously, dh channels each; consecutive
+ * tokens lie `stride` ELEMENTS apart (a multiple of 16 bytes, at least heads * dh), so
+ * that slices of a fused projection's rows are taken as they are. They are 16-byte
+ * aligned and of one type `dtype`: CXA_F32 (pool CXA_F32 or CXA_BF16) or CXA_BF16 (pool
+ * CXA_BF16). Calls with n_tokens == 0 enqueue nothing.
+ *
+ * Every kernel of these calls waits for all earlier work of its stream before it reads
+ * anything, and lets the next kernel be launched early only after that.
+ */
+
+/*
+ * Position rotation: channels (a, b) of pair i become
+ *   attn_factor * (a cos t - b sin t, a sin t + b cos t),  t = position * freq[i]
+ * for the first rot_dim channels of a head; the others pass through.
+ */
+#define CXA_ROTARY_HALF         0   /* pair i is channels (i, i + rot_dim/2) */
+#define CXA_ROTARY_INTERLEAVED  1   /* pair i is channels (2i, 2i + 1) */
+
+/* Scalings for contexts longer than the trained one. */
+#define CXA_ROTARY_PLAIN       0    /* freq[i] = base^(-2i / rot_dim) */
+#define CXA_ROTARY_LINEAR      1    /* positions divided by factor */
+#define CXA_ROTARY_NTK         2    /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define CXA_ROTARY_WAVELENGTH  3    /* by the turns a pair makes in orig_len positions (the
+                                       YaRN paper's rule): as they are from beta turns up,
+                                       divided by factor from alpha down, linear between;
+                                       attn_factor = 0.1 ln(factor) + 1 */
+
+typedef struct cxa_rotary cxa_rotary;
+
+/*
+ * Fill HOST arrays freq[rot_dim / 2] (radians a position) and *attn_factor. rot_dim even,
+ * 2 .. 128; base > 1; factor >= 1 unless PLAIN; orig_len > 0 and 0 <= alpha < beta for
+ * WAVELENGTH (unused otherwise). A caller with frequencies of its own goes straight to
+ * cxa_rotary_create. Host only.
+ */
+CXA_API int cxa_rotary_frequencies(int rot_dim, double base, int scaling, double factor, double orig_len,
+                                   double alpha, double beta, double* freq, double* attn_factor);
+
+/*
+ * A rotation (a host object, passed to the kernels by value). freq: HOST, rot_dim / 2
+ * values >= 0. Phases are taken in 64-bit fixed point, exact to |position| * 2^-65
+ * turns, so far positions are as exact as near ones. Performs no CUDA call.
+ */
+CXA_API int cxa_rotary_create(cxa_rotary** out, int rot_dim, int layout, const double* freq, double attn_factor);
+CXA_API void cxa_rotary_destroy(cxa_rotary* r);
+
+#define CXA_NORM_NONE 0
+#define CXA_NORM_RMS  1   /* x * rsqrt(mean(x^2) + eps) * weight over the dh channels of a head */
+
+/*
+ * Head norms and rotation of queries and keys in one pass, without a paged cache: a
+ * layer that rotates what it hands to cxa_self_attention_step, or the whole window of
+ * an encoder.
+ *
+ *   q, k       device [n_tokens][Hq or Hk][dh]; a tensor with 0 heads is not touched
+ *              (and may be NULL). dh 64 or 128.
+ *   pos        device int32 [n_tokens]; any value, negative ones included.
+ *   norm       CXA_NORM_NONE or CXA_NORM_RMS, before the rotation; eps >= 0;
+ *              q_weight, k_weight device fp32 [dh] or NULL (1).
+ *   rot        NULL for no rotation.
+ *   q_out, k_out  may be q and k (in place, with the same stride); any other
+ *              overlap is the caller's to avoid.
+ * One kernel.
+ */
+CXA_API int cxa_qk_norm_rope(const void* q, long long q_stride, int Hq, const void* k, long long k_stride, int Hk,
+                             int dh, int n_tokens, const int* pos, int norm, float eps, const float* q_weight,
+                             const float* k_weight, const cxa_rotary* rot, void* q_out, long long qo_stride,
+                             void* k_out, long long ko_stride, int dtype, void* stream);
+
+/*
+ * Descriptor of a caller-owned pool.
+ *   Kp, Vp      device [L][num_pages][Hkv][page_size][dh] of cache_dtype, 16-byte aligned.
+ *   page_size   16, 32, 64, 128 or 256 positions.
+ *   Hkv         K/V heads; query heads are a multiple of them (query head h reads K/V
+ *               head h / (Hq / Hkv)).
+ *   dh          64 or 128.
+ * Performs no CUDA call.
+ */
+typedef struct cxa_pages cxa_pages;
+
+CXA_API int cxa_pages_create(cxa_pages** out, void* Kp, void* Vp, int num_pages, int page_size, int L, int Hkv,
+                             int dh, int cache_dtype);
+CXA_API void cxa_pages_destroy(cxa_pages* c);
+
+/*
+ * Check a batch on the HOST (q_start, kv_len and page_table are host arrays here):
+ * CXA_EINVAL, with the sequence in cxa_last_error_message(), if q_start decreases or
+ * passes n_tokens, a sequence's keys are fewer than its new tokens or pass its table
+ * row, a needed page is not in the pool, or a page that takes new tokens is also
+ * another sequence's or stands twice in its own row. Sequences without new tokens are
+ * not looked at. Host only.
+ */
+CXA_API int cxa_paged_check(const cxa_pages* pages, int B, int n_tokens, const int* q_start, const int* kv_len,
+                            const int* page_table, int max_pages);
+
+/*
+ * Write the new tokens' keys and values into their pages of one layer, the keys
+ * normalised and rotated on the way, and, if q is given, q_out = the queries normalised
+ * and rotated the same way (in the same kernel). Arguments as for cxa_qk_norm_rope, with
+ * the batch's positions; v is stored as it is. fp32 rows round to nearest even in a bf16
+ * pool. q may be NULL (Hq and q_out are then ignored); q_out may be q.
+ */
+CXA_API int cxa_paged_append(const cxa_pages* pages, int layer, int B, int n_tokens, const int* q_start,
+                             const int* kv_len, const int* page_table, int max_pages, const void* k,
+                             long long k_stride, const void* v, long long v_stride, const void* q,
+                             long long q_stride, int Hq, void* q_out, long long qo_stride, int norm, float eps,
+                             const float* q_weight, const float* k_weight, const cxa_rotary* rot, int dtype,
+                             void* stream);
+
+/* Bytes of device workspace of cxa_paged_attention; 0 for unsupported arguments. */
+CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int max_new);
+
+/*
+ * out = softmax(scale * q K^T) V for every new token and query head, over the keys at
+ * positions up to the token's own (which are in the pool: append first).
+ *
+ *   max_new    an upper bound of the new tokens of any one sequence. It chooses
+ *              kernels and the workspace size; results do not depend on it being tight.
+ *   q, out     [n_tokens][Hq][dh] of dtype; their spans, first row to last, must not
+ *              overlap.
+ *   scale      a value <= 0 selects 1/sqrt(dh).
+ *   workspace  at least cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new) bytes,
+ *              256-byte aligned, zero before the first call on a new buffer
+ *              (cudaMemset); calls leave its counters zero. Calls that share a
+ *              workspace must be ordered on one stream.
+ * Values that no key position of a row makes visible never reach it: rows of a page
+ * behind the last key, and later tokens' rows, may hold infinities or NaN. A row that
+ * sees no key is zero. Results do not change from call to call.
+ */
+CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new,
+                                const int* q_start, const int* kv_len, const int* page_table, int max_pages,
+                                const void* q, long long q_stride, int Hq, void* out, long long o_stride, float scale,
+                                int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Cross-attention weights of selected alignment heads for one decode step
  * ("Caso de estudio: WhisperKit", §6: the cross-attention of chosen alignment
  * heads returns its weights, and their mean over heads is returned as an extra
@@ -375,7 +542,8 @@ CXA_API unsigned long long cxa_launch_count(void);
 /*
  * Read the device-side status word of the current device: 0, or CXA_ETIMEOUT
  * when a kernel's bounded wait expired since the word was last cleared (the
- * kernel then skipped its remaining work). Synchronises the device. clear != 0
+ * kernel then skipped its remaining work), or CXA_EPAGE when a paged call met a
+ * page number outside its pool. Synchronises the device. clear != 0
  * resets the word. Returns CXA_ECUDA if the word cannot be read. After a
  * timeout, the decode workspace's counters must be zeroed again before reuse.
  */

@@ -1,0 +1,624 @@
+"""Paged self-attention on the GPU (norms and rotation, append, attention) against plain
+fp64 forms written out here.
+
+Tolerances, per element, count roundings: u is half a step of the output type (bf16 2^-8,
+fp32 2^-24).
+
+* Norm and rotation: |got - ref| <= u |ref| + 2^-20 (|A| + |B|), A and B the two products
+  of the pair: fp32 steps of the norm (64 or 128 squares, rsqrt, weight) and the sine and
+  cosine (a phase rounded to 24 bits of half a turn: pi * 2^-24).
+* Attention: |got - ref| <= u |ref| + (e_p + e_s) A, A = sum p |V| of the row. e_p is the
+  probabilities' rounding: 2^-15 (two truncated bf16 parts) with bf16 tensors on the
+  few-rows kernel, 2^-8 where they are one bf16 value, 2^-19 in fp32 (parts left out, ex2,
+  sums of up to 2^11 terms); e_s that of the scores, 2 * 2^-21 * scale * max sum |q||k|
+  (fp32 sums and the parts left out).
+"""
+import math
+
+import pytest
+import torch
+
+from encoder_decoder_speech_gb300 import cxa
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cxa_lib):
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    torch.cuda.synchronize()
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+
+
+def randn(*shape, seed, dtype=torch.float32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype)
+
+
+# ------------------------------------------------------------------ plain forms, fp64
+def turn(x, pos, rotary=None, layout="half", eps=None, w=None):
+    """Returns the result and the sum of the magnitudes added for it."""
+    y = x.double().clone()
+    if eps is not None:
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + eps)
+        if w is not None:
+            y = y * w.double()
+    mag = y.abs()
+    if rotary is None:
+        return y, mag
+    h, m = rotary.rot_dim // 2, rotary.attn_factor
+    ang = pos.double()[:, None] * torch.tensor(rotary.freq, dtype=torch.float64)
+    c, s = m * torch.cos(ang)[:, None], m * torch.sin(ang)[:, None]
+    lo, hi = (slice(0, h), slice(h, 2 * h)) if layout == "half" else (slice(0, 2 * h, 2), slice(1, 2 * h, 2))
+    a, b = y[..., lo].clone(), y[..., hi].clone()
+    y[..., lo], y[..., hi] = a * c - b * s, a * s + b * c
+    mag[..., lo] = mag[..., hi] = m * (a.abs() + b.abs())
+    return y, mag
+
+
+def close_turn(got, ref, mag):
+    got = got.detach().cpu()
+    over = (got.double() - ref).abs() - U[got.dtype] * ref.abs() - 2.0 ** -20 * mag
+    assert got.numel() == 0 or float(over.max()) <= 0
+
+
+class Batch:
+    """Sequences with n new tokens of kv keys each, in shuffled pages."""
+
+    def __init__(self, n, kv, page, Hq, Hkv, dh, act, pool, seed=0, L=1, layer=0, spare=3, pad=0, extra_cols=1):
+        self.n, self.kv, self.page, self.Hq, self.Hkv, self.dh, self.layer = n, kv, page, Hq, Hkv, dh, layer
+        self.B = len(n)
+        need = [-(-k // page) for k in kv]
+        P = sum(need) + spare
+        self.cache = cxa.PagedCache(P, page, L, Hkv, dh, pool)
+        g = torch.Generator().manual_seed(seed + 77)
+        perm = torch.randperm(P, generator=g).tolist()
+        width = max(need + [0]) + extra_cols
+        self.table = torch.full((self.B, width), -1, dtype=torch.int32)
+        for b in range(self.B):
+            for i in range(need[b]):
+                self.table[b, i] = perm.pop()
+        starts = [0]
+        for x in n:
+            starts.append(starts[-1] + x)
+        self.starts, self.N = starts, starts[-1] + pad
+        self.q = randn(self.N, Hq, dh, seed=seed + 1, dtype=DT[act])
+        self.K = [randn(k, Hkv, dh, seed=seed + 100 + b, dtype=DT[pool]) for b, k in enumerate(kv)]
+        self.V = [randn(k, Hkv, dh, seed=seed + 500 + b, dtype=DT[pool]) for b, k in enumerate(kv)]
+        self.d = dict(q_start=torch.tensor(starts, dtype=torch.int32).cuda(),
+                      kv_len=torch.tensor(kv, dtype=torch.int32).cuda(), page_table=self.table.cuda())
+        self.max_new = max(n + [1])
+
+    def fill(self, rest=None):
+        """Write every key's row into its page; all other rows of the pool hold `rest`."""
+        Kp, Vp = self.cache.Kp[self.layer].cpu(), self.cache.Vp[self.layer].cpu()
+        if rest is not None:
+            Kp.fill_(rest)
+            Vp.fill_(rest)
+        for b in range(self.B):
+            for t in range(0, self.kv[b], self.page):
+                p, m = int(self.table[b, t // self.page]), min(self.page, self.kv[b] - t)
+                Kp[p, :, :m] = self.K[b][t:t + m].transpose(0, 1)
+                Vp[p, :, :m] = self.V[b][t:t + m].transpose(0, 1)
+        self.cache.Kp[self.layer].copy_(Kp)
+        self.cache.Vp[self.layer].copy_(Vp)
+        return self
+
+    def attend(self, q=None, **kw):
+        kw.setdefault("max_new", self.max_new)
+        return self.cache.attend(self.layer, (self.q if q is None else q).cuda(), **self.d, **kw)
+
+    def reference(self, scale=None):
+        """out, sum p |V|, and the largest scale * sum |q||k|, in fp64, on the GPU."""
+        scale = scale or 1 / math.sqrt(self.dh)
+        G = self.Hq // self.Hkv
+        out = torch.zeros(self.N, self.Hq, self.dh, dtype=torch.float64, device="cuda")
+        A = torch.zeros_like(out)
+        big = 0.0
+        for b in range(self.B):
+            n, kv = self.n[b], self.kv[b]
+            if n == 0 or kv == 0:
+                continue
+            q = self.q[self.starts[b]:self.starts[b + 1]].cuda().double()
+            K, V = self.K[b].cuda().double(), self.V[b].cuda().double()
+            tame = bool(V.isfinite().all())
+            seen = torch.arange(kv, device="cuda")[None] <= (kv - n + torch.arange(n, device="cuda"))[:, None]
+            for h in range(self.Hq):
+                s = q[:, h] @ K[:, h // G].T * scale
+                big = max(big, float((q[:, h].abs() @ K[:, h // G].abs().T * scale).nan_to_num(0, 0, 0).max()))
+                s = s.masked_fill(~seen, -math.inf)
+                top = s.amax(-1, keepdim=True)
+                p = torch.where(seen, torch.exp(s - torch.where(top.isinf(), 0.0, top)), 0.0)
+                l = p.sum(-1, keepdim=True)
+                w = torch.where(l == 0, 0.0, p / l)
+                rows = slice(self.starts[b], self.starts[b + 1])
+                if tame:
+                    out[rows, h], A[rows, h] = w @ V[:, h // G], w @ V[:, h // G].abs()
+                    continue
+                for i in range(n):
+                    out[rows.start + i, h] = w[i, seen[i]] @ V[seen[i], h // G]
+                    A[rows.start + i, h] = w[i, seen[i]] @ V[seen[i], h // G].abs()
+        return out.cpu(), A.cpu(), big
+
+    def close(self, got, scale=None, one_bf16=None):
+        out, A, big = self.reference(scale)
+        rows = slice(0, self.starts[-1])
+        got = got.detach().cpu()
+        if one_bf16 is None:    # a sequence of many rows may go to the kernel of one bf16 probability
+            one_bf16 = self.max_new * (self.Hq // self.Hkv) > 16
+        ep = 2.0 ** -19 if got.dtype == torch.float32 else 2.0 ** -8 if one_bf16 else 2.0 ** -15
+        over = (got.double() - out).abs() - U[got.dtype] * out.abs() - (ep + 2 * 2.0 ** -21 * big) * A
+        fin = out.isfinite()[rows]
+        assert bool((got[rows].isfinite() == fin).all())
+        assert not bool(fin.any()) or float(over[rows][fin].max()) <= 0
+
+
+# ------------------------------------------------------------------ norms and rotation
+ROT = [dict(rot_dim=64), dict(rot_dim=64, layout="interleaved"), dict(rot_dim=32, scaling="linear", factor=4.0),
+       dict(rot_dim=48, layout="interleaved", scaling="ntk", factor=8.0), dict(rot_dim=2),
+       dict(rot_dim=38, layout="half"), dict(rot_dim=10, layout="interleaved"),
+       dict(rot_dim=64, scaling="wavelength", factor=16.0, orig_len=2048), None]
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("i", range(len(ROT)))
+def test_norm_rope(dh, act, norm, i):
+    kw = dict(ROT[i]) if ROT[i] else None
+    if kw and dh == 128 and i in (0, 1, 7):
+        kw["rot_dim"] = 128
+    rot = cxa.Rotary(**kw) if kw else None
+    layout = kw.get("layout", "half") if kw else "half"
+    for N, Hq, Hk in [(1, 20, 20), (7, 6, 1), (3, 1, 9), (300, 8, 2)]:
+        qkv = randn(N, Hq + 2 * Hk, dh, seed=N + Hq, dtype=DT[act]).cuda()      # strided slices of one projection
+        q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hk]
+        before = qkv.clone()
+        pos = torch.randint(-5, 1 << 20, (N,), generator=torch.Generator().manual_seed(N), dtype=torch.int32)
+        pos[0] = 0
+        pos[-1] = 2 ** 30 - 1 if N > 1 else 447
+        wq, wk = 1 + randn(dh, seed=3, scale=0.2), 1 + randn(dh, seed=4, scale=0.2)
+        args = dict(rotary=rot, norm_eps=1e-6 if norm else None)
+        if norm and Hq != 8:
+            args.update(q_weight=wq.cuda(), k_weight=wk.cuda())
+        qo, ko = cxa.qk_norm_rope(q, k, pos.cuda(), **args)
+        assert torch.equal(qkv, before)
+        for got, x, w in [(qo, q, wq), (ko, k, wk)]:
+            ref, mag = turn(x.cpu(), pos, rot, layout, args["norm_eps"], w if "q_weight" in args else None)
+            close_turn(got, ref, mag)
+        # in place, on the strided slices
+        cxa.qk_norm_rope(q, k, pos.cuda(), q_out=q, k_out=k, **args)
+        assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(qkv[:, Hq + Hk:], before[:, Hq + Hk:])
+
+
+def test_norm_rope_queries_alone_and_empty():
+    rot = cxa.Rotary(64)
+    q = randn(5, 3, 64, seed=1).cuda()
+    pos = torch.arange(5, dtype=torch.int32).cuda()
+    qo, ko = cxa.qk_norm_rope(q, None, pos, rotary=rot)
+    assert ko is None
+    close_turn(qo, *turn(q.cpu(), pos.cpu(), rot))
+    e = cxa.qk_norm_rope(q[:0], q[:0], pos[:0], rotary=rot)
+    assert e[0].shape == (0, 3, 64) and e[1].shape == (0, 3, 64)
+
+
+def test_norm_rope_far_positions_agree_with_near_ones():
+    """With frequencies of whole eighths of a turn, position p and p + 8 * 10^7 coincide."""
+    rot = cxa.Rotary(64, freq=[2 * math.pi * (i % 8) / 8 for i in range(32)])
+    q = randn(9, 4, 64, seed=2).cuda()
+    pos = torch.arange(9, dtype=torch.int32).cuda()
+    a, _ = cxa.qk_norm_rope(q, None, pos, rotary=rot)
+    b, _ = cxa.qk_norm_rope(q, None, pos + 80_000_000, rotary=rot)
+    close_turn(b, *turn(q.cpu(), pos.cpu(), rot))
+    assert float((a - b).abs().max()) <= 2.0 ** -20 * 8
+
+
+def test_norm_rope_unrotated_channels_see_no_neighbours_infinity():
+    q = torch.ones(2, 2, 64).cuda()
+    q[:, 0, 5] = math.inf
+    q[:, 1, 40] = math.nan
+    out, _ = cxa.qk_norm_rope(q, None, torch.tensor([1, 2], dtype=torch.int32).cuda(), rotary=cxa.Rotary(16))
+    assert bool(out[:, 0, 16:].eq(1).all()) and int(out[:, 0].isfinite().logical_not().sum()) == 2 * 2
+    assert int(out[:, 1].isnan().sum()) == 2 and bool(out[:, 1, 40].isnan().all())
+
+
+def test_rotated_rows_feed_the_contiguous_step():
+    """Queries and keys rotated in front of cxa_self_attention_step: scores depend on distance alone."""
+    B, L, H, T, S = 2, 2, 3, 64, 9
+    rot = cxa.Rotary(64)
+    c = cxa.CrossAttentionCache(B, T, L, H, 64, "f32")
+    q0, k0 = randn(B, L * H, 64, seed=1), randn(B, L * H, 64, seed=2)
+    outs, vs = [], []
+    for s in range(S):
+        pos = torch.full((B,), s, dtype=torch.int32)
+        q, k = cxa.qk_norm_rope(q0.cuda(), k0.cuda(), pos.cuda(), rotary=rot, norm_eps=1e-6)
+        v = randn(B, L, H, 64, seed=10 + s)
+        vs.append(v)
+        outs.append(c.self_attention_step(pos.cuda(), q.view(B, L, H, 64), k.view(B, L, H, 64), v.cuda()))
+    qn, kn = turn(q0, torch.zeros(B), None, eps=1e-6)[0], turn(k0, torch.zeros(B), None, eps=1e-6)[0]
+    for s in range(S):
+        kr = torch.stack([turn(kn, torch.full((B,), float(t - s)), rot)[0] for t in range(s + 1)], 2)   # [B, LH, s+1, 64]
+        p = torch.softmax((qn[:, :, None] * kr).sum(-1) / 8, -1)
+        ref = (p[..., None] * torch.stack(vs[:s + 1], 3).double().view(B, L * H, s + 1, 64)).sum(2)
+        assert float((outs[s].cpu().double().view(B, L * H, 64) - ref).abs().max()) <= 1e-4
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("act,pool", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("dh,page", [(64, 16), (128, 32), (64, 256)])
+def test_append(act, pool, dh, page):
+    for n, kv, Hq, Hkv, i, norm in [([1], [1], 4, 4, 0, True), ([1, 1, 1], [17, 1, 33], 8, 2, 3, False),
+                                    ([0, 40, 0, 3, 1], [5, 50, 0, 3, 300], 6, 6, 5, True),
+                                    ([70, 33], [70, 600], 5, 1, 1, True), ([2] * 70, [9] * 70, 2, 2, 8, False)]:
+        bt = Batch(n, kv, page, Hq, Hkv, dh, act, pool, L=2, layer=1, pad=4)
+        bt.cache.Kp.copy_(randn(*bt.cache.Kp.shape, seed=5))
+        bt.cache.Vp.copy_(randn(*bt.cache.Vp.shape, seed=6))
+        K0, V0 = bt.cache.Kp.cpu(), bt.cache.Vp.cpu()
+        kw = ROT[i]
+        rot = cxa.Rotary(**kw) if kw else None
+        layout = kw.get("layout", "half") if kw else "half"
+        qkv = randn(bt.N, Hq + 2 * Hkv, dh, seed=9, dtype=DT[act]).cuda()
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        wk = 1 + randn(dh, seed=8, scale=0.2)
+        eps = 1e-5 if norm else None
+        q_out = torch.full((bt.N, Hq, dh), 7.0, dtype=DT[act]).cuda()
+        got = bt.cache.append(1, k, v, **bt.d, q=q, q_out=q_out, rotary=rot, norm_eps=eps, k_weight=wk.cuda())
+        assert got is q_out
+        T = bt.starts[-1]
+        assert bool((q_out[T:] == 7).all())                       # rows behind the last sequence
+        pos = torch.cat([torch.arange(c - a, c) for a, c in zip(n, kv)] + [torch.zeros(0)]).double()
+        close_turn(q_out[:T], *turn(q[:T].cpu(), pos, rot, layout, eps))
+        rk, mk = turn(k[:T].cpu(), pos, rot, layout, eps, wk)
+        Kg, Vg = bt.cache.Kp.cpu(), bt.cache.Vp.cpu()
+        touched = torch.zeros(Kg.shape[1], page, dtype=torch.bool)
+        for b in range(bt.B):
+            for j in range(n[b]):
+                t = kv[b] - n[b] + j
+                p, s, r = int(bt.table[b, t // page]), t % page, bt.starts[b] + j
+                touched[p, s] = True
+                close_turn(Kg[1, p, :, s], rk[r], mk[r])
+                assert torch.equal(Vg[1, p, :, s], v[r].cpu().to(DT[pool]))
+        assert torch.equal(Kg[0], K0[0]) and torch.equal(Vg[0], V0[0])
+        keep = ~touched
+        assert torch.equal(Kg[1].transpose(1, 2)[keep], K0[1].transpose(1, 2)[keep])
+        assert torch.equal(Vg[1].transpose(1, 2)[keep], V0[1].transpose(1, 2)[keep])
+
+
+def test_append_many_sequences_and_queries_in_place():
+    n = [(b * 7) % 4 for b in range(1100)]
+    bt = Batch(n, [x + b % 40 for b, x in enumerate(n)], 16, 2, 1, 64, "f32", "f32")
+    rot = cxa.Rotary(64)
+    k, v, q = (randn(bt.N, h, 64, seed=h + 3).cuda() for h in (1, 1, 2))
+    want = q.clone()
+    pos = torch.cat([torch.arange(c - a, c) for a, c in zip(bt.n, bt.kv)])
+    bt.cache.append(0, k, v, **bt.d, q=q, q_out=q, rotary=rot)
+    close_turn(q, *turn(want.cpu(), pos, rot))
+    ref, mag = turn(k.cpu(), pos, rot)
+    page = torch.cat([bt.table[b, torch.arange(c - a, c) // 16] for b, (a, c) in enumerate(zip(bt.n, bt.kv))]).long()
+    close_turn(bt.cache.Kp.cpu()[0, page, 0, pos % 16], ref[:, 0], mag[:, 0])
+
+
+# ------------------------------------------------------------------ attention
+TYPES = [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")]
+SHAPES = [  # n, kv, page, Hq, Hkv
+    ([1], [1], 16, 1, 1),
+    ([1], [448], 16, 8, 8),
+    ([1, 1, 1, 1], [15, 16, 17, 333], 16, 8, 2),
+    ([5, 5, 5], [5, 64, 1000], 32, 6, 6),
+    ([3, 0, 1, 2], [3, 90, 129, 65], 64, 20, 4),
+    ([1] * 40, [1 + 37 * b for b in range(40)], 256, 8, 1),
+    ([130], [130], 128, 4, 4),
+    ([63, 1, 257], [64, 2000, 700], 16, 5, 1),
+    ([40, 200], [4097, 200], 128, 16, 2),
+]
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_attention(act, pool, dh, i):
+    n, kv, page, Hq, Hkv = SHAPES[i]
+    bt = Batch(n, kv, page, Hq, Hkv, dh, act, pool, seed=i).fill()
+    bt.close(bt.attend())
+    bt.close(bt.attend(scale=0.3), scale=0.3)
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("n,kv", [([1, 1], [20, 470]), ([7, 5], [40, 470]), ([150, 90], [150, 470])])
+def test_rows_behind_the_last_key_may_hold_anything(act, pool, n, kv):
+    for rest in (math.nan, math.inf, -math.inf):
+        bt = Batch(n, kv, 64, 4, 2, 64, act, pool).fill(rest=rest)
+        bt.close(bt.attend())
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,kv,bad", [([6], [40], 37), ([8, 3], [8, 100], 5), ([200], [460], 300), ([300], [300], 129),
+                                      ([140], [140], 139)])
+def test_a_later_token_s_infinities_do_not_reach_an_earlier_one(act, pool, dh, n, kv, bad):
+    for what in (math.nan, math.inf):
+        bt = Batch(n, kv, 16, 4, 2, dh, act, pool)
+        bt.V[0][bad, 1, 3] = what
+        bt.K[0][bad, 0, 5] = math.nan
+        bt.fill()
+        got = bt.attend().cpu()
+        first = bad - (kv[0] - n[0])          # rows before it never see it
+        want = Batch(n, kv, 16, 4, 2, dh, act, pool).fill().attend().cpu()
+        assert bool(got[:max(first, 0)].isfinite().all())
+        if len(n) > 1:
+            assert torch.equal(got[n[0]:], want[n[0]:])
+        assert bool(got[first:n[0], :2].isnan().all())        # heads of K/V head 0: a NaN score
+        assert not bool(got[first:n[0], 2:, 3].isfinite().any())
+        bt.close(got)
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+def test_large_scores_pick_one_key(act, pool):
+    """A key along each query, 200 above the rest in the exponent: the result is its V."""
+    n, kv = [1, 4, 150], [300, 260, 700]
+    bt = Batch(n, kv, 32, 4, 4, 64, act, pool)
+    for b in range(3):
+        at = [0, 130, kv[b] - n[b]][b]
+        for h in range(4):
+            bt.K[b][:, h] = 0.01 * bt.K[b][:, h]
+            q = bt.q[bt.starts[b], h].float()
+            bt.q[bt.starts[b]:bt.starts[b + 1], h] = bt.q[bt.starts[b], h].clone()
+            bt.K[b][at, h] = (q * 1600 / (q @ q)).to(DT[pool])
+    bt.fill()
+    got = bt.attend().cpu()
+    for b, at in enumerate([0, 130, 550]):
+        rows = slice(bt.starts[b], bt.starts[b + 1])
+        assert torch.equal(got[rows], bt.V[b][at].to(got.dtype).expand(n[b], 4, 64))
+
+
+def test_masked_scores_of_the_lowest_value():
+    """K of the type's lowest value: scores of -inf weigh nothing, the rest is as without them."""
+    bt = Batch([1, 30], [200, 200], 16, 2, 2, 64, "bf16", "bf16")
+    bt.q = bt.q.abs() + 1
+    for b in range(2):
+        bt.K[b][50:90] = torch.finfo(torch.bfloat16).min
+    bt.fill()
+    got = bt.attend()
+    assert bool(got.isfinite().all())
+    one = Batch([1, 30], [160, 160], 16, 2, 2, 64, "bf16", "bf16")
+    one.q = bt.q
+    one.K, one.V = ([torch.cat([x[:50], x[90:]]) for x in y] for y in (bt.K, bt.V))
+    one.close(got)
+
+
+def test_empty_sequences_and_padding_are_left_alone():
+    for n, kv in [([0, 0], [0, 10]), ([0, 3, 0], [7, 3, 0]), ([0], [0])]:
+        bt = Batch(n, kv, 16, 4, 2, 64, "bf16", "bf16", pad=5).fill()
+        out = torch.full((bt.N, 4, 64), 3.0, dtype=torch.bfloat16).cuda()
+        bt.attend(out=out)
+        assert bool((out[bt.starts[-1]:] == 3).all())
+        bt.close(out)
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+def test_tokens_without_a_key_are_zero(act, pool):
+    """kv_len below the new tokens: the first ones see nothing."""
+    for n in (5, 200):
+        bt = Batch([n], [n], 16, 4, 2, 64, act, pool).fill()
+        bt.d["kv_len"] = torch.tensor([n - 3], dtype=torch.int32).cuda()
+        got = bt.attend().cpu()
+        assert bool((got[:3] == 0).all()) and bool(got[3:].isfinite().all())
+        one = Batch([n - 3], [n - 3], 16, 4, 2, 64, act, pool)
+        one.q, one.K, one.V = bt.q[3:], [bt.K[0][:n - 3]], [bt.V[0][:n - 3]]
+        one.close(got[3:], one_bf16=n > 100)
+        bt.d["kv_len"] = torch.tensor([0], dtype=torch.int32).cuda()
+        assert bool((bt.attend() == 0).all())
+
+
+def test_strided_queries_and_outputs():
+    for n, kv in [([1, 3], [50, 40]), ([140], [200])]:
+        bt = Batch(n, kv, 16, 6, 2, 64, "bf16", "bf16").fill()
+        want = bt.attend()
+        buf = torch.zeros(bt.N, 10, 64, dtype=torch.bfloat16).cuda()
+        buf[:, 2:8] = bt.q.cuda()
+        out = torch.full((bt.N, 9, 64), 5.0, dtype=torch.bfloat16).cuda()
+        bt.cache.attend(0, buf[:, 2:8], **bt.d, max_new=bt.max_new, out=out[:, 1:7])
+        assert torch.equal(out[:, 1:7], want)
+        assert bool((out[:, 0] == 5).all()) and bool((out[:, 7:] == 5).all())
+
+
+@pytest.mark.parametrize("max_new", [1, 4, 1000])
+def test_a_wrong_bound_of_new_tokens_changes_nothing(max_new):
+    bt = Batch([1, 60, 2, 300], [100, 90, 2, 1000], 32, 8, 4, 64, "bf16", "bf16").fill()
+    bt.close(bt.attend(max_new=max_new), one_bf16=True)
+
+
+def test_repeated_calls_agree_bit_for_bit():
+    for n, kv in [([1] * 9, [3000 - 300 * b for b in range(9)]), ([300, 1, 40], [2000, 5000, 700])]:
+        bt = Batch(n, kv, 64, 8, 2, 64, "bf16", "bf16").fill()
+        want = bt.attend()
+        for _ in range(5):
+            assert torch.equal(bt.attend(), want)
+
+
+def test_pages_outside_the_pool_are_left_out_and_reported():
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    for n in (1, 40):
+        for bad in (-1, 10 ** 6, -2 ** 31):
+            bt = Batch([n], [160], 16, 4, 2, 64, "bf16", "bf16").fill()
+            bt.d["page_table"][0, 3] = bad
+            got = bt.attend()
+            assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+            keep = [t for t in range(160) if t // 16 != 3]
+            one = Batch([n], [144], 16, 4, 2, 64, "bf16", "bf16")
+            one.q, one.K, one.V = bt.q, [bt.K[0][keep]], [bt.V[0][keep]]
+            one.close(got, one_bf16=n > 1)
+            # an append into such a page, or behind the table's row, writes nothing
+            bt.d["kv_len"] = torch.tensor([48 + n], dtype=torch.int32).cuda()
+            if n == 1:
+                K0, V0 = bt.cache.Kp.clone(), bt.cache.Vp.clone()
+                k = randn(1, 2, 64, seed=1, dtype=torch.bfloat16).cuda()
+                bt.cache.append(0, k, k, **bt.d)
+                assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+                bt.d["kv_len"] = torch.tensor([16 * 11 + 1], dtype=torch.int32).cuda()
+                bt.cache.append(0, k, k, **bt.d)
+                assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+                assert torch.equal(bt.cache.Kp, K0) and torch.equal(bt.cache.Vp, V0)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 elements, its sequences at both ends of it."""
+    page, Hkv, dh = 256, 8, 64
+    P = (1 << 32) // (page * Hkv * dh) + 40
+    bt = Batch([1, 200], [300, 700], page, 8, Hkv, dh, "bf16", "bf16")
+    bt.cache = cxa.PagedCache(P, page, 1, Hkv, dh, "bf16")
+    remap = {}
+    for b in range(2):
+        for i in range(bt.table.shape[1]):
+            t = int(bt.table[b, i])
+            if t >= 0:
+                bt.table[b, i] = remap.setdefault(t, P - 1 - len(remap) if len(remap) % 2 else len(remap))
+    bt.d["page_table"] = bt.table.cuda()
+    assert int(bt.table.max()) * page * Hkv * dh > 1 << 32
+    for b in range(2):
+        for t in range(0, bt.kv[b], page):
+            p, m = int(bt.table[b, t // page]), min(page, bt.kv[b] - t)
+            bt.cache.Kp[0, p, :, :m] = bt.K[b][t:t + m].transpose(0, 1).cuda()
+            bt.cache.Vp[0, p, :, :m] = bt.V[b][t:t + m].transpose(0, 1).cuda()
+    bt.close(bt.attend())
+    k = randn(201, Hkv, dh, seed=4, dtype=torch.bfloat16).cuda()
+    bt.cache.append(0, k, k, **bt.d)
+    for b in range(2):
+        t = bt.kv[b] - 1
+        assert torch.equal(bt.cache.Vp[0, int(bt.table[b, t // page]), :, t % page], k[bt.starts[b + 1] - 1])
+
+
+# ------------------------------------------------------------------ the run as it is used
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("graph", [False, True])
+def test_prompt_then_steps(act, pool, graph):
+    """Prompts of two sequences in chunks, then single tokens and a proposal of three, two
+    layers: append with norms and rotation, then attention, against one pass over the whole
+    sequence in fp64 on the rows that the pool holds."""
+    L, Hq, Hkv, dh, page = 2, 4, 2, 64, 16
+    total = [150, 70]
+    plan = [[100, 17], [40, 48], [1, 1], [1, 1], [3, 0], [5, 3]]
+    rot = cxa.Rotary(48, scaling="wavelength", factor=4.0, orig_len=64)
+    bt = Batch([0, 0], total, page, Hq, Hkv, dh, act, pool, L=L)
+    w = (1 + randn(dh, seed=5, scale=0.2)).cuda()
+    done = [0, 0]
+    pad = 120
+    bufs = {x: torch.zeros(pad, h, dh, dtype=DT[act]).cuda() for x, h in (("q", Hq), ("k", Hkv), ("v", Hkv))}
+    q_start, kv_len = torch.zeros(3, dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    table = bt.table.cuda()
+    outs = [torch.zeros(pad, Hq, dh, dtype=DT[act]).cuda() for _ in range(L)]
+
+    def step():
+        for l in range(L):
+            qr = bt.cache.append(l, bufs["k"] * (l + 1), bufs["v"] * (l + 1), q_start, kv_len, table, q=bufs["q"],
+                                 rotary=rot, norm_eps=1e-6, q_weight=w, k_weight=w)
+            bt.cache.attend(l, qr, q_start, kv_len, table, max_new=100, out=outs[l])
+
+    g = None
+    if graph:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()                       # a batch of nothing: loads the kernels
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+    qs, got = [[], []], [[[], []] for _ in range(L)]
+    for i, n in enumerate(plan):
+        for x in bufs:
+            bufs[x].copy_(randn(*bufs[x].shape, seed=1000 * i + ord(x), dtype=DT[act]))
+        done = [d + a for d, a in zip(done, n)]
+        q_start.copy_(torch.tensor([0, n[0], n[0] + n[1]], dtype=torch.int32))
+        kv_len.copy_(torch.tensor(done, dtype=torch.int32))
+        bt.cache.check(q_start.cpu(), kv_len.cpu(), table.cpu(), pad)
+        if g:
+            g.replay()
+        else:
+            step()
+        lo = 0
+        for b in range(2):
+            qs[b].append(bufs["q"][lo:lo + n[b]].cpu())
+            for l in range(L):
+                got[l][b].append(outs[l][lo:lo + n[b]].cpu())
+            lo += n[b]
+    assert done == total
+    for l in range(L):
+        one = Batch(total, total, page, Hq, Hkv, dh, act, pool)
+        for b in range(2):
+            ids = [int(x) for x in bt.table[b, :-(-total[b] // page)]]
+            one.K[b] = bt.cache.Kp[l, ids].cpu().transpose(1, 2).reshape(-1, Hkv, dh)[:total[b]]
+            one.V[b] = bt.cache.Vp[l, ids].cpu().transpose(1, 2).reshape(-1, Hkv, dh)[:total[b]]
+            qr, _ = cxa.qk_norm_rope(torch.cat(qs[b]).cuda(), None, torch.arange(total[b], dtype=torch.int32).cuda(),
+                                     rotary=rot, norm_eps=1e-6, q_weight=w)
+            one.q[one.starts[b]:one.starts[b + 1]] = qr.cpu()
+        one.close(torch.cat([torch.cat(got[l][0]), torch.cat(got[l][1])]))
+
+
+def test_two_streams_at_once():
+    a = Batch([1] * 8, [4000 - 100 * b for b in range(8)], 64, 8, 2, 64, "bf16", "bf16", seed=1).fill()
+    want = a.attend()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    q = a.q.cuda()
+    torch.cuda.synchronize()
+    outs = []
+    for r in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(a.cache.attend(0, q, **a.d, max_new=1))
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        outs.append(a.cache.attend(0, q, **a.d, max_new=1, stream=streams[r % 3].cuda_stream, out=out))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_two_graphs_at_once():
+    a = Batch([1] * 8, [4000 - 100 * b for b in range(8)], 64, 8, 2, 64, "bf16", "bf16", seed=1).fill()
+    want, q = a.attend(), a.q.cuda()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([a.cache.attend(0, q, **a.d, max_new=1) for _ in range(3)])
+        graphs.append((g, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for os_ in outs for o in os_)
+
+
+def test_python_refusals():
+    bt = Batch([1, 2], [5, 9], 16, 4, 2, 64, "bf16", "bf16").fill()
+    q = bt.q.cuda()
+    with pytest.raises(ValueError):
+        bt.cache.attend(0, q[:, :, :32], **bt.d, max_new=2)
+    with pytest.raises(ValueError):
+        bt.cache.attend(0, q.transpose(0, 1), **bt.d, max_new=2)
+    with pytest.raises(ValueError):
+        bt.cache.attend(0, bt.q, **bt.d, max_new=2)                       # on the host
+    with pytest.raises(TypeError):
+        bt.cache.attend(0, q.half(), **bt.d, max_new=2)
+    with pytest.raises(TypeError):
+        bt.cache.attend(0, q, **bt.d, max_new=2, out=torch.empty_like(q, dtype=torch.float32))
+    with pytest.raises(ValueError):
+        bt.cache.attend(0, q, bt.d["q_start"].long(), bt.d["kv_len"], bt.d["page_table"], max_new=2)
+    with pytest.raises(ValueError):
+        bt.cache.attend(0, q, bt.d["q_start"][:2], bt.d["kv_len"], bt.d["page_table"], max_new=2)
+    with pytest.raises(cxa.CxaError):
+        bt.cache.attend(1, q, **bt.d, max_new=2)
+    with pytest.raises(cxa.CxaError):
+        bt.cache.attend(0, q, **bt.d, max_new=2, out=q)
+    with pytest.raises(ValueError):
+        bt.cache.append(0, q, q, **bt.d)                                  # 4 heads, the pool has 2
+    with pytest.raises(ValueError):
+        cxa.qk_norm_rope(q[:1].expand(3, 4, 64), None, torch.zeros(3, dtype=torch.int32).cuda())
+    f32 = cxa.PagedCache(4, 16, 1, 2, 64, "f32")
+    with pytest.raises(cxa.CxaError):
+        f32.attend(0, q, **bt.d, max_new=2)

@@ -1,0 +1,210 @@
+"""Host side of the paged self-attention calls: frequencies, refusals and the batch check.
+No GPU is needed: every call here returns before any CUDA call, and the device pointers
+handed over are never dereferenced."""
+import math
+
+import pytest
+
+from encoder_decoder_speech_gb300 import cxa
+
+FAKE = 0x7f0000000000          # 256-byte aligned, never dereferenced
+BIG = 1 << 40
+
+
+@pytest.fixture(autouse=True)
+def _lib(cxa_lib):
+    yield
+
+
+def make_pages(num_pages=10, page_size=16, L=2, Hkv=4, dh=64, dtype=cxa.CXA_BF16, Kp=FAKE, Vp=FAKE + (1 << 32)):
+    return cxa.cxa_pages_create(Kp, Vp, num_pages, page_size, L, Hkv, dh, dtype)
+
+
+@pytest.fixture
+def pages():
+    rc, h = make_pages()
+    assert rc == cxa.CXA_OK
+    yield h
+    cxa.cxa_pages_destroy(h)
+
+
+def refused(rc, text):
+    assert rc == cxa.CXA_EINVAL
+    assert text in cxa.cxa_last_error_message()
+
+
+# ------------------------------------------------------------------ rotations
+@pytest.mark.parametrize("rot", [2, 6, 64, 128])
+def test_frequencies_follow_their_formulas(rot):
+    rc, f, att = cxa.cxa_rotary_frequencies(rot, 10000.0, cxa.CXA_ROTARY_PLAIN)
+    assert rc == cxa.CXA_OK and att == 1.0
+    plain = [10000.0 ** (-2 * i / rot) for i in range(rot // 2)]
+    assert f == pytest.approx(plain, rel=1e-14)
+    _, f, att = cxa.cxa_rotary_frequencies(rot, 10000.0, cxa.CXA_ROTARY_LINEAR, 4.0)
+    assert f == pytest.approx([x / 4 for x in plain], rel=1e-14) and att == 1.0
+    _, f, _ = cxa.cxa_rotary_frequencies(rot, 10000.0, cxa.CXA_ROTARY_NTK, 4.0)
+    base = 10000.0 * 4.0 ** (rot / (rot - 2)) if rot > 2 else 10000.0
+    assert f == pytest.approx([base ** (-2 * i / rot) for i in range(rot // 2)], rel=1e-13)
+    if rot > 2:     # the slowest pair is slowed down by exactly the factor
+        assert f[-1] == pytest.approx(plain[-1] / 4, rel=1e-13)
+    _, f, att = cxa.cxa_rotary_frequencies(rot, 10000.0, cxa.CXA_ROTARY_WAVELENGTH, 4.0, 2048.0, 1.0, 32.0)
+    assert att == pytest.approx(0.1 * math.log(4.0) + 1)
+    for x, y in zip(plain, f):
+        turns = 2048 * x / (2 * math.pi)
+        if turns >= 32:
+            assert y == pytest.approx(x, rel=1e-14)
+        elif turns <= 1:
+            assert y == pytest.approx(x / 4, rel=1e-14)
+        else:
+            keep = (turns - 1) / 31
+            assert y == pytest.approx(keep * x + (1 - keep) * x / 4, rel=1e-14)
+
+
+def test_frequency_and_rotation_refusals():
+    bad = lambda *a: cxa.cxa_rotary_frequencies(*a)[0]
+    refused(bad(0, 1e4, 0), "rot_dim")
+    refused(bad(7, 1e4, 0), "rot_dim")
+    refused(bad(130, 1e4, 0), "rot_dim")
+    refused(bad(64, 1.0, 0), "base")
+    refused(bad(64, math.nan, 0), "base")
+    refused(bad(64, 1e4, 9), "scaling")
+    refused(bad(64, 1e4, cxa.CXA_ROTARY_LINEAR, 0.5), "factor")
+    refused(bad(64, 1e4, cxa.CXA_ROTARY_WAVELENGTH, 2.0, 0.0), "orig_len")
+    refused(bad(64, 1e4, cxa.CXA_ROTARY_WAVELENGTH, 2.0, 100.0, 3.0, 3.0), "alpha")
+    mk = lambda *a: cxa.cxa_rotary_create(*a)[0]
+    refused(mk(64, 0, None), "freq")
+    refused(mk(64, 5, [0.1] * 32), "layout")
+    refused(mk(63, 0, [0.1] * 31), "rot_dim")
+    refused(mk(4, 0, [0.1, -1.0]), "frequencies")
+    refused(mk(4, 0, [0.1, math.inf]), "frequencies")
+    refused(mk(4, 0, [0.1, 1.0], math.nan), "attn_factor")
+    with pytest.raises(ValueError):
+        cxa.Rotary(64, layout="other")
+    with pytest.raises(ValueError):
+        cxa.Rotary(64, freq=[0.1])
+    with pytest.raises(cxa.CxaError):
+        cxa.Rotary(66 * 2)
+
+
+def test_norm_rope_refusals():
+    ok = dict(q=FAKE, q_stride=512, Hq=8, k=FAKE + (1 << 20), k_stride=512, Hk=8, dh=64, n_tokens=3, pos=FAKE,
+              norm=cxa.CXA_NORM_RMS, eps=1e-6, q_weight=0, k_weight=0, rot=None, q_out=FAKE, qo_stride=512,
+              k_out=FAKE, ko_stride=512, dtype=cxa.CXA_BF16, stream=0)
+    call = lambda **kw: cxa.cxa_qk_norm_rope(**dict(ok, **kw))
+    refused(call(dh=32), "head_dim")
+    refused(call(dtype=3), "dtype")
+    refused(call(Hq=0, Hk=0), "Hq and Hk")
+    refused(call(n_tokens=-1), "n_tokens")
+    refused(call(norm=2), "norm")
+    refused(call(eps=-1.0), "eps")
+    refused(call(eps=math.nan), "eps")
+    refused(call(pos=0), "pos")
+    refused(call(q=0), "q is NULL")
+    refused(call(q=FAKE + 8), "q must be 16-byte aligned")
+    refused(call(q_stride=508), "row stride of q")
+    refused(call(q_stride=516), "row stride of q")            # not a multiple of 16 bytes
+    refused(call(k_stride=256), "row stride of k")
+    refused(call(k_out=0), "k_out is NULL")
+    refused(call(q_weight=FAKE + 2), "norm weights")
+    rc, rot = cxa.cxa_rotary_create(128, 0, [0.1] * 64)
+    refused(call(rot=rot), "more channels than a head has")
+    cxa.cxa_rotary_destroy(rot)
+    before = cxa.cxa_launch_count()
+    assert call(n_tokens=0) == cxa.CXA_OK
+    assert cxa.cxa_launch_count() == before
+
+
+# ------------------------------------------------------------------ pages
+def test_pages_create_refusals():
+    refused(make_pages(Kp=0)[0], "NULL")
+    refused(make_pages(Vp=FAKE + 4)[0], "aligned")
+    for size in (0, 8, 24, 512, -16):
+        refused(make_pages(page_size=size)[0], "page_size")
+    refused(make_pages(num_pages=0)[0], "num_pages")
+    refused(make_pages(L=0)[0], "positive")
+    refused(make_pages(Hkv=70000)[0], "65535")
+    refused(make_pages(dh=96)[0], "head_dim")
+    refused(make_pages(dtype=2)[0], "cache_dtype")
+
+
+def append(pages, **kw):
+    a = dict(layer=0, B=2, n_tokens=5, q_start=FAKE, kv_len=FAKE, page_table=FAKE, max_pages=3, k=FAKE, k_stride=256,
+             v=FAKE, v_stride=256, q=None, q_stride=0, Hq=0, q_out=None, qo_stride=0, norm=0, eps=0.0, q_weight=None,
+             k_weight=None, rot=None, dtype=cxa.CXA_BF16, stream=0)
+    a.update(kw)
+    return cxa.cxa_paged_append(pages, **a)
+
+
+def attention(pages, **kw):
+    a = dict(layer=0, B=2, n_tokens=5, max_new=4, q_start=FAKE, kv_len=FAKE, page_table=FAKE, max_pages=3, q=FAKE,
+             q_stride=512, Hq=8, out=FAKE + (1 << 20), o_stride=512, scale=0.0, dtype=cxa.CXA_BF16, workspace=FAKE,
+             workspace_bytes=BIG, stream=0)
+    a.update(kw)
+    return cxa.cxa_paged_attention(pages, **a)
+
+
+@pytest.mark.parametrize("call", [append, attention])
+def test_batch_refusals(pages, call):
+    refused(call(None), "descriptor is NULL")
+    refused(call(pages, layer=2), "layer")
+    refused(call(pages, layer=-1), "layer")
+    refused(call(pages, B=0), "B and max_pages")
+    refused(call(pages, n_tokens=-1), "n_tokens")
+    refused(call(pages, max_pages=0), "max_pages")
+    refused(call(pages, max_pages=(1 << 26) + 1), "2^30")
+    refused(call(pages, q_start=0), "NULL")
+    refused(call(pages, kv_len=FAKE + 1), "aligned")
+    refused(call(pages, dtype=9), "dtype")
+    rc, f32 = make_pages(dtype=cxa.CXA_F32)
+    refused(call(f32), "bf16 pool")
+    cxa.cxa_pages_destroy(f32)
+    before = cxa.cxa_launch_count()
+    assert call(pages, n_tokens=0) == cxa.CXA_OK
+    assert cxa.cxa_launch_count() == before
+
+
+def test_append_refusals(pages):
+    refused(append(pages, k=0), "k is NULL")
+    refused(append(pages, v=FAKE + 2), "v must be 16-byte aligned")
+    refused(append(pages, v_stride=64), "row stride of v")
+    refused(append(pages, q=FAKE, Hq=0), "Hq")
+    refused(append(pages, q=FAKE, Hq=8, q_stride=512, q_out=None), "q_out is NULL")
+    refused(append(pages, norm=1, eps=-1.0), "eps")
+
+
+def test_attention_refusals(pages):
+    refused(attention(pages, Hq=6), "multiple")
+    refused(attention(pages, Hq=0), "multiple")
+    refused(attention(pages, max_new=0), "max_new")
+    refused(attention(pages, scale=math.inf), "scale")
+    refused(attention(pages, out=FAKE), "overlap")
+    refused(attention(pages, out=FAKE + 512), "overlap")
+    refused(attention(pages, workspace=0), "workspace")
+    refused(attention(pages, workspace=FAKE + 16), "256-byte")
+    need = cxa.cxa_paged_attention_workspace_bytes(8, 4, 64, 4)
+    assert need > 0
+    refused(attention(pages, workspace_bytes=need - 1), "workspace smaller")
+    refused(attention(pages, n_tokens=1 << 30, Hq=8), "too many query rows")
+    for args in [(8, 3, 64, 1), (8, 4, 32, 1), (8, 4, 64, 0), (0, 4, 64, 1), (8, 0, 64, 1)]:
+        assert cxa.cxa_paged_attention_workspace_bytes(*args) == 0
+
+
+def test_batch_check_finds_what_the_kernels_would_leave_out(pages):
+    good = dict(B=2, n_tokens=6, q_start=[0, 1, 5], kv_len=[17, 40], page_table=[3, 4, -1, 9, 0, 7], max_pages=3)
+    chk = lambda **kw: cxa.cxa_paged_check(pages, **dict(good, **kw))
+    assert chk() == cxa.CXA_OK
+    refused(chk(page_table=[3, -1, -1, 9, 0, 7]), "entry 1 is not a page of the pool (sequence 0)")
+    refused(chk(page_table=[3, 10, -1, 9, 0, 7]), "entry 1 is not a page")
+    refused(chk(page_table=[3, 4, -1, 9, 0, -5]), "entry 2 is not a page of the pool (sequence 1)")
+    refused(chk(q_start=[1, 1, 5]), "q_start[0]")
+    refused(chk(q_start=[0, 3, 2]), "must not decrease")
+    refused(chk(q_start=[0, 1, 7]), "pass n_tokens")
+    refused(chk(kv_len=[0, 40]), "less than the new tokens")
+    refused(chk(kv_len=[-3, 40]), "less than the new tokens")
+    refused(chk(kv_len=[17, 49]), "passes the table's row")
+    refused(chk(page_table=[3, 7, -1, 9, 0, 7]), "two sequences or positions write one page")
+    refused(chk(page_table=[7, 4, -1, 9, 0, 7]), "is another's")
+    refused(chk(page_table=[3, 4, -1, 9, 7, 7]), "is another's")
+    assert chk(page_table=[9, 4, -1, 9, 0, 7]) == cxa.CXA_OK           # a shared prefix page
+    assert chk(q_start=[0, 0, 4], page_table=[-1, -1, -1, 9, 0, 7]) == cxa.CXA_OK   # nothing new: not looked at
+    assert cxa.cxa_strerror(cxa.CXA_EPAGE).startswith("CXA_EPAGE")
