@@ -97,7 +97,16 @@ struct PagedAttnLaunch {
 };
 
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// Attention, one kernel or two: sequences of up to kFewRows query rows a K/V head go to
+// paged_rows.cu, the others, where paged_tile_takes(), to paged_tile.cu (with the part of
+// the workspace behind the first kernel's); the first kernel takes all of them otherwise.
+constexpr int kFewRows = 16;
 size_t paged_rows_workspace_bytes(int dh);
-cudaError_t launch_paged_rows(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream);
+bool paged_tile_takes(int G, bool act_bf16, int max_new);
+size_t paged_tile_workspace_bytes(int dh);
+cudaError_t launch_paged_tile(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
+                              std::string* msg);
 
 }  // namespace cxa

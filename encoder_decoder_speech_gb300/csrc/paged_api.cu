@@ -257,6 +257,8 @@ int cxa_pages_create(cxa_pages** out, void* Kp, void* Vp, int num_pages, int pag
       return fail(CXA_EINVAL, w + ": page_size must be 16, 32, 64, 128 or 256");
     if (num_pages < 1 || L < 1 || Hkv < 1 || L > 65535 || Hkv > 65535)
       return fail(CXA_EINVAL, w + ": num_pages, L and Hkv must be positive, L and Hkv at most 65535");
+    if (static_cast<long long>(num_pages) * Hkv > 0x7FFFFFFFLL)
+      return fail(CXA_EINVAL, w + ": num_pages * Hkv must be below 2^31");
     if (dh != 64 && dh != 128) return fail(CXA_EINVAL, w + ": head_dim must be 64 or 128");
     if (!valid_dtype(cache_dtype)) return fail(CXA_EINVAL, w + ": cache_dtype must be CXA_F32 or CXA_BF16");
     cxa_pages* c = new (std::nothrow) cxa_pages;
@@ -375,7 +377,9 @@ int cxa_paged_append(const cxa_pages* pages, int layer, int B, int n_tokens, con
 
 size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int max_new) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (dh != 64 && dh != 128) || max_new < 1) return 0;
-  return cxa::paged_rows_workspace_bytes(dh);
+  size_t n = cxa::paged_rows_workspace_bytes(dh);
+  if (cxa::paged_tile_takes(Hq / Hkv, true, max_new)) n += cxa::paged_tile_workspace_bytes(dh);
+  return n;
 }
 
 int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
@@ -423,8 +427,13 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
-    e = cxa::launch_paged_rows(a, dev, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return fail_cuda(e, w + ": launch");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
+    e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);
+    if (e == cudaSuccess && tiles)
+      e = cxa::launch_paged_tile(a, static_cast<uint8_t*>(workspace) + cxa::paged_rows_workspace_bytes(pages->dh), dev,
+                                 s, &msg);
+    if (e != cudaSuccess) return fail_cuda(e, w + ": " + (msg.empty() ? "launch" : msg));
     return CXA_OK;
   });
 }

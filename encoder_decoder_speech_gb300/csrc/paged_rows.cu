@@ -527,10 +527,11 @@ constexpr size_t kCounterBytes = (kMaxBlocks * 4 + 255) / 256 * 256;
 }  // namespace
 
 size_t paged_rows_workspace_bytes(int dh) {
-  return kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4;
+  const size_t n = kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4;
+  return (n + 255) / 256 * 256;
 }
 
-cudaError_t launch_paged_rows(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream) {
   RowsParams prm;
   prm.q = a.q;
   prm.out = a.out;
@@ -547,7 +548,7 @@ cudaError_t launch_paged_rows(const PagedAttnLaunch& a, const DeviceInfo& dev, c
   prm.shape.chunk_shift = kChunkShift;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = 0;
-  prm.shape.max_rows = 0x7FFFFFFF;
+  prm.shape.max_rows = max_rows;
   return a.dh == 64 ? launch_dh<64>(a, prm, dev, stream) : launch_dh<128>(a, prm, dev, stream);
 }
 

@@ -392,6 +392,7 @@ CXA_API int cxa_qk_norm_rope(const void* q, long long q_stride, int Hq, const vo
 /*
  * Descriptor of a caller-owned pool.
  *   Kp, Vp      device [L][num_pages][Hkv][page_size][dh] of cache_dtype, 16-byte aligned.
+ *   num_pages   num_pages * Hkv < 2^31.
  *   page_size   16, 32, 64, 128 or 256 positions.
  *   Hkv         K/V heads; query heads are a multiple of them (query head h reads K/V
  *               head h / (Hq / Hkv)).

@@ -121,6 +121,7 @@ def test_pages_create_refusals():
     for size in (0, 8, 24, 512, -16):
         refused(make_pages(page_size=size)[0], "page_size")
     refused(make_pages(num_pages=0)[0], "num_pages")
+    refused(make_pages(num_pages=1 << 29)[0], "2^31")
     refused(make_pages(L=0)[0], "positive")
     refused(make_pages(Hkv=70000)[0], "65535")
     refused(make_pages(dh=96)[0], "head_dim")
