@@ -15,10 +15,10 @@
 //  * warp 5 issues the products: scores of chunk i + 1 once the softmax warps have read
 //    those of chunk i, then P.V of chunk i. P is read from tensor memory, V as it lies in
 //    shared memory (rows of keys: an MN-major operand).
-//  * warps 0..3 own a row a thread, so that row maxima and sums need no exchange. A row's
-//    reference m moves only when a score passes it by more than 2^8 (decided per warp):
-//    the exponentials are taken at once against the old reference, in one pass over S,
-//    and taken again, with O rescaled, in the rare chunk that moves it.
+//  * warps 0..3 own a row a thread, so that row maxima and sums need no exchange. They take
+//    a row's scores into registers at once, which lets the next chunk's scores start while
+//    the exponentials run. A row's reference m moves, and O is rescaled, only when a score
+//    passes it by more than 2^8 (decided per warp).
 //
 // Bound, at 64 channels, by the exponentials and their bookkeeping together with the
 // products (about 500 clocks each a tile of 128 keys). Tensor memory: S, P and O side by
@@ -362,71 +362,64 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const bool special = key0 + T::chunk > see_all || bad != 0;   // some row does not see some key
         const int lim = see - key0;
 
-        uint32_t P[T::chunk / 2];
-        float mx;
-        float2 sum;
-        // One pass over the row's scores: the largest, and (kExp) the probabilities against m.
-        auto pass = [&](auto exp_tag, auto special_tag) {
-          constexpr bool kExp = decltype(exp_tag)::value, kSpecial = decltype(special_tag)::value;
-          const float ref = m == -INFINITY ? 0.f : -m;
-          const float2 ref2 = make_float2(ref, ref);
-          mx = -INFINITY;
-          sum = make_float2(0.f, 0.f);
-          uint32_t s[2][32];
-          tmem_ld_32x32b_x32(my_tmem, s[0]);
+        // The row's scores, all in registers, so that the next chunk's products can start
+        uint32_t x[T::chunk / 32][32];
 #pragma unroll
-          for (int b = 0; b < T::chunk / 32; ++b) {
-            tmem_ld_wait();
-            if (b + 1 < T::chunk / 32) tmem_ld_32x32b_x32(my_tmem + 32 * (b + 1), s[(b + 1) & 1]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 x = make_float2(__uint_as_float(s[b & 1][2 * e]), __uint_as_float(s[b & 1][2 * e + 1]));
-              if constexpr (kSpecial) {
-                const int k = 32 * b + 2 * e;
-                const bool gone = ((bad >> (k >> box_shift)) & 1u) != 0;   // a box holds both keys
-                if (gone || k >= lim) x.x = -INFINITY;
-                if (gone || k + 1 >= lim) x.y = -INFINITY;
-              }
-              mx = fmaxf(mx, fmaxf(x.x, x.y));
-              if constexpr (kExp) {
-                x = fma2(x, qs2, ref2);
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-                sum = add2(sum, x);
-                P[16 * b + e] = pack_bf16(x.x, x.y);
-              }
-            }
-          }
-        };
-        using Yes = std::integral_constant<bool, true>;
-        using No = std::integral_constant<bool, false>;
-        float corr = 1.f;
-        bool moved = false;
-        auto move = [&]() {    // the reference becomes the largest score so far
-          const float to = fmaxf(m, mx * p.qscale);
-          corr = m == -INFINITY ? 0.f : ex2(m - to);
-          m = to;
-          l *= corr;
-        };
-        if (starts) {
-          if (special) pass(No{}, Yes{}); else pass(No{}, No{});
-          move();
-        }
-        for (;;) {
-          if (special) pass(Yes{}, Yes{}); else pass(Yes{}, No{});
-          if (starts || moved || !__any_sync(0xffffffffu, mx * p.qscale > m + kMoveLog2)) break;
-          move();
-          moved = true;
-        }
-        l += sum.x + sum.y;
+        for (int b = 0; b < T::chunk / 32; ++b) tmem_ld_32x32b_x32(my_tmem + 32 * b, x[b]);
+        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSFree));
+        if (special) {
+#pragma unroll
+          for (int b = 0; b < T::chunk / 32; ++b)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int k = 32 * b + e;
+              if (k >= lim || ((bad >> (k >> box_shift)) & 1u) != 0) x[b][e] = 0xFF800000u;   // -inf
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < T::chunk / 32; ++b)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e / 2) & 3] = fmaxf(mx[(e / 2) & 3], fmaxf(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+        // the references of a warp's rows move together, to the largest score so far
+        float corr = 1.f;
+        const bool moved = __any_sync(0xffffffffu, top > m + kMoveLog2);
+        if (moved) {
+          const float to = fmaxf(m, top);
+          corr = m == -INFINITY ? 0.f : ex2(m - to);
+          m = to;
+          l *= corr;
+        }
+        {
+          const float ref = m == -INFINITY ? 0.f : -m;
+          const float2 ref2 = make_float2(ref, ref);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int b = 0; b < T::chunk / 32; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 v = make_float2(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1]));
+              v = fma2(v, qs2, ref2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              sum[e & 1] = add2(sum[e & 1], v);
+              x[b / 2][16 * (b & 1) + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
+            }
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+        }
 
         // P's place and O are free once the previous P.V has run
         if (i > 0) wait_warp(kPvDone, (i - 1) & 1);
         tc_fence_after();
-        if (moved) {
+        if (moved && !starts) {
 #pragma unroll
           for (int b = 0; b < kDh / 32; ++b) {
             uint32_t o[32];
@@ -438,12 +431,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           }
         }
 #pragma unroll
-        for (int b = 0; b < T::chunk / 64; ++b) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = P[32 * b + e];
-          tmem_st_32x32b_x32(my_tmem + T::p_col + 32 * b, w);
-        }
+        for (int b = 0; b < T::chunk / 64; ++b) tmem_st_32x32b_x32(my_tmem + T::p_col + 32 * b, x[b]);
         tmem_st_wait();
 
         if (special) {
@@ -582,8 +570,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 return p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTileRows * (kDh + 2) + tid;
               };
               float M = -INFINITY, L = 0.f;
+#pragma unroll 4
               for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k) + kDh * kTileRows));
               const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
               for (int k = 0; k < parts; ++k)
                 L += __ldcg(part(k) + (kDh + 1) * kTileRows) * ex2(__ldcg(part(k) + kDh * kTileRows) - ref);
               const float linv = L > 0.f || L != L ? 1.f / L : 0.f;
@@ -592,11 +582,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 2
                 for (int k = 0; k < parts; ++k) {
                   const float* src = part(k);
                   const float f = ex2(__ldcg(src + kDh * kTileRows) - ref);
+                  float w[32];
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = fmaf(f, __ldcg(src + (32 * b + e) * kTileRows), o[e]);
+                  for (int e = 0; e < 32; ++e) w[e] = __ldcg(src + (32 * b + e) * kTileRows);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = fmaf(f, w[e], o[e]);
                 }
                 put(b, o, linv);
               }
