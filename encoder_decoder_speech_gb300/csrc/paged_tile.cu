@@ -3,34 +3,39 @@
 //
 //   S = Q K^T (128 rows x a chunk of keys), P = 2^(scale log2(e) S - m), O += P V
 //
-// A work item is a tile of 128 query rows (128 / G tokens times the G query heads of one
-// K/V head), dealt out by paged_work.cuh in chunks of 16 KB of K and of V (128 keys of 64
-// channels, 64 keys of 128). Two blocks share an SM, each with its own tile, so that one
-// block's products run under the other's exponentials:
+// A work item is a pair of 128-row tiles (a tile: 128 / G tokens times the G query heads of
+// one K/V head), dealt out by paged_work.cuh in chunks of 16 KB of K and of V (128 keys of
+// 64 channels, 64 keys of 128). One block runs on an SM and works on both tiles of its item,
+// which share each K and V tile read (a block a tile, two blocks an SM, read twice as much:
+// 417 us against {NEW} us for 2048 tokens over 32768 keys of 20 heads, its K and V coming 11
+// times from DRAM); one tile's products run under the other's exponentials:
 //
-//  * warp 4 streams by TMA: the item's Q (a box of 128 / G tokens x G heads, which lands
-//    token by token, the row order of a tile), and K and V page by page into rings of two
-//    and three tiles; the boxes of a chunk are issued by a lane each. A K tile comes back
-//    as soon as its scores are done, a V tile after its P.V.
-//  * warp 5 issues the products: scores of chunk i + 1 once the softmax warps have read
-//    those of chunk i, then P.V of chunk i. P is read from tensor memory, V as it lies in
-//    shared memory (rows of keys: an MN-major operand).
-//  * warps 0..3 own a row a thread, so that row maxima and sums need no exchange. They take
-//    a row's scores into registers at once, which lets the next chunk's scores start while
-//    the exponentials run. A row's reference m moves, and O is rescaled, only when a score
-//    passes it by more than 2^8 (decided per warp).
+//  * warp 10 streams by TMA: the item's Q (a box of 128 / G tokens x G heads a tile, which
+//    lands token by token, the row order of a tile), and K and V page by page into rings of
+//    five tiles each; the boxes of a chunk are issued by a lane each. A K tile comes back as
+//    soon as both tiles' scores are done, a V tile after both P.V.
+//  * warps 8 and 9 issue the products of a tile each: scores of chunk i + 1 once the softmax
+//    warps have read those of chunk i, then P.V of chunk i. P is read from tensor memory, V
+//    as it lies in shared memory (rows of keys: an MN-major operand).
+//  * warps 0..3 and 4..7 own a row a thread, so that row maxima and sums need no exchange.
+//    They take a row's scores into registers at once, which lets the next chunk's scores
+//    start while the exponentials run. A row's reference m moves, and O is rescaled, only
+//    when a score passes it by more than 2^8 (decided per warp).
+//
+// A tile whose last token sees fewer keys than its neighbour's leaves the item's last chunks
+// out (its softmax warps then hand the K and V tiles back).
 //
 // Bound, at 64 channels, by the exponentials and their bookkeeping together with the
 // products (about 500 clocks each a tile of 128 keys). Tensor memory: S, P and O side by
-// side in 256 columns a block.
+// side in 256 columns a tile.
 //
 // P is rounded to one bf16 value (2^-9 of each weight, against the 2^-8 of the bf16
 // output); sums, references and O are fp32, the sums of the values before rounding.
 //
-// Keys behind a tile's last visible one weigh 0 and their V rows, which may hold anything,
+// Keys behind an item's last visible one weigh 0 and their V rows, which may hold anything,
 // are zeroed in shared memory before P.V. Keys that some rows see and others do not weigh
 // 0 in the others; if one of them has a V that is not finite (0 * inf), those keys are
-// added row by row on the CUDA cores instead.
+// added row by row on the CUDA cores instead. Both tiles' softmax warps meet in such chunks.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -44,31 +49,45 @@
 namespace cxa {
 namespace {
 
-constexpr int kSoftWarps = 4;
-constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kTiles = 2;                    // of an item
+constexpr int kSoftWarps = 4;                // a tile
+constexpr int kMmaWarp = kTiles * kSoftWarps, kTmaWarp = kMmaWarp + kTiles;
+constexpr int kThreads = (kTmaWarp + 1) * 32;
 constexpr int kTileRows = 128;
 constexpr int kTileBytes = 16384;            // K or V of a chunk
-constexpr int kKStages = 2, kVStages = 3;
-constexpr int kQBytes = 32768;               // two Q tiles of 64 channels, one of 128
-constexpr int kBlocksPerSm = 2;
-constexpr int kMaxBlocks = 160 * kBlocksPerSm;
-constexpr uint32_t kTmemCols = 256;
+constexpr int kStages = 5;                   // of K and of V
+constexpr int kQBytes = 65536;               // the Q tiles of two items of 64 channels, of one of 128
+constexpr int kMaxBlocks = 160;
+constexpr uint32_t kTmemTile = 256;          // columns of a tile
 constexpr float kMoveLog2 = 8.f;
 
-enum Bars { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 11, kSFull = 14, kSFree, kPFull, kPvDone, kBars };
-
+// Barriers; the last four one a tile.
+enum Bars {
+  kQFull = 0,
+  kQEmpty = kQFull + 2,
+  kKFull = kQEmpty + 2,
+  kKEmpty = kKFull + kStages,
+  kVFull = kKEmpty + kStages,
+  kVEmpty = kVFull + kStages,
+  kSFull = kVEmpty + kStages,
+  kSFree = kSFull + kTiles,
+  kPFull = kSFree + kTiles,
+  kPvDone = kPFull + kTiles,
+  kBars = kPvDone + kTiles
+};
+static_assert(kBars <= 32, "a bit mask holds the barriers");
 struct Small {
   uint64_t bars[kBars];
   WorkScratch work;
-  uint32_t bad[4];          // boxes of chunk i whose page is outside the pool, at i % 4
+  WorkCursor at[kTiles * kSoftWarps];   // the softmax warps' items: registers hold scores
+  uint32_t bad[8];          // boxes of chunk i whose page is outside the pool, at i % 8
   volatile int abort;
   int tmem;
-  int last;
-  volatile int acc;         // the segment's first P.V adds to O
+  int last[kTiles];
+  volatile int acc[kTiles]; // the segment's first P.V adds to O
 };
 
-constexpr int kSmemBytes = kQBytes + (kKStages + kVStages) * kTileBytes + 1024;
+constexpr int kSmemBytes = kQBytes + 2 * kStages * kTileBytes + 1024;
 static_assert(sizeof(Small) <= 1024, "the small arrays fit behind the tiles");
 
 template <int kDh>
@@ -86,8 +105,8 @@ struct TileParams {
   void* out;
   long long o_stride;
   float qscale;
-  unsigned int* counters;
-  float* part;               // [2 * grid][kDh + 2][128]
+  unsigned int* counters;    // [grid][kTiles]
+  float* part;               // [2 * grid][kTiles][kDh + 2][128]
   unsigned int* status;
   PagedBatch batch;
   int num_pages, Hkv, page_shift;
@@ -99,13 +118,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool named_or(bool v) {
+// The softmax warps of a tile, and of both.
+__device__ __forceinline__ void tile_sync(int tile) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + tile) : "memory");
+}
+__device__ __forceinline__ void item_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool item_or(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "bar.red.or.pred q, 3, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(v))
@@ -132,6 +155,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&p);
 }
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ uint32_t tmem_ld_1(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
@@ -145,6 +184,36 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+// One attempt that may sleep until the phase completes, 1 ms at most.
+__device__ __forceinline__ bool mbar_try_wait_1ms(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The halves of the descriptors of smem_desc_k_sw128 (leading offset 16 bytes: unused) and
+// smem_desc_mn_sw128 (1024): the address moves the low half alone.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (leading_bytes >> 4) << 16;
+}
+constexpr uint64_t desc_high(uint32_t stride_bytes) {
+  return static_cast<uint64_t>(stride_bytes >> 4 | 1u << 14 | 2u << 29) << 32;
+}
 // D[tmem] (+)= A[tmem] * B[smem]: one thread issues.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -157,18 +226,31 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 template <int kDh>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   using T = Tile<kDh>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  const uint32_t q_base = base, k_base = base + kQBytes, v_base = k_base + kKStages * kTileBytes;
-  Small* sm = reinterpret_cast<Small*>(smem + kQBytes + (kKStages + kVStages) * kTileBytes);
+  const uint32_t q_base = base, k_base = base + kQBytes, v_base = k_base + kStages * kTileBytes;
+  Small* sm = reinterpret_cast<Small*>(smem + kQBytes + 2 * kStages * kTileBytes);
   auto bar = [&](int i) { return smem_u32(&sm->bars[i]); };
+  // tile t of Q buffer qb
+  auto q_tile = [&](int qb, int t) {
+    return q_base + static_cast<uint32_t>((qb * kTiles + t) * (kTileRows * kDh * 2));
+  };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedBatch& bt = p.batch;
-  const int G = p.shape.G;
+  const int G = p.shape.G, tile_rows = p.shape.rows / kTiles;
+  // rows, keys and chunks of tile t of an item
+  auto rows_of = [&](const WorkCursor& w, int t) {
+    return max(0, min(tile_rows, work_rows(w.seq, p.shape) - w.rt * p.shape.rows - t * tile_rows));
+  };
+  auto chunks_of = [&](const WorkCursor& w, int t) {
+    if (rows_of(w, t) == 0) return 0;
+    const int last = min(w.seq.n - 1, (w.rt * p.shape.rows + (t + 1) * tile_rows - 1) / G);
+    return max(1, (visible_keys(w.seq, last, p.shape.cap) + T::chunk - 1) >> T::chunk_shift);
+  };
 
   // Launched behind paged_rows_kernel of the same call, which lets this grid start only
   // after it has waited for everything before it; the two touch different rows and
@@ -178,10 +260,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const bool active = work_locate<kThreads>(bt, p.shape, p.Hkv, &sm->work, &range, &cur);
   if (active) {
     if (tid == 0) {
-      for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kSFree || i == kPFull ? kSoftWarps : 1);
+      for (int i = 0; i < kBars; ++i) {
+        const bool by_tiles = (i >= kQEmpty && i < kKFull) || (i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kSFull);
+        mbar_init(bar(i), by_tiles ? kTiles : i >= kSFree && i < kPvDone ? kSoftWarps : 1);
+      }
       fence_mbar_init();
       sm->abort = 0;
-      sm->acc = 0;
     }
     if (warp == kTmaWarp && lane == 0) {
       prefetch_tmap(&tmQ);
@@ -189,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       prefetch_tmap(&tmV);
     }
     if (warp == kMmaWarp) {
-      tmem_alloc(smem_u32(&sm->tmem), kTmemCols);
+      tmem_alloc(smem_u32(&sm->tmem), kTiles * kTmemTile);
       tmem_relinquish();
     }
     tc_fence_before();
@@ -201,10 +285,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     // included, without waiting for anything or writing results.
     bool ok = true;
     auto wait = [&](int i, uint32_t parity) {      // by one thread
-      if (ok && !mbar_wait(bar(i), parity, &sm->abort)) {
-        ok = false;
-        sm->abort = 1;
-        atomicOr(p.status, kStatusTimeout);
+      // (the code after the first attempt is short: it stands in the softmax warps' loop)
+      uint64_t t0 = 0;
+      while (ok && __builtin_expect(!mbar_try_wait_1ms(bar(i), parity), 0)) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (sm->abort != 0 || now - t0 > kWaitLimitNs) {
+          ok = false;
+          sm->abort = 1;
+          atomicOr(p.status, kStatusTimeout);
+        }
       }
       return ok;
     };
@@ -221,7 +311,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const int box_rows = 1 << ps_shift;                // keys a box
       const int box = lane / T::halves, half = lane % T::halves;
       const bool mine = box < (T::chunk >> ps_shift);
-      const int q_tokens = p.shape.rows / G;
       int c = cur.c, item = 0;
       bool fresh = true;
       uint32_t armed = 0, parity = 0;                    // barriers copies were sent to, and the phase
@@ -233,11 +322,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (fresh) {
           const int qb = item % T::q_bufs;
           if (!wait_warp(kQEmpty + qb, ((item / T::q_bufs) & 1) ^ 1)) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(kQFull + qb), static_cast<uint32_t>(T::halves * p.shape.rows * 128));
+          const int tiles = rows_of(cur, 1) > 0 ? 2 : 1;
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(kQFull + qb), static_cast<uint32_t>(tiles * T::halves * tile_rows * 128));
           __syncwarp();
-          if (lane < T::halves)
-            tma_load_3d(q_base + qb * (kQBytes / 2) + lane * (kTileRows * 128), &tmQ, bar(kQFull + qb), lane * 64,
-                        cur.h * G, cur.seq.q0 + cur.rt * q_tokens);
+          if (lane < tiles * T::halves)
+            tma_load_3d(q_tile(qb, lane / T::halves) + (lane % T::halves) * (kTileRows * 128), &tmQ, bar(kQFull + qb),
+                        (lane % T::halves) * 64, cur.h * G,
+                        cur.seq.q0 + (cur.rt * kTiles + lane / T::halves) * (tile_rows / G));
           sent(kQFull + qb, item / T::q_bufs);
           fresh = false;
         }
@@ -253,23 +345,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, load)) * box_rows * 128);
         const int x = half * 64, y = at & ((1 << p.page_shift) - 1), z = page * p.Hkv + cur.h;
         const uint32_t dst = static_cast<uint32_t>(half * T::half_bytes + box * box_rows * 128);
-        const int ks = i % kKStages, vs = i % kVStages;
-        if (!wait_warp(kKEmpty + ks, ((i / kKStages) & 1) ^ 1)) break;
+        const int st = i % kStages, round = i / kStages;
+        if (!wait_warp(kKEmpty + st, (round & 1) ^ 1)) break;
         if (lane == 0) {
           uint32_t boxes = 0;    // a bit a box
           for (uint32_t m = bad; m != 0; m &= m - 1) boxes |= 1u << ((__ffs(m) - 1) / T::halves);
-          sm->bad[i & 3] = boxes;
+          sm->bad[i & 7] = boxes;
           if (bad != 0) atomicOr(p.status, kStatusBadPage);
-          mbar_arrive_expect_tx(bar(kKFull + ks), bytes);
+          mbar_arrive_expect_tx(bar(kKFull + st), bytes);
         }
         __syncwarp();
-        if (load) tma_load_3d(k_base + ks * kTileBytes + dst, &tmK, bar(kKFull + ks), x, y, z);
-        sent(kKFull + ks, i / kKStages);
-        if (!wait_warp(kVEmpty + vs, ((i / kVStages) & 1) ^ 1)) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + vs), bytes);
+        if (load) tma_load_3d(k_base + st * kTileBytes + dst, &tmK, bar(kKFull + st), x, y, z);
+        sent(kKFull + st, round);
+        if (!wait_warp(kVEmpty + st, (round & 1) ^ 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + st), bytes);
         __syncwarp();
-        if (load) tma_load_3d(v_base + vs * kTileBytes + dst, &tmV, bar(kVFull + vs), x, y, z);
-        sent(kVFull + vs, i / kVStages);
+        if (load) tma_load_3d(v_base + st * kTileBytes + dst, &tmV, bar(kVFull + st), x, y, z);
+        sent(kVFull + st, round);
         if (++c == cur.nc && i + 1 < n_chunks) {
           work_next(bt, p.shape, p.Hkv, &cur);
           c = 0;
@@ -280,110 +372,129 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (!ok)      // the copies under way land before the block ends
         for (int b = 0; b < kBars; ++b)
           if (armed & (1u << b)) mbar_wait(bar(b), (parity >> b) & 1u);
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = make_idesc(1u, kTileRows, T::chunk);
-        constexpr uint32_t idesc_o = make_idesc(1u, kTileRows, 64) | (1u << 16);   // V MN-major
-        int c = cur.c, nc = cur.nc;           // of the scores, one chunk ahead
-        int item = 0;
-        bool fresh = true;
-        auto scores = [&](int i) {
-          const int qb = item % T::q_bufs, ks = i % kKStages;
-          if (fresh && !wait(kQFull + qb, (item / T::q_bufs) & 1)) return;
-          fresh = false;
-          if (!wait(kKFull + ks, (i / kKStages) & 1)) return;
-          if (i > 0 && !wait(kSFree, (i - 1) & 1)) return;
-          tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < T::halves; ++h) {
-            const uint64_t qd = smem_desc_k_sw128(q_base + qb * (kQBytes / 2) + h * (kTileRows * 128));
-            const uint64_t kd = smem_desc_k_sw128(k_base + ks * kTileBytes + h * T::half_bytes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16(tmem, qd + 2 * k, kd + 2 * k, idesc_s, h + k != 0 ? 1u : 0u);
-          }
-          tc_commit(bar(kSFull));
-          tc_commit(bar(kKEmpty + ks));
-          if (++c == nc && i + 1 < n_chunks) {
-            tc_commit(bar(kQEmpty + qb));
+    } else if (warp >= kMmaWarp) {
+      // ---------------------------------------------------------------- products of a tile
+      // The whole warp walks the chunks, with one lane issuing, and the operands' addresses are
+      // known to be the same in every lane: a product of 32 or 64 clocks leaves no time to
+      // carry them over from a lane's registers one by one.
+      constexpr uint32_t idesc_s = make_idesc(1u, kTileRows, T::chunk);
+      constexpr uint32_t idesc_o = make_idesc(1u, kTileRows, 64) | (1u << 16);   // V MN-major
+      const int t = warp - kMmaWarp;
+      const uint32_t my = __shfl_sync(0xffffffffu, tmem + t * kTmemTile, 0);
+      constexpr uint64_t k_hi = desc_high(1024), mn_hi = desc_high(1024);
+      // the scores' cursor: chunk i of the range, chunk c of the item, j of the tile's own
+      int i = -1, c = cur.c - 1, item = 0, j = 0, nc = chunks_of(cur, t);
+      bool fresh = true;      // the item's Q has not been waited for
+      // To the tile's next chunk; false at the end of the range.
+      auto next = [&]() {
+        for (;;) {
+          if (++i == n_chunks) return false;
+          if (++c == cur.nc) {
+            // a Q that this tile has no (more) scores of goes back at once, or behind them
+            if (fresh) {
+              if (!wait_warp(kQFull + item % T::q_bufs, (item / T::q_bufs) & 1)) return false;
+              if (lane == 0) mbar_arrive(bar(kQEmpty + item % T::q_bufs));
+            } else if (elect_one()) {
+              tc_commit(bar(kQEmpty + item % T::q_bufs));
+            }
+            __syncwarp();
             work_next(bt, p.shape, p.Hkv, &cur);
-            nc = cur.nc;
             c = 0;
             ++item;
             fresh = true;
+            nc = chunks_of(cur, t);
           }
-        };
-        bool first = true;
-        scores(0);
-        for (int i = 0; i < n_chunks && ok; ++i) {
-          const bool starts = first;          // chunk i starts a segment
-          first = fresh && i + 1 < n_chunks;  // the scores' cursor stands at chunk i + 1 here
-          if (i + 1 < n_chunks) scores(i + 1);
-          const int vs = i % kVStages;
-          if (!wait(kPFull, i & 1) || !wait(kVFull + vs, (i / kVStages) & 1)) break;
-          tc_fence_after();
-          const uint32_t acc0 = !starts || sm->acc != 0 ? 1u : 0u;
+          if (c < nc) return true;
+        }
+      };
+      auto scores = [&]() {
+        const int qb = item % T::q_bufs, st = i % kStages;
+        if (fresh && !wait_warp(kQFull + qb, (item / T::q_bufs) & 1)) return;
+        fresh = false;
+        if (!wait_warp(kKFull + st, (i / kStages) & 1)) return;
+        if (j > 0 && !wait_warp(kSFree + t, (j - 1) & 1)) return;
+        tc_fence_after();
+        const uint32_t ql = __shfl_sync(0xffffffffu, desc_low(q_tile(qb, t), 16), 0);
+        const uint32_t kl = __shfl_sync(0xffffffffu, desc_low(k_base + st * kTileBytes, 16), 0);
+        const uint32_t k_empty = __shfl_sync(0xffffffffu, bar(kKEmpty + st), 0);
+        if (elect_one()) {
 #pragma unroll
-          for (int kb = 0; kb < T::chunk / 16; ++kb)
+          for (int h = 0; h < T::halves; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)      // 16 channels: 32 bytes
+              mma_bf16(my, k_hi | (ql + (h * (kTileRows * 128) >> 4) + 2 * k),
+                       k_hi | (kl + (h * T::half_bytes >> 4) + 2 * k), idesc_s, h + k != 0 ? 1u : 0u);
+          tc_commit(bar(kSFull + t));
+          tc_commit(k_empty);
+        }
+        __syncwarp();
+        ++j;
+      };
+      bool more = next(), starts = true;
+      if (more) scores();
+      for (int pj = 0; more && ok; ++pj) {     // P.V of the tile's chunk pj
+        const int st = i % kStages, round = i / kStages;
+        // The next scores go first, so that the softmax warps find them; but not those of
+        // another item, whose copies may wait for this P.V.
+        const bool same = c + 1 < nc && i + 1 < n_chunks;
+        if (same) {
+          ++i;
+          ++c;
+          scores();
+        }
+        if (!ok || !wait_warp(kVFull + st, round & 1) || !wait_warp(kPFull + t, pj & 1)) break;
+        tc_fence_after();
+        const uint32_t acc0 = !starts || sm->acc[t] != 0 ? 1u : 0u;
+        const uint32_t vl = __shfl_sync(0xffffffffu, desc_low(v_base + st * kTileBytes, 1024), 0);
+        const uint32_t v_empty = __shfl_sync(0xffffffffu, bar(kVEmpty + st), 0);
+        const uint32_t acc = __shfl_sync(0xffffffffu, acc0, 0);
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 0; kb < T::chunk / 16; ++kb)     // 16 keys: 2048 bytes
 #pragma unroll
             for (int h = 0; h < T::halves; ++h)
-              mma_bf16_ts(tmem + T::o_col + h * 64, tmem + T::p_col + kb * 8,
-                          smem_desc_mn_sw128(v_base + vs * kTileBytes + h * T::half_bytes + kb * 2048), idesc_o,
-                          kb != 0 ? 1u : acc0);
-          tc_commit(bar(kPvDone));
-          tc_commit(bar(kVEmpty + vs));
+              mma_bf16_ts(my + T::o_col + h * 64, my + T::p_col + kb * 8,
+                          mn_hi | (vl + ((h * T::half_bytes + kb * 2048) >> 4)), idesc_o, kb != 0 ? 1u : acc);
+          tc_commit(bar(kPvDone + t));
+          tc_commit(v_empty);
+        }
+        __syncwarp();
+        starts = !same;
+        if (!same) {
+          more = next();
+          if (more) scores();
         }
       }
       __syncwarp();
     } else {
       // ---------------------------------------------------------------- softmax, a row a thread
-      const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      const int t = warp / kSoftWarps, r = tid - t * kTileRows;
+      const uint32_t my_tmem = tmem + t * kTmemTile + (static_cast<uint32_t>((warp % kSoftWarps) * 32) << 16);
       const int box_shift = min(p.page_shift, T::chunk_shift);
       const float2 qs2 = make_float2(p.qscale, p.qscale);
-      int c = cur.c, c0 = cur.c;
+      WorkCursor& at = sm->at[warp];
+      if (lane == 0) at = cur;
+      __syncwarp();
+      int c = cur.c, c0 = cur.c, nc = 0, j = 0;       // j: chunks of this tile so far
       float m = -INFINITY, l = 0.f;
-      int row0 = 0, rows = 0, see = 0, see_all = 0, keys = 0;
-      bool starts = true;
-      for (int i = 0; i < n_chunks; ++i) {
-        if (starts) {
-          row0 = cur.rt * p.shape.rows;
-          rows = min(p.shape.rows, work_rows(cur.seq, p.shape) - row0);
-          see = tid < rows ? visible_keys(cur.seq, (row0 + tid) / G, p.shape.cap) : 0;
-          see_all = visible_keys(cur.seq, row0 / G, p.shape.cap);
-          keys = tile_keys(cur.seq, p.shape, cur.rt);
-          m = -INFINITY;
-          l = 0.f;
-          c0 = c;
-        }
-        const int key0 = c << T::chunk_shift;
-        wait_warp(kSFull, i & 1);
-        tc_fence_after();
-        const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[i & 3]);
-        const bool special = key0 + T::chunk > see_all || bad != 0;   // some row does not see some key
-        const int lim = see - key0;
-
-        // The row's scores, all in registers, so that the next chunk's products can start
-        uint32_t x[T::chunk / 32][32];
+      bool fresh = true;
+      constexpr int XB = T::chunk / 32;
+      // The row's scores, all in registers, so that the next chunk's products can start.
+      auto load_scores = [&](uint32_t (&x)[XB][32]) {
 #pragma unroll
-        for (int b = 0; b < T::chunk / 32; ++b) tmem_ld_32x32b_x32(my_tmem + 32 * b, x[b]);
+        for (int b = 0; b < XB; ++b) tmem_ld_32x32b_x32(my_tmem + 32 * b, x[b]);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kSFree));
-        if (special) {
-#pragma unroll
-          for (int b = 0; b < T::chunk / 32; ++b)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int k = 32 * b + e;
-              if (k >= lim || ((bad >> (k >> box_shift)) & 1u) != 0) x[b][e] = 0xFF800000u;   // -inf
-            }
-        }
+        if (lane == 0) mbar_arrive(bar(kSFree + t));
+      };
+      // Scores -> probabilities, which go to tensor memory; m, l and O follow.
+      auto softmax = [&](uint32_t (&x)[XB][32]) {
         float mx[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = -INFINITY;
+        for (int q = 0; q < 4; ++q) mx[q] = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < T::chunk / 32; ++b)
+        for (int b = 0; b < XB; ++b)
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             mx[(e / 2) & 3] = fmaxf(mx[(e / 2) & 3], fmaxf(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])));
@@ -391,135 +502,204 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         // the references of a warp's rows move together, to the largest score so far
         float corr = 1.f;
         const bool moved = __any_sync(0xffffffffu, top > m + kMoveLog2);
-        if (moved) {
+        if (__builtin_expect(moved, 0)) {
           const float to = fmaxf(m, top);
           corr = m == -INFINITY ? 0.f : ex2(m - to);
           m = to;
           l *= corr;
         }
-        {
-          const float ref = m == -INFINITY ? 0.f : -m;
-          const float2 ref2 = make_float2(ref, ref);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float ref = m == -INFINITY ? 0.f : -m;
+        const float2 ref2 = make_float2(ref, ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int b = 0; b < T::chunk / 32; ++b)
+        for (int b = 0; b < XB; ++b)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 v = make_float2(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1]));
-              v = fma2(v, qs2, ref2);
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              sum[e & 1] = add2(sum[e & 1], v);
-              x[b / 2][16 * (b & 1) + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
-            }
-          sum[0] = add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-        }
+          for (int e = 0; e < 16; ++e) {
+            float2 v = make_float2(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1]));
+            v = fma2(v, qs2, ref2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum[e & 1] = add2(sum[e & 1], v);
+            x[b / 2][16 * (b & 1) + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
+          }
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
 
         // P's place and O are free once the previous P.V has run
-        if (i > 0) wait_warp(kPvDone, (i - 1) & 1);
+        if (j > 0) wait_warp(kPvDone + t, (j - 1) & 1);
         tc_fence_after();
-        if (moved && !starts) {
-#pragma unroll
-          for (int b = 0; b < kDh / 32; ++b) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+        if (__builtin_expect(moved && c != c0, 0)) {
+#pragma unroll 1
+          for (int b = 0; b < kDh / 16; ++b) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(my_tmem + T::o_col + 16 * b, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st_32x32b_x16(my_tmem + T::o_col + 16 * b, o);
           }
         }
 #pragma unroll
-        for (int b = 0; b < T::chunk / 64; ++b) tmem_st_32x32b_x32(my_tmem + T::p_col + 32 * b, x[b]);
+        for (int b = 0; b < XB / 2; ++b) tmem_st_32x32b_x32(my_tmem + T::p_col + 32 * b, x[b]);
         tmem_st_wait();
+      };
+      auto give_p = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + t));
+      };
+      for (int i = 0; i < n_chunks; ++i) {
+        if (fresh) {
+          fresh = false;
+          nc = chunks_of(at, t);
+          m = -INFINITY;
+          l = 0.f;
+          c0 = c;
+          if (r == 0) sm->acc[t] = 0;
+        }
+        // The chunks that every row of the item sees, but for the tile's last, in a loop of
+        // their own: the code between two of them is fetched anew for each by every warp.
+        const int plain =
+            min(min(visible_keys(at.seq, at.rt * p.shape.rows / G, p.shape.cap) >> T::chunk_shift, nc - 1) - c,
+                n_chunks - 1 - i);
+        for (int e = i + plain; i < e; ++i) {
+          wait_warp(kSFull + t, j & 1);
+          tc_fence_after();
+          if (__builtin_expect(*const_cast<volatile uint32_t*>(&sm->bad[i & 7]) != 0, 0)) break;
+          uint32_t x[XB][32];
+          load_scores(x);
+          softmax(x);
+          give_p();
+          ++j;
+          ++c;
+        }
+        const int row0 = at.rt * p.shape.rows + t * tile_rows, rows = rows_of(at, t);
+        const int see = r < rows ? visible_keys(at.seq, (row0 + r) / G, p.shape.cap) : 0;
+        const int see_all = visible_keys(at.seq, row0 / G, p.shape.cap);                       // all of the tile's rows
+        const int see_item = visible_keys(at.seq, at.rt * p.shape.rows / G, p.shape.cap);      // and of the item's
+        const int keys = tile_keys(at.seq, p.shape, at.rt);                                    // some of the item's
+        const int key0 = c << T::chunk_shift;
+        const int st = i % kStages, round = i / kStages;
+        const bool here = c < nc;                          // the tile sees some of the chunk
+        const bool starts = c == c0, ends = here && (c + 1 == nc || i + 1 == n_chunks);
+        const int lim = see - key0;
+        if (here) {
+          wait_warp(kSFull + t, j & 1);
+          tc_fence_after();
+        } else {
+          wait_warp(kKFull + st, round & 1);
+        }
+        const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[i & 7]);
+        const bool special = key0 + T::chunk > see_item || bad != 0;   // some row of the item misses a key
+        if (!here) {
+          tile_sync(t);         // every warp of the tile has seen the chunk come
+          if ((warp % kSoftWarps) == 0 && lane == 0) mbar_arrive(bar(kKEmpty + st));
+          __syncwarp();
+        }
+        if (here) {
+          uint32_t x[XB][32];
+          load_scores(x);
+          if (key0 + T::chunk > see_all || bad != 0) {
+#pragma unroll
+            for (int b = 0; b < XB; ++b)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int k = 32 * b + e;
+                if (k >= lim || ((bad >> (k >> box_shift)) & 1u) != 0) x[b][e] = 0xFF800000u;   // -inf
+              }
+          }
+          softmax(x);
+        }
 
         if (special) {
-          // keys [lo, hi) of the chunk are seen by some rows and not by others, keys from hi
-          // on by none
-          const int lo = max(0, see_all - key0), hi = min(T::chunk, keys - key0);
-          const int vs = i % kVStages;
-          wait_warp(kVFull + vs, (i / kVStages) & 1);
-          const int key = tid & (T::chunk - 1), half = tid >> T::chunk_shift;   // this thread's part of V
-          const bool has = T::chunk * T::halves > tid;
+          // keys [lo, hi) of the chunk are seen by some rows of the item and not by others,
+          // keys from hi on by none
+          const int lo = max(0, see_item - key0), hi = min(T::chunk, keys - key0);
+          wait_warp(kVFull + st, round & 1);
+          const int key = r & (T::chunk - 1), half = r >> T::chunk_shift;   // this thread's part of V
+          const bool has = T::chunk * T::halves > r;
           const bool key_bad = ((bad >> (key >> box_shift)) & 1u) != 0;
-          const uint32_t vt = v_base + vs * kTileBytes;
+          const uint32_t vt = v_base + st * kTileBytes;
           const uint32_t vrow = vt + half * T::half_bytes + key * 128;
           bool wild = false;
           if (has && key >= lo && key < hi && !key_bad)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 u = ld_shared_v4(vrow + 16 * j);
+            for (int q = 0; q < 8; ++q) {
+              const uint4 u = ld_shared_v4(vrow + 16 * q);
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) wild |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
             }
-          wild = named_or(wild);
+          wild = item_or(wild);
           if (wild) {
-            for (int b = 0; b < kDh / 32; ++b) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
-              tmem_ld_wait();
-              if (starts)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0u;
-              for (int j = lo; j < hi; ++j) {
-                const uint32_t w = tmem_ld_1(my_tmem + T::p_col + (j >> 1));
+            if (here) {
+              for (int b = 0; b < kDh / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
                 tmem_ld_wait();
-                if (j < lim && ((bad >> (j >> box_shift)) & 1u) == 0) {
-                  const float pj = __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
-                  const uint32_t vr = vt + (b / 2) * T::half_bytes + j * 128;
+                if (starts)
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const uint4 u = ld_shared_v4(vr + (((4 * (b & 1) + q) ^ (j & 7)) << 4));
-                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                  for (int e = 0; e < 32; ++e) o[e] = 0u;
+                for (int k = lo; k < hi; ++k) {
+                  const uint32_t w = tmem_ld_1(my_tmem + T::p_col + (k >> 1));
+                  tmem_ld_wait();
+                  if (k < lim && ((bad >> (k >> box_shift)) & 1u) == 0) {
+                    const float pk = __uint_as_float((k & 1) ? w & 0xFFFF0000u : w << 16);
+                    const uint32_t vr = vt + (b / 2) * T::half_bytes + k * 128;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      float a0 = __uint_as_float(o[8 * q + 2 * e]), a1 = __uint_as_float(o[8 * q + 2 * e + 1]);
-                      a0 = fmaf(pj, __uint_as_float(x[e] << 16), a0);
-                      a1 = fmaf(pj, __uint_as_float(x[e] & 0xFFFF0000u), a1);
-                      o[8 * q + 2 * e] = __float_as_uint(a0);
-                      o[8 * q + 2 * e + 1] = __float_as_uint(a1);
+                    for (int q = 0; q < 4; ++q) {
+                      const uint4 u = ld_shared_v4(vr + (((4 * (b & 1) + q) ^ (k & 7)) << 4));
+                      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) {
+                        float a0 = __uint_as_float(o[8 * q + 2 * e]), a1 = __uint_as_float(o[8 * q + 2 * e + 1]);
+                        a0 = fmaf(pk, __uint_as_float(v[e] << 16), a0);
+                        a1 = fmaf(pk, __uint_as_float(v[e] & 0xFFFF0000u), a1);
+                        o[8 * q + 2 * e] = __float_as_uint(a0);
+                        o[8 * q + 2 * e + 1] = __float_as_uint(a1);
+                      }
                     }
                   }
+                  __syncwarp();    // the next load is the whole warp's
                 }
-                __syncwarp();    // the next load is the whole warp's
+                tmem_st_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+                tmem_st_wait();
               }
-              tmem_st_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+              for (int k = lo >> 1; 2 * k < hi; ++k) {    // P.V leaves these keys out
+                uint32_t w = tmem_ld_1(my_tmem + T::p_col + k);
+                tmem_ld_wait();
+                w &= 2 * k >= lo ? 0u : 0x0000FFFFu;
+                tmem_st_1(my_tmem + T::p_col + k, w);
+              }
               tmem_st_wait();
             }
-            for (int j = lo >> 1; 2 * j < hi; ++j) {    // P.V leaves these keys out
-              uint32_t w = tmem_ld_1(my_tmem + T::p_col + j);
-              tmem_ld_wait();
-              w &= 2 * j >= lo ? 0u : 0x0000FFFFu;
-              tmem_st_1(my_tmem + T::p_col + j, w);
-            }
-            tmem_st_wait();
-            named_sync();      // V has been read
+            item_sync();      // V has been read
           }
-          if (starts && tid == 0) sm->acc = wild ? 1 : 0;
+          if (here && starts && wild && r == 0) sm->acc[t] = 1;
           if (has && (key_bad || key >= (wild ? lo : hi)))
 #pragma unroll
-            for (int j = 0; j < 8; ++j) st_shared_v4(vrow + 16 * j, 0u, 0u, 0u, 0u);
+            for (int q = 0; q < 8; ++q) st_shared_v4(vrow + 16 * q, 0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
-        } else if (starts && tid == 0) {
-          sm->acc = 0;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull));
+        if (here) {
+          give_p();
+        } else {
+          wait_warp(kVFull + st, round & 1);
+          tile_sync(t);         // every warp of the tile has left V
+          if ((warp % kSoftWarps) == 0 && lane == 0) mbar_arrive(bar(kVEmpty + st));
+          __syncwarp();
+        }
 
-        const bool ends = c + 1 == cur.nc || i + 1 == n_chunks;
-        starts = ends;
         if (ends) {
-          // ---- the item's part in this range: written out, or left for the merge
-          wait_warp(kPvDone, i & 1);
+          // ---- the tile's part in this range: written out, or left for the merge
+          wait_warp(kPvDone + t, j & 1);
           tc_fence_after();
-          const bool whole = c0 == 0 && c + 1 == cur.nc;
-          const int tok = (row0 + tid) / G, hd = cur.h * G + (row0 + tid) % G;
+          const bool whole = c0 == 0 && c + 1 == nc;
+          const int tok = (row0 + r) / G, hd = at.h * G + (row0 + r) % G;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                               (tid < rows ? (cur.seq.q0 + tok) * p.o_stride + static_cast<long long>(hd) * kDh : 0);
-          float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTileRows * (kDh + 2);
+                               (r < rows ? (at.seq.q0 + tok) * p.o_stride + static_cast<long long>(hd) * kDh : 0);
+          constexpr size_t kSlot = static_cast<size_t>(kTileRows) * (kDh + 2);
+          float* slot = p.part + ((2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTiles + t) * kSlot;
           auto put = [&](int b, const float (&o)[32], float inv) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -537,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             uint32_t w[32];
             tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, w);
             tmem_ld_wait();
-            if (tid < rows && ok) {
+            if (r < rows && ok) {
               float o[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(w[e]);
@@ -545,29 +725,29 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 put(b, o, inv);
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) slot[(32 * b + e) * kTileRows + tid] = o[e];
+                for (int e = 0; e < 32; ++e) slot[(32 * b + e) * kTileRows + r] = o[e];
               }
             }
           }
           tc_fence_before();
           if (!whole) {
-            if (tid < rows && ok) {
-              slot[kDh * kTileRows + tid] = m;
-              slot[(kDh + 1) * kTileRows + tid] = l;
+            if (r < rows && ok) {
+              slot[kDh * kTileRows + r] = m;
+              slot[(kDh + 1) * kTileRows + r] = l;
             }
-            const long long owner0 = cur.first / range.per;
-            const int parts = static_cast<int>((cur.first + cur.nc - 1) / range.per - owner0) + 1;
-            named_sync();      // the partial state is written
-            if (tid == 0) sm->last = 0;
-            if (tid == 0 && ok) {
-              const unsigned int n = atomic_add_acq_rel_gpu(p.counters + owner0, 1u);
-              sm->last = n == static_cast<unsigned int>(parts - 1);
-              if (sm->last) p.counters[owner0] = 0u;
+            const long long owner0 = at.first / range.per;
+            const int parts = static_cast<int>((at.first + nc - 1) / range.per - owner0) + 1;
+            tile_sync(t);      // the partial state is written
+            if (r == 0) sm->last[t] = 0;
+            if (r == 0 && ok) {
+              const unsigned int n = atomic_add_acq_rel_gpu(p.counters + owner0 * kTiles + t, 1u);
+              sm->last[t] = n == static_cast<unsigned int>(parts - 1);
+              if (sm->last[t]) p.counters[owner0 * kTiles + t] = 0u;
             }
-            named_sync();
-            if (sm->last && tid < rows) {
+            tile_sync(t);
+            if (sm->last[t] && r < rows) {
               auto part = [&](int k) {
-                return p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTileRows * (kDh + 2) + tid;
+                return p.part + ((2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTiles + t) * kSlot + r;
               };
               float M = -INFINITY, L = 0.f;
 #pragma unroll 4
@@ -597,16 +777,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
           }
         }
-        if (++c == cur.nc && i + 1 < n_chunks) {
-          work_next(bt, p.shape, p.Hkv, &cur);
+        if (here) ++j;
+        if (++c == at.nc && i + 1 < n_chunks) {
+          __syncwarp();
+          if (lane == 0) work_next(bt, p.shape, p.Hkv, &at);
+          __syncwarp();
           c = 0;
+          fresh = true;
         }
       }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTiles * kTmemTile);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -643,7 +827,7 @@ bool encode(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuu
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kCounterBytes = (kMaxBlocks * 4 + 255) / 256 * 256;
+constexpr size_t kCounterBytes = (kMaxBlocks * kTiles * 4 + 255) / 256 * 256;
 
 template <int kDh>
 cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
@@ -662,7 +846,7 @@ cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& 
   prm.page_shift = a.layer.page_shift;
   const int G = a.Hq / a.layer.Hkv;
   prm.shape.G = G;
-  prm.shape.rows = kTileRows / G * G;      // whole tokens
+  prm.shape.rows = kTiles * (kTileRows / G * G);      // whole tokens
   prm.shape.chunk_shift = T::chunk_shift;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = kFewRows + 1;
@@ -687,7 +871,7 @@ cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& 
                              cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  int grid = dev.num_sms * kBlocksPerSm;
+  int grid = dev.num_sms;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
@@ -711,7 +895,7 @@ bool paged_tile_takes(int G, bool act_bf16, int max_new) {
 }
 
 size_t paged_tile_workspace_bytes(int dh) {
-  return kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kTileRows * (dh + 2) * 4;
+  return kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kTiles * kTileRows * (dh + 2) * 4;
 }
 
 cudaError_t launch_paged_tile(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
