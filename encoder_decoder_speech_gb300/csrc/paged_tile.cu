@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return ok;
     };
     auto wait_warp = [&](int i, uint32_t parity) { // by a whole warp, with one answer
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar(i), parity))) return ok;   // far quicker, if it is so
       wait(i, parity);
       ok = __all_sync(0xffffffffu, ok);
       return ok;
@@ -499,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; e += 2)
             mx[(e / 2) & 3] = fmaxf(mx[(e / 2) & 3], fmaxf(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+        const bool pv = j == 0 || mbar_test_wait(bar(kPvDone + t), (j - 1) & 1);
         // the references of a warp's rows move together, to the largest score so far
         float corr = 1.f;
         const bool moved = __any_sync(0xffffffffu, top > m + kMoveLog2);
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += sum[0].x + sum[0].y;
 
         // P's place and O are free once the previous P.V has run
-        if (j > 0) wait_warp(kPvDone + t, (j - 1) & 1);
+        if (!__all_sync(0xffffffffu, pv)) wait_warp(kPvDone + t, (j - 1) & 1);
         tc_fence_after();
         if (__builtin_expect(moved && c != c0, 0)) {
 #pragma unroll 1
