@@ -10,12 +10,18 @@
 // partner's weight): A and B depend on the token and the lane, not on the head, and stay
 // in registers over the token's heads.
 //
-// Bound by memory: every value is read once and written once, about 6 operations each. A
-// warp takes one token; a head is read by dh * size / 16 lanes, 16 bytes a lane, and
-// kBatch such loads are under way before the first is used. The phases are computed once
-// a token, one pair a lane, from a 64-bit fixed-point turn (RotaryArg), and handed round
-// through shared memory. With few tokens the heads are dealt to several warps.
+// Bound by memory: every value is read once and written once. What stands between is kept
+// short, or the instructions bind (with 175 of them for 16 bytes a lane: 83 us for 24,000
+// tokens of 40 heads, against 47 us now): a lane holds two groups of four channels of a
+// head that are each other's partners (the half layout) or hold their partners themselves
+// (interleaved), so that no value is fetched from another lane, and works on pairs
+// (fma.f32x2). A warp takes one token, with the loads of kBatch heads under way before the
+// first is used. The phases are computed once a token, one pair a lane, from a 64-bit
+// fixed-point turn (RotaryArg), and handed round through shared memory. With few tokens the
+// heads are dealt to several warps.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -24,7 +30,12 @@ namespace cxa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBatch = 4;    // heads' loads under way in a lane
+constexpr int kBatch = 4;         // heads' loads under way in a lane
+// Blocks an SM that the registers are cut to. Measured, bf16 (24,000 tokens of 40 heads, and
+// 16,391 tokens appended): 4 blocks 46.9 and 71.2 us, 3 blocks 52.8 and 73.9; fp32 (5,333
+// tokens of 10 heads), whose loads hold twice the registers: 3 blocks 6.3 us, 4 blocks 12.1.
+template <typename TA>
+constexpr int kBlocksPerSm = sizeof(TA) == 2 ? 4 : 3;
 
 struct NrParams {
   const void *q, *k, *v;
@@ -49,41 +60,45 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&p);
 }
 
-// 16 bytes of T as floats.
+// Four channels, as loaded and as pairs of floats.
 template <typename T>
-struct Vec;
+struct Quad;
 template <>
-struct Vec<float> {
-  static constexpr int n = 4;
-  __device__ static void unpack(const uint4& u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x);
-    x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z);
-    x[3] = __uint_as_float(u.w);
+struct Quad<float> {
+  using Raw = uint4;
+  __device__ static void unpack(const Raw& u, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
 };
 template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int n = 8;
-  __device__ static void unpack(const uint4& u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = lo_bf16(w[i]);
-      x[2 * i + 1] = hi_bf16(w[i]);
-    }
+struct Quad<__nv_bfloat16> {
+  using Raw = uint2;
+  __device__ static void unpack(const Raw& u, float2 (&x)[2]) {
+    x[0] = make_float2(lo_bf16(u.x), hi_bf16(u.x));
+    x[1] = make_float2(lo_bf16(u.y), hi_bf16(u.y));
   }
 };
-
-__device__ __forceinline__ void store_vec(float* p, const float (&y)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+__device__ __forceinline__ void store_quad(float* p, const float2 (&y)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
 }
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&y)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+__device__ __forceinline__ void store_quad(__nv_bfloat16* p, const float2 (&y)[2]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y));
 }
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&y)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                                            pack_bf16(y[6], y[7]));
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
 }
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -104,23 +119,40 @@ __device__ __forceinline__ int find_seq(const int* q_start, int B, int t, int la
   return lo;
 }
 
-template <typename TA, typename TP, int kDh, bool kAppend>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_constant__ NrParams p) {
-  constexpr int VE = Vec<TA>::n;           // channels a lane holds
-  constexpr int LPH = kDh / VE;            // lanes a head
+// How a lane's two groups of channels turn: the groups are partners; each holds its own
+// partners, or is not turned; or (pairs that do not fill groups) partners lie anywhere.
+enum Mode { kPartners = 0, kInside = 1, kAnywhere = 2 };
+
+template <typename TA, typename TP, int kDh, bool kAppend, int kMode>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<TA>) norm_rope_kernel(const __grid_constant__ NrParams p) {
+  using Raw = typename Quad<TA>::Raw;
+  constexpr int LPH = kDh / 8;             // lanes a head
   constexpr int HPI = 32 / LPH;            // heads a warp reads at once
-  __shared__ float2 s_cs[kWarps][kDh / 2]; // f * (cos, sin) of the token's pairs
+  __shared__ float s_w[2][kDh];            // weights of q and k
+  __shared__ __align__(16) float s_cos[kWarps][kDh / 2], s_sin[kWarps][kDh / 2];   // times f, of the token's pairs
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / LPH, li = lane % LPH;
+  const int pairs = p.rot.pairs;
+  // first channels of the lane's groups
+  const bool turns = kMode == kPartners ? li < pairs / 4 : true;
+  const int ca = kMode == kPartners && turns ? 4 * li : kMode == kPartners ? 2 * pairs + 8 * (li - pairs / 4) : 8 * li;
+  const int cb = kMode == kPartners && turns ? ca + pairs : ca + 4;
+  if (p.norm) {
+    for (int i = threadIdx.x; i < 2 * kDh; i += kWarps * 32) {
+      const float* w = i < kDh ? p.wq : p.wk;
+      s_w[i / kDh][i % kDh] = w != nullptr ? __ldg(w + i % kDh) : 1.f;
+    }
+    __syncthreads();
+  }
+
   const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
   const long long tok_ll = item / p.splits;
   if (tok_ll >= p.n_tokens) return;
   const int token = static_cast<int>(tok_ll), part = static_cast<int>(item - tok_ll * p.splits);
-  const int sub = lane / LPH, c0 = (lane % LPH) * VE;
-
   const int itq = (p.Hq + HPI - 1) / HPI, itk = (p.Hk + HPI - 1) / HPI;
   const int iters = itq + itk * (kAppend ? 2 : 1);
   const int per = (iters + p.splits - 1) / p.splits;
@@ -129,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_con
 
   int pos = 0;
   bool write_kv = false;
-  size_t kv_row = 0;      // of head 0 in the page; heads are page_size rows apart
+  long long kv_row = 0;   // of head 0 in the page; heads are page_size rows apart
   if constexpr (kAppend) {
     const int b = find_seq(p.batch.q_start, p.batch.B, token, lane);
     if (b < 0) return;
@@ -141,152 +173,148 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_con
                                     p.layer.page_shift, p.layer.num_pages, pos);
       write_kv = page >= 0;
       if (!write_kv && lane == 0) atomicOr(p.status, kStatusBadPage);
-      kv_row = ((static_cast<size_t>(write_kv ? page : 0) * p.layer.Hkv) << p.layer.page_shift) +
+      kv_row = ((static_cast<long long>(max(page, 0)) * p.layer.Hkv) << p.layer.page_shift) +
                (pos & ((1 << p.layer.page_shift) - 1));
     }
   } else {
     pos = __ldg(p.pos + token);
   }
 
-  const int pairs = p.rot.pairs;
-  bool have_cs = false;
+  bool have_phases = false;
   auto phases = [&]() {
-    have_cs = true;
+    have_phases = true;
     for (int i = lane; i < pairs; i += 32) {
       const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos)) * p.rot.step[i];
       float sn, cs;
       // half turns in [-1, 1); the 32 high bits of the phase are finer than fp32 holds
       sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.6566128730773926e-10f, &sn, &cs);
-      s_cs[warp][i] = make_float2(cs * p.rot.factor, sn * p.rot.factor);
+      s_cos[warp][i] = cs * p.rot.factor;
+      s_sin[warp][i] = sn * p.rot.factor;
     }
     __syncwarp();
   };
 
-  // Normalise and rotate heads [a0 * HPI, a1 * HPI) of one tensor; dst(h, y) stores this
-  // lane's channels of head h.
-  auto run = [&](const TA* src, int H, const float* w, int a0, int a1, auto dst) {
-    float A[VE], B[VE];
-    bool first = true;
-    // whole 16-byte groups swap places: the partner sits in another lane, else in this one
-    const bool shift_lanes = !p.rot.interleaved && pairs % VE == 0;
-    const int shift = shift_lanes ? pairs / VE : 0;
-    const int from = c0 < pairs ? lane + shift : c0 < 2 * pairs ? lane - shift : lane;
-    const bool in_lane = p.rot.interleaved || pairs == 0;
-    for (int i = a0; i < a1; i += kBatch) {
-      uint4 raw[kBatch];
+  // Iterations [i0, i1) of one tensor: head h = it * HPI + sub from src, to dst + h * hop.
+  auto heads = [&](auto kind, const TA* src, int i0, int i1, int H, auto* dst, long long hop) {
+    constexpr int kKind = decltype(kind)::value;     // q, k, v
+    float2 A[4], B[4];      // y = x A + partner B of the lane's channels: two pairs a group
+    int h0 = i0 * HPI + sub;
+    src += static_cast<long long>(h0) * kDh;
+    dst += h0 * hop;
+    for (int it = i0; it < i1; it += kBatch) {
+      Raw ra[kBatch], rb[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int h = (i + u) * HPI + sub;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (i + u < a1 && h < H) raw[u] = *reinterpret_cast<const uint4*>(src + h * kDh + c0);
+        ra[u] = Raw{};
+        rb[u] = Raw{};
+        if (it + u < i1 && h0 + u * HPI < H) {
+          ra[u] = *reinterpret_cast<const Raw*>(src + u * HPI * kDh + ca);
+          rb[u] = *reinterpret_cast<const Raw*>(src + u * HPI * kDh + cb);
+        }
       }
-      if (!have_cs) phases();
-      if (first) {
-        first = false;
+      if (kKind < 2 && it == i0) {
+        if (!have_phases) phases();
+        float c[8], sn[8], w[8], v[8];       // cosine and signed sine, own weight and the partner's
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int c = c0 + e;
-          A[e] = p.norm && w != nullptr ? __ldg(w + c) : 1.f;
-          B[e] = 0.f;
-          if (c < 2 * pairs) {
-            const int pr = p.rot.interleaved ? c / 2 : c < pairs ? c : c - pairs;
-            const bool low = p.rot.interleaved ? (c & 1) == 0 : c < pairs;
-            const int partner = p.rot.interleaved ? c ^ 1 : low ? c + pairs : c - pairs;
-            const float2 cs = s_cs[warp][pr];
-            B[e] = (low ? -cs.y : cs.y) * (p.norm && w != nullptr ? __ldg(w + partner) : 1.f);
-            A[e] *= cs.x;
+        for (int e = 0; e < 8; ++e) w[e] = p.norm ? s_w[kKind & 1][e < 4 ? ca + e : cb + e - 4] : 1.f;
+        if (kMode == kPartners) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            c[e] = c[e + 4] = turns ? s_cos[warp][ca + e] : 1.f;
+            sn[e + 4] = turns ? s_sin[warp][ca + e] : 0.f;
+            sn[e] = -sn[e + 4];
+            v[e] = w[e + 4];
+            v[e + 4] = w[e];
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int ch = ca + e;
+            const bool on = ch < 2 * pairs;
+            const int pr = kMode == kInside ? ch / 2 : ch < pairs ? ch : ch - pairs;
+            const bool low = kMode == kInside ? (ch & 1) == 0 : ch < pairs;
+            c[e] = on ? s_cos[warp][pr] : 1.f;
+            sn[e] = on ? (low ? -s_sin[warp][pr] : s_sin[warp][pr]) : 0.f;
+            v[e] = kMode == kInside ? w[e ^ 1] : on && p.norm ? s_w[kKind & 1][low ? ch + pairs : ch - pairs] : 1.f;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          A[e] = make_float2(w[2 * e] * c[2 * e], w[2 * e + 1] * c[2 * e + 1]);
+          B[e] = make_float2(v[2 * e] * sn[2 * e], v[2 * e + 1] * sn[2 * e + 1]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        if (i + u >= a1) break;          // the same in every lane
-        const int h = (i + u) * HPI + sub;
-        float x[VE], y[VE];
-        Vec<TA>::unpack(raw[u], x);
-        float r = 1.f;
-        if (p.norm) {
-          float ss = 0.f;
+        if (it + u >= i1) break;             // the same in every lane
+        const bool real = h0 + u * HPI < H;
+        float2 a[2], b[2];                   // the lane's groups
+        Quad<TA>::unpack(ra[u], a);
+        Quad<TA>::unpack(rb[u], b);
+        if (kKind < 2) {
+          float2 o[4];                       // partners; channels that do not turn see none, whatever it holds
+          if (kMode == kPartners) {
+            o[0] = turns ? b[0] : make_float2(0.f, 0.f);
+            o[1] = turns ? b[1] : make_float2(0.f, 0.f);
+            o[2] = turns ? a[0] : make_float2(0.f, 0.f);
+            o[3] = turns ? a[1] : make_float2(0.f, 0.f);
+          } else if (kMode == kInside) {
+            o[0] = ca < 2 * pairs ? make_float2(a[0].y, a[0].x) : make_float2(0.f, 0.f);
+            o[1] = ca + 2 < 2 * pairs ? make_float2(a[1].y, a[1].x) : make_float2(0.f, 0.f);
+            o[2] = ca + 4 < 2 * pairs ? make_float2(b[0].y, b[0].x) : make_float2(0.f, 0.f);
+            o[3] = ca + 6 < 2 * pairs ? make_float2(b[1].y, b[1].x) : make_float2(0.f, 0.f);
+          } else {
+            float v[8];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) ss += x[e] * x[e];
+            for (int e = 0; e < 8; ++e) {
+              const int ch = ca + e, partner = ch < pairs ? ch + pairs : ch - pairs;
+              v[e] = ch < 2 * pairs && real ? to_float(src[u * HPI * kDh + partner]) : 0.f;
+            }
+            __syncwarp();                    // every lane has read before one writes in place
 #pragma unroll
-          for (int off = LPH / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          r = rsqrtf(ss * (1.f / kDh) + p.eps);
-        }
-        float o[VE];                     // the partners
-        if (in_lane) {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) o[e] = x[e ^ 1];
-        } else if (shift_lanes) {
-          uint4 t;
-          t.x = __shfl_sync(0xffffffffu, raw[u].x, from);
-          t.y = __shfl_sync(0xffffffffu, raw[u].y, from);
-          t.z = __shfl_sync(0xffffffffu, raw[u].z, from);
-          t.w = __shfl_sync(0xffffffffu, raw[u].w, from);
-          Vec<TA>::unpack(t, o);
-        } else {                         // pairs not a multiple of a lane's channels: read again
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const int c = c0 + e;
-            o[e] = 0.f;
-            if (c < 2 * pairs && h < H) o[e] = to_float(src[h * kDh + (c < pairs ? c + pairs : c - pairs)]);
+            for (int e = 0; e < 4; ++e) o[e] = make_float2(v[2 * e], v[2 * e + 1]);
           }
-          __syncwarp();                  // every lane has read before one writes in place
-        }
+          float2 r2 = make_float2(1.f, 1.f);
+          if (p.norm) {
+            const float2 ss = fma2(b[1], b[1], fma2(b[0], b[0], fma2(a[1], a[1], mul2(a[0], a[0]))));
+            float sq = ss.x + ss.y;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          // channels behind the rotated ones see no partner, whatever it holds
-          const float rotated = c0 + e < 2 * pairs ? fmaf(o[e], B[e], x[e] * A[e]) : x[e] * A[e];
-          y[e] = rotated * r;
+            for (int off = LPH / 2; off >= 1; off >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, off);
+            r2.x = r2.y = rsqrtf(sq * (1.f / kDh) + p.eps);
+          }
+          a[0] = mul2(fma2(o[0], B[0], mul2(a[0], A[0])), r2);
+          a[1] = mul2(fma2(o[1], B[1], mul2(a[1], A[1])), r2);
+          b[0] = mul2(fma2(o[2], B[2], mul2(b[0], A[2])), r2);
+          b[1] = mul2(fma2(o[3], B[3], mul2(b[1], A[3])), r2);
         }
-        if (h < H) dst(h, y);
+        if (real) {
+          store_quad(dst + u * HPI * hop + ca, a);
+          store_quad(dst + u * HPI * hop + cb, b);
+        }
       }
+      h0 += kBatch * HPI;
+      src += kBatch * HPI * kDh;
+      dst += kBatch * HPI * hop;
     }
   };
-
-  if (it0 < itq) {
-    TA* out = static_cast<TA*>(p.q_out) + static_cast<long long>(token) * p.qo_stride;
-    run(static_cast<const TA*>(p.q) + static_cast<long long>(token) * p.q_stride, p.Hq, p.wq, it0, min(it1, itq),
-        [&](int h, const float(&y)[VE]) { store_vec(out + h * kDh + c0, y); });
-  }
-  if constexpr (!kAppend) {
-    if (it1 > itq) {
-      TA* out = static_cast<TA*>(p.k_out) + static_cast<long long>(token) * p.ko_stride;
-      run(static_cast<const TA*>(p.k) + static_cast<long long>(token) * p.k_stride, p.Hk, p.wk, max(it0, itq) - itq,
-          it1 - itq, [&](int h, const float(&y)[VE]) { store_vec(out + h * kDh + c0, y); });
-    }
-  } else {
+  using Q = std::integral_constant<int, 0>;
+  using K = std::integral_constant<int, 1>;
+  using V = std::integral_constant<int, 2>;
+  if (it0 < itq)
+    heads(Q{}, static_cast<const TA*>(p.q) + token * p.q_stride, it0, min(it1, itq), p.Hq,
+          static_cast<TA*>(p.q_out) + token * p.qo_stride, kDh);
+  if constexpr (kAppend) {
     if (!write_kv) return;
-    if (it1 > itq && it0 < itq + itk) {
-      TP* out = static_cast<TP*>(p.layer.K) + kv_row * kDh;
-      run(static_cast<const TA*>(p.k) + static_cast<long long>(token) * p.k_stride, p.Hk, p.wk, max(it0, itq) - itq,
-          min(it1, itq + itk) - itq, [&](int h, const float(&y)[VE]) {
-            store_vec(out + (static_cast<size_t>(h) << p.layer.page_shift) * kDh + c0, y);
-          });
-    }
-    if (it1 > itq + itk) {
-      const TA* src = static_cast<const TA*>(p.v) + static_cast<long long>(token) * p.v_stride;
-      TP* out = static_cast<TP*>(p.layer.V) + kv_row * kDh;
-      const int a0 = max(it0, itq + itk) - itq - itk, a1 = it1 - itq - itk;
-      for (int i = a0; i < a1; i += kBatch) {
-        uint4 raw[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int h = (i + u) * HPI + sub;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (i + u < a1 && h < p.Hk) raw[u] = *reinterpret_cast<const uint4*>(src + h * kDh + c0);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int h = (i + u) * HPI + sub;
-          if (i + u < a1 && h < p.Hk) {
-            float x[VE];
-            Vec<TA>::unpack(raw[u], x);
-            store_vec(out + (static_cast<size_t>(h) << p.layer.page_shift) * kDh + c0, x);
-          }
-        }
-      }
-    }
+    const long long hop = static_cast<long long>(kDh) << p.layer.page_shift;
+    if (it1 > itq && it0 < itq + itk)
+      heads(K{}, static_cast<const TA*>(p.k) + token * p.k_stride, max(it0, itq) - itq, min(it1, itq + itk) - itq, p.Hk,
+            static_cast<TP*>(p.layer.K) + kv_row * kDh, hop);
+    if (it1 > itq + itk)
+      heads(V{}, static_cast<const TA*>(p.v) + token * p.v_stride, max(it0, itq + itk) - itq - itk, it1 - itq - itk, p.Hk,
+            static_cast<TP*>(p.layer.V) + kv_row * kDh, hop);
+  } else if (it1 > itq) {
+    heads(K{}, static_cast<const TA*>(p.k) + token * p.k_stride, max(it0, itq) - itq, it1 - itq, p.Hk,
+          static_cast<TA*>(p.k_out) + token * p.ko_stride, kDh);
   }
 }
 
@@ -316,7 +344,7 @@ cudaError_t launch(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t 
   p.layer = a.layer;
   p.rot = a.rot;
   // one warp a token from 16 warps an SM up; with fewer tokens their heads are split
-  constexpr int HPI = 32 / (kDh / Vec<TA>::n);
+  constexpr int HPI = 32 / (kDh / 8);
   const int iters = (a.Hq + HPI - 1) / HPI + (a.Hk + HPI - 1) / HPI * (kAppend ? 2 : 1);
   const long long want = (16LL * dev.num_sms + a.n_tokens - 1) / a.n_tokens;
   p.splits = static_cast<int>(want < 1 ? 1 : want > iters ? iters : want);
@@ -331,7 +359,10 @@ cudaError_t launch(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_rope_kernel<TA, TP, kDh, kAppend>, p);
+  const int mode = a.rot.pairs == 0 || a.rot.interleaved ? kInside : a.rot.pairs % 4 == 0 ? kPartners : kAnywhere;
+  const cudaError_t e = mode == kPartners ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<TA, TP, kDh, kAppend, kPartners>, p)
+                        : mode == kInside ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<TA, TP, kDh, kAppend, kInside>, p)
+                                          : cudaLaunchKernelEx(&cfg, norm_rope_kernel<TA, TP, kDh, kAppend, kAnywhere>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
