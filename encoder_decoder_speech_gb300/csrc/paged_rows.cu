@@ -7,19 +7,23 @@
 // in one pass with the running reference m_r. Bound by memory: K and V are read once for
 // the kRows = 16 query rows of a tile (query heads of one K/V head times new tokens).
 //
-// A warp takes 16 keys a step and multiplies on the tensor cores with m16n8k16 products,
-// whose operands come straight from global memory, 16 bytes a lane, with no staging in
-// shared memory: a product does not care which channel carries which index as long as
-// both operands agree, so lane (g, t) of the K operand takes 16 consecutive bytes of
-// key g and the query operand is laid out to match; for P.V, lane (g, t) takes 16
-// consecutive bytes of keys 2t and 2t + 1 and pairs them up by byte permutes. The K of
-// the next step is under way while a step is computed.
+// A warp takes 16 keys a step, which it streams into a ring of its own in shared memory
+// (cp.async, kStages steps; no barrier but the warp's), and multiplies on the tensor cores
+// with m16n8k16 products. A product does not care which channel carries which index as long
+// as both operands agree, so operands are read 16 bytes a lane: lane (g, t) of the K operand
+// takes 16 consecutive bytes of key g, the query operand being laid out to match, and for
+// P.V lane (g, t) takes 16 consecutive bytes of keys 2t and 2t + 1 and pairs them up by byte
+// permutes. The 16-byte pieces of a row are stored permuted so that both reads are free of
+// bank conflicts.
 //
 // Rounding: fp32 values enter the products as sums of three bf16 parts (8 + 8 + 8 bits,
 // by truncation, so exactly), of whose products the six largest are taken: what is left
 // out is below 2^-22 of a term. With bf16 tensors q, K and V are exact as they are and the
 // probabilities keep two parts (16 bits), which leaves the output's own rounding as the
-// only one that shows. Sums, references and accumulators are fp32.
+// only one that shows. Sums, references and accumulators are fp32. The products round their
+// running sums towards zero; in fp32, where that would show (2e-6 of the result after 100
+// steps, against 4e-7), each step's products start from zero, smallest first, and are added
+// to the sums by ordinary additions.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -37,8 +41,7 @@ constexpr int kRows = 16;            // query rows a tile
 constexpr int kStep = 16;            // keys a warp takes at a time
 constexpr int kChunkShift = 6;       // 64 keys: one step of each warp
 constexpr int kStepsPerChunk = (1 << kChunkShift) / kStep;
-constexpr int kBlocksPerSm = 4;
-constexpr int kMaxBlocks = 160 * kBlocksPerSm;
+constexpr int kMaxBlocks = 160 * 4;
 constexpr float kMoveLog2 = 8.f;     // a row's reference moves only past this margin
 
 struct RowsParams {
@@ -101,10 +104,28 @@ struct Shape {
   static constexpr int KV = row_bytes / 64;        // 16-byte loads of a lane along a K row
   static constexpr int VV = row_bytes / 128;       // and along a V row
   static constexpr int PE = kDh + 4;               // floats of a row in the block's merge
+  static constexpr int half_bytes = kStep * row_bytes;     // K or V of a step
+  // Steps a warp's ring holds, and blocks an SM: as many bytes under way as fit
+  static constexpr int stages = 3;
+  static constexpr int blocks = row_bytes <= 128 ? 4 : row_bytes <= 256 ? 2 : 1;
+  static constexpr int ring_bytes = kWarps * stages * 2 * half_bytes;
   static constexpr int q_bytes = QP * KS * 32 * 16;
   static constexpr int merge_bytes = kWarps * kRows * PE * 4 + 2 * kWarps * kRows * 4;
-  static constexpr int smem = q_bytes + merge_bytes;
+  static constexpr int smem = q_bytes + (ring_bytes > merge_bytes ? ring_bytes : merge_bytes);
 };
+
+// Where the 16-byte piece c of row r of a step lies.
+__device__ __forceinline__ int k_piece(int r, int c) { return c ^ ((r & 1) << 2); }
+__device__ __forceinline__ int v_piece(int r, int c) { return c ^ ((r >> 1 & 3) << 1); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // B operand of product s along a head from a lane's K loads.
 template <typename S>
@@ -121,6 +142,22 @@ __device__ __forceinline__ void k_operand(const uint4 (&k)[S::KV], int s, uint32
     const uint4& u = k[s >> 1];
     b[0][0] = (s & 1) ? u.z : u.x;
     b[0][1] = (s & 1) ? u.w : u.y;
+  }
+}
+
+// sum += A B over the parts of both, smallest products first; with kApart added up by
+// themselves.
+template <bool kApart, int NA, int NB>
+__device__ __forceinline__ void add_products(float (&sum)[4], const uint4 (&a)[NA], const uint32_t (&b)[NB][2]) {
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int order = 2; order >= 0; --order)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (order - i >= 0 && order - i < NB) mma_16816(kApart ? d : sum, a[i], b[order - i][0], b[order - i][1]);
+  if (kApart) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += d[i];
   }
 }
 
@@ -151,12 +188,14 @@ __device__ __forceinline__ void v_operand(const uint4 (&v)[4][S::VV], int c, uin
 }
 
 template <typename TQ, typename TP, int kDh>
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_rows_kernel(const __grid_constant__ RowsParams p) {
   using S = Shape<TQ, TP, kDh>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ WorkScratch s_work;
   __shared__ int s_last;
   uint4* s_q = reinterpret_cast<uint4*>(smem);                             // [QP][KS][32 lanes]
+  // the warps' rings, and once they have run dry the merge of the warps' states
+  const uint32_t ring = smem_u32(smem) + S::q_bytes + (threadIdx.x >> 5) * (S::stages * 2 * S::half_bytes);
   float* s_o = reinterpret_cast<float*>(smem + S::q_bytes);                // [kWarps][kRows][PE]
   float* s_m = s_o + kWarps * kRows * S::PE;                               // [kWarps][kRows]
   float* s_l = s_m + kWarps * kRows;
@@ -230,67 +269,66 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
       if (page < 0 && lane == 0) atomicOr(p.status, kStatusBadPage);
       return page;
     };
-    // byte offset of the step's first row in the layer; a step lies in one page
-    auto step_row = [&](int s, int page) {
-      return ((((static_cast<size_t>(page) * Hkv + cur.h) << shift) + ((s * kStep) & ((1 << shift) - 1)))) *
-             S::row_bytes;
-    };
-    auto load_k = [&](int s, int page, uint4 (&k)[2][S::KV]) {
+    // Stream step s into stage st: rows that no query sees are not read and become zero (a
+    // key that no row sees weighs 0, and its V may hold anything).
+    auto fetch = [&](int s, int page, int st) {
+      constexpr int PR = S::row_bytes / 16;            // pieces a row
+      if (s < s1) {
+        const bool there = page >= 0;
+        // a step lies in one page
+        const size_t at = (((static_cast<size_t>(there ? page : 0) * Hkv + cur.h) << shift) +
+                           ((s * kStep) & ((1 << shift) - 1))) * S::row_bytes;
+        const uint32_t dst = ring + st * (2 * S::half_bytes);
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const bool ok = s < s1 && page >= 0 && s * kStep + 8 * nb + g < keys;
-        const uint8_t* src = Kb + (ok ? step_row(s, page) + (8 * nb + g) * S::row_bytes + t * 16 : 0);
-#pragma unroll
-        for (int v = 0; v < S::KV; ++v)
-          k[nb][v] = ok ? __ldg(reinterpret_cast<const uint4*>(src + v * 64)) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kStep * PR / 32; ++i) {
+          const int r = (i * 32 + lane) / PR, c = lane % PR;
+          const bool real = there && s * kStep + r < keys;
+          const size_t from = real ? at + r * S::row_bytes + c * 16 : 0;
+          cp_async16(dst + r * S::row_bytes + k_piece(r, c) * 16, Kb + from, real);
+          cp_async16(dst + S::half_bytes + r * S::row_bytes + v_piece(r, c) * 16, Vb + from, real);
+        }
       }
+      cp_commit();
     };
 
     int s = c0 * kStepsPerChunk + warp;
-    int page = step_page(s), page_next = step_page(s + kWarps);
-    uint4 kn[2][S::KV];
-    load_k(s, page, kn);
+    int page = step_page(s);
+    uint32_t gone = 0;                                 // steps under way whose page is bad, the newest at bit 0
+#pragma unroll
+    for (int i = 0; i < S::stages - 1; ++i) {
+      fetch(s + i * kWarps, page, i);
+      gone = gone << 1 | (page < 0 ? 1u : 0u);
+      page = step_page(s + (i + 1) * kWarps);
+    }
+    int st = 0;
     for (; s < s1; s += kWarps) {
-      uint4 k[2][S::KV], v[4][S::VV];
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-        for (int i = 0; i < S::KV; ++i) k[nb][i] = kn[nb][i];
-      // V of this step, K of the next
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = 8 * (j >> 1) + 2 * t + (j & 1);
-        // a key that no row sees weighs 0, and its V may hold anything: read as 0
-        const bool ok = page >= 0 && s * kStep + key < keys;
-        const uint8_t* src = Vb + (ok ? step_row(s, page) + key * S::row_bytes + g * 16 : 0);
-#pragma unroll
-        for (int i = 0; i < S::VV; ++i)
-          v[j][i] = ok ? __ldg(reinterpret_cast<const uint4*>(src + i * 128)) : make_uint4(0, 0, 0, 0);
-      }
-      const int page_now = page;
-      page = page_next;
-      load_k(s + kWarps, page, kn);
-      page_next = step_page(s + 2 * kWarps);
-      if (page_now < 0) continue;      // a bad page: its keys are left out
+      cp_wait<S::stages - 2>();
+      __syncwarp();          // the step has come for every lane, and the last one's stage is free
+      fetch(s + (S::stages - 1) * kWarps, page, st == 0 ? S::stages - 1 : st - 1);
+      gone = gone << 1 | (page < 0 ? 1u : 0u);
+      page = step_page(s + S::stages * kWarps);
+      const uint8_t* kt = smem + S::q_bytes + (warp * S::stages + st) * (2 * S::half_bytes);
+      const uint8_t* vt = kt + S::half_bytes;
+      st = st + 1 == S::stages ? 0 : st + 1;
+      if (gone >> (S::stages - 1) & 1u) continue;      // a bad page: its keys are left out
 
       // ---- scores
       float sc[2][4];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+      for (int nb = 0; nb < 2; ++nb) {
+        uint4 k[S::KV];
 #pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) {
-        uint4 a[S::QP];
+        for (int v = 0; v < S::KV; ++v)
+          k[v] = *reinterpret_cast<const uint4*>(kt + (8 * nb + g) * S::row_bytes + k_piece(8 * nb + g, 4 * v + t) * 16);
+        sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < S::QP; ++i) a[i] = s_q[(i * S::KS + ks) * 32 + lane];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+        for (int ks = 0; ks < S::KS; ++ks) {
+          uint4 a[S::QP];
           uint32_t b[S::KP][2];
-          k_operand<S>(k[nb], ks, b);
 #pragma unroll
-          for (int i = 0; i < S::QP; ++i)
-#pragma unroll
-            for (int j = 0; j < S::KP; ++j)
-              if (i + j <= 2) mma_16816(sc[nb], a[i], b[j][0], b[j][1]);
+          for (int i = 0; i < S::QP; ++i) a[i] = s_q[(i * S::KS + ks) * 32 + lane];
+          k_operand<S>(k, ks, b);
+          add_products<S::q32, S::QP, S::KP>(sc[nb], a, b);
         }
       }
       const bool masked = s * kStep + kStep > see_all;
@@ -346,6 +384,14 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
 
       // ---- values. A row's weight for a key it may not see is 0, but 0 * inf is not: if a
       // masked step holds such a value, each token's rows are taken by themselves.
+      uint4 v[4][S::VV];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 8 * (j >> 1) + 2 * t + (j & 1);
+#pragma unroll
+        for (int i = 0; i < S::VV; ++i)
+          v[j][i] = *reinterpret_cast<const uint4*>(vt + r * S::row_bytes + v_piece(r, 8 * i + g) * 16);
+      }
       bool wild = false;
       if (masked) {
 #pragma unroll
@@ -361,11 +407,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
         for (int c = 0; c < S::NB; ++c) {
           uint32_t b[S::KP][2];
           v_operand<S>(v, c, b);
-#pragma unroll
-          for (int i = 0; i < S::PP; ++i)
-#pragma unroll
-            for (int j = 0; j < S::KP; ++j)
-              if (i + j <= 2) mma_16816(o[c], pa[i], b[j][0], b[j][1]);
+          add_products<S::q32, S::PP, S::KP>(o[c], pa, b);
         }
       } else {
         for (int tok = row0 / G; tok <= (row0 + rows - 1) / G; ++tok) {
@@ -381,11 +423,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
             uint32_t b[S::KP][2];
             v_operand<S>(vm, c, b);
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < S::PP; ++i)
-#pragma unroll
-              for (int j = 0; j < S::KP; ++j)
-                if (i + j <= 2) mma_16816(d, pa[i], b[j][0], b[j][1]);
+            add_products<false, S::PP, S::KP>(d, pa, b);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if ((row0 + g + 8 * (i >> 1)) / G == tok) o[c][i] += d[i];
@@ -394,7 +432,9 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
       }
     }
 
-    // ---- the warps' states become one
+    // ---- the warps' states become one, in the rings' place
+    cp_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -499,7 +539,7 @@ cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const Device
   cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<TQ, TP, kDh>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  int grid = dev.num_sms * kBlocksPerSm;
+  int grid = dev.num_sms * Shape<TQ, TP, kDh>::blocks;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
