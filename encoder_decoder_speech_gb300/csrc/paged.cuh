@@ -103,6 +103,7 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cud
 // the workspace behind the first kernel's); the first kernel takes all of them otherwise.
 constexpr int kFewRows = 16;
 size_t paged_rows_workspace_bytes(int dh);
+bool paged_rows_countable(const PagedAttnLaunch& a);   // whether the call's work can be numbered in 31 bits
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream);
 bool paged_tile_takes(int G, bool act_bf16, int max_new);
 size_t paged_tile_workspace_bytes(int dh);

@@ -409,10 +409,6 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
       return fail(CXA_EINVAL, w + ": the workspace is NULL or not 256-byte aligned");
     if (workspace_bytes < cxa_paged_attention_workspace_bytes(Hq, pages->Hkv, pages->dh, max_new))
       return fail(CXA_EINVAL, w + ": workspace smaller than cxa_paged_attention_workspace_bytes()");
-    std::string msg;
-    cxa::DeviceInfo dev;
-    cudaError_t e = cxa::current_device_info(&dev, &msg);
-    if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     cxa::PagedAttnLaunch a = {};
     a.q = q;
     a.out = out;
@@ -427,6 +423,13 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
+    if (!cxa::paged_rows_countable(a))
+      return fail(CXA_EINVAL, w + ": Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages * page_size / 64 + 1) must be "
+                                  "below 2^31");
+    std::string msg;
+    cxa::DeviceInfo dev;
+    cudaError_t e = cxa::current_device_info(&dev, &msg);
+    if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
     e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);

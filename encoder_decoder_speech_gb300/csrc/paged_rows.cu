@@ -35,13 +35,12 @@
 namespace cxa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // query rows a tile
 constexpr int kStep = 16;            // keys a warp takes at a time
-constexpr int kChunkShift = 6;       // 64 keys: one step of each warp
-constexpr int kStepsPerChunk = (1 << kChunkShift) / kStep;
 constexpr int kMaxBlocks = 160 * 4;
+constexpr int kGroup = 16;           // parts of an item that are merged at once, and then of those
+constexpr int kMaxParts = (kMaxBlocks + kGroup - 1) / kGroup;
+constexpr int kWideItems = 1;        // items an SM below which wide blocks run
 constexpr float kMoveLog2 = 8.f;     // a row's reference moves only past this margin
 
 struct RowsParams {
@@ -49,7 +48,7 @@ struct RowsParams {
   void* out;
   long long q_stride, o_stride;
   float qscale;                      // scale * log2(e)
-  unsigned int* counters;            // [grid], zero between calls
+  unsigned int* counters;            // [grid][3], zero between calls
   float* part;                       // [2 * grid][kRows][kDh + 2]
   unsigned int* status;
   PagedBatch batch;
@@ -92,7 +91,7 @@ __device__ __forceinline__ bool nonfinite(uint32_t w, bool bf16_pair) {
   return (w & 0x7F800000u) == 0x7F800000u;
 }
 
-template <typename TQ, typename TP, int kDh>
+template <typename TQ, typename TP, int kDh, bool kWide>
 struct Shape {
   static constexpr bool q32 = sizeof(TQ) == 4, p32 = sizeof(TP) == 4;
   static constexpr int QP = q32 ? 3 : 1;           // bf16 parts of a query value,
@@ -105,12 +104,16 @@ struct Shape {
   static constexpr int VV = row_bytes / 128;       // and along a V row
   static constexpr int PE = kDh + 4;               // floats of a row in the block's merge
   static constexpr int half_bytes = kStep * row_bytes;     // K or V of a step
-  // Steps a warp's ring holds, and blocks an SM: as many bytes under way as fit
+  // One block of many warps an SM (kWide), or several of four; a chunk is a step of each
+  // warp. The rings hold three steps a warp, and as many warps run as that leaves room for.
   static constexpr int stages = 3;
-  static constexpr int blocks = row_bytes <= 128 ? 4 : row_bytes <= 256 ? 2 : 1;
-  static constexpr int ring_bytes = kWarps * stages * 2 * half_bytes;
+  static constexpr int warps_sm = 2048 / row_bytes;
+  static constexpr int warps = kWide ? warps_sm : 4, blocks = warps_sm / warps, threads = warps * 32;
+  static constexpr int chunk_shift = warps == 16 ? 8 : warps == 8 ? 7 : 6;
+  static constexpr int ring_bytes = warps * stages * 2 * half_bytes;
   static constexpr int q_bytes = QP * KS * 32 * 16;
-  static constexpr int merge_bytes = kWarps * kRows * PE * 4 + 2 * kWarps * kRows * 4;
+  static constexpr int merge_bytes = warps * kRows * PE * 4 + 2 * warps * kRows * 4;
+  static_assert(2 * kMaxParts * kRows * 4 <= merge_bytes, "the weights of a merge fit");
   static constexpr int smem = q_bytes + (ring_bytes > merge_bytes ? ring_bytes : merge_bytes);
 };
 
@@ -187,10 +190,12 @@ __device__ __forceinline__ void v_operand(const uint4 (&v)[4][S::VV], int c, uin
   }
 }
 
-template <typename TQ, typename TP, int kDh>
-__global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_rows_kernel(const __grid_constant__ RowsParams p) {
-  using S = Shape<TQ, TP, kDh>;
-  extern __shared__ __align__(16) uint8_t smem[];
+template <typename TQ, typename TP, int kDh, bool kWide>
+__global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, TP, kDh, kWide>::blocks)
+    paged_rows_kernel(const __grid_constant__ RowsParams p) {
+  using S = Shape<TQ, TP, kDh, kWide>;
+  constexpr int kWarps = S::warps, kThreads = S::threads;
+  extern __shared__ __align__(1024) uint8_t smem[];   // rows of the rings fill whole bank lines
   __shared__ WorkScratch s_work;
   __shared__ int s_last;
   uint4* s_q = reinterpret_cast<uint4*>(smem);                             // [QP][KS][32 lanes]
@@ -199,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
   float* s_o = reinterpret_cast<float*>(smem + S::q_bytes);                // [kWarps][kRows][PE]
   float* s_m = s_o + kWarps * kRows * S::PE;                               // [kWarps][kRows]
   float* s_l = s_m + kWarps * kRows;
+  float* s_w = s_o;                                                        // [2][kMaxParts][kRows], in a merge
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -208,16 +214,64 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
   const int Hkv = p.layer.Hkv, shift = p.layer.page_shift, G = p.shape.G;
   WorkRange range;
   WorkCursor cur;
-  if (!work_locate<kThreads>(bt, p.shape, Hkv, &s_work, &range, &cur)) return;
+  WorkShape shape = p.shape;
+  if (!work_locate<kThreads, true>(bt, shape, Hkv, &s_work, &range, &cur)) return;
 
   for (;;) {
     // ---- the part of the item in this block's range
-    const long long end = min(range.g1, cur.first + cur.nc);
-    const int c0 = cur.c, c1 = static_cast<int>(end - cur.first);
+    const int end = min(range.g1, cur.first + cur.nc);
+    const int c0 = cur.c, c1 = end - cur.first;
     const PagedSeq seq = cur.seq;
     const int row0 = cur.rt * kRows;
-    const int rows = min(kRows, work_rows(seq, p.shape) - row0);
-    const int keys = tile_keys(seq, p.shape, cur.rt);
+    const int rows = min(kRows, work_rows(seq, shape) - row0);
+    const int keys = tile_keys(seq, shape, cur.rt);
+
+    // ---- the first steps on their way
+    const int* table_row = bt.table + static_cast<size_t>(cur.b) * bt.width;
+    const uint8_t* Kb = static_cast<const uint8_t*>(p.layer.K);
+    const uint8_t* Vb = static_cast<const uint8_t*>(p.layer.V);
+    const int steps = tile_steps(seq, shape, cur.rt);      // of all warps, kWarps * kStep keys
+    const int s0 = chunk_step(shape, c0, cur.nc, steps) * kWarps;
+    const int s1 = min(chunk_step(shape, c1, cur.nc, steps) * kWarps, (keys + kStep - 1) / kStep);
+    auto step_page = [&](int s) {
+      if (s >= s1) return 0;
+      const int page = paged_lookup(table_row, bt.width, shift, p.layer.num_pages, s * kStep);
+      if (page < 0 && lane == 0) atomicOr(p.status, kStatusBadPage);
+      return page;
+    };
+    // Stream step s into stage st: rows that no query sees are not read and become zero (a
+    // key that no row sees weighs 0, and its V may hold anything).
+    auto fetch = [&](int s, int page, int st) {
+      constexpr int PR = S::row_bytes / 16;            // pieces a row
+      if (s < s1) {
+        const bool there = page >= 0;
+        // a step lies in one page
+        const size_t at = (((static_cast<size_t>(there ? page : 0) * Hkv + cur.h) << shift) +
+                           ((s * kStep) & ((1 << shift) - 1))) * S::row_bytes;
+        const uint32_t dst = ring + st * (2 * S::half_bytes);
+#pragma unroll
+        for (int i = 0; i < kStep * PR / 32; ++i) {
+          const int r = (i * 32 + lane) / PR, c = lane % PR;
+          const bool real = there && s * kStep + r < keys;
+          const size_t from = real ? at + r * S::row_bytes + c * 16 : 0;
+          cp_async16(dst + r * S::row_bytes + k_piece(r, c) * 16, Kb + from, real);
+          cp_async16(dst + S::half_bytes + r * S::row_bytes + v_piece(r, c) * 16, Vb + from, real);
+        }
+      }
+      cp_commit();
+    };
+
+    int s = s0 + warp;
+    int pages[S::stages];                              // looked up together, ahead of their use
+#pragma unroll
+    for (int i = 0; i < S::stages; ++i) pages[i] = step_page(s + i * kWarps);
+    uint32_t gone = 0;                                 // steps under way whose page is bad, the newest at bit 0
+#pragma unroll
+    for (int i = 0; i < S::stages - 1; ++i) {
+      fetch(s + i * kWarps, pages[i], i);
+      gone = gone << 1 | (pages[i] < 0 ? 1u : 0u);
+    }
+    int page = pages[S::stages - 1];
 
     // ---- the queries as A operands: lane (g, t) holds rows g and g + 8, channels to match
     // the K loads
@@ -249,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = g + 8 * r;
-      see[r] = row < rows ? visible_keys(seq, (row0 + row) / G, p.shape.cap) : 0;
+      see[r] = row < rows ? visible_keys(seq, (row0 + row) / G, shape.cap) : 0;
     }
-    const int see_all = visible_keys(seq, row0 / G, p.shape.cap);   // keys that every row may see
+    const int see_all = visible_keys(seq, row0 / G, shape.cap);   // keys that every row may see
     __syncthreads();
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -259,47 +313,6 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
 #pragma unroll
     for (int c = 0; c < S::NB; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
 
-    const int* table_row = bt.table + static_cast<size_t>(cur.b) * bt.width;
-    const uint8_t* Kb = static_cast<const uint8_t*>(p.layer.K);
-    const uint8_t* Vb = static_cast<const uint8_t*>(p.layer.V);
-    const int s1 = min(c1 * kStepsPerChunk, (keys + kStep - 1) / kStep);
-    auto step_page = [&](int s) {
-      if (s >= s1) return 0;
-      const int page = paged_lookup(table_row, bt.width, shift, p.layer.num_pages, s * kStep);
-      if (page < 0 && lane == 0) atomicOr(p.status, kStatusBadPage);
-      return page;
-    };
-    // Stream step s into stage st: rows that no query sees are not read and become zero (a
-    // key that no row sees weighs 0, and its V may hold anything).
-    auto fetch = [&](int s, int page, int st) {
-      constexpr int PR = S::row_bytes / 16;            // pieces a row
-      if (s < s1) {
-        const bool there = page >= 0;
-        // a step lies in one page
-        const size_t at = (((static_cast<size_t>(there ? page : 0) * Hkv + cur.h) << shift) +
-                           ((s * kStep) & ((1 << shift) - 1))) * S::row_bytes;
-        const uint32_t dst = ring + st * (2 * S::half_bytes);
-#pragma unroll
-        for (int i = 0; i < kStep * PR / 32; ++i) {
-          const int r = (i * 32 + lane) / PR, c = lane % PR;
-          const bool real = there && s * kStep + r < keys;
-          const size_t from = real ? at + r * S::row_bytes + c * 16 : 0;
-          cp_async16(dst + r * S::row_bytes + k_piece(r, c) * 16, Kb + from, real);
-          cp_async16(dst + S::half_bytes + r * S::row_bytes + v_piece(r, c) * 16, Vb + from, real);
-        }
-      }
-      cp_commit();
-    };
-
-    int s = c0 * kStepsPerChunk + warp;
-    int page = step_page(s);
-    uint32_t gone = 0;                                 // steps under way whose page is bad, the newest at bit 0
-#pragma unroll
-    for (int i = 0; i < S::stages - 1; ++i) {
-      fetch(s + i * kWarps, page, i);
-      gone = gone << 1 | (page < 0 ? 1u : 0u);
-      page = step_page(s + (i + 1) * kWarps);
-    }
     int st = 0;
     for (; s < s1; s += kWarps) {
       cp_wait<S::stages - 2>();
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
         }
       } else {
         for (int tok = row0 / G; tok <= (row0 + rows - 1) / G; ++tok) {
-          const int lim = visible_keys(seq, tok, p.shape.cap);
+          const int lim = visible_keys(seq, tok, shape.cap);
           uint4 vm[4][S::VV];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -454,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
       }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == cur.nc;
-    const long long owner0 = cur.first / range.per;       // blocks that hold a part of the item
-    const int parts = static_cast<int>((cur.first + cur.nc - 1) / range.per - owner0) + 1;
+    const int owner0 = cur.first / range.per;              // blocks that hold a part of the item
+    const int parts = (cur.first + cur.nc - 1) / range.per - owner0 + 1;
     float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kRows * (kDh + 2);
 
     auto write_out = [&](int r, int ch, float4 v, float sum) {
@@ -498,51 +511,94 @@ __global__ void __launch_bounds__(kThreads, Shape<TQ, TP, kDh>::blocks) paged_ro
       }
     }
     if (!whole) {
-      __syncthreads();      // the partial state is written
-      if (tid == 0) {
-        const unsigned int n = atomic_add_acq_rel_gpu(p.counters + owner0, 1u);
-        s_last = n == static_cast<unsigned int>(parts - 1);
-        if (s_last) p.counters[owner0] = 0u;
-      }
-      __syncthreads();
-      if (s_last) {
+      // ---- merge: groups of kGroup parts first, then the groups, each by its last arriver
+      auto slot_of = [&](int k) {
+        return p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kRows * (kDh + 2);
+      };
+      // Parts first, first + step, ... (n of them) into one state: the result, or part `first`.
+      auto merge = [&](int first, int step, int n, bool final) {
+        for (int i = tid; i < n * kRows; i += kThreads) {
+          const float* sl = slot_of(first + i / kRows * step) + kRows * kDh;
+          const int r = i % kRows;
+          s_w[i] = r < rows ? __ldcg(sl + r) : -INFINITY;
+          s_w[kMaxParts * kRows + i] = r < rows ? __ldcg(sl + kRows + r) : 0.f;
+        }
+        __syncthreads();
         for (int i = tid; i < rows * (kDh / 4); i += kThreads) {
           const int r = i / (kDh / 4), ch = 4 * (i % (kDh / 4));
           float M = -INFINITY, sum = 0.f;
+          for (int k = 0; k < n; ++k) M = fmaxf(M, s_w[k * kRows + r]);
+          const float ref = M == -INFINITY ? 0.f : M;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = 0; k < parts; ++k) {
-            const float* sl = p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kRows * (kDh + 2);
-            const float mk = __ldcg(sl + kRows * kDh + r), lk = __ldcg(sl + kRows * (kDh + 1) + r);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + r * kDh + ch));
-            const float mn = fmaxf(M, mk), ref = mn == -INFINITY ? 0.f : mn;
-            const float fo = ex2(M - ref), fk = ex2(mk - ref);
-            M = mn;
-            sum = sum * fo + lk * fk;
-            acc.x = acc.x * fo + x.x * fk;
-            acc.y = acc.y * fo + x.y * fk;
-            acc.z = acc.z * fo + x.z * fk;
-            acc.w = acc.w * fo + x.w * fk;
+          for (int k0 = 0; k0 < n; k0 += 8) {
+            float4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(first + min(k0 + j, n - 1) * step) + r * kDh + ch));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (k0 + j >= n) break;
+              const float w = ex2(s_w[(k0 + j) * kRows + r] - ref);
+              sum = fmaf(w, s_w[(kMaxParts + k0 + j) * kRows + r], sum);
+              acc.x = fmaf(w, x[j].x, acc.x);
+              acc.y = fmaf(w, x[j].y, acc.y);
+              acc.z = fmaf(w, x[j].z, acc.z);
+              acc.w = fmaf(w, x[j].w, acc.w);
+            }
           }
-          write_out(r, ch, acc, sum);
+          if (final) {
+            write_out(r, ch, acc, sum);
+          } else {
+            float* to = slot_of(first);
+            *reinterpret_cast<float4*>(to + r * kDh + ch) = acc;
+            if (ch == 0) {
+              to[kRows * kDh + r] = M;
+              to[kRows * (kDh + 1) + r] = sum;
+            }
+          }
         }
+      };
+      // Whether this block is the last of n to come to a counter, which is then zero again.
+      auto last_of = [&](unsigned int* counter, int n) {
+        __syncthreads();      // what the block has to show is written
+        if (tid == 0) {
+          const bool last = atomic_add_acq_rel_gpu(counter, 1u) == static_cast<unsigned int>(n - 1);
+          if (last) *counter = 0u;
+          s_last = last;
+        }
+        __syncthreads();
+        return s_last != 0;
+      };
+      const int me = static_cast<int>(blockIdx.x) - owner0, group = me / kGroup, leader = group * kGroup;
+      const int groups = (parts + kGroup - 1) / kGroup, n = min(kGroup, parts - leader);
+      // a block may lead a group of the item that ends in it and one of the item that begins in it
+      unsigned int* counter = p.counters + 3 * static_cast<size_t>(owner0 + leader);
+      if (last_of(counter + (group == 0 ? 0 : 1), n)) {
+        merge(leader, 1, n, groups == 1);
+        if (groups > 1 && last_of(p.counters + 3 * static_cast<size_t>(owner0) + 2, groups)) merge(0, kGroup, groups, true);
       }
     }
     if (end >= range.g1) break;
-    work_next(bt, p.shape, Hkv, &cur);
+    work_next(bt, shape, Hkv, &cur);
     __syncthreads();        // the queries and states of this item are done with
   }
 }
 
-template <typename TQ, typename TP, int kDh>
-cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr int smem = Shape<TQ, TP, kDh>::smem;
-  cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<TQ, TP, kDh>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename TQ, typename TP, int kDh, bool kWide>
+cudaError_t launch_shape(const PagedAttnLaunch& a, RowsParams prm, const DeviceInfo& dev, cudaStream_t stream) {
+  using S = Shape<TQ, TP, kDh, kWide>;
+  constexpr int smem = S::smem;
+  const auto kernel = paged_rows_kernel<TQ, TP, kDh, kWide>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
+  prm.shape.chunk_shift = S::chunk_shift;
   cudaLaunchConfig_t cfg = {};
-  int grid = dev.num_sms * Shape<TQ, TP, kDh>::blocks;
+  int grid = dev.num_sms * S::blocks;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -550,9 +606,19 @@ cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const Device
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_rows_kernel<TQ, TP, kDh>, prm);
+  e = cudaLaunchKernelEx(&cfg, kernel, prm);
   if (e == cudaSuccess) count_launches(1);
   return e;
+}
+
+// One wide block an SM for few items (K/V heads of sequences), several narrow ones for
+// many: MEASURED
+template <typename TQ, typename TP, int kDh>
+cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  const long long tiles = a.batch.B + static_cast<long long>(a.batch.n_tokens) * prm.shape.G / kRows;   // at most, a head
+  if constexpr (Shape<TQ, TP, kDh, true>::warps != Shape<TQ, TP, kDh, false>::warps)
+    if (tiles * a.layer.Hkv < kWideItems * dev.num_sms) return launch_shape<TQ, TP, kDh, true>(a, prm, dev, stream);
+  return launch_shape<TQ, TP, kDh, false>(a, prm, dev, stream);
 }
 
 template <int kDh>
@@ -562,13 +628,17 @@ cudaError_t launch_dh(const PagedAttnLaunch& a, const RowsParams& prm, const Dev
   return a.pool_bf16 ? launch<float, bf, kDh>(a, prm, dev, stream) : launch<float, float, kDh>(a, prm, dev, stream);
 }
 
-constexpr size_t kCounterBytes = (kMaxBlocks * 4 + 255) / 256 * 256;
+constexpr size_t kCounterBytes = (kMaxBlocks * 3 * 4 + 255) / 256 * 256;
 
 }  // namespace
 
 size_t paged_rows_workspace_bytes(int dh) {
   const size_t n = kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4;
   return (n + 255) / 256 * 256;
+}
+
+bool paged_rows_countable(const PagedAttnLaunch& a) {
+  return work_bound(a.batch, a.layer.page_shift, a.layer.Hkv, a.Hq / a.layer.Hkv, kRows, 6) < 1LL << 31;
 }
 
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream) {
@@ -585,7 +655,7 @@ cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const Devi
   prm.layer = a.layer;
   prm.shape.G = a.Hq / a.layer.Hkv;
   prm.shape.rows = kRows;
-  prm.shape.chunk_shift = kChunkShift;
+  prm.shape.coarse = false;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = 0;
   prm.shape.max_rows = max_rows;

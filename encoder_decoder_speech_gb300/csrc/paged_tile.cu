@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // scratch. This grid waits for that one at its end.
   WorkRange range;
   WorkCursor cur;
-  const bool active = work_locate<kThreads>(bt, p.shape, p.Hkv, &sm->work, &range, &cur);
+  WorkShape shape = p.shape;
+  const bool active = work_locate<kThreads, false>(bt, shape, p.Hkv, &sm->work, &range, &cur);
   if (active) {
     if (tid == 0) {
       for (int i = 0; i < kBars; ++i) {
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    const int n_chunks = static_cast<int>(range.g1 - range.g0);
+    const int n_chunks = range.g1 - range.g0;
 
     if (warp == kTmaWarp) {
       // ---------------------------------------------------------------- copies
@@ -737,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               slot[kDh * kTileRows + r] = m;
               slot[(kDh + 1) * kTileRows + r] = l;
             }
-            const long long owner0 = at.first / range.per;
-            const int parts = static_cast<int>((at.first + nc - 1) / range.per - owner0) + 1;
+            const int owner0 = at.first / range.per;
+            const int parts = (at.first + nc - 1) / range.per - owner0 + 1;
             tile_sync(t);      // the partial state is written
             if (r == 0) sm->last[t] = 0;
             if (r == 0 && ok) {
@@ -850,6 +851,7 @@ cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& 
   prm.shape.G = G;
   prm.shape.rows = kTiles * (kTileRows / G * G);      // whole tokens
   prm.shape.chunk_shift = T::chunk_shift;
+  prm.shape.coarse = false;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = kFewRows + 1;
   prm.shape.max_rows = 0x7FFFFFFF;

@@ -25,6 +25,7 @@ struct WorkShape {
   int G;              // query heads a K/V head
   int rows;           // rows a tile
   int chunk_shift;    // log2 of the keys a chunk
+  bool coarse;        // whether items are cut into fewer, larger chunks (work_locate may set it)
   int cap;            // keys the table's row can hold
   int min_rows, max_rows;   // sequences with fewer or more query rows a head are another kernel's
 };
@@ -44,14 +45,35 @@ __device__ __forceinline__ int tile_keys(const PagedSeq& s, const WorkShape& w, 
   return visible_keys(s, min(s.n - 1, (rt * w.rows + w.rows - 1) / w.G), w.cap);
 }
 
-__device__ __forceinline__ int tile_chunks(const PagedSeq& s, const WorkShape& w, int rt) {
+// Steps of 1 << chunk_shift keys of a tile.
+__device__ __forceinline__ int tile_steps(const PagedSeq& s, const WorkShape& w, int rt) {
   return max(1, (tile_keys(s, w, rt) + (1 << w.chunk_shift) - 1) >> w.chunk_shift);
 }
 
+// Chunks of a tile: its steps, or, coarse, four to seven of them in each.
+__device__ __forceinline__ int tile_chunks(const PagedSeq& s, const WorkShape& w, int rt) {
+  const int n = tile_steps(s, w, rt);
+  return w.coarse ? max(1, n >> 2) : n;
+}
+
+// The most chunks a call can have, by what the host knows of it. Kernels count in 32 bits:
+// calls of 2^31 and more are refused.
+inline long long work_bound(const PagedBatch& bt, int page_shift, int Hkv, int G, int rows, int chunk_shift) {
+  const long long tiles = bt.B + static_cast<long long>(bt.n_tokens) * G / rows;      // a head
+  const long long keys = static_cast<long long>(bt.width) << page_shift;
+  const double bound = static_cast<double>(tiles) * Hkv * static_cast<double>((keys >> chunk_shift) + 1);
+  return bound < 9e18 ? static_cast<long long>(bound) : 9000000000000000000LL;
+}
+
+// The first step of chunk c of nc.
+__device__ __forceinline__ int chunk_step(const WorkShape& w, int c, int nc, int steps) {
+  return w.coarse ? static_cast<int>(static_cast<long long>(c) * steps / nc) : c;   // (rare)
+}
+
 // Chunks of one head of a sequence.
-__device__ __forceinline__ long long head_chunks(const PagedSeq& s, const WorkShape& w) {
+__device__ __forceinline__ int head_chunks(const PagedSeq& s, const WorkShape& w) {
   const int m = work_rows(s, w);
-  long long u = 0;
+  int u = 0;
   for (int rt = 0; rt * w.rows < m; ++rt) u += tile_chunks(s, w, rt);
   return u;
 }
@@ -61,69 +83,92 @@ struct WorkCursor {
   int b, h, rt, c;     // c: first chunk of the item in this block's range
   int tiles;           // of a head of the sequence
   int nc;              // chunks of the item
-  long long first;     // number of the item's first chunk
+  int first;           // number of the item's first chunk
 };
 
 struct WorkRange {
-  long long g0, g1;    // this block's chunk numbers
-  long long per;
+  int g0, g1;          // this block's chunk numbers
+  int per;
 };
 
 // Scratch in shared memory for work_locate.
 struct WorkScratch {
-  long long scan[33];
+  int scan[2][32];
   WorkCursor cur;
 };
 
 // Number the chunks and find this block's range and the item it starts in. Called by all
-// kThreads threads of the block; returns false if the block has nothing to do.
-template <int kThreads>
-__device__ bool work_locate(const PagedBatch& bt, const WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
+// kThreads threads of the block; returns false if the block has nothing to do. With
+// kMayCoarsen, w becomes coarse where a block would have less than four steps: a merge costs
+// as much as some eight of them.
+template <int kThreads, bool kMayCoarsen>
+__device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
                             WorkCursor* cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kW = kThreads / 32;
-  // each thread counts a run of sequences
+  // each thread counts a run of sequences, in fine chunks and in coarse ones
   const int each = (bt.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * each, bt.B), b1 = min(b0 + each, bt.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += head_chunks(paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens), w) * Hkv;
-  long long incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
+  int mine[2] = {0, 0}, incl[2], before[2] = {0, 0}, total[2] = {0, 0};
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
+    const int m = work_rows(s, w);
+#pragma unroll 1
+    for (int rt = 0; rt * w.rows < m; ++rt) {
+      const int n = tile_steps(s, w, rt);
+      mine[0] += n * Hkv;
+      mine[1] += max(1, n >> 2) * Hkv;
+    }
   }
-  if (lane == 31) sm->scan[warp] = incl;
+#pragma unroll
+  for (int k = 0; k < (kMayCoarsen ? 2 : 1); ++k) {
+    incl[k] = mine[k];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl[k], off);
+      if (lane >= off) incl[k] += o;
+    }
+    if (lane == 31) sm->scan[k][warp] = incl[k];
+  }
   __syncthreads();
-  long long before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < kW; ++i) {
-    if (i < warp) before += sm->scan[i];
-    total += sm->scan[i];
-  }
-  range->per = (total + gridDim.x - 1) / gridDim.x;
-  range->g0 = range->per * blockIdx.x;
-  range->g1 = min(total, range->g0 + range->per);
+  for (int k = 0; k < (kMayCoarsen ? 2 : 1); ++k)
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      if (i < warp) before[k] += sm->scan[k][i];
+      total[k] += sm->scan[k][i];
+    }
+  w.coarse = kMayCoarsen && total[0] < 4 * static_cast<int>(gridDim.x);
+  const int k = w.coarse ? 1 : 0, blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+  const int all = k ? total[1] : total[0], own = k ? mine[1] : mine[0];
+  int at = k ? before[1] + incl[1] - own : before[0] + incl[0] - own;
+  // (all + blocks - 1 could pass 31 bits)
+  range->per = all / blocks + (all % blocks != 0 ? 1 : 0);
+  const long long g0 = static_cast<long long>(range->per) * block;
+  range->g0 = static_cast<int>(min(g0, static_cast<long long>(all)));
+  range->g1 = static_cast<int>(min(g0 + range->per, static_cast<long long>(all)));
   if (range->g0 >= range->g1) return false;     // the same in every thread
-  long long at = before + incl - mine;
-  if (range->g0 >= at && range->g0 < at + mine) {
+  if (range->g0 >= at && range->g0 - at < own) {
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
-      const long long u = head_chunks(s, w);
-      if (range->g0 < at + u * Hkv) {
+      const int u = head_chunks(s, w);
+      if (range->g0 - at < u * Hkv) {
         WorkCursor c;
         c.seq = s;
         c.b = b;
-        c.h = static_cast<int>((range->g0 - at) / u);
+        c.h = (range->g0 - at) / u;
         at += u * c.h;
         c.tiles = (work_rows(s, w) + w.rows - 1) / w.rows;
+#pragma unroll 1
         for (c.rt = 0;; ++c.rt) {
           c.nc = tile_chunks(s, w, c.rt);
-          if (range->g0 < at + c.nc || c.rt + 1 >= c.tiles) break;
+          if (range->g0 - at < c.nc || c.rt + 1 >= c.tiles) break;
           at += c.nc;
         }
         c.first = at;
-        c.c = static_cast<int>(range->g0 - at);
+        c.c = range->g0 - at;
         sm->cur = c;
         break;
       }

@@ -446,6 +446,8 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  *              256-byte aligned, zero before the first call on a new buffer
  *              (cudaMemset); calls leave its counters zero. Calls that share a
  *              workspace must be ordered on one stream.
+ * Work is counted in 31 bits: Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages *
+ * page_size / 64 + 1) must be below 2^31 (CXA_EINVAL otherwise).
  * Values that no key position of a row makes visible never reach it: rows of a page
  * behind the last key, and later tokens' rows, may hold infinities or NaN. A row that
  * sees no key is zero. Results do not change from call to call.

@@ -186,6 +186,7 @@ def test_attention_refusals(pages):
     assert need > 0
     refused(attention(pages, workspace_bytes=need - 1), "workspace smaller")
     refused(attention(pages, n_tokens=1 << 30, Hq=8), "too many query rows")
+    refused(attention(pages, B=1 << 17, max_pages=1 << 18), "below 2^31")
     for args in [(8, 3, 64, 1), (8, 4, 32, 1), (8, 4, 64, 0), (0, 4, 64, 1), (8, 0, 64, 1)]:
         assert cxa.cxa_paged_attention_workspace_bytes(*args) == 0
 
