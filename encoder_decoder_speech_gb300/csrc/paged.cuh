@@ -96,6 +96,22 @@ struct PagedAttnLaunch {
   void* workspace;
 };
 
+// Lets a kernel use `bytes` of dynamic shared memory, as much of it on an SM as there is;
+// once a device (done: a static of the caller's, one a kernel).
+struct SmemOnce {
+  unsigned char done[128];
+};
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, int device, SmemOnce* once) {
+  const bool known = device >= 0 && device < 128;
+  if (known && once->done[device]) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && known) once->done[device] = 1;    // (two threads may both come here: no harm)
+  return e;
+}
+
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // Attention, one kernel or two: sequences of up to kFewRows query rows a K/V head go to

@@ -63,7 +63,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -589,9 +589,8 @@ cudaError_t launch_shape(const PagedAttnLaunch& a, RowsParams prm, const DeviceI
   using S = Shape<TQ, TP, kDh, kWide>;
   constexpr int smem = S::smem;
   const auto kernel = paged_rows_kernel<TQ, TP, kDh, kWide>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  static SmemOnce once;
+  cudaError_t e = allow_smem(kernel, smem, dev.device, &once);
   if (e != cudaSuccess) return e;
   prm.shape.chunk_shift = S::chunk_shift;
   cudaLaunchConfig_t cfg = {};

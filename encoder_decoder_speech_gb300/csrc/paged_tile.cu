@@ -869,10 +869,8 @@ cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& 
     *msg = "the tensor maps of q and the pool cannot be encoded";
     return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<kDh>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_tile_kernel<kDh>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
+  static SmemOnce once;
+  cudaError_t e = allow_smem(paged_tile_kernel<kDh>, kSmemBytes, dev.device, &once);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   int grid = dev.num_sms;

@@ -543,47 +543,64 @@ class CrossAttentionCache:
 
 
 # ---------------------------------------------------------------- paged self-attention
-def _rows(name, t, dh=None, dtype=None, device=None):
-    """Check a packed [tokens, heads, dh] tensor; returns (tokens, heads, dh, row stride)."""
+# A decoding step makes these calls once a layer, with kernels of a few microseconds: their
+# checks are written to cost little.
+def _rows(name, t, heads=None, dh=None, tokens=None, dtype=None, index=None):
+    """Check a packed [tokens, heads, dh] tensor; returns its row stride."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head dim]")
     n, H, d = t.shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d != 1) or (s1 != d and H > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if n > 1 and s0 < H * d:
-        raise ValueError(f"{name}: the rows of different tokens must not overlap")
-    if dh is not None and d != dh:
-        raise ValueError(f"{name}: head dim {d}, expected {dh}")
+    if n > 1:
+        if s0 < H * d:
+            raise ValueError(f"{name}: the rows of different tokens must not overlap")
+    else:
+        s0 = H * d
+    if (tokens is not None and n != tokens) or (heads is not None and H != heads) or (dh is not None and d != dh):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(tokens, heads, dh)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return n, H, d, s0 if n > 1 else H * d
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return s0
 
 
-def _ints(name, t, shape, device):
+def _ints(name, t, shape, index):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on cuda:{index}")
 
 
-def _weight(name, t, dh, device):
+def _weight(name, t, dh, index):
     import torch
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (dh,) or not t.is_contiguous()
-                          or t.device != device):
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({dh},) on {device}")
+    if t.dtype != torch.float32 or t.shape != (dh,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({dh},) on cuda:{index}")
+    return t.data_ptr()
 
 
-def _on(device):
-    """The device's context, entered only when another device is current."""
-    import contextlib
+def _on_device(index, call, *args, where):
+    """call(*args) with the device current that the tensors are on; raises on a non-zero status."""
     import torch
-    if device.type != "cuda":
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if torch.cuda.current_device() == index:
+        rc = call(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args)
+    if rc != CXA_OK:
+        raise CxaError(rc, where)
+
+
+def _stream_on(index, stream):
+    """The handle of `stream`, or of the current stream of device `index`."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    return _stream(stream)
 
 
 _LAYOUTS = {"half": CXA_ROTARY_HALF, "interleaved": CXA_ROTARY_INTERLEAVED}
@@ -634,31 +651,33 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
     """Head norms (RMS, if norm_eps is given) and rotation of q [N, Hq, dh] and k [N, Hk, dh]
     (or None), float32 or bfloat16, at positions pos [N] int32. Token rows may be strided
     slices; q_out and k_out may be q and k. Returns (q_out, k_out)."""
-    import torch
-    n, Hq, dh, qs = _rows("q", q)
-    dev, dt = q.device, q.dtype
-    _ints("pos", pos, (n,), dev)
-    _weight("q_weight", q_weight, dh, dev)
-    _weight("k_weight", k_weight, dh, dev)
-    Hk = ks = kos = 0
+    qs = _rows("q", q)
+    n, Hq, dh = q.shape
+    dt, at = q.dtype, q.get_device()
+    if at < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    _ints("pos", pos, (n,), at)
     if q_out is None:
-        q_out = torch.empty((n, Hq, dh), dtype=dt, device=dev)
-    no, Ho, _, qos = _rows("q_out", q_out, dh, dt, dev)
-    if no != n or Ho != Hq:
-        raise ValueError("q_out must have q's shape")
+        q_out = q.new_empty((n, Hq, dh))
+    qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
+    Hk = ks = kos = 0
+    kp = kop = None
     if k is not None:
-        nk, Hk, _, ks = _rows("k", k, dh, dt, dev)
+        Hk = k.shape[1] if k.dim() == 3 else 0
+        ks = _rows("k", k, Hk, dh, n, dt, at)
         if k_out is None:
-            k_out = torch.empty((n, Hk, dh), dtype=dt, device=dev)
-        no, Ho, _, kos = _rows("k_out", k_out, dh, dt, dev)
-        if nk != n or no != n or Ho != Hk:
-            raise ValueError("k must have q's tokens and k_out k's shape")
+            k_out = k.new_empty((n, Hk, dh))
+        kos = _rows("k_out", k_out, Hk, dh, n, dt, at)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    else:
+        k_out = None
     norm, eps = _norm(norm_eps)
-    with _on(dev):
-        check(cxa_qk_norm_rope(q, qs, Hq, k, ks, Hk, dh, n, pos, norm, eps, q_weight, k_weight,
-                               rotary.handle if rotary is not None else None, q_out, qos,
-                               k_out if k is not None else None, kos, _dtype_code(dt), stream), "cxa_qk_norm_rope")
-    return q_out, (k_out if k is not None else None)
+    _on_device(at, load().cxa_qk_norm_rope, q.data_ptr(), qs, Hq, kp, ks, Hk, dh, n, pos.data_ptr(), norm, eps,
+               None if q_weight is None else _weight("q_weight", q_weight, dh, at),
+               None if k_weight is None else _weight("k_weight", k_weight, dh, at),
+               None if rotary is None else rotary.handle, q_out.data_ptr(), qos, kop, kos, _dtype_code(dt),
+               _stream_on(at, stream), where="cxa_qk_norm_rope")
+    return q_out, k_out
 
 
 class PagedCache:
@@ -676,35 +695,40 @@ class PagedCache:
         tdt = torch.float32 if _DTYPES[cache_dtype] == CXA_F32 else torch.bfloat16
         self.Kp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
         self.Vp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
-        self._ws = {}
+        self._ws, self._ws_bytes = {}, {}
+        self._at = self.Kp.get_device()
         rc, self.handle = cxa_pages_create(self.Kp, self.Vp, num_pages, page_size, L, Hkv, dh, _DTYPES[cache_dtype])
         check(rc, "cxa_pages_create")
 
     def _batch(self, q_start, kv_len, page_table):
-        dev = self.Kp.device
         if page_table.dim() != 2:
             raise ValueError("page_table must be [sequences, pages]")
         B, width = page_table.shape
-        _ints("q_start", q_start, (B + 1,), dev)
-        _ints("kv_len", kv_len, (B,), dev)
-        _ints("page_table", page_table, (B, width), dev)
+        _ints("q_start", q_start, (B + 1,), self._at)
+        _ints("kv_len", kv_len, (B,), self._at)
+        _ints("page_table", page_table, (B, width), self._at)
         return B, width
 
     def workspace(self, Hq: int, max_new: int, stream=None):
         """A zeroed attention workspace, kept per stream. While a graph is captured it is a
         new one (cleared in the graph), as replays may run beside anything else."""
         import torch
-        n = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
-        key = _stream(stream)
+        n = self._ws_bytes.get((Hq, max_new))
+        if n is None:
+            if len(self._ws_bytes) > 4096:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[Hq, max_new] = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
+        key = _stream_on(self._at, stream)
         ws = self._ws.get(key)
         capturing = torch.cuda.is_current_stream_capturing()
         if ws is not None and ws.numel() >= n and not capturing:
             return ws
-        if stream is None or key == torch.cuda.current_stream().cuda_stream:
-            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(key)):
+        with torch.cuda.device(self._at):
+            if stream is None or key == torch.cuda.current_stream().cuda_stream:
                 ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(key)):
+                    ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
         if not capturing:
             self._ws[key] = ws
         return ws
@@ -714,29 +738,26 @@ class PagedCache:
         """Write k, v [N, Hkv, dh] of the new tokens into their pages, k normalised (RMS, if
         norm_eps is given) and rotated; with q [N, Hq, dh] also return q_out, the queries
         normalised and rotated (rows behind the batch's last token are left as they are)."""
-        import torch
-        dev, dt = self.Kp.device, k.dtype
+        at, dh, dt, n = self._at, self.dh, k.dtype, k.shape[0]
         B, width = self._batch(q_start, kv_len, page_table)
-        n, Hk, _, ks = _rows("k", k, self.dh, None, dev)
-        nv, Hv, _, vs = _rows("v", v, self.dh, dt, dev)
-        if (Hk, nv, Hv) != (self.Hkv, n, self.Hkv):
-            raise ValueError(f"k and v must be [tokens, {self.Hkv}, {self.dh}]")
-        _weight("q_weight", q_weight, self.dh, dev)
-        _weight("k_weight", k_weight, self.dh, dev)
+        ks = _rows("k", k, self.Hkv, dh, n, dt, at)
+        vs = _rows("v", v, self.Hkv, dh, n, dt, at)
         Hq = qs = qos = 0
+        qp = qop = None
         if q is not None:
-            nq, Hq, _, qs = _rows("q", q, self.dh, dt, dev)
+            Hq = q.shape[1] if q.dim() == 3 else 0
+            qs = _rows("q", q, Hq, dh, n, dt, at)
             if q_out is None:
-                q_out = torch.empty((n, Hq, self.dh), dtype=dt, device=dev)
-            no, Ho, _, qos = _rows("q_out", q_out, self.dh, dt, dev)
-            if nq != n or no != n or Ho != Hq:
-                raise ValueError("q must have k's tokens and q_out q's shape")
+                q_out = q.new_empty((n, Hq, dh))
+            qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
         norm, eps = _norm(norm_eps)
-        with _on(dev):
-            check(cxa_paged_append(self.handle, layer, B, n, q_start, kv_len, page_table, width, k, ks, v, vs, q, qs,
-                                   Hq, q_out if q is not None else None, qos, norm, eps, q_weight, k_weight,
-                                   rotary.handle if rotary is not None else None, _dtype_code(dt), stream),
-                  "cxa_paged_append")
+        _on_device(at, load().cxa_paged_append, self.handle, layer, B, n, q_start.data_ptr(), kv_len.data_ptr(),
+                   page_table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, qop, qos, norm, eps,
+                   None if q_weight is None else _weight("q_weight", q_weight, dh, at),
+                   None if k_weight is None else _weight("k_weight", k_weight, dh, at),
+                   None if rotary is None else rotary.handle, _dtype_code(dt), _stream_on(at, stream),
+                   where="cxa_paged_append")
         return q_out if q is not None else None
 
     def attend(self, layer: int, q, q_start, kv_len, page_table, max_new: int, out=None, scale: float = 0.0,
@@ -744,19 +765,20 @@ class PagedCache:
         """Attention of the new tokens' queries q [N, Hq, dh] over their sequences' keys up to
         each token's own. max_new: an upper bound of the new tokens of one sequence. Returns
         out [N, Hq, dh] (rows behind the batch's last token are left as they are)."""
-        import torch
-        dev, dt = self.Kp.device, q.dtype
+        at, dh, dt = self._at, self.dh, q.dtype
         B, width = self._batch(q_start, kv_len, page_table)
-        n, Hq, _, qs = _rows("q", q, self.dh, None, dev)
+        qs = _rows("q", q, None, dh, None, None, at)
+        n, Hq, _ = q.shape
         if out is None:
-            out = torch.empty((n, Hq, self.dh), dtype=dt, device=dev)
-        no, Ho, _, os_ = _rows("out", out, self.dh, dt, dev)
-        if (no, Ho) != (n, Hq):
-            raise ValueError("out must have q's shape")
-        with _on(dev):
-            ws = workspace if workspace is not None else self.workspace(Hq, max_new, stream)
-            check(cxa_paged_attention(self.handle, layer, B, n, max_new, q_start, kv_len, page_table, width, q, qs, Hq,
-                                      out, os_, scale, _dtype_code(dt), ws, ws.numel(), stream), "cxa_paged_attention")
+            out = q.new_empty((n, Hq, dh))
+        os_ = _rows("out", out, Hq, dh, n, dt, at)
+        ws = workspace if workspace is not None else self.workspace(Hq, max_new, stream)
+        if ws.get_device() != at or not ws.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
+        _on_device(at, load().cxa_paged_attention, self.handle, layer, B, n, max_new, q_start.data_ptr(),
+                   kv_len.data_ptr(), page_table.data_ptr(), width, q.data_ptr(), qs, Hq, out.data_ptr(), os_, scale,
+                   _dtype_code(dt), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(at, stream),
+                   where="cxa_paged_attention")
         return out
 
     def check(self, q_start, kv_len, page_table, n_tokens: int) -> None:
