@@ -7,7 +7,7 @@
 // one K/V head), dealt out by paged_work.cuh in chunks of 16 KB of K and of V (128 keys of
 // 64 channels, 64 keys of 128). One block runs on an SM and works on both tiles of its item,
 // which share each K and V tile read (a block a tile, two blocks an SM, read twice as much:
-// 417 us against {NEW} us for 2048 tokens over 32768 keys of 20 heads, its K and V coming 11
+// 417 us against 345 us for 2048 tokens over 32768 keys of 20 heads, its K and V coming 11
 // times from DRAM); one tile's products run under the other's exponentials:
 //
 //  * warp 10 streams by TMA: the item's Q (a box of 128 / G tokens x G heads a tile, which
@@ -50,7 +50,7 @@ namespace cxa {
 namespace {
 
 constexpr int kTiles = 2;                    // of an item
-constexpr int kSoftWarps = 4;                // a tile
+constexpr int kSoftWarps = 8;                // a tile: two to 32 rows, each with half of a chunk's keys
 constexpr int kMmaWarp = kTiles * kSoftWarps, kTmaWarp = kMmaWarp + kTiles;
 constexpr int kThreads = (kTmaWarp + 1) * 32;
 constexpr int kTileRows = 128;
@@ -60,6 +60,7 @@ constexpr int kQBytes = 65536;               // the Q tiles of two items of 64 c
 constexpr int kMaxBlocks = 160;
 constexpr uint32_t kTmemTile = 256;          // columns of a tile
 constexpr float kMoveLog2 = 8.f;
+constexpr int kGroup = 8;                    // parts of an item that are merged at once, and then of those
 
 // Barriers; the last four one a tile.
 enum Bars {
@@ -75,7 +76,7 @@ enum Bars {
   kPvDone = kPFull + kTiles,
   kBars = kPvDone + kTiles
 };
-static_assert(kBars <= 32, "a bit mask holds the barriers");
+static_assert(kSFull <= 32, "a bit mask holds the barriers that copies complete");
 struct Small {
   uint64_t bars[kBars];
   WorkScratch work;
@@ -85,10 +86,11 @@ struct Small {
   int tmem;
   int last[kTiles];
   volatile int acc[kTiles]; // the segment's first P.V adds to O
+  float swap[kTiles][kTileRows];   // between the two threads of a row
 };
 
-constexpr int kSmemBytes = kQBytes + 2 * kStages * kTileBytes + 1024;
-static_assert(sizeof(Small) <= 1024, "the small arrays fit behind the tiles");
+constexpr int kSmemBytes = kQBytes + 2 * kStages * kTileBytes + 3072;
+static_assert(sizeof(Small) <= 3072, "the small arrays fit behind the tiles");
 
 template <int kDh>
 struct Tile {
@@ -105,7 +107,7 @@ struct TileParams {
   void* out;
   long long o_stride;
   float qscale;
-  unsigned int* counters;    // [grid][kTiles]
+  unsigned int* counters;    // [grid][kTiles][3]
   float* part;               // [2 * grid][kTiles][kDh + 2][128]
   unsigned int* status;
   PagedBatch batch;
@@ -118,20 +120,33 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The softmax warps of a tile, and of both.
+// The softmax warps of a tile, of both, and the two of 32 rows.
 __device__ __forceinline__ void tile_sync(int tile) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + tile) : "memory");
+  asm volatile("bar.sync %0, 256;" ::"r"(1 + tile) : "memory");
 }
-__device__ __forceinline__ void item_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void item_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 __device__ __forceinline__ bool item_or(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 3, 256, p;\n\t"
+      "bar.red.or.pred q, 3, 512, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_or(int pair, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(4 + pair)
       : "memory");
   return r != 0;
 }
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok)      // the copies under way land before the block ends
-        for (int b = 0; b < kBars; ++b)
+        for (int b = 0; b < kSFull; ++b)
           if (armed & (1u << b)) mbar_wait(bar(b), (parity >> b) & 1u);
     } else if (warp >= kMmaWarp) {
       // ---------------------------------------------------------------- products of a tile
@@ -469,9 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------------- softmax, a row a thread
-      const int t = warp / kSoftWarps, r = tid - t * kTileRows;
-      const uint32_t my_tmem = tmem + t * kTmemTile + (static_cast<uint32_t>((warp % kSoftWarps) * 32) << 16);
+      // ---------------------------------------------------------------- softmax, two threads a row
+      const int t = warp / kSoftWarps, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, pair = t * 4 + (warp & 3);
+      const uint32_t my_tmem = tmem + t * kTmemTile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      constexpr int XC = T::chunk / 2, OC = kDh / 2;      // this thread's columns of S and of O
+      const uint32_t my_s = my_tmem + hf * XC, my_p = my_tmem + T::p_col + hf * (XC / 2), my_o = my_tmem + T::o_col + hf * OC;
       const int box_shift = min(p.page_shift, T::chunk_shift);
       const float2 qs2 = make_float2(p.qscale, p.qscale);
       WorkCursor& at = sm->at[warp];
@@ -480,11 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int c = cur.c, c0 = cur.c, nc = 0, j = 0;       // j: chunks of this tile so far
       float m = -INFINITY, l = 0.f;
       bool fresh = true;
-      constexpr int XB = T::chunk / 32;
+      constexpr int XB = XC / 32;
       // The row's scores, all in registers, so that the next chunk's products can start.
       auto load_scores = [&](uint32_t (&x)[XB][32]) {
 #pragma unroll
-        for (int b = 0; b < XB; ++b) tmem_ld_32x32b_x32(my_tmem + 32 * b, x[b]);
+        for (int b = 0; b < XB; ++b) tmem_ld_32x32b_x32(my_s + 32 * b, x[b]);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
@@ -500,12 +517,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             mx[(e / 2) & 3] = fmaxf(mx[(e / 2) & 3], fmaxf(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
         const bool pv = j == 0 || mbar_test_wait(bar(kPvDone + t), (j - 1) & 1);
-        // the references of a warp's rows move together, to the largest score so far
+        // the references of 32 rows move together, to the largest score so far
         float corr = 1.f;
-        const bool moved = __any_sync(0xffffffffu, top > m + kMoveLog2);
+        const bool moved = pair_or(pair, top > m + kMoveLog2);
         if (__builtin_expect(moved, 0)) {
+          if (hf == 1) sm->swap[t][r] = top;
+          pair_sync(pair);
+          if (hf == 0) {
+            top = fmaxf(top, sm->swap[t][r]);
+            sm->swap[t][r] = top;
+          }
+          pair_sync(pair);
+          top = sm->swap[t][r];
           const float to = fmaxf(m, top);
           corr = m == -INFINITY ? 0.f : ex2(m - to);
           m = to;
@@ -523,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             v.x = ex2(v.x);
             v.y = ex2(v.y);
             sum[e & 1] = add2(sum[e & 1], v);
-            x[b / 2][16 * (b & 1) + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
+            x[0][16 * b + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
           }
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
@@ -533,17 +558,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (__builtin_expect(moved && c != c0, 0)) {
 #pragma unroll 1
-          for (int b = 0; b < kDh / 16; ++b) {
+          for (int b = 0; b < OC / 16; ++b) {
             uint32_t o[16];
-            tmem_ld_32x32b_x16(my_tmem + T::o_col + 16 * b, o);
+            tmem_ld_32x32b_x16(my_o + 16 * b, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st_32x32b_x16(my_tmem + T::o_col + 16 * b, o);
+            tmem_st_32x32b_x16(my_o + 16 * b, o);
           }
         }
+        if constexpr (XB == 2) {
+          tmem_st_32x32b_x32(my_p, x[0]);
+        } else {
+          uint32_t w[16];
 #pragma unroll
-        for (int b = 0; b < XB / 2; ++b) tmem_st_32x32b_x32(my_tmem + T::p_col + 32 * b, x[b]);
+          for (int e = 0; e < 16; ++e) w[e] = x[0][e];
+          tmem_st_32x32b_x16(my_p, w);
+        }
         tmem_st_wait();
       };
       auto give_p = [&]() {
@@ -558,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = -INFINITY;
           l = 0.f;
           c0 = c;
-          if (r == 0) sm->acc[t] = 0;
+          if (r == 0 && hf == 0) sm->acc[t] = 0;
         }
         // The chunks that every row of the item sees, but for the tile's last, in a loop of
         // their own: the code between two of them is fetched anew for each by every warp.
@@ -596,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool special = key0 + T::chunk > see_item || bad != 0;   // some row of the item misses a key
         if (!here) {
           tile_sync(t);         // every warp of the tile has seen the chunk come
-          if ((warp % kSoftWarps) == 0 && lane == 0) mbar_arrive(bar(kKEmpty + st));
+          if (warp % kSoftWarps == 0 && lane == 0) mbar_arrive(bar(kKEmpty + st));
           __syncwarp();
         }
         if (here) {
@@ -607,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < XB; ++b)
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const int k = 32 * b + e;
+                const int k = hf * XC + 32 * b + e;
                 if (k >= lim || ((bad >> (k >> box_shift)) & 1u) != 0) x[b][e] = 0xFF800000u;   // -inf
               }
           }
@@ -619,39 +650,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           // keys from hi on by none
           const int lo = max(0, see_item - key0), hi = min(T::chunk, keys - key0);
           wait_warp(kVFull + st, round & 1);
-          const int key = r & (T::chunk - 1), half = r >> T::chunk_shift;   // this thread's part of V
+          const int key = r & (T::chunk - 1), half = r >> T::chunk_shift;   // this thread's part of V: 64 bytes
           const bool has = T::chunk * T::halves > r;
           const bool key_bad = ((bad >> (key >> box_shift)) & 1u) != 0;
           const uint32_t vt = v_base + st * kTileBytes;
-          const uint32_t vrow = vt + half * T::half_bytes + key * 128;
+          const uint32_t vrow = vt + half * T::half_bytes + key * 128 + hf * 64;
           bool wild = false;
           if (has && key >= lo && key < hi && !key_bad)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
               const uint4 u = ld_shared_v4(vrow + 16 * q);
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) wild |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
             }
+          tc_fence_before();     // (the other thread's half of P)
           wild = item_or(wild);
+          tc_fence_after();
           if (wild) {
             if (here) {
-              for (int b = 0; b < kDh / 32; ++b) {
+#pragma unroll 1
+              for (int b = 0; b < OC / 32; ++b) {
+                const int ch = hf * OC + 32 * b;         // first of 32 channels
                 uint32_t o[32];
-                tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+                tmem_ld_32x32b_x32(my_o + 32 * b, o);
                 tmem_ld_wait();
                 if (starts)
 #pragma unroll
                   for (int e = 0; e < 32; ++e) o[e] = 0u;
+#pragma unroll 1
                 for (int k = lo; k < hi; ++k) {
                   const uint32_t w = tmem_ld_1(my_tmem + T::p_col + (k >> 1));
                   tmem_ld_wait();
                   if (k < lim && ((bad >> (k >> box_shift)) & 1u) == 0) {
                     const float pk = __uint_as_float((k & 1) ? w & 0xFFFF0000u : w << 16);
-                    const uint32_t vr = vt + (b / 2) * T::half_bytes + k * 128;
+                    const uint32_t vr = vt + (ch / 64) * T::half_bytes + k * 128;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                      const uint4 u = ld_shared_v4(vr + (((4 * (b & 1) + q) ^ (k & 7)) << 4));
+                      const uint4 u = ld_shared_v4(vr + (((ch % 64 / 8 + q) ^ (k & 7)) << 4));
                       const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                       for (int e = 0; e < 4; ++e) {
@@ -665,9 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   __syncwarp();    // the next load is the whole warp's
                 }
-                tmem_st_32x32b_x32(my_tmem + T::o_col + 32 * b, o);
+                tmem_st_32x32b_x32(my_o + 32 * b, o);
                 tmem_st_wait();
               }
+            }
+            tc_fence_before();
+            item_sync();      // V and P have been read
+            tc_fence_after();
+            if (here && hf == 0) {
               for (int k = lo >> 1; 2 * k < hi; ++k) {    // P.V leaves these keys out
                 uint32_t w = tmem_ld_1(my_tmem + T::p_col + k);
                 tmem_ld_wait();
@@ -676,12 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tmem_st_wait();
             }
-            item_sync();      // V has been read
           }
-          if (here && starts && wild && r == 0) sm->acc[t] = 1;
+          if (here && starts && wild && r == 0 && hf == 0) sm->acc[t] = 1;
           if (has && (key_bad || key >= (wild ? lo : hi)))
 #pragma unroll
-            for (int q = 0; q < 8; ++q) st_shared_v4(vrow + 16 * q, 0u, 0u, 0u, 0u);
+            for (int q = 0; q < 4; ++q) st_shared_v4(vrow + 16 * q, 0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
         }
         if (here) {
@@ -689,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           wait_warp(kVFull + st, round & 1);
           tile_sync(t);         // every warp of the tile has left V
-          if ((warp % kSoftWarps) == 0 && lane == 0) mbar_arrive(bar(kVEmpty + st));
+          if (warp % kSoftWarps == 0 && lane == 0) mbar_arrive(bar(kVEmpty + st));
           __syncwarp();
         }
 
@@ -703,6 +743,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (r < rows ? (at.seq.q0 + tok) * p.o_stride + static_cast<long long>(hd) * kDh : 0);
           constexpr size_t kSlot = static_cast<size_t>(kTileRows) * (kDh + 2);
           float* slot = p.part + ((2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTiles + t) * kSlot;
+          // the two threads of a row add their sums up
+          if (hf == 1) sm->swap[t][r] = l;
+          pair_sync(pair);
+          if (hf == 0) {
+            l += sm->swap[t][r];
+            sm->swap[t][r] = l;
+          }
+          pair_sync(pair);
+          l = sm->swap[t][r];
+          // 32 channels, from hf * OC + 32 * b on
           auto put = [&](int b, const float (&o)[32], float inv) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -711,14 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               u.y = pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
               u.z = pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
               u.w = pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * b + 8 * q) = u;
+              *reinterpret_cast<uint4*>(dst + hf * OC + 32 * b + 8 * q) = u;
             }
           };
           const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-          for (int b = 0; b < kDh / 32; ++b) {
+#pragma unroll 1
+          for (int b = 0; b < OC / 32; ++b) {
             uint32_t w[32];
-            tmem_ld_32x32b_x32(my_tmem + T::o_col + 32 * b, w);
+            tmem_ld_32x32b_x32(my_o + 32 * b, w);
             tmem_ld_wait();
             if (r < rows && ok) {
               float o[32];
@@ -728,55 +778,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put(b, o, inv);
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) slot[(32 * b + e) * kTileRows + r] = o[e];
+                for (int e = 0; e < 32; ++e) slot[(hf * OC + 32 * b + e) * kTileRows + r] = o[e];
               }
             }
+            __syncwarp();
           }
           tc_fence_before();
           if (!whole) {
-            if (r < rows && ok) {
+            if (r < rows && ok && hf == 0) {
               slot[kDh * kTileRows + r] = m;
               slot[(kDh + 1) * kTileRows + r] = l;
             }
+            // merged in groups of kGroup parts first, then the groups, each by its last arriver
             const int owner0 = at.first / range.per;
             const int parts = (at.first + nc - 1) / range.per - owner0 + 1;
-            tile_sync(t);      // the partial state is written
-            if (r == 0) sm->last[t] = 0;
-            if (r == 0 && ok) {
-              const unsigned int n = atomic_add_acq_rel_gpu(p.counters + owner0 * kTiles + t, 1u);
-              sm->last[t] = n == static_cast<unsigned int>(parts - 1);
-              if (sm->last[t]) p.counters[owner0 * kTiles + t] = 0u;
-            }
-            tile_sync(t);
-            if (sm->last[t] && r < rows) {
-              auto part = [&](int k) {
-                return p.part + ((2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTiles + t) * kSlot + r;
-              };
+            auto part = [&](int k) {
+              return p.part + ((2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTiles + t) * kSlot + r;
+            };
+            auto last_of = [&](int counter, int n) {
+              tile_sync(t);      // what the tile's warps have to show is written
+              if (r == 0 && hf == 0) {
+                bool last = false;
+                if (ok) {
+                  unsigned int* const at_counter = p.counters + counter;
+                  last = atomic_add_acq_rel_gpu(at_counter, 1u) == static_cast<unsigned int>(n - 1);
+                  if (last) *at_counter = 0u;
+                }
+                sm->last[t] = last;
+              }
+              tile_sync(t);
+              return sm->last[t] != 0;
+            };
+            // parts first, first + step, ... (n of them) into the result, or into part `first`
+            auto merge = [&](int first, int step, int n, bool final) {
+              const int m_n = r < rows ? n : 0;
               float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-              for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k) + kDh * kTileRows));
+              for (int k = 0; k < m_n; ++k) M = fmaxf(M, __ldcg(part(first + k * step) + kDh * kTileRows));
               const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-              for (int k = 0; k < parts; ++k)
-                L += __ldcg(part(k) + (kDh + 1) * kTileRows) * ex2(__ldcg(part(k) + kDh * kTileRows) - ref);
+              for (int k = 0; k < m_n; ++k) {
+                const float* src = part(first + k * step) + kDh * kTileRows;
+                L += __ldcg(src + kTileRows) * ex2(__ldcg(src) - ref);
+              }
               const float linv = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll 1
-              for (int b = 0; b < kDh / 32; ++b) {
+              for (int b = 0; b < OC / 32; ++b) {
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 2
-                for (int k = 0; k < parts; ++k) {
-                  const float* src = part(k);
+#pragma unroll 1
+                for (int k = 0; k < m_n; ++k) {
+                  const float* src = part(first + k * step);
                   const float f = ex2(__ldcg(src + kDh * kTileRows) - ref);
                   float w[32];
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) w[e] = __ldcg(src + (32 * b + e) * kTileRows);
+                  for (int e = 0; e < 32; ++e) w[e] = __ldcg(src + (hf * OC + 32 * b + e) * kTileRows);
 #pragma unroll
                   for (int e = 0; e < 32; ++e) o[e] = fmaf(f, w[e], o[e]);
                 }
-                put(b, o, linv);
+                if (m_n == 0) continue;
+                if (final) {
+                  put(b, o, linv);
+                } else {
+                  float* to = const_cast<float*>(part(first));
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) to[(hf * OC + 32 * b + e) * kTileRows] = o[e];
+                }
               }
+              if (!final) {
+                __syncwarp();
+                pair_sync(pair);      // both threads of a row have read the old values
+                if (hf == 0 && m_n != 0) {
+                  float* to = const_cast<float*>(part(first)) + kDh * kTileRows;
+                  to[0] = M;
+                  to[kTileRows] = L;
+                }
+              }
+            };
+            const int group = (static_cast<int>(blockIdx.x) - owner0) / kGroup, leader = group * kGroup;
+            const int groups = (parts + kGroup - 1) / kGroup, n = min(kGroup, parts - leader);
+            // a block may lead a group of the item that ends in it and one of the item that begins in it
+            const int counter = ((owner0 + leader) * kTiles + t) * 3;
+            if (last_of(counter + (group == 0 ? 0 : 1), n)) {
+              merge(leader, 1, n, groups == 1);
+              if (groups > 1 && last_of((owner0 * kTiles + t) * 3 + 2, groups)) merge(0, kGroup, groups, true);
             }
           }
         }
@@ -830,7 +916,7 @@ bool encode(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuu
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kCounterBytes = (kMaxBlocks * kTiles * 4 + 255) / 256 * 256;
+constexpr size_t kCounterBytes = (kMaxBlocks * kTiles * 3 * 4 + 255) / 256 * 256;
 
 template <int kDh>
 cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
