@@ -5,7 +5,11 @@
 //   s_rj = scale * log2(e) * q_r . K_j  over the keys j that row r may see,
 //
 // in one pass with the running reference m_r. Bound by memory: K and V are read once for
-// the kRows = 16 query rows of a tile (query heads of one K/V head times new tokens).
+// the 16 query rows of a tile (query heads of one K/V head times new tokens; 32 in fp32
+// chunks). 64 single tokens over 4400 keys of 8 heads of 128 channels, 4 query heads each:
+// 181 us, 6.5 TB/s; one token over 262144 keys of 4 heads of 64: 57 us, of which some 18 are
+// start, merge and imbalance; 5 fp32 tokens in each of 16 sequences: 39 us, 3.4 TB/s, where
+// a block's two items of 8 us each pay start and merge for themselves.
 //
 // A warp takes 16 keys a step, which it streams into a ring of its own in shared memory
 // (cp.async, kStages steps; no barrier but the warp's), and multiplies on the tensor cores
@@ -35,12 +39,12 @@
 namespace cxa {
 namespace {
 
-constexpr int kRows = 16;            // query rows a tile
+constexpr int kRows = 16;            // query rows of a product
 constexpr int kStep = 16;            // keys a warp takes at a time
 constexpr int kMaxBlocks = 160 * 4;
 constexpr int kGroup = 16;           // parts of an item that are merged at once, and then of those
 constexpr int kMaxParts = (kMaxBlocks + kGroup - 1) / kGroup;
-constexpr int kWideItems = 1;        // items an SM below which wide blocks run
+constexpr int kWideItems = 1;        // items an SM below which wide blocks run (see launch)
 constexpr float kMoveLog2 = 8.f;     // a row's reference moves only past this margin
 
 struct RowsParams {
@@ -49,7 +53,7 @@ struct RowsParams {
   long long q_stride, o_stride;
   float qscale;                      // scale * log2(e)
   unsigned int* counters;            // [grid][3], zero between calls
-  float* part;                       // [2 * grid][kRows][kDh + 2]
+  float* part;                       // [2 * grid][rows of a tile][kDh + 2]
   unsigned int* status;
   PagedBatch batch;
   PagedLayer layer;
@@ -91,8 +95,9 @@ __device__ __forceinline__ bool nonfinite(uint32_t w, bool bf16_pair) {
   return (w & 0x7F800000u) == 0x7F800000u;
 }
 
-template <typename TQ, typename TP, int kDh, bool kWide>
+template <typename TQ, typename TP, int kDh, bool kWide, int kMt>
 struct Shape {
+  static constexpr int rows = kMt * kRows;         // query rows a tile
   static constexpr bool q32 = sizeof(TQ) == 4, p32 = sizeof(TP) == 4;
   static constexpr int QP = q32 ? 3 : 1;           // bf16 parts of a query value,
   static constexpr int KP = p32 ? 3 : 1;           // of a K or V value
@@ -107,13 +112,13 @@ struct Shape {
   // One block of many warps an SM (kWide), or several of four; a chunk is a step of each
   // warp. The rings hold three steps a warp, and as many warps run as that leaves room for.
   static constexpr int stages = 3;
-  static constexpr int warps_sm = 2048 / row_bytes;
+  static constexpr int warps_sm = kMt > 1 && row_bytes <= 128 ? 8 : 2048 / row_bytes;
   static constexpr int warps = kWide ? warps_sm : 4, blocks = warps_sm / warps, threads = warps * 32;
   static constexpr int chunk_shift = warps == 16 ? 8 : warps == 8 ? 7 : 6;
   static constexpr int ring_bytes = warps * stages * 2 * half_bytes;
-  static constexpr int q_bytes = QP * KS * 32 * 16;
-  static constexpr int merge_bytes = warps * kRows * PE * 4 + 2 * warps * kRows * 4;
-  static_assert(2 * kMaxParts * kRows * 4 <= merge_bytes, "the weights of a merge fit");
+  static constexpr int q_bytes = kMt * QP * KS * 32 * 16;
+  static constexpr int merge_bytes = warps * rows * PE * 4 + 2 * warps * rows * 4;
+  static_assert(2 * kMaxParts * rows * 4 <= merge_bytes, "the weights of a merge fit");
   static constexpr int smem = q_bytes + (ring_bytes > merge_bytes ? ring_bytes : merge_bytes);
 };
 
@@ -190,21 +195,21 @@ __device__ __forceinline__ void v_operand(const uint4 (&v)[4][S::VV], int c, uin
   }
 }
 
-template <typename TQ, typename TP, int kDh, bool kWide>
-__global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, TP, kDh, kWide>::blocks)
+template <typename TQ, typename TP, int kDh, bool kWide, int kMt>
+__global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide, kMt>::threads, Shape<TQ, TP, kDh, kWide, kMt>::blocks)
     paged_rows_kernel(const __grid_constant__ RowsParams p) {
-  using S = Shape<TQ, TP, kDh, kWide>;
-  constexpr int kWarps = S::warps, kThreads = S::threads;
+  using S = Shape<TQ, TP, kDh, kWide, kMt>;
+  constexpr int kWarps = S::warps, kThreads = S::threads, kTile = S::rows;
   extern __shared__ __align__(1024) uint8_t smem[];   // rows of the rings fill whole bank lines
   __shared__ WorkScratch s_work;
   __shared__ int s_last;
-  uint4* s_q = reinterpret_cast<uint4*>(smem);                             // [QP][KS][32 lanes]
+  uint4* s_q = reinterpret_cast<uint4*>(smem);                             // [kMt][QP][KS][32 lanes]
   // the warps' rings, and once they have run dry the merge of the warps' states
   const uint32_t ring = smem_u32(smem) + S::q_bytes + (threadIdx.x >> 5) * (S::stages * 2 * S::half_bytes);
-  float* s_o = reinterpret_cast<float*>(smem + S::q_bytes);                // [kWarps][kRows][PE]
-  float* s_m = s_o + kWarps * kRows * S::PE;                               // [kWarps][kRows]
-  float* s_l = s_m + kWarps * kRows;
-  float* s_w = s_o;                                                        // [2][kMaxParts][kRows], in a merge
+  float* s_o = reinterpret_cast<float*>(smem + S::q_bytes);                // [kWarps][rows][PE]
+  float* s_m = s_o + kWarps * kTile * S::PE;                               // [kWarps][rows]
+  float* s_l = s_m + kWarps * kTile;
+  float* s_w = s_o;                                                        // [2][kMaxParts][rows], in a merge
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -222,8 +227,8 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
     const int end = min(range.g1, cur.first + cur.nc);
     const int c0 = cur.c, c1 = end - cur.first;
     const PagedSeq seq = cur.seq;
-    const int row0 = cur.rt * kRows;
-    const int rows = min(kRows, work_rows(seq, shape) - row0);
+    const int row0 = cur.rt * kTile;
+    const int rows = min(kTile, work_rows(seq, shape) - row0);
     const int keys = tile_keys(seq, shape, cur.rt);
 
     // ---- the first steps on their way
@@ -275,13 +280,13 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
 
     // ---- the queries as A operands: lane (g, t) holds rows g and g + 8, channels to match
     // the K loads
-    for (int i = tid; i < S::KS * 32; i += kThreads) {
-      const int s = i >> 5, ql = i & 31, qg = ql >> 2, qt = ql & 3;
+    for (int i = tid; i < kMt * S::KS * 32; i += kThreads) {
+      const int mt = i / (S::KS * 32), s = (i >> 5) % S::KS, ql = i & 31, qg = ql >> 2, qt = ql & 3;
       const int ch = S::p32 ? 16 * s + 4 * qt : 32 * (s >> 1) + 8 * qt + 4 * (s & 1);
       uint32_t w[2][2][S::QP];     // [row][pair of channels]
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = qg + 8 * r;
+        const int row = mt * kRows + qg + 8 * r;
         const bool ok = row < rows;
         const int tok = (row0 + row) / G, hd = cur.h * G + (row0 + row) % G;
         const TQ* src = static_cast<const TQ*>(p.q) + (ok ? (seq.q0 + tok) * p.q_stride + hd * kDh + ch : 0);
@@ -296,22 +301,28 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
         }
       }
 #pragma unroll
-      for (int j = 0; j < S::QP; ++j) s_q[j * S::KS * 32 + i] = make_uint4(w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j]);
+      for (int j = 0; j < S::QP; ++j) s_q[(mt * S::QP + j) * S::KS * 32 + i % (S::KS * 32)] = make_uint4(w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j]);
     }
-    // keys that this lane's two rows may see
-    int see[2];
+    // keys that this lane's rows (two a product) may see
+    int see[2 * kMt];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2 * kMt; ++r) {
       const int row = g + 8 * r;
       see[r] = row < rows ? visible_keys(seq, (row0 + row) / G, shape.cap) : 0;
     }
     const int see_all = visible_keys(seq, row0 / G, shape.cap);   // keys that every row may see
     __syncthreads();
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[S::NB][4];
+    float m[2 * kMt], l[2 * kMt], o[kMt][S::NB][4];
 #pragma unroll
-    for (int c = 0; c < S::NB; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+    for (int r = 0; r < 2 * kMt; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int c = 0; c < S::NB; ++c) o[mt][c][0] = o[mt][c][1] = o[mt][c][2] = o[mt][c][3] = 0.f;
 
     int st = 0;
     for (; s < s1; s += kWarps) {
@@ -326,42 +337,52 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
       if (gone >> (S::stages - 1) & 1u) continue;      // a bad page: its keys are left out
 
       // ---- scores
-      float sc[2][4];
+      float sc[kMt][2][4];
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb) {
         uint4 k[S::KV];
 #pragma unroll
         for (int v = 0; v < S::KV; ++v)
           k[v] = *reinterpret_cast<const uint4*>(kt + (8 * nb + g) * S::row_bytes + k_piece(8 * nb + g, 4 * v + t) * 16);
-        sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) sc[mt][nb][0] = sc[mt][nb][1] = sc[mt][nb][2] = sc[mt][nb][3] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < S::KS; ++ks) {
-          uint4 a[S::QP];
           uint32_t b[S::KP][2];
-#pragma unroll
-          for (int i = 0; i < S::QP; ++i) a[i] = s_q[(i * S::KS + ks) * 32 + lane];
           k_operand<S>(k, ks, b);
-          add_products<S::q32, S::QP, S::KP>(sc[nb], a, b);
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) {
+            uint4 a[S::QP];
+#pragma unroll
+            for (int i = 0; i < S::QP; ++i) a[i] = s_q[((mt * S::QP + i) * S::KS + ks) * 32 + lane];
+            add_products<S::q32, S::QP, S::KP>(sc[mt][nb], a, b);
+          }
         }
       }
       const bool masked = s * kStep + kStep > see_all;
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[nb][i] *= p.qscale;
-          if (masked && s * kStep + 8 * nb + 2 * t + (i & 1) >= see[i >> 1]) sc[nb][i] = -INFINITY;
-        }
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[mt][nb][i] *= p.qscale;
+            if (masked && s * kStep + 8 * nb + 2 * t + (i & 1) >= see[2 * mt + (i >> 1)]) sc[mt][nb][i] = -INFINITY;
+          }
 
       // ---- running reference: moved for the whole tile when some row passes the margin
+      auto largest = [&](int r) {
+        const float(&x)[2][4] = sc[r / 2];
+        const int i = 2 * (r & 1);
+        return fmaxf(fmaxf(x[0][i], x[0][i + 1]), fmaxf(x[1][i], x[1][i + 1]));
+      };
       bool move = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        move |= fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1])) > m[r] + kMoveLog2;
+      for (int r = 0; r < 2 * kMt; ++r) move |= largest(r) > m[r] + kMoveLog2;
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+        for (int r = 0; r < 2 * kMt; ++r) {
+          float mx = largest(r);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           mx = fmaxf(mx, m[r]);
@@ -370,21 +391,23 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
           l[r] *= corr;
 #pragma unroll
           for (int c = 0; c < S::NB; ++c) {
-            o[c][2 * r] *= corr;
-            o[c][2 * r + 1] *= corr;
+            o[r / 2][c][2 * (r & 1)] *= corr;
+            o[r / 2][c][2 * (r & 1) + 1] *= corr;
           }
         }
       }
-      uint4 pa[S::PP];
-      {
+      uint4 pa[kMt][S::PP];
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
         float pr[2][4];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float ref = m[i >> 1] == -INFINITY ? 0.f : m[i >> 1];   // nothing visible yet
-            pr[nb][i] = ex2(sc[nb][i] - ref);
-            l[i >> 1] += pr[nb][i];
+            const int r = 2 * mt + (i >> 1);
+            const float ref = m[r] == -INFINITY ? 0.f : m[r];             // nothing visible yet
+            pr[nb][i] = ex2(sc[mt][nb][i] - ref);
+            l[r] += pr[nb][i];
           }
         uint32_t w[4][S::PP];
         split_pair<S::PP>(pr[0][0], pr[0][1], w[0]);
@@ -392,7 +415,7 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
         split_pair<S::PP>(pr[1][0], pr[1][1], w[2]);
         split_pair<S::PP>(pr[1][2], pr[1][3], w[3]);
 #pragma unroll
-        for (int i = 0; i < S::PP; ++i) pa[i] = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+        for (int i = 0; i < S::PP; ++i) pa[mt][i] = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
       }
 
       // ---- values. A row's weight for a key it may not see is 0, but 0 * inf is not: if a
@@ -420,7 +443,8 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
         for (int c = 0; c < S::NB; ++c) {
           uint32_t b[S::KP][2];
           v_operand<S>(v, c, b);
-          add_products<S::q32, S::PP, S::KP>(o[c], pa, b);
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) add_products<S::q32, S::PP, S::KP>(o[mt][c], pa[mt], b);
         }
       } else {
         for (int tok = row0 / G; tok <= (row0 + rows - 1) / G; ++tok) {
@@ -435,11 +459,14 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
           for (int c = 0; c < S::NB; ++c) {
             uint32_t b[S::KP][2];
             v_operand<S>(vm, c, b);
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            add_products<false, S::PP, S::KP>(d, pa, b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((row0 + g + 8 * (i >> 1)) / G == tok) o[c][i] += d[i];
+            for (int mt = 0; mt < kMt; ++mt) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              add_products<false, S::PP, S::KP>(d, pa[mt], b);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((row0 + mt * kRows + g + 8 * (i >> 1)) / G == tok) o[mt][c][i] += d[i];
+            }
           }
         }
       }
@@ -449,27 +476,28 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
     cp_wait<0>();
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2 * kMt; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (t == 0) {
-        s_m[warp * kRows + g + 8 * r] = m[r];
-        s_l[warp * kRows + g + 8 * r] = l[r];
+        s_m[warp * kTile + g + 8 * r] = m[r];
+        s_l[warp * kTile + g + 8 * r] = l[r];
       }
     }
 #pragma unroll
-    for (int c = 0; c < S::NB; ++c)
+    for (int c = 0; c < kMt * S::NB; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = 2 * t + (i & 1);     // the block's column: which lanes' 16 bytes
-        const int ch = S::p32 ? 32 * (c / 4) + 4 * n + c % 4 : 64 * (c / 8) + 8 * n + c % 8;
-        s_o[(warp * kRows + g + 8 * (i >> 1)) * S::PE + ch] = o[c][i];
+        const int mt = c / S::NB, cc = c % S::NB;
+        const int ch = S::p32 ? 32 * (cc / 4) + 4 * n + cc % 4 : 64 * (cc / 8) + 8 * n + cc % 8;
+        s_o[(warp * kTile + mt * kRows + g + 8 * (i >> 1)) * S::PE + ch] = o[mt][cc][i];
       }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == cur.nc;
     const int owner0 = cur.first / range.per;              // blocks that hold a part of the item
     const int parts = (cur.first + cur.nc - 1) / range.per - owner0 + 1;
-    float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kRows * (kDh + 2);
+    float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * kTile * (kDh + 2);
 
     auto write_out = [&](int r, int ch, float4 v, float sum) {
       const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
@@ -487,14 +515,14 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
       const int r = i / (kDh / 4), ch = 4 * (i % (kDh / 4));
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kTile + r]);
       const float ref = M == -INFINITY ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_m[w * kRows + r] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * S::PE + ch);
-        sum += f * s_l[w * kRows + r];
+        const float f = ex2(s_m[w * kTile + r] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kTile + r) * S::PE + ch);
+        sum += f * s_l[w * kTile + r];
         acc.x += f * x.x;
         acc.y += f * x.y;
         acc.z += f * x.z;
@@ -505,29 +533,29 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
       } else {
         *reinterpret_cast<float4*>(slot + r * kDh + ch) = acc;
         if (ch == 0) {
-          slot[kRows * kDh + r] = M;
-          slot[kRows * (kDh + 1) + r] = sum;
+          slot[kTile * kDh + r] = M;
+          slot[kTile * (kDh + 1) + r] = sum;
         }
       }
     }
     if (!whole) {
       // ---- merge: groups of kGroup parts first, then the groups, each by its last arriver
       auto slot_of = [&](int k) {
-        return p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kRows * (kDh + 2);
+        return p.part + (2 * static_cast<size_t>(owner0 + k) + (k == 0 ? 1 : 0)) * kTile * (kDh + 2);
       };
       // Parts first, first + step, ... (n of them) into one state: the result, or part `first`.
       auto merge = [&](int first, int step, int n, bool final) {
-        for (int i = tid; i < n * kRows; i += kThreads) {
-          const float* sl = slot_of(first + i / kRows * step) + kRows * kDh;
-          const int r = i % kRows;
+        for (int i = tid; i < n * kTile; i += kThreads) {
+          const float* sl = slot_of(first + i / kTile * step) + kTile * kDh;
+          const int r = i % kTile;
           s_w[i] = r < rows ? __ldcg(sl + r) : -INFINITY;
-          s_w[kMaxParts * kRows + i] = r < rows ? __ldcg(sl + kRows + r) : 0.f;
+          s_w[kMaxParts * kTile + i] = r < rows ? __ldcg(sl + kTile + r) : 0.f;
         }
         __syncthreads();
         for (int i = tid; i < rows * (kDh / 4); i += kThreads) {
           const int r = i / (kDh / 4), ch = 4 * (i % (kDh / 4));
           float M = -INFINITY, sum = 0.f;
-          for (int k = 0; k < n; ++k) M = fmaxf(M, s_w[k * kRows + r]);
+          for (int k = 0; k < n; ++k) M = fmaxf(M, s_w[k * kTile + r]);
           const float ref = M == -INFINITY ? 0.f : M;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int k0 = 0; k0 < n; k0 += 8) {
@@ -538,8 +566,8 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               if (k0 + j >= n) break;
-              const float w = ex2(s_w[(k0 + j) * kRows + r] - ref);
-              sum = fmaf(w, s_w[(kMaxParts + k0 + j) * kRows + r], sum);
+              const float w = ex2(s_w[(k0 + j) * kTile + r] - ref);
+              sum = fmaf(w, s_w[(kMaxParts + k0 + j) * kTile + r], sum);
               acc.x = fmaf(w, x[j].x, acc.x);
               acc.y = fmaf(w, x[j].y, acc.y);
               acc.z = fmaf(w, x[j].z, acc.z);
@@ -552,8 +580,8 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
             float* to = slot_of(first);
             *reinterpret_cast<float4*>(to + r * kDh + ch) = acc;
             if (ch == 0) {
-              to[kRows * kDh + r] = M;
-              to[kRows * (kDh + 1) + r] = sum;
+              to[kTile * kDh + r] = M;
+              to[kTile * (kDh + 1) + r] = sum;
             }
           }
         }
@@ -584,18 +612,19 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide>::threads, Shape<TQ, 
   }
 }
 
-template <typename TQ, typename TP, int kDh, bool kWide>
+template <typename TQ, typename TP, int kDh, bool kWide, int kMt>
 cudaError_t launch_shape(const PagedAttnLaunch& a, RowsParams prm, const DeviceInfo& dev, cudaStream_t stream) {
-  using S = Shape<TQ, TP, kDh, kWide>;
+  using S = Shape<TQ, TP, kDh, kWide, kMt>;
   constexpr int smem = S::smem;
-  const auto kernel = paged_rows_kernel<TQ, TP, kDh, kWide>;
+  const auto kernel = paged_rows_kernel<TQ, TP, kDh, kWide, kMt>;
   static SmemOnce once;
   cudaError_t e = allow_smem(kernel, smem, dev.device, &once);
   if (e != cudaSuccess) return e;
   prm.shape.chunk_shift = S::chunk_shift;
+  prm.shape.rows = S::rows;
   cudaLaunchConfig_t cfg = {};
   int grid = dev.num_sms * S::blocks;
-  if (grid > kMaxBlocks) grid = kMaxBlocks;
+  if (grid > kMaxBlocks / kMt) grid = kMaxBlocks / kMt;      // the workspace's rows
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(S::threads);
   cfg.dynamicSmemBytes = smem;
@@ -610,14 +639,22 @@ cudaError_t launch_shape(const PagedAttnLaunch& a, RowsParams prm, const DeviceI
   return e;
 }
 
-// One wide block an SM for few items (K/V heads of sequences), several narrow ones for
-// many: MEASURED
+// One wide block an SM where there are fewer items (K/V heads of sequences) than SMs, several
+// narrow ones otherwise. One item over 262144 keys of 4 heads: wide 59 us, narrow 62; 320 items
+// (16 sequences, 20 heads, fp32): narrow 39 us, wide 54.
 template <typename TQ, typename TP, int kDh>
 cudaError_t launch(const PagedAttnLaunch& a, const RowsParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  // fp32 queries, more than 16 rows: tiles of 32 share what it costs to read and split K and V
+  // (512 tokens over 2048 keys of 20 heads: 99 us against 118 with tiles of 16, 63 against 67
+  // with a bf16 pool). Not at 512-byte rows, where the registers do not hold them (323 us
+  // against 274).
+  if constexpr (sizeof(TQ) == 4 && kDh * sizeof(TP) <= 256)
+    if (static_cast<long long>(a.max_new) * prm.shape.G > kRows)
+      return launch_shape<TQ, TP, kDh, false, 2>(a, prm, dev, stream);
   const long long tiles = a.batch.B + static_cast<long long>(a.batch.n_tokens) * prm.shape.G / kRows;   // at most, a head
-  if constexpr (Shape<TQ, TP, kDh, true>::warps != Shape<TQ, TP, kDh, false>::warps)
-    if (tiles * a.layer.Hkv < kWideItems * dev.num_sms) return launch_shape<TQ, TP, kDh, true>(a, prm, dev, stream);
-  return launch_shape<TQ, TP, kDh, false>(a, prm, dev, stream);
+  if constexpr (Shape<TQ, TP, kDh, true, 1>::warps != Shape<TQ, TP, kDh, false, 1>::warps)
+    if (tiles * a.layer.Hkv < kWideItems * dev.num_sms) return launch_shape<TQ, TP, kDh, true, 1>(a, prm, dev, stream);
+  return launch_shape<TQ, TP, kDh, false, 1>(a, prm, dev, stream);
 }
 
 template <int kDh>
@@ -653,7 +690,6 @@ cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const Devi
   prm.batch = a.batch;
   prm.layer = a.layer;
   prm.shape.G = a.Hq / a.layer.Hkv;
-  prm.shape.rows = kRows;
   prm.shape.coarse = false;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = 0;
