@@ -150,6 +150,11 @@ __device__ __forceinline__ bool pair_or(int pair, bool v) {
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // a * b + c and a + b on pairs.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < XB; ++b)
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
-            mx[(e / 2) & 3] = fmaxf(mx[(e / 2) & 3], fmaxf(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])));
+            mx[(e / 2) & 3] = max3(mx[(e / 2) & 3], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
         const bool pv = j == 0 || mbar_test_wait(bar(kPvDone + t), (j - 1) & 1);
         // the references of 32 rows move together, to the largest score so far
@@ -547,6 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = fma2(v, qs2, ref2);
             v.x = ex2(v.x);
             v.y = ex2(v.y);
+            x[b][2 * e] = __float_as_uint(v.x);
+            x[b][2 * e + 1] = __float_as_uint(v.y);
+          }
+        // (apart: in one loop each sum and conversion stands behind its own exponential)
+#pragma unroll
+        for (int b = 0; b < XB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 v = make_float2(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1]));
             sum[e & 1] = add2(sum[e & 1], v);
             x[0][16 * b + e] = pack_bf16(v.x, v.y);     // behind what is still to be read
           }
@@ -599,9 +613,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = i + plain; i < e; ++i) {
           wait_warp(kSFull + t, j & 1);
           tc_fence_after();
-          if (__builtin_expect(*const_cast<volatile uint32_t*>(&sm->bad[i & 7]) != 0, 0)) break;
-          uint32_t x[XB][32];
-          load_scores(x);
+          const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[i & 7]);
+          uint32_t x[XB][32];        // (load_scores, with the look at `bad` under its latency)
+#pragma unroll
+          for (int b = 0; b < XB; ++b) tmem_ld_32x32b_x32(my_s + 32 * b, x[b]);
+          tmem_ld_wait();
+          if (__builtin_expect(bad != 0, 0)) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kSFree + t));
           softmax(x);
           give_p();
           ++j;
