@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Shape<TQ, TP, kDh, kWide, kMt>::threads, Shape
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
-  if (!work_locate<kThreads, true>(bt, shape, Hkv, &s_work, &range, &cur)) return;
+  if (!work_locate<kThreads, true>(bt, shape, Hkv, &s_work, &range, &cur, p.status)) return;
 
   for (;;) {
     // ---- the part of the item in this block's range

@@ -100,10 +100,11 @@ struct WorkScratch {
 // Number the chunks and find this block's range and the item it starts in. Called by all
 // kThreads threads of the block; returns false if the block has nothing to do. With
 // kMayCoarsen, w becomes coarse where a block would have less than four steps: a merge costs
-// as much as some eight of them.
+// as much as some eight of them. With a status word, sequences whose keys pass their row of
+// the table are reported there, whichever kernel they are of.
 template <int kThreads, bool kMayCoarsen>
 __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
-                            WorkCursor* cur) {
+                            WorkCursor* cur, unsigned int* status = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kW = kThreads / 32;
   // each thread counts a run of sequences, in fine chunks and in coarse ones
@@ -114,6 +115,7 @@ __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScr
   for (int b = b0; b < b1; ++b) {
     const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
     const int m = work_rows(s, w);
+    if (status != nullptr && s.n > 0 && s.kv > w.cap) atomicOr(status, kStatusBadPage);
 #pragma unroll 1
     for (int rt = 0; rt * w.rows < m; ++rt) {
       const int n = tile_steps(s, w, rt);

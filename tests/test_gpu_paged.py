@@ -464,6 +464,21 @@ def test_pages_outside_the_pool_are_left_out_and_reported():
                 assert torch.equal(bt.cache.Kp, K0) and torch.equal(bt.cache.Vp, V0)
 
 
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("n", [1, 40])
+def test_keys_behind_the_table_s_row_are_left_out_and_reported(act, pool, n):
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    bt = Batch([n], [160], 16, 4, 2, 64, act, pool, extra_cols=0).fill()
+    bt.close(bt.attend(), one_bf16=n > 1)
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    bt.d["kv_len"] = torch.tensor([160 + n], dtype=torch.int32).cuda()      # no token sees less than 160
+    got = bt.attend()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    one = Batch([1] * n, [160] * n, 16, 4, 2, 64, act, pool)
+    one.q, one.K, one.V = bt.q, [bt.K[0]] * n, [bt.V[0]] * n
+    one.close(got, one_bf16=n > 1)
+
+
 def test_offsets_past_32_bits():
     """A pool of more than 2^32 elements, its sequences at both ends of it."""
     page, Hkv, dh = 256, 8, 64
