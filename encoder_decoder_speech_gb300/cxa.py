@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 from . import _build
 
@@ -603,6 +604,24 @@ def _stream_on(index, stream):
     return _stream(stream)
 
 
+def _capturing(index, stream, raw):
+    """Whether the call's stream (handle raw, of device index) is being captured."""
+    import torch
+    if stream is None and torch.cuda.current_device() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=index)):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _new(q, stream, index):
+    """An empty tensor like q for the result of a call on `stream`, in that stream's memory."""
+    if stream is None:
+        return q.new_empty(q.shape)
+    import torch
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=index)):
+        return q.new_empty(q.shape)
+
+
 _LAYOUTS = {"half": CXA_ROTARY_HALF, "interleaved": CXA_ROTARY_INTERLEAVED}
 _SCALINGS = {"none": CXA_ROTARY_PLAIN, "linear": CXA_ROTARY_LINEAR, "ntk": CXA_ROTARY_NTK,
              "wavelength": CXA_ROTARY_WAVELENGTH}
@@ -658,7 +677,7 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
         raise ValueError("the tensors must be on a CUDA device")
     _ints("pos", pos, (n,), at)
     if q_out is None:
-        q_out = q.new_empty((n, Hq, dh))
+        q_out = _new(q, stream, at)
     qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
     Hk = ks = kos = 0
     kp = kop = None
@@ -666,7 +685,7 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
         Hk = k.shape[1] if k.dim() == 3 else 0
         ks = _rows("k", k, Hk, dh, n, dt, at)
         if k_out is None:
-            k_out = k.new_empty((n, Hk, dh))
+            k_out = _new(k, stream, at)
         kos = _rows("k_out", k_out, Hk, dh, n, dt, at)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     else:
@@ -718,17 +737,14 @@ class PagedCache:
             if len(self._ws_bytes) > 4096:
                 self._ws_bytes.clear()
             n = self._ws_bytes[Hq, max_new] = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
-        key = _stream_on(self._at, stream)
+        raw = _stream_on(self._at, stream)
+        key = (raw, threading.get_ident()) if raw == 2 else raw     # 2: each thread's own default stream
         ws = self._ws.get(key)
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = _capturing(self._at, stream, raw)
         if ws is not None and ws.numel() >= n and not capturing:
             return ws
-        with torch.cuda.device(self._at):
-            if stream is None or key == torch.cuda.current_stream().cuda_stream:
-                ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
-            else:
-                with torch.cuda.stream(torch.cuda.ExternalStream(key)):
-                    ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self._at)):
+            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
         if not capturing:
             self._ws[key] = ws
         return ws
@@ -748,7 +764,7 @@ class PagedCache:
             Hq = q.shape[1] if q.dim() == 3 else 0
             qs = _rows("q", q, Hq, dh, n, dt, at)
             if q_out is None:
-                q_out = q.new_empty((n, Hq, dh))
+                q_out = _new(q, stream, at)
             qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
             qp, qop = q.data_ptr(), q_out.data_ptr()
         norm, eps = _norm(norm_eps)
@@ -763,14 +779,15 @@ class PagedCache:
     def attend(self, layer: int, q, q_start, kv_len, page_table, max_new: int, out=None, scale: float = 0.0,
                workspace=None, stream=None):
         """Attention of the new tokens' queries q [N, Hq, dh] over their sequences' keys up to
-        each token's own. max_new: an upper bound of the new tokens of one sequence. Returns
-        out [N, Hq, dh] (rows behind the batch's last token are left as they are)."""
+        each token's own. max_new: an upper bound of the new tokens of one sequence; workspace:
+        a zeroed tensor to use instead of the cache's own. Returns out [N, Hq, dh] (rows behind
+        the batch's last token are left as they are)."""
         at, dh, dt = self._at, self.dh, q.dtype
         B, width = self._batch(q_start, kv_len, page_table)
         qs = _rows("q", q, None, dh, None, None, at)
         n, Hq, _ = q.shape
         if out is None:
-            out = q.new_empty((n, Hq, dh))
+            out = _new(q, stream, at)
         os_ = _rows("out", out, Hq, dh, n, dt, at)
         ws = workspace if workspace is not None else self.workspace(Hq, max_new, stream)
         if ws.get_device() != at or not ws.is_contiguous():

@@ -327,6 +327,11 @@ def test_attention(act, pool, dh, i):
 
 
 @pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,kv,Hq,Hkv", [([1], [70001], 2, 1), ([24], [40003], 1, 1), ([200, 1], [30001, 9000], 2, 1),
+                                         ([3, 1], [70, 50], 100, 1), ([9, 1, 70], [90, 20, 75], 130, 1),
+                                         ([1] * 700, [1 + b % 40 for b in range(700)], 2, 1)])
+@pytest.mark.parametrize("act,pool", TYPES)
 @pytest.mark.parametrize("n,kv", [([1, 1], [20, 470]), ([7, 5], [40, 470]), ([150, 90], [150, 470])])
 def test_rows_behind_the_last_key_may_hold_anything(act, pool, n, kv):
     for rest in (math.nan, math.inf, -math.inf):
@@ -589,6 +594,42 @@ def test_two_streams_at_once():
         outs.append(a.cache.attend(0, q, **a.d, max_new=1, stream=streams[r % 3].cuda_stream, out=out))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_results_on_another_stream_have_memory_of_that_stream():
+    """Memory that the current stream still has work for is not handed to a call on another."""
+    a = Batch([1] * 2, [300, 200], 16, 8, 2, 64, "bf16", "bf16").fill()
+    want, q, s = a.attend(), a.q.cuda(), torch.cuda.Stream()
+    pos = torch.arange(2, dtype=torch.int32).cuda()
+    turned, _ = cxa.qk_norm_rope(q, None, pos, rotary=cxa.Rotary(64))
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: a.cache.attend(0, q, **a.d, max_new=1, stream=s), want),
+                      (lambda: cxa.qk_norm_rope(q, None, pos, rotary=cxa.Rotary(64), stream=s)[0], turned)):
+        call()                                   # (kernels and workspace are there)
+        torch.cuda.synchronize()
+        old = [torch.empty_like(q) for _ in range(64)]
+        torch.cuda._sleep(20_000_000)
+        for x in old:
+            x.fill_(7.0)
+        del old, x
+        got = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+
+
+def test_workspaces_are_kept_apart():
+    a = Batch([1], [40], 16, 2, 2, 64, "bf16", "bf16").fill()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    kept = [a.cache.workspace(2, 1, stream=x).data_ptr() for x in (None, s, t)]
+    assert len(set(kept)) == 3
+    assert kept == [a.cache.workspace(2, 1, stream=x).data_ptr() for x in (None, s, t)]
+    torch.cuda.synchronize()
+    # the stream that is captured is the one the call names, whichever is current
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+        with torch.cuda.stream(t):
+            assert a.cache.workspace(2, 1, stream=s).data_ptr() not in kept
+        assert a.cache.workspace(2, 1).data_ptr() not in kept
+    assert kept[1] == a.cache.workspace(2, 1, stream=s).data_ptr()
 
 
 def test_two_graphs_at_once():
