@@ -331,6 +331,15 @@ def test_attention(act, pool, dh, i):
 @pytest.mark.parametrize("n,kv,Hq,Hkv", [([1], [70001], 2, 1), ([24], [40003], 1, 1), ([200, 1], [30001, 9000], 2, 1),
                                          ([3, 1], [70, 50], 100, 1), ([9, 1, 70], [90, 20, 75], 130, 1),
                                          ([1] * 700, [1 + b % 40 for b in range(700)], 2, 1)])
+def test_long_merges_many_heads_and_many_sequences(act, pool, dh, n, kv, Hq, Hkv):
+    """One K/V head cut into more parts than are merged at once; more query heads on a K/V head
+    than a tile has rows; more sequences than a block has threads."""
+    bt = Batch(n, kv, 16 if len(n) > 10 else 256, Hq, Hkv, dh, act, pool).fill()
+    got = bt.attend()
+    bt.close(got)
+    assert torch.equal(bt.attend(), got)
+
+
 @pytest.mark.parametrize("act,pool", TYPES)
 @pytest.mark.parametrize("n,kv", [([1, 1], [20, 470]), ([7, 5], [40, 470]), ([150, 90], [150, 470])])
 def test_rows_behind_the_last_key_may_hold_anything(act, pool, n, kv):
