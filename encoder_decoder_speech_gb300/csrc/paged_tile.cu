@@ -274,7 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Launched behind paged_rows_kernel of the same call, which lets this grid start only
   // after it has waited for everything before it; the two touch different rows and
-  // scratch. This grid waits for that one at its end.
+  // scratch. This grid waits for that one at its end. Starting without a wait of its own, it
+  // drops what its SM's L1 may hold from before the batch was written.
+  __threadfence();
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
