@@ -7,27 +7,36 @@
 // one K/V head), dealt out by paged_work.cuh in chunks of 16 KB of K and of V (128 keys of
 // 64 channels, 64 keys of 128). One block runs on an SM and works on both tiles of its item,
 // which share each K and V tile read (a block a tile, two blocks an SM, read twice as much:
-// 417 us against 345 us for 2048 tokens over 32768 keys of 20 heads, its K and V coming 11
-// times from DRAM); one tile's products run under the other's exponentials:
+// 418 us against 401 us, where the change was made, for 2048 tokens over 32768 keys of 20
+// heads, its K and V coming 11 times from DRAM); one tile's products run under the other's
+// exponentials:
 //
-//  * warp 10 streams by TMA: the item's Q (a box of 128 / G tokens x G heads a tile, which
+//  * warp 18 streams by TMA: the item's Q (a box of 128 / G tokens x G heads a tile, which
 //    lands token by token, the row order of a tile), and K and V page by page into rings of
 //    five tiles each; the boxes of a chunk are issued by a lane each. A K tile comes back as
 //    soon as both tiles' scores are done, a V tile after both P.V.
-//  * warps 8 and 9 issue the products of a tile each: scores of chunk i + 1 once the softmax
-//    warps have read those of chunk i, then P.V of chunk i. P is read from tensor memory, V
-//    as it lies in shared memory (rows of keys: an MN-major operand).
-//  * warps 0..3 and 4..7 own a row a thread, so that row maxima and sums need no exchange.
-//    They take a row's scores into registers at once, which lets the next chunk's scores
-//    start while the exponentials run. A row's reference m moves, and O is rescaled, only
-//    when a score passes it by more than 2^8 (decided per warp).
+//  * warps 16 and 17 issue the products of a tile each: scores of chunk i + 1 once the
+//    softmax warps have read those of chunk i, then P.V of chunk i. P is read from tensor
+//    memory, V as it lies in shared memory (rows of keys: an MN-major operand).
+//  * warps 0..7 and 8..15 do the softmax of a tile each, two threads a row: a warp has 32 rows
+//    and one half of a chunk's keys, its partner the other half (one thread a row: 352 us
+//    against 345, the mixed batch below 197 against 180). They take their scores into
+//    registers at once, which lets the next chunk's scores start while the exponentials run.
+//    A row's reference m moves, and O is rescaled, only when a score passes it by more than
+//    2^8 (decided for the 32 rows of two partners together, so that the common chunk costs
+//    them one barrier and no exchange); the sums of the halves meet at an item's end.
 //
 // A tile whose last token sees fewer keys than its neighbour's leaves the item's last chunks
 // out (its softmax warps then hand the K and V tiles back).
 //
-// Bound, at 64 channels, by the exponentials and their bookkeeping together with the
-// products (about 500 clocks each a tile of 128 keys). Tensor memory: S, P and O side by
-// side in 256 columns a tile.
+// Measured: 2048 tokens over 32768 keys of 20 heads of 64 channels 318 us, 1045 TFLOP/s, with
+// 128 channels 505 us, 1320 TFLOP/s. Bound by the chain of a tile's steps, some 2250 clocks a
+// chunk of 128 keys for the two tiles: scores, read, exponentials (1024 clocks of the SM's
+// units for the two tiles), conversion, P.V (the products of both: 1045 clocks), each handing
+// over through a barrier (some 250 clocks there and back). Tensor pipe 45 %, exponentials
+// 45 %, issue 62 % busy. A barrier order that sends the tiles in turns, and a start of one half
+// a chunk behind the other, gained nothing. Tensor memory: S, P and O side by side in 256
+// columns a tile.
 //
 // P is rounded to one bf16 value (2^-9 of each weight, against the 2^-8 of the bf16
 // output); sums, references and O are fp32, the sums of the values before rounding.

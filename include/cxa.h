@@ -438,7 +438,8 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  * positions up to the token's own (which are in the pool: append first).
  *
  *   max_new    an upper bound of the new tokens of any one sequence. It chooses
- *              kernels and the workspace size; results do not depend on it being tight.
+ *              kernels and the workspace size; a loose one costs time at most (results
+ *              may then differ by their rounding).
  *   q, out     [n_tokens][Hq][dh] of dtype; their spans, first row to last, must not
  *              overlap.
  *   scale      a value <= 0 selects 1/sqrt(dh).
@@ -450,7 +451,8 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  * page_size / 64 + 1) must be below 2^31 (CXA_EINVAL otherwise).
  * Values that no key position of a row makes visible never reach it: rows of a page
  * behind the last key, and later tokens' rows, may hold infinities or NaN. A row that
- * sees no key is zero. Results do not change from call to call.
+ * sees no key is zero. A row that sees an infinity or a NaN in q, K or V may be
+ * NaN throughout. Results do not change from call to call.
  */
 CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new,
                                 const int* q_start, const int* kv_len, const int* page_table, int max_pages,
@@ -548,7 +550,8 @@ CXA_API unsigned long long cxa_launch_count(void);
  * kernel then skipped its remaining work), or CXA_EPAGE when a paged call met a
  * page number outside its pool. Synchronises the device. clear != 0
  * resets the word. Returns CXA_ECUDA if the word cannot be read. After a
- * timeout, the decode workspace's counters must be zeroed again before reuse.
+ * timeout, the counters of a decode or paged attention workspace must be zeroed
+ * again before reuse.
  */
 CXA_API int cxa_device_status(int clear);
 
