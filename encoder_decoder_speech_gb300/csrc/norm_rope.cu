@@ -12,7 +12,7 @@
 //
 // Bound by memory: every value is read once and written once. What stands between is kept
 // short, or the instructions bind (with 175 of them for 16 bytes a lane: 83 us for 24,000
-// tokens of 40 heads, against 47 us now): a lane holds two groups of four channels of a
+// tokens of 40 heads, against 45 us now): a lane holds two groups of four channels of a
 // head that are each other's partners (the half layout) or hold their partners themselves
 // (interleaved), so that no value is fetched from another lane, and works on pairs
 // (fma.f32x2). A warp takes one token, with the loads of kBatch heads under way before the
@@ -29,13 +29,16 @@
 namespace cxa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kBatch = 4;         // heads' loads under way in a lane
-// Blocks an SM that the registers are cut to. Measured, bf16 (24,000 tokens of 40 heads, and
-// 16,391 tokens appended): 4 blocks 46.9 and 71.2 us, 3 blocks 52.8 and 73.9; fp32 (5,333
-// tokens of 10 heads), whose loads hold twice the registers: 3 blocks 6.3 us, 4 blocks 12.1.
-template <typename TA>
-constexpr int kBlocksPerSm = sizeof(TA) == 2 ? 4 : 3;
+// Blocks an SM that the registers are cut to: the append's threads hold more, fp32 loads twice
+// the registers. Measured, in us: bf16 without the append (24,000 tokens of 40 heads) 8 blocks
+// 45.6, 7 blocks 47.5, 9 blocks 51.3; with it (16,391 tokens) 7 blocks 67.9, 8 blocks 69.7, 9
+// blocks 76.7; fp32 without (5,333 tokens of 10 heads) 6 blocks 6.1, 5 blocks 6.7, 7 blocks
+// 8.1; with it (1,237 tokens of 6 heads) 5 blocks 3.9, 6 blocks 4.6, 7 blocks 4.9. Half as many
+// blocks of 8 warps: 46.9, 71.1, 6.4 and 4.6.
+template <typename TA, bool kAppend>
+constexpr int kBlocksPerSm = (sizeof(TA) == 2 ? 8 : 6) - (kAppend ? 1 : 0);
 
 struct NrParams {
   const void *q, *k, *v;
@@ -124,7 +127,7 @@ __device__ __forceinline__ int find_seq(const int* q_start, int B, int t, int la
 enum Mode { kPartners = 0, kInside = 1, kAnywhere = 2 };
 
 template <typename TA, typename TP, int kDh, bool kAppend, int kMode>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<TA>) norm_rope_kernel(const __grid_constant__ NrParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<TA, kAppend>) norm_rope_kernel(const __grid_constant__ NrParams p) {
   using Raw = typename Quad<TA>::Raw;
   constexpr int LPH = kDh / 8;             // lanes a head
   constexpr int HPI = 32 / LPH;            // heads a warp reads at once
