@@ -336,6 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
+    auto wait_both = [&](int i, uint32_t pi, int k, uint32_t pk) {   // for two barriers, as wait_warp
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar(i), pi) && mbar_test_wait(bar(k), pk))) return ok;
+      wait(i, pi);
+      wait(k, pk);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
     const int n_chunks = range.g1 - range.g0;
 
     if (warp == kTmaWarp) {
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // carry them over from a lane's registers one by one.
       constexpr uint32_t idesc_s = make_idesc(1u, kTileRows, T::chunk);
       constexpr uint32_t idesc_o = make_idesc(1u, kTileRows, 64) | (1u << 16);   // V MN-major
-      const int t = warp - kMmaWarp;
+      const int t = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;
       const uint32_t my = __shfl_sync(0xffffffffu, tmem + t * kTmemTile, 0);
       constexpr uint64_t k_hi = desc_high(1024), mn_hi = desc_high(1024);
       // the scores' cursor: chunk i of the range, chunk c of the item, j of the tile's own
@@ -444,12 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qb = item % T::q_bufs, st = i % kStages;
         if (fresh && !wait_warp(kQFull + qb, (item / T::q_bufs) & 1)) return;
         fresh = false;
-        if (!wait_warp(kKFull + st, (i / kStages) & 1)) return;
-        if (j > 0 && !wait_warp(kSFree + t, (j - 1) & 1)) return;
+        // (a barrier that nothing has completed yet passes for the phase before its first)
+        if (!wait_both(kKFull + st, (i / kStages) & 1, kSFree + t, (j & 1) ^ 1)) return;
         tc_fence_after();
-        const uint32_t ql = __shfl_sync(0xffffffffu, desc_low(q_tile(qb, t), 16), 0);
-        const uint32_t kl = __shfl_sync(0xffffffffu, desc_low(k_base + st * kTileBytes, 16), 0);
-        const uint32_t k_empty = __shfl_sync(0xffffffffu, bar(kKEmpty + st), 0);
+        const int at = __shfl_sync(0xffffffffu, st | qb << 8, 0), k_at = at & 255;
+        const uint32_t ql = desc_low(q_tile(at >> 8, t), 16), kl = desc_low(k_base + k_at * kTileBytes, 16);
+        const uint32_t k_empty = bar(kKEmpty + k_at);
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < T::halves; ++h)
@@ -475,12 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++c;
           scores();
         }
-        if (!ok || !wait_warp(kVFull + st, round & 1) || !wait_warp(kPFull + t, pj & 1)) break;
+        if (!ok || !wait_both(kVFull + st, round & 1, kPFull + t, pj & 1)) break;
         tc_fence_after();
         const uint32_t acc0 = !starts || sm->acc[t] != 0 ? 1u : 0u;
-        const uint32_t vl = __shfl_sync(0xffffffffu, desc_low(v_base + st * kTileBytes, 1024), 0);
-        const uint32_t v_empty = __shfl_sync(0xffffffffu, bar(kVEmpty + st), 0);
-        const uint32_t acc = __shfl_sync(0xffffffffu, acc0, 0);
+        const uint32_t at = __shfl_sync(0xffffffffu, st | acc0 << 8, 0), acc = at >> 8;
+        const uint32_t vl = desc_low(v_base + (at & 255) * kTileBytes, 1024), v_empty = bar(kVEmpty + (at & 255));
         if (elect_one()) {
 #pragma unroll
           for (int kb = 0; kb < T::chunk / 16; ++kb)     // 16 keys: 2048 bytes
