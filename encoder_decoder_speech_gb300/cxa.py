@@ -545,80 +545,101 @@ class CrossAttentionCache:
 
 # ---------------------------------------------------------------- paged self-attention
 # A decoding step makes these calls once a layer, with kernels of a few microseconds: their
-# checks are written to cost little.
-def _rows(name, t, heads=None, dh=None, tokens=None, dtype=None, index=None):
-    """Check a packed [tokens, heads, dh] tensor; returns its row stride."""
-    if t.dim() != 3:
+# checks are written to cost little (together with the call, 8 us of the host's time).
+class _TorchCalls:
+    """torch's types and its shortest ways to the current device, stream and capture state."""
+
+    def __init__(self):
+        import torch
+        c = torch._C
+        self.torch, self.i32, self.f32 = torch, torch.int32, torch.float32
+        self.code = {torch.float32: CXA_F32, torch.bfloat16: CXA_BF16}
+        self.device = getattr(c, "_cuda_getDevice", torch.cuda.current_device)
+        self.stream = getattr(c, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self.capturing = getattr(c, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+_torch_calls = None
+
+
+def _calls():
+    global _torch_calls
+    if _torch_calls is None:
+        _torch_calls = _TorchCalls()
+    return _torch_calls
+
+
+def _rows(name, t, H, dh, n, dtype, index):
+    """Check a packed [n tokens, H heads, dh] tensor; returns its row stride."""
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head dim]")
-    n, H, d = t.shape
+    if shape != (n, H, dh):
+        raise ValueError(f"{name} is {tuple(shape)}, expected {(n, H, dh)}")
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d != 1) or (s1 != d and H > 1):
+    if s2 != 1 or (s1 != dh and H > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if n > 1:
-        if s0 < H * d:
-            raise ValueError(f"{name}: the rows of different tokens must not overlap")
-    else:
-        s0 = H * d
-    if (tokens is not None and n != tokens) or (heads is not None and H != heads) or (dh is not None and d != dh):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(tokens, heads, dh)}")
-    if dtype is not None and t.dtype != dtype:
+    if n <= 1:
+        s0 = H * dh
+    elif s0 < H * dh:
+        raise ValueError(f"{name}: the rows of different tokens must not overlap")
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if index is not None and t.get_device() != index:
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     return s0
 
 
-def _ints(name, t, shape, index):
-    import torch
-    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+def _heads(name, t):
+    """The tokens and heads of a packed tensor."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head dim]")
+    return shape[0], shape[1]
+
+
+def _ints(name, t, shape, index, i32):
+    if t.dtype is not i32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on cuda:{index}")
 
 
-def _weight(name, t, dh, index):
-    import torch
-    if t.dtype != torch.float32 or t.shape != (dh,) or t.get_device() != index or not t.is_contiguous():
+def _weight(name, t, dh, index, f32):
+    if t.dtype is not f32 or t.shape != (dh,) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({dh},) on cuda:{index}")
     return t.data_ptr()
 
 
-def _on_device(index, call, *args, where):
+def _code(tc, dtype):
+    code = tc.code.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; expected float32 or bfloat16")
+    return code
+
+
+def _run(tc, index, where, call, args):
     """call(*args) with the device current that the tensors are on; raises on a non-zero status."""
-    import torch
-    if index < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    if torch.cuda.current_device() == index:
+    if tc.device() == index:
         rc = call(*args)
     else:
-        with torch.cuda.device(index):
+        with tc.torch.cuda.device(index):
             rc = call(*args)
     if rc != CXA_OK:
         raise CxaError(rc, where)
 
 
-def _stream_on(index, stream):
-    """The handle of `stream`, or of the current stream of device `index`."""
-    if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
-    return _stream(stream)
-
-
-def _capturing(index, stream, raw):
+def _capturing(tc, index, stream, raw):
     """Whether the call's stream (handle raw, of device index) is being captured."""
-    import torch
-    if stream is None and torch.cuda.current_device() == index:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=index)):
-        return torch.cuda.is_current_stream_capturing()
+    if stream is None and tc.device() == index:
+        return tc.capturing()
+    with tc.torch.cuda.stream(tc.torch.cuda.ExternalStream(raw, device=index)):
+        return tc.capturing()
 
 
-def _new(q, stream, index):
+def _new(tc, q, stream, index):
     """An empty tensor like q for the result of a call on `stream`, in that stream's memory."""
     if stream is None:
         return q.new_empty(q.shape)
-    import torch
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=index)):
+    with tc.torch.cuda.stream(tc.torch.cuda.ExternalStream(_stream(stream), device=index)):
         return q.new_empty(q.shape)
 
 
@@ -661,41 +682,39 @@ class Rotary:
             pass
 
 
-def _norm(norm_eps):
-    return (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
-
-
 def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None = None, q_weight=None, k_weight=None,
                  q_out=None, k_out=None, stream=None):
     """Head norms (RMS, if norm_eps is given) and rotation of q [N, Hq, dh] and k [N, Hk, dh]
     (or None), float32 or bfloat16, at positions pos [N] int32. Token rows may be strided
     slices; q_out and k_out may be q and k. Returns (q_out, k_out)."""
-    qs = _rows("q", q)
-    n, Hq, dh = q.shape
-    dt, at = q.dtype, q.get_device()
+    tc = _torch_calls or _calls()
+    n, Hq = _heads("q", q)
+    dh, dt, at = q.shape[2], q.dtype, q.get_device()
     if at < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    _ints("pos", pos, (n,), at)
+    qs = _rows("q", q, Hq, dh, n, dt, at)
+    _ints("pos", pos, (n,), at, tc.i32)
     if q_out is None:
-        q_out = _new(q, stream, at)
+        q_out = _new(tc, q, stream, at)
     qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
     Hk = ks = kos = 0
     kp = kop = None
     if k is not None:
-        Hk = k.shape[1] if k.dim() == 3 else 0
+        Hk = _heads("k", k)[1]
         ks = _rows("k", k, Hk, dh, n, dt, at)
         if k_out is None:
-            k_out = _new(k, stream, at)
+            k_out = _new(tc, k, stream, at)
         kos = _rows("k_out", k_out, Hk, dh, n, dt, at)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     else:
         k_out = None
-    norm, eps = _norm(norm_eps)
-    _on_device(at, load().cxa_qk_norm_rope, q.data_ptr(), qs, Hq, kp, ks, Hk, dh, n, pos.data_ptr(), norm, eps,
-               None if q_weight is None else _weight("q_weight", q_weight, dh, at),
-               None if k_weight is None else _weight("k_weight", k_weight, dh, at),
-               None if rotary is None else rotary.handle, q_out.data_ptr(), qos, kop, kos, _dtype_code(dt),
-               _stream_on(at, stream), where="cxa_qk_norm_rope")
+    norm, eps = (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
+    _run(tc, at, "cxa_qk_norm_rope", load().cxa_qk_norm_rope, (
+        q.data_ptr(), qs, Hq, kp, ks, Hk, dh, n, pos.data_ptr(), norm, eps,
+        None if q_weight is None else _weight("q_weight", q_weight, dh, at, tc.f32),
+        None if k_weight is None else _weight("k_weight", k_weight, dh, at, tc.f32),
+        None if rotary is None else rotary.handle, q_out.data_ptr(), qos, kop, kos, _code(tc, dt),
+        tc.stream(at) if stream is None else _stream(stream)))
     return q_out, k_out
 
 
@@ -719,61 +738,72 @@ class PagedCache:
         rc, self.handle = cxa_pages_create(self.Kp, self.Vp, num_pages, page_size, L, Hkv, dh, _DTYPES[cache_dtype])
         check(rc, "cxa_pages_create")
 
-    def _batch(self, q_start, kv_len, page_table):
-        if page_table.dim() != 2:
+    def _batch(self, q_start, kv_len, page_table, i32):
+        shape, at = page_table.shape, self._at
+        if at < 0:
+            raise ValueError("the tensors must be on a CUDA device")
+        if len(shape) != 2:
             raise ValueError("page_table must be [sequences, pages]")
-        B, width = page_table.shape
-        _ints("q_start", q_start, (B + 1,), self._at)
-        _ints("kv_len", kv_len, (B,), self._at)
-        _ints("page_table", page_table, (B, width), self._at)
-        return B, width
+        B = shape[0]
+        _ints("q_start", q_start, (B + 1,), at, i32)
+        _ints("kv_len", kv_len, (B,), at, i32)
+        _ints("page_table", page_table, shape, at, i32)
+        return B, shape[1]
+
+    def _scratch(self, tc, Hq, max_new, stream, raw):
+        """The workspace of a call on the stream with handle raw: the tensor, its address and bytes."""
+        need = self._ws_bytes.get((Hq, max_new))
+        if need is None:
+            if len(self._ws_bytes) > 4096:
+                self._ws_bytes.clear()
+            need = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
+            self._ws_bytes[Hq, max_new] = need
+        key = (raw, threading.get_ident()) if raw == 2 else raw     # 2: each thread's own default stream
+        kept = self._ws.get(key)
+        capturing = _capturing(tc, self._at, stream, raw)
+        if kept is not None and kept[2] >= need and not capturing:
+            return kept
+        torch = tc.torch
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self._at)):
+            ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.Kp.device)
+        new = (ws, ws.data_ptr(), ws.numel())
+        if not capturing:
+            self._ws[key] = new
+        return new
 
     def workspace(self, Hq: int, max_new: int, stream=None):
         """A zeroed attention workspace, kept per stream. While a graph is captured it is a
         new one (cleared in the graph), as replays may run beside anything else."""
-        import torch
-        n = self._ws_bytes.get((Hq, max_new))
-        if n is None:
-            if len(self._ws_bytes) > 4096:
-                self._ws_bytes.clear()
-            n = self._ws_bytes[Hq, max_new] = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
-        raw = _stream_on(self._at, stream)
-        key = (raw, threading.get_ident()) if raw == 2 else raw     # 2: each thread's own default stream
-        ws = self._ws.get(key)
-        capturing = _capturing(self._at, stream, raw)
-        if ws is not None and ws.numel() >= n and not capturing:
-            return ws
-        with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self._at)):
-            ws = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.Kp.device)
-        if not capturing:
-            self._ws[key] = ws
-        return ws
+        tc = _calls()
+        return self._scratch(tc, Hq, max_new, stream, tc.stream(self._at) if stream is None else _stream(stream))[0]
 
     def append(self, layer: int, k, v, q_start, kv_len, page_table, q=None, q_out=None, rotary: Rotary | None = None,
                norm_eps: float | None = None, q_weight=None, k_weight=None, stream=None):
         """Write k, v [N, Hkv, dh] of the new tokens into their pages, k normalised (RMS, if
         norm_eps is given) and rotated; with q [N, Hq, dh] also return q_out, the queries
         normalised and rotated (rows behind the batch's last token are left as they are)."""
-        at, dh, dt, n = self._at, self.dh, k.dtype, k.shape[0]
-        B, width = self._batch(q_start, kv_len, page_table)
+        tc = _torch_calls or _calls()
+        at, dh, dt, n = self._at, self.dh, k.dtype, _heads("k", k)[0]
+        B, width = self._batch(q_start, kv_len, page_table, tc.i32)
         ks = _rows("k", k, self.Hkv, dh, n, dt, at)
         vs = _rows("v", v, self.Hkv, dh, n, dt, at)
         Hq = qs = qos = 0
         qp = qop = None
         if q is not None:
-            Hq = q.shape[1] if q.dim() == 3 else 0
+            Hq = _heads("q", q)[1]
             qs = _rows("q", q, Hq, dh, n, dt, at)
             if q_out is None:
-                q_out = _new(q, stream, at)
+                q_out = _new(tc, q, stream, at)
             qos = _rows("q_out", q_out, Hq, dh, n, dt, at)
             qp, qop = q.data_ptr(), q_out.data_ptr()
-        norm, eps = _norm(norm_eps)
-        _on_device(at, load().cxa_paged_append, self.handle, layer, B, n, q_start.data_ptr(), kv_len.data_ptr(),
-                   page_table.data_ptr(), width, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, qop, qos, norm, eps,
-                   None if q_weight is None else _weight("q_weight", q_weight, dh, at),
-                   None if k_weight is None else _weight("k_weight", k_weight, dh, at),
-                   None if rotary is None else rotary.handle, _dtype_code(dt), _stream_on(at, stream),
-                   where="cxa_paged_append")
+        norm, eps = (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
+        _run(tc, at, "cxa_paged_append", load().cxa_paged_append, (
+            self.handle, layer, B, n, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
+            k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, qop, qos, norm, eps,
+            None if q_weight is None else _weight("q_weight", q_weight, dh, at, tc.f32),
+            None if k_weight is None else _weight("k_weight", k_weight, dh, at, tc.f32),
+            None if rotary is None else rotary.handle, _code(tc, dt),
+            tc.stream(at) if stream is None else _stream(stream)))
         return q_out if q is not None else None
 
     def attend(self, layer: int, q, q_start, kv_len, page_table, max_new: int, out=None, scale: float = 0.0,
@@ -782,20 +812,24 @@ class PagedCache:
         each token's own. max_new: an upper bound of the new tokens of one sequence; workspace:
         a zeroed tensor to use instead of the cache's own. Returns out [N, Hq, dh] (rows behind
         the batch's last token are left as they are)."""
+        tc = _torch_calls or _calls()
         at, dh, dt = self._at, self.dh, q.dtype
-        B, width = self._batch(q_start, kv_len, page_table)
-        qs = _rows("q", q, None, dh, None, None, at)
-        n, Hq, _ = q.shape
+        B, width = self._batch(q_start, kv_len, page_table, tc.i32)
+        n, Hq = _heads("q", q)
+        qs = _rows("q", q, Hq, dh, n, dt, at)
         if out is None:
-            out = _new(q, stream, at)
+            out = _new(tc, q, stream, at)
         os_ = _rows("out", out, Hq, dh, n, dt, at)
-        ws = workspace if workspace is not None else self.workspace(Hq, max_new, stream)
-        if ws.get_device() != at or not ws.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
-        _on_device(at, load().cxa_paged_attention, self.handle, layer, B, n, max_new, q_start.data_ptr(),
-                   kv_len.data_ptr(), page_table.data_ptr(), width, q.data_ptr(), qs, Hq, out.data_ptr(), os_, scale,
-                   _dtype_code(dt), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(at, stream),
-                   where="cxa_paged_attention")
+        raw = tc.stream(at) if stream is None else _stream(stream)
+        if workspace is None:
+            ws = self._scratch(tc, Hq, max_new, stream, raw)
+        else:
+            if workspace.get_device() != at or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
+            ws = workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _run(tc, at, "cxa_paged_attention", load().cxa_paged_attention, (
+            self.handle, layer, B, n, max_new, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
+            q.data_ptr(), qs, Hq, out.data_ptr(), os_, scale, _code(tc, dt), ws[1], ws[2], raw))
         return out
 
     def check(self, q_start, kv_len, page_table, n_tokens: int) -> None:
