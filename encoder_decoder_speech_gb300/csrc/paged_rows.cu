@@ -7,12 +7,12 @@
 // in one pass with the running reference m_r. Bound by memory: K and V are read once for
 // the 16 query rows of a tile (query heads of one K/V head times new tokens; 32 in fp32
 // chunks). 64 single tokens over 4400 keys of 8 heads of 128 channels, 4 query heads each:
-// 181 us, 6.5 TB/s; one token over 262144 keys of 4 heads of 64: 57 us, of which some 18 are
-// start, merge and imbalance; 5 fp32 tokens in each of 16 sequences: 39 us, 3.4 TB/s, where
-// a block's two items of 8 us each pay start and merge for themselves.
+// 181 us, 6.5 TB/s; one token over 262144 keys of 4 heads of 64: 56 us, of which some 16 are
+// start, merge and imbalance; 5 fp32 tokens in each of 16 sequences: 38 us, 3.6 TB/s, in 64
+// sequences 133 us, 4.3 TB/s: two warps a scheduler wait for each other's products.
 //
 // A warp takes 16 keys a step, which it streams into a ring of its own in shared memory
-// (cp.async, kStages steps; no barrier but the warp's), and multiplies on the tensor cores
+// (cp.async, two or three steps; no barrier but the warp's), and multiplies on the tensor cores
 // with m16n8k16 products. A product does not care which channel carries which index as long
 // as both operands agree, so operands are read 16 bytes a lane: lane (g, t) of the K operand
 // takes 16 consecutive bytes of key g, the query operand being laid out to match, and for
@@ -42,7 +42,9 @@ namespace {
 constexpr int kRows = 16;            // query rows of a product
 constexpr int kStep = 16;            // keys a warp takes at a time
 constexpr int kMaxBlocks = 160 * 4;
-constexpr int kGroup = 16;           // parts of an item that are merged at once, and then of those
+// Parts of an item that are merged at once, and then of those. One token over 262144 keys: 8 at a
+// time 55.7 us, 6 55.7, 10 56.5, 16 57.1.
+constexpr int kGroup = 8;
 constexpr int kMaxParts = (kMaxBlocks + kGroup - 1) / kGroup;
 constexpr int kWideItems = 1;        // items an SM below which wide blocks run (see launch)
 constexpr float kMoveLog2 = 8.f;     // a row's reference moves only past this margin
@@ -110,8 +112,10 @@ struct Shape {
   static constexpr int PE = kDh + 4;               // floats of a row in the block's merge
   static constexpr int half_bytes = kStep * row_bytes;     // K or V of a step
   // One block of many warps an SM (kWide), or several of four; a chunk is a step of each
-  // warp. The rings hold three steps a warp, and as many warps run as that leaves room for.
-  static constexpr int stages = 3;
+  // warp. The rings hold three steps a warp, and as many warps run as that leaves room for; two
+  // of the 8 KB steps of fp32 rows of 64 channels do (5 tokens in each of 16 sequences: 37.6 us,
+  // three steps 38.5; two steps and half as many warps again, whose registers spill: 40.3).
+  static constexpr int stages = p32 && kDh == 64 && kMt == 1 ? 2 : 3;
   static constexpr int warps_sm = kMt > 1 && row_bytes <= 128 ? 8 : 2048 / row_bytes;
   static constexpr int warps = kWide ? warps_sm : 4, blocks = warps_sm / warps, threads = warps * 32;
   static constexpr int chunk_shift = warps == 16 ? 8 : warps == 8 ? 7 : 6;
