@@ -115,15 +115,20 @@ cudaError_t allow_smem(K kernel, int bytes, int device, SmemOnce* once) {
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // Attention, one kernel or two: sequences of up to kFewRows query rows a K/V head go to
-// paged_rows.cu, the others, where paged_tile_takes(), to paged_tile.cu (with the part of
-// the workspace behind the first kernel's); the first kernel takes all of them otherwise.
+// paged_rows.cu, the others, where paged_tile_takes(), to paged_tile.cu; the first kernel
+// takes all of them otherwise.
 constexpr int kFewRows = 16;
-size_t paged_rows_workspace_bytes(int dh);
+// The workspace: both kernels' arrival counters, at places that no argument moves (so that calls
+// of different shapes may share it), then the partial states of the first and of the second.
+constexpr int kRowsMaxBlocks = 160 * 4, kTileMaxBlocks = 160;
+constexpr size_t kRowsCounters = kRowsMaxBlocks * 3, kTileCounters = kTileMaxBlocks * 2 * 3;
+constexpr size_t kPagedCounterBytes = (kRowsCounters + kTileCounters) * 4;
+static_assert(kPagedCounterBytes % 256 == 0, "the partial states behind the counters are aligned");
+size_t paged_rows_part_bytes(int dh);
 bool paged_rows_countable(const PagedAttnLaunch& a);   // whether the call's work can be numbered in 31 bits
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream);
 bool paged_tile_takes(int G, bool act_bf16, int max_new);
-size_t paged_tile_workspace_bytes(int dh);
-cudaError_t launch_paged_tile(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
-                              std::string* msg);
+size_t paged_tile_part_bytes(int dh);
+cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
 
 }  // namespace cxa

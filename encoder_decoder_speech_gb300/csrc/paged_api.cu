@@ -377,8 +377,8 @@ int cxa_paged_append(const cxa_pages* pages, int layer, int B, int n_tokens, con
 
 size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int max_new) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (dh != 64 && dh != 128) || max_new < 1) return 0;
-  size_t n = cxa::paged_rows_workspace_bytes(dh);
-  if (cxa::paged_tile_takes(Hq / Hkv, true, max_new)) n += cxa::paged_tile_workspace_bytes(dh);
+  size_t n = cxa::kPagedCounterBytes + cxa::paged_rows_part_bytes(dh);
+  if (cxa::paged_tile_takes(Hq / Hkv, true, max_new)) n += cxa::paged_tile_part_bytes(dh);
   return n;
 }
 
@@ -433,9 +433,7 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
     e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);
-    if (e == cudaSuccess && tiles)
-      e = cxa::launch_paged_tile(a, static_cast<uint8_t*>(workspace) + cxa::paged_rows_workspace_bytes(pages->dh), dev,
-                                 s, &msg);
+    if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, dev, s, &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + (msg.empty() ? "launch" : msg));
     return CXA_OK;
   });

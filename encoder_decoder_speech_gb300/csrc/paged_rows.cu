@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kRows = 16;            // query rows of a product
 constexpr int kStep = 16;            // keys a warp takes at a time
-constexpr int kMaxBlocks = 160 * 4;
+constexpr int kMaxBlocks = kRowsMaxBlocks;
 // Parts of an item that are merged at once, and then of those. One token over 262144 keys: 8 at a
 // time 55.7 us, 6 55.7, 10 56.5, 16 57.1.
 constexpr int kGroup = 8;
@@ -668,14 +668,9 @@ cudaError_t launch_dh(const PagedAttnLaunch& a, const RowsParams& prm, const Dev
   return a.pool_bf16 ? launch<float, bf, kDh>(a, prm, dev, stream) : launch<float, float, kDh>(a, prm, dev, stream);
 }
 
-constexpr size_t kCounterBytes = (kMaxBlocks * 3 * 4 + 255) / 256 * 256;
-
 }  // namespace
 
-size_t paged_rows_workspace_bytes(int dh) {
-  const size_t n = kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4;
-  return (n + 255) / 256 * 256;
-}
+size_t paged_rows_part_bytes(int dh) { return static_cast<size_t>(2 * kMaxBlocks) * kRows * (dh + 2) * 4; }
 
 bool paged_rows_countable(const PagedAttnLaunch& a) {
   return work_bound(a.batch, a.layer.page_shift, a.layer.Hkv, a.Hq / a.layer.Hkv, kRows, 6) < 1LL << 31;
@@ -689,7 +684,7 @@ cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const Devi
   prm.o_stride = a.o_stride;
   prm.qscale = a.scale * 1.4426950408889634f;
   prm.counters = static_cast<unsigned int*>(a.workspace);
-  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kCounterBytes);
+  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kPagedCounterBytes);
   prm.status = dev.status_word;
   prm.batch = a.batch;
   prm.layer = a.layer;

@@ -66,7 +66,7 @@ constexpr int kTileRows = 128;
 constexpr int kTileBytes = 16384;            // K or V of a chunk
 constexpr int kStages = 5;                   // of K and of V
 constexpr int kQBytes = 65536;               // the Q tiles of two items of 64 channels, of one of 128
-constexpr int kMaxBlocks = 160;
+constexpr int kMaxBlocks = kTileMaxBlocks;
 constexpr uint32_t kTmemTile = 256;          // columns of a tile
 constexpr float kMoveLog2 = 8.f;
 constexpr int kGroup = 8;                    // parts of an item that are merged at once, and then of those
@@ -953,18 +953,18 @@ bool encode(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuu
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kCounterBytes = (kMaxBlocks * kTiles * 3 * 4 + 255) / 256 * 256;
+static_assert(kTileCounters == kMaxBlocks * kTiles * 3, "three counters a tile of a block");
 
 template <int kDh>
-cudaError_t launch(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
-                   std::string* msg) {
+cudaError_t launch(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
   using T = Tile<kDh>;
   TileParams prm;
   prm.out = a.out;
   prm.o_stride = a.o_stride;
   prm.qscale = a.scale * 1.4426950408889634f;
-  prm.counters = static_cast<unsigned int*>(workspace);
-  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
+  prm.counters = static_cast<unsigned int*>(a.workspace) + kRowsCounters;
+  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kPagedCounterBytes +
+                                      paged_rows_part_bytes(kDh));
   prm.status = dev.status_word;
   prm.batch = a.batch;
   prm.num_pages = a.layer.num_pages;
@@ -1019,13 +1019,12 @@ bool paged_tile_takes(int G, bool act_bf16, int max_new) {
   return act_bf16 && G <= kTileRows && static_cast<long long>(max_new) * G > kFewRows;
 }
 
-size_t paged_tile_workspace_bytes(int dh) {
-  return kCounterBytes + static_cast<size_t>(2 * kMaxBlocks) * kTiles * kTileRows * (dh + 2) * 4;
+size_t paged_tile_part_bytes(int dh) {
+  return static_cast<size_t>(2 * kMaxBlocks) * kTiles * kTileRows * (dh + 2) * 4;
 }
 
-cudaError_t launch_paged_tile(const PagedAttnLaunch& a, void* workspace, const DeviceInfo& dev, cudaStream_t stream,
-                              std::string* msg) {
-  return a.dh == 64 ? launch<64>(a, workspace, dev, stream, msg) : launch<128>(a, workspace, dev, stream, msg);
+cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
+  return a.dh == 64 ? launch<64>(a, dev, stream, msg) : launch<128>(a, dev, stream, msg);
 }
 
 }  // namespace cxa

@@ -445,8 +445,9 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  *   scale      a value <= 0 selects 1/sqrt(dh).
  *   workspace  at least cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new) bytes,
  *              256-byte aligned, zero before the first call on a new buffer
- *              (cudaMemset); calls leave its counters zero. Calls that share a
- *              workspace must be ordered on one stream.
+ *              (cudaMemset); calls leave its counters zero, so that calls of any
+ *              shapes may use it in turn. Calls that share a workspace must be
+ *              ordered on one stream.
  * Work is counted in 31 bits: Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages *
  * page_size / 64 + 1) must be below 2^31 (CXA_EINVAL otherwise).
  * Values that no key position of a row makes visible never reach it: rows of a page

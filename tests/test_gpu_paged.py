@@ -641,6 +641,18 @@ def test_workspaces_are_kept_apart():
     assert kept[1] == a.cache.workspace(2, 1, stream=s).data_ptr()
 
 
+def test_one_workspace_for_calls_of_all_shapes():
+    cases = [Batch([200, 1], [3000, 9000], 64, 4, 1, dh, act, act, seed=dh).fill()
+             for dh in (64, 128) for act in ("bf16", "f32")]
+    cases.append(Batch([1], [60000], 64, 40, 1, 64, "bf16", "bf16").fill())
+    want = [bt.attend() for bt in cases]
+    n = max(cxa.cxa_paged_attention_workspace_bytes(bt.Hq, bt.Hkv, bt.dh, bt.max_new) for bt in cases)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for bt, ref in zip(cases, want):
+            assert torch.equal(bt.attend(workspace=ws), ref)
+
+
 def test_two_graphs_at_once():
     a = Batch([1] * 8, [4000 - 100 * b for b in range(8)], 64, 8, 2, 64, "bf16", "bf16", seed=1).fill()
     want, q = a.attend(), a.q.cuda()
