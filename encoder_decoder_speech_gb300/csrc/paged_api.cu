@@ -14,6 +14,8 @@
 #include "internal.h"
 #include "paged.cuh"
 
+static_assert(cxa::kPagedCounterBytes == CXA_PAGED_COUNTER_BYTES, "what a caller has to clear");
+
 struct cxa_rotary {
   cxa::RotaryArg arg;
 };

@@ -108,6 +108,8 @@ CXA_MAX_SHARED_QUERIES = 16
 
 # bytes of the fixed device scratch behind cxa_decode_noalloc (CXA_NOALLOC_SCRATCH_BYTES)
 CXA_NOALLOC_SCRATCH_BYTES = 8 << 20
+# bytes at the start of a cxa_paged_attention workspace to clear before its first use
+CXA_PAGED_COUNTER_BYTES = 11520
 
 _lib = None
 
@@ -765,15 +767,16 @@ class PagedCache:
             return kept
         torch = tc.torch
         with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self._at)):
-            ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.Kp.device)
+            ws = torch.empty(max(need, CXA_PAGED_COUNTER_BYTES), dtype=torch.uint8, device=self.Kp.device)
+            ws[:CXA_PAGED_COUNTER_BYTES].zero_()
         new = (ws, ws.data_ptr(), ws.numel())
         if not capturing:
             self._ws[key] = new
         return new
 
     def workspace(self, Hq: int, max_new: int, stream=None):
-        """A zeroed attention workspace, kept per stream. While a graph is captured it is a
-        new one (cleared in the graph), as replays may run beside anything else."""
+        """An attention workspace (its counters zeroed), kept per stream. While a graph is captured
+        it is a new one (cleared in the graph), as replays may run beside anything else."""
         tc = _calls()
         return self._scratch(tc, Hq, max_new, stream, tc.stream(self._at) if stream is None else _stream(stream))[0]
 
@@ -810,7 +813,7 @@ class PagedCache:
                workspace=None, stream=None):
         """Attention of the new tokens' queries q [N, Hq, dh] over their sequences' keys up to
         each token's own. max_new: an upper bound of the new tokens of one sequence; workspace:
-        a zeroed tensor to use instead of the cache's own. Returns out [N, Hq, dh] (rows behind
+        a tensor, its counters zeroed, to use instead of the cache's own. Returns out [N, Hq, dh] (rows behind
         the batch's last token are left as they are)."""
         tc = _torch_calls or _calls()
         at, dh, dt = self._at, self.dh, q.dtype

@@ -430,7 +430,9 @@ CXA_API int cxa_paged_append(const cxa_pages* pages, int layer, int B, int n_tok
                              const float* q_weight, const float* k_weight, const cxa_rotary* rot, int dtype,
                              void* stream);
 
-/* Bytes of device workspace of cxa_paged_attention; 0 for unsupported arguments. */
+/* Bytes of device workspace of cxa_paged_attention; 0 for unsupported arguments. Its first
+ * CXA_PAGED_COUNTER_BYTES are counters, which must be zero before a buffer's first call. */
+#define CXA_PAGED_COUNTER_BYTES 11520
 CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int max_new);
 
 /*
@@ -444,9 +446,9 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  *              overlap.
  *   scale      a value <= 0 selects 1/sqrt(dh).
  *   workspace  at least cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new) bytes,
- *              256-byte aligned, zero before the first call on a new buffer
- *              (cudaMemset); calls leave its counters zero, so that calls of any
- *              shapes may use it in turn. Calls that share a workspace must be
+ *              256-byte aligned, its first CXA_PAGED_COUNTER_BYTES zero before the
+ *              first call on a new buffer (cudaMemset); calls leave them zero, so that
+ *              calls of any shapes may use it in turn. Calls that share a workspace must be
  *              ordered on one stream.
  * Work is counted in 31 bits: Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages *
  * page_size / 64 + 1) must be below 2^31 (CXA_EINVAL otherwise).

@@ -647,7 +647,8 @@ def test_one_workspace_for_calls_of_all_shapes():
     cases.append(Batch([1], [60000], 64, 40, 1, 64, "bf16", "bf16").fill())
     want = [bt.attend() for bt in cases]
     n = max(cxa.cxa_paged_attention_workspace_bytes(bt.Hq, bt.Hkv, bt.dh, bt.max_new) for bt in cases)
-    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")       # only the counters need be zero
+    ws[:cxa.CXA_PAGED_COUNTER_BYTES] = 0
     for _ in range(2):
         for bt, ref in zip(cases, want):
             assert torch.equal(bt.attend(workspace=ws), ref)
