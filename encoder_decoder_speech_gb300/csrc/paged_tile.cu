@@ -38,8 +38,9 @@
 // a chunk behind the other, gained nothing. Tensor memory: S, P and O side by side in 256
 // columns a tile.
 //
-// P is rounded to one bf16 value (2^-9 of each weight, against the 2^-8 of the bf16
-// output); sums, references and O are fp32, the sums of the values before rounding.
+// P is rounded to one bf16 value (an error of up to 2^-8 of each weight, of either sign, as
+// the bf16 output has itself: 2.3e-3 of a result in all, against 1.7e-3 with exact weights);
+// sums, references and O are fp32, the sums of the values before rounding.
 //
 // Keys behind an item's last visible one weigh 0 and their V rows, which may hold anything,
 // are zeroed in shared memory before P.V. Keys that some rows see and others do not weigh

@@ -210,3 +210,17 @@ def test_batch_check_finds_what_the_kernels_would_leave_out(pages):
     assert chk(page_table=[9, 4, -1, 9, 0, 7]) == cxa.CXA_OK           # a shared prefix page
     assert chk(q_start=[0, 0, 4], page_table=[-1, -1, -1, 9, 0, 7]) == cxa.CXA_OK   # nothing new: not looked at
     assert cxa.cxa_strerror(cxa.CXA_EPAGE).startswith("CXA_EPAGE")
+
+
+def test_workspace_holds_its_counters_and_a_part_for_each_kernel():
+    import pathlib
+    import re
+    header = (pathlib.Path(__file__).parents[1] / "include" / "cxa.h").read_text()
+    assert int(re.search(r"#define CXA_PAGED_COUNTER_BYTES (\d+)", header)[1]) == cxa.CXA_PAGED_COUNTER_BYTES
+    few = cxa.cxa_paged_attention_workspace_bytes(8, 8, 64, 16)
+    many = cxa.cxa_paged_attention_workspace_bytes(8, 8, 64, 17)
+    assert cxa.CXA_PAGED_COUNTER_BYTES < few < many
+    assert many == cxa.cxa_paged_attention_workspace_bytes(16, 8, 64, 9)
+    assert many < cxa.cxa_paged_attention_workspace_bytes(8, 8, 128, 17)
+    for bad in ((0, 1, 64, 1), (8, 3, 64, 1), (8, 8, 32, 1), (8, 8, 64, 0)):
+        assert cxa.cxa_paged_attention_workspace_bytes(*bad) == 0
