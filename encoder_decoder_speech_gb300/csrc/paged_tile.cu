@@ -23,8 +23,9 @@
 //    against 345, the mixed batch below 197 against 180). They take their scores into
 //    registers at once, which lets the next chunk's scores start while the exponentials run.
 //    A row's reference m moves, and O is rescaled, only when a score passes it by more than
-//    2^8 (decided for the 32 rows of two partners together, so that the common chunk costs
-//    them one barrier and no exchange); the sums of the halves meet at an item's end.
+//    2^8 (decided for the sequence's rows among the 32 of two partners together, so that the
+//    common chunk costs them one barrier and no exchange); the sums of the halves meet at an
+//    item's end.
 //
 // A tile whose last token sees fewer keys than its neighbour's leaves the item's last chunks
 // out (its softmax warps then hand the K and V tiles back).
@@ -618,7 +619,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (fresh) {
           fresh = false;
           nc = chunks_of(at, t);
-          m = -INFINITY;
+          // A row that is no token's of the sequence (it holds padding, the next sequence's
+          // tokens, or what no copy has filled) starts with a reference that no score passes:
+          // it has no say in when the references of its 32 rows move.
+          m = r < rows_of(at, t) ? -INFINITY : INFINITY;
           l = 0.f;
           c0 = c;
           if (r == 0 && hf == 0) sm->acc[t] = 0;

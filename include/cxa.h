@@ -304,7 +304,8 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
  * The batch, common to the calls below. The new tokens of all sequences are packed:
  *   B          sequences, >= 1.
  *   n_tokens   rows of the packed tensors (at least the batch's new tokens: rows from
- *              q_start[B] on are padding, neither read nor written).
+ *              q_start[B] on are padding: not written, and what they hold changes no
+ *              bit of the others).
  *   q_start    device int32 [B + 1]: sequence b owns rows q_start[b] .. q_start[b+1]
  *              (none, if equal); q_start[0] = 0, not decreasing.
  *   kv_len     device int32 [B]: keys of each sequence, its new tokens included; its

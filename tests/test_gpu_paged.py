@@ -700,3 +700,26 @@ def test_python_refusals():
     f32 = cxa.PagedCache(4, 16, 1, 2, 64, "f32")
     with pytest.raises(cxa.CxaError):
         f32.attend(0, q, **bt.d, max_new=2)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("G", [3, 4, 5, 7])
+@pytest.mark.parametrize("n", [17, 60, 200])
+def test_query_rows_of_no_token_change_no_bit(dh, G, n):
+    """A 128-row tile also holds rows that are no token's of its sequence: padding behind the
+    last sequence, the next sequence's tokens, and (G no divisor of 128) rows that no copy fills."""
+    bt = Batch([n, 19], [n + 80000, 30000], 256, G, 1, dh, "bf16", "bf16", pad=50)
+    for x in bt.K:          # scores that grow from chunk to chunk: rows with large q move their reference again and again
+        x.mul_((1 + torch.arange(len(x)) // 64 % 16 / 2)[:, None, None])
+    bt.q.mul_(0.25)
+    bt.fill()
+    filler = Batch([400], [400], 64, 4, 1, dh, "bf16", "bf16").fill()
+    want = bt.attend()
+    for i, scale in enumerate((0.0, 8.0, 60.0, math.inf, math.nan)):
+        filler.attend(filler.q * (scale if scale < 1e3 else 1e4))      # what shared memory holds from before
+        rest = randn(50, G, dh, seed=90 + i, dtype=torch.bfloat16)
+        q = bt.q.clone()
+        q[n + 19:] = rest * scale
+        assert torch.equal(bt.attend(q)[:n + 19], want[:n + 19])
+        q[n:n + 19] = rest[:19] * scale                                # the next sequence's
+        assert torch.equal(bt.attend(q)[:n], want[:n])
