@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <exception>
+#include <mutex>
 #include <new>
 #include <string>
 #include <vector>
@@ -120,6 +121,15 @@ cxa::RotaryArg rotary_arg(const cxa_rotary* rot) {
   cxa::RotaryArg none = {};
   none.factor = 1.f;
   return none;
+}
+
+// A call's two kernels are enqueued with nothing of another thread's call on the same stream
+// between them: the second starts without waiting for anything but the first (paged_tile.cu),
+// so the scratch it uses must not be under the second kernel of another call. One lock for the
+// streams whose handles fall together.
+std::mutex& stream_lock(cudaStream_t s) {
+  static std::mutex locks[61];
+  return locks[reinterpret_cast<uintptr_t>(s) / 16 % 61];
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -434,6 +444,8 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
+    std::unique_lock<std::mutex> together;
+    if (tiles) together = std::unique_lock<std::mutex>(stream_lock(s));
     e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);
     if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, dev, s, &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + (msg.empty() ? "launch" : msg));

@@ -327,8 +327,10 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
  * aligned and of one type `dtype`: CXA_F32 (pool CXA_F32 or CXA_BF16) or CXA_BF16 (pool
  * CXA_BF16). Calls with n_tokens == 0 enqueue nothing.
  *
- * Every kernel of these calls waits for all earlier work of its stream before it reads
- * anything, and lets the next kernel be launched early only after that.
+ * No kernel of these calls reads or writes anything before all earlier work of its stream
+ * is done: each waits for it (the second kernel of an attention call starts beside the first,
+ * which has waited), and lets the next kernel be launched early only after that. Calls of
+ * several threads on one stream are each enqueued whole.
  */
 
 /*

@@ -14,6 +14,7 @@ fp32 2^-24).
   (fp32 sums and the parts left out).
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -723,3 +724,49 @@ def test_query_rows_of_no_token_change_no_bit(dh, G, n):
         assert torch.equal(bt.attend(q)[:n + 19], want[:n + 19])
         q[n:n + 19] = rest[:19] * scale                                # the next sequence's
         assert torch.equal(bt.attend(q)[:n], want[:n])
+
+
+def test_threads_share_a_stream_and_its_workspace():
+    """Calls of two kernels, enqueued by threads at once on one stream: each is enqueued whole,
+    so that the second kernels, which start early, never work on one another's scratch."""
+    bts = [Batch([150, 1, 30], [20000, 900, 70], 64, 4, 1, dh, "bf16", "bf16", seed=s).fill() for s, dh in ((1, 64), (2, 128))]
+    n = max(cxa.cxa_paged_attention_workspace_bytes(4, 1, bt.dh, bt.max_new) for bt in bts)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    want = [bt.attend() for bt in bts]
+    outs = [[torch.zeros_like(w) for _ in range(40)] for w in want]
+    qs = [bt.q.cuda() for bt in bts]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls(i):
+        for out in outs[i]:
+            bts[i].cache.attend(0, qs[i], **bts[i].d, max_new=bts[i].max_new, out=out, workspace=ws, stream=stream)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in outs[i])
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_reads_what_the_grid_before_has_just_written(dh):
+    """Append (which lets the next grid start early) and attention behind it, again and again over
+    the same pages and queries: every call sees the rows of its own append, through copies too."""
+    n, past, Hkv = 96, 700, 2
+    bt = Batch([n], [past + n], 64, 4, Hkv, dh, "bf16", "bf16").fill()
+    steps = []
+    for i in range(12):
+        k, v, q = (randn(n, h, dh, seed=10 * i + h + 40, dtype=torch.bfloat16).cuda() for h in (Hkv, Hkv, 4))
+        steps.append((k, v, q, torch.zeros(n, 4, dh, dtype=torch.bfloat16, device="cuda")))
+    qr = torch.empty_like(steps[0][2])
+    torch.cuda.synchronize()
+    for k, v, q, out in steps:
+        bt.cache.append(0, k, v, **bt.d, q=q, q_out=qr)
+        bt.cache.attend(0, qr, **bt.d, max_new=n, out=out)
+    torch.cuda.synchronize()
+    for k, v, q, out in steps:
+        bt.K[0][past:], bt.V[0][past:], bt.q = k.cpu(), v.cpu(), q.cpu()
+        bt.close(out)
