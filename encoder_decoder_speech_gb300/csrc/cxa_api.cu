@@ -75,6 +75,16 @@ cudaError_t current_device_info(DeviceInfo* info, std::string* msg) {
     *msg = "cudaGetDevice";
     return e;
   }
+  // A thread's first call: make the device's context current in it. Launches would do that, but
+  // tensor maps are encoded by the driver before a call's first launch, and need it.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) {
+      *msg = "cudaSetDevice";
+      return e;
+    }
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < 128 && have[dev]) {
     *info = cache[dev];
