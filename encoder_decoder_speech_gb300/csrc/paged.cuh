@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <string>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -129,6 +130,12 @@ bool paged_rows_countable(const PagedAttnLaunch& a);   // whether the call's wor
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream);
 bool paged_tile_takes(int G, bool act_bf16, int max_new);
 size_t paged_tile_part_bytes(int dh);
-cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
+// The tensor maps of q and of the layer's pages, made before anything of the call is enqueued.
+struct PagedTileMaps {
+  CUtensorMap q, k, v;
+};
+cudaError_t prepare_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, PagedTileMaps* maps, std::string* msg);
+cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const PagedTileMaps& maps, const DeviceInfo& dev,
+                              cudaStream_t stream);
 
 }  // namespace cxa

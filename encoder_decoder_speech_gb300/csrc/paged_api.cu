@@ -55,13 +55,17 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool valid_dtype(int t) { return t == CXA_F32 || t == CXA_BF16; }
 int elt(int t) { return t == CXA_BF16 ? 2 : 4; }
 
-// A packed tensor of rows: one token's heads contiguous, tokens `stride` elements apart.
-int check_rows(const std::string& w, const char* name, const void* p, long long stride, int H, int dh, int dtype) {
+// A packed tensor of rows: one token's heads contiguous, tokens `stride` elements apart. A
+// tensor map's strides are below 2^40 bytes, whichever kernel a call goes to.
+int check_rows(const std::string& w, const char* name, const void* p, long long stride, int rows, int H, int dh,
+               int dtype) {
   if (p == nullptr) return fail(CXA_EINVAL, w + ": " + name + " is NULL");
   if (!aligned(p, 16)) return fail(CXA_EINVAL, w + ": " + name + " must be 16-byte aligned");
-  if (stride < static_cast<long long>(H) * dh || stride > (1LL << 40) || stride * elt(dtype) % 16 != 0)
+  if (stride < static_cast<long long>(H) * dh || stride >= (1LL << 40) / elt(dtype) || stride * elt(dtype) % 16 != 0)
     return fail(CXA_EINVAL, w + ": the row stride of " + name +
-                                " must hold its heads and be a multiple of 16 bytes");
+                                " must hold its heads, be a multiple of 16 bytes and below 2^40 bytes");
+  if (static_cast<double>(rows) * static_cast<double>(stride) * elt(dtype) > 72057594037927936.0)
+    return fail(CXA_EINVAL, w + ": the rows of " + name + " span more than 2^56 bytes");
   return CXA_OK;
 }
 
@@ -222,10 +226,10 @@ int cxa_qk_norm_rope(const void* q, long long q_stride, int Hq, const void* k, l
     if (rc != CXA_OK) return rc;
     if (n_tokens == 0) return CXA_OK;
     if (pos == nullptr || !aligned(pos, 4)) return fail(CXA_EINVAL, w + ": pos is NULL or misaligned");
-    if (Hq > 0) rc = check_rows(w, "q", q, q_stride, Hq, dh, dtype);
-    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q_out", q_out, qo_stride, Hq, dh, dtype);
-    if (rc == CXA_OK && Hk > 0) rc = check_rows(w, "k", k, k_stride, Hk, dh, dtype);
-    if (rc == CXA_OK && Hk > 0) rc = check_rows(w, "k_out", k_out, ko_stride, Hk, dh, dtype);
+    if (Hq > 0) rc = check_rows(w, "q", q, q_stride, n_tokens, Hq, dh, dtype);
+    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q_out", q_out, qo_stride, n_tokens, Hq, dh, dtype);
+    if (rc == CXA_OK && Hk > 0) rc = check_rows(w, "k", k, k_stride, n_tokens, Hk, dh, dtype);
+    if (rc == CXA_OK && Hk > 0) rc = check_rows(w, "k_out", k_out, ko_stride, n_tokens, Hk, dh, dtype);
     if (rc != CXA_OK) return rc;
     std::string msg;
     cxa::DeviceInfo dev;
@@ -349,10 +353,10 @@ int cxa_paged_append(const cxa_pages* pages, int layer, int B, int n_tokens, con
     if (rc == CXA_OK) rc = check_rotary(w, rot, pages->dh);
     if (rc != CXA_OK) return rc;
     if (n_tokens == 0) return CXA_OK;
-    rc = check_rows(w, "k", k, k_stride, pages->Hkv, pages->dh, dtype);
-    if (rc == CXA_OK) rc = check_rows(w, "v", v, v_stride, pages->Hkv, pages->dh, dtype);
-    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q", q, q_stride, Hq, pages->dh, dtype);
-    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q_out", q_out, qo_stride, Hq, pages->dh, dtype);
+    rc = check_rows(w, "k", k, k_stride, n_tokens, pages->Hkv, pages->dh, dtype);
+    if (rc == CXA_OK) rc = check_rows(w, "v", v, v_stride, n_tokens, pages->Hkv, pages->dh, dtype);
+    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q", q, q_stride, n_tokens, Hq, pages->dh, dtype);
+    if (rc == CXA_OK && Hq > 0) rc = check_rows(w, "q_out", q_out, qo_stride, n_tokens, Hq, pages->dh, dtype);
     if (rc != CXA_OK) return rc;
     std::string msg;
     cxa::DeviceInfo dev;
@@ -412,8 +416,8 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
       return fail(CXA_EINVAL, w + ": too many query rows");
     if (!std::isfinite(scale)) return fail(CXA_EINVAL, w + ": scale must be finite");
     if (n_tokens == 0) return CXA_OK;
-    rc = check_rows(w, "q", q, q_stride, Hq, pages->dh, dtype);
-    if (rc == CXA_OK) rc = check_rows(w, "out", out, o_stride, Hq, pages->dh, dtype);
+    rc = check_rows(w, "q", q, q_stride, n_tokens, Hq, pages->dh, dtype);
+    if (rc == CXA_OK) rc = check_rows(w, "out", out, o_stride, n_tokens, Hq, pages->dh, dtype);
     if (rc != CXA_OK) return rc;
     if (overlap(q, q_stride, out, o_stride, n_tokens, Hq, Hq, pages->dh, elt(dtype)))
       return fail(CXA_EINVAL, w + ": out must not overlap q");
@@ -444,11 +448,15 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
+    cxa::PagedTileMaps maps;
     std::unique_lock<std::mutex> together;
-    if (tiles) together = std::unique_lock<std::mutex>(stream_lock(s));
+    if (tiles) {      // whatever can fail does before the first kernel is enqueued
+      if ((e = cxa::prepare_paged_tile(a, dev, &maps, &msg)) != cudaSuccess) return fail_cuda(e, w + ": " + msg);
+      together = std::unique_lock<std::mutex>(stream_lock(s));
+    }
     e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);
-    if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, dev, s, &msg);
-    if (e != cudaSuccess) return fail_cuda(e, w + ": " + (msg.empty() ? "launch" : msg));
+    if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, maps, dev, s);
+    if (e != cudaSuccess) return fail_cuda(e, w + ": launch");
     return CXA_OK;
   });
 }

@@ -970,7 +970,29 @@ bool encode(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuu
 static_assert(kTileCounters == kMaxBlocks * kTiles * 3, "three counters a tile of a block");
 
 template <int kDh>
-cudaError_t launch(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
+cudaError_t prepare(const PagedAttnLaunch& a, const DeviceInfo& dev, PagedTileMaps* maps, std::string* msg) {
+  using T = Tile<kDh>;
+  const int G = a.Hq / a.layer.Hkv;
+  const int page_size = 1 << a.layer.page_shift;
+  const int box_rows = page_size < T::chunk ? page_size : T::chunk;
+  const cuuint64_t slabs = static_cast<cuuint64_t>(a.layer.num_pages) * a.layer.Hkv;
+  if (!encode(&maps->q, a.q, kDh, a.Hq, a.batch.n_tokens, kDh * 2, static_cast<cuuint64_t>(a.q_stride) * 2, G,
+              kTileRows / G) ||
+      !encode(&maps->k, a.layer.K, kDh, page_size, slabs, kDh * 2, static_cast<cuuint64_t>(page_size) * kDh * 2,
+              box_rows, 1) ||
+      !encode(&maps->v, a.layer.V, kDh, page_size, slabs, kDh * 2, static_cast<cuuint64_t>(page_size) * kDh * 2,
+              box_rows, 1)) {
+    *msg = "the tensor maps of q and the pool cannot be encoded";
+    return cudaErrorInvalidValue;
+  }
+  static SmemOnce once;
+  const cudaError_t e = allow_smem(paged_tile_kernel<kDh>, kSmemBytes, dev.device, &once);
+  if (e != cudaSuccess) *msg = "shared memory of the tile kernel";
+  return e;
+}
+
+template <int kDh>
+cudaError_t launch(const PagedAttnLaunch& a, const PagedTileMaps& maps, const DeviceInfo& dev, cudaStream_t stream) {
   using T = Tile<kDh>;
   TileParams prm;
   prm.out = a.out;
@@ -984,31 +1006,14 @@ cudaError_t launch(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t
   prm.num_pages = a.layer.num_pages;
   prm.Hkv = a.layer.Hkv;
   prm.page_shift = a.layer.page_shift;
-  const int G = a.Hq / a.layer.Hkv;
-  prm.shape.G = G;
-  prm.shape.rows = kTiles * (kTileRows / G * G);      // whole tokens
+  prm.shape.G = a.Hq / a.layer.Hkv;
+  prm.shape.rows = kTiles * (kTileRows / prm.shape.G * prm.shape.G);      // whole tokens
   prm.shape.chunk_shift = T::chunk_shift;
   prm.shape.coarse = false;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
   prm.shape.min_rows = kFewRows + 1;
   prm.shape.max_rows = 0x7FFFFFFF;
 
-  const int page_size = 1 << a.layer.page_shift;
-  const int box_rows = page_size < T::chunk ? page_size : T::chunk;
-  const cuuint64_t slabs = static_cast<cuuint64_t>(a.layer.num_pages) * a.layer.Hkv;
-  CUtensorMap tmQ, tmK, tmV;
-  if (!encode(&tmQ, a.q, kDh, a.Hq, a.batch.n_tokens, kDh * 2, static_cast<cuuint64_t>(a.q_stride) * 2, G,
-              kTileRows / G) ||
-      !encode(&tmK, a.layer.K, kDh, page_size, slabs, kDh * 2, static_cast<cuuint64_t>(page_size) * kDh * 2, box_rows,
-              1) ||
-      !encode(&tmV, a.layer.V, kDh, page_size, slabs, kDh * 2, static_cast<cuuint64_t>(page_size) * kDh * 2, box_rows,
-              1)) {
-    *msg = "the tensor maps of q and the pool cannot be encoded";
-    return cudaErrorInvalidValue;
-  }
-  static SmemOnce once;
-  cudaError_t e = allow_smem(paged_tile_kernel<kDh>, kSmemBytes, dev.device, &once);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   int grid = dev.num_sms;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
@@ -1021,7 +1026,7 @@ cudaError_t launch(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_tile_kernel<kDh>, tmQ, tmK, tmV, prm);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel<kDh>, maps.q, maps.k, maps.v, prm);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -1037,8 +1042,13 @@ size_t paged_tile_part_bytes(int dh) {
   return static_cast<size_t>(2 * kMaxBlocks) * kTiles * kTileRows * (dh + 2) * 4;
 }
 
-cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
-  return a.dh == 64 ? launch<64>(a, dev, stream, msg) : launch<128>(a, dev, stream, msg);
+cudaError_t prepare_paged_tile(const PagedAttnLaunch& a, const DeviceInfo& dev, PagedTileMaps* maps, std::string* msg) {
+  return a.dh == 64 ? prepare<64>(a, dev, maps, msg) : prepare<128>(a, dev, maps, msg);
+}
+
+cudaError_t launch_paged_tile(const PagedAttnLaunch& a, const PagedTileMaps& maps, const DeviceInfo& dev,
+                              cudaStream_t stream) {
+  return a.dh == 64 ? launch<64>(a, maps, dev, stream) : launch<128>(a, maps, dev, stream);
 }
 
 }  // namespace cxa

@@ -322,8 +322,8 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
  * such entries beforehand on the host.
  *
  * Packed tensors hold a token's heads contiguously, dh channels each; consecutive
- * tokens lie `stride` ELEMENTS apart (a multiple of 16 bytes, at least heads * dh), so
- * that slices of a fused projection's rows are taken as they are. They are 16-byte
+ * tokens lie `stride` ELEMENTS apart (a multiple of 16 bytes, at least heads * dh, less
+ * than 2^40 bytes; all rows together span at most 2^56 bytes), so that slices of a fused projection's rows are taken as they are. They are 16-byte
  * aligned and of one type `dtype`: CXA_F32 (pool CXA_F32 or CXA_BF16) or CXA_BF16 (pool
  * CXA_BF16). Calls with n_tokens == 0 enqueue nothing.
  *

@@ -224,3 +224,23 @@ def test_workspace_holds_its_counters_and_a_part_for_each_kernel():
     assert many < cxa.cxa_paged_attention_workspace_bytes(8, 8, 128, 17)
     for bad in ((0, 1, 64, 1), (8, 3, 64, 1), (8, 8, 32, 1), (8, 8, 64, 0)):
         assert cxa.cxa_paged_attention_workspace_bytes(*bad) == 0
+
+
+def test_strides_that_no_tensor_map_holds_are_refused_before_anything_is_enqueued(pages):
+    """Strides stay below 2^40 bytes, even where one token makes them unused, and rows times
+    stride below what 64 bits of address hold. (The calls that pass stop at their workspace.)"""
+    before = cxa.cxa_launch_count()
+    for n in (1, 5):
+        kw = dict(n_tokens=n, workspace=0)
+        refused(attention(pages, q_stride=1 << 39, **kw), "row stride of q must")
+        refused(attention(pages, q_stride=1 << 40, **kw), "row stride of q must")
+        refused(attention(pages, o_stride=1 << 39, **kw), "row stride of out must")
+        refused(attention(pages, q_stride=(1 << 39) - 8, out=FAKE - (1 << 20), **kw), "workspace")
+        refused(append(pages, n_tokens=n, k_stride=1 << 39), "row stride of k must")
+        refused(append(pages, n_tokens=n, v_stride=1 << 39), "row stride of v must")
+    rc, f32 = make_pages(dtype=cxa.CXA_F32)
+    refused(attention(f32, dtype=cxa.CXA_F32, q_stride=1 << 38, workspace=0), "row stride of q must")
+    cxa.cxa_pages_destroy(f32)
+    for n, stride in ((1 << 26, 1 << 31), (1 << 18, (1 << 39) - 8), ((1 << 28), 1 << 38)):
+        refused(attention(pages, n_tokens=n, q_stride=stride, workspace=0), "rows of q span")
+    assert cxa.cxa_launch_count() == before
