@@ -44,7 +44,8 @@
 // sums, references and O are fp32, the sums of the values before rounding.
 //
 // Keys behind an item's last visible one weigh 0 and their V rows, which may hold anything,
-// are zeroed in shared memory before P.V. Keys that some rows see and others do not weigh
+// are zeroed in shared memory before P.V, as are those of a page outside the pool, which the
+// copy warp leaves out. Keys that some rows see and others do not weigh
 // 0 in the others; if one of them has a V that is not finite (0 * inf), those keys are
 // added row by row on the CUDA cores instead. Both tiles' softmax warps meet in such chunks.
 #include <cuda.h>
@@ -258,6 +259,18 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// Zeroes `bytes` of shared memory from each address that a lane gives (0: none), by the warp, for
+// the products that read it next. (Rare, and apart: in line it moves the other warps' registers
+// about, 2048 tokens over 32768 keys of 20 heads on 4 331 us against 329.)
+__device__ __noinline__ void zero_rows(uint32_t to, int bytes, int lane) {
+  for (uint32_t m = __ballot_sync(0xffffffffu, to != 0u); m != 0; m &= m - 1) {
+    const uint32_t at = __shfl_sync(0xffffffffu, to, __ffs(m) - 1);
+    for (int o = lane * 16; o < bytes; o += 512) st_shared_v4(at + o, 0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 template <int kDh>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -309,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_mbar_init();
       sm->abort = 0;
     }
+    if (tid < 8) sm->bad[tid] = 0;
     if (warp == kTmaWarp && lane == 0) {
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
@@ -392,14 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (want)
           page = paged_lookup(bt.table + static_cast<size_t>(cur.b) * bt.width, bt.width, p.page_shift, p.num_pages, at);
         const bool load = want && page >= 0;
-        const uint32_t bad = __ballot_sync(0xffffffffu, want && page < 0 && half == 0);
+        const uint32_t bad = __ballot_sync(0xffffffffu, want && page < 0);
         const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, load)) * box_rows * 128);
         const int x = half * 64, y = at & ((1 << p.page_shift) - 1), z = page * p.Hkv + cur.h;
         const uint32_t dst = static_cast<uint32_t>(half * T::half_bytes + box * box_rows * 128);
         const int st = i % kStages, round = i / kStages;
         if (!wait_warp(kKEmpty + st, (round & 1) ^ 1)) break;
         if (lane == 0) {
-          uint32_t boxes = 0;    // a bit a box
+          uint32_t boxes = 0;    // a bit a box, whose scores are left out
           for (uint32_t m = bad; m != 0; m &= m - 1) boxes |= 1u << ((__ffs(m) - 1) / T::halves);
           sm->bad[i & 7] = boxes;
           if (bad != 0) atomicOr(p.status, kStatusBadPage);
@@ -409,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (load) tma_load_3d(k_base + st * kTileBytes + dst, &tmK, bar(kKFull + st), x, y, z);
         sent(kKFull + st, round);
         if (!wait_warp(kVEmpty + st, (round & 1) ^ 1)) break;
+        if (bad != 0)            // no copy fills the V rows of a bad page, and 0 * inf is not 0
+          zero_rows(want && page < 0 ? v_base + st * kTileBytes + dst : 0u, box_rows * 128, lane);
         if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + st), bytes);
         __syncwarp();
         if (load) tma_load_3d(v_base + st * kTileBytes + dst, &tmV, bar(kVFull + st), x, y, z);
@@ -675,7 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_warp(kKFull + st, round & 1);
         }
         const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[i & 7]);
-        const bool special = key0 + T::chunk > see_item || bad != 0;   // some row of the item misses a key
+        // Some row of the item misses a key. Both tiles' warps meet at barriers then: this goes by
+        // positions alone, so that they agree on it also after a wait that ran out, when what
+        // they read in shared memory (`bad`) may differ.
+        const bool special = key0 + T::chunk > see_item;
         if (!here) {
           tile_sync(t);         // every warp of the tile has seen the chunk come
           if (warp % kSoftWarps == 0 && lane == 0) mbar_arrive(bar(kKEmpty + st));
@@ -703,11 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_warp(kVFull + st, round & 1);
           const int key = r & (T::chunk - 1), half = r >> T::chunk_shift;   // this thread's part of V: 64 bytes
           const bool has = T::chunk * T::halves > r;
-          const bool key_bad = ((bad >> (key >> box_shift)) & 1u) != 0;
           const uint32_t vt = v_base + st * kTileBytes;
           const uint32_t vrow = vt + half * T::half_bytes + key * 128 + hf * 64;
           bool wild = false;
-          if (has && key >= lo && key < hi && !key_bad)
+          if (has && key >= lo && key < hi)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint4 u = ld_shared_v4(vrow + 16 * q);
@@ -733,6 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = lo; k < hi; ++k) {
                   const uint32_t w = tmem_ld_1(my_tmem + T::p_col + (k >> 1));
                   tmem_ld_wait();
+                  // (a bad page's keys, P and V of which are 0 anyway, are passed over: without the
+                  // second condition the compiler spills 276 bytes instead of 56)
                   if (k < lim && ((bad >> (k >> box_shift)) & 1u) == 0) {
                     const float pk = __uint_as_float((k & 1) ? w & 0xFFFF0000u : w << 16);
                     const uint32_t vr = vt + (ch / 64) * T::half_bytes + k * 128;
@@ -770,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (here && starts && wild && r == 0 && hf == 0) sm->acc[t] = 1;
-          if (has && (key_bad || key >= (wild ? lo : hi)))
+          if (has && key >= (wild ? lo : hi))
 #pragma unroll
             for (int q = 0; q < 4; ++q) st_shared_v4(vrow + 16 * q, 0u, 0u, 0u, 0u);
           fence_proxy_async_smem();

@@ -770,3 +770,43 @@ def test_attention_reads_what_the_grid_before_has_just_written(dh):
     for k, v, q, out in steps:
         bt.K[0][past:], bt.V[0][past:], bt.q = k.cpu(), v.cpu(), q.cpu()
         bt.close(out)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("n,kv", [(40, 2100), (300, 700), (300, 300)])
+def test_bad_pages_among_chunks_of_many_rows(dh, page, n, kv):
+    """Pages outside the pool at the start, in a row, at the causal limit and at the end: their keys
+    are left out, whatever the places in shared memory held that no copy fills now; and a later
+    token's infinity beside them stays with the tokens that see it."""
+    poison = Batch([n], [kv], page, 4, 2, dh, "bf16", "bf16").fill(rest=math.nan)
+    for t in (poison.cache.Kp, poison.cache.Vp):
+        t.fill_(math.nan)
+    bt = Batch([n], [kv], page, 4, 2, dh, "bf16", "bf16", seed=3)
+    inf_at = kv - n + 5                                  # seen by the tokens from the sixth on
+    bt.V[0][inf_at, 1, 3] = math.inf
+    bt.fill()
+    last = (kv - 1) // page
+    bad = {i for i in (0, 2, 3, (kv - n) // page + 1, last) if i <= last and i != inf_at // page}
+    for j, i in enumerate(sorted(bad)):
+        bt.d["page_table"][0, i] = (-1, 10 ** 6, -2 ** 31)[j % 3]
+    poison.attend()
+    got = bt.attend().cpu()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    pos = torch.arange(kv)
+    here = torch.tensor([i not in bad for i in range(last + 1)])[pos // page]
+    K, V = bt.K[0].double(), bt.V[0].double()
+    for h in range(4):
+        q = bt.q[:, h].double()
+        s = q @ K[:, h // 2].T / math.sqrt(dh)
+        seen = (pos[None] <= (kv - n + torch.arange(n))[:, None]) & here[None]
+        p = torch.softmax(s.masked_fill(~seen, -math.inf), -1).nan_to_num(0)       # (a row of bad pages alone: zero)
+        big = float((q.abs() @ K[:, h // 2].abs().T / math.sqrt(dh)).max())
+        Vh = V[:, h // 2].clone()
+        hot = seen[:, inf_at] if h >= 2 else torch.zeros(n, dtype=torch.bool)
+        Vh[inf_at, 3] = 0 if h >= 2 else Vh[inf_at, 3]
+        ref, A = p @ Vh, p @ Vh.abs()
+        g = got[:, h].double()
+        assert bool(g[hot][:, 3].isinf().all())
+        g[hot, 3] = ref[hot, 3]
+        assert bool(((g - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * 2.0 ** -21 * big) * A).all())
