@@ -640,12 +640,14 @@ int cxa_device_status(int clear) {
   if ((e = cudaMemcpy(&word, dev.status_word, sizeof(word), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return fail_cuda(e, "cxa_device_status: read");
   if (word & cxa::kStatusTimeout) g_timeouts_seen.fetch_add(1, std::memory_order_acq_rel);
-  if (clear) {
-    const unsigned int zero = 0;
-    if ((e = cudaMemcpy(dev.status_word, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
+  // one report a call, and only that one is cleared
+  const unsigned int told = (word & cxa::kStatusTimeout) ? cxa::kStatusTimeout : word & cxa::kStatusBadPage;
+  if (clear && told != 0) {
+    const unsigned int rest = word & ~told;
+    if ((e = cudaMemcpy(dev.status_word, &rest, sizeof(rest), cudaMemcpyHostToDevice)) != cudaSuccess)
       return fail_cuda(e, "cxa_device_status: clear");
   }
-  return (word & cxa::kStatusTimeout) ? CXA_ETIMEOUT : (word & cxa::kStatusBadPage) ? CXA_EPAGE : CXA_OK;
+  return told == cxa::kStatusTimeout ? CXA_ETIMEOUT : told != 0 ? CXA_EPAGE : CXA_OK;
 }
 
 }  // extern "C"

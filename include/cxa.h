@@ -555,7 +555,8 @@ CXA_API unsigned long long cxa_launch_count(void);
  * when a kernel's bounded wait expired since the word was last cleared (the
  * kernel then skipped its remaining work), or CXA_EPAGE when a paged call met a
  * page number outside its pool. Synchronises the device. clear != 0
- * resets the word. Returns CXA_ECUDA if the word cannot be read. After a
+ * takes back what is returned; where both happened, CXA_ETIMEOUT comes first and CXA_EPAGE
+ * with the next call. Returns CXA_ECUDA if the word cannot be read. After a
  * timeout, the counters of a decode or paged attention workspace must be zeroed
  * again before reuse.
  */

@@ -810,3 +810,25 @@ def test_bad_pages_among_chunks_of_many_rows(dh, page, n, kv):
         assert bool(g[hot][:, 3].isinf().all())
         g[hot, 3] = ref[hot, 3]
         assert bool(((g - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * 2.0 ** -21 * big) * A).all())
+
+
+def bad_page_call(stream=None):
+    bt = Batch([1], [160], 16, 4, 2, 64, "bf16", "bf16").fill()
+    bt.d["page_table"][0, 3] = -1
+    q = bt.q.cuda()
+    bt.cache.attend(0, q, **bt.d, max_new=1)         # (workspace and kernels are there)
+    torch.cuda.synchronize()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    return lambda: bt.cache.attend(0, q, **bt.d, max_new=1, stream=stream)
+
+
+def test_a_bad_page_is_not_lost_behind_a_timeout():
+    """Two reports at once come one after the other; clearing takes back the one that was returned."""
+    call = bad_page_call()
+    call()
+    assert cxa.cxa_selftest_wait_timeout(1000) == cxa.CXA_OK
+    assert cxa.cxa_device_status(0) == cxa.CXA_ETIMEOUT
+    assert cxa.cxa_device_status(1) == cxa.CXA_ETIMEOUT
+    assert cxa.cxa_device_status(0) == cxa.CXA_EPAGE
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
