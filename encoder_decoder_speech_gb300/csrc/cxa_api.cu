@@ -637,6 +637,8 @@ int cxa_device_status(int clear) {
   cudaError_t e = cxa::current_device_info(&dev, &msg);
   if (e != cudaSuccess) return fail_cuda(e, "cxa_device_status: " + msg);
   unsigned int word = 0;
+  // (the copy alone would wait for blocking streams only)
+  if ((e = cudaDeviceSynchronize()) != cudaSuccess) return fail_cuda(e, "cxa_device_status: synchronise");
   if ((e = cudaMemcpy(&word, dev.status_word, sizeof(word), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return fail_cuda(e, "cxa_device_status: read");
   if (word & cxa::kStatusTimeout) g_timeouts_seen.fetch_add(1, std::memory_order_acq_rel);

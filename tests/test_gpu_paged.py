@@ -832,3 +832,17 @@ def test_a_bad_page_is_not_lost_behind_a_timeout():
     assert cxa.cxa_device_status(0) == cxa.CXA_EPAGE
     assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
     assert cxa.cxa_device_status(1) == cxa.CXA_OK
+
+
+def test_device_status_waits_for_streams_of_any_kind():
+    s = torch.cuda.Stream()                          # one that the default stream does not wait for
+    call = bad_page_call(s)
+    call()
+    torch.cuda.synchronize()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    call()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
+    torch.cuda.synchronize()
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
