@@ -126,7 +126,9 @@ constexpr size_t kRowsCounters = kRowsMaxBlocks * 3, kTileCounters = kTileMaxBlo
 constexpr size_t kPagedCounterBytes = (kRowsCounters + kTileCounters) * 4;
 static_assert(kPagedCounterBytes % 256 == 0, "the partial states behind the counters are aligned");
 size_t paged_rows_part_bytes(int dh);
-bool paged_rows_countable(const PagedAttnLaunch& a);   // whether the call's work can be numbered in 31 bits
+// Whether the work of each kernel can be numbered in 31 bits.
+bool paged_rows_countable(const PagedAttnLaunch& a, int max_rows);
+bool paged_tile_countable(const PagedAttnLaunch& a);
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream);
 bool paged_tile_takes(int G, bool act_bf16, int max_new);
 size_t paged_tile_part_bytes(int dh);

@@ -439,22 +439,22 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
-    if (!cxa::paged_rows_countable(a))
-      return fail(CXA_EINVAL, w + ": Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages * page_size / 64 + 1) must be "
-                                  "below 2^31");
+    const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
+    const int max_rows = tiles ? cxa::kFewRows : 0x7FFFFFFF;
+    if (!cxa::paged_rows_countable(a, max_rows) || (tiles && !cxa::paged_tile_countable(a)))
+      return fail(CXA_EINVAL, w + ": the chunks of keys of all tiles of query rows (see cxa.h) must be below 2^31");
     std::string msg;
     cxa::DeviceInfo dev;
     cudaError_t e = cxa::current_device_info(&dev, &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool tiles = cxa::paged_tile_takes(Hq / pages->Hkv, a.act_bf16, max_new);
     cxa::PagedTileMaps maps;
     std::unique_lock<std::mutex> together;
     if (tiles) {      // whatever can fail does before the first kernel is enqueued
       if ((e = cxa::prepare_paged_tile(a, dev, &maps, &msg)) != cudaSuccess) return fail_cuda(e, w + ": " + msg);
       together = std::unique_lock<std::mutex>(stream_lock(s));
     }
-    e = cxa::launch_paged_rows(a, tiles ? cxa::kFewRows : 0x7FFFFFFF, dev, s);
+    e = cxa::launch_paged_rows(a, max_rows, dev, s);
     if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, maps, dev, s);
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch");
     return CXA_OK;

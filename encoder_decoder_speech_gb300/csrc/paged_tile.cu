@@ -989,6 +989,9 @@ bool encode(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuu
 
 static_assert(kTileCounters == kMaxBlocks * kTiles * 3, "three counters a tile of a block");
 
+// Query rows of an item: whole tokens in each tile.
+int item_rows(int G) { return kTiles * (kTileRows / G * G); }
+
 template <int kDh>
 cudaError_t prepare(const PagedAttnLaunch& a, const DeviceInfo& dev, PagedTileMaps* maps, std::string* msg) {
   using T = Tile<kDh>;
@@ -1027,7 +1030,7 @@ cudaError_t launch(const PagedAttnLaunch& a, const PagedTileMaps& maps, const De
   prm.Hkv = a.layer.Hkv;
   prm.page_shift = a.layer.page_shift;
   prm.shape.G = a.Hq / a.layer.Hkv;
-  prm.shape.rows = kTiles * (kTileRows / prm.shape.G * prm.shape.G);      // whole tokens
+  prm.shape.rows = item_rows(prm.shape.G);
   prm.shape.chunk_shift = T::chunk_shift;
   prm.shape.coarse = false;
   prm.shape.cap = a.batch.width << a.layer.page_shift;
@@ -1056,6 +1059,12 @@ cudaError_t launch(const PagedAttnLaunch& a, const PagedTileMaps& maps, const De
 bool paged_tile_takes(int G, bool act_bf16, int max_new) {
   // A tile holds whole tokens, so G query heads have to fit into it.
   return act_bf16 && G <= kTileRows && static_cast<long long>(max_new) * G > kFewRows;
+}
+
+bool paged_tile_countable(const PagedAttnLaunch& a) {
+  const int G = a.Hq / a.layer.Hkv;
+  return work_bound(a.batch, a.layer.page_shift, a.layer.Hkv, G, item_rows(G),
+                    a.dh == 64 ? Tile<64>::chunk_shift : Tile<128>::chunk_shift) < 1LL << 31;
 }
 
 size_t paged_tile_part_bytes(int dh) {

@@ -453,8 +453,11 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  *              first call on a new buffer (cudaMemset); calls leave them zero, so that
  *              calls of any shapes may use it in turn. Calls that share a workspace must be
  *              ordered on one stream.
- * Work is counted in 31 bits: Hkv * (B + n_tokens * Hq / Hkv / 16) * (max_pages *
- * page_size / 64 + 1) must be below 2^31 (CXA_EINVAL otherwise).
+ * Work is counted in 31 bits (CXA_EINVAL otherwise), by what the host knows of the batch. With
+ * G = Hq / Hkv and t = max_pages * page_size, Hkv * (B + n_tokens * G / 16) * (t / 64 + 1) must
+ * be below 2^31; for CXA_BF16 with max_new * G > 16 and G <= 128 instead Hkv * B * (t / 64 + 1)
+ * and Hkv * (B + n_tokens * G / r) * (t * dh / 8192 + 1), r = 2 * (128 / G * G) rows (128 / G
+ * rounded down).
  * Values that no key position of a row makes visible never reach it: rows of a page
  * behind the last key, and later tokens' rows, may hold infinities or NaN. A row that
  * sees no key is zero. A row that sees an infinity or a NaN in q, K or V may be

@@ -846,3 +846,30 @@ def test_device_status_waits_for_streams_of_any_kind():
     assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE
     torch.cuda.synchronize()
     assert cxa.cxa_device_status(1) == cxa.CXA_OK
+
+
+def test_a_wide_table_gives_what_a_narrow_one_does():
+    """A prompt of 65,536 tokens over a table of 2^20 positions (kept wide for a captured graph)."""
+    n, past, page = 65536, 4000, 256
+    need = -(-(n + past) // page)
+    cache = cxa.PagedCache(need, page, 1, 8, 64, "bf16")
+    cache.Kp.normal_()
+    cache.Vp.normal_()
+    q = torch.randn(n, 32, 64, device="cuda", dtype=torch.bfloat16)
+    at = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [n + past])]
+    narrow = torch.randperm(need, device="cuda").to(torch.int32)[None].contiguous()
+    wide = torch.full((1, 4096), -1, dtype=torch.int32, device="cuda")
+    wide[:, :need] = narrow
+    want = cache.attend(0, q, *at, narrow, max_new=n)
+    assert bool(want.isfinite().all())
+    assert torch.equal(cache.attend(0, q, *at, wide, max_new=n), want)
+    # one bf16 probability, scores of up to 8 in magnitude
+    # (the table's order of pages is the keys': the first token sees past + 1 of them)
+    K = cache.Kp[0, narrow[0].long()].transpose(0, 1).reshape(8, -1, 64)
+    V = cache.Vp[0, narrow[0].long()].transpose(0, 1).reshape(8, -1, 64)
+    for i in (0, 12345, n - 1):
+        kv = past + i + 1
+        p = torch.softmax(torch.einsum("hgd,hkd->hgk", q[i].view(8, 4, 64).double(), K[:, :kv].double()) / 8, -1)
+        ref = torch.einsum("hgk,hkd->hgd", p, V[:, :kv].double()).view(32, 64)
+        A = torch.einsum("hgk,hkd->hgd", p, V[:, :kv].double().abs()).view(32, 64)
+        assert bool(((want[i].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -16) * A).all())

@@ -2,11 +2,15 @@
 No GPU is needed: every call here returns before any CUDA call, and the device pointers
 handed over are never dereferenced."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
 from encoder_decoder_speech_gb300 import cxa
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x7f0000000000          # 256-byte aligned, never dereferenced
 BIG = 1 << 40
 
@@ -244,3 +248,30 @@ def test_strides_that_no_tensor_map_holds_are_refused_before_anything_is_enqueue
     for n, stride in ((1 << 26, 1 << 31), (1 << 18, (1 << 39) - 8), ((1 << 28), 1 << 38)):
         refused(attention(pages, n_tokens=n, q_stride=stride, workspace=0), "rows of q span")
     assert cxa.cxa_launch_count() == before
+
+
+def test_calls_that_can_be_numbered_are_not_refused():
+    """65,536 tokens of 4 heads a K/V head, 8 K/V heads, over a table of 2^20 positions: 1,025
+    tiles of 256 rows a head, 8,193 chunks each. In a process that sees no GPU, where a call that
+    passes every check ends with CXA_ECUDA."""
+    code = """if True:
+        from encoder_decoder_speech_gb300 import cxa
+        rc, p = cxa.cxa_pages_create(1 << 46, 1 << 47, 5000, 256, 1, 8, {dh}, cxa.CXA_BF16)
+        assert rc == cxa.CXA_OK
+        rc = cxa.cxa_paged_attention(p, 0, {B}, {n}, {m}, 1 << 40, 1 << 40, 1 << 40, {w}, 1 << 45, 32 * {dh}, 32, 1 << 48,
+                                     32 * {dh}, 0.0, cxa.CXA_BF16, 1 << 40, 1 << 40, 0)
+        print(rc, cxa.cxa_last_error_message())
+    """
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+
+    def call(**kw):
+        a = dict(dict(dh=64, B=1, n=65536, m=65536, w=4096), **kw)
+        r = subprocess.run([sys.executable, "-c", code.format(**a)], env=env, cwd=ROOT, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        return r.stdout
+
+    for kw in (dict(), dict(dh=128), dict(B=1000, m=64), dict(n=1 << 21, m=1 << 21, w=256)):
+        assert call(**kw).startswith(str(cxa.CXA_ECUDA)), kw
+    for kw in (dict(m=1), dict(B=1 << 14), dict(n=1 << 25, m=100), dict(n=1 << 24, m=100, dh=128)):
+        out = call(**kw)
+        assert out.startswith(str(cxa.CXA_EINVAL)) and "below 2^31" in out, kw
