@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import threading
 
 from . import _build
 
@@ -637,10 +636,23 @@ def _capturing(tc, index, stream, raw):
         return tc.capturing()
 
 
+# cudaStreamPerThread: one handle for every thread's own default stream. The allocator takes
+# them for one stream, so memory of theirs may be handed from one thread to another while the
+# first one's work is still using it.
+_PER_THREAD = 2
+
+
+def _own_handle(raw, what):
+    if raw == _PER_THREAD:
+        raise ValueError(f"memory cannot be kept apart for threads' own default streams: pass {what}, or name "
+                         "another stream")
+
+
 def _new(tc, q, stream, index):
     """An empty tensor like q for the result of a call on `stream`, in that stream's memory."""
     if stream is None:
         return q.new_empty(q.shape)
+    _own_handle(_stream(stream), "the tensors for the results")
     with tc.torch.cuda.stream(tc.torch.cuda.ExternalStream(_stream(stream), device=index)):
         return q.new_empty(q.shape)
 
@@ -723,8 +735,13 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
 class PagedCache:
     """Owns a [L][num_pages][Hkv][page_size][dh] pool of K/V pages (``Kp``, ``Vp``, zeroed),
     its descriptor, and the attention's workspaces: one per stream, so that calls on
-    different streams do not share one. The batch of a call is q_start [B + 1], kv_len [B]
+    different streams do not share one (of more than 64 the oldest are dropped; a stream's
+    calls must be done before it is destroyed, as its handle may come back as another's).
+    Calls on a thread's own default stream (cudaStreamPerThread) need a workspace and an
+    out of the caller's. The batch of a call is q_start [B + 1], kv_len [B]
     and page_table [B, max_pages], int32 on the device (see include/cxa.h)."""
+
+    KEPT_WORKSPACES = 64
 
     def __init__(self, num_pages: int, page_size: int, L: int, Hkv: int, dh: int = 64, cache_dtype: str = "bf16",
                  device="cuda"):
@@ -760,8 +777,8 @@ class PagedCache:
                 self._ws_bytes.clear()
             need = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
             self._ws_bytes[Hq, max_new] = need
-        key = (raw, threading.get_ident()) if raw == 2 else raw     # 2: each thread's own default stream
-        kept = self._ws.get(key)
+        _own_handle(raw, "a workspace")
+        kept = self._ws.get(raw)
         capturing = _capturing(tc, self._at, stream, raw)
         if kept is not None and kept[2] >= need and not capturing:
             return kept
@@ -771,7 +788,10 @@ class PagedCache:
             ws[:CXA_PAGED_COUNTER_BYTES].zero_()
         new = (ws, ws.data_ptr(), ws.numel())
         if not capturing:
-            self._ws[key] = new
+            self._ws.pop(raw, None)
+            self._ws[raw] = new                # the newest last
+            while len(self._ws) > self.KEPT_WORKSPACES:
+                self._ws.pop(next(iter(self._ws), None), None)     # its memory goes back to its stream's
         return new
 
     def workspace(self, Hq: int, max_new: int, stream=None):
@@ -844,6 +864,7 @@ class PagedCache:
         if getattr(self, "handle", None):
             cxa_pages_destroy(self.handle)
             self.handle = None
+            self._ws.clear()
 
     def __del__(self):
         try:

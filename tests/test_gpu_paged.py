@@ -873,3 +873,47 @@ def test_a_wide_table_gives_what_a_narrow_one_does():
         ref = torch.einsum("hgk,hkd->hgd", p, V[:, :kv].double()).view(32, 64)
         A = torch.einsum("hgk,hkd->hgd", p, V[:, :kv].double().abs()).view(32, 64)
         assert bool(((want[i].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -16) * A).all())
+
+
+def test_threads_own_default_streams_need_memory_of_the_caller():
+    """One handle (2) stands for every thread's own default stream: no memory is kept or made for it."""
+    a = Batch([1] * 2, [300, 200], 16, 8, 2, 64, "bf16", "bf16").fill()
+    want, q, out = a.attend(), a.q.cuda(), torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    ws = a.cache.workspace(8, 1)
+    pos = torch.arange(2, dtype=torch.int32).cuda()
+    turned, _ = cxa.qk_norm_rope(q, None, pos, rotary=cxa.Rotary(64))
+    torch.cuda.synchronize()
+    for kw in (dict(), dict(out=out), dict(workspace=ws)):
+        with pytest.raises(ValueError, match="own default stream"):
+            a.cache.attend(0, q, **a.d, max_new=1, stream=2, **kw)
+    with pytest.raises(ValueError, match="own default stream"):
+        a.cache.workspace(8, 1, stream=2)
+    with pytest.raises(ValueError, match="own default stream"):
+        cxa.qk_norm_rope(q, None, pos, rotary=cxa.Rotary(64), stream=2)
+    got = []
+
+    def calls():
+        got.append(a.cache.attend(0, q, **a.d, max_new=1, stream=2, out=out, workspace=ws))
+        got.append(cxa.qk_norm_rope(q, None, pos, rotary=cxa.Rotary(64), stream=2, q_out=torch.empty_like(q))[0])
+
+    t = threading.Thread(target=calls)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], turned)
+
+
+def test_workspaces_of_many_streams_are_bounded(monkeypatch):
+    monkeypatch.setattr(cxa.PagedCache, "KEPT_WORKSPACES", 3)
+    a = Batch([1] * 4, [2000, 900, 30, 4000], 16, 8, 2, 64, "bf16", "bf16").fill()
+    want, q = a.attend(), a.q.cuda()
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    torch.cuda.synchronize()
+    outs = [a.cache.attend(0, q, **a.d, max_new=1, stream=s) for _ in range(6) for s in streams]
+    assert len(a.cache._ws) == 3 and [s.cuda_stream for s in streams[-3:]] == list(a.cache._ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    a.cache.close()
+    assert not a.cache._ws
+    with pytest.raises(cxa.CxaError, match="descriptor is NULL"):
+        a.attend()
