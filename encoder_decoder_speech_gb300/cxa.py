@@ -860,11 +860,16 @@ class PagedCache:
         check(cxa_paged_check(self.handle, page_table.shape[0], n_tokens, q_start.tolist(), kv_len.tolist(),
                               page_table.reshape(-1).tolist(), page_table.shape[1]), "cxa_paged_check")
 
+    def drop_workspaces(self) -> None:
+        """Give the kept workspaces back: the next calls get new ones, with counters of zero. To be
+        called after a CXA_ETIMEOUT, which may leave counters behind."""
+        self._ws.clear()
+
     def close(self) -> None:
         if getattr(self, "handle", None):
             cxa_pages_destroy(self.handle)
             self.handle = None
-            self._ws.clear()
+            self.drop_workspaces()
 
     def __del__(self):
         try:

@@ -561,7 +561,7 @@ CXA_API unsigned long long cxa_launch_count(void);
  * takes back what is returned; where both happened, CXA_ETIMEOUT comes first and CXA_EPAGE
  * with the next call. Returns CXA_ECUDA if the word cannot be read. After a
  * timeout, the counters of a decode or paged attention workspace must be zeroed
- * again before reuse.
+ * again before reuse (a Python PagedCache drops its own with drop_workspaces()).
  */
 CXA_API int cxa_device_status(int clear);
 

@@ -917,3 +917,18 @@ def test_workspaces_of_many_streams_are_bounded(monkeypatch):
     assert not a.cache._ws
     with pytest.raises(cxa.CxaError, match="descriptor is NULL"):
         a.attend()
+
+
+def test_counters_left_behind_go_with_the_kept_workspaces():
+    """After a wait that ran out a kept workspace may hold counters: dropping it is enough."""
+    a = Batch([1] * 4 + [60], [2000, 900, 30, 4000, 800], 16, 8, 2, 64, "bf16", "bf16").fill()
+    want, s = a.attend(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, s):
+        a.cache.workspace(8, 60, stream=stream)[:cxa.CXA_PAGED_COUNTER_BYTES] = 1
+    torch.cuda.synchronize()
+    a.cache.drop_workspaces()
+    for stream in (None, s):
+        got = a.attend(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
