@@ -311,10 +311,10 @@ int cxa_paged_check(const cxa_pages* pages, int B, int n_tokens, const int* q_st
       for (int b = 0; b < B; ++b) {
         const std::string at = " (sequence " + std::to_string(b) + ")";
         const cxa::PagedSeq s = cxa::paged_seq(q_start, kv_len, b, n_tokens);
+        if (s.n == 0) continue;
         if (kv_len[b] < s.n) return fail(CXA_EINVAL, w + ": kv_len is less than the new tokens" + at);
         if (s.kv > max_pages << pages->page_shift)
           return fail(CXA_EINVAL, w + ": kv_len passes the table's row" + at);
-        if (s.n == 0) continue;
         const int* row = page_table + static_cast<size_t>(b) * max_pages;
         const int first_new = (s.kv - s.n) >> pages->page_shift;
         for (int t = 0; t < s.kv; t += pages->page_size) {

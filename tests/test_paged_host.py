@@ -275,3 +275,11 @@ def test_calls_that_can_be_numbered_are_not_refused():
     for kw in (dict(m=1), dict(B=1 << 14), dict(n=1 << 25, m=100), dict(n=1 << 24, m=100, dh=128)):
         out = call(**kw)
         assert out.startswith(str(cxa.CXA_EINVAL)) and "below 2^31" in out, kw
+
+
+def test_batch_check_leaves_sequences_without_new_tokens_alone(pages):
+    """Their keys and pages are not read by any kernel: a slot that is free may hold anything."""
+    for kv in (-1, 0, 49, 2 ** 31 - 1, -2 ** 31):
+        assert cxa.cxa_paged_check(pages, 2, 4, [0, 0, 4], [kv, 40], [-1, 99, -7, 9, 0, 7], 3) == cxa.CXA_OK
+        assert cxa.cxa_paged_check(pages, 2, 4, [0, 4, 4], [40, kv], [9, 0, 7, 9, 99, 0], 3) == cxa.CXA_OK
+        refused(cxa.cxa_paged_check(pages, 2, 4, [0, 1, 4], [kv, 40], [-1, 99, -7, 9, 0, 7], 3), "(sequence 0)")
