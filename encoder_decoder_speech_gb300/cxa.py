@@ -291,6 +291,8 @@ def cxa_rotary_frequencies(rot_dim, base, scaling, factor=1.0, orig_len=0.0, alp
 
 def cxa_rotary_create(rot_dim, layout, freq, attn_factor=1.0):
     """freq: host sequence of rot_dim / 2 numbers. Returns (status, handle)."""
+    if freq is not None and len(freq) < rot_dim // 2:
+        raise ValueError("freq must have rot_dim / 2 entries")
     h = ctypes.c_void_p()
     arr = None if freq is None else (ctypes.c_double * max(len(freq), 1))(*freq)
     rc = load().cxa_rotary_create(ctypes.byref(h), rot_dim, layout, arr, attn_factor)

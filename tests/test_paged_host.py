@@ -283,3 +283,9 @@ def test_batch_check_leaves_sequences_without_new_tokens_alone(pages):
         assert cxa.cxa_paged_check(pages, 2, 4, [0, 0, 4], [kv, 40], [-1, 99, -7, 9, 0, 7], 3) == cxa.CXA_OK
         assert cxa.cxa_paged_check(pages, 2, 4, [0, 4, 4], [40, kv], [9, 0, 7, 9, 99, 0], 3) == cxa.CXA_OK
         refused(cxa.cxa_paged_check(pages, 2, 4, [0, 1, 4], [kv, 40], [-1, 99, -7, 9, 0, 7], 3), "(sequence 0)")
+
+
+def test_short_lists_of_frequencies_are_not_read_past_their_end():
+    for rot, n in ((64, 0), (64, 1), (64, 31), (2, 0), (128, 63)):
+        with pytest.raises(ValueError, match="rot_dim / 2"):
+            cxa.cxa_rotary_create(rot, 0, [0.1] * n)
