@@ -325,6 +325,8 @@ def cxa_paged_check(handle, B, n_tokens, q_start, kv_len, page_table, max_pages)
     """q_start [B + 1], kv_len [B], page_table [B * max_pages]: host sequences of ints."""
     def ints(x):
         x = [int(v) for v in x]
+        if any(v < -2 ** 31 or v >= 2 ** 31 for v in x):
+            raise ValueError("q_start, kv_len and page_table must hold 32-bit integers")
         return (ctypes.c_int * max(len(x), 1))(*x)
     if len(q_start) != B + 1 or len(kv_len) != B or len(page_table) != B * max_pages:
         raise ValueError("q_start, kv_len and page_table must have B + 1, B and B * max_pages entries")

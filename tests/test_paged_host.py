@@ -289,3 +289,14 @@ def test_short_lists_of_frequencies_are_not_read_past_their_end():
     for rot, n in ((64, 0), (64, 1), (64, 31), (2, 0), (128, 63)):
         with pytest.raises(ValueError, match="rot_dim / 2"):
             cxa.cxa_rotary_create(rot, 0, [0.1] * n)
+
+
+def test_batch_check_does_not_wrap_large_numbers(pages):
+    """What 32 bits do not hold is refused, not taken for what its low bits are."""
+    good = dict(q_start=[0, 1, 5], kv_len=[17, 40], page_table=[3, 4, -1, 9, 0, 7])
+    for name, i, v in (("kv_len", 1, 2 ** 32 + 40), ("page_table", 0, 2 ** 32 + 3), ("q_start", 2, 5 - 2 ** 32)):
+        kw = {k: list(x) for k, x in good.items()}
+        assert cxa.cxa_paged_check(pages, 2, 6, **kw, max_pages=3) == cxa.CXA_OK
+        kw[name][i] = v
+        with pytest.raises(ValueError, match="32-bit"):
+            cxa.cxa_paged_check(pages, 2, 6, **kw, max_pages=3)
