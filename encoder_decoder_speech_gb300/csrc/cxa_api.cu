@@ -17,7 +17,7 @@
 #include "ptx.cuh"
 
 // Device-side status word: kernels OR in 1 when a bounded wait expires, 2 for a page
-// number outside the pool (paged.cuh).
+// number outside the pool, 4 for a q_start that decreases (paged.cuh).
 static __device__ unsigned int g_cxa_status_word = 0;
 
 struct cxa_cache {
@@ -643,13 +643,18 @@ int cxa_device_status(int clear) {
     return fail_cuda(e, "cxa_device_status: read");
   if (word & cxa::kStatusTimeout) g_timeouts_seen.fetch_add(1, std::memory_order_acq_rel);
   // one report a call, and only that one is cleared
-  const unsigned int told = (word & cxa::kStatusTimeout) ? cxa::kStatusTimeout : word & cxa::kStatusBadPage;
+  const unsigned int told = (word & cxa::kStatusTimeout)   ? cxa::kStatusTimeout
+                            : (word & cxa::kStatusBadPage) ? cxa::kStatusBadPage
+                                                           : word & cxa::kStatusBadBatch;
   if (clear && told != 0) {
     const unsigned int rest = word & ~told;
     if ((e = cudaMemcpy(dev.status_word, &rest, sizeof(rest), cudaMemcpyHostToDevice)) != cudaSuccess)
       return fail_cuda(e, "cxa_device_status: clear");
   }
-  return told == cxa::kStatusTimeout ? CXA_ETIMEOUT : told != 0 ? CXA_EPAGE : CXA_OK;
+  return told == 0                         ? CXA_OK
+         : told == cxa::kStatusTimeout     ? CXA_ETIMEOUT
+         : told == cxa::kStatusBadPage     ? CXA_EPAGE
+                                           : fail(CXA_EINVAL, "cxa_device_status: a q_start that decreases");
 }
 
 }  // extern "C"

@@ -66,7 +66,7 @@ __host__ __device__ inline int paged_lookup(const int* table_row, int width, int
 }
 
 // Bits of the device status word.
-constexpr unsigned int kStatusTimeout = 1u, kStatusBadPage = 2u;
+constexpr unsigned int kStatusTimeout = 1u, kStatusBadPage = 2u, kStatusBadBatch = 4u;
 
 struct NormRopeLaunch {
   const void *q, *k, *v;            // k, v may be null; v only with pages

@@ -675,7 +675,7 @@ size_t paged_rows_part_bytes(int dh) { return static_cast<size_t>(2 * kMaxBlocks
 bool paged_rows_countable(const PagedAttnLaunch& a, int max_rows) {
   PagedBatch bt = a.batch;
   if (max_rows <= kRows) bt.n_tokens = 0;      // a tile a sequence and head, whatever the others bring
-  return work_bound(bt, a.layer.page_shift, a.layer.Hkv, a.Hq / a.layer.Hkv, kRows, 6) < 1LL << 31;
+  return work_bound(bt, a.layer.page_shift, a.layer.Hkv, a.Hq / a.layer.Hkv, kRows, 6) < kCountLimit;
 }
 
 cudaError_t launch_paged_rows(const PagedAttnLaunch& a, int max_rows, const DeviceInfo& dev, cudaStream_t stream) {

@@ -1064,7 +1064,7 @@ bool paged_tile_takes(int G, bool act_bf16, int max_new) {
 bool paged_tile_countable(const PagedAttnLaunch& a) {
   const int G = a.Hq / a.layer.Hkv;
   return work_bound(a.batch, a.layer.page_shift, a.layer.Hkv, G, item_rows(G),
-                    a.dh == 64 ? Tile<64>::chunk_shift : Tile<128>::chunk_shift) < 1LL << 31;
+                    a.dh == 64 ? Tile<64>::chunk_shift : Tile<128>::chunk_shift) < kCountLimit;
 }
 
 size_t paged_tile_part_bytes(int dh) {

@@ -56,13 +56,20 @@ __device__ __forceinline__ int tile_chunks(const PagedSeq& s, const WorkShape& w
   return w.coarse ? max(1, n >> 2) : n;
 }
 
-// The most chunks a call can have, by what the host knows of it. Kernels count in 32 bits:
-// calls of 2^31 and more are refused.
+// The most chunks a call can have, by what the host knows of it. Kernels count in 31 bits:
+// calls that could reach kCountLimit are refused.
 inline long long work_bound(const PagedBatch& bt, int page_shift, int Hkv, int G, int rows, int chunk_shift) {
   const long long tiles = bt.B + static_cast<long long>(bt.n_tokens) * G / rows;      // a head
   const long long keys = static_cast<long long>(bt.width) << page_shift;
   const double bound = static_cast<double>(tiles) * Hkv * static_cast<double>((keys >> chunk_shift) + 1);
   return bound < 9e18 ? static_cast<long long>(bound) : 9000000000000000000LL;
+}
+
+// Sums that stop at the limit. Sequences overlap where q_start decreases, against its contract;
+// their chunks may then pass what the host allowed for, and must not wrap around.
+constexpr int kCountLimit = 0x7FFFFFFF;
+__device__ __forceinline__ int count_add(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), static_cast<unsigned>(kCountLimit)));
 }
 
 // The first step of chunk c of nc.
@@ -101,7 +108,8 @@ struct WorkScratch {
 // kThreads threads of the block; returns false if the block has nothing to do. With
 // kMayCoarsen, w becomes coarse where a block would have less than four steps: a merge costs
 // as much as some eight of them. With a status word, sequences whose keys pass their row of
-// the table are reported there, whichever kernel they are of.
+// the table are reported there, whichever kernel they are of, and a q_start that decreases. A
+// batch of more chunks than can be numbered, which only such a q_start brings, is left out.
 template <int kThreads, bool kMayCoarsen>
 __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
                             WorkCursor* cur, unsigned int* status = nullptr) {
@@ -116,11 +124,12 @@ __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScr
     const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
     const int m = work_rows(s, w);
     if (status != nullptr && s.n > 0 && s.kv > w.cap) atomicOr(status, kStatusBadPage);
+    if (status != nullptr && bt.q_start[b + 1] < bt.q_start[b]) atomicOr(status, kStatusBadBatch);
 #pragma unroll 1
     for (int rt = 0; rt * w.rows < m; ++rt) {
       const int n = tile_steps(s, w, rt);
-      mine[0] += n * Hkv;
-      mine[1] += max(1, n >> 2) * Hkv;
+      mine[0] = count_add(mine[0], n * Hkv);
+      mine[1] = count_add(mine[1], max(1, n >> 2) * Hkv);
     }
   }
 #pragma unroll
@@ -129,7 +138,7 @@ __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScr
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl[k], off);
-      if (lane >= off) incl[k] += o;
+      if (lane >= off) incl[k] = count_add(incl[k], o);
     }
     if (lane == 31) sm->scan[k][warp] = incl[k];
   }
@@ -138,9 +147,10 @@ __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScr
   for (int k = 0; k < (kMayCoarsen ? 2 : 1); ++k)
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
-      if (i < warp) before[k] += sm->scan[k][i];
-      total[k] += sm->scan[k][i];
+      if (i < warp) before[k] = count_add(before[k], sm->scan[k][i]);
+      total[k] = count_add(total[k], sm->scan[k][i]);
     }
+  if (total[0] == kCountLimit) return false;    // the same in every thread
   w.coarse = kMayCoarsen && total[0] < 4 * static_cast<int>(gridDim.x);
   const int k = w.coarse ? 1 : 0, blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
   const int all = k ? total[1] : total[0], own = k ? mine[1] : mine[0];

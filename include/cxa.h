@@ -307,7 +307,9 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
  *              q_start[B] on are padding: not written, and what they hold changes no
  *              bit of the others).
  *   q_start    device int32 [B + 1]: sequence b owns rows q_start[b] .. q_start[b+1]
- *              (none, if equal); q_start[0] = 0, not decreasing.
+ *              (none, if equal); q_start[0] = 0, not decreasing. Where it decreases,
+ *              attention reports CXA_EINVAL in cxa_device_status, and the rows that two
+ *              sequences share, or all rows, are undefined.
  *   kv_len     device int32 [B]: keys of each sequence, its new tokens included; its
  *              last new token has position kv_len[b] - 1. A new token of negative
  *              position (kv_len less than the new tokens) is not appended and its
@@ -557,9 +559,9 @@ CXA_API unsigned long long cxa_launch_count(void);
  * Read the device-side status word of the current device: 0, or CXA_ETIMEOUT
  * when a kernel's bounded wait expired since the word was last cleared (the
  * kernel then skipped its remaining work), or CXA_EPAGE when a paged call met a
- * page number outside its pool. Synchronises the device. clear != 0
- * takes back what is returned; where both happened, CXA_ETIMEOUT comes first and CXA_EPAGE
- * with the next call. Returns CXA_ECUDA if the word cannot be read. After a
+ * page number outside its pool, or CXA_EINVAL when one met a q_start that decreases.
+ * Synchronises the device. clear != 0 takes back what is returned; where several happened,
+ * they come in this order, one a call. Returns CXA_ECUDA if the word cannot be read. After a
  * timeout, the counters of a decode or paged attention workspace must be zeroed
  * again before reuse (a Python PagedCache drops its own with drop_workspaces()).
  */

@@ -932,3 +932,33 @@ def test_counters_left_behind_go_with_the_kept_workspaces():
         got = a.attend(stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_starts_that_decrease_are_reported_and_touch_nothing_else(act):
+    """Overlapping sequences, against the contract of q_start: reported, and never more work than
+    can be numbered, however often they repeat."""
+    bt = Batch([40, 3, 30], [300, 100, 90], 16, 4, 2, 64, act, act, pad=6).fill()
+    bt.d["q_start"] = torch.tensor([0, 70, 20, 73], dtype=torch.int32).cuda()
+    out = torch.full((bt.N, 4, 64), 3.0, dtype=DT[act]).cuda()
+    K0, V0 = bt.cache.Kp.clone(), bt.cache.Vp.clone()
+    bt.attend(out=out, max_new=70)
+    assert cxa.cxa_device_status(1) == cxa.CXA_EINVAL
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    assert bool((out[73:] == 3).all()) and torch.equal(bt.cache.Kp, K0) and torch.equal(bt.cache.Vp, V0)
+    bt.d["q_start"] = torch.tensor(bt.starts, dtype=torch.int32).cuda()
+    bt.close(bt.attend())                                     # the workspace is as it was
+
+    # 4096 sequences, every second one of all tokens: 3.2e9 chunks of 64 keys in tiles of 32 rows
+    if act == "bf16":                                         # (items of 256 rows do not come to that many)
+        return
+    n, B = 32768, 4096
+    c = cxa.PagedCache(256, 256, 1, 2, 64, act)
+    q = torch.zeros(n, 2, 64, dtype=DT[act], device="cuda")
+    out = torch.full_like(q, 3.0)
+    starts = torch.tensor([0, n] * (B // 2) + [0], dtype=torch.int32).cuda()
+    kv = torch.full((B,), 65536, dtype=torch.int32).cuda()
+    table = torch.arange(256, dtype=torch.int32).cuda().expand(B, 256).contiguous()
+    c.attend(0, q, starts, kv, table, max_new=n, out=out)
+    assert cxa.cxa_device_status(1) == cxa.CXA_EINVAL
+    assert bool((out == 3).all())
