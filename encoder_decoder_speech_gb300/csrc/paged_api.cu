@@ -99,6 +99,7 @@ int check_batch(const std::string& w, const cxa_pages* pages, int layer, int B, 
   if (layer < 0 || layer >= pages->L) return fail(CXA_EINVAL, w + ": layer out of range");
   if (B < 1 || n_tokens < 0 || max_pages < 1)
     return fail(CXA_EINVAL, w + ": B and max_pages must be positive, n_tokens not negative");
+  if (B > 1 << 30) return fail(CXA_EINVAL, w + ": B must be at most 2^30");
   if (static_cast<long long>(max_pages) << pages->page_shift > (1LL << 30))
     return fail(CXA_EINVAL, w + ": a table row may span at most 2^30 positions");
   if (q_start == nullptr || kv_len == nullptr || page_table == nullptr)

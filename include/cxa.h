@@ -302,7 +302,7 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
  * input that one run writes and the next reads).
  *
  * The batch, common to the calls below. The new tokens of all sequences are packed:
- *   B          sequences, >= 1.
+ *   B          sequences, 1 .. 2^30.
  *   n_tokens   rows of the packed tensors (at least the batch's new tokens: rows from
  *              q_start[B] on are padding: not written, and what they hold changes no
  *              bit of the others).

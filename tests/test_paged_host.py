@@ -300,3 +300,9 @@ def test_batch_check_does_not_wrap_large_numbers(pages):
         kw[name][i] = v
         with pytest.raises(ValueError, match="32-bit"):
             cxa.cxa_paged_check(pages, 2, 6, **kw, max_pages=3)
+
+
+@pytest.mark.parametrize("call", [append, attention])
+def test_more_sequences_than_kernels_count_are_refused(pages, call):
+    for B in (2 ** 30 + 1, 2 ** 31 - 1):
+        refused(call(pages, B=B, workspace=0) if call is attention else call(pages, B=B), "at most 2^30")
