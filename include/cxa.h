@@ -449,7 +449,7 @@ CXA_API size_t cxa_paged_attention_workspace_bytes(int Hq, int Hkv, int dh, int 
  *              may then differ by their rounding).
  *   q, out     [n_tokens][Hq][dh] of dtype; their spans, first row to last, must not
  *              overlap.
- *   scale      a value <= 0 selects 1/sqrt(dh).
+ *   scale      a value <= 0 selects 1/sqrt(dh); log2(e) times it must be finite in fp32.
  *   workspace  at least cxa_paged_attention_workspace_bytes(Hq, Hkv, dh, max_new) bytes,
  *              256-byte aligned, its first CXA_PAGED_COUNTER_BYTES zero before the
  *              first call on a new buffer (cudaMemset); calls leave them zero, so that
