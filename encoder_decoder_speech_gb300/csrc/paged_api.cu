@@ -415,7 +415,8 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     if (max_new < 1) return fail(CXA_EINVAL, w + ": max_new must be positive");
     if (static_cast<long long>(n_tokens) * (Hq / pages->Hkv) > 0x7FFFFFFFLL - 256)
       return fail(CXA_EINVAL, w + ": too many query rows");
-    if (!std::isfinite(scale * 1.4426950408889634f)) return fail(CXA_EINVAL, w + ": scale must be finite, log2(e) times it too");
+    if (!std::isfinite(scale) || (scale > 0.f && !std::isfinite(scale * 1.4426950408889634f)))
+      return fail(CXA_EINVAL, w + ": scale must be finite, log2(e) times it too");
     if (n_tokens == 0) return CXA_OK;
     rc = check_rows(w, "q", q, q_stride, n_tokens, Hq, pages->dh, dtype);
     if (rc == CXA_OK) rc = check_rows(w, "out", out, o_stride, n_tokens, Hq, pages->dh, dtype);
