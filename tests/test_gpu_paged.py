@@ -962,3 +962,42 @@ def test_starts_that_decrease_are_reported_and_touch_nothing_else(act):
     c.attend(0, q, starts, kv, table, max_new=n, out=out)
     assert cxa.cxa_device_status(1) == cxa.CXA_EINVAL
     assert bool((out == 3).all())
+
+
+def test_chunks_on_streams_and_in_graphs_at_once():
+    """The two kernels of a call on several streams, eager and replayed, each with its own scratch."""
+    bts = [Batch([200, 1, 33], [9000, 3000, 500], 64, 5, 1, dh, "bf16", "bf16", seed=s).fill() for s, dh in ((1, 64), (2, 128))]
+    want = [bt.attend() for bt in bts]
+    qs = [bt.q.cuda() for bt in bts]
+    call = lambda i, **kw: bts[i].cache.attend(0, qs[i], **bts[i].d, max_new=200, **kw)
+    graphs, outs = [], []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs += [(i, call(i)) for _ in range(3)]
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+            with torch.cuda.stream(streams[2 + i]):
+                outs.append((i, call(i)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in outs)
+
+
+@pytest.mark.parametrize("act,pool", TYPES)
+@pytest.mark.parametrize("n", [1, 7, 90])
+def test_sequences_share_the_pages_of_a_prefix(act, pool, n):
+    """Three sequences whose tables begin with the same pages; their own pages follow."""
+    page, prefix, own = 16, 160, [0, 33, 100]
+    bt = Batch([n] * 3, [prefix + n + x for x in own], page, 4, 2, 64, act, pool)
+    for b in (1, 2):
+        bt.K[b][:prefix], bt.V[b][:prefix] = bt.K[0][:prefix], bt.V[0][:prefix]
+        bt.table[b, :prefix // page] = bt.table[0, :prefix // page]
+    bt.d["page_table"] = bt.table.cuda()
+    bt.fill()
+    bt.cache.check(bt.d["q_start"].cpu(), bt.d["kv_len"].cpu(), bt.table, bt.N)
+    bt.close(bt.attend())
