@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = 0.f;
           c0 = c;
           if (r == 0 && hf == 0) sm->acc[t] = 0;
+          __syncwarp();       // (without it 323 us against 319 for 2048 tokens over 32768 keys)
         }
         // The chunks that every row of the item sees, but for the tile's last, in a loop of
         // their own: the code between two of them is fetched anew for each by every warp.
