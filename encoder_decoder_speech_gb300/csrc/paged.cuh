@@ -117,7 +117,11 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& a, const DeviceInfo& dev, cud
 
 // Attention, one kernel or two: sequences of up to kFewRows query rows a K/V head go to
 // paged_rows.cu, the others, where paged_tile_takes(), to paged_tile.cu; the first kernel
-// takes all of them otherwise.
+// takes all of them otherwise. Both sides of the border, in us for 16 sequences, 8 K/V heads of
+// 64 channels, bf16 (few-rows kernel / tile kernel): over 32768 keys 16 rows 173 / 247, 20 rows
+// 323 / 249, 64 rows 637 / 248; 128 channels 326 / 436, 630 / 439, 1216 / 438: from 17 rows on the
+// few-rows kernel reads the keys once more. Over 1024 keys, which L2 holds, it stays ahead to some
+// 40 rows (25 / 27; 128 channels 32 rows 29 / 34), one sequence over 32768 keys to 40 (37 / 41).
 constexpr int kFewRows = 16;
 // The workspace: both kernels' arrival counters, at places that no argument moves (so that calls
 // of different shapes may share it), then the partial states of the first and of the second.

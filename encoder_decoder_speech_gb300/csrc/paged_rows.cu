@@ -22,7 +22,7 @@
 //
 // Rounding: fp32 values enter the products as sums of three bf16 parts (8 + 8 + 8 bits,
 // by truncation, so exactly), of whose products the six largest are taken: what is left
-// out is below 2^-22 of a term. With bf16 tensors q, K and V are exact as they are and the
+// out (second by third part both ways, third by third) is below 2^-21 of a term. With bf16 tensors q, K and V are exact as they are and the
 // probabilities keep two parts (16 bits), which leaves the output's own rounding as the
 // only one that shows. Sums, references and accumulators are fp32. The products round their
 // running sums towards zero; in fp32, where that would show (2e-6 of the result after 100

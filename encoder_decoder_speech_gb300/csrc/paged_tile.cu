@@ -30,11 +30,11 @@
 // A tile whose last token sees fewer keys than its neighbour's leaves the item's last chunks
 // out (its softmax warps then hand the K and V tiles back).
 //
-// Measured: 2048 tokens over 32768 keys of 20 heads of 64 channels 318 us, 1045 TFLOP/s, with
-// 128 channels 505 us, 1320 TFLOP/s. Bound by the chain of a tile's steps, some 2250 clocks a
+// Measured: 2048 tokens over 32768 keys of 20 heads of 64 channels 319 us, 1040 TFLOP/s, with
+// 128 channels 505 to 520 us, 1290 to 1320 TFLOP/s. Bound by the chain of a tile's steps, some 2250 clocks a
 // chunk of 128 keys for the two tiles: scores, read, exponentials (1024 clocks of the SM's
 // units for the two tiles), conversion, P.V (the products of both: 1045 clocks), each handing
-// over through a barrier (some 250 clocks there and back). Tensor pipe 45 %, exponentials
+// over through a barrier (some 250 clocks there and back). Tensor pipe 43 %, exponentials
 // 45 %, issue 62 % busy. A barrier order that sends the tiles in turns, and a start of one half
 // a chunk behind the other, gained nothing. Tensor memory: S, P and O side by side in 256
 // columns a tile.

@@ -2,7 +2,7 @@
 //
 // A work item is a tile of query rows of one (sequence, K/V head): the rows are the
 // sequence's new tokens times the G query heads of the K/V head, token by token. Its cost
-// is its number of 64- or 128-key chunks, the causal limit of its last token deciding how
+// is its number of chunks of 64 to 256 keys, the causal limit of its last token deciding how
 // many there are; an item without a visible key counts one chunk, in which its rows are
 // written as zeros. All chunks of all items are numbered densely, in the order (sequence,
 // head, tile, chunk), and block c of the grid takes the numbers [c * per, (c + 1) * per):

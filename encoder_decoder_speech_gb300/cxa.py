@@ -669,7 +669,8 @@ _SCALINGS = {"none": CXA_ROTARY_PLAIN, "linear": CXA_ROTARY_LINEAR, "ntk": CXA_R
 class Rotary:
     """A position rotation of the first ``rot_dim`` channels of a head (cxa_rotary): layout
     "half" pairs channels (i, i + rot_dim / 2), "interleaved" (2i, 2i + 1); scaling "none",
-    "linear", "ntk" or "wavelength" for contexts longer than the trained one. ``freq``
+    "linear", "ntk" or "wavelength" (the YaRN paper's ramp in turns; checkpoints that ramp by
+    pair number pass ``freq``) for contexts longer than the trained one. ``freq``
     (rot_dim / 2 radians a position) replaces the frequencies that base and scaling give,
     ``attn_factor`` the factor of the rotated values."""
 
@@ -704,7 +705,8 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
                  q_out=None, k_out=None, stream=None):
     """Head norms (RMS, if norm_eps is given) and rotation of q [N, Hq, dh] and k [N, Hk, dh]
     (or None), float32 or bfloat16, at positions pos [N] int32. Token rows may be strided
-    slices; q_out and k_out may be q and k. Returns (q_out, k_out)."""
+    slices; q_out and k_out may be q and k. Without norm_eps, or without k for k's, weights
+    have no effect. Returns (q_out, k_out)."""
     tc = _torch_calls or _calls()
     n, Hq = _heads("q", q)
     dh, dt, at = q.shape[2], q.dtype, q.get_device()
@@ -807,8 +809,9 @@ class PagedCache:
     def append(self, layer: int, k, v, q_start, kv_len, page_table, q=None, q_out=None, rotary: Rotary | None = None,
                norm_eps: float | None = None, q_weight=None, k_weight=None, stream=None):
         """Write k, v [N, Hkv, dh] of the new tokens into their pages, k normalised (RMS, if
-        norm_eps is given) and rotated; with q [N, Hq, dh] also return q_out, the queries
-        normalised and rotated (rows behind the batch's last token are left as they are)."""
+        norm_eps is given: without it weights have no effect) and rotated; with q [N, Hq, dh]
+        also return q_out, the queries normalised and rotated (rows behind the batch's last
+        token are left as they are)."""
         tc = _torch_calls or _calls()
         at, dh, dt, n = self._at, self.dh, k.dtype, _heads("k", k)[0]
         B, width = self._batch(q_start, kv_len, page_table, tc.i32)

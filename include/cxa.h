@@ -350,7 +350,9 @@ CXA_API int cxa_self_attention_step(cxa_cache* c, const int* pos, const float* Q
 #define CXA_ROTARY_WAVELENGTH  3    /* by the turns a pair makes in orig_len positions (the
                                        YaRN paper's rule): as they are from beta turns up,
                                        divided by factor from alpha down, linear between;
-                                       attn_factor = 0.1 ln(factor) + 1 */
+                                       attn_factor = 0.1 ln(factor) + 1. Checkpoints that
+                                       ramp by pair number between rounded limits need
+                                       frequencies of the caller's (cxa_rotary_create) */
 
 typedef struct cxa_rotary cxa_rotary;
 
@@ -383,7 +385,9 @@ CXA_API void cxa_rotary_destroy(cxa_rotary* r);
  *              (and may be NULL). dh 64 or 128.
  *   pos        device int32 [n_tokens]; any value, negative ones included.
  *   norm       CXA_NORM_NONE or CXA_NORM_RMS, before the rotation; eps >= 0;
- *              q_weight, k_weight device fp32 [dh] or NULL (1).
+ *              q_weight, k_weight device fp32 [dh] or NULL (1). Without a norm, or for
+ *              a tensor that is not given, a weight has no effect. Squares are summed in
+ *              fp32: channels up to some 2^60 in magnitude.
  *   rot        NULL for no rotation.
  *   q_out, k_out  may be q and k (in place, with the same stride); any other
  *              overlap is the caller's to avoid.
