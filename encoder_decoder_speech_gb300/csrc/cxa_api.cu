@@ -75,12 +75,14 @@ cudaError_t current_device_info(DeviceInfo* info, std::string* msg) {
     *msg = "cudaGetDevice";
     return e;
   }
-  // A thread's first call: make the device's context current in it. Launches would do that, but
-  // tensor maps are encoded by the driver before a call's first launch, and need it.
+  // A thread's first call: make a context current in it, if none is. Launches would do that, but
+  // tensor maps are encoded by the driver before a call's first launch, and need it. (cudaSetDevice
+  // would take the thread out of a context of its own.)
   static thread_local int bound = -1;
   if (bound != dev) {
-    if ((e = cudaSetDevice(dev)) != cudaSuccess) {
-      *msg = "cudaSetDevice";
+    void* any = nullptr;
+    if ((e = cudaGetSymbolAddress(&any, g_cxa_status_word)) != cudaSuccess) {
+      *msg = "cudaGetSymbolAddress(status word)";
       return e;
     }
     bound = dev;
