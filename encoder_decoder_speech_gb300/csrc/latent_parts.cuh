@@ -1,0 +1,40 @@
+// What the two kernels of the latent attention leave for the merge of items that were cut between
+// blocks, and the workspace that holds it.
+//
+// Work is dealt out as in paged_work.cuh. An item cut by a block boundary leaves one partial state
+// per block that holds a part of it: block c's slot 2c if the item began before its range, 2c + 1 if
+// it goes on behind. The block in which a cut item begins says so in cut[c]; a second kernel merges
+// the parts, whose rows and channels it deals out over the whole GPU. (Merging in the last block to
+// arrive, as the few-rows kernel of the K/V pages does, would leave one block with 64 rows of 512
+// channels of up to 152 parts: 20 MB.)
+#pragma once
+
+#include "latent.cuh"
+
+namespace cxa {
+
+constexpr int kLatentMaxBlocks = 160;
+
+struct LatentCut {
+  int q0, rt, parts, rows;     // of the item: first token row, tile, parts (0: none), rows of the tile
+};
+
+constexpr size_t kLatentCutBytes = kLatentMaxBlocks * sizeof(LatentCut);
+static_assert(kLatentCutBytes % 256 == 0, "the partial states behind are aligned");
+
+// A partial state: [R][latent] sums, then R references (base 2) and R sums of weights.
+__host__ __device__ constexpr size_t latent_slot(int R, int latent) { return static_cast<size_t>(R) * (latent + 2); }
+
+inline size_t latent_parts_bytes(int R, int latent) {
+  return kLatentCutBytes + 2 * static_cast<size_t>(kLatentMaxBlocks) * latent_slot(R, latent) * 4;
+}
+
+// Enqueues the merge behind a kernel of `blocks` blocks (latent_merge.cu).
+cudaError_t launch_latent_merge(const LatentAttnLaunch& a, int R, int blocks, const DeviceInfo& dev,
+                                cudaStream_t stream);
+
+// latent_rows.cu: fp32; latent_tile.cu: bf16.
+constexpr int kLatentRowsF32 = 16;
+cudaError_t launch_latent_rows(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+
+}  // namespace cxa

@@ -100,6 +100,38 @@ SIGNATURES = {
                                            ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
                                            ctypes.c_longlong, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
                                            ctypes.c_size_t, ctypes.c_void_p]),
+    "cxa_latent_create": (ctypes.c_int, [_c_void_pp, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "cxa_latent_destroy": (None, [ctypes.c_void_p]),
+    "cxa_latent_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int]),
+    "cxa_latent_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                         ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int,
+                                         ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p]),
+    "cxa_latent_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "cxa_latent_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.c_longlong, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.c_size_t, ctypes.c_void_p]),
+    "cxa_latent_expand": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]),
+    "cxa_paged_weights_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "cxa_paged_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
+                                         ctypes.c_float, ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
+                                         ctypes.c_void_p]),
+    "cxa_paged_evict": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "cxa_paged_evict_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int]),
 }
 
 # most query rows cxa_decode_shared takes per cache row (CXA_MAX_SHARED_QUERIES)
@@ -349,6 +381,85 @@ def cxa_paged_attention(handle, layer, B, n_tokens, max_new, q_start, kv_len, pa
     return load().cxa_paged_attention(handle, layer, B, n_tokens, max_new, _ptr(q_start), _ptr(kv_len),
                                       _ptr(page_table), max_pages, _ptr(q), q_stride, Hq, _ptr(out), o_stride, scale,
                                       dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def _host_ints(*lists):
+    """C arrays of the lists' numbers, which 32 bits have to hold."""
+    out = []
+    for x in lists:
+        x = [int(v) for v in x]
+        if any(v < -2 ** 31 or v >= 2 ** 31 for v in x):
+            raise ValueError("lengths and page tables must hold 32-bit integers")
+        out.append((ctypes.c_int * max(len(x), 1))(*x))
+    return out
+
+
+def cxa_latent_create(Cp, num_pages, page_size, L, latent, rope, cache_dtype):
+    """Returns (status, handle); handle is None unless status == CXA_OK."""
+    h = ctypes.c_void_p()
+    rc = load().cxa_latent_create(ctypes.byref(h), _ptr(Cp), num_pages, page_size, L, latent, rope, cache_dtype)
+    return rc, (h.value if rc == CXA_OK else None)
+
+
+def cxa_latent_destroy(handle) -> None:
+    load().cxa_latent_destroy(handle)
+
+
+def cxa_latent_check(handle, B, n_tokens, q_start, kv_len, page_table, max_pages) -> int:
+    """q_start [B + 1], kv_len [B], page_table [B * max_pages]: host sequences of ints."""
+    if len(q_start) != B + 1 or len(kv_len) != B or len(page_table) != B * max_pages:
+        raise ValueError("q_start, kv_len and page_table must have B + 1, B and B * max_pages entries")
+    return load().cxa_latent_check(handle, B, n_tokens, *_host_ints(q_start, kv_len, page_table), max_pages)
+
+
+def cxa_latent_append(handle, layer, B, n_tokens, q_start, kv_len, page_table, max_pages, c, c_stride, kr, kr_stride,
+                      norm, eps, weight, rot, dtype, stream=None) -> int:
+    return load().cxa_latent_append(handle, layer, B, n_tokens, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                    max_pages, _ptr(c), c_stride, _ptr(kr), kr_stride, norm, eps, _ptr(weight), rot,
+                                    dtype, _stream(stream))
+
+
+def cxa_latent_attention_workspace_bytes(H, latent, max_new, dtype) -> int:
+    return load().cxa_latent_attention_workspace_bytes(H, latent, max_new, dtype)
+
+
+def cxa_latent_attention(handle, layer, B, n_tokens, max_new, q_start, kv_len, page_table, max_pages, q, q_stride, H,
+                         out, o_stride, scale, dtype, workspace, workspace_bytes, stream=None) -> int:
+    return load().cxa_latent_attention(handle, layer, B, n_tokens, max_new, _ptr(q_start), _ptr(kv_len),
+                                       _ptr(page_table), max_pages, _ptr(q), q_stride, H, _ptr(out), o_stride, scale,
+                                       dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def cxa_latent_expand(handle, layer, to, to_layer, B, from_, kv_len, page_table, max_pages, to_table, to_max_pages, WK,
+                      WV, stream=None) -> int:
+    return load().cxa_latent_expand(handle, layer, to, to_layer, B, _ptr(from_), _ptr(kv_len), _ptr(page_table),
+                                    max_pages, _ptr(to_table), to_max_pages, _ptr(WK), _ptr(WV), _stream(stream))
+
+
+def cxa_paged_weights_workspace_bytes(n_tokens, Hq, Hkv, dh, max_new, dtype) -> int:
+    return load().cxa_paged_weights_workspace_bytes(n_tokens, Hq, Hkv, dh, max_new, dtype)
+
+
+def cxa_paged_weights(handle, layer, B, n_tokens, max_new, q_start, kv_len, page_table, max_pages, q, q_stride, Hq,
+                      weights, decay, scale, dtype, workspace, workspace_bytes, stream=None) -> int:
+    return load().cxa_paged_weights(handle, layer, B, n_tokens, max_new, _ptr(q_start), _ptr(kv_len),
+                                    _ptr(page_table), max_pages, _ptr(q), q_stride, Hq, _ptr(weights), decay, scale,
+                                    dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def cxa_paged_evict(handle, l0, nl, weights, B, keep, first, recent, kv_len, page_table, max_pages, out_table,
+                    out_max_pages, kept, out_len, stream=None) -> int:
+    return load().cxa_paged_evict(handle, l0, nl, _ptr(weights), B, keep, first, recent, _ptr(kv_len),
+                                  _ptr(page_table), max_pages, _ptr(out_table), out_max_pages, _ptr(kept),
+                                  _ptr(out_len), _stream(stream))
+
+
+def cxa_paged_evict_check(handle, B, keep, kv_len, page_table, max_pages, out_table, out_max_pages) -> int:
+    """kv_len [B], page_table [B * max_pages], out_table [B * out_max_pages]: host sequences of ints."""
+    if len(kv_len) != B or len(page_table) != B * max_pages or len(out_table) != B * out_max_pages:
+        raise ValueError("kv_len and the tables must have B, B * max_pages and B * out_max_pages entries")
+    kv_len, page_table, out_table = _host_ints(kv_len, page_table, out_table)
+    return load().cxa_paged_evict_check(handle, B, keep, kv_len, page_table, max_pages, out_table, out_max_pages)
 
 
 def cxa_invalidate(handle, b=-1) -> int:
@@ -652,13 +763,18 @@ def _own_handle(raw, what):
                          "another stream")
 
 
-def _new(tc, q, stream, index):
-    """An empty tensor like q for the result of a call on `stream`, in that stream's memory."""
+def _empty(tc, like, shape, dtype, stream, index):
+    """An empty tensor for the result of a call on `stream`, in that stream's memory."""
     if stream is None:
-        return q.new_empty(q.shape)
+        return like.new_empty(shape, dtype=dtype)
     _own_handle(_stream(stream), "the tensors for the results")
     with tc.torch.cuda.stream(tc.torch.cuda.ExternalStream(_stream(stream), device=index)):
-        return q.new_empty(q.shape)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _new(tc, q, stream, index):
+    """An empty tensor like q for the result of a call on `stream`, in that stream's memory."""
+    return _empty(tc, q, q.shape, q.dtype, stream, index)
 
 
 _LAYOUTS = {"half": CXA_ROTARY_HALF, "interleaved": CXA_ROTARY_INTERLEAVED}
@@ -738,30 +854,11 @@ def qk_norm_rope(q, k, pos, rotary: Rotary | None = None, norm_eps: float | None
     return q_out, k_out
 
 
-class PagedCache:
-    """Owns a [L][num_pages][Hkv][page_size][dh] pool of K/V pages (``Kp``, ``Vp``, zeroed),
-    its descriptor, and the attention's workspaces: one per stream, so that calls on
-    different streams do not share one (of more than 64 the oldest are dropped; a stream's
-    calls must be done before it is destroyed, as its handle may come back as another's).
-    Calls on a thread's own default stream (cudaStreamPerThread) need a workspace and an
-    out of the caller's. The batch of a call is q_start [B + 1], kv_len [B]
-    and page_table [B, max_pages], int32 on the device (see include/cxa.h)."""
+class _Paged:
+    """What the paged caches share: a batch's checks, and the workspaces, one per stream."""
 
     KEPT_WORKSPACES = 64
-
-    def __init__(self, num_pages: int, page_size: int, L: int, Hkv: int, dh: int = 64, cache_dtype: str = "bf16",
-                 device="cuda"):
-        import torch
-        self.handle = None
-        self.num_pages, self.page_size, self.L, self.Hkv, self.dh = num_pages, page_size, L, Hkv, dh
-        self.cache_dtype = cache_dtype
-        tdt = torch.float32 if _DTYPES[cache_dtype] == CXA_F32 else torch.bfloat16
-        self.Kp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
-        self.Vp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
-        self._ws, self._ws_bytes = {}, {}
-        self._at = self.Kp.get_device()
-        rc, self.handle = cxa_pages_create(self.Kp, self.Vp, num_pages, page_size, L, Hkv, dh, _DTYPES[cache_dtype])
-        check(rc, "cxa_pages_create")
+    _cleared = 0               # bytes at a workspace's start that must be zero before its first use
 
     def _batch(self, q_start, kv_len, page_table, i32):
         shape, at = page_table.shape, self._at
@@ -775,14 +872,24 @@ class PagedCache:
         _ints("page_table", page_table, shape, at, i32)
         return B, shape[1]
 
-    def _scratch(self, tc, Hq, max_new, stream, raw):
-        """The workspace of a call on the stream with handle raw: the tensor, its address and bytes."""
-        need = self._ws_bytes.get((Hq, max_new))
+    def _table(self, name, table, B, i32):
+        shape = table.shape
+        if len(shape) != 2 or shape[0] != B:
+            raise ValueError(f"{name} must be [{B} sequences, pages]")
+        _ints(name, table, shape, self._at, i32)
+        return shape[1]
+
+    def _need(self, key, size):
+        """The bytes that size(*key) gives, looked up if they have been asked for."""
+        need = self._ws_bytes.get(key)
         if need is None:
             if len(self._ws_bytes) > 4096:
                 self._ws_bytes.clear()
-            need = cxa_paged_attention_workspace_bytes(Hq, self.Hkv, self.dh, max_new)
-            self._ws_bytes[Hq, max_new] = need
+            need = self._ws_bytes[key] = size(*key)
+        return need
+
+    def _kept(self, tc, need, stream, raw):
+        """The workspace of a call on the stream with handle raw: the tensor, its address and bytes."""
         _own_handle(raw, "a workspace")
         kept = self._ws.get(raw)
         capturing = _capturing(tc, self._at, stream, raw)
@@ -790,8 +897,9 @@ class PagedCache:
             return kept
         torch = tc.torch
         with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=self._at)):
-            ws = torch.empty(max(need, CXA_PAGED_COUNTER_BYTES), dtype=torch.uint8, device=self.Kp.device)
-            ws[:CXA_PAGED_COUNTER_BYTES].zero_()
+            ws = torch.empty(max(need, self._cleared, 256), dtype=torch.uint8, device=self._pool.device)
+            if self._cleared:
+                ws[:self._cleared].zero_()
         new = (ws, ws.data_ptr(), ws.numel())
         if not capturing:
             self._ws.pop(raw, None)
@@ -799,6 +907,47 @@ class PagedCache:
             while len(self._ws) > self.KEPT_WORKSPACES:
                 self._ws.pop(next(iter(self._ws), None), None)     # its memory goes back to its stream's
         return new
+
+    def _given(self, workspace):
+        if workspace.get_device() != self._at or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{self._at}")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+    def drop_workspaces(self) -> None:
+        """Give the kept workspaces back: the next calls get new ones, with counters of zero. To be
+        called after a CXA_ETIMEOUT, which may leave counters behind."""
+        self._ws.clear()
+
+
+class PagedCache(_Paged):
+    """Owns a [L][num_pages][Hkv][page_size][dh] pool of K/V pages (``Kp``, ``Vp``, zeroed),
+    its descriptor, and the attention's workspaces: one per stream, so that calls on
+    different streams do not share one (of more than 64 the oldest are dropped; a stream's
+    calls must be done before it is destroyed, as its handle may come back as another's).
+    Calls on a thread's own default stream (cudaStreamPerThread) need a workspace and an
+    out of the caller's. The batch of a call is q_start [B + 1], kv_len [B]
+    and page_table [B, max_pages], int32 on the device (see include/cxa.h)."""
+
+    _cleared = CXA_PAGED_COUNTER_BYTES
+
+    def __init__(self, num_pages: int, page_size: int, L: int, Hkv: int, dh: int = 64, cache_dtype: str = "bf16",
+                 device="cuda"):
+        import torch
+        self.handle = None
+        self.num_pages, self.page_size, self.L, self.Hkv, self.dh = num_pages, page_size, L, Hkv, dh
+        self.cache_dtype = cache_dtype
+        tdt = torch.float32 if _DTYPES[cache_dtype] == CXA_F32 else torch.bfloat16
+        self.Kp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
+        self.Vp = torch.zeros((L, num_pages, Hkv, page_size, dh), dtype=tdt, device=device)
+        self._ws, self._ws_bytes, self._pool = {}, {}, self.Kp
+        self._at = self.Kp.get_device()
+        rc, self.handle = cxa_pages_create(self.Kp, self.Vp, num_pages, page_size, L, Hkv, dh, _DTYPES[cache_dtype])
+        check(rc, "cxa_pages_create")
+
+    def _scratch(self, tc, Hq, max_new, stream, raw):
+        """The attention's workspace on the stream with handle raw."""
+        need = self._need((Hq, self.Hkv, self.dh, max_new), cxa_paged_attention_workspace_bytes)
+        return self._kept(tc, need, stream, raw)
 
     def workspace(self, Hq: int, max_new: int, stream=None):
         """An attention workspace (its counters zeroed), kept per stream. While a graph is captured
@@ -854,9 +1003,7 @@ class PagedCache:
         if workspace is None:
             ws = self._scratch(tc, Hq, max_new, stream, raw)
         else:
-            if workspace.get_device() != at or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous tensor on cuda:{at}")
-            ws = workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            ws = self._given(workspace)
         _run(tc, at, "cxa_paged_attention", load().cxa_paged_attention, (
             self.handle, layer, B, n, max_new, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
             q.data_ptr(), qs, Hq, out.data_ptr(), os_, scale, _code(tc, dt), ws[1], ws[2], raw))
@@ -867,14 +1014,198 @@ class PagedCache:
         check(cxa_paged_check(self.handle, page_table.shape[0], n_tokens, q_start.tolist(), kv_len.tolist(),
                               page_table.reshape(-1).tolist(), page_table.shape[1]), "cxa_paged_check")
 
-    def drop_workspaces(self) -> None:
-        """Give the kept workspaces back: the next calls get new ones, with counters of zero. To be
-        called after a CXA_ETIMEOUT, which may leave counters behind."""
-        self._ws.clear()
+    def new_weights(self):
+        """Room for the attention weight that every key of the pool gathers (zeros, float32)."""
+        return self.Kp.new_zeros((self.L, self.num_pages, self.Hkv, self.page_size), dtype=_calls().f32)
+
+    def _weights(self, weights, f32):
+        shape = (self.L, self.num_pages, self.Hkv, self.page_size)
+        if weights.dtype is not f32 or weights.shape != shape or weights.get_device() != self._at or \
+                not weights.is_contiguous():
+            raise ValueError(f"weights must be a contiguous float32 tensor of shape {shape} on cuda:{self._at}")
+        return weights.data_ptr()
+
+    def accumulate(self, layer: int, q, q_start, kv_len, page_table, max_new: int, weights, decay: float = 1.0,
+                   scale: float = 0.0, workspace=None, stream=None):
+        """Add to weights (new_weights()) the attention weight that the new tokens' queries q
+        [N, Hq, dh], of the pool's type, give each key, over the query heads of its K/V head; what it
+        had gathered before counts decay times, and new tokens' entries start at zero. No page may be two
+        sequences' of the batch. max_new and workspace as for attend. Returns weights."""
+        tc = _torch_calls or _calls()
+        at, dh, dt = self._at, self.dh, q.dtype
+        B, width = self._batch(q_start, kv_len, page_table, tc.i32)
+        n, Hq = _heads("q", q)
+        qs = _rows("q", q, Hq, dh, n, dt, at)
+        wp, code = self._weights(weights, tc.f32), _code(tc, dt)
+        raw = tc.stream(at) if stream is None else _stream(stream)
+        if workspace is None:
+            need = self._need((n, Hq, self.Hkv, dh, max_new, code), cxa_paged_weights_workspace_bytes)
+            ws = self._kept(tc, need, stream, raw)
+        else:
+            ws = self._given(workspace)
+        _run(tc, at, "cxa_paged_weights", load().cxa_paged_weights, (
+            self.handle, layer, B, n, max_new, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
+            q.data_ptr(), qs, Hq, wp, decay, scale, code, ws[1], ws[2], raw))
+        return weights
+
+    def evict(self, weights, keep: int, kv_len, page_table, out_table, first: int = 0, recent: int = 0, l0: int = 0,
+              nl: int | None = None, kept=None, out_len=None, stream=None):
+        """Let min(keep, kv_len) tokens stay of every sequence, layer l0 .. l0 + nl - 1 (default: all
+        from l0 on) and K/V head: the `first` first, the `recent` last, and of the others those that have gathered the
+        largest weights. Their K, V and weights are copied in order into the pages of out_table
+        [B, pages], which no sequence of the call may be reading. Returns (kept [nl, B, Hkv, keep], their old positions and then
+        -1; out_len [B], the new lengths)."""
+        tc = _torch_calls or _calls()
+        at, i32 = self._at, tc.i32
+        if at < 0:
+            raise ValueError("the tensors must be on a CUDA device")
+        if len(page_table.shape) != 2:
+            raise ValueError("page_table must be [sequences, pages]")
+        B = page_table.shape[0]
+        width, out_width = self._table("page_table", page_table, B, i32), self._table("out_table", out_table, B, i32)
+        _ints("kv_len", kv_len, (B,), at, i32)
+        wp = self._weights(weights, tc.f32)
+        if nl is None:
+            nl = self.L - l0
+        if keep < 1 or nl < 1:
+            raise ValueError("keep and nl must be positive")
+        shape = (nl, B, self.Hkv, keep)
+        if kept is None:
+            kept = _empty(tc, kv_len, shape, i32, stream, at)
+        if out_len is None:
+            out_len = _empty(tc, kv_len, (B,), i32, stream, at)
+        _ints("kept", kept, shape, at, i32)
+        _ints("out_len", out_len, (B,), at, i32)
+        _run(tc, at, "cxa_paged_evict", load().cxa_paged_evict, (
+            self.handle, l0, nl, wp, B, keep, first, recent, kv_len.data_ptr(), page_table.data_ptr(), width,
+            out_table.data_ptr(), out_width, kept.data_ptr(), out_len.data_ptr(),
+            tc.stream(at) if stream is None else _stream(stream)))
+        return kept, out_len
+
+    def check_evict(self, keep: int, kv_len, page_table, out_table) -> None:
+        """Raise CxaError if the eviction's batch (host or device tensors) is not sound
+        (cxa_paged_evict_check)."""
+        check(cxa_paged_evict_check(self.handle, page_table.shape[0], keep, kv_len.tolist(),
+                                    page_table.reshape(-1).tolist(), page_table.shape[1],
+                                    out_table.reshape(-1).tolist(), out_table.shape[1]), "cxa_paged_evict_check")
 
     def close(self) -> None:
         if getattr(self, "handle", None):
             cxa_pages_destroy(self.handle)
+            self.handle = None
+            self.drop_workspaces()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LatentCache(_Paged):
+    """Owns a [L][num_pages][page_size][latent + rope] pool (``Cp``, zeroed) of one row a token that all
+    heads share (latent attention: see include/cxa.h), its descriptor, and workspaces as a PagedCache
+    does. latent is 128, 256, 384 or 512, rope 0, 16, 32, 48 or 64; the batch of a call is that of a PagedCache's."""
+
+    def __init__(self, num_pages: int, page_size: int, L: int, latent: int, rope: int = 0, cache_dtype: str = "bf16",
+                 device="cuda"):
+        import torch
+        self.handle = None
+        self.num_pages, self.page_size, self.L, self.latent, self.rope = num_pages, page_size, L, latent, rope
+        self.cache_dtype = cache_dtype
+        tdt = torch.float32 if _DTYPES[cache_dtype] == CXA_F32 else torch.bfloat16
+        self.Cp = torch.zeros((L, num_pages, page_size, latent + rope), dtype=tdt, device=device)
+        self._ws, self._ws_bytes, self._pool = {}, {}, self.Cp
+        self._at = self.Cp.get_device()
+        rc, self.handle = cxa_latent_create(self.Cp, num_pages, page_size, L, latent, rope, _DTYPES[cache_dtype])
+        check(rc, "cxa_latent_create")
+
+    def append(self, layer: int, c, kr, q_start, kv_len, page_table, rotary: Rotary | None = None,
+               norm_eps: float | None = None, weight=None, stream=None) -> None:
+        """Write the new tokens' rows into their pages: c [N, latent], normalised (RMS, if norm_eps is
+        given: without it the weight has no effect), and kr [N, rope] (None where rope is 0), rotated."""
+        tc = _torch_calls or _calls()
+        at, dt = self._at, c.dtype
+        B, width = self._batch(q_start, kv_len, page_table, tc.i32)
+        if len(c.shape) != 2:
+            raise ValueError("c must be [tokens, latent]")
+        n = c.shape[0]
+        cs = _rows("c", c.unsqueeze(1), 1, self.latent, n, dt, at)
+        ks, kp = 0, None
+        if self.rope:
+            if kr is None or len(kr.shape) != 2:
+                raise ValueError("kr must be [tokens, rope]")
+            ks, kp = _rows("kr", kr.unsqueeze(1), 1, self.rope, n, dt, at), kr.data_ptr()
+        elif kr is not None:
+            raise ValueError("kr must be None where rope is 0")
+        norm, eps = (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
+        _run(tc, at, "cxa_latent_append", load().cxa_latent_append, (
+            self.handle, layer, B, n, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
+            c.data_ptr(), cs, kp, ks, norm, eps,
+            None if weight is None else _weight("weight", weight, self.latent, at, tc.f32),
+            None if rotary is None else rotary.handle, _code(tc, dt),
+            tc.stream(at) if stream is None else _stream(stream)))
+
+    def attend(self, layer: int, q, q_start, kv_len, page_table, max_new: int, scale: float, out=None, workspace=None,
+               stream=None):
+        """The absorbed form: attention of the new tokens' queries q [N, H, latent + rope], of the
+        pool's type, over their sequences' rows up to each token's own, whose first `latent` channels are the
+        values. max_new: an upper bound of the new tokens of one sequence; scale > 0. Returns out
+        [N, H, latent] (rows behind the batch's last token are left as they are)."""
+        tc = _torch_calls or _calls()
+        at, dt = self._at, q.dtype
+        B, width = self._batch(q_start, kv_len, page_table, tc.i32)
+        n, H = _heads("q", q)
+        qs = _rows("q", q, H, self.latent + self.rope, n, dt, at)
+        if out is None:
+            out = _empty(tc, q, (n, H, self.latent), dt, stream, at)
+        os_, code = _rows("out", out, H, self.latent, n, dt, at), _code(tc, dt)
+        raw = tc.stream(at) if stream is None else _stream(stream)
+        if workspace is None:
+            ws = self._kept(tc, self._need((H, self.latent, max_new, code), cxa_latent_attention_workspace_bytes),
+                            stream, raw)
+        else:
+            ws = self._given(workspace)
+        _run(tc, at, "cxa_latent_attention", load().cxa_latent_attention, (
+            self.handle, layer, B, n, max_new, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width,
+            q.data_ptr(), qs, H, out.data_ptr(), os_, scale, code, ws[1], ws[2], raw))
+        return out
+
+    def expand(self, layer: int, WK, WV, kv_len, page_table, to: PagedCache, to_layer: int, to_table, start=None,
+               stream=None) -> None:
+        """The expanded form: write K_h = [r | c WK_h] and V_h = c WV_h of positions start[b] (default 0)
+        .. kv_len[b] - 1 of every sequence into layer to_layer of a PagedCache of the same type, at the same
+        positions of to_table's rows; its attend() then reads them. WK [latent, Hkv * (dh - rope)],
+        WV [latent, Hkv * dh] of the pools' type."""
+        tc = _torch_calls or _calls()
+        at, i32, dt = self._at, tc.i32, self.Cp.dtype
+        if at < 0:
+            raise ValueError("the tensors must be on a CUDA device")
+        if len(page_table.shape) != 2:
+            raise ValueError("page_table must be [sequences, pages]")
+        B = page_table.shape[0]
+        width, to_width = self._table("page_table", page_table, B, i32), self._table("to_table", to_table, B, i32)
+        _ints("kv_len", kv_len, (B,), at, i32)
+        if start is not None:
+            _ints("start", start, (B,), at, i32)
+        if to._at != at:
+            raise ValueError(f"both caches must be on cuda:{at}")
+        for name, w, cols in (("WK", WK, to.Hkv * (to.dh - self.rope)), ("WV", WV, to.Hkv * to.dh)):
+            if w.dtype is not dt or w.shape != (self.latent, cols) or w.get_device() != at or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {(self.latent, cols)} on cuda:{at}")
+        _run(tc, at, "cxa_latent_expand", load().cxa_latent_expand, (
+            self.handle, layer, to.handle, to_layer, B, None if start is None else start.data_ptr(),
+            kv_len.data_ptr(), page_table.data_ptr(), width, to_table.data_ptr(), to_width, WK.data_ptr(),
+            WV.data_ptr(), tc.stream(at) if stream is None else _stream(stream)))
+
+    def check(self, q_start, kv_len, page_table, n_tokens: int) -> None:
+        """Raise CxaError if the batch (host or device tensors) is not sound (cxa_latent_check)."""
+        check(cxa_latent_check(self.handle, page_table.shape[0], n_tokens, q_start.tolist(), kv_len.tolist(),
+                               page_table.reshape(-1).tolist(), page_table.shape[1]), "cxa_latent_check")
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            cxa_latent_destroy(self.handle)
             self.handle = None
             self.drop_workspaces()
 

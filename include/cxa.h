@@ -475,6 +475,148 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
                                 int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * How much attention each key of a layer's pages has gathered, for an eviction by it. For every
+ * sequence with new tokens, K/V head h and key position j (< kv_len):
+ *
+ *   weights[j] = (j new: 0, otherwise decay * weights[j])
+ *                + sum over new tokens i that see j, and h's query heads g, of p_ig(j)
+ *
+ * with p_ig = softmax of scale * q_ig . K over the keys that token i sees, as in
+ * cxa_paged_attention. The new tokens' keys are in the pool (append first); their entries need no
+ * clearing. A call may be given some of a prompt's last tokens alone, as the batch's new ones.
+ *
+ *   weights    device fp32 [L][num_pages][Hkv][page_size], 4-byte aligned: one number for each row
+ *              of K. Entries of no key of the batch are left as they are.
+ *   decay      finite, >= 0; with 0 nothing of the old numbers is read into the new.
+ *   workspace  at least cxa_paged_weights_workspace_bytes() bytes, otherwise as for
+ *              cxa_paged_attention, whose workspace may be the same buffer (its first
+ *              CXA_PAGED_COUNTER_BYTES are the same counters).
+ * Pages that two sequences of the batch share must not be given: their entries would be written by
+ * both. Arguments, the limit on the work and errors otherwise as for cxa_paged_attention; dtype is
+ * the pool's. A token that sees an infinity or a NaN in q or K may make the weights of all keys that
+ * it sees NaN. Results do not change from call to call.
+ */
+CXA_API size_t cxa_paged_weights_workspace_bytes(int n_tokens, int Hq, int Hkv, int dh, int max_new, int dtype);
+
+CXA_API int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
+                              const int* kv_len, const int* page_table, int max_pages, const void* q,
+                              long long q_stride, int Hq, float* weights, float decay, float scale, int dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction: of every sequence, layer in [l0, l0 + nl) and K/V head, min(keep, kv_len) tokens stay:
+ * the first `first`, the last `recent`, and of the others those of the largest weights (of equal
+ * ones the earlier; -0 counts as 0, a NaN below everything). Their rows of K, V and weights are copied, in
+ * the order of their positions, into the pages of out_table: positions 0 .. min(keep, kv_len) - 1 of
+ * a shorter sequence. What is copied is not changed, so keys keep the rotation of their old
+ * positions; new tokens are rotated by cxa_qk_norm_rope at positions that the caller counts on,
+ * and appended without a rotation.
+ *
+ *   keep       >= 1, first + recent <= keep.
+ *   kv_len     device int32 [B], page_table device int32 [B][max_pages]: the sequences as they are.
+ *   out_table  device int32 [B][out_max_pages]: pages that no sequence of the call reads, each
+ *              once (cxa_paged_evict_check); room for min(keep, max_pages * page_size) positions.
+ *   kept       device int32 [nl][B][Hkv][keep]: the old positions of what stays, ascending, then -1.
+ *   out_len    device int32 [B], not kv_len: min(keep, kv_len).
+ * Rows of the destination behind the last one are left as they are. Two kernels.
+ */
+CXA_API int cxa_paged_evict(const cxa_pages* pages, int l0, int nl, float* weights, int B, int keep, int first,
+                            int recent, const int* kv_len, const int* page_table, int max_pages,
+                            const int* out_table, int out_max_pages, int* kept, int* out_len, void* stream);
+
+/*
+ * Check an eviction's batch on the HOST (kv_len and both tables are host arrays here): CXA_EINVAL if
+ * kv_len is negative or passes its row, a needed page is not in the pool, or a page of out_table that is
+ * written is read by a sequence of the batch or written twice. Host only.
+ */
+CXA_API int cxa_paged_evict_check(const cxa_pages* pages, int B, int keep, const int* kv_len, const int* page_table,
+                                  int max_pages, const int* out_table, int out_max_pages);
+
+/*
+ * Latent attention: a cache of one vector a token that all heads share, in place of K and V of
+ * every head. With c_t [latent] the token's latent vector, r_t [rope] its rotated part (rope may be
+ * 0), and a head's projections WK_h [latent][dh - rope] and WV_h [latent][dh],
+ *
+ *   K_h(t) = [ r_t | c_t WK_h ],   V_h(t) = c_t WV_h
+ *
+ * (the rotated channels of a head come first, as in a rotation of part of a head). There are two
+ * ways to the same attention:
+ *   absorbed   q' = [ q_nope WK_h^T | q_rope ] against the rows [ c_t | r_t ] themselves, which are
+ *              key and, in their first `latent` channels, value: cxa_latent_attention; WV_h goes
+ *              behind the result. For single tokens and few: a token's row is read once for
+ *              all heads.
+ *   expanded   cxa_latent_expand writes K_h and V_h into the pages of an ordinary pool, and
+ *              cxa_paged_attention reads those. For prompts: a third of the products.
+ *
+ * Descriptor of a caller-owned latent pool.
+ *   Cp          device [L][num_pages][page_size][latent + rope] of cache_dtype, 16-byte aligned: rows
+ *               [ c | r ].
+ *   page_size   16, 32, 64, 128 or 256 positions.
+ *   latent      128, 256, 384 or 512;  rope 0, 16, 32, 48 or 64.
+ * Performs no CUDA call.
+ */
+typedef struct cxa_latent cxa_latent;
+
+CXA_API int cxa_latent_create(cxa_latent** out, void* Cp, int num_pages, int page_size, int L, int latent, int rope,
+                              int cache_dtype);
+CXA_API void cxa_latent_destroy(cxa_latent* c);
+
+/* As cxa_paged_check, for a batch over latent pages. */
+CXA_API int cxa_latent_check(const cxa_latent* c, int B, int n_tokens, const int* q_start, const int* kv_len,
+                             const int* page_table, int max_pages);
+
+/*
+ * Write the new tokens' rows into their pages of one layer: c [n_tokens][latent] normalised (RMS over
+ * its channels, with a weight, if norm is CXA_NORM_RMS), kr [n_tokens][rope] rotated by its position
+ * (rot NULL: as it is; of at most rope channels). kr is NULL where rope is 0. fp32 rows round to
+ * nearest even in a bf16 pool. Strides are elements from one token's row to the next; batch, norm and errors as for
+ * cxa_paged_append. One kernel.
+ */
+CXA_API int cxa_latent_append(const cxa_latent* cache, int layer, int B, int n_tokens, const int* q_start,
+                              const int* kv_len, const int* page_table, int max_pages, const void* c,
+                              long long c_stride, const void* kr, long long kr_stride, int norm, float eps,
+                              const float* weight, const cxa_rotary* rot, int dtype, void* stream);
+
+/* Bytes of device workspace of cxa_latent_attention; 0 for unsupported arguments. It needs no
+ * clearing. */
+CXA_API size_t cxa_latent_attention_workspace_bytes(int H, int latent, int max_new, int dtype);
+
+/*
+ * out = softmax(scale * q . row) row[0 .. latent) for every new token and head, over the rows at
+ * positions up to the token's own (which are in the pool: append first).
+ *
+ *   q          [n_tokens][H][latent + rope], out [n_tokens][H][latent], of dtype, which is the
+ *              pool's; their spans must not overlap. H at most 65535.
+ *   max_new    an upper bound of the new tokens of any one sequence, as for cxa_paged_attention.
+ *   scale      > 0 and finite, log2(e) times it too (the heads' width before the projections is not
+ *              known here, so there is no default).
+ *   workspace  256-byte aligned. Calls that share one must be ordered on one stream.
+ * (B + n_tokens * H / 16) * (max_pages * page_size / 32 + 1) must be below 2^31.
+ * Hidden positions, rows that see no key, and values that are not finite as for
+ * cxa_paged_attention. Results do not change from call to call.
+ */
+CXA_API int cxa_latent_attention(const cxa_latent* cache, int layer, int B, int n_tokens, int max_new,
+                                 const int* q_start, const int* kv_len, const int* page_table, int max_pages,
+                                 const void* q, long long q_stride, int H, void* out, long long o_stride, float scale,
+                                 int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expand positions [from[b], kv_len[b]) of every sequence (from NULL: from 0) into the pages of
+ * layer to_layer of an ordinary pool of the same type: K_h and V_h as above for its Hkv heads, at the
+ * same positions of to_table's rows. Page sizes may differ.
+ *
+ *   WK       device [latent][Hkv * (dh - rope)], WV device [latent][Hkv * dh] of the pools' type,
+ *            contiguous, 16-byte aligned. rope < dh.
+ *   from     device int32 [B] or NULL.
+ * Pages of `to` that are written must be written by one position alone. Products in bf16 pools are
+ * exact, their sums fp32. Positions whose page is outside the pool, on either side, are left out and reported
+ * (CXA_EPAGE from cxa_device_status). B * (max_pages * page_size / 64 + 1) must be below 2^31.
+ */
+CXA_API int cxa_latent_expand(const cxa_latent* cache, int layer, const cxa_pages* to, int to_layer, int B,
+                              const int* from, const int* kv_len, const int* page_table, int max_pages,
+                              const int* to_table, int to_max_pages, const void* WK, const void* WV, void* stream);
+
+/*
  * Cross-attention weights of selected alignment heads for one decode step
  * ("Caso de estudio: WhisperKit", §6: the cross-attention of chosen alignment
  * heads returns its weights, and their mean over heads is returned as an extra
