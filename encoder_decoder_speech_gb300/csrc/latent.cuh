@@ -63,7 +63,7 @@ struct WeightsLaunch {
   PagedLayer layer;
   void* workspace;
 };
-size_t weights_workspace(int n_tokens, int Hq, int Hkv, int dh, int max_new, bool bf16);
+size_t weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new, bool bf16);
 cudaError_t launch_weights(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
 
 struct EvictLaunch {

@@ -248,11 +248,14 @@ int cxa_latent_expand(const cxa_latent* cache, int layer, const cxa_pages* to, i
   });
 }
 
-size_t cxa_paged_weights_workspace_bytes(int n_tokens, int Hq, int Hkv, int dh, int max_new, int dtype) {
-  if (n_tokens < 0 || Hq < 1 || Hkv < 1 || Hq > 65535 || Hq % Hkv != 0 || (dh != 64 && dh != 128) || max_new < 1 ||
-      !valid_dtype(dtype))
+size_t cxa_paged_weights_workspace_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new, int max_pages,
+                                         int Hq) {
+  if (pages == nullptr || B < 1 || B > 1 << 30 || n_tokens < 0 || max_new < 1 || max_pages < 1 ||
+      static_cast<long long>(max_pages) << pages->page_shift > (1LL << 30) || Hq < 1 || Hq > 65535 ||
+      Hq % pages->Hkv != 0)
     return 0;
-  return cxa::weights_workspace(n_tokens, Hq, Hkv, dh, max_new, dtype == CXA_BF16);
+  return cxa::weights_workspace(B, n_tokens, max_pages, pages->page_shift, Hq, pages->Hkv, max_new,
+                                pages->dtype == CXA_BF16);
 }
 
 int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
@@ -279,7 +282,7 @@ int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, in
     if (weights == nullptr || !aligned(weights, 4))
       return fail(CXA_EINVAL, w + ": weights is NULL or not 4-byte aligned");
     rc = check_workspace(w, workspace, workspace_bytes,
-                         cxa_paged_weights_workspace_bytes(n_tokens, Hq, pages->Hkv, pages->dh, max_new, dtype));
+                         cxa_paged_weights_workspace_bytes(pages, B, n_tokens, max_new, max_pages, Hq));
     if (rc != CXA_OK) return rc;
     const double tiles = static_cast<double>(B) + static_cast<double>(n_tokens) * (Hq / pages->Hkv) / 16.0;
     const double chunks = static_cast<double>((static_cast<long long>(max_pages) << pages->page_shift) / 64 + 1);

@@ -75,6 +75,54 @@ __host__ __device__ constexpr uint64_t desc_high(uint32_t stride_bytes) {
   return static_cast<uint64_t>(stride_bytes >> 4 | 1u << 14 | 2u << 29) << 32;
 }
 
+// The waits of a block's warps on its barriers. A wait that runs out, or that another warp's has cut
+// short, leaves ok false for its warp, which from then on waits for nothing.
+struct Waits {
+  uint32_t bars;               // shared-memory address of the first
+  volatile int* abort;
+  unsigned int* status;
+  bool ok;
+  __device__ uint32_t bar(int i) const { return bars + 8u * static_cast<uint32_t>(i); }
+  // By a whole warp, with one answer.
+  __device__ bool warp(int i, uint32_t parity, unsigned int timeout_bit) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar(i), parity))) return ok;
+    uint64_t t0 = 0;
+    while (ok && __builtin_expect(!mbar_try_wait_1ms(bar(i), parity), 0)) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort != 0 || now - t0 > kWaitLimitNs) {
+        ok = false;
+        *abort = 1;
+        atomicOr(status, timeout_bit);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  }
+};
+
+// max of three, a * b + c and a + b on pairs.
+__device__ __forceinline__ float max_of_3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

@@ -6,16 +6,21 @@
 namespace cxa {
 
 // The workspace: the counters of the paged attention's workspace (the first kernel's arrivals use
-// the few-rows kernel's), the rows' references, and the partial states of items that were cut.
-// A row's reference is log2 of the sum of its weights' numerators, +inf where it sees no key, so that
-// p_j = 2^(s_j - ref) either way.
+// the few-rows kernel's), the rows' references, the partial states of items that were cut, and the
+// scores of calls with few rows. A row's reference is log2 of the sum of its weights' numerators, +inf where
+// it sees no key, so that p_j = 2^(s_j - ref) either way.
 constexpr int kWeightsMaxBlocks = 160 * 2;
-constexpr int kWeightsMaxRows = 128;            // of a tile
+constexpr int kWeightsMaxRows = 256;            // of an item
 static_assert(kWeightsMaxBlocks * 3 <= static_cast<int>(kRowsCounters), "the arrivals fit the shared counters");
 inline size_t weights_ref_bytes(long long rows) { return (static_cast<size_t>(rows) * 4 + 255) / 256 * 256; }
 constexpr size_t kWeightsPartBytes = static_cast<size_t>(2 * kWeightsMaxBlocks) * kWeightsMaxRows * 2 * 4;
 
-// fp32, on the CUDA cores (weights_rows.cu).
+// fp32, and bf16 with more query heads a K/V head than a tile holds, on the CUDA cores (weights_rows.cu).
 cudaError_t launch_weights_rows(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
+// bf16 (weights_tile.cu): whether a call has few query rows, and the room that their scores take (0:
+// too much, they are not kept).
+bool weights_few(int G, int max_new);
+size_t weights_score_bytes(int B, int width, int page_shift, int Hkv, int G, int max_new);
+cudaError_t launch_weights_tile(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
 
 }  // namespace cxa

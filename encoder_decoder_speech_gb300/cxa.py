@@ -120,7 +120,7 @@ SIGNATURES = {
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p]),
-    "cxa_paged_weights_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "cxa_paged_weights_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p] + [ctypes.c_int] * 5),
     "cxa_paged_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
@@ -436,8 +436,8 @@ def cxa_latent_expand(handle, layer, to, to_layer, B, from_, kv_len, page_table,
                                     max_pages, _ptr(to_table), to_max_pages, _ptr(WK), _ptr(WV), _stream(stream))
 
 
-def cxa_paged_weights_workspace_bytes(n_tokens, Hq, Hkv, dh, max_new, dtype) -> int:
-    return load().cxa_paged_weights_workspace_bytes(n_tokens, Hq, Hkv, dh, max_new, dtype)
+def cxa_paged_weights_workspace_bytes(handle, B, n_tokens, max_new, max_pages, Hq) -> int:
+    return load().cxa_paged_weights_workspace_bytes(handle, B, n_tokens, max_new, max_pages, Hq)
 
 
 def cxa_paged_weights(handle, layer, B, n_tokens, max_new, q_start, kv_len, page_table, max_pages, q, q_stride, Hq,
@@ -1039,7 +1039,7 @@ class PagedCache(_Paged):
         wp, code = self._weights(weights, tc.f32), _code(tc, dt)
         raw = tc.stream(at) if stream is None else _stream(stream)
         if workspace is None:
-            need = self._need((n, Hq, self.Hkv, dh, max_new, code), cxa_paged_weights_workspace_bytes)
+            need = self._need((self.handle, B, n, max_new, width, Hq), cxa_paged_weights_workspace_bytes)
             ws = self._kept(tc, need, stream, raw)
         else:
             ws = self._given(workspace)

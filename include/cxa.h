@@ -488,15 +488,18 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  *   weights    device fp32 [L][num_pages][Hkv][page_size], 4-byte aligned: one number for each row
  *              of K. Entries of no key of the batch are left as they are.
  *   decay      finite, >= 0; with 0 nothing of the old numbers is read into the new.
- *   workspace  at least cxa_paged_weights_workspace_bytes() bytes, otherwise as for
+ *   workspace  at least cxa_paged_weights_workspace_bytes() bytes (0 for unsupported arguments; the
+ *              scores of single tokens are in it, if they take 256 MB at most), otherwise as for
  *              cxa_paged_attention, whose workspace may be the same buffer (its first
  *              CXA_PAGED_COUNTER_BYTES are the same counters).
  * Pages that two sequences of the batch share must not be given: their entries would be written by
  * both. Arguments, the limit on the work and errors otherwise as for cxa_paged_attention; dtype is
  * the pool's. A token that sees an infinity or a NaN in q or K may make the weights of all keys that
- * it sees NaN. Results do not change from call to call.
+ * it sees NaN. A sequence with more than max_new new tokens may be left out. Results do not change from call to
+ * call.
  */
-CXA_API size_t cxa_paged_weights_workspace_bytes(int n_tokens, int Hq, int Hkv, int dh, int max_new, int dtype);
+CXA_API size_t cxa_paged_weights_workspace_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new,
+                                                 int max_pages, int Hq);
 
 CXA_API int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
                               const int* kv_len, const int* page_table, int max_pages, const void* q,

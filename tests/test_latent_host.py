@@ -135,16 +135,20 @@ def test_attention_refusals(latent):
     assert attend(latent, n_tokens=0) == cxa.CXA_OK
 
 
-def test_workspace_sizes():
+def test_workspace_sizes(pages):
     size = cxa.cxa_latent_attention_workspace_bytes
     assert size(8, 256, 1, cxa.CXA_BF16) > 2 * 152 * 16 * 256 * 4
     assert size(8, 256, 1, cxa.CXA_BF16) < size(8, 256, 4, cxa.CXA_BF16) < size(8, 512, 4, cxa.CXA_BF16)
     for bad in ((0, 256, 1, 0), (8, 100, 1, 0), (8, 256, 0, 0), (8, 256, 1, 5), (70000, 256, 1, 0)):
         assert size(*bad) == 0
     size = cxa.cxa_paged_weights_workspace_bytes
-    assert size(100, 8, 4, 64, 3, cxa.CXA_BF16) >= cxa.CXA_PAGED_COUNTER_BYTES + 100 * 8 * 4
-    for bad in ((-1, 8, 4, 64, 1, 0), (1, 0, 4, 64, 1, 0), (1, 8, 3, 64, 1, 0), (1, 8, 4, 96, 1, 0),
-                (1, 8, 4, 64, 0, 0), (1, 8, 4, 64, 1, 4)):
+    base = size(pages, 2, 100, 50, 3, 8)
+    assert base >= cxa.CXA_PAGED_COUNTER_BYTES + 100 * 8 * 4
+    # the scores of single tokens, unless they take more than 256 MB
+    assert size(pages, 2, 2, 1, 80, 8) >= 2 * 4 * 80 * 16 * 2 * 4 + cxa.CXA_PAGED_COUNTER_BYTES
+    assert size(pages, 64, 64, 1, 1 << 16, 8) < base + (1 << 20)
+    for bad in ((None, 2, 100, 3, 3, 8), (pages, 0, 1, 1, 3, 8), (pages, 1, -1, 1, 3, 8), (pages, 1, 1, 0, 3, 8),
+                (pages, 1, 1, 1, 0, 8), (pages, 1, 1, 1, 1 << 27, 8), (pages, 1, 1, 1, 3, 6), (pages, 1, 1, 1, 3, 0)):
         assert size(*bad) == 0
 
 
