@@ -5,7 +5,7 @@
 
 namespace cxa {
 
-// fp32, on the CUDA cores (expand_rows.cu).
+// fp32, on the CUDA cores (expand_rows.cu; bf16 goes to expand_tile.cu).
 cudaError_t launch_expand_rows(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // Positions of sequence b that are expanded: [lo, hi).

@@ -1,12 +1,10 @@
-// The expansion of latent rows into pages of keys and values, on the CUDA cores:
+// The expansion of latent rows into pages of keys and values in fp32, on the CUDA cores:
 //
 //   K_h(t) = [ r_t | c_t WK_h ],  V_h(t) = c_t WV_h
 //
 // as one product of positions by the columns of all heads' WK and WV side by side, in tiles of 64 x 64
 // with 4 x 4 sums a thread, 16 latent channels at a time. Bound by the products: 2 latent operations a
 // value.
-#include <cuda_bf16.h>
-
 #include "expand.cuh"
 #include "ptx.cuh"
 #include "span_work.cuh"
@@ -22,12 +20,6 @@ struct ExpandParams {
   unsigned int* status;
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-template <typename T>
 __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_constant__ ExpandParams p) {
   __shared__ SpanScratch s_span;
   __shared__ __align__(16) float s_a[kStep][kTile + 4], s_b[kStep][kTile + 4];
@@ -72,19 +64,19 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_cons
       s_dst[tid] = dst;
     }
     __syncthreads();
-    const T* C = static_cast<const T*>(a.layer.C);
+    const float* C = static_cast<const float*>(a.layer.C);
     for (int ct = blockIdx.y; ct < col_tiles; ct += gridDim.y) {
       const bool is_v = ct >= k_tiles;
       const int n0 = (is_v ? ct - k_tiles : ct) * kTile, nc = is_v ? vc : kc;
-      const T* W = static_cast<const T*>(is_v ? a.WV : a.WK);
+      const float* W = static_cast<const float*>(is_v ? a.WV : a.WK);
       float acc[4][4] = {};
       for (int k0 = 0; k0 < dc; k0 += kStep) {
         __syncthreads();
         for (int i = tid; i < kTile * kStep; i += kThreads) {
           const int r = i / kStep, k = i % kStep;
-          s_a[k][r] = s_src[r] >= 0 ? to_f(C[s_src[r] + k0 + k]) : 0.f;
+          s_a[k][r] = s_src[r] >= 0 ? C[s_src[r] + k0 + k] : 0.f;
           const int kk = i / kTile, n = i % kTile;
-          s_b[kk][n] = n0 + n < nc ? to_f(W[static_cast<size_t>(k0 + kk) * nc + n0 + n]) : 0.f;
+          s_b[kk][n] = n0 + n < nc ? W[static_cast<size_t>(k0 + kk) * nc + n0 + n] : 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -98,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_cons
             for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
         }
       }
-      T* out = static_cast<T*>(is_v ? a.to.V : a.to.K);
+      float* out = static_cast<float*>(is_v ? a.to.V : a.to.K);
       const int each = is_v ? dh : nope, skip = is_v ? 0 : rope;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -108,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const long long dst = s_dst[ty * 4 + i];
-          if (dst >= 0) put(out + (dst + (static_cast<long long>(h) << a.to.page_shift)) * dh + ch, acc[i][j]);
+          if (dst >= 0) out[(dst + (static_cast<long long>(h) << a.to.page_shift)) * dh + ch] = acc[i][j];
         }
       }
     }
@@ -117,15 +109,16 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_cons
       for (int i = tid; i < kTile * rope; i += kThreads) {
         const int r = i / rope, ch = i % rope;
         if (s_dst[r] < 0) continue;
-        const T x = C[s_src[r] + dc + ch];
+        const float x = C[s_src[r] + dc + ch];
         for (int h = 0; h < H; ++h)
-          static_cast<T*>(a.to.K)[(s_dst[r] + (static_cast<long long>(h) << a.to.page_shift)) * dh + ch] = x;
+          static_cast<float*>(a.to.K)[(s_dst[r] + (static_cast<long long>(h) << a.to.page_shift)) * dh + ch] = x;
       }
   }
 }
 
-template <typename T>
-cudaError_t launch(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_expand_rows(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
   ExpandParams p = {a, dev.status_word};
   cudaLaunchConfig_t cfg = {};
   // the blocks of a column go over all positions, those of a row over all columns
@@ -137,19 +130,9 @@ cudaError_t launch(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_rows_kernel<T>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_rows_kernel, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
-}
-
-}  // namespace
-
-cudaError_t launch_expand_rows(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
-  return a.bf16 ? launch<__nv_bfloat16>(a, dev, stream) : launch<float>(a, dev, stream);
-}
-
-cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string*) {
-  return launch_expand_rows(a, dev, stream);
 }
 
 }  // namespace cxa

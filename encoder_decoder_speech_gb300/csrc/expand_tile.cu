@@ -1,0 +1,374 @@
+// The expansion of latent rows into pages of keys and values in bf16, as tcgen05 products:
+//
+//   K_h(t) = [ r_t | c_t WK_h ],  V_h(t) = c_t WV_h
+//
+// 128 positions (the rows of a product) by the columns of a few heads, those of WK and those of WV side by side in
+// tensor memory: g heads with g (2 dh - rope) <= 256 columns, in two buffers. Weights are taken as they are,
+// [latent][columns]: an operand across the channels (MN-major) needs no copy of theirs turned round.
+//
+// All (128 positions, g heads) are numbered densely, positions first, and a block takes an equal range of them. The
+// positions' latent rows stay in shared memory over all heads (128 KB of 512 channels); what streams are the
+// weights, 32 channels of all columns a stage.
+//
+//  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages.
+//  * warp 4 issues the products.
+//  * warps 0 to 3 take the sums out, a position a lane, round them, and turn them round through shared
+//    memory, 64 channels at a time, so that 8 lanes write a row's 128 bytes together; the rotated part, the same
+//    in every head, is put in front on the way.
+//
+// Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "expand.cuh"
+#include "ptx.cuh"
+#include "span_work.cuh"
+#include "tc_util.cuh"
+
+namespace cxa {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kThreads = 6 * 32, kMmaWarp = 4, kTmaWarp = 5;
+constexpr int kABlock = 16384;            // 64 channels of 128 positions
+constexpr int kBox = 4096;                // 32 channels of 64 columns of the weights
+constexpr int kMaxStages = 16, kMaxA = 8;
+constexpr int kStageBytes = 4 * 4096, kRopeBytes = 4 * 4096;      // of the four warps: 32 rows of 128 bytes
+constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
+
+enum Bars {
+  kAFull = 0,
+  kAEmpty = kAFull + kMaxA,
+  kBFull = kAEmpty + kMaxA,
+  kBEmpty = kBFull + kMaxStages,
+  kDFull = kBEmpty + kMaxStages,
+  kDFree = kDFull + 2,
+  kBars = kDFree + 2
+};
+struct Small {
+  uint64_t bars[kBars];
+  SpanScratch span;
+  volatile int abort;
+  int tmem;
+};
+static_assert(sizeof(Small) <= kSmallBytes, "the small arrays fit");
+
+struct TileParams {
+  const __nv_bfloat16* C;
+  __nv_bfloat16 *K, *V;
+  unsigned int* status;
+  int B, num_pages, page_shift, width, latent, rope;
+  int to_pages, to_shift, to_width, H, dh;
+  const int *from, *kv_len, *table, *to_table;
+  int heads, groups;         // heads of a product, and how many of those there are
+  int k_boxes, v_boxes, stages;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    expand_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int a_blocks = p.latent / 64, boxes = p.k_boxes + p.v_boxes;
+  const uint32_t a_base = smem_u32(smem), b_base = a_base + a_blocks * kABlock;
+  const uint32_t s_base = b_base + p.stages * boxes * kBox, r_base = s_base + kStageBytes;
+  Small* sm = reinterpret_cast<Small*>(smem + kSmemBytes - kSmallBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nope = p.dh - p.rope, steps = p.latent / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cap = p.width << p.page_shift, to_cap = p.to_width << p.to_shift;
+  auto tiles = [&](int b) {
+    const ExpandSpan s = expand_span(p.from, p.kv_len, cap, b);
+    return s.hi > s.lo ? (s.hi + kRows - 1) / kRows - s.lo / kRows : 0;
+  };
+  auto units = [&](int b) {
+    const long long u = static_cast<long long>(tiles(b)) * p.groups;
+    return static_cast<int>(min(u, static_cast<long long>(kCountLimit)));
+  };
+  SpanRange range;
+  if (!span_locate<kThreads>(p.B, units, &sm->span, &range)) return;
+  Waits w = {smem_u32(sm->bars), &sm->abort, p.status, true};
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i) mbar_init(w.bar(i), i >= kDFree ? 4 : 1);
+    fence_mbar_init();
+    sm->abort = 0;
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tmap(&tmC);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sm->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+
+  // this block's work, in order; each role walks it by itself
+  int b = range.b, first = range.first;
+  auto seek = [&](int g) {
+    for (int n = units(b); g - first >= n; n = units(b)) {
+      first += n;
+      ++b;
+    }
+  };
+  // first position of the tile that unit g is of
+  auto tile_of = [&](int g) {
+    return (expand_span(p.from, p.kv_len, cap, b).lo / kRows + (g - first) / p.groups) * kRows;
+  };
+
+  if (warp == kTmaWarp) {
+    fence_proxy_async_global();
+    const int box_shift = min(p.page_shift, 7), box_rows = 1 << box_shift;
+    int stage = 0, tile = 0, page = -1, y = 0;
+    uint32_t round = 0, armed = 0, parity = 0, a_armed = 0, a_parity = 0, good = 0;
+    for (int g = range.g0; g < range.g1 && w.ok; ++g) {
+      seek(g);
+      const int grp = (g - first) % p.groups;
+      const bool fresh = g == range.g0 || grp == 0;
+      if (fresh) {
+        const ExpandSpan span = expand_span(p.from, p.kv_len, cap, b);
+        const int at = tile_of(g) + lane * box_rows;
+        const bool want = lane < (kRows >> box_shift) && at < span.hi && at + box_rows > span.lo;
+        page = want ? paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, at) : -1;
+        y = at & ((1 << p.page_shift) - 1);
+        good = __ballot_sync(0xffffffffu, page >= 0);
+        ++tile;
+      }
+      const int h0 = grp * p.heads;
+      for (int k = 0; k < steps; ++k) {
+        if (fresh && (k & 1) == 0) {
+          const int kb = k >> 1;
+          if (!w.warp(kAEmpty + kb, tile & 1, kStatusTimeout)) break;      // (the first passes: tile is 1)
+          if (lane == 0) mbar_arrive_expect_tx(w.bar(kAFull + kb), static_cast<uint32_t>(__popc(good) * box_rows * 128));
+          __syncwarp();
+          if (page >= 0) tma_load_3d(a_base + kb * kABlock + lane * box_rows * 128, &tmC, w.bar(kAFull + kb), kb * 64, y, page);
+          a_armed |= 1u << kb;
+          a_parity = (a_parity & ~(1u << kb)) | (static_cast<uint32_t>(tile - 1) & 1u) << kb;
+        }
+        if (!w.warp(kBEmpty + stage, (round & 1) ^ 1, kStatusTimeout)) break;
+        if (lane == 0) mbar_arrive_expect_tx(w.bar(kBFull + stage), static_cast<uint32_t>(boxes * kBox));
+        __syncwarp();
+        if (lane < boxes) {
+          const bool v = lane >= p.k_boxes;
+          const int col = v ? h0 * p.dh + (lane - p.k_boxes) * 64 : h0 * nope + lane * 64;
+          tma_load_2d(b_base + (stage * boxes + lane) * kBox, v ? &tmV : &tmK, w.bar(kBFull + stage), col, k * 32);
+        }
+        armed |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (round & 1u) << stage;
+        if (++stage == p.stages) {
+          stage = 0;
+          ++round;
+        }
+      }
+    }
+    if (!w.ok) {      // the copies under way land before the block ends
+      for (int i = 0; i < p.stages; ++i)
+        if (armed & (1u << i)) mbar_wait(w.bar(kBFull + i), (parity >> i) & 1u);
+      for (int i = 0; i < a_blocks; ++i)
+        if (a_armed & (1u << i)) mbar_wait(w.bar(kAFull + i), (a_parity >> i) & 1u);
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint64_t hi = desc_high(1024);
+    const uint32_t idesc_k = make_idesc(1u, kRows, static_cast<uint32_t>(p.heads * nope)) | 1u << 16;
+    const uint32_t idesc_v = make_idesc(1u, kRows, static_cast<uint32_t>(p.heads * p.dh)) | 1u << 16;
+    int stage = 0, tile = 0;
+    uint32_t round = 0;
+    for (int g = range.g0, i = 0; g < range.g1 && w.ok; ++g, ++i) {
+      seek(g);
+      const int grp = (g - first) % p.groups;
+      const bool fresh = g == range.g0 || grp == 0, last = g + 1 == range.g1 || grp + 1 == p.groups;
+      tile += fresh ? 1 : 0;
+      if (!w.warp(kDFree + (i & 1), ((i >> 1) & 1) ^ 1, kStatusTimeout)) break;
+      const uint32_t d = tmem + (i & 1) * 256, dv = d + p.heads * nope;
+      for (int k = 0; k < steps; ++k) {
+        if (fresh && (k & 1) == 0 && !w.warp(kAFull + (k >> 1), (tile - 1) & 1, kStatusTimeout)) break;
+        if (!w.warp(kBFull + stage, round & 1, kStatusTimeout)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t al = desc_low(a_base + (k >> 1) * kABlock, 16) + (k & 1) * 4;
+          const uint32_t bl = desc_low(b_base + stage * boxes * kBox, kBox);
+          const uint32_t vl = bl + static_cast<uint32_t>(p.k_boxes * kBox >> 4);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {      // 16 channels: 32 bytes of a row, 16 rows of the weights
+            mma_bf16(d, hi | (al + 2 * s), hi | (bl + s * (2048 >> 4)), idesc_k, k + s != 0 ? 1u : 0u);
+            mma_bf16(dv, hi | (al + 2 * s), hi | (vl + s * (2048 >> 4)), idesc_v, k + s != 0 ? 1u : 0u);
+          }
+          tc_commit(w.bar(kBEmpty + stage));
+          if (last && (k & 1) != 0) tc_commit(w.bar(kAEmpty + (k >> 1)));
+          if (k + 1 == steps) tc_commit(w.bar(kDFull + (i & 1)));
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          ++round;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // a position a lane
+    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t stage = s_base + warp * 4096, rotated = r_base + warp * 4096;
+    const int sub = lane >> 3, piece = lane & 7;
+    const int rope_pieces = p.rope / 8;
+    int dst = -1;              // row of head 0 of this lane's position, in units of dh (pool rows)
+    for (int g = range.g0, i = 0; g < range.g1; ++g, ++i) {
+      seek(g);
+      const int grp = (g - first) % p.groups;
+      long long row = -1;
+      if (g == range.g0 || grp == 0) {
+        const ExpandSpan span = expand_span(p.from, p.kv_len, cap, b);
+        const int t = tile_of(g) + warp * 32 + lane;
+        dst = -1;
+        if (t >= span.lo && t < span.hi) {
+          const int sp = paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, t);
+          const int dp = paged_lookup(p.to_table + static_cast<size_t>(b) * p.to_width, p.to_width, p.to_shift, p.to_pages,
+                                      t < to_cap ? t : -1);
+          if (sp < 0 || dp < 0) {
+            atomicOr(p.status, kStatusBadPage);
+          } else {
+            dst = dp;
+            row = ((static_cast<long long>(sp) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * (p.latent + p.rope);
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int j = 0; j < rope_pieces; ++j) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + j * 8);
+          st_shared_v4(rotated + lane * 128 + ((j ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+        __syncwarp();
+      }
+      const int slot = (tile_of(g) + warp * 32 + lane) & ((1 << p.to_shift) - 1);
+      w.warp(kDFull + (i & 1), (i >> 1) & 1, kStatusTimeout);
+      tc_fence_after();
+      const int nh = min(p.heads, p.H - grp * p.heads);
+      const uint32_t d = my_tmem + (i & 1) * 256;
+      // 64 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's
+      auto put = [&](__nv_bfloat16* pool, int h, int c0, int skip, uint32_t col) {
+        uint32_t x[4][16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q * 16 >= skip) tmem_ld_32x32b_x16(col + q * 16, x[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q * 16 >= skip)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                v[f] = pack_bf16(__uint_as_float(x[q][8 * e + 2 * f]), __uint_as_float(x[q][8 * e + 2 * f + 1]));
+              st_shared_v4(stage + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+            }
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int r = n * 4 + sub;
+          const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
+          const uint4 v = ld_shared_v4((piece * 8 < skip ? rotated : stage) + r * 128 + ((piece ^ (r & 7)) << 4));
+          if (to >= 0 && w.ok)
+            *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
+                                      piece * 8) = v;
+        }
+        __syncwarp();
+      };
+      for (int j = 0; j < nh; ++j) {
+        const int h = grp * p.heads + j;
+        for (int c0 = 0; c0 < p.dh; c0 += 64) {
+          const int skip = min(64, max(0, p.rope - c0));
+          // (a channel c of K stands in column j * nope + c - rope)
+          put(p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
+        }
+        for (int c0 = 0; c0 < p.dh; c0 += 64) put(p.V, h, c0, 0, d + static_cast<uint32_t>(p.heads * nope + j * p.dh + c0));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w.bar(kDFree + (i & 1)));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// A 2-D bf16 map of boxes of 64 columns by 32 rows of a [rows][cols] matrix.
+bool encode_weights(CUtensorMap* map, const void* ptr, int rows, int cols) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {64, 32}, estr[2] = {1, 1};
+  return fn != nullptr &&
+         fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& dev, cudaStream_t stream,
+                                 std::string* msg) {
+  if (!a.bf16) return launch_expand_rows(a, dev, stream);
+  const int width = a.layer.latent + a.layer.rope, page_size = 1 << a.layer.page_shift, H = a.to.Hkv;
+  const int nope = a.dh - a.layer.rope;
+  CUtensorMap c, k, v;
+  if (!encode_tiles(&c, a.layer.C, width, page_size, a.layer.num_pages, static_cast<cuuint64_t>(width) * 2,
+                    static_cast<cuuint64_t>(page_size) * width * 2, page_size < kRows ? page_size : kRows, 1) ||
+      !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh)) {
+    *msg = "(the tensor maps of the pool and the weights cannot be encoded)";
+    return cudaErrorInvalidValue;
+  }
+  TileParams p;
+  p.C = static_cast<const __nv_bfloat16*>(a.layer.C);
+  p.K = static_cast<__nv_bfloat16*>(a.to.K);
+  p.V = static_cast<__nv_bfloat16*>(a.to.V);
+  p.status = dev.status_word;
+  p.B = a.B;
+  p.num_pages = a.layer.num_pages;
+  p.page_shift = a.layer.page_shift;
+  p.width = a.width;
+  p.latent = a.layer.latent;
+  p.rope = a.layer.rope;
+  p.to_pages = a.to.num_pages;
+  p.to_shift = a.to.page_shift;
+  p.to_width = a.to_width;
+  p.H = H;
+  p.dh = a.dh;
+  p.from = a.from;
+  p.kv_len = a.kv_len;
+  p.table = a.table;
+  p.to_table = a.to_table;
+  const int fit = 256 / (2 * a.dh - a.layer.rope);
+  p.heads = fit < H ? fit : H;
+  p.groups = (H + p.heads - 1) / p.heads;
+  p.k_boxes = (p.heads * nope + 63) / 64;
+  p.v_boxes = p.heads * a.dh / 64;
+  const int stage = (p.k_boxes + p.v_boxes) * kBox;
+  const int stages = (kSmemBytes - kSmallBytes - kStageBytes - kRopeBytes - p.latent / 64 * kABlock) / stage;
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  static SmemOnce once;
+  cudaError_t e = allow_smem(expand_tile_kernel, kSmemBytes, dev.device, &once);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, p);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace cxa
