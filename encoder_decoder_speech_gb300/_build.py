@@ -22,6 +22,7 @@ LIB = os.path.join(OUT_DIR, "libcxa.so")
 SOURCES = ["cxa_api.cu", "populate.cu", "decode.cu", "decode_noalloc.cu", "block.cu", "append.cu", "alignment.cu", "decode_shared_tc.cu", "block_fused.cu", "decode_rows.cu",
            "paged_api.cu", "norm_rope.cu", "paged_rows.cu", "paged_tile.cu",
            "latent_api.cu", "latent_append.cu", "latent_rows.cu", "latent_tile.cu", "latent_merge.cu", "expand_rows.cu",
+           "expand_tile.cu",
            "weights.cu", "weights_rows.cu", "weights_tile.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -2,16 +2,21 @@
 //
 //   K_h(t) = [ r_t | c_t WK_h ],  V_h(t) = c_t WV_h
 //
-// 128 positions (the rows of a product) by the columns of a few heads, those of WK and those of WV side by side in
-// tensor memory: g heads with g (2 dh - rope) <= 256 columns, in two buffers. Weights are taken as they are,
-// [latent][columns]: an operand across the channels (MN-major) needs no copy of theirs turned round.
+// Two blocks work as a pair (cta_group::2) on two tiles of 128 positions, of any sequences, by the columns
+// of a few heads, those of WK and those of WV side by side in tensor memory: g heads with g (2 dh - rope) <= 256
+// columns, in two buffers. Each block holds its own positions and streams half of the columns' weights: half the
+// traffic of blocks by themselves (which took 183 us for 32768 positions, 20 heads of 128, 512 + 64 channels).
+// Weights are taken as they are, [latent][columns]: an operand across the channels (MN-major) needs no copy
+// of theirs turned round. Where the columns of WK fill blocks of 64, both parts go through one product,
+// otherwise through one each.
 //
-// All (128 positions, g heads) are numbered densely, positions first, and a block takes an equal range of them. The
+// All (pairs of tiles, g heads) are numbered densely, positions first, and a pair takes an equal range of them. The
 // positions' latent rows stay in shared memory over all heads (128 KB of 512 channels); what streams are the
-// weights, 32 channels of all columns a stage.
+// weights, 64 channels a stage.
 //
-//  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages.
-//  * warp 4 issues the products.
+//  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
+//    copies are counted by the even block's barriers.
+//  * warp 4 of the even block issues the products.
 //  * warps 0 to 3 take the sums out, a position a lane, round them, and turn them round through shared
 //    memory, 64 channels at a time, so that 8 lanes write a row's 128 bytes together; the rotated part, the same
 //    in every head, is put in front on the way.
@@ -20,6 +25,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "expand.cuh"
 #include "ptx.cuh"
 #include "span_work.cuh"
@@ -31,7 +37,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kThreads = 6 * 32, kMmaWarp = 4, kTmaWarp = 5;
 constexpr int kABlock = 16384;            // 64 channels of 128 positions
-constexpr int kBox = 4096;                // 32 channels of 64 columns of the weights
+constexpr int kBox = 8192;                // 64 channels of 64 columns of the weights
 constexpr int kMaxStages = 16, kMaxA = 8;
 constexpr int kStageBytes = 4 * 4096, kRopeBytes = 4 * 4096;      // of the four warps: 32 rows of 128 bytes
 constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
@@ -61,19 +67,23 @@ struct TileParams {
   int to_pages, to_shift, to_width, H, dh;
   const int *from, *kv_len, *table, *to_table;
   int heads, groups;         // heads of a product, and how many of those there are
-  int k_boxes, v_boxes, stages;
+  int k_cols, v_cols;        // columns of a product
+  int one;                   // both parts through one product
+  int boxes, k_boxes, stages;      // boxes of a stage in a block, those of WK (by itself) among them
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
     expand_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int a_blocks = p.latent / 64, boxes = p.k_boxes + p.v_boxes;
+  const int a_blocks = p.latent / 64, boxes = p.boxes;
   const uint32_t a_base = smem_u32(smem), b_base = a_base + a_blocks * kABlock;
   const uint32_t s_base = b_base + p.stages * boxes * kBox, r_base = s_base + kStageBytes;
   Small* sm = reinterpret_cast<Small*>(smem + kSmemBytes - kSmallBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nope = p.dh - p.rope, steps = p.latent / 32;
+  const int nope = p.dh - p.rope;
+  const uint32_t rank = cluster_rank();
+  const bool even = rank == 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cap = p.width << p.page_shift, to_cap = p.to_width << p.to_shift;
@@ -81,15 +91,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const ExpandSpan s = expand_span(p.from, p.kv_len, cap, b);
     return s.hi > s.lo ? (s.hi + kRows - 1) / kRows - s.lo / kRows : 0;
   };
-  auto units = [&](int b) {
-    const long long u = static_cast<long long>(tiles(b)) * p.groups;
-    return static_cast<int>(min(u, static_cast<long long>(kCountLimit)));
-  };
-  SpanRange range;
-  if (!span_locate<kThreads>(p.B, units, &sm->span, &range)) return;
+  // this pair's work [g0, g1), and the sequence of its first tile; the same in both blocks
+  int g0 = 0, g1 = 0, total = 0, b = 0, first = 0;
+  if (!span_find<kThreads>(
+          p.B, tiles, &sm->span,
+          [&](int n) {
+            const long long pairs = static_cast<long long>(n + 1) / 2 * p.groups, by = gridDim.x / 2, at = blockIdx.x / 2;
+            total = n;
+            if (pairs > 0x7FFFFFFFLL - 1024) return -1;
+            g0 = static_cast<int>(pairs / by * at + min(at, pairs % by));
+            g1 = g0 + static_cast<int>(pairs / by + (at < pairs % by ? 1 : 0));
+            return g0 < g1 ? g0 / p.groups * 2 : -1;
+          },
+          &b, &first))
+    return;
   Waits w = {smem_u32(sm->bars), &sm->abort, p.status, true};
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(w.bar(i), i >= kDFree ? 4 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(w.bar(i), i >= kDFree ? 8 : 1);
     fence_mbar_init();
     sm->abort = 0;
   }
@@ -99,64 +117,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmV);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&sm->tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&sm->tmem), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();      // both blocks' barriers are there before anything arrives from the other
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
 
-  // this block's work, in order; each role walks it by itself
-  int b = range.b, first = range.first;
-  auto seek = [&](int g) {
-    for (int n = units(b); g - first >= n; n = units(b)) {
+  // To tile i of all (i < total, not before the last one asked for): b is its sequence.
+  auto seek = [&](int i) {
+    for (int n = tiles(b); i - first >= n; n = tiles(b)) {
       first += n;
       ++b;
     }
-  };
-  // first position of the tile that unit g is of
-  auto tile_of = [&](int g) {
-    return (expand_span(p.from, p.kv_len, cap, b).lo / kRows + (g - first) / p.groups) * kRows;
+    return (expand_span(p.from, p.kv_len, cap, b).lo / kRows + (i - first)) * kRows;      // its first position
   };
 
   if (warp == kTmaWarp) {
     fence_proxy_async_global();
-    const int box_shift = min(p.page_shift, 7), box_rows = 1 << box_shift;
+    const int box_shift = min(p.page_shift, 7), box_rows = 1 << box_shift, per_tile = kRows >> box_shift;
     int stage = 0, tile = 0, page = -1, y = 0;
-    uint32_t round = 0, armed = 0, parity = 0, a_armed = 0, a_parity = 0, good = 0;
-    for (int g = range.g0; g < range.g1 && w.ok; ++g) {
-      seek(g);
-      const int grp = (g - first) % p.groups;
-      const bool fresh = g == range.g0 || grp == 0;
+    uint32_t round = 0, armed = 0, parity = 0, a_armed = 0, a_parity = 0, a_bytes = 0;
+    for (int g = g0; g < g1 && w.ok; ++g) {
+      const int grp = g % p.groups;
+      const bool fresh = g == g0 || grp == 0;
       if (fresh) {
-        const ExpandSpan span = expand_span(p.from, p.kv_len, cap, b);
-        const int at = tile_of(g) + lane * box_rows;
-        const bool want = lane < (kRows >> box_shift) && at < span.hi && at + box_rows > span.lo;
-        page = want ? paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, at) : -1;
-        y = at & ((1 << p.page_shift) - 1);
-        good = __ballot_sync(0xffffffffu, page >= 0);
+        // the boxes of both blocks' tiles, a lane each: the even block counts them all
+        page = -1;
+        int boxes_there = 0;
+        for (int t = 0; t < 2; ++t) {
+          const int i = g / p.groups * 2 + t;
+          int got = -1, slot = 0;
+          if (i < total) {
+            const int at = seek(i) + lane * box_rows;
+            const ExpandSpan span = expand_span(p.from, p.kv_len, cap, b);
+            if (lane < per_tile && at < span.hi && at + box_rows > span.lo)
+              got = paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, at);
+            slot = at & ((1 << p.page_shift) - 1);
+          }
+          boxes_there += __popc(__ballot_sync(0xffffffffu, got >= 0));
+          if (t == static_cast<int>(rank)) {
+            page = got;
+            y = slot;
+          }
+        }
+        a_bytes = static_cast<uint32_t>(boxes_there * box_rows * 128);
         ++tile;
       }
       const int h0 = grp * p.heads;
-      for (int k = 0; k < steps; ++k) {
-        if (fresh && (k & 1) == 0) {
-          const int kb = k >> 1;
-          if (!w.warp(kAEmpty + kb, tile & 1, kStatusTimeout)) break;      // (the first passes: tile is 1)
-          if (lane == 0) mbar_arrive_expect_tx(w.bar(kAFull + kb), static_cast<uint32_t>(__popc(good) * box_rows * 128));
+      // where this block's half of the columns begins, by the box of this lane
+      int col = 0;
+      bool v = false;
+      if (p.one) {
+        const int c = static_cast<int>(rank) * (p.k_cols + p.v_cols) / 2 + lane * 64;
+        v = c >= p.k_cols;
+        col = v ? h0 * p.dh + c - p.k_cols : h0 * nope + c;
+      } else {
+        v = lane >= p.k_boxes;
+        col = v ? h0 * p.dh + static_cast<int>(rank) * p.v_cols / 2 + (lane - p.k_boxes) * 64
+                : h0 * nope + static_cast<int>(rank) * p.k_cols / 2 + lane * 64;
+      }
+      for (int k = 0; k < a_blocks; ++k) {
+        if (fresh) {
+          if (!w.warp(kAEmpty + k, tile & 1, kStatusTimeout)) break;      // (the first passes: tile is 1)
+          if (even && lane == 0) mbar_arrive_expect_tx(w.bar(kAFull + k), a_bytes);
           __syncwarp();
-          if (page >= 0) tma_load_3d(a_base + kb * kABlock + lane * box_rows * 128, &tmC, w.bar(kAFull + kb), kb * 64, y, page);
-          a_armed |= 1u << kb;
-          a_parity = (a_parity & ~(1u << kb)) | (static_cast<uint32_t>(tile - 1) & 1u) << kb;
+          if (page >= 0)
+            tma_load_3d_pair(a_base + k * kABlock + lane * box_rows * 128, &tmC, mapa_shared(w.bar(kAFull + k), 0), k * 64,
+                             y, page);
+          a_armed |= 1u << k;
+          a_parity = (a_parity & ~(1u << k)) | (static_cast<uint32_t>(tile - 1) & 1u) << k;
         }
         if (!w.warp(kBEmpty + stage, (round & 1) ^ 1, kStatusTimeout)) break;
-        if (lane == 0) mbar_arrive_expect_tx(w.bar(kBFull + stage), static_cast<uint32_t>(boxes * kBox));
+        if (even && lane == 0) mbar_arrive_expect_tx(w.bar(kBFull + stage), static_cast<uint32_t>(2 * boxes * kBox));
         __syncwarp();
-        if (lane < boxes) {
-          const bool v = lane >= p.k_boxes;
-          const int col = v ? h0 * p.dh + (lane - p.k_boxes) * 64 : h0 * nope + lane * 64;
-          tma_load_2d(b_base + (stage * boxes + lane) * kBox, v ? &tmV : &tmK, w.bar(kBFull + stage), col, k * 32);
-        }
+        if (lane < boxes)
+          tma_load_2d_pair(b_base + (stage * boxes + lane) * kBox, v ? &tmV : &tmK, mapa_shared(w.bar(kBFull + stage), 0),
+                           col, k * 64);
         armed |= 1u << stage;
         parity = (parity & ~(1u << stage)) | (round & 1u) << stage;
         if (++stage == p.stages) {
@@ -165,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!w.ok) {      // the copies under way land before the block ends
+    if (!w.ok && even) {      // the copies under way land before the pair ends
       for (int i = 0; i < p.stages; ++i)
         if (armed & (1u << i)) mbar_wait(w.bar(kBFull + i), (parity >> i) & 1u);
       for (int i = 0; i < a_blocks; ++i)
@@ -173,33 +211,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint64_t hi = desc_high(1024);
-    const uint32_t idesc_k = make_idesc(1u, kRows, static_cast<uint32_t>(p.heads * nope)) | 1u << 16;
-    const uint32_t idesc_v = make_idesc(1u, kRows, static_cast<uint32_t>(p.heads * p.dh)) | 1u << 16;
+    const uint32_t n0 = static_cast<uint32_t>(p.one ? p.k_cols + p.v_cols : p.k_cols);
+    const uint32_t idesc_0 = make_idesc(1u, 2 * kRows, n0) | 1u << 16;
+    const uint32_t idesc_v = make_idesc(1u, 2 * kRows, static_cast<uint32_t>(p.v_cols)) | 1u << 16;
     int stage = 0, tile = 0;
     uint32_t round = 0;
-    for (int g = range.g0, i = 0; g < range.g1 && w.ok; ++g, ++i) {
-      seek(g);
-      const int grp = (g - first) % p.groups;
-      const bool fresh = g == range.g0 || grp == 0, last = g + 1 == range.g1 || grp + 1 == p.groups;
+    for (int g = g0, i = 0; even && g < g1 && w.ok; ++g, ++i) {
+      const int grp = g % p.groups;
+      const bool fresh = g == g0 || grp == 0, last = g + 1 == g1 || grp + 1 == p.groups;
       tile += fresh ? 1 : 0;
       if (!w.warp(kDFree + (i & 1), ((i >> 1) & 1) ^ 1, kStatusTimeout)) break;
-      const uint32_t d = tmem + (i & 1) * 256, dv = d + p.heads * nope;
-      for (int k = 0; k < steps; ++k) {
-        if (fresh && (k & 1) == 0 && !w.warp(kAFull + (k >> 1), (tile - 1) & 1, kStatusTimeout)) break;
+      const uint32_t d = tmem + (i & 1) * 256, dv = d + p.k_cols;
+      for (int k = 0; k < a_blocks; ++k) {
+        if (fresh && !w.warp(kAFull + k, (tile - 1) & 1, kStatusTimeout)) break;
         if (!w.warp(kBFull + stage, round & 1, kStatusTimeout)) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t al = desc_low(a_base + (k >> 1) * kABlock, 16) + (k & 1) * 4;
+          const uint32_t al = desc_low(a_base + k * kABlock, 16);
           const uint32_t bl = desc_low(b_base + stage * boxes * kBox, kBox);
           const uint32_t vl = bl + static_cast<uint32_t>(p.k_boxes * kBox >> 4);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {      // 16 channels: 32 bytes of a row, 16 rows of the weights
-            mma_bf16(d, hi | (al + 2 * s), hi | (bl + s * (2048 >> 4)), idesc_k, k + s != 0 ? 1u : 0u);
-            mma_bf16(dv, hi | (al + 2 * s), hi | (vl + s * (2048 >> 4)), idesc_v, k + s != 0 ? 1u : 0u);
+          for (int s = 0; s < 4; ++s) {      // 16 channels: 32 bytes of a row, 16 rows of the weights
+            mma_bf16_pair(d, hi | (al + 2 * s), hi | (bl + s * (2048 >> 4)), idesc_0, k + s != 0 ? 1u : 0u);
+            if (!p.one) mma_bf16_pair(dv, hi | (al + 2 * s), hi | (vl + s * (2048 >> 4)), idesc_v, k + s != 0 ? 1u : 0u);
           }
-          tc_commit(w.bar(kBEmpty + stage));
-          if (last && (k & 1) != 0) tc_commit(w.bar(kAEmpty + (k >> 1)));
-          if (k + 1 == steps) tc_commit(w.bar(kDFull + (i & 1)));
+          tc_commit_pair(w.bar(kBEmpty + stage), 0x3);
+          if (last) tc_commit_pair(w.bar(kAEmpty + k), 0x3);
+          if (k + 1 == a_blocks) tc_commit_pair(w.bar(kDFull + (i & 1)), 0x3);
         }
         __syncwarp();
         if (++stage == p.stages) {
@@ -216,14 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = lane >> 3, piece = lane & 7;
     const int rope_pieces = p.rope / 8;
     int dst = -1;              // row of head 0 of this lane's position, in units of dh (pool rows)
-    for (int g = range.g0, i = 0; g < range.g1; ++g, ++i) {
-      seek(g);
-      const int grp = (g - first) % p.groups;
+    int slot = 0;
+    for (int g = g0, i = 0; g < g1; ++g, ++i) {
+      const int grp = g % p.groups;
       long long row = -1;
-      if (g == range.g0 || grp == 0) {
-        const ExpandSpan span = expand_span(p.from, p.kv_len, cap, b);
-        const int t = tile_of(g) + warp * 32 + lane;
+      if (g == g0 || grp == 0) {
+        const int mine = g / p.groups * 2 + static_cast<int>(rank);
+        const int t = mine < total ? seek(mine) + warp * 32 + lane : 0;
         dst = -1;
+        slot = t & ((1 << p.to_shift) - 1);
+        const ExpandSpan span = mine < total ? expand_span(p.from, p.kv_len, cap, b) : ExpandSpan{0, 0};
         if (t >= span.lo && t < span.hi) {
           const int sp = paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, t);
           const int dp = paged_lookup(p.to_table + static_cast<size_t>(b) * p.to_width, p.to_width, p.to_shift, p.to_pages,
@@ -244,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      const int slot = (tile_of(g) + warp * 32 + lane) & ((1 << p.to_shift) - 1);
       w.warp(kDFull + (i & 1), (i >> 1) & 1, kStatusTimeout);
       tc_fence_after();
       const int nh = min(p.heads, p.H - grp * p.heads);
@@ -286,25 +325,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (a channel c of K stands in column j * nope + c - rope)
           put(p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
         }
-        for (int c0 = 0; c0 < p.dh; c0 += 64) put(p.V, h, c0, 0, d + static_cast<uint32_t>(p.heads * nope + j * p.dh + c0));
+        for (int c0 = 0; c0 < p.dh; c0 += 64) put(p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(w.bar(kDFree + (i & 1)));
+      if (lane == 0) mbar_arrive_cluster(w.bar(kDFree + (i & 1)), 0);      // the even block's products wait for both
     }
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();      // neither block leaves while the pair's products or arrivals may still touch it
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-// A 2-D bf16 map of boxes of 64 columns by 32 rows of a [rows][cols] matrix.
+// A 2-D bf16 map of boxes of 64 columns by 64 rows of a [rows][cols] matrix.
 bool encode_weights(CUtensorMap* map, const void* ptr, int rows, int cols) {
   const EncodeTiledFn fn = tensor_map_encoder();
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {64, 32}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
   return fn != nullptr &&
          fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -345,27 +384,49 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   p.kv_len = a.kv_len;
   p.table = a.table;
   p.to_table = a.to_table;
-  const int fit = 256 / (2 * a.dh - a.layer.rope);
-  p.heads = fit < H ? fit : H;
+  // a pair's product has a multiple of 32 columns: those of WK are filled up (with the next head's, unused)
+  p.heads = 256 / (2 * a.dh - a.layer.rope);
+  if (p.heads > H) p.heads = H;
+  while (p.heads > 1 && (p.heads * nope + 31) / 32 * 32 + p.heads * a.dh > 256) --p.heads;
   p.groups = (H + p.heads - 1) / p.heads;
-  p.k_boxes = (p.heads * nope + 63) / 64;
-  p.v_boxes = p.heads * a.dh / 64;
-  const int stage = (p.k_boxes + p.v_boxes) * kBox;
-  const int stages = (kSmemBytes - kSmallBytes - kStageBytes - kRopeBytes - p.latent / 64 * kABlock) / stage;
+  p.k_cols = (p.heads * nope + 31) / 32 * 32;
+  p.v_cols = p.heads * a.dh;
+  p.one = p.k_cols % 64 == 0;
+  p.k_boxes = p.one ? 0 : (p.k_cols / 2 + 63) / 64;
+  p.boxes = p.one ? ((p.k_cols + p.v_cols) / 2 + 63) / 64 : p.k_boxes + (p.v_cols / 2 + 63) / 64;
+  const int stages = (kSmemBytes - kSmallBytes - kStageBytes - kRopeBytes - p.latent / 64 * kABlock) / (p.boxes * kBox);
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   static SmemOnce once;
   cudaError_t e = allow_smem(expand_tile_kernel, kSmemBytes, dev.device, &once);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
+  cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // the pairs that are resident at once, asked for once a device
+  static int resident[128];
+  int pairs = dev.device >= 0 && dev.device < 128 ? resident[dev.device] : 0;
+  if (pairs == 0) {
+    e = cudaOccupancyMaxActiveClusters(&pairs, expand_tile_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) {
+      *msg = "(pairs of blocks cannot be resident)";
+      return cudaErrorInvalidValue;
+    }
+    if (dev.device >= 0 && dev.device < 128) resident[dev.device] = pairs;      // (two threads may both: no harm)
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, p);
   if (e == cudaSuccess) count_launches(1);
   return e;

@@ -18,11 +18,12 @@ struct SpanRange {
   int b, first;
 };
 
-// Called by all kThreads threads of the block; false if the block has nothing to do. units(b) >= 0. A
-// batch of more units than can be numbered is left out (only numbers that the host cannot see
-// bring one).
-template <int kThreads, typename F>
-__device__ bool span_locate(int B, F units, SpanScratch* sm, SpanRange* r) {
+// Counts all units, asks want(total) for the number of one of them (the same in every thread; below 0: none),
+// and finds the sequence that holds it. Called by all kThreads threads of the block; false if
+// there is none, or if there are more units than can be numbered (only numbers that the host cannot see
+// bring that). units(b) >= 0.
+template <int kThreads, typename F, typename G>
+__device__ bool span_find(int B, F units, SpanScratch* sm, G want, int* seq, int* first) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (B + kThreads - 1) / kThreads;
   const int b0 = min(tid * each, B), b1 = min(b0 + each, B);
@@ -44,17 +45,14 @@ __device__ bool span_locate(int B, F units, SpanScratch* sm, SpanRange* r) {
     total = count_add(total, sm->scan[i]);
   }
   if (total == kCountLimit || total == 0) return false;
-  const int blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
-  const int per = total / blocks, more = total % blocks;     // the first `more` blocks take one more
-  r->g0 = per * block + min(block, more);
-  r->g1 = r->g0 + per + (block < more ? 1 : 0);
-  if (r->g0 >= r->g1) return false;
+  const int g = want(total);
+  if (g < 0) return false;
   int at = before + incl - mine;
-  if (r->g0 >= at && r->g0 - at < mine) {
+  if (g >= at && g - at < mine) {
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int u = units(b);
-      if (r->g0 - at < u) {
+      if (g - at < u) {
         sm->b = b;
         sm->first = at;
         break;
@@ -63,9 +61,24 @@ __device__ bool span_locate(int B, F units, SpanScratch* sm, SpanRange* r) {
     }
   }
   __syncthreads();
-  r->b = sm->b;
-  r->first = sm->first;
+  *seq = sm->b;
+  *first = sm->first;
   return true;
+}
+
+// The block's equal range of all units; false if it has nothing to do.
+template <int kThreads, typename F>
+__device__ bool span_locate(int B, F units, SpanScratch* sm, SpanRange* r) {
+  return span_find<kThreads>(
+      B, units, sm,
+      [&](int total) {
+        const int blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+        const int per = total / blocks, more = total % blocks;     // the first `more` blocks take one more
+        r->g0 = per * block + min(block, more);
+        r->g1 = r->g0 + per + (block < more ? 1 : 0);
+        return r->g0 < r->g1 ? r->g0 : -1;
+      },
+      &r->b, &r->first);
 }
 
 }  // namespace cxa
