@@ -17,9 +17,10 @@
 //  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
 //    copies are counted by the even block's barriers.
 //  * warp 4 of the even block issues the products.
-//  * warps 0 to 3 take the sums out, a position a lane, round them, and turn them round through shared
-//    memory, 64 channels at a time, so that 8 lanes write a row's 128 bytes together; the rotated part, the same
-//    in every head, is put in front on the way.
+//  * warps 0 to 3 take the sums out, a position a lane, round them and put them, 64 channels at a time, into
+//    shared memory, from where a bulk tensor store writes the rows of a page (rows of which some are not to be
+//    written: 8 lanes write a row's 128 bytes). The rotated part, the same in every head, stays in a buffer
+//    of its own.
 //
 // Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
 #include <cuda.h>
@@ -74,7 +75,8 @@ struct TileParams {
 
 __global__ void __launch_bounds__(kThreads, 1)
     expand_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap toK,
+                       const __grid_constant__ CUtensorMap toV, const __grid_constant__ TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int a_blocks = p.latent / 64, boxes = p.boxes;
   const uint32_t a_base = smem_u32(smem), b_base = a_base + a_blocks * kABlock;
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row = ((static_cast<long long>(sp) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * (p.latent + p.rope);
           }
         }
+        bulk_wait_group_read<0>();
         __syncwarp();
 #pragma unroll 4
         for (int j = 0; j < rope_pieces; ++j) {
@@ -288,13 +291,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int nh = min(p.heads, p.H - grp * p.heads);
       const uint32_t d = my_tmem + (i & 1) * 256;
-      // 64 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's
-      auto put = [&](__nv_bfloat16* pool, int h, int c0, int skip, uint32_t col) {
+      // the rows of all 32 lanes go out: a bulk store for each 32 or 16 of them (a page's)
+      const bool whole = __all_sync(0xffffffffu, dst >= 0 && w.ok);
+      const bool stores = (lane & ((1 << min(p.to_shift, 5)) - 1)) == 0;
+      // 64 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's.
+      // They stand in a buffer of 32 rows of 128 bytes, the rotated part's own if it has some of them.
+      auto put = [&](const CUtensorMap* map, __nv_bfloat16* pool, int h, int c0, int skip, uint32_t col) {
+        const uint32_t buf = skip > 0 ? rotated : stage;
         uint32_t x[4][16];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (q * 16 >= skip) tmem_ld_32x32b_x16(col + q * 16, x[q]);
+        bulk_wait_group_read<0>();      // the buffer's last store has read it
         tmem_ld_wait();
+        __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (q * 16 >= skip)
@@ -304,33 +314,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int f = 0; f < 4; ++f)
                 v[f] = pack_bf16(__uint_as_float(x[q][8 * e + 2 * f]), __uint_as_float(x[q][8 * e + 2 * f + 1]));
-              st_shared_v4(stage + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+              st_shared_v4(buf + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
             }
-        __syncwarp();
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (stores) {
+            tma_store_3d(map, buf + lane * 128, c0, slot, dst * p.H + h);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int r = n * 4 + sub;
-          const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
-          const uint4 v = ld_shared_v4((piece * 8 < skip ? rotated : stage) + r * 128 + ((piece ^ (r & 7)) << 4));
-          if (to >= 0 && w.ok)
-            *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
-                                      piece * 8) = v;
+          for (int n = 0; n < 8; ++n) {
+            const int r = n * 4 + sub;
+            const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
+            const uint4 v = ld_shared_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+            if (to >= 0 && w.ok)
+              *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
+                                        piece * 8) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       };
       for (int j = 0; j < nh; ++j) {
         const int h = grp * p.heads + j;
         for (int c0 = 0; c0 < p.dh; c0 += 64) {
           const int skip = min(64, max(0, p.rope - c0));
           // (a channel c of K stands in column j * nope + c - rope)
-          put(p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
+          put(&toK, p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
         }
-        for (int c0 = 0; c0 < p.dh; c0 += 64) put(p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
+        for (int c0 = 0; c0 < p.dh; c0 += 64) put(&toV, p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(w.bar(kDFree + (i & 1)), 0);      // the even block's products wait for both
     }
+    bulk_wait_group_all();
   }
   tc_fence_before();
   cluster_sync();      // neither block leaves while the pair's products or arrivals may still touch it
@@ -357,11 +377,15 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   if (!a.bf16) return launch_expand_rows(a, dev, stream);
   const int width = a.layer.latent + a.layer.rope, page_size = 1 << a.layer.page_shift, H = a.to.Hkv;
   const int nope = a.dh - a.layer.rope;
-  CUtensorMap c, k, v;
+  CUtensorMap c, k, v, to_k, to_v;
+  const int to_page = 1 << a.to.page_shift, out_rows = to_page < 32 ? to_page : 32;
+  const cuuint64_t slabs = static_cast<cuuint64_t>(a.to.num_pages) * H, row = static_cast<cuuint64_t>(a.dh) * 2;
   if (!encode_tiles(&c, a.layer.C, width, page_size, a.layer.num_pages, static_cast<cuuint64_t>(width) * 2,
                     static_cast<cuuint64_t>(page_size) * width * 2, page_size < kRows ? page_size : kRows, 1) ||
-      !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh)) {
-    *msg = "(the tensor maps of the pool and the weights cannot be encoded)";
+      !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh) ||
+      !encode_tiles(&to_k, a.to.K, a.dh, to_page, slabs, row, row * to_page, out_rows, 1) ||
+      !encode_tiles(&to_v, a.to.V, a.dh, to_page, slabs, row, row * to_page, out_rows, 1)) {
+    *msg = "(the tensor maps of the pools and the weights cannot be encoded)";
     return cudaErrorInvalidValue;
   }
   TileParams p;
@@ -427,7 +451,7 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   }
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, p);
+  e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, to_k, to_v, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
