@@ -7,8 +7,7 @@
 // columns, in two buffers. Each block holds its own positions and streams half of the columns' weights: half the
 // traffic of blocks by themselves (which took 183 us for 32768 positions, 20 heads of 128, 512 + 64 channels).
 // Weights are taken as they are, [latent][columns]: an operand across the channels (MN-major) needs no copy
-// of theirs turned round. Where the columns of WK fill blocks of 64, both parts go through one product,
-// otherwise through one each.
+// of theirs turned round.
 //
 // All (pairs of tiles, g heads) are numbered densely, positions first, and a pair takes an equal range of them. The
 // positions' latent rows stay in shared memory over all heads (128 KB of 512 channels); what streams are the
@@ -17,9 +16,9 @@
 //  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
 //    copies are counted by the even block's barriers.
 //  * warp 4 of the even block issues the products.
-//  * warps 0 to 3 take the sums out, a position a lane, round them and put them, 64 channels at a time, into
+//  * warps 0 to 3 take the sums out, a position a lane, round them and put them, 32 channels at a time, into
 //    shared memory, from where a bulk tensor store writes the rows of a page (rows of which some are not to be
-//    written: 8 lanes write a row's 128 bytes). The rotated part, the same in every head, stays in a buffer
+//    written: 4 lanes write a row's 64 bytes). The rotated part, the same in every head, stays in buffers
 //    of its own.
 //
 // Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
@@ -38,9 +37,10 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kThreads = 6 * 32, kMmaWarp = 4, kTmaWarp = 5;
 constexpr int kABlock = 16384;            // 64 channels of 128 positions
-constexpr int kBox = 8192;                // 64 channels of 64 columns of the weights
+constexpr int kBox = 4096;                // 64 channels of 32 columns of the weights
 constexpr int kMaxStages = 16, kMaxA = 8;
-constexpr int kStageBytes = 4 * 4096, kRopeBytes = 4 * 4096;      // of the four warps: 32 rows of 128 bytes
+constexpr int kPut = 32, kPutBytes = 32 * 64;      // channels that a warp stores at once: 32 rows of 64 bytes
+constexpr int kStageBytes = 2 * 4 * kPutBytes, kRopeBytes = 2 * 4 * kPutBytes;      // two buffers of each warp
 constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
 
 enum Bars {
@@ -69,8 +69,7 @@ struct TileParams {
   const int *from, *kv_len, *table, *to_table;
   int heads, groups;         // heads of a product, and how many of those there are
   int k_cols, v_cols;        // columns of a product
-  int one;                   // both parts through one product
-  int boxes, k_boxes, stages;      // boxes of a stage in a block, those of WK (by itself) among them
+  int boxes, stages;         // boxes of a stage in a block
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -169,17 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int h0 = grp * p.heads;
       // where this block's half of the columns begins, by the box of this lane
-      int col = 0;
-      bool v = false;
-      if (p.one) {
-        const int c = static_cast<int>(rank) * (p.k_cols + p.v_cols) / 2 + lane * 64;
-        v = c >= p.k_cols;
-        col = v ? h0 * p.dh + c - p.k_cols : h0 * nope + c;
-      } else {
-        v = lane >= p.k_boxes;
-        col = v ? h0 * p.dh + static_cast<int>(rank) * p.v_cols / 2 + (lane - p.k_boxes) * 64
-                : h0 * nope + static_cast<int>(rank) * p.k_cols / 2 + lane * 64;
-      }
+      const int c = static_cast<int>(rank) * (p.k_cols + p.v_cols) / 2 + lane * 32;
+      const bool v = c >= p.k_cols;
+      const int col = v ? h0 * p.dh + c - p.k_cols : h0 * nope + c;
       for (int k = 0; k < a_blocks; ++k) {
         if (fresh) {
           if (!w.warp(kAEmpty + k, tile & 1, kStatusTimeout)) break;      // (the first passes: tile is 1)
@@ -213,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint64_t hi = desc_high(1024);
-    const uint32_t n0 = static_cast<uint32_t>(p.one ? p.k_cols + p.v_cols : p.k_cols);
-    const uint32_t idesc_0 = make_idesc(1u, 2 * kRows, n0) | 1u << 16;
-    const uint32_t idesc_v = make_idesc(1u, 2 * kRows, static_cast<uint32_t>(p.v_cols)) | 1u << 16;
+    // the weights' blocks: 32 columns in rows of 64 bytes with a swizzle of that width, 8 rows 512 bytes apart
+    constexpr uint64_t w_hi = static_cast<uint64_t>(512u >> 4 | 1u << 14 | 4u << 29) << 32;
+    const uint32_t idesc = make_idesc(1u, 2 * kRows, static_cast<uint32_t>(p.k_cols + p.v_cols)) | 1u << 16;
     int stage = 0, tile = 0;
     uint32_t round = 0;
     for (int g = g0, i = 0; even && g < g1 && w.ok; ++g, ++i) {
@@ -223,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool fresh = g == g0 || grp == 0, last = g + 1 == g1 || grp + 1 == p.groups;
       tile += fresh ? 1 : 0;
       if (!w.warp(kDFree + (i & 1), ((i >> 1) & 1) ^ 1, kStatusTimeout)) break;
-      const uint32_t d = tmem + (i & 1) * 256, dv = d + p.k_cols;
+      const uint32_t d = tmem + (i & 1) * 256;
       for (int k = 0; k < a_blocks; ++k) {
         if (fresh && !w.warp(kAFull + k, (tile - 1) & 1, kStatusTimeout)) break;
         if (!w.warp(kBFull + stage, round & 1, kStatusTimeout)) break;
@@ -231,12 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           const uint32_t al = desc_low(a_base + k * kABlock, 16);
           const uint32_t bl = desc_low(b_base + stage * boxes * kBox, kBox);
-          const uint32_t vl = bl + static_cast<uint32_t>(p.k_boxes * kBox >> 4);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {      // 16 channels: 32 bytes of a row, 16 rows of the weights
-            mma_bf16_pair(d, hi | (al + 2 * s), hi | (bl + s * (2048 >> 4)), idesc_0, k + s != 0 ? 1u : 0u);
-            if (!p.one) mma_bf16_pair(dv, hi | (al + 2 * s), hi | (vl + s * (2048 >> 4)), idesc_v, k + s != 0 ? 1u : 0u);
-          }
+          for (int s = 0; s < 4; ++s)      // 16 channels: 32 bytes of a position's row, 16 rows of the weights
+            mma_bf16_pair(d, hi | (al + 2 * s), w_hi | (bl + s * (1024 >> 4)), idesc, k + s != 0 ? 1u : 0u);
           tc_commit_pair(w.bar(kBEmpty + stage), 0x3);
           if (last) tc_commit_pair(w.bar(kAEmpty + k), 0x3);
           if (k + 1 == a_blocks) tc_commit_pair(w.bar(kDFull + (i & 1)), 0x3);
@@ -252,11 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // a position a lane
     const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const uint32_t stage = s_base + warp * 4096, rotated = r_base + warp * 4096;
-    const int sub = lane >> 3, piece = lane & 7;
-    const int rope_pieces = p.rope / 8;
+    const int sub = lane >> 2, piece = lane & 3;
+    // where 16-byte piece j of a row stands in a buffer, and the buffers of the rotated part's channels c ..
+    auto place = [](int row, int j) { return static_cast<uint32_t>(row * 64 + ((j ^ (row >> 1 & 3)) << 4)); };
+    auto rotated = [&](int c) { return r_base + (warp * 2 + c / kPut) * kPutBytes; };
     int dst = -1;              // row of head 0 of this lane's position, in units of dh (pool rows)
-    int slot = 0;
+    int slot = 0, turn = 0;
     for (int g = g0, i = 0; g < g1; ++g, ++i) {
       const int grp = g % p.groups;
       long long row = -1;
@@ -280,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait_group_read<0>();
         __syncwarp();
 #pragma unroll 4
-        for (int j = 0; j < rope_pieces; ++j) {
+        for (int c = 0; c < p.rope; c += 8) {
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + j * 8);
-          st_shared_v4(rotated + lane * 128 + ((j ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+          if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + c);
+          st_shared_v4(rotated(c) + place(lane, c % kPut / 8), v.x, v.y, v.z, v.w);
         }
         __syncwarp();
       }
@@ -294,19 +283,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the rows of all 32 lanes go out: a bulk store for each 32 or 16 of them (a page's)
       const bool whole = __all_sync(0xffffffffu, dst >= 0 && w.ok);
       const bool stores = (lane & ((1 << min(p.to_shift, 5)) - 1)) == 0;
-      // 64 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's.
-      // They stand in a buffer of 32 rows of 128 bytes, the rotated part's own if it has some of them.
+      // 32 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's.
+      // They stand in a buffer of 32 rows of 64 bytes, the rotated part's own if it has some of them.
       auto put = [&](const CUtensorMap* map, __nv_bfloat16* pool, int h, int c0, int skip, uint32_t col) {
-        const uint32_t buf = skip > 0 ? rotated : stage;
-        uint32_t x[4][16];
+        const uint32_t buf = skip > 0 ? rotated(c0) : s_base + ((turn & 1) * 4 + warp) * kPutBytes;
+        turn += skip > 0 ? 0 : 1;
+        uint32_t x[2][16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
           if (q * 16 >= skip) tmem_ld_32x32b_x16(col + q * 16, x[q]);
-        bulk_wait_group_read<0>();      // the buffer's last store has read it
+        bulk_wait_group_read<1>();      // the buffer's last store, which is not the one before this, has read it
         tmem_ld_wait();
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
           if (q * 16 >= skip)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -314,22 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int f = 0; f < 4; ++f)
                 v[f] = pack_bf16(__uint_as_float(x[q][8 * e + 2 * f]), __uint_as_float(x[q][8 * e + 2 * f + 1]));
-              st_shared_v4(buf + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+              st_shared_v4(buf + place(lane, 2 * q + e), v[0], v[1], v[2], v[3]);
             }
         if (whole) {
           fence_proxy_async_smem();
           __syncwarp();
           if (stores) {
-            tma_store_3d(map, buf + lane * 128, c0, slot, dst * p.H + h);
+            tma_store_3d(map, buf + lane * 64, c0, slot, dst * p.H + h);
             bulk_commit_group();
           }
         } else {
           __syncwarp();
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int r = n * 4 + sub;
+          for (int n = 0; n < 4; ++n) {
+            const int r = n * 8 + sub;
             const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
-            const uint4 v = ld_shared_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+            const uint4 v = ld_shared_v4(buf + place(r, piece));
             if (to >= 0 && w.ok)
               *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
                                         piece * 8) = v;
@@ -339,12 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int j = 0; j < nh; ++j) {
         const int h = grp * p.heads + j;
-        for (int c0 = 0; c0 < p.dh; c0 += 64) {
-          const int skip = min(64, max(0, p.rope - c0));
+        for (int c0 = 0; c0 < p.dh; c0 += kPut) {
+          const int skip = min(kPut, max(0, p.rope - c0));
           // (a channel c of K stands in column j * nope + c - rope)
           put(&toK, p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
         }
-        for (int c0 = 0; c0 < p.dh; c0 += 64) put(&toV, p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
+        for (int c0 = 0; c0 < p.dh; c0 += kPut) put(&toV, p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
       }
       tc_fence_before();
       __syncwarp();
@@ -358,15 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-// A 2-D bf16 map of boxes of 64 columns by 64 rows of a [rows][cols] matrix.
+// A 2-D bf16 map of boxes of 32 columns by 64 rows of a [rows][cols] matrix.
 bool encode_weights(CUtensorMap* map, const void* ptr, int rows, int cols) {
   const EncodeTiledFn fn = tensor_map_encoder();
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {32, 64}, estr[2] = {1, 1};
   return fn != nullptr &&
          fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -383,8 +373,8 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   if (!encode_tiles(&c, a.layer.C, width, page_size, a.layer.num_pages, static_cast<cuuint64_t>(width) * 2,
                     static_cast<cuuint64_t>(page_size) * width * 2, page_size < kRows ? page_size : kRows, 1) ||
       !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh) ||
-      !encode_tiles(&to_k, a.to.K, a.dh, to_page, slabs, row, row * to_page, out_rows, 1) ||
-      !encode_tiles(&to_v, a.to.V, a.dh, to_page, slabs, row, row * to_page, out_rows, 1)) {
+      !encode_boxes(&to_k, a.to.K, a.dh, to_page, slabs, row, row * to_page, kPut, out_rows, 1) ||
+      !encode_boxes(&to_v, a.to.V, a.dh, to_page, slabs, row, row * to_page, kPut, out_rows, 1)) {
     *msg = "(the tensor maps of the pools and the weights cannot be encoded)";
     return cudaErrorInvalidValue;
   }
@@ -415,9 +405,7 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   p.groups = (H + p.heads - 1) / p.heads;
   p.k_cols = (p.heads * nope + 31) / 32 * 32;
   p.v_cols = p.heads * a.dh;
-  p.one = p.k_cols % 64 == 0;
-  p.k_boxes = p.one ? 0 : (p.k_cols / 2 + 63) / 64;
-  p.boxes = p.one ? ((p.k_cols + p.v_cols) / 2 + 63) / 64 : p.k_boxes + (p.v_cols / 2 + 63) / 64;
+  p.boxes = ((p.k_cols + p.v_cols) / 2 + 31) / 32;
   const int stages = (kSmemBytes - kSmallBytes - kStageBytes - kRopeBytes - p.latent / 64 * kABlock) / (p.boxes * kBox);
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   static SmemOnce once;
