@@ -2,24 +2,26 @@
 //
 //   K_h(t) = [ r_t | c_t WK_h ],  V_h(t) = c_t WV_h
 //
-// Two blocks work as a pair (cta_group::2) on two tiles of 128 positions, of any sequences, by the columns
-// of a few heads, those of WK and those of WV side by side in tensor memory: g heads with g (2 dh - rope) <= 256
-// columns, in two buffers. Each block holds its own positions and streams half of the columns' weights: half the
-// traffic of blocks by themselves (which took 183 us for 32768 positions, 20 heads of 128, 512 + 64 channels).
-// Weights are taken as they are, [latent][columns]: an operand across the channels (MN-major) needs no copy
-// of theirs turned round.
+// Two blocks work as a pair (cta_group::2) on two tiles of 128 positions, of any sequences, by 256 columns. Each block
+// holds its own positions and streams half of the columns' weights: half the traffic of blocks by themselves
+// (which took 183 us for 32768 positions, 20 heads of 128, 512 + 64 channels). The columns are blocks of 64,
+// those of a head's K and V behind each other and heads in turn: any four of them make a product, so that all
+// products are of the full width, whatever heads are made of (products of one head's 192 columns took as long as
+// ones of 256). Weights are taken as they are, [latent][columns]: an operand across the channels
+// (MN-major) needs no copy of theirs turned round, and one along them is no faster.
 //
-// All (pairs of tiles, g heads) are numbered densely, positions first, and a pair takes an equal range of them. The
-// positions' latent rows stay in shared memory over all heads (128 KB of 512 channels); what streams are the
-// weights, 64 channels a stage.
+// All (pairs of tiles, products) are numbered densely, positions first, and a pair takes an equal range of them. The
+// positions' latent rows stay in shared memory over all products (128 KB of 512 channels); what streams are the
+// weights, 64 channels a stage. (Stages of 32 channels, in smaller boxes, take the copy warp longer than the
+// products: 165 us.)
 //
-//  * warp 5 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
+//  * warp 9 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
 //    copies are counted by the even block's barriers.
-//  * warp 4 of the even block issues the products.
-//  * warps 0 to 3 take the sums out, a position a lane, round them and put them, 32 channels at a time, into
-//    shared memory, from where a bulk tensor store writes the rows of a page (rows of which some are not to be
-//    written: 4 lanes write a row's 64 bytes). The rotated part, the same in every head, stays in buffers
-//    of its own.
+//  * warp 8 of the even block issues the products, into two buffers of tensor memory.
+//  * warps 0 to 7 take the sums out, a position a lane and every other 32 columns a group of four warps, round
+//    them and put them into shared memory, from where a bulk tensor store writes the rows of a page (rows of
+//    which some are not to be written: 4 lanes write a row's 64 bytes). The rotated part, the same in every head,
+//    stays in buffers of its own. (Four warps: 118 us, all of which they were busy.)
 //
 // Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
 #include <cuda.h>
@@ -35,12 +37,16 @@ namespace cxa {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kThreads = 6 * 32, kMmaWarp = 4, kTmaWarp = 5;
+constexpr int kOutWarps = 8, kMmaWarp = kOutWarps, kTmaWarp = kMmaWarp + 1, kThreads = (kTmaWarp + 1) * 32;
+constexpr int kBlocks = 4, kCols = 64;    // blocks of a product, and columns of a block
+constexpr int kPut = 32;                  // columns that a warp takes out at once
 constexpr int kABlock = 16384;            // 64 channels of 128 positions
-constexpr int kBox = 4096;                // 64 channels of 32 columns of the weights
+constexpr int kStep = 64;                 // channels of a stage of the weights
+constexpr int kBox = kStep * kCols * 2;   // of a block
+constexpr int kStage = kBlocks / 2 * kBox;
 constexpr int kMaxStages = 16, kMaxA = 8;
-constexpr int kPut = 32, kPutBytes = 32 * 64;      // channels that a warp stores at once: 32 rows of 64 bytes
-constexpr int kStageBytes = 2 * 4 * kPutBytes, kRopeBytes = 2 * 4 * kPutBytes;      // two buffers of each warp
+constexpr int kPutBytes = 32 * kPut * 2;  // 32 rows of them, as they are written
+constexpr int kOutBytes = kOutWarps * kPutBytes;
 constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
 
 enum Bars {
@@ -67,9 +73,9 @@ struct TileParams {
   int B, num_pages, page_shift, width, latent, rope;
   int to_pages, to_shift, to_width, H, dh;
   const int *from, *kv_len, *table, *to_table;
-  int heads, groups;         // heads of a product, and how many of those there are
-  int k_cols, v_cols;        // columns of a product
-  int boxes, stages;         // boxes of a stage in a block
+  int k_blocks, head_blocks, blocks, products;      // blocks of a head's K, of a head, of all heads
+  int k_first;               // the first channel of K's blocks
+  int stages;
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -77,9 +83,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap toK,
                        const __grid_constant__ CUtensorMap toV, const __grid_constant__ TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int a_blocks = p.latent / 64, boxes = p.boxes;
+  const int a_blocks = p.latent / 64, steps = a_blocks;
   const uint32_t a_base = smem_u32(smem), b_base = a_base + a_blocks * kABlock;
-  const uint32_t s_base = b_base + p.stages * boxes * kBox, r_base = s_base + kStageBytes;
+  const uint32_t s_base = b_base + p.stages * kStage, r_base = s_base + kOutBytes;
   Small* sm = reinterpret_cast<Small*>(smem + kSmemBytes - kSmallBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nope = p.dh - p.rope;
@@ -97,18 +103,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!span_find<kThreads>(
           p.B, tiles, &sm->span,
           [&](int n) {
-            const long long pairs = static_cast<long long>(n + 1) / 2 * p.groups, by = gridDim.x / 2, at = blockIdx.x / 2;
+            const long long pairs = static_cast<long long>(n + 1) / 2 * p.products, by = gridDim.x / 2, at = blockIdx.x / 2;
             total = n;
             if (pairs > 0x7FFFFFFFLL - 1024) return -1;
             g0 = static_cast<int>(pairs / by * at + min(at, pairs % by));
             g1 = g0 + static_cast<int>(pairs / by + (at < pairs % by ? 1 : 0));
-            return g0 < g1 ? g0 / p.groups * 2 : -1;
+            return g0 < g1 ? g0 / p.products * 2 : -1;
           },
           &b, &first))
     return;
   Waits w = {smem_u32(sm->bars), &sm->abort, p.status, true};
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(w.bar(i), i >= kDFree ? 8 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(w.bar(i), i >= kDFree ? 2 * kOutWarps : 1);
     fence_mbar_init();
     sm->abort = 0;
   }
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();      // both blocks' barriers are there before anything arrives from the other
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(sm->tmem), 0);
 
   // To tile i of all (i < total, not before the last one asked for): b is its sequence.
   auto seek = [&](int i) {
@@ -141,14 +147,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0, tile = 0, page = -1, y = 0;
     uint32_t round = 0, armed = 0, parity = 0, a_armed = 0, a_parity = 0, a_bytes = 0;
     for (int g = g0; g < g1 && w.ok; ++g) {
-      const int grp = g % p.groups;
+      const int grp = g % p.products;
       const bool fresh = g == g0 || grp == 0;
       if (fresh) {
         // the boxes of both blocks' tiles, a lane each: the even block counts them all
         page = -1;
         int boxes_there = 0;
         for (int t = 0; t < 2; ++t) {
-          const int i = g / p.groups * 2 + t;
+          const int i = g / p.products * 2 + t;
           int got = -1, slot = 0;
           if (i < total) {
             const int at = seek(i) + lane * box_rows;
@@ -166,12 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         a_bytes = static_cast<uint32_t>(boxes_there * box_rows * 128);
         ++tile;
       }
-      const int h0 = grp * p.heads;
-      // where this block's half of the columns begins, by the box of this lane
-      const int c = static_cast<int>(rank) * (p.k_cols + p.v_cols) / 2 + lane * 32;
-      const bool v = c >= p.k_cols;
-      const int col = v ? h0 * p.dh + c - p.k_cols : h0 * nope + c;
-      for (int k = 0; k < a_blocks; ++k) {
+      // this block's half of the columns: a block of them a lane
+      const int id = grp * kBlocks + static_cast<int>(rank) * (kBlocks / 2) + lane, h = id / p.head_blocks, j = id % p.head_blocks;
+      const bool mine = lane < kBlocks / 2 && id < p.blocks, v = j >= p.k_blocks;
+      const int col = v ? h * p.dh + (j - p.k_blocks) * kCols : h * nope + p.k_first - p.rope + j * kCols;
+      const uint32_t b_bytes = static_cast<uint32_t>(min(kBlocks, p.blocks - grp * kBlocks) * kBox);
+      for (int k = 0; k < steps; ++k) {
         if (fresh) {
           if (!w.warp(kAEmpty + k, tile & 1, kStatusTimeout)) break;      // (the first passes: tile is 1)
           if (even && lane == 0) mbar_arrive_expect_tx(w.bar(kAFull + k), a_bytes);
@@ -183,11 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           a_parity = (a_parity & ~(1u << k)) | (static_cast<uint32_t>(tile - 1) & 1u) << k;
         }
         if (!w.warp(kBEmpty + stage, (round & 1) ^ 1, kStatusTimeout)) break;
-        if (even && lane == 0) mbar_arrive_expect_tx(w.bar(kBFull + stage), static_cast<uint32_t>(2 * boxes * kBox));
+        if (even && lane == 0) mbar_arrive_expect_tx(w.bar(kBFull + stage), b_bytes);
         __syncwarp();
-        if (lane < boxes)
-          tma_load_2d_pair(b_base + (stage * boxes + lane) * kBox, v ? &tmV : &tmK, mapa_shared(w.bar(kBFull + stage), 0),
-                           col, k * 64);
+        if (mine)
+          tma_load_2d_pair(b_base + stage * kStage + lane * kBox, v ? &tmV : &tmK, mapa_shared(w.bar(kBFull + stage), 0), col,
+                           k * kStep);
         armed |= 1u << stage;
         parity = (parity & ~(1u << stage)) | (round & 1u) << stage;
         if (++stage == p.stages) {
@@ -204,30 +210,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint64_t hi = desc_high(1024);
-    // the weights' blocks: 32 columns in rows of 64 bytes with a swizzle of that width, 8 rows 512 bytes apart
-    constexpr uint64_t w_hi = static_cast<uint64_t>(512u >> 4 | 1u << 14 | 4u << 29) << 32;
-    const uint32_t idesc = make_idesc(1u, 2 * kRows, static_cast<uint32_t>(p.k_cols + p.v_cols)) | 1u << 16;
+    const uint32_t idesc = make_idesc(1u, 2 * kRows, kBlocks * kCols) | 1u << 16;
     int stage = 0, tile = 0;
     uint32_t round = 0;
     for (int g = g0, i = 0; even && g < g1 && w.ok; ++g, ++i) {
-      const int grp = g % p.groups;
-      const bool fresh = g == g0 || grp == 0, last = g + 1 == g1 || grp + 1 == p.groups;
+      const int grp = g % p.products;
+      const bool fresh = g == g0 || grp == 0, last = g + 1 == g1 || grp + 1 == p.products;
       tile += fresh ? 1 : 0;
       if (!w.warp(kDFree + (i & 1), ((i >> 1) & 1) ^ 1, kStatusTimeout)) break;
-      const uint32_t d = tmem + (i & 1) * 256;
-      for (int k = 0; k < a_blocks; ++k) {
+      for (int k = 0; k < steps; ++k) {
         if (fresh && !w.warp(kAFull + k, (tile - 1) & 1, kStatusTimeout)) break;
         if (!w.warp(kBFull + stage, round & 1, kStatusTimeout)) break;
         tc_fence_after();
+        // (known to be the same in every lane, the operands' addresses need no carrying over from one)
+        const int at = __shfl_sync(0xffffffffu, stage | k << 8 | (i & 1) << 16, 0);
+        const uint32_t al = desc_low(a_base + (at >> 8 & 255) * kABlock, 16), bl = desc_low(b_base + (at & 255) * kStage, kBox);
+        const uint32_t d = tmem + (at >> 16) * 256, first_k = (at >> 8 & 255) == 0 ? 0u : 1u;
         if (elect_one()) {
-          const uint32_t al = desc_low(a_base + k * kABlock, 16);
-          const uint32_t bl = desc_low(b_base + stage * boxes * kBox, kBox);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)      // 16 channels: 32 bytes of a position's row, 16 rows of the weights
-            mma_bf16_pair(d, hi | (al + 2 * s), w_hi | (bl + s * (1024 >> 4)), idesc, k + s != 0 ? 1u : 0u);
+          for (int s = 0; s < kStep / 16; ++s)      // 16 channels: 32 bytes of a position's row, 16 rows of the weights
+            mma_bf16_pair(d, hi | (al + 2 * s), hi | (bl + s * (2048 >> 4)), idesc, s != 0 ? 1u : first_k);
           tc_commit_pair(w.bar(kBEmpty + stage), 0x3);
           if (last) tc_commit_pair(w.bar(kAEmpty + k), 0x3);
-          if (k + 1 == a_blocks) tc_commit_pair(w.bar(kDFull + (i & 1)), 0x3);
+          if (k + 1 == steps) tc_commit_pair(w.bar(kDFull + (i & 1)), 0x3);
         }
         __syncwarp();
         if (++stage == p.stages) {
@@ -238,20 +243,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // a position a lane
-    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // a position a lane, every other block of columns
+    const int quad = warp & 3, grp_of = warp >> 2;
+    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int sub = lane >> 2, piece = lane & 3;
     // where 16-byte piece j of a row stands in a buffer, and the buffers of the rotated part's channels c ..
     auto place = [](int row, int j) { return static_cast<uint32_t>(row * 64 + ((j ^ (row >> 1 & 3)) << 4)); };
-    auto rotated = [&](int c) { return r_base + (warp * 2 + c / kPut) * kPutBytes; };
+    auto rotated = [&](int c) { return r_base + (c / kPut * 4 + quad) * kPutBytes; };
+    const uint32_t buf = s_base + warp * kPutBytes;
+    auto quad_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
     int dst = -1;              // row of head 0 of this lane's position, in units of dh (pool rows)
-    int slot = 0, turn = 0;
+    int slot = 0;
     for (int g = g0, i = 0; g < g1; ++g, ++i) {
-      const int grp = g % p.groups;
+      const int grp = g % p.products;
       long long row = -1;
       if (g == g0 || grp == 0) {
-        const int mine = g / p.groups * 2 + static_cast<int>(rank);
-        const int t = mine < total ? seek(mine) + warp * 32 + lane : 0;
+        const int mine = g / p.products * 2 + static_cast<int>(rank);
+        const int t = mine < total ? seek(mine) + quad * 32 + lane : 0;
         dst = -1;
         slot = t & ((1 << p.to_shift) - 1);
         const ExpandSpan span = mine < total ? expand_span(p.from, p.kv_len, cap, b) : ExpandSpan{0, 0};
@@ -267,59 +275,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         bulk_wait_group_read<0>();
-        __syncwarp();
+        quad_sync();         // neither warp's stores read the rotated part of the tile before
+        if (grp_of == 0) {
 #pragma unroll 4
-        for (int c = 0; c < p.rope; c += 8) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + c);
-          st_shared_v4(rotated(c) + place(lane, c % kPut / 8), v.x, v.y, v.z, v.w);
+          for (int c = 0; c < p.rope; c += 8) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + c);
+            st_shared_v4(rotated(c) + place(lane, c % kPut / 8), v.x, v.y, v.z, v.w);
+          }
+          fence_proxy_async_smem();
         }
-        __syncwarp();
+        quad_sync();
       }
       w.warp(kDFull + (i & 1), (i >> 1) & 1, kStatusTimeout);
       tc_fence_after();
-      const int nh = min(p.heads, p.H - grp * p.heads);
       const uint32_t d = my_tmem + (i & 1) * 256;
       // the rows of all 32 lanes go out: a bulk store for each 32 or 16 of them (a page's)
       const bool whole = __all_sync(0xffffffffu, dst >= 0 && w.ok);
       const bool stores = (lane & ((1 << min(p.to_shift, 5)) - 1)) == 0;
-      // 32 channels of a head's K or V, from channel c0 on, whose first `skip` channels are the rotated part's.
-      // They stand in a buffer of 32 rows of 64 bytes, the rotated part's own if it has some of them.
-      auto put = [&](const CUtensorMap* map, __nv_bfloat16* pool, int h, int c0, int skip, uint32_t col) {
-        const uint32_t buf = skip > 0 ? rotated(c0) : s_base + ((turn & 1) * 4 + warp) * kPutBytes;
-        turn += skip > 0 ? 0 : 1;
-        uint32_t x[2][16];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (q * 16 >= skip) tmem_ld_32x32b_x16(col + q * 16, x[q]);
-        bulk_wait_group_read<1>();      // the buffer's last store, which is not the one before this, has read it
-        tmem_ld_wait();
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (q * 16 >= skip)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t v[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                v[f] = pack_bf16(__uint_as_float(x[q][8 * e + 2 * f]), __uint_as_float(x[q][8 * e + 2 * f + 1]));
-              st_shared_v4(buf + place(lane, 2 * q + e), v[0], v[1], v[2], v[3]);
-            }
+      // 32 channels of a head's K or V from a buffer, from channel c0 on
+      auto write = [&](const CUtensorMap* map, __nv_bfloat16* pool, uint32_t from, int h, int c0) {
         if (whole) {
-          fence_proxy_async_smem();
-          __syncwarp();
           if (stores) {
-            tma_store_3d(map, buf + lane * 64, c0, slot, dst * p.H + h);
+            tma_store_3d(map, from + lane * 64, c0, slot, dst * p.H + h);
             bulk_commit_group();
           }
         } else {
-          __syncwarp();
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const int r = n * 8 + sub;
             const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
-            const uint4 v = ld_shared_v4(buf + place(r, piece));
+            const uint4 v = ld_shared_v4(from + place(r, piece));
             if (to >= 0 && w.ok)
               *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
                                         piece * 8) = v;
@@ -327,14 +313,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      for (int j = 0; j < nh; ++j) {
-        const int h = grp * p.heads + j;
-        for (int c0 = 0; c0 < p.dh; c0 += kPut) {
-          const int skip = min(kPut, max(0, p.rope - c0));
-          // (a channel c of K stands in column j * nope + c - rope)
-          put(&toK, p.K, h, c0, skip, d + static_cast<uint32_t>(j * nope + c0 - p.rope));
+#pragma unroll 1
+      for (int n = grp_of; n < kBlocks * kCols / kPut; n += 2) {
+        const int id = grp * kBlocks + n / (kCols / kPut), h = id / p.head_blocks, j = id % p.head_blocks;
+        if (id >= p.blocks) break;
+        const bool is_k = j < p.k_blocks;
+        const int c0 = (is_k ? p.k_first + j * kCols : (j - p.k_blocks) * kCols) + n % (kCols / kPut) * kPut;
+        const int skip = is_k ? min(kPut, max(0, p.rope - c0)) : 0;      // channels of the rotated part
+        // (one that fills whole blocks goes with the first block behind it)
+        if (is_k && j == 0)
+          for (int c = n % (kCols / kPut) * kPut; c < p.k_first; c += kCols) write(&toK, p.K, rotated(c), h, c);
+        if (skip == kPut) {
+          write(&toK, p.K, rotated(c0), h, c0);
+          continue;
         }
-        for (int c0 = 0; c0 < p.dh; c0 += kPut) put(&toV, p.V, h, c0, 0, d + static_cast<uint32_t>(p.k_cols + j * p.dh + c0));
+        uint32_t x[32];
+        tmem_ld_32x32b_x32(d + n * kPut, x);
+        bulk_wait_group_read<0>();      // the buffer's last store has read it
+        tmem_ld_wait();
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t v[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            v[f] = pack_bf16(__uint_as_float(x[8 * e + 2 * f]), __uint_as_float(x[8 * e + 2 * f + 1]));
+          if (e * 8 < skip) {
+            const uint4 r = ld_shared_v4(rotated(c0) + place(lane, e));
+            v[0] = r.x;
+            v[1] = r.y;
+            v[2] = r.z;
+            v[3] = r.w;
+          }
+          st_shared_v4(buf + place(lane, e), v[0], v[1], v[2], v[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        write(is_k ? &toK : &toV, is_k ? p.K : p.V, buf, h, c0);
       }
       tc_fence_before();
       __syncwarp();
@@ -348,15 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
 }
 
-// A 2-D bf16 map of boxes of 32 columns by 64 rows of a [rows][cols] matrix.
+// A 2-D bf16 map of boxes of 64 columns by 64 rows of a [rows][cols] matrix.
 bool encode_weights(CUtensorMap* map, const void* ptr, int rows, int cols) {
   const EncodeTiledFn fn = tensor_map_encoder();
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {32, 64}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {kCols, kStep}, estr[2] = {1, 1};
   return fn != nullptr &&
          fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -398,15 +413,13 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   p.kv_len = a.kv_len;
   p.table = a.table;
   p.to_table = a.to_table;
-  // a pair's product has a multiple of 32 columns: those of WK are filled up (with the next head's, unused)
-  p.heads = 256 / (2 * a.dh - a.layer.rope);
-  if (p.heads > H) p.heads = H;
-  while (p.heads > 1 && (p.heads * nope + 31) / 32 * 32 + p.heads * a.dh > 256) --p.heads;
-  p.groups = (H + p.heads - 1) / p.heads;
-  p.k_cols = (p.heads * nope + 31) / 32 * 32;
-  p.v_cols = p.heads * a.dh;
-  p.boxes = ((p.k_cols + p.v_cols) / 2 + 31) / 32;
-  const int stages = (kSmemBytes - kSmallBytes - kStageBytes - kRopeBytes - p.latent / 64 * kABlock) / (p.boxes * kBox);
+  p.k_first = a.layer.rope / kCols * kCols;
+  p.k_blocks = (a.dh - p.k_first) / kCols;
+  p.head_blocks = p.k_blocks + a.dh / kCols;
+  p.blocks = H * p.head_blocks;
+  p.products = (p.blocks + kBlocks - 1) / kBlocks;
+  const int rope_bytes = (a.layer.rope + kPut - 1) / kPut * 4 * kPutBytes;
+  const int stages = (kSmemBytes - kSmallBytes - kOutBytes - rope_bytes - p.latent / 64 * kABlock) / kStage;
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   static SmemOnce once;
   cudaError_t e = allow_smem(expand_tile_kernel, kSmemBytes, dev.device, &once);
