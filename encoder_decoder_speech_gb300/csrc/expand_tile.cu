@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       w.warp(kDFull + (i & 1), (i >> 1) & 1, kStatusTimeout);
       tc_fence_after();
-      const uint32_t d = my_tmem + (i & 1) * 256;
+      const uint32_t d = my_tmem + (i & 1) * 256 + grp_of * kPut;
       // the rows of all 32 lanes go out: a bulk store for each 32 or 16 of them (a page's)
       const bool whole = __all_sync(0xffffffffu, dst >= 0 && w.ok);
       const bool stores = (lane & ((1 << min(p.to_shift, 5)) - 1)) == 0;
@@ -313,47 +313,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-#pragma unroll 1
-      for (int n = grp_of; n < kBlocks * kCols / kPut; n += 2) {
-        const int id = grp * kBlocks + n / (kCols / kPut), h = id / p.head_blocks, j = id % p.head_blocks;
-        if (id >= p.blocks) break;
-        const bool is_k = j < p.k_blocks;
-        const int c0 = (is_k ? p.k_first + j * kCols : (j - p.k_blocks) * kCols) + n % (kCols / kPut) * kPut;
-        const int skip = is_k ? min(kPut, max(0, p.rope - c0)) : 0;      // channels of the rotated part
-        // (one that fills whole blocks goes with the first block behind it)
-        if (is_k && j == 0)
-          for (int c = n % (kCols / kPut) * kPut; c < p.k_first; c += kCols) write(&toK, p.K, rotated(c), h, c);
-        if (skip == kPut) {
-          write(&toK, p.K, rotated(c0), h, c0);
-          continue;
-        }
-        uint32_t x[32];
-        tmem_ld_32x32b_x32(d + n * kPut, x);
-        bulk_wait_group_read<0>();      // the buffer's last store has read it
+      int h = grp * kBlocks / p.head_blocks, j = grp * kBlocks % p.head_blocks;      // of the product's first block
+      const int there = min(kBlocks, p.blocks - grp * kBlocks);
+      uint32_t x[2][32];
+      tmem_ld_32x32b_x32(d, x[0]);
+#pragma unroll
+      for (int n = 0; n < kBlocks; ++n) {
         tmem_ld_wait();
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t v[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            v[f] = pack_bf16(__uint_as_float(x[8 * e + 2 * f]), __uint_as_float(x[8 * e + 2 * f + 1]));
-          if (e * 8 < skip) {
-            const uint4 r = ld_shared_v4(rotated(c0) + place(lane, e));
-            v[0] = r.x;
-            v[1] = r.y;
-            v[2] = r.z;
-            v[3] = r.w;
-          }
-          st_shared_v4(buf + place(lane, e), v[0], v[1], v[2], v[3]);
+        if (n + 1 < kBlocks) {
+          tmem_ld_32x32b_x32(d + (n + 1) * kCols, x[(n + 1) & 1]);      // under what is done with this one
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(w.bar(kDFree + (i & 1)), 0);      // the even block's products wait for both
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        write(is_k ? &toK : &toV, is_k ? p.K : p.V, buf, h, c0);
+        if (n < there) {
+          const bool is_k = j < p.k_blocks;
+          const int c0 = (is_k ? p.k_first + j * kCols : (j - p.k_blocks) * kCols) + grp_of * kPut;
+          const int skip = is_k && j == 0 ? min(kPut, max(0, p.rope - c0)) : 0;      // channels of the rotated part
+          // (one that fills a whole block goes with the block behind it)
+          if (is_k && j == 0 && p.k_first > 0) write(&toK, p.K, rotated(grp_of * kPut), h, grp_of * kPut);
+          if (skip == kPut) {
+            write(&toK, p.K, rotated(c0), h, c0);
+          } else {
+            bulk_wait_group_read<0>();      // the buffer's last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                v[f] = pack_bf16(__uint_as_float(x[n & 1][8 * e + 2 * f]), __uint_as_float(x[n & 1][8 * e + 2 * f + 1]));
+              if (e * 8 < skip) {
+                const uint4 r = ld_shared_v4(rotated(c0) + place(lane, e));
+                v[0] = r.x;
+                v[1] = r.y;
+                v[2] = r.z;
+                v[3] = r.w;
+              }
+              st_shared_v4(buf + place(lane, e), v[0], v[1], v[2], v[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            write(is_k ? &toK : &toV, is_k ? p.K : p.V, buf, h, c0);
+          }
+          if (++j == p.head_blocks) {
+            j = 0;
+            ++h;
+          }
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(w.bar(kDFree + (i & 1)), 0);      // the even block's products wait for both
     }
     bulk_wait_group_all();
   }
