@@ -18,10 +18,11 @@
 //  * warp 9 copies: latent rows page by page, 64 channels at a time, and the weights' stages. All of a pair's
 //    copies are counted by the even block's barriers.
 //  * warp 8 of the even block issues the products, into two buffers of tensor memory.
-//  * warps 0 to 7 take the sums out, a position a lane and every other 32 columns a group of four warps, round
-//    them and put them into shared memory, from where a bulk tensor store writes the rows of a page (rows of
-//    which some are not to be written: 4 lanes write a row's 64 bytes). The rotated part, the same in every head,
-//    stays in buffers of its own. (Four warps: 118 us, all of which they were busy.)
+//  * warps 0 to 7 take the sums out, a position a lane and 128 columns a group of four warps, round them, and turn
+//    them round through shared memory, 64 channels at a time, so that 8 lanes write a row's 128 bytes together
+//    (32 bytes a lane straight from registers: 150 us). The rotated part, the same in every head, stays in
+//    registers. They give tensor memory back by an arrival without a release: one with it waits until the
+//    rows written before are performed (98 us against 76 where 128 latent channels make the products short).
 //
 // Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
 #include <cuda.h>
@@ -39,14 +40,13 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kOutWarps = 8, kMmaWarp = kOutWarps, kTmaWarp = kMmaWarp + 1, kThreads = (kTmaWarp + 1) * 32;
 constexpr int kBlocks = 4, kCols = 64;    // blocks of a product, and columns of a block
-constexpr int kPut = 32;                  // columns that a warp takes out at once
 constexpr int kABlock = 16384;            // 64 channels of 128 positions
 constexpr int kStep = 64;                 // channels of a stage of the weights
 constexpr int kBox = kStep * kCols * 2;   // of a block
 constexpr int kStage = kBlocks / 2 * kBox;
 constexpr int kMaxStages = 16, kMaxA = 8;
-constexpr int kPutBytes = 32 * kPut * 2;  // 32 rows of them, as they are written
-constexpr int kOutBytes = kOutWarps * kPutBytes;
+constexpr int kPutBytes = 32 * kCols * 2;  // 32 rows of them, as they are written
+constexpr int kOutBytes = kOutWarps * kPutBytes;      // a buffer of each warp
 constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
 
 enum Bars {
@@ -80,12 +80,11 @@ struct TileParams {
 
 __global__ void __launch_bounds__(kThreads, 1)
     expand_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap toK,
-                       const __grid_constant__ CUtensorMap toV, const __grid_constant__ TileParams p) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int a_blocks = p.latent / 64, steps = a_blocks;
   const uint32_t a_base = smem_u32(smem), b_base = a_base + a_blocks * kABlock;
-  const uint32_t s_base = b_base + p.stages * kStage, r_base = s_base + kOutBytes;
+  const uint32_t s_base = b_base + p.stages * kStage;
   Small* sm = reinterpret_cast<Small*>(smem + kSmemBytes - kSmallBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nope = p.dh - p.rope;
@@ -243,26 +242,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // a position a lane, every other block of columns
-    const int quad = warp & 3, grp_of = warp >> 2;
-    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int sub = lane >> 2, piece = lane & 3;
-    // where 16-byte piece j of a row stands in a buffer, and the buffers of the rotated part's channels c ..
-    auto place = [](int row, int j) { return static_cast<uint32_t>(row * 64 + ((j ^ (row >> 1 & 3)) << 4)); };
-    auto rotated = [&](int c) { return r_base + (c / kPut * 4 + quad) * kPutBytes; };
+    // a position a lane, two of a product's four blocks of columns
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * (kBlocks / 2 * kCols));
     const uint32_t buf = s_base + warp * kPutBytes;
-    auto quad_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
-    int dst = -1;              // row of head 0 of this lane's position, in units of dh (pool rows)
-    int slot = 0;
+    const uint32_t mine = lane * 128, swz = static_cast<uint32_t>(lane & 7) << 4;      // its row of a buffer
+    const int sub = lane >> 3, piece = lane & 7;
+    // the pool's rows (of head 0) that this lane writes a 16-byte piece of (-1: none), and that piece of their
+    // rotated parts
+    long long to[8];
+    uint4 rotated[8];
     for (int g = g0, i = 0; g < g1; ++g, ++i) {
       const int grp = g % p.products;
       long long row = -1;
       if (g == g0 || grp == 0) {
-        const int mine = g / p.products * 2 + static_cast<int>(rank);
-        const int t = mine < total ? seek(mine) + quad * 32 + lane : 0;
-        dst = -1;
-        slot = t & ((1 << p.to_shift) - 1);
-        const ExpandSpan span = mine < total ? expand_span(p.from, p.kv_len, cap, b) : ExpandSpan{0, 0};
+        const int nth = g / p.products * 2 + static_cast<int>(rank);
+        const int t = nth < total ? seek(nth) + quad * 32 + lane : 0;
+        long long dst = -1;
+        const ExpandSpan span = nth < total ? expand_span(p.from, p.kv_len, cap, b) : ExpandSpan{0, 0};
         if (t >= span.lo && t < span.hi) {
           const int sp = paged_lookup(p.table + static_cast<size_t>(b) * p.width, p.width, p.page_shift, p.num_pages, t);
           const int dp = paged_lookup(p.to_table + static_cast<size_t>(b) * p.to_width, p.to_width, p.to_shift, p.to_pages,
@@ -270,93 +267,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sp < 0 || dp < 0) {
             atomicOr(p.status, kStatusBadPage);
           } else {
-            dst = dp;
+            dst = ((static_cast<long long>(dp) * p.H) << p.to_shift) + (t & ((1 << p.to_shift) - 1));
             row = ((static_cast<long long>(sp) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * (p.latent + p.rope);
           }
         }
-        bulk_wait_group_read<0>();
-        quad_sync();         // neither warp's stores read the rotated part of the tile before
-        if (grp_of == 0) {
-#pragma unroll 4
-          for (int c = 0; c < p.rope; c += 8) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row >= 0) v = *reinterpret_cast<const uint4*>(p.C + row + p.latent + c);
-            st_shared_v4(rotated(c) + place(lane, c % kPut / 8), v.x, v.y, v.z, v.w);
-          }
-          fence_proxy_async_smem();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) to[n] = __shfl_sync(0xffffffffu, dst, n * 4 + sub);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const long long from = __shfl_sync(0xffffffffu, row, n * 4 + sub);
+          if (from >= 0 && piece * 8 < p.rope)
+            rotated[n] = *reinterpret_cast<const uint4*>(p.C + from + p.latent + piece * 8);
         }
-        quad_sync();
       }
       w.warp(kDFull + (i & 1), (i >> 1) & 1, kStatusTimeout);
       tc_fence_after();
-      const uint32_t d = my_tmem + (i & 1) * 256 + grp_of * kPut;
-      // the rows of all 32 lanes go out: a bulk store for each 32 or 16 of them (a page's)
-      const bool whole = __all_sync(0xffffffffu, dst >= 0 && w.ok);
-      const bool stores = (lane & ((1 << min(p.to_shift, 5)) - 1)) == 0;
-      // 32 channels of a head's K or V from a buffer, from channel c0 on
-      auto write = [&](const CUtensorMap* map, __nv_bfloat16* pool, uint32_t from, int h, int c0) {
-        if (whole) {
-          if (stores) {
-            tma_store_3d(map, from + lane * 64, c0, slot, dst * p.H + h);
-            bulk_commit_group();
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int r = n * 8 + sub;
-            const int to = __shfl_sync(0xffffffffu, dst, r), s = __shfl_sync(0xffffffffu, slot, r);
-            const uint4 v = ld_shared_v4(from + place(r, piece));
-            if (to >= 0 && w.ok)
-              *reinterpret_cast<uint4*>(pool + (((static_cast<long long>(to) * p.H + h) << p.to_shift) + s) * p.dh + c0 +
-                                        piece * 8) = v;
-          }
-          __syncwarp();
-        }
-      };
-      int h = grp * kBlocks / p.head_blocks, j = grp * kBlocks % p.head_blocks;      // of the product's first block
-      const int there = min(kBlocks, p.blocks - grp * kBlocks);
+      const uint32_t d = my_tmem + (i & 1) * 256;
+      const int id = grp * kBlocks + half * (kBlocks / 2);
+      int h = id / p.head_blocks, j = id % p.head_blocks;
       uint32_t x[2][32];
       tmem_ld_32x32b_x32(d, x[0]);
+      tmem_ld_32x32b_x32(d + 32, x[1]);
 #pragma unroll
-      for (int n = 0; n < kBlocks; ++n) {
+      for (int n = 0; n < kBlocks / 2; ++n) {
         tmem_ld_wait();
-        if (n + 1 < kBlocks) {
-          tmem_ld_32x32b_x32(d + (n + 1) * kCols, x[(n + 1) & 1]);      // under what is done with this one
+        uint32_t v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          v[e] = pack_bf16(__uint_as_float(x[e >> 4][2 * e & 31]), __uint_as_float(x[e >> 4][(2 * e & 31) + 1]));
+        if (n == 0) {      // under what is done with the first block
+          tmem_ld_32x32b_x32(d + kCols, x[0]);
+          tmem_ld_32x32b_x32(d + kCols + 32, x[1]);
         } else {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(w.bar(kDFree + (i & 1)), 0);      // the even block's products wait for both
+          // the even block's products wait for both
+          if (lane == 0) mbar_arrive_cluster_relaxed(w.bar(kDFree + (i & 1)), 0);
         }
-        if (n < there) {
+        if (id + n < p.blocks && w.ok) {
           const bool is_k = j < p.k_blocks;
-          const int c0 = (is_k ? p.k_first + j * kCols : (j - p.k_blocks) * kCols) + grp_of * kPut;
-          const int skip = is_k && j == 0 ? min(kPut, max(0, p.rope - c0)) : 0;      // channels of the rotated part
-          // (one that fills a whole block goes with the block behind it)
-          if (is_k && j == 0 && p.k_first > 0) write(&toK, p.K, rotated(grp_of * kPut), h, grp_of * kPut);
-          if (skip == kPut) {
-            write(&toK, p.K, rotated(c0), h, c0);
-          } else {
-            bulk_wait_group_read<0>();      // the buffer's last store has read it
-            __syncwarp();
+          const int c0 = is_k ? p.k_first + j * kCols : (j - p.k_blocks) * kCols;
+          const int skip = is_k && j == 0 ? p.rope - p.k_first : 0;      // channels of the rotated part (below 64)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t v[4];
+          for (int e = 0; e < 8; ++e)
+            st_shared_v4(buf + mine + ((16u * e) ^ swz), v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          __syncwarp();
+          // 8 lanes a row
+          const long long at = (static_cast<long long>(h) << p.to_shift) * p.dh + piece * 8;
+          __nv_bfloat16* base = (is_k ? p.K : p.V) + at + c0;
 #pragma unroll
-              for (int f = 0; f < 4; ++f)
-                v[f] = pack_bf16(__uint_as_float(x[n & 1][8 * e + 2 * f]), __uint_as_float(x[n & 1][8 * e + 2 * f + 1]));
-              if (e * 8 < skip) {
-                const uint4 r = ld_shared_v4(rotated(c0) + place(lane, e));
-                v[0] = r.x;
-                v[1] = r.y;
-                v[2] = r.z;
-                v[3] = r.w;
-              }
-              st_shared_v4(buf + place(lane, e), v[0], v[1], v[2], v[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            write(is_k ? &toK : &toV, is_k ? p.K : p.V, buf, h, c0);
+          for (int r = 0; r < 8; ++r) {
+            uint4 u = ld_shared_v4(buf + (r * 4 + sub) * 128 + ((piece ^ ((r * 4 + sub) & 7)) << 4));
+            if (piece * 8 < skip) u = rotated[r];
+            if (to[r] >= 0) *reinterpret_cast<uint4*>(base + to[r] * p.dh) = u;
           }
+          // (a rotated part of 64 channels goes with the block behind it)
+          if (is_k && j == 0 && p.k_first > 0)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (to[r] >= 0) *reinterpret_cast<uint4*>(p.K + at + to[r] * p.dh) = rotated[r];
+          __syncwarp();
           if (++j == p.head_blocks) {
             j = 0;
             ++h;
@@ -364,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    bulk_wait_group_all();
   }
   tc_fence_before();
   cluster_sync();      // neither block leaves while the pair's products or arrivals may still touch it
@@ -391,15 +360,11 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   if (!a.bf16) return launch_expand_rows(a, dev, stream);
   const int width = a.layer.latent + a.layer.rope, page_size = 1 << a.layer.page_shift, H = a.to.Hkv;
   const int nope = a.dh - a.layer.rope;
-  CUtensorMap c, k, v, to_k, to_v;
-  const int to_page = 1 << a.to.page_shift, out_rows = to_page < 32 ? to_page : 32;
-  const cuuint64_t slabs = static_cast<cuuint64_t>(a.to.num_pages) * H, row = static_cast<cuuint64_t>(a.dh) * 2;
+  CUtensorMap c, k, v;
   if (!encode_tiles(&c, a.layer.C, width, page_size, a.layer.num_pages, static_cast<cuuint64_t>(width) * 2,
                     static_cast<cuuint64_t>(page_size) * width * 2, page_size < kRows ? page_size : kRows, 1) ||
-      !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh) ||
-      !encode_boxes(&to_k, a.to.K, a.dh, to_page, slabs, row, row * to_page, kPut, out_rows, 1) ||
-      !encode_boxes(&to_v, a.to.V, a.dh, to_page, slabs, row, row * to_page, kPut, out_rows, 1)) {
-    *msg = "(the tensor maps of the pools and the weights cannot be encoded)";
+      !encode_weights(&k, a.WK, a.layer.latent, H * nope) || !encode_weights(&v, a.WV, a.layer.latent, H * a.dh)) {
+    *msg = "(the tensor maps of the pool and the weights cannot be encoded)";
     return cudaErrorInvalidValue;
   }
   TileParams p;
@@ -427,8 +392,7 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   p.head_blocks = p.k_blocks + a.dh / kCols;
   p.blocks = H * p.head_blocks;
   p.products = (p.blocks + kBlocks - 1) / kBlocks;
-  const int rope_bytes = (a.layer.rope + kPut - 1) / kPut * 4 * kPutBytes;
-  const int stages = (kSmemBytes - kSmallBytes - kOutBytes - rope_bytes - p.latent / 64 * kABlock) / kStage;
+  const int stages = (kSmemBytes - kSmallBytes - kOutBytes - p.latent / 64 * kABlock) / kStage;
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   static SmemOnce once;
   cudaError_t e = allow_smem(expand_tile_kernel, kSmemBytes, dev.device, &once);
@@ -461,7 +425,7 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& a, const DeviceInfo& 
   }
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, to_k, to_v, p);
+  e = cudaLaunchKernelEx(&cfg, expand_tile_kernel, c, k, v, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -242,6 +242,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank)
                : "memory");
 }
 
+// The same without a release: for an arrival that hands over nothing in memory (tensor memory that has
+// been read, say). A release at cluster scope waits until this thread's earlier global stores are performed.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, rank))
+               : "memory");
+}
+
 // Tiled TMA loads into this CTA's shared memory whose completion is counted on an
 // mbarrier of either CTA of the pair (`bar` a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
