@@ -9,10 +9,11 @@
 // of 128 channels by kR columns, where O would not leave room for S. The keys' rows are read by both products
 // from the one copy in shared memory, along the channels in the first and across them in the second.
 //
-//  * warp 5 streams the keys' rows by TMA into a ring of 16 KB units: 128 channels of 64 keys (the
-//    rotated part takes a unit of its own). A unit comes back as soon as P.V has read it.
-//  * warp 4 issues the products: the scores of step i + 1, as far as the ring holds it beside step i,
-//    go before P.V of step i, so that the softmax of one runs under the products of the other.
+//  * warp 6 streams the keys' rows by TMA into a ring of 16 KB units: 128 channels of 64 keys (the
+//    rotated part takes a unit of its own). A unit comes back as soon as P.V has read it. It also copies an item's
+//    queries, where tokens' rows stand one behind the other (the softmax warps do, otherwise).
+//  * warps 4 and 5 issue the products, one the scores, as units come, the other P.V: each waits for what it
+//    needs alone (one warp for both, scores first: 112 us for 64 single tokens over 287,000 keys of 20 heads).
 //  * warps 0 to 3 do the softmax, 16 keys each; a thread has two keys and a quarter of the rows. A row's
 //    reference m moves, and O^T is rescaled, only when a score passes it by more than 2^8 (agreed on by one barrier a
 //    step). Sums stay in each thread and meet at an item's end.
@@ -40,7 +41,7 @@ namespace cxa {
 namespace {
 
 constexpr int kSoftWarps = 4;
-constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kMmaWarp + 1;
+constexpr int kSWarp = kSoftWarps, kPvWarp = kSWarp + 1, kTmaWarp = kPvWarp + 1;
 constexpr int kThreads = (kTmaWarp + 1) * 32;
 constexpr int kKeys = 64, kChunkShift = 6;
 constexpr int kUnitBytes = 16384;            // 128 channels of 64 keys
@@ -49,7 +50,17 @@ constexpr int kMaxUnits = 13;
 constexpr int kSmemBytes = 232448;
 constexpr float kMoveLog2 = 8.f;
 
-enum Bars { kQFull = 0, kSFull = 1, kPFull = 3, kPvDone = 4, kUFull = 5, kUEmpty = kUFull + kMaxUnits, kBars = kUEmpty + kMaxUnits };
+enum Bars {
+  kQFull = 0,
+  kQEmpty = 1,
+  kSFull = 2,
+  kSFree = 4,
+  kPFull = 6,
+  kPvDone = 7,
+  kUFull = 8,
+  kUEmpty = kUFull + kMaxUnits,
+  kBars = kUEmpty + kMaxUnits
+};
 
 struct Small {
   uint64_t bars[kBars];
@@ -60,6 +71,7 @@ struct Small {
   float top[kSoftWarps][64];
   __align__(16) float corr[64];
   float m[64], inv[64];
+  long long row[64];           // where the rows' results begin
 };
 constexpr int kSmallBytes = 3072;
 static_assert(sizeof(Small) <= kSmallBytes, "the small arrays fit behind the ring");
@@ -75,6 +87,7 @@ struct TileParams {
   PagedBatch batch;
   int num_pages, page_shift, latent, rope;
   int units;                   // of the ring
+  int q_packed;                // queries stand one behind the other: copied by their map
   WorkShape shape;
 };
 
@@ -141,7 +154,8 @@ constexpr uint64_t p_desc_high() {
 
 template <int kR>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ TileParams p) {
+    latent_tile_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int quads = p.latent / 128, blocks = 2 * quads + (p.rope > 0 ? 1 : 0);      // of 64 channels
@@ -165,19 +179,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kQFull || i == kPFull ? kSoftWarps : 1);
+    for (int i = 0; i < kBars; ++i)
+      mbar_init(bar(i), (i == kQFull && !p.q_packed) || (i >= kSFree && i <= kPFull) ? kSoftWarps : 1);
     fence_mbar_init();
     sm->abort = 0;
   }
-  if (warp == kTmaWarp && lane == 0) prefetch_tmap(&tmC);
-  if (warp == kMmaWarp) {
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tmap(&tmC);
+    prefetch_tmap(&tmQ);
+  }
+  if (warp == kSWarp) {
     tmem_alloc(smem_u32(&sm->tmem), Tm<kR>::cols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(sm->tmem), 0);
   // A wait that runs out, or that another warp's has cut short, leaves ok false: the copy and product
   // warps then stop; the softmax warps go on through their loop, barriers included, without waiting for
   // anything or writing results.
@@ -219,10 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_global();
     const int box_shift = min(p.page_shift, kChunkShift), box_rows = 1 << box_shift;      // keys a box
     const int boxes = kKeys >> box_shift, box = lane % boxes, blk = lane / boxes;
-    int pos = 0, step = 0;
+    int pos = 0, step = 0, item = 0, q_sent = -1;
     uint32_t round = 0, armed = 0, parity = 0;      // units copies were sent to, and the phase
-    for (bool more = true; more && ok;) {
+    for (bool more = true; more && ok; ++item) {
       const Part t = part_of(cur);
+      if (p.q_packed) {
+        if (!wait_warp(kQEmpty, (item & 1) ^ 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kQFull), static_cast<uint32_t>(blocks * kR * 128));
+        __syncwarp();
+        if (lane < blocks)
+          tma_load_3d(q_base + lane * (kR * 128), &tmQ, bar(kQFull), lane * 64, cur.seq.q0 * H + cur.rt * kR, 0);
+        q_sent = item;
+      }
       const int* row = bt.table + static_cast<size_t>(cur.b) * bt.width;
       auto page_of = [&](int s) {
         const int at = s * kKeys + box * box_rows;
@@ -264,69 +290,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       more = !t.last;
       if (more) work_next(bt, shape, 1, &cur);
     }
-    if (!ok)      // the copies under way land before the block ends
+    if (!ok) {      // the copies under way land before the block ends
       for (int b = 0; b < NU; ++b)
         if (armed & (1u << b)) mbar_wait(bar(kUFull + b), (parity >> b) & 1u);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ products
-    constexpr uint32_t idesc_s = make_idesc(1u, kKeys, kR);
-    constexpr uint32_t idesc_o = make_idesc(1u, 128, kR) | 1u << 15 | 1u << 16;      // both operands MN-major
-    constexpr uint64_t hi = desc_high(1024), p_hi = p_desc_high<kR>();
-    const uint32_t pl = desc_low(p_base, 1024);
-    const int early = min(per, NU - per);      // units of the next step that the ring holds beside a step
-    int pos = 0, vpos = 0, item = 0, step = 0, vstep = 0;
+      if (q_sent >= 0) mbar_wait(bar(kQFull), static_cast<uint32_t>(q_sent) & 1u);
+    }
+  } else if (warp == kSWarp) {
+    // ------------------------------------------------------------------ scores
+    // (Addresses that are known to be the same in every lane need no carrying over from one: each product
+    // of 32 clocks took 60 to issue otherwise.)
+    constexpr uint32_t idesc = make_idesc(1u, kKeys, kR);
+    constexpr uint64_t hi = desc_high(1024);
+    const uint32_t ub = __shfl_sync(0xffffffffu, u_base, 0), qb = __shfl_sync(0xffffffffu, q_base, 0);
+    int pos = 0, item = 0, step = 0;
     uint32_t round = 0;
-    // scores of the units [u0, u1) of the step at `pos`
-    auto scores = [&](int u0, int u1) {
-      for (int u = u0; u < u1; ++u) {
-        if (!wait_warp(kUFull + pos, round & 1)) return;
-        tc_fence_after();
-        const uint32_t at = u_base + pos * kUnitBytes, d = tmem + (step & 1) * kR;
-        const int n = u < quads ? 2 : 1;
-        if (elect_one()) {
-          for (int h = 0; h < n; ++h) {
-            const uint32_t al = desc_low(at + h * kHalf, 16), bl = desc_low(q_base + (2 * u + h) * (kR * 128), 16);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)       // 16 channels: 32 bytes
-              mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc_s, u + h + k != 0 ? 1u : 0u);
-          }
-          if (u >= quads) tc_commit(bar(kUEmpty + pos));     // P.V has no use for the rotated part
-          if (u + 1 == per) tc_commit(bar(kSFull + (step & 1)));
-        }
-        __syncwarp();
-        if (++pos == NU) {
-          pos = 0;
-          ++round;
-        }
-      }
-      if (u1 == per) ++step;
-    };
     for (bool more = true; more && ok; ++item) {
       const Part t = part_of(cur);
       if (!wait_warp(kQFull, item & 1)) break;
-      scores(0, per);
-      for (int s = t.s0; s < t.s1 && ok; ++s, ++vstep) {
-        const bool next = s + 1 < t.s1;
-        if (next) scores(0, early);
-        if (!ok || !wait_warp(kPFull, vstep & 1)) break;
+      for (int s = t.s0; s < t.s1 && ok; ++s, ++step) {
+        if (!wait_warp(kSFree + (step & 1), ((step >> 1) & 1) ^ 1)) break;
+        const uint32_t d = tmem + __shfl_sync(0xffffffffu, step & 1, 0) * kR;
+        for (int u = 0; u < per; ++u) {
+          if (!wait_warp(kUFull + pos, round & 1)) break;
+          tc_fence_after();
+          const int at = __shfl_sync(0xffffffffu, pos, 0), un = __shfl_sync(0xffffffffu, u, 0);
+          const uint32_t al = desc_low(ub + at * kUnitBytes, 16), bl = desc_low(qb + un * (2 * kR * 128), 16);
+          const uint32_t acc = un != 0 ? 1u : 0u;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)       // 16 channels: 32 bytes
+              mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, k != 0 ? 1u : acc);
+            if (un < quads) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16(d, hi | (al + (kHalf >> 4) + 2 * k), hi | (bl + (kR * 128 >> 4) + 2 * k), idesc, 1u);
+            } else {
+              tc_commit(bar(kUEmpty + at));      // P.V has no use for the rotated part
+            }
+            if (un + 1 == per) {
+              tc_commit(bar(kSFull + (step & 1)));
+              if (s + 1 == t.s1) tc_commit(bar(kQEmpty));
+            }
+          }
+          __syncwarp();
+          if (++pos == NU) {
+            pos = 0;
+            ++round;
+          }
+        }
+      }
+      more = !t.last;
+      if (more) work_next(bt, shape, 1, &cur);
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------------ P.V
+    constexpr uint32_t idesc = make_idesc(1u, 128, kR) | 1u << 15 | 1u << 16;      // both operands MN-major
+    constexpr uint64_t hi = desc_high(1024), p_hi = p_desc_high<kR>();
+    const uint32_t ub = __shfl_sync(0xffffffffu, u_base, 0);
+    const uint32_t pl = desc_low(__shfl_sync(0xffffffffu, p_base, 0), 1024);
+    int pos = 0, step = 0;
+    for (bool more = true; more && ok;) {
+      const Part t = part_of(cur);
+      for (int s = t.s0; s < t.s1 && ok; ++s, ++step) {
+        if (!wait_warp(kPFull, step & 1)) break;
         tc_fence_after();
-        if (elect_one()) {
-          int at = vpos;
-          for (int u = 0; u < quads; ++u) {
-            const uint32_t al = desc_low(u_base + at * kUnitBytes, kHalf), d = tmem + Tm<kR>::o + u * kR;
+        const uint32_t acc = __shfl_sync(0xffffffffu, s != t.s0 ? 1u : 0u, 0);
+        for (int u = 0; u < quads; ++u) {
+          int next = pos + u;
+          if (next >= NU) next -= NU;
+          const int at = __shfl_sync(0xffffffffu, next, 0), un = __shfl_sync(0xffffffffu, u, 0);
+          const uint32_t al = desc_low(ub + at * kUnitBytes, kHalf), d = tmem + Tm<kR>::o + un * kR;
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)       // 16 keys: 2048 bytes of the rows, 32 kR of P
-              mma_bf16(d, hi | (al + k * (2048 >> 4)), p_hi | (pl + k * ((32 * kR) >> 4)), idesc_o,
-                       s != t.s0 || k != 0 ? 1u : 0u);
+              mma_bf16(d, hi | (al + k * (2048 >> 4)), p_hi | (pl + k * ((32 * kR) >> 4)), idesc, k != 0 ? 1u : acc);
             tc_commit(bar(kUEmpty + at));
-            if (++at == NU) at = 0;
+            if (un + 1 == quads) tc_commit(bar(kPvDone));
           }
-          tc_commit(bar(kPvDone));
+          __syncwarp();
         }
-        __syncwarp();
-        vpos += per;
-        if (vpos >= NU) vpos -= NU;
-        if (next && early < per) scores(early, per);
+        pos += per;
+        if (pos >= NU) pos -= NU;
       }
       more = !t.last;
       if (more) work_next(bt, shape, 1, &cur);
@@ -344,21 +389,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (;;) {
       const Part t = part_of(cur);
       const int row0 = cur.rt * kR, rows = min(kR, work_rows(cur.seq, shape) - row0);
-      // the rows' queries (the scores of the item before have been taken)
-      {
-        const int pieces = kR * blocks * 8;
-#pragma unroll 4
-        for (int i = tid; i < pieces; i += kSoftWarps * 32) {
-          const int j = i & 7, blk = (i >> 3) % blocks, r = (i >> 3) / blocks, ch = blk * 64 + j * 8, at = row0 + r;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows && ch < width)
-            v = *reinterpret_cast<const uint4*>(p.q + (cur.seq.q0 + at / H) * p.q_stride +
-                                                static_cast<long long>(at % H) * width + ch);
-          st_shared_v4(q_base + blk * (kR * 128) + r * 128 + ((j ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+      if (!p.q_packed) {
+        // the rows' queries (the scores of the item before have been taken): a row a warp
+        const int pieces = blocks * 8;
+#pragma unroll 2
+        for (int r = warp; r < kR; r += kSoftWarps) {
+          const int at = row0 + r;
+          const __nv_bfloat16* src = p.q + (cur.seq.q0 + at / H) * p.q_stride + static_cast<long long>(at % H) * width;
+          uint4 v[3];
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            const int i = lane + 32 * j;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows && i * 8 < width) v[j] = *reinterpret_cast<const uint4*>(src + i * 8);
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            const int i = lane + 32 * j;
+            if (i < pieces)
+              st_shared_v4(q_base + (i >> 3) * (kR * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4), v[j].x, v[j].y, v[j].z, v[j].w);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQFull));
+      }
+      if (tid < kR) {
+        const int at = row0 + tid;
+        sm->row[tid] = (cur.seq.q0 + at / H) * p.o_stride + static_cast<long long>(at % H) * p.latent;
       }
       const int see_all = visible_keys(cur.seq, row0 / H, shape.cap);      // of all of the tile's rows
       float m[CN], l[CN];
@@ -375,6 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[XN];
         tmem_ld_16x256b(my_tmem + (step & 1) * kR, x);
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSFree + (step & 1)));
         const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[step & 15]);
         const bool special = key0 + kKeys > see_all;       // some row misses a key
         uint32_t wild = 0;                                 // of this thread's two keys
@@ -529,31 +590,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       soft_sync();
       wait_warp(kPvDone, (step - 1) & 1);
       tc_fence_after();
+      {
+        // (tensor memory a batch of 16 columns ahead)
+        uint32_t o[2][16];
+        const uint32_t from = my_tmem + Tm<kR>::o;
+        constexpr int B = kR / 16;      // batches of a tile
+        tmem_ld_32x32b_x16(from, o[0]);
 #pragma unroll 1
-      for (int u = 0; u < quads; ++u) {
-        const int ch = u * 128 + warp * 32 + lane;
-        int tok = row0 / H, hd = row0 % H;
-#pragma unroll 1
-        for (int c = 0; c < kR; c += 16) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(my_tmem + Tm<kR>::o + u * kR + c, o);
-          tmem_ld_wait();
+        for (int u = 0; u < quads; ++u) {
+          const int ch = u * 128 + warp * 32 + lane;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (c + e < rows && ok) {
-              if (whole)
-                p.out[(cur.seq.q0 + tok) * p.o_stride + static_cast<long long>(hd) * p.latent + ch] =
-                    __float2bfloat16_rn(__uint_as_float(o[e]) * sm->inv[c + e]);
-              else
-                slot[static_cast<size_t>(c + e) * p.latent + ch] = __uint_as_float(o[e]);
+          for (int c = 0; c < B; ++c) {
+            const int now = B % 2 == 0 ? c & 1 : 0;
+            tmem_ld_wait();
+            if constexpr (B % 2 == 0) {
+              if (c + 1 < B || u + 1 < quads) tmem_ld_32x32b_x16(from + u * kR + (c + 1) * 16, o[now ^ 1]);
             }
-            if (++hd == H) {
-              hd = 0;
-              ++tok;
+            if (ok) {
+              if (whole) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (c * 16 + e < rows)
+                    p.out[sm->row[c * 16 + e] + ch] = __float2bfloat16_rn(__uint_as_float(o[now][e]) * sm->inv[c * 16 + e]);
+              } else {
+                float* to = slot + static_cast<size_t>(c * 16) * p.latent + ch;
+#pragma unroll
+                for (int e = 0; e < 16; ++e, to += p.latent)
+                  if (c * 16 + e < rows) *to = __uint_as_float(o[now][e]);
+              }
+            }
+            __syncwarp();
+            if constexpr (B % 2 != 0) {
+              if (u + 1 < quads) tmem_ld_32x32b_x16(from + (u + 1) * kR, o[0]);
             }
           }
-          __syncwarp();
         }
+        tmem_ld_wait();
       }
       tc_fence_before();
       if (t.begins && !t.ends && ok)
@@ -567,16 +639,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, Tm<kR>::cols);
+  if (warp == kSWarp) tmem_dealloc(tmem, Tm<kR>::cols);
 }
 
 template <int kR>
 cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
   const int width = a.layer.latent + a.layer.rope, page_size = 1 << a.layer.page_shift;
-  CUtensorMap map;
+  CUtensorMap map, q_map;
+  // rows of all tokens and heads in one, if they stand so and a map holds them (strides below 2^40 bytes)
+  const long long q_rows = static_cast<long long>(a.batch.n_tokens) * a.H, q_bytes = q_rows * width * 2;
+  const bool q_packed =
+      (a.q_stride == static_cast<long long>(a.H) * width || a.batch.n_tokens == 1) && q_bytes < (1LL << 40);
   if (!encode_tiles(&map, a.layer.C, width, page_size, a.layer.num_pages, static_cast<cuuint64_t>(width) * 2,
-                    static_cast<cuuint64_t>(page_size) * width * 2, page_size < kKeys ? page_size : kKeys, 1)) {
-    *msg = "(the tensor map of the pool cannot be encoded)";
+                    static_cast<cuuint64_t>(page_size) * width * 2, page_size < kKeys ? page_size : kKeys, 1) ||
+      !encode_tiles(&q_map, a.q, width, q_packed ? q_rows : 1, 1, static_cast<cuuint64_t>(width) * 2,
+                    q_packed ? q_bytes : width * 2, kR, 1)) {
+    *msg = "(the tensor maps of the pool and the queries cannot be encoded)";
     return cudaErrorInvalidValue;
   }
   TileParams p;
@@ -596,6 +674,7 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   const int blocks = a.layer.latent / 64 + (a.layer.rope > 0 ? 1 : 0);
   const int units = (kSmemBytes - kSmallBytes - blocks * kR * 128 - kKeys * kR * 2) / kUnitBytes;
   p.units = units < kMaxUnits ? units : kMaxUnits;
+  p.q_packed = q_packed ? 1 : 0;
   p.shape.G = a.H;
   p.shape.rows = kR;
   p.shape.chunk_shift = kChunkShift;
@@ -617,7 +696,7 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_tile_kernel<kR>, map, p);
+  e = cudaLaunchKernelEx(&cfg, latent_tile_kernel<kR>, map, q_map, p);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return launch_latent_merge(a, kR, grid, dev, stream);
