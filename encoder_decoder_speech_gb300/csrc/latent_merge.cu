@@ -42,6 +42,7 @@ template <typename TO>
 __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_constant__ MergeParams p) {
   __shared__ LatentCut s_cut[kLatentMaxBlocks];
   __shared__ int s_end[2][kThreads];          // ends of the items' units: of few parts, of many
+  __shared__ unsigned long long s_warp[kWarps];
   __shared__ float s_w[kLatentMaxBlocks];
   __shared__ float s_red[2][kWarps];
   __shared__ float4 s_acc[kWarps][32];
@@ -57,16 +58,21 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
     s_cut[tid] = c;
     (c.parts <= kWarpParts ? few : many) = c.parts > 0 ? c.rows * cols : 0;
   }
-  s_end[0][tid] = few;
-  s_end[1][tid] = many;
-  __syncthreads();
-  for (int off = 1; off < kThreads; off <<= 1) {
-    const int x = tid >= off ? s_end[0][tid - off] : 0, y = tid >= off ? s_end[1][tid - off] : 0;
-    __syncthreads();
-    s_end[0][tid] += x;
-    s_end[1][tid] += y;
-    __syncthreads();
+  // both kinds' counts summed up to each item in one number, 32 bits of each
+  unsigned long long sum = static_cast<unsigned long long>(many) << 32 | static_cast<unsigned>(few);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += o;
   }
+  if (lane == 31) s_warp[warp] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i)
+    if (i < warp) sum += s_warp[i];
+  s_end[0][tid] = static_cast<int>(sum & 0xFFFFFFFFu);
+  s_end[1][tid] = static_cast<int>(sum >> 32);
+  __syncthreads();
   // the item that holds unit u, and the unit's row and channels
   auto find = [&](int k, int u, int* row, int* col) {
     int lo = 0, hi = p.blocks - 1;
