@@ -1,7 +1,7 @@
 // The merge of the latent attention's cut items: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k
 // over an item's parts k, for every row. The parts were written a moment ago and lie in L2; bound by
-// the latency of reading them. A unit is a row's 128 channels: a warp's where parts are few (a
-// batch), a block's where they are many (one long context).
+// the latency of reading them. A unit is a warp's row where parts are few (a batch), a block's 128 channels of
+// a row where they are many (one long context).
 #include <cuda_bf16.h>
 
 #include "latent_parts.cuh"
@@ -56,7 +56,10 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
     const int4 v = __ldcg(reinterpret_cast<const int4*>(p.cut) + tid);
     const LatentCut c = {v.x, v.y, v.z, v.w};
     s_cut[tid] = c;
-    (c.parts <= kWarpParts ? few : many) = c.parts > 0 ? c.rows * cols : 0;
+    if (c.parts > kWarpParts)
+      many = c.rows * cols;
+    else if (c.parts > 0)
+      few = c.rows;
   }
   // both kinds' counts summed up to each item in one number, 32 bits of each
   unsigned long long sum = static_cast<unsigned long long>(many) << 32 | static_cast<unsigned>(few);
@@ -73,16 +76,14 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
   s_end[0][tid] = static_cast<int>(sum & 0xFFFFFFFFu);
   s_end[1][tid] = static_cast<int>(sum >> 32);
   __syncthreads();
-  // the item that holds unit u, and the unit's row and channels
-  auto find = [&](int k, int u, int* row, int* col) {
+  // the item that holds unit u, and the unit's number in it
+  auto find = [&](int k, int u, int* in) {
     int lo = 0, hi = p.blocks - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (s_end[k][mid] > u) hi = mid; else lo = mid + 1;
     }
-    const int in = u - (lo > 0 ? s_end[k][lo - 1] : 0);
-    *row = in / cols;
-    *col = in - *row * cols;
+    *in = u - (lo > 0 ? s_end[k][lo - 1] : 0);
     return lo;
   };
   auto part = [&](int owner, int k) { return p.part + (2 * static_cast<size_t>(owner + k) + (k == 0 ? 1 : 0)) * slot; };
@@ -93,8 +94,8 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
   };
 
   for (int u = blockIdx.x; u < s_end[1][kThreads - 1]; u += gridDim.x) {
-    int row, col;
-    const int owner = find(1, u, &row, &col);
+    int in;
+    const int owner = find(1, u, &in), row = in / cols, col = in - row * cols;
     const LatentCut c = s_cut[owner];
     const bool has = tid < c.parts;            // (parts <= blocks <= kThreads)
     const float* ml = part(owner, has ? tid : 0) + static_cast<size_t>(p.R) * p.latent + row;
@@ -132,13 +133,13 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
     __syncthreads();
   }
   for (int u = blockIdx.x * kWarps + warp; u < s_end[0][kThreads - 1]; u += gridDim.x * kWarps) {
-    int row, col;
-    const int owner = find(0, u, &row, &col);
+    int row;
+    const int owner = find(0, u, &row);
     const LatentCut c = s_cut[owner];
     const bool has = lane < c.parts;
     const float* ml = part(owner, has ? lane : 0) + static_cast<size_t>(p.R) * p.latent + row;
     const float m = has ? __ldcg(ml) : -INFINITY, l = has ? __ldcg(ml + p.R) : 0.f;
-    const size_t at = static_cast<size_t>(row) * p.latent + col * 128 + lane * 4;
+    const size_t at = static_cast<size_t>(row) * p.latent + lane * 4;
     float M = m;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -146,12 +147,22 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
     float L = l * w;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < c.parts; ++k)
-      acc = fma4(__shfl_sync(0xffffffffu, w, k), __ldcg(reinterpret_cast<const float4*>(part(owner, k) + at)), acc);
+    float4 acc[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < c.parts; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* src = part(owner, k) + at;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < cols) acc[q] = fma4(wk, __ldcg(reinterpret_cast<const float4*>(src + q * 128)), acc[q]);
+    }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    store4(dst(c, row, col), make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < cols)
+        store4(dst(c, row, q), make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv));
   }
 }
 
