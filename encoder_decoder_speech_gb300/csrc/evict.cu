@@ -2,10 +2,10 @@
 //
 // evict_select_kernel finds, for every (layer, sequence, K/V head), the keep heaviest positions (the
 // first and the last ones before all others) and lists them in order. A cluster of up to 8 blocks has the
-// item's keys (weights as integers in their order) in shared memory, read once; three passes over their digits
-// of 11, 11 and 10 bits, histograms added up over distributed shared memory, find the keep-th largest; one more
-// writes the positions above it, and of those equal to it the first ones. (A block an item, which read the
-// weights anew in each pass: 225 us for 32 lists of 65536.) evict_copy_kernel copies the listed rows of K, V and
+// item's keys (weights as integers in their order) in shared memory, read once; passes over their digits, with
+// histograms added up over distributed shared memory, find the keep-th largest; one more writes the
+// positions above it, and of those equal to it the first ones. (A block an item, which read the weights anew in
+// each pass: 225 us for 32 lists of 65536.) evict_copy_kernel copies the listed rows of K, V and
 // weights, a block 64 of them. Bound by memory: weights are read once, what stays is read and written once.
 #include "cluster.cuh"
 #include "latent.cuh"
@@ -14,7 +14,6 @@
 namespace cxa {
 namespace {
 
-constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxRoom = 49152;      // keys in a block's shared memory; more are read again
 constexpr int kCopyThreads = 256, kCopyRows = 64;
@@ -39,12 +38,22 @@ __device__ __forceinline__ int ld_cluster(const int* local, uint32_t rank) {
   return v;
 }
 
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictParams p, int blocks, int room) {
-  constexpr int kWarps = kThreads / 32;
+// Alone: one block an item, digits of 8 bits; otherwise a cluster of 4 or 8, digits of 11, 11 and 10.
+template <bool kAlone>
+struct Select {
+  static constexpr int threads = kAlone ? 256 : 512, warps = threads / 32;
+  static constexpr int bins = kAlone ? 256 : 2048, passes = kAlone ? 4 : 3;
+};
+
+template <bool kAlone>
+__global__ void __launch_bounds__(Select<kAlone>::threads)
+    evict_select_kernel(const __grid_constant__ EvictParams p, int blocks, int room) {
+  using S = Select<kAlone>;
+  constexpr int kThreads = S::threads, kWarps = S::warps, kBins = S::bins;
   extern __shared__ uint32_t s_key[];        // [room]
-  __shared__ int s_hist[kBins], s_sum[kBins];      // of this block; of its share of the bins, over the cluster
-  __shared__ int s_group[32];                      // of 32 groups of the share's bins
+  __shared__ int s_hist[kBins];              // of this block
+  __shared__ int s_sum[kAlone ? 1 : kBins / 4];      // of its share of the bins, over the cluster
+  __shared__ int s_group[32];                // of 32 bins each
   __shared__ int s_scan[2][kWarps];
   __shared__ int s_count[2];
   __shared__ uint32_t s_prefix;
@@ -53,7 +62,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const EvictLaunch& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blocks > 1 ? static_cast<int>(cluster_rank()) : 0;
+  if (kAlone) blocks = 1;
+  const int rank = kAlone ? 0 : static_cast<int>(cluster_rank());
   const int item = blockIdx.x / blocks, h = item % a.Hkv, b = item / a.Hkv % a.B, l = item / a.Hkv / a.B;
   const int cap = a.width << a.page_shift;
   const int given = max(0, a.kv_len[b]), kv = min(given, cap), m = min(kv, a.keep);
@@ -66,12 +76,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     return;
   }
   auto all_sync = [&]() {
-    if (blocks > 1)
-      cluster_sync();
-    else
+    if constexpr (kAlone)
       __syncthreads();
+    else
+      cluster_sync();
   };
-  auto remote = [&](const int* x, int r) { return blocks > 1 ? ld_cluster(x, static_cast<uint32_t>(r)) : *x; };
   const int* row = a.table + static_cast<size_t>(b) * a.width;
   const float* W = a.W + (static_cast<size_t>(l) * a.num_pages * a.Hkv << a.page_shift);
   auto key_of = [&](int t) {
@@ -87,15 +96,29 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   // this block's positions [lo, lo + n)
   const int per = ((kv + blocks - 1) / blocks + 31) / 32 * 32;
   const int lo = min(kv, rank * per), n = min(kv, lo + per) - lo;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid; i < min(n, room); i += kThreads) s_key[i] = key_of(lo + i);
   auto key = [&](int i) { return i < room ? s_key[i] : key_of(lo + i); };
   uint32_t prefix = 0;
   int left = m;               // to be taken among the keys that share the prefix
-  const int share = kBins / blocks;
+  int above = 0;              // keys above the bins that are looked at
+  // Of counts c in 32 lanes, the later ones above, the lane in which the count from above reaches `left`.
+  auto find = [&](int c) {
+    int sum = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_down_sync(0xffffffffu, sum, off);
+      if (lane + off < 32) sum += o;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, above + sum >= left && above + sum - c < left);
+    const int at = 31 - __clz(hit | 1u);
+    above += __shfl_sync(0xffffffffu, sum - c, at);
+    return at;
+  };
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+  for (int pass = 0; pass < S::passes; ++pass) {
+    const int shift = kAlone ? 24 - 8 * pass : pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int top = kAlone ? 32 - 8 * pass : pass == 0 ? 32 : pass == 1 ? 21 : 10;
     for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
@@ -103,116 +126,110 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       if (pass == 0 || (k >> top) == (prefix >> top)) atomicAdd(&s_hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1);
     }
     all_sync();
-    const int each = share / 32;      // bins of a group: 8 to 64
-    for (int i = tid; i < share; i += kThreads) {
-      int sum = 0;
-      for (int c = 0; c < blocks; ++c) sum += remote(&s_hist[rank * share + i], c);
-      s_sum[i] = sum;
-    }
-    __syncthreads();
-    for (int g = warp; g < 32; g += kWarps) {
-      int sum = (lane < each ? s_sum[g * each + lane] : 0) + (lane + 32 < each ? s_sum[g * each + lane + 32] : 0);
+    above = 0;
+    if constexpr (kAlone) {
+      if (warp == 0) {
+        int c[8], sum = 0;      // this lane's bins
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      if (lane == 0) s_group[g] = sum;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int sum = s_group[lane];
+        for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[lane * 8 + i];
+        const int at = find(sum);
+        if (lane == at) {
+          int bin = 7;
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      if (lane == 0) s_count[0] = sum;
-    }
-    all_sync();
-    if (warp == 0) {
-      // the share, the group in it and the bin in that, in which the count from above reaches `left`
-      int above = 0;
-      auto find = [&](int c) {      // a lane's count; the lane, `above` then counts what is above it
-        int sum = c;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int o = __shfl_down_sync(0xffffffffu, sum, off);
-          if (lane + off < 32) sum += o;
+          for (int i = 7; i > 0; --i)
+            if (bin == i && above + c[i] < left) {
+              above += c[i];
+              bin = i - 1;
+            }
+          s_prefix = prefix | static_cast<uint32_t>(lane * 8 + bin) << shift;
+          s_left = left - above;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, above + sum >= left && above + sum - c < left);
-        const int at = 31 - __clz(hit | 1u);
-        above += __shfl_sync(0xffffffffu, sum - c, at);
-        return at;
-      };
-      const int at = find(lane < blocks ? remote(&s_count[0], lane) : 0);
-      const int group = find(remote(&s_group[lane], at));
-      const int two = each == 64 ? 2 : 1, first = group * each + lane * two;      // of this lane's bins
-      const bool has = lane * two < each;
-      const int c0 = has ? remote(&s_sum[first], at) : 0, c1 = has && two == 2 ? remote(&s_sum[first + 1], at) : 0;
-      const int in = find(c0 + c1);
-      if (lane == in) {
-        const bool upper = two == 2 && above + c1 >= left;
-        const int bin = first + (upper ? 1 : 0);
-        s_prefix = prefix | static_cast<uint32_t>(at * share + bin) << shift;
-        s_left = left - (above + (two == 2 && !upper ? c1 : 0));
+      }
+    } else {
+      // this block's share of the bins, over the cluster, and the sums of 32 of them
+      const int share = kBins / blocks;
+      if (tid < share) {
+        int sum = 0;
+        for (int c = 0; c < blocks; ++c) sum += ld_cluster(&s_hist[rank * share + tid], static_cast<uint32_t>(c));
+        s_sum[tid] = sum;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) s_group[warp] = sum;
+      }
+      all_sync();
+      if (warp == 0) {
+        // 64 groups in the order of their bins, two a lane
+        const int groups = share / 32, g = lane * 2;
+        const int c0 = ld_cluster(&s_group[g % groups], static_cast<uint32_t>(g / groups));
+        const int c1 = ld_cluster(&s_group[(g + 1) % groups], static_cast<uint32_t>((g + 1) / groups));
+        const int two = find(c0 + c1);
+        const int upper_count = __shfl_sync(0xffffffffu, c1, two);
+        const bool upper = above + upper_count >= left;
+        if (!upper) above += upper_count;
+        const int group = two * 2 + (upper ? 1 : 0);
+        const int bin = find(ld_cluster(&s_sum[group % groups * 32 + lane], static_cast<uint32_t>(group / groups)));
+        if (lane == 0) {
+          s_prefix = prefix | static_cast<uint32_t>(group * 32 + bin) << shift;
+          s_left = left - above;
+        }
       }
     }
     __syncthreads();
     prefix = s_prefix;
     left = s_left;
-    __syncthreads();
   }
-  // prefix is the m-th largest key; `left` of the positions that have it stay
-  int counts[2] = {0, 0};
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t k = key(i);
-    counts[0] += k > prefix ? 1 : 0;
-    counts[1] += k == prefix ? 1 : 0;
+  // prefix is the m-th largest key; `left` of the positions that have it stay. Each warp has a run of the
+  // block's positions: how many of both there are in it, and with what stands before it, where they go.
+  const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(n, warp * run), i1 = min(n, i0 + run);
+  int count = 0, tied = 0;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+    count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k > prefix));
+    tied += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k == prefix));
   }
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) counts[q] += __shfl_xor_sync(0xffffffffu, counts[q], off);
-    if (lane == 0) s_scan[q][warp] = counts[q];
+  if (lane == 0) {
+    s_scan[0][warp] = count;
+    s_scan[1][warp] = tied;
   }
   __syncthreads();
-  if (tid < 2) {
-    int sum = 0;
-    for (int i = 0; i < kWarps; ++i) sum += s_scan[tid][i];
-    s_count[tid] = sum;
-  }
-  all_sync();
-  int out = 0, ties = 0;      // in the positions before
-  for (int c = 0; c < rank; ++c) {
-    out += remote(&s_count[0], c);
-    ties += remote(&s_count[1], c);
-  }
-  out += min(ties, left);
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < n ? key(i) : 0u;
-    const bool above = i < n && k > prefix, tie = i < n && k == prefix;
-    const uint32_t ma = __ballot_sync(0xffffffffu, above), mt = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) {
-      s_scan[0][warp] = __popc(ma);
-      s_scan[1][warp] = __popc(mt);
-    }
-    __syncthreads();
-    int na = 0, nt = 0, ba = 0, bt = 0;
+  int out = lane < warp ? s_scan[0][lane] : 0, ties = lane < warp ? s_scan[1][lane] : 0;      // in the positions before
+  if constexpr (!kAlone) {
+    if (warp == 0) {
+      int x = lane < kWarps ? s_scan[0][lane] : 0, y = lane < kWarps ? s_scan[1][lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        ba += s_scan[0][w];
-        bt += s_scan[1][w];
+      for (int off = 16; off >= 1; off >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, off);
+        y += __shfl_xor_sync(0xffffffffu, y, off);
       }
-      na += s_scan[0][w];
-      nt += s_scan[1][w];
+      if (lane == 0) {
+        s_count[0] = x;
+        s_count[1] = y;
+      }
     }
-    const uint32_t below = (1u << lane) - 1u;
-    const int my_above = ba + __popc(ma & below), my_tie = ties + bt + __popc(mt & below);
-    // ties before this position, of those that stay
-    const int at = out + my_above + (min(my_tie, left) - min(ties, left));
-    if (above || (tie && my_tie < left)) kept[at] = lo + i;
-    out += na + (min(ties + nt, left) - min(ties, left));
-    ties += nt;
-    __syncthreads();
+    all_sync();
+    if (lane < rank) {
+      out += ld_cluster(&s_count[0], static_cast<uint32_t>(lane));
+      ties += ld_cluster(&s_count[1], static_cast<uint32_t>(lane));
+    }
   }
-  if (blocks > 1) cluster_sync();      // no block leaves while another may read its counts
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    out += __shfl_xor_sync(0xffffffffu, out, off);
+    ties += __shfl_xor_sync(0xffffffffu, ties, off);
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+    const bool more = i + lane < i1 && k > prefix, tie = i + lane < i1 && k == prefix;
+    const uint32_t ma = __ballot_sync(0xffffffffu, more), mt = __ballot_sync(0xffffffffu, tie);
+    const int my_tie = ties + __popc(mt & below);
+    // behind all larger ones before it, and the ties before it that stay
+    const int at = out + __popc(ma & below) + min(my_tie, left);
+    if ((more || (tie && my_tie < left)) && at < m) kept[at] = lo + i + lane;
+    out += __popc(ma);
+    ties += __popc(mt);
+  }
+  if constexpr (!kAlone) cluster_sync();      // no block leaves while another may read its counts
 }
 
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
@@ -256,18 +273,17 @@ cudaError_t launch_evict(const EvictLaunch& a, const DeviceInfo& dev, cudaStream
   EvictParams p = {a, dev.status_word};
   const long long items = static_cast<long long>(a.nl) * a.B * a.Hkv;
   const long long cap = static_cast<long long>(a.width) << a.page_shift;
-  // blocks of 2048 positions and more, up to 8 an item
-  int blocks = 1;
-  while (blocks < kMaxCluster && cap / blocks > 4096) blocks *= 2;
+  // up to 4096 positions go to a block by itself; a share of the bins has to fit a block's threads otherwise
+  const int blocks = cap <= 4096 ? 1 : cap <= 16384 ? kMaxCluster / 2 : kMaxCluster;
   const long long want = (cap + blocks - 1) / blocks + 32;
   const int room = static_cast<int>(want < kMaxRoom ? want : kMaxRoom);
   const bool small = blocks == 1;
   cudaError_t e = cudaSuccess;
   static SmemOnce once;
-  if (!small && (e = allow_smem(evict_select_kernel<1024>, kMaxRoom * 4, dev.device, &once)) != cudaSuccess) return e;
+  if (!small && (e = allow_smem(evict_select_kernel<false>, kMaxRoom * 4, dev.device, &once)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * blocks));
-  cfg.blockDim = dim3(small ? 256 : 1024);
+  cfg.blockDim = dim3(small ? Select<true>::threads : Select<false>::threads);
   cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -279,8 +295,8 @@ cudaError_t launch_evict(const EvictLaunch& a, const DeviceInfo& dev, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = small ? 1 : 2;
-  e = small ? cudaLaunchKernelEx(&cfg, evict_select_kernel<256>, p, blocks, room)
-            : cudaLaunchKernelEx(&cfg, evict_select_kernel<1024>, p, blocks, room);
+  e = small ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p, blocks, room)
+            : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p, blocks, room);
   if (e != cudaSuccess) return e;
   count_launches(1);
   cfg.gridDim = dim3(static_cast<unsigned>(items * ((a.keep + kCopyRows - 1) / kCopyRows)));
