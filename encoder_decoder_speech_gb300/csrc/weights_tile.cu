@@ -59,6 +59,9 @@ struct WeightsParams {
 __device__ __forceinline__ int lookup(const WeightsParams& p, int b, int t) {
   return paged_lookup(p.batch.table + static_cast<size_t>(b) * p.batch.width, p.batch.width, p.page_shift, p.num_pages, t);
 }
+// A value that every lane has, known as such: operands' addresses need no carrying over from a lane then, which
+// takes longer than a product of 32 clocks.
+__device__ __forceinline__ uint32_t same_in_all(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ float* refs_of(const WeightsParams& p, const PagedSeq& s, int h) {
   return p.ref + (static_cast<size_t>(h) * p.batch.n_tokens + s.q0) * p.shape.G;
 }
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+  const uint32_t tmem = same_in_all(static_cast<uint32_t>(sm->tmem));
   const int n_chunks = range.g1 - range.g0;
 
   if (warp == kTmaWarp) {
@@ -185,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc = make_idesc(1u, kKeys, kRows);
     constexpr uint64_t hi = desc_high(1024);
+    const uint32_t ub = same_in_all(u_base), qb = same_in_all(q_base);
     int pos = 0, item = 0, c = cur.c;
     uint32_t round = 0;
     bool fresh = true;
@@ -197,11 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = 0; u < kUnits; ++u) {
         if (!w.warp(kUFull + pos, round & 1, kStatusTimeout)) break;
         tc_fence_after();
+        const int at = __shfl_sync(0xffffffffu, pos | buf << 8, 0);
+        const uint32_t al = desc_low(ub + (at & 255) * kUnitBytes, 16), bl = desc_low(qb + u * (kRows * 128), 16);
+        const uint32_t d = tmem + (at >> 8) * kRows;
         if (elect_one()) {
-          const uint32_t al = desc_low(u_base + pos * kUnitBytes, 16), bl = desc_low(q_base + u * (kRows * 128), 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + buf * kRows, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, u + k != 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, u + k != 0 ? 1u : 0u);
           tc_commit(w.bar(kUEmpty + pos));
           if (u + 1 == kUnits) tc_commit(w.bar(kSFull + buf));
         }
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-constexpr int kAddThreads = 128;
+constexpr int kAddThreads = 512, kAddChunks = kAddThreads / kKeys;      // chunks at once
 __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ WorkScratch s_work;
   __shared__ float s_ref[kRows];
@@ -358,10 +363,11 @@ __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const __grid_c
     __syncthreads();
     if (tid < rows) s_ref[tid] = __ldcg(refs_of(p, seq, cur.h) + tid);
     __syncthreads();
-    for (int c = c0; c < c1; ++c) {
-      const int key = c * kKeys + tid;
+#pragma unroll 2
+    for (int c = c0 + tid / kKeys; c < c1; c += kAddChunks) {
+      const int key = c * kKeys + tid % kKeys;
       const int page = key < keys ? lookup(p, cur.b, key) : -1;
-      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kKeys + tid;
+      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kKeys + tid % kKeys;
       float add = 0.f;
 #pragma unroll 4
       for (int r = 0; r < rows; ++r) {
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+  const uint32_t tmem = same_in_all(static_cast<uint32_t>(sm->tmem));
   const int n_chunks = range.g1 - range.g0;
   auto tiles_of = [&](const WorkCursor& c) { return work_rows(c.seq, shape) - c.rt * shape.rows > tile_rows ? 2 : 1; };
 
@@ -473,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc = make_idesc(1u, kTileRows, kKeys);
     constexpr uint64_t hi = desc_high(1024);
+    const uint32_t ub = same_in_all(u_base), qb = same_in_all(q_base);
     int pos = 0, item = 0, c = cur.c, used[kTiles] = {0, 0}, tiles = tiles_of(cur);
     uint32_t round = 0;
     bool fresh = true;
@@ -490,12 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < C::units; ++u) {
           if (!w.warp(kUFull + at, rd & 1, kStatusTimeout)) break;
           tc_fence_after();
+          const uint32_t all = same_in_all(static_cast<uint32_t>(at | buf << 8 | t << 16));
+          const uint32_t al = desc_low(qb + ((all >> 16) * C::units + u) * kUnitBytes, 16);
+          const uint32_t bl = desc_low(ub + (all & 255) * kUnitBytes, 16), d = tmem + (all >> 8 & 255) * kKeys;
           if (elect_one()) {
-            const uint32_t al = desc_low(q_base + (t * C::units + u) * kUnitBytes, 16);
-            const uint32_t bl = desc_low(u_base + at * kUnitBytes, 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16(tmem + buf * kKeys, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, u + k != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, u + k != 0 ? 1u : 0u);
             if (t + 1 == tiles) tc_commit(w.bar(kUEmpty + at));
             if (u + 1 == C::units) {
               tc_commit(w.bar(kSFull + buf));
@@ -545,51 +552,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[(i + c - c0) & 31]);
           const bool edge = key0 + kKeys > see_all || bad != 0;
+          uint32_t x[4][32];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t x[2][32];
-            tmem_ld_32x32b_x32(my_tmem + buf * kKeys + half * 64, x[0]);
-            tmem_ld_32x32b_x32(my_tmem + buf * kKeys + half * 64 + 32, x[1]);
-            tmem_ld_wait();
-            if (half == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
-            }
-            if (__builtin_expect(edge, 0)) {
+          for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(my_tmem + buf * kKeys + q * 32, x[q]);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
+          if (__builtin_expect(edge, 0)) {
 #pragma unroll
-              for (int b = 0; b < 2; ++b)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int k = half * 64 + b * 32 + e;
-                  if (key0 + k >= see || (bad >> (k >> 4) & 1u) != 0) x[b][e] = 0xFF800000u;      // -inf
-                }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mx[(e / 2) & 3] = max_of_3(mx[(e / 2) & 3], __uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
-            const float up = fmaxf(m, top);
-            l *= safe_ex2(m, up);
-            m = up;
-            const float ref = m == -INFINITY ? 0.f : -m;
-            const float2 ref2 = make_float2(ref, ref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 v = fma_pair(make_float2(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])), qs2, ref2);
-                v.x = ex2(v.x);
-                v.y = ex2(v.y);
-                sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], v);
+              for (int e = 0; e < 32; ++e) {
+                const int k = q * 32 + e;
+                if (key0 + k >= see || (bad >> (k >> 4) & 1u) != 0) x[q][e] = 0xFF800000u;      // -inf
               }
-            sum[0] = add_pair(sum[0], sum[1]);
-            l += sum[0].x + sum[0].y;
           }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mx[(e / 2) & 3] = max_of_3(mx[(e / 2) & 3], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+          const float up = fmaxf(m, top);
+          l *= safe_ex2(m, up);
+          m = up;
+          const float ref = m == -INFINITY ? 0.f : -m;
+          const float2 ref2 = make_float2(ref, ref);
+          float2 sum[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 v = fma_pair(make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), qs2, ref2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              sum[(e >> 1) & 3] = add_pair(sum[(e >> 1) & 3], v);
+            }
+          sum[0] = add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
         }
       }
       i += c1 - c0;
@@ -736,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm->tmem);
+  const uint32_t tmem = same_in_all(static_cast<uint32_t>(sm->tmem));
 
   // this block's units, in order; each role walks them by itself
   int u = static_cast<int>(blockIdx.x), b = 0, first = 0;
@@ -789,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc = make_idesc(1u, kKeys, kTileRows);
     constexpr uint64_t hi = desc_high(1024);
+    const uint32_t kbase = same_in_all(k_base), qb = same_in_all(q_base);
     int pos = 0, kb = 0, j = 0;
     uint32_t round = 0, k_round = 0;
     while (w.ok && next_unit(&un)) {
@@ -799,15 +804,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!w.warp(kSFree + buf, ((j / kBufs) & 1) ^ 1, kStatusTimeout) || !w.warp(kQFull + pos, round & 1, kStatusTimeout))
           break;
         tc_fence_after();
+        const uint32_t all = same_in_all(static_cast<uint32_t>(pos | buf << 8 | kb << 16));
+        const uint32_t al = desc_low(kbase + (all >> 16) * C::units * kUnitBytes, 16);
+        const uint32_t bl = desc_low(qb + (all & 255) * C::units * kUnitBytes, 16), d = tmem + (all >> 8 & 255) * kTileRows;
         if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < C::units; ++i) {
-            const uint32_t al = desc_low(k_base + (kb * C::units + i) * kUnitBytes, 16);
-            const uint32_t bl = desc_low(q_base + (pos * C::units + i) * kUnitBytes, 16);
+          for (int i = 0; i < C::units; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16(tmem + buf * kTileRows, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, i + k != 0 ? 1u : 0u);
-          }
+              mma_bf16(d, hi | (al + (i * kUnitBytes >> 4) + 2 * k), hi | (bl + (i * kUnitBytes >> 4) + 2 * k), idesc,
+                       i + k != 0 ? 1u : 0u);
           tc_commit(w.bar(kQEmpty + pos));
           if (t + 1 == un.t1)
             for (int i = 0; i < C::units; ++i) tc_commit(w.bar(kKEmpty + kb * C::units + i));
@@ -854,43 +860,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hi_ = min(tile_rows, all - row0);
         w.warp(kSFull + buf, (at / kBufs) & 1, kStatusTimeout);
         tc_fence_after();
+        uint32_t x[4][32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[2][32];
-          tmem_ld_32x32b_x32(my_tmem + buf * kTileRows + half * 64, x[0]);
-          tmem_ld_32x32b_x32(my_tmem + buf * kTileRows + half * 64 + 32, x[1]);
-          tmem_ld_wait();
-          if (half == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
-          }
-          if (__builtin_expect(edge, 0)) {
+        for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(my_tmem + buf * kTileRows + q * 32, x[q]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
+        if (__builtin_expect(edge, 0)) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int col = half * 64 + q * 32 + e;
-                if (col < lo || col >= hi_) x[q][e] = 0xFF800000u;       // -inf
-              }
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 r4 = *reinterpret_cast<const float4*>(&rs[half * 64 + q * 32 + e]);
-              float2 v = fma_pair(make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), qs2,
-                                  make_float2(r4.x, r4.y));
-              float2 z = fma_pair(make_float2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3])), qs2,
-                                  make_float2(r4.z, r4.w));
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              z.x = ex2(z.x);
-              z.y = ex2(z.y);
-              acc[0] = add_pair(acc[0], v);
-              acc[1] = add_pair(acc[1], z);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e < lo || q * 32 + e >= hi_) x[q][e] = 0xFF800000u;       // -inf
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 r4 = *reinterpret_cast<const float4*>(&rs[q * 32 + e]);
+            float2 v = fma_pair(make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), qs2,
+                                make_float2(r4.x, r4.y));
+            float2 z = fma_pair(make_float2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3])), qs2,
+                                make_float2(r4.z, r4.w));
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            acc[0] = add_pair(acc[0], v);
+            acc[1] = add_pair(acc[1], z);
+          }
       }
       j += un.t1 - un.t0;
       acc[0] = add_pair(acc[0], acc[1]);
@@ -983,7 +982,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (p.scores != nullptr) {
-    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms * 8));
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms * 4));
     cfg.blockDim = dim3(few::kAddThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, few::weights_add_kernel, p);
