@@ -10,7 +10,8 @@
 namespace cxa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 320, kWarps = kThreads / 32;
+static_assert(kThreads >= kLatentMaxBlocks, "a thread a block's item, and a part");
 constexpr int kWarpParts = 16;     // parts that a warp merges by itself
 
 struct MergeParams {

@@ -13,7 +13,7 @@
 
 namespace cxa {
 
-constexpr int kLatentMaxBlocks = 160;
+constexpr int kLatentMaxBlocks = 320;      // two an SM, where rows are narrow (latent_rows.cu)
 
 struct LatentCut {
   int q0, rt, parts, rows;     // of the item: first token row, tile, parts (0: none), rows of the tile
@@ -25,9 +25,12 @@ static_assert(kLatentCutBytes % 256 == 0, "the partial states behind are aligned
 // A partial state: [R][latent] sums, then R references (base 2) and R sums of weights.
 __host__ __device__ constexpr size_t latent_slot(int R, int latent) { return static_cast<size_t>(R) * (latent + 2); }
 
-inline size_t latent_parts_bytes(int R, int latent) {
-  return kLatentCutBytes + 2 * static_cast<size_t>(kLatentMaxBlocks) * latent_slot(R, latent) * 4;
+inline size_t latent_parts_bytes(int R, int latent, int blocks) {
+  return kLatentCutBytes + 2 * static_cast<size_t>(blocks) * latent_slot(R, latent) * 4;
 }
+// Blocks an SM of the fp32 kernel, and the most that a kernel of so many an SM runs.
+constexpr int latent_rows_blocks(int latent) { return latent <= 256 ? 2 : 1; }
+constexpr int latent_max_blocks(int per_sm) { return 160 * per_sm; }
 
 // Enqueues the merge behind a kernel of `blocks` blocks (latent_merge.cu).
 cudaError_t launch_latent_merge(const LatentAttnLaunch& a, int R, int blocks, const DeviceInfo& dev,

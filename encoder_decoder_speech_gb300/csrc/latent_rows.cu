@@ -57,7 +57,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
 }
 
 template <int kQuads>
-__global__ void __launch_bounds__(kThreads, 1) latent_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) latent_rows_kernel(const __grid_constant__ RowsParams p) {
   using S = Shape<kQuads>;
   extern __shared__ __align__(16) float smem[];
   float* const s_k = smem;                               // [2][kKeys][row]
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_rows_kernel(const __grid_c
   WorkCursor cur;
   WorkShape shape = p.shape;
   LatentCut cut = {0, 0, 0, 0};
-  if (!work_locate<kThreads, true>(bt, shape, 1, &s_work, &range, &cur, p.status)) {
+  if (!work_locate<kThreads, false>(bt, shape, 1, &s_work, &range, &cur, p.status)) {
     if (tid == 0) p.cut[blockIdx.x] = cut;
     return;
   }
@@ -93,25 +93,35 @@ __global__ void __launch_bounds__(kThreads, 1) latent_rows_kernel(const __grid_c
     const int s0 = chunk_step(shape, c0, cur.nc, steps), s1 = chunk_step(shape, c1, cur.nc, steps);
     const int* table_row = bt.table + static_cast<size_t>(cur.b) * bt.width;
     const float* pool = static_cast<const float*>(p.layer.C);
+    // the pages of a step's groups of 16 keys, in lanes 0 and 1 (-1: none, or outside the pool); asked for a
+    // step before they are used
+    auto look = [&](int s) {
+      const int key = s * kKeys + lane * 16;
+      int page = -1;
+      if (lane < kKeys / 16 && s < s1 && key < keys) {
+        page = paged_lookup(table_row, bt.width, shift, p.layer.num_pages, key);
+        if (page < 0 && warp == 0) atomicOr(p.status, kStatusBadPage);
+      }
+      return page;
+    };
     // rows that no query sees, and of bad pages, become zero
-    auto fetch = [&](int s) {
+    auto fetch = [&](int s, int pages) {
       const int pieces = width / 4;
       float* buf = s_k + (s & 1) * (kKeys * S::row);
-      for (int k = warp; k < kKeys; k += kWarps) {
-        const int key = s * kKeys + k;
-        int page = -1;
-        if (key < keys) {
-          page = paged_lookup(table_row, bt.width, shift, p.layer.num_pages, key);
-          if (page < 0 && lane == 0) atomicOr(p.status, kStatusBadPage);
-        }
+#pragma unroll
+      for (int i = 0; i < kKeys / kWarps; ++i) {
+        const int k = warp + i * kWarps, key = s * kKeys + k;
+        const int page = __shfl_sync(0xffffffffu, pages, k >> 4);
+        const bool real = page >= 0 && key < keys;
         const float* src =
             pool + ((static_cast<size_t>(max(page, 0)) << shift) + (key & ((1 << shift) - 1))) * static_cast<size_t>(width);
         for (int c = lane; c < pieces; c += 32)
-          cp_async16(smem_u32(buf + k * S::row + c * 4), page >= 0 ? src + c * 4 : pool, page >= 0);
+          cp_async16(smem_u32(buf + k * S::row + c * 4), real ? src + c * 4 : pool, real);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(s0);
+    int pages = look(s0), next = look(s0 + 1);
+    fetch(s0, pages);
     for (int i = warp; i < kRows; i += kWarps) {
       const int at = row0 + i;
       const float* src = p.q + (seq.q0 + at / H) * p.q_stride + static_cast<long long>(at % H) * width;
@@ -136,8 +146,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_rows_kernel(const __grid_c
     for (int i = 0; i < S::rows; ++i) o[i][0] = o[i][1] = 0.f;
 
     for (int s = s0; s < s1; ++s) {
+      const int now = pages;
       if (s + 1 < s1) {
-        fetch(s + 1);
+        fetch(s + 1, next);
+        pages = next;
+        next = look(s + 2);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
       } else {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_rows_kernel(const __grid_c
       // ---- softmax
       {
         const int key = key0 + lane;
-        const bool there = key < keys && paged_lookup(table_row, bt.width, shift, p.layer.num_pages, key) >= 0;
+        const bool there = __shfl_sync(0xffffffffu, now, lane >> 4) >= 0 && key < keys;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = 2 * warp + i;
@@ -312,7 +325,8 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   cudaError_t e = allow_smem(latent_rows_kernel<kQuads>, Shape<kQuads>::smem, dev.device, &once);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int grid = dev.num_sms < kLatentMaxBlocks ? dev.num_sms : kLatentMaxBlocks;
+  constexpr int per_sm = latent_rows_blocks(kQuads * 128);
+  const int most = latent_max_blocks(per_sm), grid = dev.num_sms * per_sm < most ? dev.num_sms * per_sm : most;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<kQuads>::smem;

@@ -696,7 +696,7 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   cudaError_t e = allow_smem(latent_tile_kernel<kR>, kSmemBytes, dev.device, &once);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int grid = dev.num_sms < kLatentMaxBlocks ? dev.num_sms : kLatentMaxBlocks;
+  const int grid = dev.num_sms < latent_max_blocks(1) ? dev.num_sms : latent_max_blocks(1);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
@@ -721,7 +721,8 @@ int tile_rows(int H, int max_new) {
 }  // namespace
 
 size_t latent_attention_workspace(int H, int latent, int max_new, bool bf16) {
-  return latent_parts_bytes(bf16 ? tile_rows(H, max_new) : kLatentRowsF32, latent);
+  if (!bf16) return latent_parts_bytes(kLatentRowsF32, latent, latent_max_blocks(latent_rows_blocks(latent)));
+  return latent_parts_bytes(tile_rows(H, max_new), latent, latent_max_blocks(1));
 }
 
 cudaError_t launch_latent_attention(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_t stream,

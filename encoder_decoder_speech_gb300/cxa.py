@@ -706,6 +706,24 @@ def _rows(name, t, H, dh, n, dtype, index):
     return s0
 
 
+def _row(name, t, width, n, dtype, index):
+    """Check a packed [n tokens, width] tensor; returns its row stride."""
+    if t.shape != (n, width):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(n, width)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and width > 1:
+        raise ValueError(f"{name}: a token's channels must be contiguous")
+    if n <= 1:
+        s0 = width
+    elif s0 < width:
+        raise ValueError(f"{name}: the rows of different tokens must not overlap")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return s0
+
+
 def _heads(name, t):
     """The tokens and heads of a packed tensor."""
     shape = t.shape
@@ -1130,12 +1148,12 @@ class LatentCache(_Paged):
         if len(c.shape) != 2:
             raise ValueError("c must be [tokens, latent]")
         n = c.shape[0]
-        cs = _rows("c", c.unsqueeze(1), 1, self.latent, n, dt, at)
+        cs = _row("c", c, self.latent, n, dt, at)
         ks, kp = 0, None
         if self.rope:
-            if kr is None or len(kr.shape) != 2:
+            if kr is None:
                 raise ValueError("kr must be [tokens, rope]")
-            ks, kp = _rows("kr", kr.unsqueeze(1), 1, self.rope, n, dt, at), kr.data_ptr()
+            ks, kp = _row("kr", kr, self.rope, n, dt, at), kr.data_ptr()
         elif kr is not None:
             raise ValueError("kr must be None where rope is 0")
         norm, eps = (CXA_NORM_NONE, 0.0) if norm_eps is None else (CXA_NORM_RMS, norm_eps)
