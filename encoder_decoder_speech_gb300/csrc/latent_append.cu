@@ -23,7 +23,7 @@ struct AppendParams {
   long long c_stride, kr_stride;
   const float* weight;
   float eps;
-  int norm;
+  int norm, wide;             // wide: the weights are 16-byte aligned
   unsigned int* status;
   PagedBatch batch;
   LatentLayer layer;
@@ -77,6 +77,17 @@ __global__ void __launch_bounds__(kWarps * 32) latent_append_kernel(const __grid
   if (e0 < dr) s0 = to_f(kr[e0]);
   if (e1 < dr) s1 = to_f(kr[e1]);
 
+  float4 g[4];      // weights
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    g[j] = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (j < quads && p.norm && p.weight != nullptr) {
+      const float* from = p.weight + j * 128 + lane * 4;
+      g[j] = p.wide ? __ldg(reinterpret_cast<const float4*>(from))
+                    : make_float4(__ldg(from), __ldg(from + 1), __ldg(from + 2), __ldg(from + 3));
+    }
+  }
+
   const int seq = find_seq(p.batch.q_start, p.batch.B, token, lane);
   if (seq < 0) return;
   const PagedSeq s = paged_seq(p.batch.q_start, p.batch.kv_len, seq, p.batch.n_tokens);
@@ -103,14 +114,9 @@ __global__ void __launch_bounds__(kWarps * 32) latent_append_kernel(const __grid
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j < quads) {
-      float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (p.norm && p.weight != nullptr) {
-        const float* g = p.weight + j * 128 + lane * 4;
-        w = make_float4(__ldg(g), __ldg(g + 1), __ldg(g + 2), __ldg(g + 3));
-      }
-      store4(row + j * 128 + lane * 4, make_float4(x[j].x * r * w.x, x[j].y * r * w.y, x[j].z * r * w.z, x[j].w * r * w.w));
-    }
+    if (j < quads)
+      store4(row + j * 128 + lane * 4,
+             make_float4(x[j].x * r * g[j].x, x[j].y * r * g[j].y, x[j].z * r * g[j].z, x[j].w * r * g[j].w));
   if (lane < pairs) {
     const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos)) * p.rot.step[lane];
     float sn, cs;
@@ -135,6 +141,7 @@ cudaError_t launch(const LatentAppendLaunch& a, const DeviceInfo& dev, cudaStrea
   p.weight = a.weight;
   p.eps = a.eps;
   p.norm = a.norm ? 1 : 0;
+  p.wide = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 ? 1 : 0;
   p.status = dev.status_word;
   p.batch = a.batch;
   p.layer = a.layer;
