@@ -322,9 +322,6 @@ int cxa_paged_evict(const cxa_pages* pages, int l0, int nl, float* weights, int 
     if (nl < 1 || nl > pages->L - l0) return fail(CXA_EINVAL, w + ": layers out of range");
     if (keep < 1 || first < 0 || recent < 0 || static_cast<long long>(first) + recent > keep)
       return fail(CXA_EINVAL, w + ": keep must be positive and hold first and recent, which must not be negative");
-    const long long cap = static_cast<long long>(max_pages) << pages->page_shift;
-    if ((static_cast<long long>(out_max_pages) << pages->page_shift) < (keep < cap ? keep : cap))
-      return fail(CXA_EINVAL, w + ": a row of out_table must hold what stays of a sequence");
     if (weights == nullptr || kept == nullptr || out_len == nullptr || !aligned(weights, 4) || !aligned(kept, 4) ||
         !aligned(out_len, 4))
       return fail(CXA_EINVAL, w + ": weights, kept or out_len is NULL or not 4-byte aligned");

@@ -518,7 +518,8 @@ CXA_API int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_to
  *   keep       >= 1, first + recent <= keep, nl * B * Hkv * (keep / 64 + 8) below 2^31.
  *   kv_len     device int32 [B], page_table device int32 [B][max_pages]: the sequences as they are.
  *   out_table  device int32 [B][out_max_pages]: pages that no sequence of the call reads, each
- *              once (cxa_paged_evict_check); room for min(keep, max_pages * page_size) positions.
+ *              once (cxa_paged_evict_check), with room for min(keep, kv_len) positions. What has no page of
+ *              the pool is left out and reported (CXA_EPAGE from cxa_device_status).
  *   kept       device int32 [nl][B][Hkv][keep]: the old positions of what stays, ascending, then -1.
  *   out_len    device int32 [B], not kv_len: min(keep, kv_len).
  * Rows of the destination behind the last one are left as they are. Two kernels.

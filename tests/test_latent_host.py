@@ -227,7 +227,7 @@ def test_evict_refusals(pages):
     refused(evict(pages, l0=1, nl=2), "layers")
     for kw in (dict(keep=0), dict(first=-1), dict(recent=-1), dict(first=17), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1)):
         refused(evict(pages, **kw), "keep must be positive")
-    refused(evict(pages, out_max_pages=1), "a row of out_table")
+    refused(evict(pages, out_max_pages=0), "max_pages")
     refused(evict(pages, out_table=0), "NULL")
     refused(evict(pages, weights=0), "weights, kept or out_len")
     refused(evict(pages, kept=0), "weights, kept or out_len")
