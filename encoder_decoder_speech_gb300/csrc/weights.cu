@@ -12,7 +12,7 @@ bool on_tiles(int G, bool bf16) { return bf16 && G <= 128; }
 size_t weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new, bool bf16) {
   const int G = Hq / Hkv;
   size_t n = kPagedCounterBytes + weights_ref_bytes(static_cast<long long>(n_tokens) * Hq) + kWeightsPartBytes;
-  if (on_tiles(G, bf16) && weights_few(G, max_new)) n += weights_score_bytes(B, width, page_shift, Hkv, G, max_new);
+  if (on_tiles(G, bf16)) n += weights_split(B, width, page_shift, Hkv, G, max_new).score_bytes;
   return n;
 }
 

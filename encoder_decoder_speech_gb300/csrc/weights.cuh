@@ -17,10 +17,14 @@ constexpr size_t kWeightsPartBytes = static_cast<size_t>(2 * kWeightsMaxBlocks) 
 
 // fp32, and bf16 with more query heads a K/V head than a tile holds, on the CUDA cores (weights_rows.cu).
 cudaError_t launch_weights_rows(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream);
-// bf16 (weights_tile.cu): whether a call has few query rows, and the room that their scores take (0:
-// too much, they are not kept).
-bool weights_few(int G, int max_new);
-size_t weights_score_bytes(int B, int width, int page_shift, int Hkv, int G, int max_new);
+// bf16 (weights_tile.cu): sequences of up to few_rows query rows a K/V head go one way, the others
+// another; score_bytes is the room that the former's scores take (0: too much, they are not kept).
+struct WeightsSplit {
+  int few_rows;       // 0: none do
+  bool many;          // whether there can be others
+  size_t score_bytes;
+};
+WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new);
 cudaError_t launch_weights_tile(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
 
 }  // namespace cxa

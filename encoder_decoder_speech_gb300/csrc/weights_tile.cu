@@ -12,7 +12,8 @@
 // Both are bound by the exponentials, 32 a clock of an SM: 512 clocks for 128 x 128 scores, against 256 (64
 // channels) or 512 (128) for their product.
 //
-// Few query rows (16 a K/V head at most: single tokens), bound by reading K:
+// Few query rows (16 a K/V head at most: single tokens, in a batch of their own or beside prompts, see
+// weights_split), bound by reading K:
 //   weights_few_kernel   the transposed product again, of 128 keys by 16 rows; a thread has a key, keeps
 //                        references and sums of its own until the item's end, and stores the scores (4 bytes a row
 //                        and key, against 2 dh bytes of the key itself).
@@ -549,6 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = c0; c < c1; ++c, ++used) {
           const int buf = t * 2 + (used & 1), key0 = c * kKeys;
           w.warp(kSFull + buf, (used >> 1) & 1, kStatusTimeout);
+          if ((warp & 3) * 32 >= rows) {      // (none of the warp's rows is a token's)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
+            continue;
+          }
           tc_fence_after();
           const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[(i + c - c0) & 31]);
           const bool edge = key0 + kKeys > see_all || bad != 0;
@@ -915,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace sum
 
 constexpr size_t kMaxScoreBytes = 256u << 20;
+constexpr double kSplitChunks = 8192;
 
 template <int kDh>
 cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
@@ -941,22 +948,30 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   ws += weights_ref_bytes(static_cast<long long>(a.batch.n_tokens) * a.Hq);
   p.part = reinterpret_cast<float*>(ws);
   ws += kWeightsPartBytes;
-  const bool few_rows = weights_few(G, a.max_new);
-  const size_t score_bytes = few_rows ? weights_score_bytes(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, G, a.max_new) : 0;
-  p.scores = score_bytes != 0 ? reinterpret_cast<float*>(ws) : nullptr;
-  p.max_rows = G * a.max_new;
+  const WeightsSplit split = weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, G, a.max_new);
+  p.scores = split.score_bytes != 0 ? reinterpret_cast<float*>(ws) : nullptr;
+  p.max_rows = split.few_rows;
   p.status = dev.status_word;
   p.batch = a.batch;
   p.num_pages = a.layer.num_pages;
   p.Hkv = a.layer.Hkv;
   p.page_shift = a.layer.page_shift;
   p.shape.G = G;
-  p.shape.rows = few_rows ? few::kRows : many::kTiles * (kTileRows / G * G);
   p.shape.chunk_shift = kChunkShift;
   p.shape.coarse = false;
   p.shape.cap = a.batch.width << a.layer.page_shift;
-  p.shape.min_rows = 0;
-  p.shape.max_rows = few_rows ? p.max_rows : 0x7FFFFFFF;      // (the room for scores holds no more)
+  WeightsParams few = p;
+  few.shape.rows = few::kRows;
+  few.shape.min_rows = 0;
+  few.shape.max_rows = split.few_rows;      // (the room for scores holds no more)
+  p.shape.rows = many::kTiles * (kTileRows / G * G);
+  p.shape.min_rows = split.few_rows + 1;
+  p.shape.max_rows = 0x7FFFFFFF;
+  WeightsParams sums = p;                   // without their scores, the few rows' weights too
+  if (split.few_rows > 0 && p.scores == nullptr) {
+    sums.shape.min_rows = 0;
+    if (!split.many) sums.shape.max_rows = split.few_rows;
+  }
   static SmemOnce once[3];
   cudaError_t e = allow_smem(few::weights_few_kernel<kDh>, kSmemBytes, dev.device, &once[0]);
   if (e == cudaSuccess) e = allow_smem(many::weights_ref_kernel<kDh>, kSmemBytes, dev.device, &once[1]);
@@ -972,36 +987,51 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (few_rows) {
+  auto launched = [&](cudaError_t r) {
+    if (r == cudaSuccess) count_launches(1);
+    e = r;
+    return r == cudaSuccess;
+  };
+  if (split.few_rows > 0) {
     cfg.blockDim = dim3(few::kThreads);
-    e = cudaLaunchKernelEx(&cfg, few::weights_few_kernel<kDh>, k, p);
-  } else {
-    cfg.blockDim = dim3(many::kThreads);
-    e = cudaLaunchKernelEx(&cfg, many::weights_ref_kernel<kDh>, q, k, p);
+    if (!launched(cudaLaunchKernelEx(&cfg, few::weights_few_kernel<kDh>, k, few))) return e;
   }
-  if (e != cudaSuccess) return e;
-  count_launches(1);
+  if (split.many) {
+    cfg.blockDim = dim3(many::kThreads);
+    if (!launched(cudaLaunchKernelEx(&cfg, many::weights_ref_kernel<kDh>, q, k, p))) return e;
+  }
+  if (split.many || p.scores == nullptr) {
+    cfg.blockDim = dim3(sum::kThreads);
+    if (!launched(cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh>, q, k, sums))) return e;
+  }
   if (p.scores != nullptr) {
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms * 4));
     cfg.blockDim = dim3(few::kAddThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, few::weights_add_kernel, p);
-  } else {
-    cfg.blockDim = dim3(sum::kThreads);
-    e = cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh>, q, k, p);
+    launched(cudaLaunchKernelEx(&cfg, few::weights_add_kernel, few));
   }
-  if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
 }  // namespace
 
-bool weights_few(int G, int max_new) { return static_cast<long long>(G) * max_new <= few::kRows; }
-
-size_t weights_score_bytes(int B, int width, int page_shift, int Hkv, int G, int max_new) {
+// Which sequences have few rows: all, where no sequence can have more than a product's 16; otherwise those of one
+// or two tokens (more would take room for scores that hardly any use), if their scores can be kept, there is more
+// than one sequence, and the keys are many enough to pay for two more launches. (20 single tokens beside 4
+// chunks of a prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 240 so; 5 tokens in each
+// of 16 sequences of up to 1500 keys of 8 heads: 39 us and 45.)
+WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new) {
   const double chunks = static_cast<double>(B) * Hkv * (((static_cast<long long>(width) << page_shift) >> kChunkShift) + 1);
-  const double bytes = chunks * G * max_new * kKeys * 4;
-  return bytes <= static_cast<double>(kMaxScoreBytes) ? static_cast<size_t>(bytes) : 0;
+  auto bytes = [&](int rows) {
+    const double n = chunks * rows * kKeys * 4;
+    return n <= static_cast<double>(kMaxScoreBytes) ? static_cast<size_t>(n) : 0;
+  };
+  WeightsSplit s;
+  s.many = static_cast<long long>(G) * max_new > few::kRows;
+  s.few_rows = !s.many ? G * max_new : B == 1 || chunks < kSplitChunks ? 0 : 2 * G < few::kRows ? 2 * G : few::kRows;
+  s.score_bytes = bytes(s.few_rows);
+  if (s.many && s.score_bytes == 0) s.few_rows = 0;
+  return s;
 }
 
 cudaError_t launch_weights_tile(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {

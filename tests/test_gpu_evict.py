@@ -489,3 +489,15 @@ def test_a_decoder_that_evicts(pool):
             at = torch.arange(lens[b] - n[b], lens[b], device="cuda")
             gathered = W[0][as_table()[b][at // page].long(), :, at % page].T.double()
             assert float((gathered - own).abs().max()) <= 2.0 ** -10 * (Hq // Hkv)
+
+
+@pytest.mark.parametrize("Hq, Hkv", [(8, 8), (8, 2), (5, 1)])
+def test_single_tokens_beside_prompts_over_long_contexts(Hq, Hkv):
+    """Enough keys that sequences of few query rows go a way of their own."""
+    b = Batch([1, 70, 2, 0, 1, 3, 40], [70000, 300, 66000, 100, 1, 9000, 40], 256, Hq, Hkv, 64, "bf16", seed=Hq).fill()
+    b.d["page_table"] = torch.cat([b.table, torch.full((7, 400), -1, dtype=torch.int32)], 1).cuda()
+    before = b.W.clone()
+    first = b.accumulate().clone()
+    b.close(before, first)
+    b.W.copy_(before)
+    assert torch.equal(b.accumulate(), first)
