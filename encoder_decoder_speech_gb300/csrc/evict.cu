@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
     if (!stays) {
       const int page = paged_lookup(row, a.width, a.page_shift, a.num_pages, t);
       if (page < 0) atomicOr(p.status, kStatusBadPage);
-      w = page < 0 ? 0.f : __ldg(W + ((static_cast<size_t>(page) * a.Hkv + h) << a.page_shift) + (t & ((1 << a.page_shift) - 1)));
+      w = page < 0 ? 0.f : __ldcg(W + ((static_cast<size_t>(page) * a.Hkv + h) << a.page_shift) + (t & ((1 << a.page_shift) - 1)));
     }
     return order_key(w, stays);
   };

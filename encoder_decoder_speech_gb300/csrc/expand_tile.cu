@@ -47,7 +47,7 @@ constexpr int kStage = kBlocks / 2 * kBox;
 constexpr int kMaxStages = 16, kMaxA = 8;
 constexpr int kPutBytes = 32 * kCols * 2;  // 32 rows of them, as they are written
 constexpr int kOutBytes = kOutWarps * kPutBytes;      // a buffer of each warp
-constexpr int kSmemBytes = 232448, kSmallBytes = 3072;
+constexpr int kSmemBytes = 232448, kSmallBytes = 3 << 10;
 
 enum Bars {
   kAFull = 0,

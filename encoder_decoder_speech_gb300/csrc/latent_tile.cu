@@ -73,7 +73,7 @@ struct Small {
   float m[64], inv[64];
   long long row[64];           // where the rows' results begin
 };
-constexpr int kSmallBytes = 3072;
+constexpr int kSmallBytes = 3 << 10;
 static_assert(sizeof(Small) <= kSmallBytes, "the small arrays fit behind the ring");
 
 struct TileParams {

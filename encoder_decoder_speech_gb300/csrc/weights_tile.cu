@@ -1028,7 +1028,8 @@ WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int
   };
   WeightsSplit s;
   s.many = static_cast<long long>(G) * max_new > few::kRows;
-  s.few_rows = !s.many ? G * max_new : B == 1 || chunks < kSplitChunks ? 0 : 2 * G < few::kRows ? 2 * G : few::kRows;
+  const int tokens = few::kRows / G < 2 ? few::kRows / G : 2;
+  s.few_rows = !s.many ? G * max_new : B == 1 || chunks < kSplitChunks ? 0 : tokens * G;
   s.score_bytes = bytes(s.few_rows);
   if (s.many && s.score_bytes == 0) s.few_rows = 0;
   return s;

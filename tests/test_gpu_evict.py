@@ -491,13 +491,63 @@ def test_a_decoder_that_evicts(pool):
             assert float((gathered - own).abs().max()) <= 2.0 ** -10 * (Hq // Hkv)
 
 
-@pytest.mark.parametrize("Hq, Hkv", [(8, 8), (8, 2), (5, 1)])
+@pytest.mark.parametrize("Hq, Hkv", [(8, 8), (8, 2), (5, 1), (12, 1), (20, 1)])
 def test_single_tokens_beside_prompts_over_long_contexts(Hq, Hkv):
     """Enough keys that sequences of few query rows go a way of their own."""
     b = Batch([1, 70, 2, 0, 1, 3, 40], [70000, 300, 66000, 100, 1, 9000, 40], 256, Hq, Hkv, 64, "bf16", seed=Hq).fill()
-    b.d["page_table"] = torch.cat([b.table, torch.full((7, 400), -1, dtype=torch.int32)], 1).cuda()
+    b.d["page_table"] = torch.cat([b.table, torch.full((7, 2000), -1, dtype=torch.int32)], 1).cuda()
     before = b.W.clone()
     first = b.accumulate().clone()
     b.close(before, first)
     b.W.copy_(before)
     assert torch.equal(b.accumulate(), first)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 0, 2], [3, 40, 1, 2]])
+def test_scores_that_have_no_room(n):
+    """Rows of the table for more keys than scores are kept of: the keys are read twice instead."""
+    b = Batch(n, [700, 90, 30, 2], 64, 4, 2, 128, "bf16", seed=6).fill()
+    b.d["page_table"] = torch.cat([b.table, torch.full((4, 1 << 20), -1, dtype=torch.int32)], 1).cuda()
+    before = b.W.clone()
+    b.close(before, b.accumulate(decay=0.5), decay=0.5)
+
+
+def test_evict_more_keys_than_shared_memory_holds():
+    kv, keep, page = 400_003, 5000, 256
+    need, out_need = -(-kv // page), -(-keep // page)
+    cache = cxa.PagedCache(need + out_need, page, 1, 1, 64, "bf16")
+    g = torch.Generator().manual_seed(3)
+    cache.Kp.copy_(torch.randn(cache.Kp.shape, generator=g))
+    cache.Vp.copy_(torch.randn(cache.Vp.shape, generator=g))
+    W = cache.new_weights()
+    W.copy_(torch.randint(0, 3000, W.shape, generator=g).float())      # (many are equal)
+    perm = torch.randperm(need + out_need, generator=g).to(torch.int32)
+    table, out = perm[None, :need].contiguous(), perm[None, need:].contiguous()
+    t = torch.arange(kv)
+    place = (table[0, t // page].long(), t % page)
+    w = W.cpu()[0, :, 0][place]
+    w[:7], w[-9:] = math.inf, math.inf
+    want = torch.sort(torch.sort(w, descending=True, stable=True).indices[:keep]).values
+    K = cache.Kp.cpu()[0, :, 0][place][want]
+    kept, out_len = cache.evict(W, keep, torch.tensor([kv], dtype=torch.int32).cuda(), table.cuda(), out.cuda(),
+                                first=7, recent=9)
+    assert torch.equal(kept.cpu()[0, 0, 0].long(), want) and out_len.tolist() == [keep]
+    t = torch.arange(keep)
+    assert torch.equal(cache.Kp.cpu()[0, :, 0][out[0, t // page].long(), t % page], K)
+
+
+def test_evict_with_too_few_pages_reports_them():
+    """What has a page is copied; the positions without one are left out, and the status says so."""
+    b = Batch([0, 0], [100, 20], 16, 2, 2, 64, "bf16", seed=8, spare=6).fill()
+    free = [p for p in range(b.cache.num_pages) if p not in b.table.flatten().tolist()][:4]
+    out = torch.tensor([[free[0], free[1]], [free[2], free[3]]], dtype=torch.int32).cuda()
+    before = b.cache.Kp.clone()
+    kept, out_len = b.cache.evict(b.W, 64, b.d["kv_len"], b.d["page_table"], out)
+    torch.cuda.synchronize()
+    assert cxa.cxa_device_status(1) == cxa.CXA_EPAGE and cxa.cxa_device_status(1) == cxa.CXA_OK
+    assert out_len.tolist() == [64, 20]
+    for h in range(2):
+        t = kept[0, 0, h, :32].cpu().long()
+        got = torch.cat([b.cache.Kp[0, free[0], h], b.cache.Kp[0, free[1], h]])
+        page, at = b.table[0][t // 16].long(), t % 16
+        assert torch.equal(got.cpu(), before.cpu()[0, page, h, at])

@@ -175,6 +175,19 @@ def test_append_leaves_out_bad_pages_and_rows_of_no_sequence():
     assert torch.equal(before, b.cache.Cp)
 
 
+def test_append_with_weights_anywhere():
+    """Norm weights need 4 bytes of alignment, no more."""
+    b = Batch([1, 3], [20, 3], 16, 1, 384, 0, "bf16")
+    b.cache.Cp.zero_()
+    c = randn(b.N, 384, seed=3).cuda()
+    w = randn(385, seed=4).cuda()
+    b.cache.append(0, c, None, **b.d, norm_eps=1e-5, weight=w[1:].clone())
+    want = b.cache.Cp.clone()
+    b.cache.Cp.zero_()
+    b.cache.append(0, c, None, **b.d, norm_eps=1e-5, weight=w[1:])
+    assert torch.equal(b.cache.Cp, want) and float(want.float().abs().max()) > 0
+
+
 # ------------------------------------------------------------------ attention
 CASES = [
     dict(n=[1], kv=[1]),
