@@ -543,18 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = max(0, min(tile_rows, work_rows(seq, shape) - row0));
       const bool real = r < rows;
       float m = -INFINITY, l = 0.f;
-      if (rows > 0) {
+      if (rows > 0 && (warp & 3) * 32 >= rows) {      // (none of this warp's rows is a token's)
+        for (int c = c0; c < c1; ++c, ++used) {
+          w.warp(kSFull + t * 2 + (used & 1), (used >> 1) & 1, kStatusTimeout);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w.bar(kSFree + t * 2 + (used & 1)));
+        }
+      } else if (rows > 0) {
         // (rows of no token go without masks: nothing of theirs is written)
         const int see = real ? visible_keys(seq, (row0 + r) / G, shape.cap) : 0x7FFFFFFF;
         const int see_all = visible_keys(seq, row0 / G, shape.cap);
         for (int c = c0; c < c1; ++c, ++used) {
           const int buf = t * 2 + (used & 1), key0 = c * kKeys;
           w.warp(kSFull + buf, (used >> 1) & 1, kStatusTimeout);
-          if ((warp & 3) * 32 >= rows) {      // (none of the warp's rows is a token's)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
-            continue;
-          }
           tc_fence_after();
           const uint32_t bad = *const_cast<volatile uint32_t*>(&sm->bad[(i + c - c0) & 31]);
           const bool edge = key0 + kKeys > see_all || bad != 0;
