@@ -5,8 +5,11 @@
 // item's keys (weights as integers in their order) in shared memory, read once; passes over their digits, with
 // histograms added up over distributed shared memory, find the keep-th largest; one more writes the
 // positions above it, and of those equal to it the first ones. (A block an item, which read the weights anew in
-// each pass: 225 us for 32 lists of 65536.) evict_copy_kernel copies the listed rows of K, V and
-// weights, a block 64 of them. Bound by memory: weights are read once, what stays is read and written once.
+// each pass: 225 us for 32 lists of 65536; a cluster 29, of which the first reads of the weights take 5 to 10, the
+// passes 3 each.) evict_copy_kernel copies the listed rows of K, V and weights, a block 64 of them.
+// Bound by memory: weights are read once, what stays is read and written once. 4 sequences of up to 65536 keys of
+// 8 heads of 128 down to 8192, bf16: 80 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
+// of 448 keys down to 112: 19 us, latency of the two kernels.
 #include "cluster.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
@@ -51,9 +54,9 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
   using S = Select<kAlone>;
   constexpr int kThreads = S::threads, kWarps = S::warps, kBins = S::bins;
   extern __shared__ uint32_t s_key[];        // [room]
-  __shared__ int s_hist[kBins];              // of this block
-  __shared__ int s_sum[kAlone ? 1 : kBins / 4];      // of its share of the bins, over the cluster
-  __shared__ int s_group[32];                // of 32 bins each
+  constexpr int kHists = kAlone ? 1 : S::passes;      // (one a pass: other blocks may still read the last one's)
+  __shared__ __align__(16) int s_hist[kHists][kBins];              // of this block
+  __shared__ int s_group[kHists][kAlone ? 1 : kBins / 32];         // sums of 32 of them
   __shared__ int s_scan[2][kWarps];
   __shared__ int s_count[2];
   __shared__ uint32_t s_prefix;
@@ -75,30 +78,41 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
     for (int i = rank * kThreads + tid; i < m; i += blocks * kThreads) kept[i] = i;
     return;
   }
-  auto all_sync = [&]() {
-    if constexpr (kAlone)
-      __syncthreads();
-    else
-      cluster_sync();
-  };
   const int* row = a.table + static_cast<size_t>(b) * a.width;
   const float* W = a.W + (static_cast<size_t>(l) * a.num_pages * a.Hkv << a.page_shift);
+  auto stays = [&](int t) { return t < a.first || t >= kv - a.recent; };
+  auto page_of = [&](int t) { return paged_lookup(row, a.width, a.page_shift, a.num_pages, t); };
+  auto weight = [&](int page, int t) {
+    return __ldcg(W + ((static_cast<size_t>(page) * a.Hkv + h) << a.page_shift) + (t & ((1 << a.page_shift) - 1)));
+  };
   auto key_of = [&](int t) {
-    const bool stays = t < a.first || t >= kv - a.recent;
-    float w = 0.f;
-    if (!stays) {
-      const int page = paged_lookup(row, a.width, a.page_shift, a.num_pages, t);
-      if (page < 0) atomicOr(p.status, kStatusBadPage);
-      w = page < 0 ? 0.f : __ldcg(W + ((static_cast<size_t>(page) * a.Hkv + h) << a.page_shift) + (t & ((1 << a.page_shift) - 1)));
-    }
-    return order_key(w, stays);
+    const int page = stays(t) ? -2 : page_of(t);
+    if (page == -1) atomicOr(p.status, kStatusBadPage);
+    return order_key(page < 0 ? 0.f : weight(page, t), stays(t));
   };
   // this block's positions [lo, lo + n)
   const int per = ((kv + blocks - 1) / blocks + 31) / 32 * 32;
-  const int lo = min(kv, rank * per), n = min(kv, lo + per) - lo;
-#pragma unroll 8
-  for (int i = tid; i < min(n, room); i += kThreads) s_key[i] = key_of(lo + i);
-  auto key = [&](int i) { return i < room ? s_key[i] : key_of(lo + i); };
+  const int lo = min(kv, rank * per), n = min(kv, lo + per) - lo, held = min(n, room);
+  // (a batch of pages is looked up before their weights are: one after the other took 5 to 12 us of 8192 keys)
+  constexpr int kBatch = kAlone ? 2 : 8;
+  for (int i = tid; i < held; i += kBatch * kThreads) {
+    int page[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int at = i + j * kThreads;
+      page[j] = at < held && !stays(lo + at) ? page_of(lo + at) : -2;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) w[j] = page[j] >= 0 ? weight(page[j], lo + i + j * kThreads) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int at = i + j * kThreads;
+      if (page[j] == -1) atomicOr(p.status, kStatusBadPage);
+      if (at < held) s_key[at] = order_key(w[j], stays(lo + at));
+    }
+  }
+  auto key = [&](int i) { return i < held ? s_key[i] : key_of(lo + i); };
   uint32_t prefix = 0;
   int left = m;               // to be taken among the keys that share the prefix
   int above = 0;              // keys above the bins that are looked at
@@ -119,19 +133,31 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
   for (int pass = 0; pass < S::passes; ++pass) {
     const int shift = kAlone ? 24 - 8 * pass : pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int top = kAlone ? 32 - 8 * pass : pass == 0 ? 32 : pass == 1 ? 21 : 10;
-    for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
-    __syncthreads();
+    int* hist = s_hist[kAlone ? 0 : pass];
+    if (kAlone || pass == 0) {
+      for (int i = tid; i < kHists * kBins; i += kThreads) s_hist[0][i] = 0;
+      __syncthreads();
+    }
     for (int i = tid; i < n; i += kThreads) {
       const uint32_t k = key(i);
-      if (pass == 0 || (k >> top) == (prefix >> top)) atomicAdd(&s_hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1);
+      if (pass == 0 || (k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1);
     }
-    all_sync();
+    __syncthreads();
+    if constexpr (!kAlone) {
+      for (int g = warp; g < kBins / 32; g += kWarps) {
+        const int sum = __reduce_add_sync(0xffffffffu, hist[g * 32 + lane]);
+        if (lane == 0) s_group[pass][g] = sum;
+      }
+      cluster_sync();
+    }
     above = 0;
     if constexpr (kAlone) {
       if (warp == 0) {
         int c[8], sum = 0;      // this lane's bins
+        *reinterpret_cast<int4*>(&c[0]) = *reinterpret_cast<const int4*>(&hist[lane * 8]);
+        *reinterpret_cast<int4*>(&c[4]) = *reinterpret_cast<const int4*>(&hist[lane * 8 + 4]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[lane * 8 + i];
+        for (int i = 0; i < 8; ++i) sum += c[i];
         const int at = find(sum);
         if (lane == at) {
           int bin = 7;
@@ -146,28 +172,22 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
         }
       }
     } else {
-      // this block's share of the bins, over the cluster, and the sums of 32 of them
-      const int share = kBins / blocks;
-      if (tid < share) {
-        int sum = 0;
-        for (int c = 0; c < blocks; ++c) sum += ld_cluster(&s_hist[rank * share + tid], static_cast<uint32_t>(c));
-        s_sum[tid] = sum;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) s_group[warp] = sum;
-      }
-      all_sync();
       if (warp == 0) {
-        // 64 groups in the order of their bins, two a lane
-        const int groups = share / 32, g = lane * 2;
-        const int c0 = ld_cluster(&s_group[g % groups], static_cast<uint32_t>(g / groups));
-        const int c1 = ld_cluster(&s_group[(g + 1) % groups], static_cast<uint32_t>((g + 1) / groups));
+        // the sum over the cluster, all reads under way at once; 64 groups in the order of their bins, two a lane
+        auto over_all = [&](const int* local) {
+          int sum = 0;
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c)
+            if (c < blocks) sum += ld_cluster(local, static_cast<uint32_t>(c));
+          return sum;
+        };
+        const int c0 = over_all(&s_group[pass][lane * 2]), c1 = over_all(&s_group[pass][lane * 2 + 1]);
         const int two = find(c0 + c1);
         const int upper_count = __shfl_sync(0xffffffffu, c1, two);
         const bool upper = above + upper_count >= left;
         if (!upper) above += upper_count;
         const int group = two * 2 + (upper ? 1 : 0);
-        const int bin = find(ld_cluster(&s_sum[group % groups * 32 + lane], static_cast<uint32_t>(group / groups)));
+        const int bin = find(over_all(&hist[group * 32 + lane]));
         if (lane == 0) {
           s_prefix = prefix | static_cast<uint32_t>(group * 32 + bin) << shift;
           s_left = left - above;
@@ -182,6 +202,7 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
   // block's positions: how many of both there are in it, and with what stands before it, where they go.
   const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(n, warp * run), i1 = min(n, i0 + run);
   int count = 0, tied = 0;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
     const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
     count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k > prefix));
@@ -206,7 +227,7 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
         s_count[1] = y;
       }
     }
-    all_sync();
+    cluster_sync();
     if (lane < rank) {
       out += ld_cluster(&s_count[0], static_cast<uint32_t>(lane));
       ties += ld_cluster(&s_count[1], static_cast<uint32_t>(lane));
