@@ -23,7 +23,7 @@ SOURCES = ["cxa_api.cu", "populate.cu", "decode.cu", "decode_noalloc.cu", "block
            "paged_api.cu", "norm_rope.cu", "paged_rows.cu", "paged_tile.cu",
            "latent_api.cu", "latent_append.cu", "latent_rows.cu", "latent_tile.cu", "latent_merge.cu", "expand_rows.cu",
            "expand_tile.cu",
-           "weights.cu", "weights_rows.cu", "weights_tile.cu", "evict.cu"]
+           "weights.cu", "weights_few.cu", "weights_rows.cu", "weights_tile.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -17,7 +17,7 @@
 //   weights_few_kernel   the transposed product again, of 128 keys by 16 rows; a thread has a key, keeps
 //                        references and sums of its own until the item's end, and stores the scores (4 bytes a row
 //                        and key, against 2 dh bytes of the key itself).
-//   weights_add_kernel   reads the scores back, mostly from L2, and adds the weights to W.
+//   weights_add_kernel   (weights_few.cu) reads the scores back and adds the weights to W.
 // Where the scores might take more than kMaxScoreBytes the second pass is weights_sum_kernel, which reads K once
 // more.
 //
@@ -31,12 +31,12 @@
 #include "ptx.cuh"
 #include "span_work.cuh"
 #include "tc_util.cuh"
-#include "weights.cuh"
+#include "weights_few.cuh"
 
 namespace cxa {
 namespace {
 
-constexpr int kKeys = 128, kChunkShift = 7;
+constexpr int kKeys = kFewKeys, kChunkShift = kFewChunkShift;
 constexpr int kUnitBytes = 16384;               // 64 channels of 128 keys or query rows
 constexpr int kSmemBytes = 232448, kSmallBytes = 6144;
 constexpr int kTileRows = 128;
@@ -66,9 +66,6 @@ __device__ __forceinline__ uint32_t same_in_all(uint32_t x) { return __shfl_sync
 __device__ __forceinline__ float* refs_of(const WeightsParams& p, const PagedSeq& s, int h) {
   return p.ref + (static_cast<size_t>(h) * p.batch.n_tokens + s.q0) * p.shape.G;
 }
-// log2 of a sum with reference M; +inf for a row that sees no key.
-__device__ __forceinline__ float log_sum(float M, float L) { return L > 0.f || L != L ? M + log2f(L) : INFINITY; }
-__device__ __forceinline__ float safe_ex2(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
 
 // A warp's copies of 128 keys of head h, 64 channels a unit, into units of a ring: a lane a box.
 template <int kUnits>
@@ -125,7 +122,7 @@ struct KeyCopies {
 // ============================================================================ few rows
 namespace few {
 
-constexpr int kRows = 16;
+constexpr int kRows = kScoreRows;
 constexpr int kThreads = 6 * 32, kMmaWarp = 4, kTmaWarp = 5;
 constexpr int kBufs = 4;               // of S^T
 constexpr int kRing = 12;
@@ -135,8 +132,8 @@ struct Small {
   WorkScratch work;
   uint32_t bad[32];           // (copies run up to 16 steps ahead of who reads it)
   volatile int abort;
-  int tmem, last;
-  float m[4][kRows], l[4][kRows];
+  int tmem;
+  FewShared few;
 };
 static_assert(sizeof(Small) <= kSmallBytes, "the small arrays fit");
 constexpr uint32_t kTmemCols = 64;
@@ -264,76 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
-        const bool gone = (bad >> (tid >> 4) & 1u) != 0;
+        const bool gone = (bad >> (tid >> 4) & 1u) != 0 || key >= shape.cap;
         const bool edge = (c + 1) * kKeys > see_all;
         float* to = p.scores != nullptr ? p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kKeys + tid : nullptr;
-        // rows before it do not see the key
-        const int hidden = edge ? min(max(key - (seq.kv - seq.n), 0), kRows) * G : 0;
+        const int hidden = gone ? kRows : edge ? min(max(key - (seq.kv - seq.n), 0), kRows) * G : 0;
+        float s[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          if (r >= rows) break;
-          const bool on = !gone && (!edge || (r >= hidden && key < shape.cap));
-          const float s = on ? __uint_as_float(x[r]) * p.qscale : -INFINITY;
-          if (to != nullptr) __stcg(to + r * kKeys, s);
-          const float up = fmaxf(m[r], s);
-          l[r] = l[r] * safe_ex2(m[r], up) + (s == -INFINITY ? 0.f : ex2(s - up));
-          m[r] = up;
-        }
+        for (int r = 0; r < kRows; ++r) s[r] = __uint_as_float(x[r]);
+        few_take(s, rows, hidden, p.qscale, to, m, l);
       }
-      // ---- the item's keys together
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (r >= rows) break;
-        float M = m[r];
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float L = l[r] * safe_ex2(m[r], M);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-        if (lane == 0) {
-          sm->m[warp][r] = M;
-          sm->l[warp][r] = L;
-        }
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      const bool whole = c0 == 0 && c1 == cur.nc;
-      float M = -INFINITY, L = 0.f;
-      if (tid < rows) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) M = fmaxf(M, sm->m[q][tid]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) L += sm->l[q][tid] * safe_ex2(sm->m[q][tid], M);
-        if (!whole) {
-          float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * (kRows * 2);
-          slot[tid] = M;
-          slot[kRows + tid] = L;
-        }
-      }
-      bool write = whole && w.ok;
-      if (!whole) {
-        const int owner = cur.first / range.per, parts = (cur.first + cur.nc - 1) / range.per - owner + 1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (tid == 0) {
-          bool last = false;
-          if (w.ok) {
-            last = atomic_add_acq_rel_gpu(p.counters + owner, 1u) == static_cast<unsigned int>(parts - 1);
-            if (last) p.counters[owner] = 0u;
-          }
-          sm->last = last;
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        write = sm->last != 0;
-        if (write && tid < rows) {
-          auto part = [&](int k) { return p.part + (2 * static_cast<size_t>(owner + k) + (k == 0 ? 1 : 0)) * (kRows * 2) + tid; };
-          M = -INFINITY;
-          L = 0.f;
-#pragma unroll 8
-          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k)));
-#pragma unroll 8
-          for (int k = 0; k < parts; ++k) L += __ldcg(part(k) + kRows) * safe_ex2(__ldcg(part(k)), M);
-        }
-      }
-      if (write && tid < rows) refs_of(p, seq, cur.h)[tid] = log_sum(M, L);
+      few_finish(&sm->few, m, l, rows, cur, range, c0, c1, w.ok, p.part, p.counters, refs_of(p, seq, cur.h));
       if (end >= range.g1) break;
       work_next(bt, shape, p.Hkv, &cur);
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -343,46 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-}
-
-constexpr int kAddThreads = 512, kAddChunks = kAddThreads / kKeys;      // chunks at once
-__global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const __grid_constant__ WeightsParams p) {
-  __shared__ WorkScratch s_work;
-  __shared__ float s_ref[kRows];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x;
-  const PagedBatch& bt = p.batch;
-  WorkRange range;
-  WorkCursor cur;
-  WorkShape shape = p.shape;
-  if (!work_locate<kAddThreads, false>(bt, shape, p.Hkv, &s_work, &range, &cur)) return;
-  for (;;) {
-    const int end = min(range.g1, cur.first + cur.nc), c0 = cur.c, c1 = end - cur.first;
-    const PagedSeq seq = cur.seq;
-    const int rows = work_rows(seq, shape), keys = min(seq.kv, shape.cap);
-    __syncthreads();
-    if (tid < rows) s_ref[tid] = __ldcg(refs_of(p, seq, cur.h) + tid);
-    __syncthreads();
-#pragma unroll 2
-    for (int c = c0 + tid / kKeys; c < c1; c += kAddChunks) {
-      const int key = c * kKeys + tid % kKeys;
-      const int page = key < keys ? lookup(p, cur.b, key) : -1;
-      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kKeys + tid % kKeys;
-      float add = 0.f;
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const float s = __ldcg(from + r * kKeys);
-        add += s == -INFINITY ? 0.f : ex2(s - s_ref[r]);      // (a hidden key's may not become NaN)
-      }
-      if (page >= 0) {
-        float* W = p.W + ((static_cast<size_t>(page) * p.Hkv + cur.h) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-        *W = (key >= seq.kv - seq.n || p.decay == 0.f ? 0.f : p.decay * *W) + add;
-      }
-    }
-    if (end >= range.g1) return;
-    work_next(bt, shape, p.Hkv, &cur);
-  }
 }
 
 }  // namespace few
@@ -583,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx[(e / 2) & 3] = max_of_3(mx[(e / 2) & 3], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
           const float up = fmaxf(m, top);
-          l *= safe_ex2(m, up);
+          l *= few_rescale(m, up);
           m = up;
           const float ref = m == -INFINITY ? 0.f : -m;
           const float2 ref2 = make_float2(ref, ref);
@@ -632,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
           for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k)));
 #pragma unroll 4
-          for (int k = 0; k < parts; ++k) L += __ldcg(part(k) + kTiles * kTileRows) * safe_ex2(__ldcg(part(k)), M);
+          for (int k = 0; k < parts; ++k) L += __ldcg(part(k) + kTiles * kTileRows) * few_rescale(__ldcg(part(k)), M);
           refs[row0 + r] = log_sum(M, L);
         }
       }
@@ -921,7 +818,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace sum
 
-constexpr size_t kMaxScoreBytes = 256u << 20;
 constexpr double kSplitChunks = 8192;
 
 template <int kDh>
@@ -1006,10 +902,8 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
     if (!launched(cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh>, q, k, sums))) return e;
   }
   if (p.scores != nullptr) {
-    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms * 4));
-    cfg.blockDim = dim3(few::kAddThreads);
-    cfg.dynamicSmemBytes = 0;
-    launched(cudaLaunchKernelEx(&cfg, few::weights_add_kernel, few));
+    WeightsAdd add = {p.batch, few.shape, p.num_pages, p.Hkv, p.page_shift, p.scores, p.ref, p.max_rows, p.W, p.decay};
+    e = launch_weights_add(add, dev, stream);
   }
   return e;
 }
@@ -1022,16 +916,12 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
 // chunks of a prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 240 so; 5 tokens in each
 // of 16 sequences of up to 1500 keys of 8 heads: 39 us and 45.)
 WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new) {
-  const double chunks = static_cast<double>(B) * Hkv * (((static_cast<long long>(width) << page_shift) >> kChunkShift) + 1);
-  auto bytes = [&](int rows) {
-    const double n = chunks * rows * kKeys * 4;
-    return n <= static_cast<double>(kMaxScoreBytes) ? static_cast<size_t>(n) : 0;
-  };
+  const double chunks = weights_chunks(B, width, page_shift, Hkv);
   WeightsSplit s;
   s.many = static_cast<long long>(G) * max_new > few::kRows;
   const int tokens = few::kRows / G < 2 ? few::kRows / G : 2;
   s.few_rows = !s.many ? G * max_new : B == 1 || chunks < kSplitChunks ? 0 : tokens * G;
-  s.score_bytes = bytes(s.few_rows);
+  s.score_bytes = weights_score_bytes(B, width, page_shift, Hkv, s.few_rows);
   if (s.many && s.score_bytes == 0) s.few_rows = 0;
   return s;
 }

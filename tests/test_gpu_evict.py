@@ -503,10 +503,11 @@ def test_single_tokens_beside_prompts_over_long_contexts(Hq, Hkv):
     assert torch.equal(b.accumulate(), first)
 
 
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [[1, 1, 0, 2], [3, 40, 1, 2]])
-def test_scores_that_have_no_room(n):
+def test_scores_that_have_no_room(n, pool):
     """Rows of the table for more keys than scores are kept of: the keys are read twice instead."""
-    b = Batch(n, [700, 90, 30, 2], 64, 4, 2, 128, "bf16", seed=6).fill()
+    b = Batch(n, [700, 90, 30, 2], 64, 4, 2, 128, pool, seed=6).fill()
     b.d["page_table"] = torch.cat([b.table, torch.full((4, 1 << 20), -1, dtype=torch.int32)], 1).cuda()
     before = b.W.clone()
     b.close(before, b.accumulate(decay=0.5), decay=0.5)
