@@ -4,8 +4,10 @@
 //   ref_r = log2 sum_j 2^s_rj,   W_j = decay W_j + sum_r 2^(s_rj - ref_r),   s = scale log2(e) q K^T
 //
 // weights_few_rows_kernel is bound by reading K: chunks of 128 keys come by cp.async two ahead, a thread takes
-// one key's row from shared memory and the rows' queries as broadcasts, four rows at a time, and stores
-// the scores (4 bytes a row and key, against 4 dh bytes of the key itself).
+// one key's row from shared memory and the rows' queries as broadcasts, up to four rows at a time (always four:
+// 31 us and 142 of the two calls below), and stores the scores (4 bytes a row and key, against 4 dh bytes
+// of the key itself). 16 single tokens over up to 4000 keys of 8 heads of 64: 29 us; 32 over up to 8000 keys of 8 heads
+// of 128: 123 us, 4.4 TB/s.
 // weights_add_kernel reads them back, mostly from L2, and adds the weights to W.
 #include "ptx.cuh"
 #include "weights_few.cuh"
@@ -40,6 +42,26 @@ struct Shape {
   static constexpr int smem = (kStages * kFewKeys * row + kScoreRows * kDh) * 4;
   static constexpr int per_sm = kDh == 64 ? 2 : 1;
 };
+
+// A key's products with kN rows of queries.
+template <int kDh, int kN>
+__device__ __forceinline__ void products(const float* key, const float* q, float* x) {
+  float s[kN][2];
+#pragma unroll
+  for (int r = 0; r < kN; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < kDh; i += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(key + i);
+#pragma unroll
+    for (int r = 0; r < kN; ++r) {
+      const float4 v = *reinterpret_cast<const float4*>(q + r * kDh + i);
+      s[r][0] = fmaf(v.y, k.y, fmaf(v.x, k.x, s[r][0]));
+      s[r][1] = fmaf(v.w, k.w, fmaf(v.z, k.z, s[r][1]));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kN; ++r) x[r] = s[r][0] + s[r][1];
+}
 
 template <int kDh>
 __global__ void __launch_bounds__(kThreads, Shape<kDh>::per_sm)
@@ -133,18 +155,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kDh>::per_sm)
 #pragma unroll
       for (int r0 = 0; r0 < kScoreRows; r0 += 4) {
         if (r0 >= rows) break;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int i = 0; i < kDh; i += 4) {
-          const float4 k = *reinterpret_cast<const float4*>(row + i);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float4 q = *reinterpret_cast<const float4*>(s_q + (r0 + r) * kDh + i);
-            s[r] = fmaf(q.w, k.w, fmaf(q.z, k.z, fmaf(q.y, k.y, fmaf(q.x, k.x, s[r]))));
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r0 + r] = s[r];
+        const float* q = s_q + r0 * kDh;
+        if (rows - r0 == 1)
+          products<kDh, 1>(row, q, x + r0);
+        else if (rows - r0 == 2)
+          products<kDh, 2>(row, q, x + r0);
+        else
+          products<kDh, 4>(row, q, x + r0);
       }
       const int key = c * kFewKeys + tid;
       const bool gone = (s_bad[stage] >> (tid >> 4) & 1u) != 0 || key >= shape.cap;
