@@ -24,7 +24,10 @@
 //    registers. They give tensor memory back by an arrival without a release: one with it waits until the
 //    rows written before are performed (98 us against 76 where 128 latent channels make the products short).
 //
-// Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long.
+// Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long. 32768
+// positions, 20 heads of 128, 512 + 64 channels: 109 us, 1180 TFLOP/s and 3.5 TB/s (main loop alone 67 at
+// cuBLAS's rate; without the stores 85). 24 sequences of up to 1500 positions, 8 heads of 64, 256 + 32: 24 us, of
+// which the floor of bytes is 9.5: start, and two or three products a pair.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
