@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) la
   WorkCursor cur;
   WorkShape shape = p.shape;
   LatentCut cut = {0, 0, 0, 0};
-  if (!work_locate<kThreads, false>(bt, shape, 1, &s_work, &range, &cur, p.status)) {
+  if (!work_locate<kThreads, false, true>(bt, shape, 1, &s_work, &range, &cur, p.status)) {
     if (tid == 0) p.cut[blockIdx.x] = cut;
     return;
   }

@@ -20,9 +20,9 @@
 //
 // Work is dealt out in steps of 64 keys (paged_work.cuh); items that a block boundary cuts are merged
 // by latent_merge.cu. Bound by memory: a row of 1152 bytes is read once for the tile's rows. Measured, both
-// kernels: 64 single tokens over 287,000 keys of 20 heads, 512 + 64 channels, 75 us (4.3 TB/s: the merge is 5 to 8 of
+// kernels: 64 single tokens over 287,000 keys of 20 heads, 512 + 64 channels, 73 us (4.4 TB/s: the merge is 5 to 8 of
 // them, the start 3, and an item's beginning and end are not covered by copies of the next); one token of 64 heads
-// over 262,144 keys 73 us (4.2 TB/s: 64 rows leave a ring of 9 units, less than two steps, so that copies wait for
+// over 262,144 keys 72 us (4.2 TB/s: 64 rows leave a ring of 9 units, less than two steps, so that copies wait for
 // P.V); one token over 448 keys of 256 channels, 8 heads, 12 us, latency.
 //
 // P is rounded to one bf16 value (an error of up to 2^-8 of each weight, of either sign, as the bf16 output
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   WorkCursor cur;
   WorkShape shape = p.shape;
   LatentCut cut = {0, 0, 0, 0};
-  const bool active = work_locate<kThreads, false>(bt, shape, 1, &sm->work, &range, &cur, p.status);
+  const bool active = work_locate<kThreads, false, true>(bt, shape, 1, &sm->work, &range, &cur, p.status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -605,39 +605,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_warp(kPvDone, (step - 1) & 1);
       tc_fence_after();
       {
-        // (tensor memory a batch of 16 columns ahead)
-        uint32_t o[2][16];
+        // 16 rows of 128 channels at a time, the next ones on their way out of tensor memory. (The loop is not
+        // unrolled: fetching that much code took as long as running it.)
+        constexpr int B = kR / 16;
+        uint32_t o[16];
         const uint32_t from = my_tmem + Tm<kR>::o;
-        constexpr int B = kR / 16;      // batches of a tile
-        tmem_ld_32x32b_x16(from, o[0]);
+        tmem_ld_32x32b_x16(from, o);
 #pragma unroll 1
-        for (int u = 0; u < quads; ++u) {
-          const int ch = u * 128 + warp * 32 + lane;
+        for (int k = 0; k < quads * B; ++k) {
+          const int c = k % B * 16, ch = k / B * 128 + warp * 32 + lane;
+          tmem_ld_wait();
+          float v[16];
 #pragma unroll
-          for (int c = 0; c < B; ++c) {
-            const int now = B % 2 == 0 ? c & 1 : 0;
-            tmem_ld_wait();
-            if constexpr (B % 2 == 0) {
-              if (c + 1 < B || u + 1 < quads) tmem_ld_32x32b_x16(from + u * kR + (c + 1) * 16, o[now ^ 1]);
-            }
-            if (ok) {
-              if (whole) {
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * (whole ? sm->inv[c + e] : 1.f);
+          if (k + 1 < quads * B) tmem_ld_32x32b_x16(from + (k + 1) * 16, o);
+          if (ok) {
+            if (whole) {
+              // (the rows' places before the first store: one after the other took 150 clocks a row)
+              long long at[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (c * 16 + e < rows)
-                    p.out[sm->row[c * 16 + e] + ch] = __float2bfloat16_rn(__uint_as_float(o[now][e]) * sm->inv[c * 16 + e]);
-              } else {
-                float* to = slot + static_cast<size_t>(c * 16) * p.latent + ch;
+              for (int e = 0; e < 16; ++e) at[e] = sm->row[c + e] + ch;
 #pragma unroll
-                for (int e = 0; e < 16; ++e, to += p.latent)
-                  if (c * 16 + e < rows) *to = __uint_as_float(o[now][e]);
-              }
-            }
-            __syncwarp();
-            if constexpr (B % 2 != 0) {
-              if (u + 1 < quads) tmem_ld_32x32b_x16(from + (u + 1) * kR, o[0]);
+              for (int e = 0; e < 16; ++e)
+                if (c + e < rows) p.out[at[e]] = __float2bfloat16_rn(v[e]);
+            } else {
+              float* to = slot + static_cast<size_t>(c) * p.latent + ch;
+#pragma unroll
+              for (int e = 0; e < 16; ++e, to += p.latent)
+                if (c + e < rows) *to = v[e];
             }
           }
+          __syncwarp();
         }
         tmem_ld_wait();
       }
