@@ -455,45 +455,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t wild = 0;                                 // of this thread's two keys
         if (__builtin_expect(special || bad != 0, 0)) {
           const int k0 = warp * 16 + g;
-          const bool gone = (bad >> warp & 1u) != 0;
+          const bool gone = (bad >> warp & 1u) != 0, one = (row0 + rows - 1) / H == row0 / H;      // (one token)
           const int lo = max(0, see_all - key0), hi = min(kKeys, t.keys - key0);
-          // this thread's part of the rows in shared memory: half of the channels of one key
-          const int key = tid >> 1, half = tid & 1;
+          // this warp's 16 keys' rows in shared memory: 8 lanes a row of 64 channels, four rows at a time
+          const int sub = lane >> 3;
           auto each_piece = [&](auto body) {
             int at = step * per % NU, round = step * per / NU;
             for (int u = 0; u < quads; ++u) {
               wait_warp(kUFull + at, round & 1);      // (it has come: the products have read it)
-              const uint32_t to = u_base + at * kUnitBytes + half * kHalf + key * 128;
+              const uint32_t to = u_base + at * kUnitBytes + (warp * 16 + sub) * 128 + (lane & 7) * 16;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) body(to + 16 * q);
+              for (int q = 0; q < 8; ++q) body(q & 3, to + (q >> 2) * kHalf + (q & 3) * 512);
               if (++at == NU) {
                 at = 0;
                 ++round;
               }
             }
           };
-          uint32_t all = 0;
-          if (lo < hi) {
-            bool w = false;
-            const bool look = key >= lo && key < hi && (bad >> (key >> 4) & 1u) == 0;
-            each_piece([&](uint32_t at) {
-              if (!look) return;
+          uint32_t all = 0;        // keys with values that are not finite
+          if (lo < hi && !gone) {
+            uint32_t w = 0;        // of key 4 i + sub: bit i
+            each_piece([&](int i, uint32_t at) {
+              const int key = warp * 16 + 4 * i + sub;
+              if (key < lo || key >= hi) return;
               const uint4 u = ld_shared_v4(at);
               const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
+              for (int e = 0; e < 4; ++e)
+                if ((v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u) w |= 1u << i;
             });
-            const uint32_t two = __ballot_sync(0xffffffffu, w);      // two bits a key
-            uint32_t keys = 0;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) keys |= (two >> (2 * k) & 3u) != 0 ? 1u << k : 0u;
-            all = keys;
-            wild = keys >> g & 0x101u;
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t eight = __ballot_sync(0xffffffffu, (w >> i & 1u) != 0);      // bits a key
+#pragma unroll
+              for (int k = 0; k < 4; ++k) all |= (eight >> (8 * k) & 255u) != 0 ? 1u << (4 * i + k) : 0u;
+            }
+            wild = all >> g & 0x101u;
           }
 #pragma unroll
           for (int i = 0; i < CN; ++i) {
             const int col = col_of(i);
-            const int see = col < rows ? visible_keys(cur.seq, (row0 + col) / H, shape.cap) : 0;
+            const int see = col >= rows ? 0 : one ? see_all : visible_keys(cur.seq, (row0 + col) / H, shape.cap);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int k = key0 + k0 + 8 * e;
@@ -505,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const bool clear = key >= hi || (all >> (key & 15) & 1u) != 0 || (bad >> (key >> 4) & 1u) != 0;
-          each_piece([&](uint32_t at) {
-            if (clear) st_shared_v4(at, 0u, 0u, 0u, 0u);
+          each_piece([&](int i, uint32_t at) {
+            const int key = 4 * i + sub;
+            if (gone || warp * 16 + key >= hi || (all >> key & 1u) != 0) st_shared_v4(at, 0u, 0u, 0u, 0u);
           });
         }
         // ---- references
