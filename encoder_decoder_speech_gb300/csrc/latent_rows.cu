@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) la
   __shared__ __align__(16) float s_s[kRows][kKeys + 1];  // scores
   __shared__ __align__(16) float s_p[kKeys][kRows];      // weights
   __shared__ float s_corr[kRows], s_m[kRows], s_l[kRows];
+  __shared__ long long s_row[kRows];      // where the rows' results begin
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,6 +132,10 @@ __global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) la
       for (int c = lane; c < width / 4; c += 32)
         *reinterpret_cast<float4*>(s_q + i * S::row + c * 4) =
             i < rows ? *reinterpret_cast<const float4*>(src + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (tid < kRows) {
+      const int at = row0 + tid;
+      s_row[tid] = (seq.q0 + at / H) * p.o_stride + static_cast<long long>(at % H) * S::dc;
     }
     // softmax: warp w has rows 2w and 2w + 1, a key a lane
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -278,18 +283,19 @@ __global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) la
     const bool whole = c0 == 0 && c1 == cur.nc;
     float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * latent_slot(kRows, S::dc);
     if (pv) {
+      // (places and factors before the first store: one row after the other took 430 clocks each)
+      float* to[S::rows];
+      float by[S::rows];
 #pragma unroll
       for (int i = 0; i < S::rows; ++i) {
-        const int r = rg * S::rows + i, at = row0 + r;
-        if (r >= rows) continue;
-        if (whole) {
-          const float sum = s_l[r], inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-          *reinterpret_cast<float2*>(p.out + (seq.q0 + at / H) * p.o_stride + static_cast<long long>(at % H) * S::dc + ch) =
-              make_float2(o[i][0] * inv, o[i][1] * inv);
-        } else {
-          *reinterpret_cast<float2*>(slot + static_cast<size_t>(r) * S::dc + ch) = make_float2(o[i][0], o[i][1]);
-        }
+        const int r = rg * S::rows + i;
+        const float sum = s_l[r];
+        by[i] = !whole ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        to[i] = (whole ? p.out + s_row[r] : slot + static_cast<size_t>(r) * S::dc) + ch;
       }
+#pragma unroll
+      for (int i = 0; i < S::rows; ++i)
+        if (rg * S::rows + i < rows) *reinterpret_cast<float2*>(to[i]) = make_float2(o[i][0] * by[i], o[i][1] * by[i]);
     }
     if (!whole && tid < rows) {
       slot[kRows * S::dc + tid] = s_m[tid];
