@@ -8,7 +8,7 @@
 // 136 clocks of an SM, against 98 for reading the key's 2304 bytes. 5 tokens in each of 16 sequences of up to 1500
 // keys, 8 heads, 128 + 32 channels: 32 us with the merge, of which the products alone take 4: a block has five steps,
 // each a chain of three barriers, behind the start and before the merge. 16 tokens of 20 heads over up to 4000 keys of
-// 512 + 64: 97 us, 18 TFLOP/s.
+// 512 + 64: 99 us, 18 TFLOP/s.
 //
 // A step is 32 keys, copied into shared memory a step ahead (cp.async). Scores: a warp has four keys
 // in registers, a 32nd of the channels in each lane, and takes a row of q after the other from shared
@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(kThreads, latent_rows_blocks(kQuads * 128)) la
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int pages = look(s0), next = look(s0 + 1);
-    fetch(s0, pages);
+    // the queries, with the first keys (by loads and stores, one after the other, an item began 3 us later)
     for (int i = warp; i < kRows; i += kWarps) {
       const int at = row0 + i;
-      const float* src = p.q + (seq.q0 + at / H) * p.q_stride + static_cast<long long>(at % H) * width;
+      const float* src = i < rows ? p.q + (seq.q0 + at / H) * p.q_stride + static_cast<long long>(at % H) * width : p.q;
       for (int c = lane; c < width / 4; c += 32)
-        *reinterpret_cast<float4*>(s_q + i * S::row + c * 4) =
-            i < rows ? *reinterpret_cast<const float4*>(src + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        cp_async16(smem_u32(s_q + i * S::row + c * 4), src + (i < rows ? c * 4 : 0), i < rows);
     }
+    fetch(s0, pages);
     if (tid < kRows) {
       const int at = row0 + tid;
       s_row[tid] = (seq.q0 + at / H) * p.o_stride + static_cast<long long>(at % H) * S::dc;
