@@ -747,6 +747,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (next_unit(&un)) {
       const float* refs = refs_of(p, un.seq, un.h);
       const int all = un.seq.n * G, key = un.key0 + k, past = un.seq.kv - un.seq.n;
+      // the key's place and old weight, on their way under the products
+      float* W = nullptr;
+      float old = 0.f;
+      if (grp == 0 && key < un.keys) {
+        const int page = lookup(p, un.b, key);
+        if (page >= 0) {
+          W = p.W + ((static_cast<size_t>(page) * p.Hkv + un.h) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+          if (key < past && p.decay != 0.f) old = *W;
+        }
+      }
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       int t = un.t0 + ((j + grp) & 1);
       auto fetch = [&](int tile) {
@@ -803,13 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float add = acc[0].x + acc[0].y;
       if (grp == 1) sm->sums[unit & 1][k] = add;
       asm volatile("bar.sync 3, 256;" ::: "memory");
-      if (grp == 0 && key < un.keys && w.ok) {
-        const int page = lookup(p, un.b, key);
-        if (page >= 0) {
-          float* W = p.W + ((static_cast<size_t>(page) * p.Hkv + un.h) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-          *W = (key >= past || p.decay == 0.f ? 0.f : p.decay * *W) + (add + sm->sums[unit & 1][k]);
-        }
-      }
+      if (W != nullptr && w.ok) *W = p.decay * old + (add + sm->sums[unit & 1][k]);
       ++unit;
     }
   }
