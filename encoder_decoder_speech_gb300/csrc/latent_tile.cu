@@ -20,7 +20,7 @@
 //
 // Work is dealt out in steps of 64 keys (paged_work.cuh); items that a block boundary cuts are merged
 // by latent_merge.cu. Bound by memory: a row of 1152 bytes is read once for the tile's rows. Measured, both
-// kernels: 64 single tokens over 287,000 keys of 20 heads, 512 + 64 channels, 73 us (4.4 TB/s: the merge is 5 to 8 of
+// kernels: 64 single tokens over 287,000 keys of 20 heads, 512 + 64 channels, 72 us (4.5 TB/s: the merge is 5 to 8 of
 // them, the start 3, and an item's beginning and end are not covered by copies of the next); one token of 64 heads
 // over 262,144 keys 72 us (4.2 TB/s: 64 rows leave a ring of 9 units, less than two steps, so that copies wait for
 // P.V); one token over 448 keys of 256 channels, 8 heads, 12 us, latency.

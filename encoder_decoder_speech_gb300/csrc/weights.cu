@@ -7,7 +7,7 @@ namespace {
 // A tile of 128 rows holds whole tokens, so G query heads have to fit into it.
 bool on_tiles(int G, bool bf16) { return bf16 && G <= 128; }
 // The room for scores that an fp32 call of few rows takes; 0: it goes the way of many. (16 single tokens over up to
-// 4000 keys of 8 heads of 64: 194 us that way, 29 this.)
+// 4000 keys of 8 heads of 64: 194 us that way, 27 this.)
 size_t few_scores(int B, int width, int page_shift, int Hkv, int G, int max_new, bool bf16) {
   return bf16 || static_cast<long long>(G) * max_new > 16 ? 0 : weights_score_bytes(B, width, page_shift, Hkv, G * max_new);
 }

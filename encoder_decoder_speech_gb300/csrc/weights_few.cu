@@ -5,9 +5,9 @@
 //
 // weights_few_rows_kernel is bound by reading K: chunks of 128 keys come by cp.async two ahead, a thread takes
 // one key's row from shared memory and the rows' queries as broadcasts, up to four rows at a time (always four:
-// 31 us and 142 of the two calls below), and stores the scores (4 bytes a row and key, against 4 dh bytes
-// of the key itself). 16 single tokens over up to 4000 keys of 8 heads of 64: 29 us; 32 over up to 8000 keys of 8 heads
-// of 128: 123 us, 4.4 TB/s.
+// 2 us and 19 more of the two calls below), and stores the scores (4 bytes a row and key, against 4 dh bytes
+// of the key itself). 16 single tokens over up to 4000 keys of 8 heads of 64: 27 us; 32 over up to 8000 keys of 8 heads
+// of 128: 121 us, 4.5 TB/s.
 // weights_add_kernel reads them back, mostly from L2, and adds the weights to W.
 #include "ptx.cuh"
 #include "weights_few.cuh"
@@ -176,9 +176,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDh>::per_sm)
   }
 }
 
-constexpr int kAddThreads = 512, kAddChunks = kAddThreads / kFewKeys;      // chunks at once
-constexpr int kAddBlocks = 4;                                              // an SM
-__global__ void __launch_bounds__(kAddThreads, kAddBlocks) weights_add_kernel(const __grid_constant__ WeightsAdd p) {
+constexpr int kAddBlocks = 16;      // an SM, small ones: a block of 512 threads waits longer for its last (127 us, 124 so)
+__global__ void __launch_bounds__(kThreads, kAddBlocks) weights_add_kernel(const __grid_constant__ WeightsAdd p) {
   __shared__ WorkScratch s_work;
   __shared__ float s_ref[kScoreRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kAddThreads, kAddBlocks) weights_add_kernel(co
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
-  if (!work_locate<kAddThreads, false>(bt, shape, p.Hkv, &s_work, &range, &cur)) return;
+  if (!work_locate<kThreads, false>(bt, shape, p.Hkv, &s_work, &range, &cur)) return;
   for (;;) {
     const int end = min(range.g1, cur.first + cur.nc), c0 = cur.c, c1 = end - cur.first;
     const PagedSeq seq = cur.seq;
@@ -197,11 +196,11 @@ __global__ void __launch_bounds__(kAddThreads, kAddBlocks) weights_add_kernel(co
     __syncthreads();
     if (tid < rows) s_ref[tid] = __ldcg(p.ref + (static_cast<size_t>(cur.h) * bt.n_tokens + seq.q0) * shape.G + tid);
     __syncthreads();
-#pragma unroll 2
-    for (int c = c0 + tid / kFewKeys; c < c1; c += kAddChunks) {
-      const int key = c * kFewKeys + tid % kFewKeys;
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) {
+      const int key = c * kFewKeys + tid;
       const int page = key < keys ? paged_lookup(row, bt.width, p.page_shift, p.num_pages, key) : -1;
-      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kFewKeys + tid % kFewKeys;
+      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kFewKeys + tid;
       float add = 0.f;
 #pragma unroll 4
       for (int r = 0; r < rows; ++r) add += few_rescale(__ldcg(from + r * kFewKeys), s_ref[r]);      // (0 of a hidden key)
@@ -264,7 +263,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
 cudaError_t launch_weights_add(const WeightsAdd& a, const DeviceInfo& dev, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms * kAddBlocks));
-  cfg.blockDim = dim3(kAddThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

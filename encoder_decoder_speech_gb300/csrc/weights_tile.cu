@@ -10,9 +10,10 @@
 //                        over all tiles of 128 query rows that see them. A thread adds up its own key's weights,
 //                        so that every W is written once and in one order.
 // Both are bound by the exponentials, 32 a clock of an SM: 512 clocks for 128 x 128 scores, against 256 (64
-// channels) or 512 (128) for their product. 2048 tokens over 8192 keys of 20 heads of 64: 147 us, the exponential
-// units busy 46 and 40 % of the two passes. (A second warp for the products, and 16 softmax warps in place of
-// 8, gained nothing.)
+// channels) or 512 (128) for their product. 2048 tokens over 8192 keys of 20 heads of 64: 145 us, the exponential
+// units busy 44 and 41 % of the two passes: two warps a scheduler do not cover each other's waits and reads of
+// tensor memory (registers alone: 82 %). Tried: a second warp for the products and 16 softmax warps, no gain; 64
+// columns at a time with the next ones on their way, 183 us; sums with a reference that seldom moves, 170 us.
 //
 // Few query rows (16 a K/V head at most: single tokens, in a batch of their own or beside prompts, see
 // weights_split), bound by reading K:
@@ -20,7 +21,7 @@
 //                        references and sums of its own until the item's end, and stores the scores (4 bytes a row
 //                        and key, against 2 dh bytes of the key itself).
 //   weights_add_kernel   (weights_few.cu) reads the scores back and adds the weights to W.
-// 64 single tokens, 32 heads on 8 of 128, over 287,000 keys: 127 us, 104 of them the first at 5.7 TB/s.
+// 64 single tokens, 32 heads on 8 of 128, over 287,000 keys: 124 us, 104 of them the first at 5.7 TB/s.
 // Where the scores might take more than kMaxScoreBytes the second pass is weights_sum_kernel, which reads K once
 // more.
 //
@@ -920,7 +921,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
 // Which sequences have few rows: all, where no sequence can have more than a product's 16; otherwise those of one
 // or two tokens (more would take room for scores that hardly any use), if their scores can be kept, there is more
 // than one sequence, and the keys are many enough to pay for two more launches. (20 single tokens beside 4
-// chunks of a prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 240 so; 5 tokens in each
+// chunks of a prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 237 so; 5 tokens in each
 // of 16 sequences of up to 1500 keys of 8 heads: 39 us and 45.)
 WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new) {
   const double chunks = weights_chunks(B, width, page_shift, Hkv);
