@@ -221,6 +221,14 @@ def test_attention_over_a_long_context(pool, H, n):
 
 
 @pytest.mark.parametrize("pool", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [128, 45, 7])
+def test_many_tiles_of_a_sequence(pool, H):
+    """Tiles of equal numbers of chunks are numbered together: prompts alone, behind context, and cut off by their rows."""
+    b = Batch([153, 1, 0, 70, 200], [153, 900, 5, 1500, 190], 32, H, 128, 16, pool, seed=H).fill(float("nan"))
+    b.close(b.attend())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
 def test_scores_of_growing_size(pool):
     """References that move at every step, and scores far apart."""
     b = Batch([2, 1], [700, 650], 64, 20, 256, 32, pool, seed=3)
