@@ -6,10 +6,11 @@
 // histograms added up over distributed shared memory, find the keep-th largest; one more writes the
 // positions above it, and of those equal to it the first ones. (A block an item, which read the weights anew in
 // each pass: 225 us for 32 lists of 65536; a cluster 29, of which the first reads of the weights take 5 to 10, the
-// passes 3 each.) evict_copy_kernel copies the listed rows of K, V and weights, a block 64 of them.
+// passes 3 each.) evict_copy_kernel copies the listed rows of K, V and weights, a block 32 of them
+// (rows looked up and read two or four at a time by a thread: slower, 83 and 89 us).
 // Bound by memory: weights are read once, what stays is read and written once. 4 sequences of up to 65536 keys of
-// 8 heads of 128 down to 8192, bf16: 80 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
-// of 448 keys down to 112: 19 us, latency of the two kernels.
+// 8 heads of 128 down to 8192, bf16: 79.7 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
+// of 448 keys down to 112: 18.9 us, latency of the two kernels.
 #include "cluster.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
@@ -19,7 +20,7 @@ namespace {
 
 constexpr int kMaxCluster = 8;
 constexpr int kMaxRoom = 49152;      // keys in a block's shared memory; more are read again
-constexpr int kCopyThreads = 256, kCopyRows = 64;
+constexpr int kCopyThreads = 128, kCopyRows = 32;
 
 struct EvictParams {
   EvictLaunch a;

@@ -329,8 +329,8 @@ int cxa_paged_evict(const cxa_pages* pages, int l0, int nl, float* weights, int 
     if (o0 < k0 + static_cast<uintptr_t>(B) * 4 && k0 < o0 + static_cast<uintptr_t>(B) * 4)
       return fail(CXA_EINVAL, w + ": out_len must not overlap kv_len");
     const double rows = static_cast<double>(nl) * B * pages->Hkv;
-    if (rows * (static_cast<double>(keep) / 64.0 + 8.0) >= 2147483647.0)
-      return fail(CXA_EINVAL, w + ": nl * B * Hkv * (keep / 64 + 8) must be below 2^31");
+    if (rows * (static_cast<double>(keep) / 32.0 + 8.0) >= 2147483647.0)
+      return fail(CXA_EINVAL, w + ": nl * B * Hkv * (keep / 32 + 8) must be below 2^31");
     std::string msg;
     cxa::DeviceInfo dev;
     cudaError_t e = cxa::current_device_info(&dev, &msg);

@@ -134,8 +134,9 @@ struct WorkScratch {
 // kThreads threads of the block; returns false if the block has nothing to do. With
 // kMayCoarsen, w becomes coarse where a block would have less than four steps: a merge costs
 // as much as some eight of them. With kRuns, tiles are counted in runs (each_run). With a
-// status word, sequences whose keys pass their row of the table are reported there, whichever kernel they are of, and a q_start that decreases. A
-// batch of more chunks than can be numbered, which only such a q_start brings, is left out.
+// status word, sequences whose keys pass their row of the table are reported there, whichever
+// kernel they are of, and a q_start that decreases. A batch of more chunks than can be numbered,
+// which only such a q_start brings, is left out.
 template <int kThreads, bool kMayCoarsen, bool kRuns = false>
 __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
                             WorkCursor* cur, unsigned int* status = nullptr) {

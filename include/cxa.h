@@ -515,7 +515,7 @@ CXA_API int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_to
  * positions; new tokens are rotated by cxa_qk_norm_rope at positions that the caller counts on,
  * and appended without a rotation.
  *
- *   keep       >= 1, first + recent <= keep, nl * B * Hkv * (keep / 64 + 8) below 2^31.
+ *   keep       >= 1, first + recent <= keep, nl * B * Hkv * (keep / 32 + 8) below 2^31.
  *   kv_len     device int32 [B], page_table device int32 [B][max_pages]: the sequences as they are.
  *   out_table  device int32 [B][out_max_pages]: pages that no sequence of the call reads, each
  *              once (cxa_paged_evict_check), with room for min(keep, kv_len) positions. What has no page of
