@@ -5,7 +5,8 @@
 // as one product of positions by the columns of all heads' WK and WV side by side, in tiles of 64 x 128
 // with 4 x 8 sums a thread, 16 latent channels at a time, the next ones under way meanwhile. Bound by the
 // products: 2 latent operations a value. 8 sequences of up to 1000 positions, 8 heads of 64, 512 + 48 channels: 117 us,
-// 26 TFLOP/s (one product of 64 x 64 with the loads in the way of the products: 14).
+// 26 TFLOP/s (tiles of 64 x 64 with the loads in the way of the products: 14; of 128 x 128: 26, and 16 against 27
+// where that leaves too few of them).
 #include "expand.cuh"
 #include "ptx.cuh"
 #include "span_work.cuh"
