@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <new>
 #include <string>
 #include <vector>
@@ -201,6 +202,7 @@ int cxa_latent_attention(const cxa_latent* cache, int layer, int B, int n_tokens
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = latent_layer(cache, layer);
     a.workspace = workspace;
+    const std::lock_guard<std::mutex> together(stream_lock(static_cast<cudaStream_t>(stream)));
     e = cxa::launch_latent_attention(a, dev, static_cast<cudaStream_t>(stream), &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch " + msg);
     return CXA_OK;
@@ -305,6 +307,7 @@ int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, in
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
+    const std::lock_guard<std::mutex> together(stream_lock(static_cast<cudaStream_t>(stream)));
     e = cxa::launch_weights(a, dev, static_cast<cudaStream_t>(stream), &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch " + msg);
     return CXA_OK;
@@ -357,6 +360,7 @@ int cxa_paged_evict(const cxa_pages* pages, int l0, int nl, float* weights, int 
     a.out_width = out_max_pages;
     a.kept = kept;
     a.out_len = out_len;
+    const std::lock_guard<std::mutex> together(stream_lock(static_cast<cudaStream_t>(stream)));
     e = cxa::launch_evict(a, dev, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch");
     return CXA_OK;

@@ -22,21 +22,17 @@ using namespace cxa::api;
 
 namespace {
 
-// A call's two kernels are enqueued with nothing of another thread's call on the same stream
-// between them: the second starts without waiting for anything but the first (paged_tile.cu),
-// so the scratch it uses must not be under the second kernel of another call. One lock for the
-// streams whose handles fall together.
-std::mutex& stream_lock(cudaStream_t s) {
-  static std::mutex locks[61];
-  return locks[reinterpret_cast<uintptr_t>(s) / 16 % 61];
-}
-
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 }  // namespace
 
 namespace cxa {
 namespace api {
+
+std::mutex& stream_lock(cudaStream_t s) {
+  static std::mutex locks[61];
+  return locks[reinterpret_cast<uintptr_t>(s) / 16 % 61];
+}
 
 int check_host_batch(const std::string& w, int num_pages, int page_shift, int B, int n_tokens, const int* q_start,
                      const int* kv_len, const int* page_table, int max_pages) {
@@ -356,11 +352,9 @@ int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_tokens, 
     if (e != cudaSuccess) return fail_cuda(e, w + ": " + msg);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cxa::PagedTileMaps maps;
-    std::unique_lock<std::mutex> together;
-    if (tiles) {      // whatever can fail does before the first kernel is enqueued
-      if ((e = cxa::prepare_paged_tile(a, dev, &maps, &msg)) != cudaSuccess) return fail_cuda(e, w + ": " + msg);
-      together = std::unique_lock<std::mutex>(stream_lock(s));
-    }
+    // whatever can fail does before the first kernel is enqueued
+    if (tiles && (e = cxa::prepare_paged_tile(a, dev, &maps, &msg)) != cudaSuccess) return fail_cuda(e, w + ": " + msg);
+    const std::lock_guard<std::mutex> together(stream_lock(s));      // (of one kernel too: its workspace may be another call's)
     e = cxa::launch_paged_rows(a, max_rows, dev, s);
     if (e == cudaSuccess && tiles) e = cxa::launch_paged_tile(a, maps, dev, s);
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch");

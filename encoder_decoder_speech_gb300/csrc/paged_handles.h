@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 #include "cxa.h"
@@ -46,6 +47,12 @@ int guarded(F body) noexcept {
     return CXA_EINVAL;
   }
 }
+
+// Held while a call of several kernels, or of one that works on a workspace, is enqueued, so that nothing of
+// another thread's call on the same stream comes between its kernels: they hand scratch to each other in a workspace
+// that calls of one stream may share, and the second kernel of the paged attention starts without waiting for
+// anything but the first (paged_tile.cu). One lock for the streams whose handles fall together.
+std::mutex& stream_lock(cudaStream_t s);
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool valid_dtype(int t) { return t == CXA_F32 || t == CXA_BF16; }

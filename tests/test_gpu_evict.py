@@ -9,6 +9,7 @@ weight below the smallest normal number, 2^-126, becomes 0 (ex2 flushes it): 2^-
 Evictions copy: they are compared bit for bit.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -552,3 +553,40 @@ def test_evict_with_too_few_pages_reports_them():
         got = torch.cat([b.cache.Kp[0, free[0], h], b.cache.Kp[0, free[1], h]])
         page, at = b.table[0][t // 16].long(), t % 16
         assert torch.equal(got.cpu(), before.cpu()[0, page, h, at])
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+def test_threads_share_a_stream_and_its_workspace(pool):
+    """Gathered weights and attention, enqueued by threads at once on one stream with one workspace: each call's
+    kernels hand scratch to one another there, so each is enqueued whole."""
+    bs = [Batch([1] * 5, [3000, 20, 900, 77, 2500], 64, 8, 2, 64, pool, seed=1).fill(),
+          Batch([70, 1, 30], [6000, 900, 70], 64, 8, 2, 64, pool, seed=2).fill()]
+    need = []
+    for b in bs:
+        b.cache.Vp.copy_(randn(*b.cache.Vp.shape, seed=9))
+        need += [cxa.cxa_paged_weights_workspace_bytes(b.cache.handle, b.B, b.N, b.max_new, b.table.shape[1], 8),
+                 cxa.cxa_paged_attention_workspace_bytes(8, 2, 64, b.max_new)]
+    ws = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+    calls = 40
+    weights = [[b.W.clone() for _ in range(calls)] for b in bs]
+    want = [(b.accumulate(), b.cache.attend(0, b.q.cuda(), **b.d, max_new=b.max_new)) for b in bs]
+    got = [(w, [torch.zeros_like(a) for _ in range(calls)]) for w, (_, a) in zip(weights, want)]
+    qs = [b.q.cuda() for b in bs]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def accumulate(i):
+        for w in got[i][0]:
+            bs[i].cache.accumulate(0, qs[i], **bs[i].d, max_new=bs[i].max_new, weights=w, workspace=ws,
+                                   stream=stream)
+
+    def attend(i):
+        for o in got[i][1]:
+            bs[i].cache.attend(0, qs[i], **bs[i].d, max_new=bs[i].max_new, out=o, workspace=ws, stream=stream)
+
+    threads = [threading.Thread(target=f, args=(i,)) for f in (accumulate, attend) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for (w, a), (ws_, as_) in zip(want, got):
+        assert all(torch.equal(w, x) for x in ws_) and all(torch.equal(a, x) for x in as_)

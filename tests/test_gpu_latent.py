@@ -512,3 +512,31 @@ def test_both_forms_give_the_same_attention(pool):
                 A = torch.einsum("ht,thd->hd", p, torch.einsum("tc,chd->thd", rows[:see, :latent].abs(), wv.abs()))
                 e = (4 * u + 2 * u * big if pool == "bf16" else 2.0 ** -18 * (1 + big))
                 assert float(((got[at] - want).abs() - e * A).max()) <= 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+def test_threads_share_a_stream_and_its_workspace(pool):
+    """Attention is two kernels that hand partial states to one another in the workspace: calls that threads enqueue
+    at once on one stream are each enqueued whole."""
+    bs = [Batch([1] * 4, [3000, 20, 9000, 77], 64, 20, 512, 64, pool, seed=1).fill(),
+          Batch([3, 1], [5000, 700], 64, 8, 128, 16, pool, seed=2).fill(), Batch([40], [900], 32, 6, 256, 0, pool, seed=3).fill()]
+    code = {"bf16": cxa.CXA_BF16, "f32": cxa.CXA_F32}[pool]
+    need = max(cxa.cxa_latent_attention_workspace_bytes(b.H, b.latent, b.max_new, code) for b in bs)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = [b.attend() for b in bs]
+    outs = [[torch.zeros_like(w) for _ in range(40)] for w in want]
+    qs = [b.q.cuda() for b in bs]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls(i):
+        for out in outs[i]:
+            bs[i].cache.attend(0, qs[i], **bs[i].d, max_new=bs[i].max_new, scale=bs[i].scale, out=out, workspace=ws,
+                               stream=stream)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(3)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
