@@ -590,3 +590,23 @@ def test_threads_share_a_stream_and_its_workspace(pool):
     torch.cuda.synchronize()
     for (w, a), (ws_, as_) in zip(want, got):
         assert all(torch.equal(w, x) for x in ws_) and all(torch.equal(a, x) for x in as_)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+@pytest.mark.parametrize("n, Hq, at", [(3, 4, 1), (70, 4, 40), (300, 4, 10), (300, 10, 299), (90, 400, 30), (130, 2, 0)])
+def test_a_query_that_is_not_finite_leaves_later_keys_alone(n, Hq, at, pool, value):
+    """Keys behind the token's own have the weights of a batch whose queries are all finite, bit for bit."""
+    b = Batch([n], [200 + n], 64, Hq, 2, 64, pool).fill()
+    before = b.W.clone()
+    clean = b.accumulate().clone()
+    b.W.copy_(before)
+    b.q[at, 0, 7] = value                 # of the first K/V head
+    b.accumulate()
+    p, slot = b.places(0)
+    got, want = b.W.cpu()[0][p, :, slot], clean.cpu()[0][p, :, slot]
+    assert torch.equal(got[:, 1], want[:, 1])
+    assert torch.equal(got[200 + at + 1:, 0], want[200 + at + 1:, 0])
+    assert bool(got[:200 + at + 1, 0].isnan().any())
+    if value != value:
+        assert bool(got[:200 + at + 1, 0].isnan().all())
