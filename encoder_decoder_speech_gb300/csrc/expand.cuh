@@ -20,5 +20,9 @@ __host__ __device__ inline ExpandSpan expand_span(const int* from, const int* kv
   s.lo = f < 0 ? 0 : f > s.hi ? s.hi : f;
   return s;
 }
+// Whether some positions of sequence b that are to be expanded lie behind its row of the table.
+__host__ __device__ inline bool expand_passes(const int* from, const int* kv_len, int cap, int b) {
+  return kv_len[b] > cap && (from == nullptr || from[b] < kv_len[b]);
+}
 
 }  // namespace cxa

@@ -40,7 +40,11 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(const __grid_cons
     return (s.hi - s.lo + kTile - 1) / kTile;
   };
   SpanRange range;
-  if (!span_locate<kThreads>(a.B, tiles, &s_span, &range)) return;
+  auto count = [&](int b) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && expand_passes(a.from, a.kv_len, cap, b)) atomicOr(p.status, kStatusBadPage);
+    return tiles(b);
+  };
+  if (!span_locate<kThreads>(a.B, count, &s_span, &range)) return;
   int b = range.b, first = range.first;
   for (int g = range.g0; g < range.g1; ++g) {
     while (g - first >= tiles(b)) first += tiles(b++);

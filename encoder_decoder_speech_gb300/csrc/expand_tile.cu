@@ -100,10 +100,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const ExpandSpan s = expand_span(p.from, p.kv_len, cap, b);
     return s.hi > s.lo ? (s.hi + kRows - 1) / kRows - s.lo / kRows : 0;
   };
+  auto count = [&](int b) {
+    if (blockIdx.x == 0 && expand_passes(p.from, p.kv_len, cap, b)) atomicOr(p.status, kStatusBadPage);
+    return tiles(b);
+  };
   // this pair's work [g0, g1), and the sequence of its first tile; the same in both blocks
   int g0 = 0, g1 = 0, total = 0, b = 0, first = 0;
   if (!span_find<kThreads>(
-          p.B, tiles, &sm->span,
+          p.B, count, &sm->span,
           [&](int n) {
             const long long pairs = static_cast<long long>(n + 1) / 2 * p.products, by = gridDim.x / 2, at = blockIdx.x / 2;
             total = n;

@@ -540,3 +540,31 @@ def test_threads_share_a_stream_and_its_workspace(pool):
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert all(torch.equal(w, x) for x in o)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+def test_expand_reports_positions_behind_the_row_of_the_table(pool):
+    """kv_len past what page_table's row holds: the positions that it does hold are written, the others reported."""
+    kw = dict(kv=[100, 50], start=None, H=4, dh=64, latent=128, rope=16, page=32, to_page=16)
+    b, to, table, WK, WV = expand_case(pool=pool, **kw)
+    wide = torch.cat([table, torch.full((2, 40), to.num_pages - 1, dtype=torch.int32)], 1)     # (no position writes there)
+
+    def call(kv, start=None, t=b.table):
+        ints = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32).cuda()
+        b.cache.expand(0, WK.cuda(), WV.cuda(), ints(kv), t.cuda(), to, 1, wide.cuda(), start=ints(start))
+        return cxa.cxa_device_status(1)
+
+    assert b.table.shape[1] * 32 == 160
+    assert call([100, 50]) == cxa.CXA_OK
+    good = to.Kp.clone(), to.Vp.clone()
+    narrow = b.table[:, :3].contiguous()              # 96 positions
+    to.Kp.fill_(5.0)
+    to.Vp.fill_(6.0)
+    assert call([100, 50], t=narrow) == cxa.CXA_EPAGE
+    last = int(table[0, 6])                           # of positions 96 to 99
+    kept = [p for p in range(to.num_pages) if p != last]
+    assert torch.equal(to.Kp[:, kept], good[0][:, kept]) and torch.equal(to.Vp[:, kept], good[1][:, kept])
+    assert bool((to.Kp[1, last] == 5.0).all()) and bool((to.Vp[1, last] == 6.0).all())
+    for kv, start, status in (([97, 0], [97, 0], cxa.CXA_OK), ([97, 0], [96, 0], cxa.CXA_EPAGE),
+                              ([0, 2 ** 31 - 1], [0, 97], cxa.CXA_EPAGE), ([96, 96], [-5, 500], cxa.CXA_OK)):
+        assert call(kv, start, narrow) == status
