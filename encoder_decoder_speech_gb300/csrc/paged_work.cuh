@@ -28,6 +28,7 @@ struct WorkShape {
   bool coarse;        // whether items are cut into fewer, larger chunks (work_locate may set it)
   int cap;            // keys the table's row can hold
   int min_rows, max_rows;   // sequences with fewer or more query rows a head are another kernel's
+  bool alone = false;       // no other kernel takes those with more: they are reported
 };
 
 // The rows of one K/V head of a sequence; 0 if the sequence is not this kernel's.
@@ -135,7 +136,7 @@ struct WorkScratch {
 // kMayCoarsen, w becomes coarse where a block would have less than four steps: a merge costs
 // as much as some eight of them. With kRuns, tiles are counted in runs (each_run). With a
 // status word, sequences whose keys pass their row of the table are reported there, whichever
-// kernel they are of, and a q_start that decreases. A batch of more chunks than can be numbered,
+// kernel they are of, those that no kernel takes, and a q_start that decreases. A batch of more chunks than can be numbered,
 // which only such a q_start brings, is left out.
 template <int kThreads, bool kMayCoarsen, bool kRuns = false>
 __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScratch* sm, WorkRange* range,
@@ -153,6 +154,7 @@ __device__ bool work_locate(const PagedBatch& bt, WorkShape& w, int Hkv, WorkScr
     const int m = work_rows(s, w);
     if (status != nullptr && s.n > 0 && s.kv > w.cap) atomicOr(status, kStatusBadPage);
     if (status != nullptr && bt.q_start[b + 1] < bt.q_start[b]) atomicOr(status, kStatusBadBatch);
+    if (status != nullptr && w.alone && static_cast<long long>(s.n) * w.G > w.max_rows) atomicOr(status, kStatusBadBatch);
     if constexpr (kRuns) {
       each_run(s, w, m, [&](int, int tiles, int c) {
         const long long all = static_cast<long long>(tiles) * c * Hkv;

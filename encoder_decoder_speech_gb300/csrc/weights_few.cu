@@ -236,6 +236,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.shape.cap = a.batch.width << a.layer.page_shift;
   p.shape.min_rows = 0;
   p.shape.max_rows = p.max_rows = p.shape.G * a.max_new;      // (the room for scores holds no more)
+  p.shape.alone = true;
   static SmemOnce once;
   cudaError_t e = allow_smem(weights_few_rows_kernel<kDh>, S::smem, dev.device, &once);
   if (e != cudaSuccess) return e;

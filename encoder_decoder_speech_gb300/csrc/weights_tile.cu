@@ -882,6 +882,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   few.shape.rows = few::kRows;
   few.shape.min_rows = 0;
   few.shape.max_rows = split.few_rows;      // (the room for scores holds no more)
+  few.shape.alone = !split.many;
   p.shape.rows = many::kTiles * (kTileRows / G * G);
   p.shape.min_rows = split.few_rows + 1;
   p.shape.max_rows = 0x7FFFFFFF;

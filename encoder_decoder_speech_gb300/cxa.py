@@ -1048,7 +1048,8 @@ class PagedCache(_Paged):
         """Add to weights (new_weights()) the attention weight that the new tokens' queries q
         [N, Hq, dh], of the pool's type, give each key, over the query heads of its K/V head; what it
         had gathered before counts decay times, and new tokens' entries start at zero. No page may be two
-        sequences' of the batch. max_new and workspace as for attend. Returns weights."""
+        sequences' of the batch. max_new and workspace as for attend, but a sequence with more new tokens
+        than max_new may be left out (cxa_device_status then says CXA_EINVAL). Returns weights."""
         tc = _torch_calls or _calls()
         at, dh, dt = self._at, self.dh, q.dtype
         B, width = self._batch(q_start, kv_len, page_table, tc.i32)

@@ -495,8 +495,8 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  * Pages that two sequences of the batch share must not be given: their entries would be written by
  * both. Arguments, the limit on the work and errors otherwise as for cxa_paged_attention; dtype is
  * the pool's. A token that sees an infinity or a NaN in q or K may make the weights of all keys that
- * it sees NaN. A sequence with more than max_new new tokens may be left out. Results do not change from call to
- * call.
+ * it sees NaN. A sequence with more than max_new new tokens may be left out, its entries as they were; if it is,
+ * cxa_device_status reports CXA_EINVAL. Results do not change from call to call.
  */
 CXA_API size_t cxa_paged_weights_workspace_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new,
                                                  int max_pages, int Hq);

@@ -610,3 +610,28 @@ def test_a_query_that_is_not_finite_leaves_later_keys_alone(n, Hq, at, pool, val
     assert bool(got[:200 + at + 1, 0].isnan().any())
     if value != value:
         assert bool(got[:200 + at + 1, 0].isnan().all())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+def test_a_max_new_that_is_too_small_is_reported(pool):
+    """A sequence that has no room is left out and reported; the others' weights are right. Where the call's kernels
+    take it all the same, nothing is reported."""
+    b = Batch([1, 5, 2], [300, 200, 90], 32, 8, 4, 64, pool).fill()
+    before = b.W.clone()
+    b.accumulate(max_new=2)
+    assert cxa.cxa_device_status(1) == cxa.CXA_EINVAL
+    p, at = b.places(1)
+    assert torch.equal(b.W[0][p, :, at], before[0][p, :, at])
+    b.n[1] = 0
+    b.close(before, b.W)
+    b.n[1] = 5
+    b.W.copy_(before)
+    b.accumulate(max_new=9)                       # 18 rows a K/V head: any sequence is taken
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    b.close(before, b.W)
+    b.W.copy_(before)
+    many = Batch([1, 60], [300, 200], 32, 8, 4, 64, pool).fill()
+    before = many.W.clone()
+    many.accumulate(max_new=9)
+    assert cxa.cxa_device_status(1) == cxa.CXA_OK
+    many.close(before, many.W)
