@@ -6,11 +6,13 @@
 // histograms added up over distributed shared memory, find the keep-th largest; one more writes the
 // positions above it, and of those equal to it the first ones. (A block an item, which read the weights anew in
 // each pass: 225 us for 32 lists of 65536; a cluster 29, of which the first reads of the weights take 5 to 10, the
-// passes 3 each.) evict_copy_kernel copies the listed rows of K, V and weights, a block 32 of them
+// passes 3 each.) Items of up to 4096 positions take one block, those of up to 16384 four. evict_copy_kernel copies the listed rows of K, V and weights, a block 32 of them
 // (rows looked up and read two or four at a time by a thread: slower, 83 and 89 us).
 // Bound by memory: weights are read once, what stays is read and written once. 4 sequences of up to 65536 keys of
 // 8 heads of 128 down to 8192, bf16: 79.7 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
 // of 448 keys down to 112: 18.9 us, latency of the two kernels.
+#include <algorithm>
+
 #include "cluster.cuh"
 #include "latent.cuh"
 #include "ptx.cuh"
@@ -19,7 +21,9 @@ namespace cxa {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr int kMaxRoom = 49152;      // keys in a block's shared memory; more are read again
+constexpr int kShort = 4096;         // positions of an item that one block takes
+// Keys in a block's shared memory; more are read again. Fewer where an SM has more than one block.
+constexpr int kMaxRoom = 49152, kSharedRoom = 21504;
 constexpr int kCopyThreads = 128, kCopyRows = 32;
 
 struct EvictParams {
@@ -42,36 +46,35 @@ __device__ __forceinline__ int ld_cluster(const int* local, uint32_t rank) {
   return v;
 }
 
-// Alone: one block an item, digits of 8 bits; otherwise a cluster of 4 or 8, digits of 11, 11 and 10.
-template <bool kAlone>
-struct Select {
-  static constexpr int threads = kAlone ? 256 : 512, warps = threads / 32;
-  static constexpr int bins = kAlone ? 256 : 2048, passes = kAlone ? 4 : 3;
-};
+// The keys that a sequence has.
+__device__ __forceinline__ int length_of(const EvictLaunch& a, int b) {
+  return min(max(0, a.kv_len[b]), a.width << a.page_shift);
+}
 
-template <bool kAlone>
-__global__ void __launch_bounds__(Select<kAlone>::threads)
-    evict_select_kernel(const __grid_constant__ EvictParams p, int blocks, int room) {
-  using S = Select<kAlone>;
-  constexpr int kThreads = S::threads, kWarps = S::warps, kBins = S::bins;
-  extern __shared__ uint32_t s_key[];        // [room]
-  constexpr int kHists = kAlone ? 1 : S::passes;      // (one a pass: other blocks may still read the last one's)
+// The blocks that take an item of so many positions.
+__host__ __device__ constexpr int blocks_of(long long positions) {
+  return positions <= kShort ? 1 : positions <= 4 * kShort ? kMaxCluster / 2 : kMaxCluster;
+}
+
+// Alone: one block an item, digits of 8 bits; otherwise a cluster of 4 or 8, digits of 11, 11 and 10.
+// By all threads of the block, or of the cluster.
+template <bool kAlone, int kThreads>
+__device__ __forceinline__ void select_item(const EvictParams& p, int item, int kv, int blocks, uint32_t* s_key, int room) {
+  constexpr int kWarps = kThreads / 32, kBins = kAlone ? 256 : 2048, kPasses = kAlone ? 4 : 3;
+  constexpr int kHists = kAlone ? 1 : kPasses;        // (one a pass: other blocks may still read the last one's)
   __shared__ __align__(16) int s_hist[kHists][kBins];              // of this block
   __shared__ int s_group[kHists][kAlone ? 1 : kBins / 32];         // sums of 32 of them
   __shared__ int s_scan[2][kWarps];
   __shared__ int s_count[2];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const EvictLaunch& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (kAlone) blocks = 1;
   const int rank = kAlone ? 0 : static_cast<int>(cluster_rank());
-  const int item = blockIdx.x / blocks, h = item % a.Hkv, b = item / a.Hkv % a.B, l = item / a.Hkv / a.B;
-  const int cap = a.width << a.page_shift;
-  const int given = max(0, a.kv_len[b]), kv = min(given, cap), m = min(kv, a.keep);
-  if (tid == 0 && rank == 0 && given > cap) atomicOr(p.status, kStatusBadPage);
+  const int h = item % a.Hkv, b = item / a.Hkv % a.B, l = item / a.Hkv / a.B;
+  const int m = min(kv, a.keep);
+  if (tid == 0 && rank == 0 && a.kv_len[b] > kv) atomicOr(p.status, kStatusBadPage);
   if (l == 0 && h == 0 && tid == 0 && rank == 0) a.out_len[b] = m;
   int* kept = a.kept + static_cast<size_t>(item) * a.keep;
   for (int i = m + rank * kThreads + tid; i < a.keep; i += blocks * kThreads) kept[i] = -1;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
     return at;
   };
 #pragma unroll 1
-  for (int pass = 0; pass < S::passes; ++pass) {
+  for (int pass = 0; pass < kPasses; ++pass) {
     const int shift = kAlone ? 24 - 8 * pass : pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int top = kAlone ? 32 - 8 * pass : pass == 0 ? 32 : pass == 1 ? 21 : 10;
     int* hist = s_hist[kAlone ? 0 : pass];
@@ -251,7 +254,40 @@ __global__ void __launch_bounds__(Select<kAlone>::threads)
     out += __popc(ma);
     ties += __popc(mt);
   }
-  if constexpr (!kAlone) cluster_sync();      // no block leaves while another may read its counts
+  if constexpr (!kAlone) cluster_sync();      // no block goes on while another may read its counts
+}
+
+// Tables of up to kShort positions: a block an item.
+constexpr int kSmallThreads = 256;
+__global__ void __launch_bounds__(kSmallThreads) evict_select_kernel(const __grid_constant__ EvictParams p, int room) {
+  extern __shared__ uint32_t s_key[];        // [room]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int item = blockIdx.x;
+  select_item<true, kSmallThreads>(p, item, length_of(p.a, item / p.a.Hkv % p.a.B), 1, s_key, room);
+}
+
+// Wider ones: a cluster of `launched` blocks an item, of which those stay that its sequence has work for; the others
+// leave. 768 windows of up to 448 keys: 22 us in a table of 512 positions, 65 in one of 1,048,576, and 565 there where
+// all blocks took part, with room for the table's keys. (A grid that stays and deals itself the items: 45 us there, but
+// 61 in place of 53 for 128 of up to 8000 keys, and 235 in place of 172 for 128 of up to 120,000.)
+constexpr int kWideThreads = 512;
+// (by itself, so that it costs the other way no registers: 80.5 us, 79.2 so, for 32 lists of up to 65536)
+__device__ __noinline__ void select_short(const EvictParams& p, int item, int kv, uint32_t* s_key, int room) {
+  select_item<true, kWideThreads>(p, item, kv, 1, s_key, room);
+}
+__global__ void __launch_bounds__(kWideThreads, 4)
+    evict_select_wide_kernel(const __grid_constant__ EvictParams p, int launched, int room) {
+  extern __shared__ uint32_t s_key[];        // [room]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int item = blockIdx.x / launched, kv = length_of(p.a, item / p.a.Hkv % p.a.B);
+  const int blocks = blocks_of(kv);          // (<= launched, as kv fits the table)
+  if (static_cast<int>(cluster_rank()) >= blocks) return;      // (a cluster's barrier is of the threads that are left)
+  if (blocks == 1)
+    select_short(p, item, kv, s_key, room);
+  else
+    select_item<false, kWideThreads>(p, item, kv, blocks, s_key, room);
 }
 
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
@@ -295,19 +331,9 @@ cudaError_t launch_evict(const EvictLaunch& a, const DeviceInfo& dev, cudaStream
   EvictParams p = {a, dev.status_word};
   const long long items = static_cast<long long>(a.nl) * a.B * a.Hkv;
   const long long cap = static_cast<long long>(a.width) << a.page_shift;
-  // up to 4096 positions go to a block by itself; a share of the bins has to fit a block's threads otherwise
-  const int blocks = cap <= 4096 ? 1 : cap <= 16384 ? kMaxCluster / 2 : kMaxCluster;
-  const long long want = (cap + blocks - 1) / blocks + 32;
-  const int room = static_cast<int>(want < kMaxRoom ? want : kMaxRoom);
+  const int blocks = blocks_of(cap);
   const bool small = blocks == 1;
-  cudaError_t e = cudaSuccess;
-  static SmemOnce once;
-  if (!small && (e = allow_smem(evict_select_kernel<false>, kMaxRoom * 4, dev.device, &once)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * blocks));
-  cfg.blockDim = dim3(small ? Select<true>::threads : Select<false>::threads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -315,10 +341,27 @@ cudaError_t launch_evict(const EvictLaunch& a, const DeviceInfo& dev, cudaStream
   attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
+  cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = small ? 1 : 2;
-  e = small ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p, blocks, room)
-            : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p, blocks, room);
+  cudaError_t e = cudaSuccess;
+  if (small) {
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(cap) * 4;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, static_cast<int>(cap));
+  } else {
+    static SmemOnce once;
+    if ((e = allow_smem(evict_select_wide_kernel, kMaxRoom * 4, dev.device, &once)) != cudaSuccess) return e;
+    // (Sequences may be short in a wide table: what room costs is blocks an SM, of those too that leave at once.)
+    const long long want = std::max((cap + blocks - 1) / blocks + 32, static_cast<long long>(kShort));
+    const int room = static_cast<int>(std::min<long long>(want, items * blocks <= dev.num_sms ? kMaxRoom : kSharedRoom));
+    cfg.gridDim = dim3(static_cast<unsigned>(items * blocks));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, evict_select_wide_kernel, p, blocks, room);
+  }
   if (e != cudaSuccess) return e;
   count_launches(1);
   cfg.gridDim = dim3(static_cast<unsigned>(items * ((a.keep + kCopyRows - 1) / kCopyRows)));

@@ -635,3 +635,33 @@ def test_a_max_new_that_is_too_small_is_reported(pool):
     many.accumulate(max_new=9)
     assert cxa.cxa_device_status(1) == cxa.CXA_OK
     many.close(before, many.W)
+
+
+@pytest.mark.parametrize("positions", [5120, 16384, 32768, 1 << 20])
+def test_evict_in_wide_tables(positions):
+    """Short and long sequences in one call, in tables as wide as the longest that a server allows."""
+    kv, keep, L, Hkv, page = [448, 5000, 1, 4096, 0, 4097, 3000], 700, 2, 3, 64
+    kv += [k for k in (16384, 16385, 30000) if k <= positions]
+    b = Batch([0] * len(kv), kv, page, Hkv, Hkv, 64, "bf16", L=L, spare=len(kv) * 11 + 3)
+    free = [p for p in range(b.cache.num_pages) if p not in set(b.table.flatten().tolist())]
+    table = torch.full((len(kv), positions // page), -1, dtype=torch.int32)
+    w = min(table.shape[1], b.table.shape[1])
+    table[:, :w] = b.table[:, :w]
+    out = torch.tensor(free[:len(kv) * 11], dtype=torch.int32).view(len(kv), 11)
+    b.W.copy_((b.W * 50).floor())                                # (many ties)
+    W, before = b.W.cpu(), randn(*b.cache.Kp.shape, seed=3, dtype=torch.bfloat16)
+    b.cache.Kp.copy_(before)
+    kept, out_len = b.cache.evict(b.W, keep, b.d["kv_len"], table.cuda(), out.cuda(), first=5, recent=100)
+    assert out_len.tolist() == [min(k, keep) for k in kv]
+    kept, K = kept.cpu().long(), b.cache.Kp.cpu()
+    for s, n in enumerate(kv):
+        m, t = min(n, keep), torch.arange(n)
+        p, at = b.places(s)
+        for l in range(L):
+            for h in range(Hkv):
+                x = W[l][p, h, at]
+                x[(t < 5) | (t >= n - 100)] = math.inf
+                want = torch.sort(torch.sort(x, descending=True, stable=True).indices[:m]).values
+                assert torch.equal(kept[l, s, h, :m], want) and bool((kept[l, s, h, m:] == -1).all())
+                j = torch.arange(m)
+                assert torch.equal(K[l][out[s][j // page].long(), h, j % page], before[l][p[want], h, at[want]])
