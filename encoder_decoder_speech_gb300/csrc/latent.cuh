@@ -62,8 +62,14 @@ struct WeightsLaunch {
   PagedBatch batch;
   PagedLayer layer;
   void* workspace;
+  size_t workspace_bytes;
 };
-size_t weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new, bool bf16);
+// The least that a call needs, and the most that it makes use of.
+struct WeightsWorkspace {
+  size_t least, most;
+};
+WeightsWorkspace weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new,
+                                   bool bf16);
 cudaError_t launch_weights(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);
 
 struct EvictLaunch {

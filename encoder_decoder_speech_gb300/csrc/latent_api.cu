@@ -58,6 +58,16 @@ int check_workspace(const std::string& w, const void* p, size_t bytes, size_t ne
   return CXA_OK;
 }
 
+cxa::WeightsWorkspace weights_workspace_of(const cxa_pages* pages, int B, int n_tokens, int max_new, int max_pages,
+                                           int Hq) {
+  if (pages == nullptr || B < 1 || B > 1 << 30 || n_tokens < 0 || max_new < 1 || max_pages < 1 ||
+      static_cast<long long>(max_pages) << pages->page_shift > (1LL << 30) || Hq < 1 || Hq > 65535 ||
+      Hq % pages->Hkv != 0)
+    return {0, 0};
+  return cxa::weights_workspace(B, n_tokens, max_pages, pages->page_shift, Hq, pages->Hkv, max_new,
+                                pages->dtype == CXA_BF16);
+}
+
 }  // namespace
 
 extern "C" {
@@ -252,12 +262,11 @@ int cxa_latent_expand(const cxa_latent* cache, int layer, const cxa_pages* to, i
 
 size_t cxa_paged_weights_workspace_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new, int max_pages,
                                          int Hq) {
-  if (pages == nullptr || B < 1 || B > 1 << 30 || n_tokens < 0 || max_new < 1 || max_pages < 1 ||
-      static_cast<long long>(max_pages) << pages->page_shift > (1LL << 30) || Hq < 1 || Hq > 65535 ||
-      Hq % pages->Hkv != 0)
-    return 0;
-  return cxa::weights_workspace(B, n_tokens, max_pages, pages->page_shift, Hq, pages->Hkv, max_new,
-                                pages->dtype == CXA_BF16);
+  return weights_workspace_of(pages, B, n_tokens, max_new, max_pages, Hq).least;
+}
+
+size_t cxa_paged_weights_room_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new, int max_pages, int Hq) {
+  return weights_workspace_of(pages, B, n_tokens, max_new, max_pages, Hq).most;
 }
 
 int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
@@ -307,6 +316,7 @@ int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, in
     a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
     const std::lock_guard<std::mutex> together(stream_lock(static_cast<cudaStream_t>(stream)));
     e = cxa::launch_weights(a, dev, static_cast<cudaStream_t>(stream), &msg);
     if (e != cudaSuccess) return fail_cuda(e, w + ": launch " + msg);

@@ -1,31 +1,67 @@
-// Dispatch of the gathered attention weights.
+// Dispatch of the gathered attention weights, and what is decided by sizes.
+#include <algorithm>
+
 #include "weights.cuh"
 
 namespace cxa {
 namespace {
 
+constexpr int kFewRows16 = 16;              // query rows a K/V head of a few-rows product
+constexpr double kSplitChunks = 8192;
+
 // A tile of 128 rows holds whole tokens, so G query heads have to fit into it.
 bool on_tiles(int G, bool bf16) { return bf16 && G <= 128; }
-// The room for scores that an fp32 call of few rows takes; 0: it goes the way of many. (16 single tokens over up to
-// 4000 keys of 8 heads of 64: 194 us that way, 27 this.)
-size_t few_scores(int B, int width, int page_shift, int Hkv, int G, int max_new, bool bf16) {
-  return bf16 || static_cast<long long>(G) * max_new > 16 ? 0 : weights_score_bytes(B, width, page_shift, Hkv, G * max_new);
-}
+// (16 single tokens over up to 4000 keys of 8 heads of 64 in fp32: 194 us the way of many rows, 27 this.)
+bool few_in_fp32(int G, int max_new, bool bf16) { return !bf16 && static_cast<long long>(G) * max_new <= kFewRows16; }
 
 }  // namespace
 
-size_t weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new, bool bf16) {
+// All have few rows, where no sequence can have more than a product's 16; otherwise those of one or two
+// tokens (more would take room for scores that hardly any use), if their scores can be kept, there is more than
+// one sequence, and the keys are many enough to pay for two more launches. (20 single tokens beside 4 chunks of a
+// prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 237 so; 5 tokens in each of 16 sequences of
+// up to 1500 keys of 8 heads: 39 us and 45.) Whether the keys are enough goes by the table's width: where they are not,
+// in a wide table, the launches cost 13 us (24 sequences, 300 tokens, up to 500 keys: 35 us and 48). Asked of
+// the device, the kernels that then find nothing to do cost more: 52 us, and 248 in place of 241 where they have.
+WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new) {
+  WeightsSplit s;
+  s.chunks = weights_chunks(B, width, page_shift, Hkv);
+  s.many = static_cast<long long>(G) * max_new > kFewRows16;
+  const int tokens = kFewRows16 / G < 2 ? kFewRows16 / G : 2;
+  s.few_rows = !s.many ? G * max_new : B == 1 || s.chunks < kSplitChunks ? 0 : tokens * G;
+  return s;
+}
+
+ScoreRule score_rule(const WeightsSplit& s, const WeightsPlaces& at) {
+  ScoreRule r = {};
+  if (s.few_rows == 0) return r;
+  // (no more than a workspace of the recommended size has: what a larger one gave would depend on other calls)
+  const size_t room = std::min(at.score_bytes, kMaxScoreBytes) / score_chunk_bytes(s.few_rows);
+  r.room = static_cast<int>(std::min<size_t>(room, 0x7FFFFFFE));
+  r.max_rows = s.few_rows;
+  r.others = s.many;
+  r.kept = s.chunks <= r.room;
+  r.ask = !r.kept && r.room > 0;
+  r.word = at.word;
+  return r;
+}
+
+WeightsWorkspace weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new,
+                                   bool bf16) {
   const int G = Hq / Hkv;
-  size_t n = kPagedCounterBytes + weights_ref_bytes(static_cast<long long>(n_tokens) * Hq) + kWeightsPartBytes;
-  if (on_tiles(G, bf16)) return n + weights_split(B, width, page_shift, Hkv, G, max_new).score_bytes;
-  return n + few_scores(B, width, page_shift, Hkv, G, max_new, bf16);
+  const size_t fixed = weights_fixed_bytes(static_cast<long long>(n_tokens) * Hq);
+  WeightsSplit s = {};
+  if (on_tiles(G, bf16) || few_in_fp32(G, max_new, bf16)) s = weights_split(B, width, page_shift, Hkv, G, max_new);
+  const double scores = s.chunks * static_cast<double>(score_chunk_bytes(s.few_rows));
+  const bool fit = scores <= static_cast<double>(kMaxScoreBytes);
+  return {fixed + (fit ? static_cast<size_t>(scores) : 0), fixed + (fit ? static_cast<size_t>(scores) : kMaxScoreBytes)};
 }
 
 cudaError_t launch_weights(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
-  if (on_tiles(a.Hq / a.layer.Hkv, a.bf16)) return launch_weights_tile(a, dev, stream, msg);
-  if (few_scores(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, a.Hq / a.layer.Hkv, a.max_new, a.bf16) != 0)
-    return launch_weights_few_rows(a, dev, stream);
-  return launch_weights_rows(a, dev, stream);
+  const int G = a.Hq / a.layer.Hkv;
+  if (on_tiles(G, a.bf16)) return launch_weights_tile(a, dev, stream, msg);
+  if (few_in_fp32(G, a.max_new, a.bf16)) return launch_weights_few_rows(a, dev, stream);
+  return launch_weights_rows(a, nullptr, dev, stream);
 }
 
 }  // namespace cxa

@@ -25,7 +25,7 @@ struct FewParams {
   float* ref;               // [Hkv][n_tokens][G]
   float* part;              // [2 * grid][kScoreRows][2]
   float* scores;
-  int max_rows;
+  ScoreRule rule;
   unsigned int* status;
   PagedBatch batch;
   PagedLayer layer;
@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDh>::per_sm)
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
+  const bool kept = p.rule.ask ? score_ask<kThreads>(p.rule, bt, G, Hkv, shape.cap, &s_work) : p.rule.kept;
   if (!work_locate<kThreads, false>(bt, shape, Hkv, &s_work, &range, &cur, p.status)) return;
   const int n_chunks = range.g1 - range.g0;
 
@@ -166,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDh>::per_sm)
       const int key = c * kFewKeys + tid;
       const bool gone = (s_bad[stage] >> (tid >> 4) & 1u) != 0 || key >= shape.cap;
       const int hidden = gone ? kScoreRows : (c + 1) * kFewKeys > see_all ? min(max(key - (seq.kv - seq.n), 0), kScoreRows) * G : 0;
-      few_take(x, rows, hidden, p.qscale, p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kFewKeys + tid, m, l);
+      float* to = kept ? p.scores + static_cast<size_t>(cur.first + c) * p.rule.max_rows * kFewKeys + tid : nullptr;
+      few_take(x, rows, hidden, p.qscale, to, m, l);
       if (++stage == kStages) stage = 0;
     }
     few_finish(&s_few, m, l, rows, cur, range, c0, c1, true, p.part, p.counters,
@@ -187,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, kAddBlocks) weights_add_kernel(const
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
+  if (!scores_kept(p.rule)) return;
   if (!work_locate<kThreads, false>(bt, shape, p.Hkv, &s_work, &range, &cur)) return;
   for (;;) {
     const int end = min(range.g1, cur.first + cur.nc), c0 = cur.c, c1 = end - cur.first;
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, kAddBlocks) weights_add_kernel(const
     for (int c = c0; c < c1; ++c) {
       const int key = c * kFewKeys + tid;
       const int page = key < keys ? paged_lookup(row, bt.width, p.page_shift, p.num_pages, key) : -1;
-      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kFewKeys + tid;
+      const float* from = p.scores + static_cast<size_t>(cur.first + c) * p.rule.max_rows * kFewKeys + tid;
       float add = 0.f;
 #pragma unroll 4
       for (int r = 0; r < rows; ++r) add += few_rescale(__ldcg(from + r * kFewKeys), s_ref[r]);      // (0 of a hidden key)
@@ -221,21 +224,23 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.q = static_cast<const float*>(a.q);
   p.q_stride = a.q_stride;
   p.qscale = a.scale * 1.4426950408889634f;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  p.counters = reinterpret_cast<unsigned int*>(ws);
-  p.ref = reinterpret_cast<float*>(ws + kPagedCounterBytes);
-  p.part = reinterpret_cast<float*>(ws + kPagedCounterBytes + weights_ref_bytes(static_cast<long long>(a.batch.n_tokens) * a.Hq));
-  p.scores = p.part + kWeightsPartBytes / 4;
+  const WeightsPlaces at = weights_places(a);
+  p.counters = at.counters;
+  p.ref = at.ref;
+  p.part = at.part;
+  p.scores = at.scores;
   p.status = dev.status_word;
   p.batch = a.batch;
   p.layer = a.layer;
   p.shape.G = a.Hq / a.layer.Hkv;
+  p.rule = score_rule(
+      weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, p.shape.G, a.max_new), at);
   p.shape.rows = kScoreRows;
   p.shape.chunk_shift = kFewChunkShift;
   p.shape.coarse = false;
   p.shape.cap = a.batch.width << a.layer.page_shift;
   p.shape.min_rows = 0;
-  p.shape.max_rows = p.max_rows = p.shape.G * a.max_new;      // (the room for scores holds no more)
+  p.shape.max_rows = p.rule.max_rows;      // (the room for scores holds no more)
   p.shape.alone = true;
   static SmemOnce once;
   cudaError_t e = allow_smem(weights_few_rows_kernel<kDh>, S::smem, dev.device, &once);
@@ -254,8 +259,10 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   e = cudaLaunchKernelEx(&cfg, weights_few_rows_kernel<kDh>, p);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  WeightsAdd add = {p.batch, p.shape, a.layer.num_pages, a.layer.Hkv, a.layer.page_shift, p.scores, p.ref, p.max_rows,
-                    a.weights, a.decay};
+  if (!p.rule.kept && (e = launch_weights_rows(a, &p.rule, dev, stream)) != cudaSuccess) return e;
+  if (!p.rule.kept && !p.rule.ask) return e;
+  WeightsAdd add = {p.rule, p.batch, p.shape, a.layer.num_pages, a.layer.Hkv, a.layer.page_shift, p.scores, p.ref, a.weights,
+                    a.decay};
   return launch_weights_add(add, dev, stream);
 }
 

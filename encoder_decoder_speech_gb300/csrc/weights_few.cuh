@@ -18,6 +18,35 @@ struct FewShared {
   int last;
 };
 
+// Whether the scores of sequences with few rows are kept, by all kThreads threads of a first kernel's block, which
+// leaves it for the kernels behind. (rule.ask)
+template <int kThreads>
+__device__ bool score_ask(const ScoreRule& rule, const PagedBatch& bt, int G, int Hkv, int cap, WorkScratch* sm) {
+  int chunks = 0;
+  for (int b = threadIdx.x; b < bt.B; b += kThreads) {
+    const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
+    const long long rows = static_cast<long long>(s.n) * G;
+    if (rows == 0 || rows > rule.max_rows) continue;
+    const long long n = static_cast<long long>(max(1, (min(s.kv, cap) + kFewKeys - 1) / kFewKeys)) * Hkv;
+    chunks = count_add(chunks, static_cast<int>(min(n, static_cast<long long>(kCountLimit))));
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) chunks = count_add(chunks, __shfl_xor_sync(0xffffffffu, chunks, off));
+  if ((threadIdx.x & 31) == 0) sm->scan[0][threadIdx.x >> 5] = chunks;
+  __syncthreads();
+  chunks = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) chunks = count_add(chunks, sm->scan[0][i]);
+  __syncthreads();
+  const bool kept = chunks <= rule.room;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *rule.word = kept ? 1u : 0u;
+  return kept;
+}
+// In the kernels behind.
+__device__ __forceinline__ bool scores_kept(const ScoreRule& rule) {
+  return rule.ask ? __ldcg(rule.word) != 0u : rule.kept;
+}
+
 // For a rescaling from reference m to `to`.
 __device__ __forceinline__ float few_rescale(float m, float to) {
   float y;
@@ -105,14 +134,14 @@ __device__ __forceinline__ void few_finish(FewShared* sm, const float (&m)[kScor
   if (write && tid < rows) refs[tid] = log_sum(M, L);
 }
 
-// Adds the weights of stored scores to W.
+// Adds the weights of stored scores to W, if there are any.
 struct WeightsAdd {
+  ScoreRule rule;
   PagedBatch batch;
   WorkShape shape;         // of the kernel that stored them
   int num_pages, Hkv, page_shift;
-  const float* scores;     // of chunk c, row r: [c * max_rows + r][kFewKeys]
+  const float* scores;     // of chunk c, row r: [c * rule.max_rows + r][kFewKeys]
   const float* ref;        // [Hkv][n_tokens][G]
-  int max_rows;
   float* W;
   float decay;
 };

@@ -15,6 +15,7 @@
 #include "ptx.cuh"
 #include "span_work.cuh"
 #include "weights.cuh"
+#include "weights_few.cuh"
 
 namespace cxa {
 namespace {
@@ -29,14 +30,19 @@ struct WeightsParams {
   float* W;
   float decay, qscale;
   unsigned int* counters;
-  float* ref;               // [n_tokens][Hq]
+  float* ref;               // [Hkv][n_tokens][G]
   float* part;              // [2 * grid][kRows][2]
   unsigned int* status;
   PagedBatch batch;
   PagedLayer layer;
   WorkShape shape;
-  int Hq;
+  ScoreRule rule;           // of the second pass: nothing to do if scores were kept
 };
+
+// The references of a head's rows.
+__device__ __forceinline__ float* refs_of(const WeightsParams& p, const PagedSeq& s, int h) {
+  return p.ref + (static_cast<size_t>(h) * p.batch.n_tokens + s.q0) * p.shape.G;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -174,11 +180,8 @@ __global__ void __launch_bounds__(kThreads) weights_ref_kernel(const __grid_cons
 #pragma unroll
       for (int off = 8; off >= 1; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
     }
-    auto put = [&](int r, float M_, float L_) {
-      const int at = row0 + r;
-      p.ref[static_cast<long long>(seq.q0 + at / G) * p.Hq + cur.h * G + at % G] =
-          L_ > 0.f || L_ != L_ ? M_ + log2f(L_) : INFINITY;
-    };
+    float* refs = refs_of(p, seq, cur.h) + row0;
+    auto put = [&](int r, float M_, float L_) { refs[r] = log_sum(M_, L_); };
     const bool whole = c0 == 0 && c1 == cur.nc;
     if (whole) {
       if (tx < 2 && 2 * ty + tx < rows) put(2 * ty + tx, tx == 0 ? M[0] : M[1], tx == 0 ? l[0] : l[1]);
@@ -225,9 +228,10 @@ __global__ void __launch_bounds__(kThreads) weights_sum_kernel(const __grid_cons
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const PagedBatch& bt = p.batch;
   const int Hkv = p.layer.Hkv, G = p.shape.G, cap = p.shape.cap;
+  if (scores_kept(p.rule)) return;
   auto key_tiles = [&](int b) {
     const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
-    return s.n == 0 ? 0 : (min(s.kv, cap) + kKeys - 1) / kKeys;
+    return work_rows(s, p.shape) == 0 ? 0 : (min(s.kv, cap) + kKeys - 1) / kKeys;
   };
   SpanRange range;
   if (!span_locate<kThreads>(bt.B, [&](int b) {
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) weights_sum_kernel(const __grid_cons
         const int at = row0 + 2 * ty + i;
         if (at >= all) continue;
         const int see = visible_keys(seq, at / G, cap);
-        const float ref = __ldcg(p.ref + static_cast<long long>(seq.q0 + at / G) * p.Hq + h * G + at % G);
+        const float ref = __ldcg(refs_of(p, seq, h) + at);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (ok[j] && key0 + tx + 16 * j < see) sum[j] += ex2(s[i][j] * p.qscale - ref);
@@ -293,28 +297,28 @@ __global__ void __launch_bounds__(kThreads) weights_sum_kernel(const __grid_cons
 }
 
 template <typename T, int kDh>
-cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch(const WeightsLaunch& a, const ScoreRule* rule, const DeviceInfo& dev, cudaStream_t stream) {
   WeightsParams p;
   p.q = a.q;
   p.q_stride = a.q_stride;
   p.W = a.weights;
   p.decay = a.decay;
   p.qscale = a.scale * 1.4426950408889634f;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  p.counters = reinterpret_cast<unsigned int*>(ws);
-  p.ref = reinterpret_cast<float*>(ws + kPagedCounterBytes);
-  p.part = reinterpret_cast<float*>(ws + kPagedCounterBytes + weights_ref_bytes(static_cast<long long>(a.batch.n_tokens) * a.Hq));
+  const WeightsPlaces at = weights_places(a);
+  p.counters = at.counters;
+  p.ref = at.ref;
+  p.part = at.part;
+  p.rule = rule != nullptr ? *rule : ScoreRule{};
   p.status = dev.status_word;
   p.batch = a.batch;
   p.layer = a.layer;
-  p.Hq = a.Hq;
   p.shape.G = a.Hq / a.layer.Hkv;
   p.shape.rows = kRows;
   p.shape.chunk_shift = 6;
   p.shape.coarse = false;
   p.shape.cap = a.batch.width << a.layer.page_shift;
   p.shape.min_rows = 0;
-  p.shape.max_rows = 0x7FFFFFFF;
+  p.shape.max_rows = rule != nullptr ? rule->max_rows : 0x7FFFFFFF;
   constexpr int smem = sizeof(Tiles<T, kDh>);
   static SmemOnce once[2];
   cudaError_t e = allow_smem(weights_ref_kernel<T, kDh>, smem, dev.device, &once[0]);
@@ -331,9 +335,11 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, weights_ref_kernel<T, kDh>, p);
-  if (e != cudaSuccess) return e;
-  count_launches(1);
+  if (rule == nullptr) {
+    e = cudaLaunchKernelEx(&cfg, weights_ref_kernel<T, kDh>, p);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+  }
   e = cudaLaunchKernelEx(&cfg, weights_sum_kernel<T, kDh>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
@@ -341,10 +347,10 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_weights_rows(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_weights_rows(const WeightsLaunch& a, const ScoreRule* rule, const DeviceInfo& dev, cudaStream_t stream) {
   using bf = __nv_bfloat16;
-  if (a.bf16) return a.dh == 64 ? launch<bf, 64>(a, dev, stream) : launch<bf, 128>(a, dev, stream);
-  return a.dh == 64 ? launch<float, 64>(a, dev, stream) : launch<float, 128>(a, dev, stream);
+  if (a.bf16) return a.dh == 64 ? launch<bf, 64>(a, rule, dev, stream) : launch<bf, 128>(a, rule, dev, stream);
+  return a.dh == 64 ? launch<float, 64>(a, rule, dev, stream) : launch<float, 128>(a, rule, dev, stream);
 }
 
 }  // namespace cxa

@@ -22,8 +22,7 @@
 //                        and key, against 2 dh bytes of the key itself).
 //   weights_add_kernel   (weights_few.cu) reads the scores back and adds the weights to W.
 // 64 single tokens, 32 heads on 8 of 128, over 287,000 keys: 124 us, 104 of them the first at 5.7 TB/s.
-// Where the scores might take more than kMaxScoreBytes the second pass is weights_sum_kernel, which reads K once
-// more.
+// Where the scores have no room, the second pass is weights_sum_kernel, which reads K once more (ScoreRule).
 //
 // Products of bf16 values are exact; sums, references and weights are fp32.
 #include <cuda.h>
@@ -53,8 +52,8 @@ struct WeightsParams {
   unsigned int* counters;
   float* ref;               // [Hkv][n_tokens][G]
   float* part;              // [2 * grid][rows][2]
-  float* scores;            // of chunk c, row r: [c * max_rows + r][kKeys], or null
-  int max_rows;
+  float* scores;            // of chunk c, row r: [c * rule.max_rows + r][kKeys]
+  ScoreRule rule;
   unsigned int* status;
   PagedBatch batch;
   int num_pages, Hkv, page_shift;
@@ -157,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
+  const bool kept = p.rule.ask ? score_ask<kThreads>(p.rule, bt, G, p.Hkv, shape.cap, &sm->work) : p.rule.kept;
+  if (!kept && p.rule.others) return;      // these sequences go with those of many
   if (!work_locate<kThreads, false>(bt, shape, p.Hkv, &sm->work, &range, &cur, p.status)) return;
   Waits w = {smem_u32(sm->bars), &sm->abort, p.status, true};
   if (tid == 0) {
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(w.bar(kSFree + buf));
         const bool gone = (bad >> (tid >> 4) & 1u) != 0 || key >= shape.cap;
         const bool edge = (c + 1) * kKeys > see_all;
-        float* to = p.scores != nullptr ? p.scores + static_cast<size_t>(cur.first + c) * p.max_rows * kKeys + tid : nullptr;
+        float* to = kept ? p.scores + static_cast<size_t>(cur.first + c) * p.rule.max_rows * kKeys + tid : nullptr;
         const int hidden = gone ? kRows : edge ? min(max(key - (seq.kv - seq.n), 0), kRows) * G : 0;
         float s[kRows];
 #pragma unroll
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   WorkRange range;
   WorkCursor cur;
   WorkShape shape = p.shape;
+  if (!scores_kept(p.rule)) shape.min_rows = 0;      // those of few rows too
   if (!work_locate<kThreads, false>(bt, shape, p.Hkv, &sm->work, &range, &cur, p.status)) return;
   Waits w = {smem_u32(sm->bars), &sm->abort, p.status, true};
   if (tid == 0) {
@@ -589,7 +591,9 @@ struct Unit {
   int t0, t1;              // tiles
 };
 
-template <int kDh>
+// kAsk: whether the scores of few rows were kept is for the first kernel to say. (In one kernel with the other case,
+// the products' loop was laid out worse: 148 us in place of 145.)
+template <int kDh, bool kAsk>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_sum_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ WeightsParams p) {
@@ -605,9 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // All units are numbered by (sequence, keys, head), and block c takes every grid-th of them: keys that few
   // rows see stand behind those that many do, so that all blocks get some of both.
+  WorkShape shape = p.shape;
+  if (kAsk && !scores_kept(p.rule)) shape.min_rows = 0;      // those of few rows too
   auto key_tiles = [&](int b) {
     const PagedSeq s = paged_seq(bt.q_start, bt.kv_len, b, bt.n_tokens);
-    return work_rows(s, p.shape) == 0 ? 0 : (min(s.kv, cap) + kKeys - 1) / kKeys;
+    return work_rows(s, kAsk ? shape : p.shape) == 0 ? 0 : (min(s.kv, cap) + kKeys - 1) / kKeys;
   };
   auto units_of = [&](int b) {
     const long long u = static_cast<long long>(key_tiles(b)) * p.Hkv;
@@ -839,8 +845,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace sum
 
-constexpr double kSplitChunks = 8192;
-
 template <int kDh>
 cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
   const int G = a.Hq / a.layer.Hkv, page_size = 1 << a.layer.page_shift;
@@ -859,16 +863,14 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.W = a.weights;
   p.decay = a.decay;
   p.qscale = a.scale * 1.4426950408889634f;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  p.counters = reinterpret_cast<unsigned int*>(ws);
-  ws += kPagedCounterBytes;
-  p.ref = reinterpret_cast<float*>(ws);
-  ws += weights_ref_bytes(static_cast<long long>(a.batch.n_tokens) * a.Hq);
-  p.part = reinterpret_cast<float*>(ws);
-  ws += kWeightsPartBytes;
-  const WeightsSplit split = weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, G, a.max_new);
-  p.scores = split.score_bytes != 0 ? reinterpret_cast<float*>(ws) : nullptr;
-  p.max_rows = split.few_rows;
+  const WeightsPlaces at = weights_places(a);
+  p.counters = at.counters;
+  p.ref = at.ref;
+  p.part = at.part;
+  p.scores = at.scores;
+  WeightsSplit split = weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, G, a.max_new);
+  p.rule = score_rule(split, at);
+  if (split.many && !p.rule.kept && !p.rule.ask) split.few_rows = 0;      // (no room at all)
   p.status = dev.status_word;
   p.batch = a.batch;
   p.num_pages = a.layer.num_pages;
@@ -886,15 +888,14 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.shape.rows = many::kTiles * (kTileRows / G * G);
   p.shape.min_rows = split.few_rows + 1;
   p.shape.max_rows = 0x7FFFFFFF;
-  WeightsParams sums = p;                   // without their scores, the few rows' weights too
-  if (split.few_rows > 0 && p.scores == nullptr) {
-    sums.shape.min_rows = 0;
-    if (!split.many) sums.shape.max_rows = split.few_rows;
-  }
-  static SmemOnce once[3];
+  WeightsParams sums = p;
+  if (!p.rule.kept && !p.rule.ask) sums.shape.min_rows = 0;      // without their scores, the few rows' weights too
+  if (!split.many) sums.shape.max_rows = split.few_rows;
+  static SmemOnce once[4];
   cudaError_t e = allow_smem(few::weights_few_kernel<kDh>, kSmemBytes, dev.device, &once[0]);
   if (e == cudaSuccess) e = allow_smem(many::weights_ref_kernel<kDh>, kSmemBytes, dev.device, &once[1]);
-  if (e == cudaSuccess) e = allow_smem(sum::weights_sum_kernel<kDh>, kSmemBytes, dev.device, &once[2]);
+  if (e == cudaSuccess) e = allow_smem(sum::weights_sum_kernel<kDh, false>, kSmemBytes, dev.device, &once[2]);
+  if (e == cudaSuccess) e = allow_smem(sum::weights_sum_kernel<kDh, true>, kSmemBytes, dev.device, &once[3]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int grid = dev.num_sms < kWeightsMaxBlocks ? dev.num_sms : kWeightsMaxBlocks;
@@ -919,34 +920,20 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
     cfg.blockDim = dim3(many::kThreads);
     if (!launched(cudaLaunchKernelEx(&cfg, many::weights_ref_kernel<kDh>, q, k, p))) return e;
   }
-  if (split.many || p.scores == nullptr) {
+  if (split.many || !p.rule.kept) {
     cfg.blockDim = dim3(sum::kThreads);
-    if (!launched(cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh>, q, k, sums))) return e;
+    if (!launched(p.rule.ask ? cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh, true>, q, k, sums)
+                             : cudaLaunchKernelEx(&cfg, sum::weights_sum_kernel<kDh, false>, q, k, sums)))
+      return e;
   }
-  if (p.scores != nullptr) {
-    WeightsAdd add = {p.batch, few.shape, p.num_pages, p.Hkv, p.page_shift, p.scores, p.ref, p.max_rows, p.W, p.decay};
+  if (split.few_rows > 0 && (p.rule.kept || p.rule.ask)) {
+    WeightsAdd add = {p.rule, p.batch, few.shape, p.num_pages, p.Hkv, p.page_shift, p.scores, p.ref, p.W, p.decay};
     e = launch_weights_add(add, dev, stream);
   }
   return e;
 }
 
 }  // namespace
-
-// Which sequences have few rows: all, where no sequence can have more than a product's 16; otherwise those of one
-// or two tokens (more would take room for scores that hardly any use), if their scores can be kept, there is more
-// than one sequence, and the keys are many enough to pay for two more launches. (20 single tokens beside 4
-// chunks of a prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 237 so; 5 tokens in each
-// of 16 sequences of up to 1500 keys of 8 heads: 39 us and 45.)
-WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new) {
-  const double chunks = weights_chunks(B, width, page_shift, Hkv);
-  WeightsSplit s;
-  s.many = static_cast<long long>(G) * max_new > few::kRows;
-  const int tokens = few::kRows / G < 2 ? few::kRows / G : 2;
-  s.few_rows = !s.many ? G * max_new : B == 1 || chunks < kSplitChunks ? 0 : tokens * G;
-  s.score_bytes = weights_score_bytes(B, width, page_shift, Hkv, s.few_rows);
-  if (s.many && s.score_bytes == 0) s.few_rows = 0;
-  return s;
-}
 
 cudaError_t launch_weights_tile(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {
   return a.dh == 64 ? launch<64>(a, dev, stream, msg) : launch<128>(a, dev, stream, msg);

@@ -121,6 +121,7 @@ SIGNATURES = {
                                          ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_void_p]),
     "cxa_paged_weights_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p] + [ctypes.c_int] * 5),
+    "cxa_paged_weights_room_bytes": (ctypes.c_size_t, [ctypes.c_void_p] + [ctypes.c_int] * 5),
     "cxa_paged_weights": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                          ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
@@ -438,6 +439,10 @@ def cxa_latent_expand(handle, layer, to, to_layer, B, from_, kv_len, page_table,
 
 def cxa_paged_weights_workspace_bytes(handle, B, n_tokens, max_new, max_pages, Hq) -> int:
     return load().cxa_paged_weights_workspace_bytes(handle, B, n_tokens, max_new, max_pages, Hq)
+
+
+def cxa_paged_weights_room_bytes(handle, B, n_tokens, max_new, max_pages, Hq) -> int:
+    return load().cxa_paged_weights_room_bytes(handle, B, n_tokens, max_new, max_pages, Hq)
 
 
 def cxa_paged_weights(handle, layer, B, n_tokens, max_new, q_start, kv_len, page_table, max_pages, q, q_stride, Hq,
@@ -1049,7 +1054,9 @@ class PagedCache(_Paged):
         [N, Hq, dh], of the pool's type, give each key, over the query heads of its K/V head; what it
         had gathered before counts decay times, and new tokens' entries start at zero. No page may be two
         sequences' of the batch. max_new and workspace as for attend, but a sequence with more new tokens
-        than max_new may be left out (cxa_device_status then says CXA_EINVAL). Returns weights."""
+        than max_new may be left out (cxa_device_status then says CXA_EINVAL). The kept workspace has room for the scores
+        of single tokens, 256 MB of them at most, as far as the table may need it; one of the caller's needs
+        cxa_paged_weights_workspace_bytes, and without that room keys are read twice. Returns weights."""
         tc = _torch_calls or _calls()
         at, dh, dt = self._at, self.dh, q.dtype
         B, width = self._batch(q_start, kv_len, page_table, tc.i32)
@@ -1058,7 +1065,7 @@ class PagedCache(_Paged):
         wp, code = self._weights(weights, tc.f32), _code(tc, dt)
         raw = tc.stream(at) if stream is None else _stream(stream)
         if workspace is None:
-            need = self._need((self.handle, B, n, max_new, width, Hq), cxa_paged_weights_workspace_bytes)
+            need = self._need((self.handle, B, n, max_new, width, Hq), cxa_paged_weights_room_bytes)
             ws = self._kept(tc, need, stream, raw)
         else:
             ws = self._given(workspace)

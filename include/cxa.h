@@ -488,10 +488,14 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  *   weights    device fp32 [L][num_pages][Hkv][page_size], 4-byte aligned: one number for each row
  *              of K. Entries of no key of the batch are left as they are.
  *   decay      finite, >= 0; with 0 nothing of the old numbers is read into the new.
- *   workspace  at least cxa_paged_weights_workspace_bytes() bytes (0 for unsupported arguments; the
- *              scores of single tokens are in it, if they take 256 MB at most), otherwise as for
+ *   workspace  at least cxa_paged_weights_workspace_bytes() bytes (0 for unsupported arguments), otherwise as for
  *              cxa_paged_attention, whose workspace may be the same buffer (its first
- *              CXA_PAGED_COUNTER_BYTES are the same counters).
+ *              CXA_PAGED_COUNTER_BYTES are the same counters). Sequences of few new tokens leave their scores in it,
+ *              4 bytes for each key (in chunks of 128), K/V head and query row: the least size has room for them if
+ *              a table of that width can need 256 MB at most. In wider tables what a call needs goes by its keys:
+ *              the scores are kept if what there is beyond the least size, 256 MB of it at most, holds them, and
+ *              K is read twice otherwise (the weights then differ by their rounding).
+ *              cxa_paged_weights_room_bytes() is the size with all the room that a call makes use of.
  * Pages that two sequences of the batch share must not be given: their entries would be written by
  * both. Arguments, the limit on the work and errors otherwise as for cxa_paged_attention; dtype is
  * the pool's. A token that sees an infinity or a NaN in q or K may make the weights of all keys that
@@ -500,6 +504,9 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  */
 CXA_API size_t cxa_paged_weights_workspace_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new,
                                                  int max_pages, int Hq);
+
+CXA_API size_t cxa_paged_weights_room_bytes(const cxa_pages* pages, int B, int n_tokens, int max_new, int max_pages,
+                                            int Hq);
 
 CXA_API int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, int max_new, const int* q_start,
                               const int* kv_len, const int* page_table, int max_pages, const void* q,

@@ -665,3 +665,40 @@ def test_evict_in_wide_tables(positions):
                 assert torch.equal(kept[l, s, h, :m], want) and bool((kept[l, s, h, m:] == -1).all())
                 j = torch.arange(m)
                 assert torch.equal(K[l][out[s][j // page].long(), h, j % page], before[l][p[want], h, at[want]])
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [[1, 1, 0, 2], [3, 40, 1, 2]])
+def test_a_wide_table_changes_nothing(n, pool):
+    """Whether scores are kept is by the keys. (Whether single tokens beside prompts go a way of their own, which rounds
+    differently, is by the table.)"""
+    b = Batch(n, [700, 5000, 30, 2], 64, 4, 2, 128, pool, seed=6).fill()
+    before = b.W.clone()
+    want = b.accumulate(decay=0.5).clone()
+    b.close(before, want, decay=0.5)
+    b.d["page_table"] = torch.cat([b.table, torch.full((4, 1 << 20), -1, dtype=torch.int32)], 1).cuda()
+    b.W.copy_(before)
+    got = b.accumulate(decay=0.5)
+    b.close(before, got, decay=0.5)
+    assert torch.equal(got, want) or (pool == "bf16" and max(n) > 2)
+
+
+@pytest.mark.parametrize("pool, n, more", [("bf16", [1, 1, 0, 2], 0), ("f32", [1, 1, 0, 2], 0), ("bf16", [1, 40, 2, 1], 21)])
+def test_scores_that_a_workspace_has_room_for_or_not(pool, n, more):
+    """In a wide table scores are kept in what the workspace has beyond its least size, if it holds all of them."""
+    kv = [70000, 5000, 66000, 2] if more else [700, 5000, 30, 2]
+    Hq, Hkv = (2 * more, more) if more else (4, 2)
+    b = Batch(n, kv, 256, Hq, Hkv, 64, pool, seed=6).fill()
+    b.d["page_table"] = torch.cat([b.table, torch.full((4, 1 << 20), -1, dtype=torch.int32)], 1).cuda()
+    least = cxa.cxa_paged_weights_workspace_bytes(b.cache.handle, 4, b.N, b.max_new, b.d["page_table"].shape[1], Hq)
+    before = b.W.clone()
+    few = [k for m, k in zip(n, kv) if 1 <= m <= 2]
+    chunks, rows = sum(-(-k // 128) for k in few) * Hkv, 2 * (Hq // Hkv)
+    for room in (chunks, chunks - 1, 0, 1):
+        ws = torch.zeros(least + room * rows * 512 + (1 << 12), dtype=torch.uint8, device="cuda")
+        ws[cxa.CXA_PAGED_COUNTER_BYTES:] = 255
+        size = least + room * rows * 512
+        b.W.copy_(before)
+        b.accumulate(workspace=ws[:size])
+        b.close(before, b.W)
+        assert bool((ws[size:] == 255).all())

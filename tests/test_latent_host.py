@@ -276,3 +276,12 @@ def test_python_refusals_without_a_device():
     for kw in (dict(latent=100), dict(rope=8), dict(page_size=20)):
         with pytest.raises(cxa.CxaError):
             cxa.LatentCache(**dict(dict(num_pages=4, page_size=16, L=1, latent=128, rope=16, device="cpu"), **kw))
+
+
+def test_room_for_scores(pages):
+    """The least workspace has room for the scores of tables that can need 256 MB; in wider ones room is the caller's."""
+    least, room = cxa.cxa_paged_weights_workspace_bytes, cxa.cxa_paged_weights_room_bytes
+    assert room(pages, 2, 2, 1, 80, 8) == least(pages, 2, 2, 1, 80, 8)
+    assert room(pages, 64, 64, 1, 1 << 16, 8) == least(pages, 64, 64, 1, 1 << 16, 8) + (256 << 20)
+    assert room(pages, 1, 2000, 2000, 1 << 16, 8) == least(pages, 1, 2000, 2000, 1 << 16, 8)      # no sequence of few rows
+    assert room(pages, 1, 1, 1, 3, 6) == 0 and room(None, 1, 1, 1, 3, 8) == 0
