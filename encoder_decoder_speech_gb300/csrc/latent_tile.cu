@@ -9,8 +9,9 @@
 // of 128 channels by kR columns, where O would not leave room for S. The keys' rows are read by both products
 // from the one copy in shared memory, along the channels in the first and across them in the second.
 //
-//  * warp 6 streams the keys' rows by TMA into a ring of 16 KB units: 128 channels of 64 keys (the
-//    rotated part takes a unit of its own). A unit comes back as soon as P.V has read it. It also copies an item's
+//  * warp 6 streams the keys' rows by TMA into two rings: 128 latent channels of 64 keys, 16 KB, a unit, which comes
+//    back as soon as P.V has read it, and the rotated part's 8 KB, which the scores alone need. (One ring, where the
+//    rotated part took a unit: 84 us for 64 heads over 262,144 keys, 72 so.) It also copies an item's
 //    queries, where tokens' rows stand one behind the other (the softmax warps do, otherwise).
 //  * warps 4 and 5 issue the products, one the scores, as units come, the other P.V: each waits for what it
 //    needs alone (one warp for both, scores first: 112 us for 64 single tokens over 287,000 keys of 20 heads).
@@ -20,13 +21,15 @@
 //
 // Work is dealt out in steps of 64 keys (paged_work.cuh); items that a block boundary cuts are merged
 // by latent_merge.cu. Bound by memory: a row of 1152 bytes is read once for the tile's rows. Measured, both
-// kernels: 64 single tokens over 287,000 keys of 20 heads, 512 + 64 channels, 72 us (4.5 TB/s: the merge is 5 to 8 of
+// kernels: 64 single tokens over 276,698 keys of 20 heads, 512 + 64 channels, 72 us (4.5 TB/s: the merge is 5 to 8 of
 // them, the start 3, and an item's beginning and end are not covered by copies of the next); one token of 64 heads
-// over 262,144 keys 72 us (4.2 TB/s: 64 rows leave a ring of 9 units, less than two steps, so that copies wait for
-// P.V); one token over 448 keys of 256 channels, 8 heads, 12 us, latency.
+// over 262,144 keys 72 us (4.2 TB/s: 64 rows leave rings of two steps, so that copies wait for P.V); one token over
+// 448 keys of 256 channels, 8 heads, 12 us, latency.
 //
-// P is rounded to one bf16 value (an error of up to 2^-8 of each weight, of either sign, as the bf16 output
-// has itself); sums, references and O are fp32, the sums of the values before rounding.
+// P is taken as two bf16 values (an error of up to 2^-16 of each weight), so that the output's own rounding is
+// the only one that shows: with one, the error of single tokens' outputs was 1.9e-3 to 2.0e-3 in place of 1.7e-3. P.V
+// then takes twice the products, which the reading of keys covers: 64 tokens over 276,698 keys 71.3 -> 72.3 us. Sums,
+// references and O are fp32.
 //
 // Rows of keys behind an item's last visible one, and those of a page outside the pool, weigh 0 and are
 // zeroed in shared memory before P.V, as they may hold anything. If a key that some rows see and others do
@@ -50,7 +53,7 @@ constexpr int kThreads = (kTmaWarp + 1) * 32;
 constexpr int kKeys = 64, kChunkShift = 6;
 constexpr int kUnitBytes = 16384;            // 128 channels of 64 keys
 constexpr int kHalf = kUnitBytes / 2;        // 64 channels
-constexpr int kMaxUnits = 13;
+constexpr int kMaxUnits = 12, kMaxRopes = 8;
 constexpr int kSmemBytes = 232448;
 constexpr float kMoveLog2 = 8.f;
 
@@ -63,7 +66,9 @@ enum Bars {
   kPvDone = 7,
   kUFull = 8,
   kUEmpty = kUFull + kMaxUnits,
-  kBars = kUEmpty + kMaxUnits
+  kRFull = kUEmpty + kMaxUnits,
+  kREmpty = kRFull + kMaxRopes,
+  kBars = kREmpty + kMaxRopes
 };
 
 struct Small {
@@ -90,7 +95,7 @@ struct TileParams {
   unsigned int* status;
   PagedBatch batch;
   int num_pages, page_shift, latent, rope;
-  int units;                   // of the ring
+  int units, ropes;            // of the rings: of 128 latent channels, and of the rotated part
   int q_packed;                // queries stand one behind the other: copied by their map
   WorkShape shape;
 };
@@ -151,6 +156,8 @@ __device__ __forceinline__ uint32_t p_piece(int key, int piece) {
   return static_cast<uint32_t>(key * (2 * kR) + ((piece ^ x) << 4));
 }
 template <int kR>
+constexpr int kPartBytes = kKeys * kR * 2;      // the low part stands behind the high one
+template <int kR>
 constexpr uint64_t p_desc_high() {
   constexpr uint32_t layout = kR == 64 ? 2u : kR == 32 ? 4u : 6u;      // 128-, 64-, 32-byte swizzle
   return static_cast<uint64_t>((8u * 2 * kR) >> 4 | 1u << 14 | layout << 29) << 32;
@@ -163,9 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int quads = p.latent / 128, blocks = 2 * quads + (p.rope > 0 ? 1 : 0);      // of 64 channels
-  const int per = quads + (p.rope > 0 ? 1 : 0);                                     // units a step
-  const int NU = p.units;
-  const uint32_t u_base = base, q_base = u_base + NU * kUnitBytes, p_base = q_base + blocks * (kR * 128);
+  const int NU = p.units, NR = p.ropes;
+  const uint32_t u_base = base, r_base = u_base + NU * kUnitBytes, q_base = r_base + NR * kHalf;
+  const uint32_t p_base = q_base + blocks * (kR * 128);
   Small* sm = reinterpret_cast<Small*>(smem + kSmemBytes - kSmallBytes);
   auto bar = [&](int i) { return smem_u32(&sm->bars[i]); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -242,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_global();
     const int box_shift = min(p.page_shift, kChunkShift), box_rows = 1 << box_shift;      // keys a box
     const int boxes = kKeys >> box_shift, box = lane % boxes, blk = lane / boxes;
-    int pos = 0, step = 0, item = 0, q_sent = -1;
+    int pos = 0, r_pos = 0, step = 0, item = 0, q_sent = -1;
     uint32_t round = 0, armed = 0, parity = 0;      // units copies were sent to, and the phase
+    uint32_t r_round = 0, r_armed = 0, r_parity = 0;
     for (bool more = true; more && ok; ++item) {
       const Part t = part_of(cur);
       if (p.q_packed) {
@@ -275,9 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lows = (1u << boxes) - 1u;                  // a lane a box
         const uint32_t good = __ballot_sync(0xffffffffu, page >= 0) & lows;
         const uint32_t bad = __ballot_sync(0xffffffffu, page == -1) & lows;
-        for (int u = 0; u < per; ++u) {
+        for (int u = 0; u < quads; ++u) {
           if (!wait_warp(kUEmpty + pos, (round & 1) ^ 1)) break;
-          const int n = u < quads ? 2 : 1;                         // blocks of the unit
           if (lane == 0) {
             if (u == 0) {
               uint32_t groups = 0;       // of 16 keys
@@ -286,18 +293,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               sm->bad[step & 15] = groups;
               if (bad != 0) atomicOr(p.status, kStatusBadPage);
             }
-            mbar_arrive_expect_tx(bar(kUFull + pos), static_cast<uint32_t>(__popc(good) * n * box_rows * 128));
+            mbar_arrive_expect_tx(bar(kUFull + pos), static_cast<uint32_t>(__popc(good) * 2 * box_rows * 128));
           }
           __syncwarp();
-          if (blk < n && page >= 0)
+          if (blk < 2 && page >= 0)
             tma_load_3d(u_base + pos * kUnitBytes + blk * kHalf + box * box_rows * 128, &tmC, bar(kUFull + pos),
                         u * 128 + blk * 64, y, page);
-          if (kAhead > 0 && blk < n && pages[kAhead] >= 0) tma_prefetch_3d(&tmC, u * 128 + blk * 64, y_ahead, pages[kAhead]);
+          if (kAhead > 0 && blk < 2 && pages[kAhead] >= 0) tma_prefetch_3d(&tmC, u * 128 + blk * 64, y_ahead, pages[kAhead]);
           armed |= 1u << pos;
           parity = (parity & ~(1u << pos)) | (round & 1u) << pos;
           if (++pos == NU) {
             pos = 0;
             ++round;
+          }
+        }
+        if (NR > 0 && ok && wait_warp(kREmpty + r_pos, (r_round & 1) ^ 1)) {
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(kRFull + r_pos), static_cast<uint32_t>(__popc(good) * box_rows * 128));
+          __syncwarp();
+          if (blk == 0 && page >= 0)
+            tma_load_3d(r_base + r_pos * kHalf + box * box_rows * 128, &tmC, bar(kRFull + r_pos), p.latent, y, page);
+          if (kAhead > 0 && blk == 0 && pages[kAhead] >= 0) tma_prefetch_3d(&tmC, p.latent, y_ahead, pages[kAhead]);
+          r_armed |= 1u << r_pos;
+          r_parity = (r_parity & ~(1u << r_pos)) | (r_round & 1u) << r_pos;
+          if (++r_pos == NR) {
+            r_pos = 0;
+            ++r_round;
           }
         }
       }
@@ -307,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {      // the copies under way land before the block ends
       for (int b = 0; b < NU; ++b)
         if (armed & (1u << b)) mbar_wait(bar(kUFull + b), (parity >> b) & 1u);
+      for (int b = 0; b < NR; ++b)
+        if (r_armed & (1u << b)) mbar_wait(bar(kRFull + b), (r_parity >> b) & 1u);
       if (q_sent >= 0) mbar_wait(bar(kQFull), static_cast<uint32_t>(q_sent) & 1u);
     }
   } else if (warp == kSWarp) {
@@ -316,15 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc = make_idesc(1u, kKeys, kR);
     constexpr uint64_t hi = desc_high(1024);
     const uint32_t ub = __shfl_sync(0xffffffffu, u_base, 0), qb = __shfl_sync(0xffffffffu, q_base, 0);
-    int pos = 0, item = 0, step = 0;
-    uint32_t round = 0;
+    const uint32_t rb = __shfl_sync(0xffffffffu, r_base, 0);
+    int pos = 0, r_pos = 0, item = 0, step = 0;
+    uint32_t round = 0, r_round = 0;
     for (bool more = true; more && ok; ++item) {
       const Part t = part_of(cur);
       if (!wait_warp(kQFull, item & 1)) break;
       for (int s = t.s0; s < t.s1 && ok; ++s, ++step) {
         if (!wait_warp(kSFree + (step & 1), ((step >> 1) & 1) ^ 1)) break;
         const uint32_t d = tmem + __shfl_sync(0xffffffffu, step & 1, 0) * kR;
-        for (int u = 0; u < per; ++u) {
+        for (int u = 0; u < quads; ++u) {
           if (!wait_warp(kUFull + pos, round & 1)) break;
           tc_fence_after();
           const int at = __shfl_sync(0xffffffffu, pos, 0), un = __shfl_sync(0xffffffffu, u, 0);
@@ -334,14 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)       // 16 channels: 32 bytes
               mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, k != 0 ? 1u : acc);
-            if (un < quads) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16(d, hi | (al + (kHalf >> 4) + 2 * k), hi | (bl + (kR * 128 >> 4) + 2 * k), idesc, 1u);
-            } else {
-              tc_commit(bar(kUEmpty + at));      // P.V has no use for the rotated part
-            }
-            if (un + 1 == per) {
+            for (int k = 0; k < 4; ++k)
+              mma_bf16(d, hi | (al + (kHalf >> 4) + 2 * k), hi | (bl + (kR * 128 >> 4) + 2 * k), idesc, 1u);
+            if (NR == 0 && un + 1 == quads) {
               tc_commit(bar(kSFull + (step & 1)));
               if (s + 1 == t.s1) tc_commit(bar(kQEmpty));
             }
@@ -350,6 +370,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++pos == NU) {
             pos = 0;
             ++round;
+          }
+        }
+        if (NR > 0 && ok && wait_warp(kRFull + r_pos, r_round & 1)) {
+          tc_fence_after();
+          const int at = __shfl_sync(0xffffffffu, r_pos, 0);
+          const uint32_t al = desc_low(rb + at * kHalf, 16), bl = desc_low(qb + quads * (2 * kR * 128), 16);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_bf16(d, hi | (al + 2 * k), hi | (bl + 2 * k), idesc, 1u);
+            tc_commit(bar(kREmpty + at));      // P.V has no use for the rotated part
+            tc_commit(bar(kSFull + (step & 1)));
+            if (s + 1 == t.s1) tc_commit(bar(kQEmpty));
+          }
+          __syncwarp();
+          if (++r_pos == NR) {
+            r_pos = 0;
+            ++r_round;
           }
         }
       }
@@ -377,14 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t al = desc_low(ub + at * kUnitBytes, kHalf), d = tmem + Tm<kR>::o + un * kR;
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)       // 16 keys: 2048 bytes of the rows, 32 kR of P
-              mma_bf16(d, hi | (al + k * (2048 >> 4)), p_hi | (pl + k * ((32 * kR) >> 4)), idesc, k != 0 ? 1u : acc);
+            for (int k = 0; k < 2 * (kKeys / 16); ++k)       // 16 keys: 2048 bytes of the rows, 32 kR of a part of P
+              mma_bf16(d, hi | (al + k % (kKeys / 16) * (2048 >> 4)), p_hi | (pl + k * ((32 * kR) >> 4)), idesc,
+                       k != 0 ? 1u : acc);
             tc_commit(bar(kUEmpty + at));
             if (un + 1 == quads) tc_commit(bar(kPvDone));
           }
           __syncwarp();
         }
-        pos += per;
+        pos += quads;
         if (pos >= NU) pos -= NU;
       }
       more = !t.last;
@@ -460,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // this warp's 16 keys' rows in shared memory: 8 lanes a row of 64 channels, four rows at a time
           const int sub = lane >> 3;
           auto each_piece = [&](auto body) {
-            int at = step * per % NU, round = step * per / NU;
+            int at = step * quads % NU, round = step * quads / NU;
             for (int u = 0; u < quads; ++u) {
               wait_warp(kUFull + at, round & 1);      // (it has come: the products have read it)
               const uint32_t to = u_base + at * kUnitBytes + (warp * 16 + sub) * 128 + (lane & 7) * 16;
@@ -542,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           soft_sync();
         }
         // ---- weights
-        uint32_t w[XN / 2];        // pairs of columns: w[2 j] of the first key, w[2 j + 1] of the second
+        uint32_t w[2][XN / 2];     // parts; pairs of columns: w[.][2 j] of the first key, w[.][2 j + 1] of the second
 #pragma unroll
         for (int j = 0; j < CN / 2; ++j) {
           const float2 ref = make_float2(m[2 * j] == -INFINITY ? 0.f : -m[2 * j], m[2 * j + 1] == -INFINITY ? 0.f : -m[2 * j + 1]);
@@ -552,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float b = ex2(fmaf(__uint_as_float(x[4 * j + 2 * e + 1]), p.qscale, ref.y));
             l[2 * j] += a;
             l[2 * j + 1] += b;
-            w[2 * j + e] = pack_bf16(a, b);
+            w[0][2 * j + e] = pack_bf16(a, b);
+            w[1][2 * j + e] = pack_bf16(a - __uint_as_float(w[0][2 * j + e] << 16), b - __uint_as_float(w[0][2 * j + e] & 0xFFFF0000u));
           }
         }
         // P's place and O are free once the previous P.V has run
@@ -574,8 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < CN / 2; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int key = warp * 16 + g + 8 * e;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_base + p_piece<kR>(key, j) + 4 * tq), "r"(w[2 * j + e]) : "memory");
+            const uint32_t at = p_base + p_piece<kR>(warp * 16 + g + 8 * e, j) + 4 * tq;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + part * kPartBytes<kR>), "r"(w[part][2 * j + e]) : "memory");
           }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -685,8 +726,12 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   p.page_shift = a.layer.page_shift;
   p.latent = a.layer.latent;
   p.rope = a.layer.rope;
-  const int blocks = a.layer.latent / 64 + (a.layer.rope > 0 ? 1 : 0);
-  const int units = (kSmemBytes - kSmallBytes - blocks * kR * 128 - kKeys * kR * 2) / kUnitBytes;
+  // the rings hold the same number of steps, as far as they can
+  const int quads = a.layer.latent / 128, blocks = 2 * quads + (a.layer.rope > 0 ? 1 : 0);
+  const int room = kSmemBytes - kSmallBytes - blocks * kR * 128 - 2 * kPartBytes<kR>;
+  const int steps = room / (quads * kUnitBytes + (a.layer.rope > 0 ? kHalf : 0));
+  p.ropes = a.layer.rope == 0 ? 0 : steps < 1 ? 1 : steps > kMaxRopes ? kMaxRopes : steps;
+  const int units = (room - p.ropes * kHalf) / kUnitBytes;
   p.units = units < kMaxUnits ? units : kMaxUnits;
   p.q_packed = q_packed ? 1 : 0;
   p.shape.G = a.H;

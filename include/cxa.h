@@ -603,6 +603,7 @@ CXA_API size_t cxa_latent_attention_workspace_bytes(int H, int latent, int max_n
  *              known here, so there is no default).
  *   workspace  256-byte aligned. Calls that share one must be ordered on one stream.
  * (B + n_tokens * H / 16) * (max_pages * page_size / 32 + 1) must be below 2^31.
+ * Softmax weights are taken as two bf16 values in bf16 pools; all sums are fp32.
  * Hidden positions, rows that see no key, and values that are not finite as for
  * cxa_paged_attention. Results do not change from call to call.
  */

@@ -568,3 +568,14 @@ def test_expand_reports_positions_behind_the_row_of_the_table(pool):
     for kv, start, status in (([97, 0], [97, 0], cxa.CXA_OK), ([97, 0], [96, 0], cxa.CXA_EPAGE),
                               ([0, 2 ** 31 - 1], [0, 97], cxa.CXA_EPAGE), ([96, 96], [-5, 500], cxa.CXA_OK)):
         assert call(kv, start, narrow) == status
+
+
+@pytest.mark.parametrize("H, latent, rope", [(8, 256, 0), (20, 512, 64), (64, 512, 64), (128, 128, 16), (40, 384, 32)])
+def test_bf16_weights_are_two_values(H, latent, rope):
+    """As in `close`, but for the softmax weights' rounding: to two bf16 values, 2^-8 of 2^-8, whose products add
+    2^-23 for each 16 keys of either. (To one, a sum of few values of either sign is off by up to 2^-8 of their magnitudes.)"""
+    b = Batch([1, 1, 3, 1], [5, 30, 70, 2000], 64, H, latent, rope, "bf16", seed=H).fill(float("nan"))
+    got, (out, A, big) = b.attend().cpu(), b.reference()
+    e = 2.0 ** -16 + 2.0 ** -21 + (2 * 2000 / 16 + 64) * 2.0 ** -23 + 2 * (b.width / 16 + 1) * 2.0 ** -23 * big
+    over = (got.double() - out).abs() - U[got.dtype] * out.abs() - e * A
+    assert float(over.max()) <= 0
