@@ -579,3 +579,35 @@ def test_bf16_weights_are_two_values(H, latent, rope):
     e = 2.0 ** -16 + 2.0 ** -21 + (2 * 2000 / 16 + 64) * 2.0 ** -23 + 2 * (b.width / 16 + 1) * 2.0 ** -23 * big
     over = (got.double() - out).abs() - U[got.dtype] * out.abs() - e * A
     assert float(over.max()) <= 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+@pytest.mark.parametrize("H, n", [(16, 1), (8, 4), (64, 1), (20, 3)])
+def test_every_key_of_a_long_context_counts(pool, H, n):
+    """Items cut between many blocks. Each run of 64 keys has a channel of its own (or one of two), and weights rise
+    along the context, so that a part that is lost, taken twice or misweighted moves a channel by a large share of it."""
+    kv, latent, rope = 40000, 512, 64
+    b = Batch([n], [kv], 128, H, latent, rope, pool, seed=H)
+    at = torch.arange(kv)
+    C = b.C[0].float() * 0.01
+    C[at, (at // 64) % latent] += 8.0
+    C[:, latent] = torch.linspace(0, 8, kv)
+    q = b.q.float() * 0.05
+    q[:, :, latent] = 8.0
+    b.C[0], b.q = C.to(DT[pool]), q.to(DT[pool])
+    b.fill(float("inf"))
+    got, (out, A, big) = b.attend().cpu(), b.reference()
+    if pool == "f32":
+        e = 2.0 ** -21 + (kv + 64) * 2.0 ** -24 + 2 * 23 * 2.0 ** -24 * big
+    else:
+        e = 2.0 ** -16 + 2.0 ** -21 + (2 * kv / 16 + 64) * 2.0 ** -23 + 2 * (b.width / 16 + 1) * 2.0 ** -23 * big
+    bound = U[got.dtype] * out.abs() + e * A
+    assert float(((got.double() - out).abs() - bound).max()) <= 0
+    # what the bound would see: the result without some run of 64 keys, or with a run twice
+    for run in (0, 77, 300, 624):
+        keys = b.C[0][64 * run:64 * run + 64].double()
+        logits = b.q.double() @ b.C[0].double().T * b.scale
+        p = torch.softmax(logits[0], -1)[:, 64 * run:64 * run + 64]          # the first token's
+        for times in (-1, 1):
+            wrong = (out[0] + times * p @ keys[:, :latent]) / (1 + times * p.sum(-1, keepdim=True))
+            assert bool(((wrong - out[0]).abs() > 4 * bound[0]).any(-1).all())
