@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kThreads) latent_merge_kernel(const __grid_con
 cudaError_t launch_latent_merge(const LatentAttnLaunch& a, int R, int blocks, const DeviceInfo& dev,
                                 cudaStream_t stream) {
   MergeParams p;
-  p.cut = static_cast<const LatentCut*>(a.workspace);
-  p.part = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kLatentCutBytes);
+  p.cut = latent_cuts(a.workspace);
+  p.part = latent_part(a.workspace);
   p.out = a.out;
   p.o_stride = a.o_stride;
   p.blocks = blocks;

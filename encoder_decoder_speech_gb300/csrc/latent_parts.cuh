@@ -19,14 +19,22 @@ struct LatentCut {
   int q0, rt, parts, rows;     // of the item: first token row, tile, parts (0: none), rows of the tile
 };
 
+// In the workspace: room that stands for the counters of the paged attention's, which must stay as they are where a
+// caller has one buffer for both, the cuts, and the partial states.
 constexpr size_t kLatentCutBytes = kLatentMaxBlocks * sizeof(LatentCut);
-static_assert(kLatentCutBytes % 256 == 0, "the partial states behind are aligned");
+static_assert((kPagedCounterBytes + kLatentCutBytes) % 256 == 0, "the partial states behind are aligned");
+inline LatentCut* latent_cuts(void* workspace) {
+  return reinterpret_cast<LatentCut*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes);
+}
+inline float* latent_part(void* workspace) {
+  return reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes + kLatentCutBytes);
+}
 
 // A partial state: [R][latent] sums, then R references (base 2) and R sums of weights.
 __host__ __device__ constexpr size_t latent_slot(int R, int latent) { return static_cast<size_t>(R) * (latent + 2); }
 
 inline size_t latent_parts_bytes(int R, int latent, int blocks) {
-  return kLatentCutBytes + 2 * static_cast<size_t>(blocks) * latent_slot(R, latent) * 4;
+  return kPagedCounterBytes + kLatentCutBytes + 2 * static_cast<size_t>(blocks) * latent_slot(R, latent) * 4;
 }
 // Blocks an SM of the fp32 kernel, and the most that a kernel of so many an SM runs.
 constexpr int latent_rows_blocks(int latent) { return latent <= 256 ? 2 : 1; }

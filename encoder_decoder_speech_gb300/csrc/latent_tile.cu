@@ -718,8 +718,8 @@ cudaError_t launch(const LatentAttnLaunch& a, const DeviceInfo& dev, cudaStream_
   p.q_stride = a.q_stride;
   p.o_stride = a.o_stride;
   p.qscale = a.scale * 1.4426950408889634f;
-  p.cut = static_cast<LatentCut*>(a.workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kLatentCutBytes);
+  p.cut = latent_cuts(a.workspace);
+  p.part = latent_part(a.workspace);
   p.status = dev.status_word;
   p.batch = a.batch;
   p.num_pages = a.layer.num_pages;

@@ -601,7 +601,8 @@ CXA_API size_t cxa_latent_attention_workspace_bytes(int H, int latent, int max_n
  *   max_new    an upper bound of the new tokens of any one sequence, as for cxa_paged_attention.
  *   scale      > 0 and finite, log2(e) times it too (the heads' width before the projections is not
  *              known here, so there is no default).
- *   workspace  256-byte aligned. Calls that share one must be ordered on one stream.
+ *   workspace  256-byte aligned. Calls that share one must be ordered on one stream; they may be calls of
+ *              cxa_paged_attention and cxa_paged_weights too, whose counters it leaves as they are.
  * (B + n_tokens * H / 16) * (max_pages * page_size / 32 + 1) must be below 2^31.
  * Softmax weights are taken as two bf16 values in bf16 pools; all sums are fp32.
  * Hidden positions, rows that see no key, and values that are not finite as for

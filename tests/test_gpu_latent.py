@@ -611,3 +611,32 @@ def test_every_key_of_a_long_context_counts(pool, H, n):
         for times in (-1, 1):
             wrong = (out[0] + times * p @ keys[:, :latent]) / (1 + times * p.sum(-1, keepdim=True))
             assert bool(((wrong - out[0]).abs() > 4 * bound[0]).any(-1).all())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "f32"])
+def test_one_workspace_for_calls_of_both_caches(pool):
+    """One buffer, cleared once, for latent attention, paged attention and gathered weights in turn."""
+    b = Batch([1, 4], [9000, 700], 64, 20, 512, 64, pool).fill()
+    kv = cxa.PagedCache(200, 64, 1, 2, 64, pool)
+    for i, x in enumerate((kv.Kp, kv.Vp)):
+        x.copy_(randn(*x.shape, seed=i))
+    d = dict(b.d, page_table=torch.arange(180, dtype=torch.int32, device="cuda").view(1, 180).repeat(2, 1))
+    d["page_table"][1] += 20
+    d["kv_len"] = torch.tensor([180 * 64, 300], dtype=torch.int32, device="cuda")
+    d["page_table"][1, 5:] = -1
+    d["page_table"][1, :5] = torch.arange(190, 195, dtype=torch.int32)
+    q = randn(5, 8, 64, seed=3, dtype=DT[pool]).cuda()
+    W = kv.new_weights()
+    want = kv.attend(0, q, **d, max_new=4), kv.accumulate(0, q, **d, max_new=4, weights=W, decay=0.0).clone(), b.attend()
+    code = {"bf16": cxa.CXA_BF16, "f32": cxa.CXA_F32}[pool]
+    ws = torch.zeros(max(cxa.cxa_latent_attention_workspace_bytes(20, 512, 4, code),
+                         cxa.cxa_paged_attention_workspace_bytes(8, 2, 64, 4),
+                         cxa.cxa_paged_weights_workspace_bytes(kv.handle, 2, 5, 4, 180, 8)), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(b.attend(workspace=ws), want[2])
+        assert torch.equal(kv.attend(0, q, **d, max_new=4, workspace=ws), want[0])
+        assert torch.equal(b.attend(workspace=ws), want[2])
+        W.fill_(float("nan"))
+        kv.accumulate(0, q, **d, max_new=4, weights=W, decay=0.0, workspace=ws)
+        assert torch.equal(W.nan_to_num(0), want[1])
+    assert not bool(ws[:cxa.CXA_PAGED_COUNTER_BYTES].any())
