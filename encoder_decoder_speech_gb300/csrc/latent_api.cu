@@ -295,9 +295,8 @@ int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, in
     rc = check_workspace(w, workspace, workspace_bytes,
                          cxa_paged_weights_workspace_bytes(pages, B, n_tokens, max_new, max_pages, Hq));
     if (rc != CXA_OK) return rc;
-    const double tiles = static_cast<double>(B) + static_cast<double>(n_tokens) * (Hq / pages->Hkv) / 16.0;
-    const double chunks = static_cast<double>((static_cast<long long>(max_pages) << pages->page_shift) / 64 + 1);
-    if (tiles * chunks * pages->Hkv >= 2147483647.0)
+    const cxa::PagedBatch batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
+    if (!cxa::weights_countable(batch, pages->page_shift, pages->Hkv, Hq / pages->Hkv, dtype == CXA_BF16))
       return fail(CXA_EINVAL, w + ": the chunks of keys of all tiles of query rows (see cxa.h) must be below 2^31");
     std::string msg;
     cxa::DeviceInfo dev;
@@ -313,7 +312,7 @@ int cxa_paged_weights(const cxa_pages* pages, int layer, int B, int n_tokens, in
     a.decay = decay;
     a.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(pages->dh));
     a.bf16 = dtype == CXA_BF16;
-    a.batch = {q_start, kv_len, page_table, B, n_tokens, max_pages};
+    a.batch = batch;
     a.layer = layer_of(pages, layer);
     a.workspace = workspace;
     a.workspace_bytes = workspace_bytes;

@@ -1,6 +1,7 @@
 // Dispatch of the gathered attention weights, and what is decided by sizes.
 #include <algorithm>
 
+#include "paged_work.cuh"
 #include "weights.cuh"
 
 namespace cxa {
@@ -55,6 +56,11 @@ WeightsWorkspace weights_workspace(int B, int n_tokens, int width, int page_shif
   const double scores = s.chunks * static_cast<double>(score_chunk_bytes(s.few_rows));
   const bool fit = scores <= static_cast<double>(kMaxScoreBytes);
   return {fixed + (fit ? static_cast<size_t>(scores) : 0), fixed + (fit ? static_cast<size_t>(scores) : kMaxScoreBytes)};
+}
+
+bool weights_countable(const PagedBatch& bt, int page_shift, int Hkv, int G, bool bf16) {
+  return on_tiles(G, bf16) ? work_bound(bt, page_shift, Hkv, G, 2 * (128 / G * G), 7) < kCountLimit
+                           : work_bound(bt, page_shift, Hkv, G, 32, 6) < kCountLimit;
 }
 
 cudaError_t launch_weights(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg) {

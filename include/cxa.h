@@ -496,8 +496,11 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  *              the scores are kept if what there is beyond the least size, 256 MB of it at most, holds them, and
  *              K is read twice otherwise (the weights then differ by their rounding).
  *              cxa_paged_weights_room_bytes() is the size with all the room that a call makes use of.
+ * Work is counted in 31 bits: with G = Hq / Hkv, t = max_pages * page_size, and r = 2 * (128 / G * G) rows (128 / G
+ * rounded down) and k = 128 keys for CXA_BF16 and G <= 128, r = 32 and k = 64 otherwise,
+ * Hkv * (B + n_tokens * G / r) * (t / k + 1) must be below 2^31.
  * Pages that two sequences of the batch share must not be given: their entries would be written by
- * both. Arguments, the limit on the work and errors otherwise as for cxa_paged_attention; dtype is
+ * both. Arguments and errors otherwise as for cxa_paged_attention; dtype is
  * the pool's. A token that sees an infinity or a NaN in q or K may make the weights of all keys that
  * it sees NaN. A sequence with more than max_new new tokens may be left out, its entries as they were; if it is,
  * cxa_device_status reports CXA_EINVAL. Results do not change from call to call.

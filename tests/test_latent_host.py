@@ -2,11 +2,15 @@
 the checks of batches. No GPU is needed: every call here returns before any CUDA call, and the device
 pointers handed over are never dereferenced."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
 from encoder_decoder_speech_gb300 import cxa
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x7f0000000000          # 256-byte aligned, never dereferenced
 BIG = 1 << 40
 
@@ -285,3 +289,29 @@ def test_room_for_scores(pages):
     assert room(pages, 64, 64, 1, 1 << 16, 8) == least(pages, 64, 64, 1, 1 << 16, 8) + (256 << 20)
     assert room(pages, 1, 2000, 2000, 1 << 16, 8) == least(pages, 1, 2000, 2000, 1 << 16, 8)      # no sequence of few rows
     assert room(pages, 1, 1, 1, 3, 6) == 0 and room(None, 1, 1, 1, 3, 8) == 0
+
+
+def test_weights_of_calls_that_can_be_numbered_are_not_refused():
+    """65,536 tokens of 4 heads a K/V head, 8 K/V heads, over a table of 2^20 positions: 1,025 tiles of 256 rows a head,
+    8,193 chunks each, in bf16. In a process that sees no GPU, where a call that passes every check ends with CXA_ECUDA."""
+    code = """if True:
+        from encoder_decoder_speech_gb300 import cxa
+        rc, p = cxa.cxa_pages_create(1 << 46, 1 << 47, 5000, 256, 1, 8, 64, {t})
+        assert rc == cxa.CXA_OK
+        rc = cxa.cxa_paged_weights(p, 0, {B}, {n}, {m}, 1 << 40, 1 << 40, 1 << 40, {w}, 1 << 45, 2048, 32, 1 << 48, 1.0, 0.0,
+                                   {t}, 1 << 40, 1 << 40, 0)
+        print(rc, cxa.cxa_last_error_message())
+    """
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+
+    def call(**kw):
+        a = dict(dict(t=cxa.CXA_BF16, B=1, n=65536, m=65536, w=4096), **kw)
+        r = subprocess.run([sys.executable, "-c", code.format(**a)], env=env, cwd=ROOT, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        return r.stdout
+
+    for kw in (dict(), dict(t=cxa.CXA_F32), dict(B=1000, m=1), dict(n=1 << 20, m=100, w=4096)):
+        assert call(**kw).startswith(str(cxa.CXA_ECUDA)), kw
+    for kw in (dict(B=1 << 15), dict(n=1 << 18, t=cxa.CXA_F32), dict(n=1 << 22, m=100)):
+        out = call(**kw)
+        assert out.startswith(str(cxa.CXA_EINVAL)) and "below 2^31" in out, kw
