@@ -6,10 +6,11 @@
 // histograms added up over distributed shared memory, find the keep-th largest; one more writes the
 // positions above it, and of those equal to it the first ones. (A block an item, which read the weights anew in
 // each pass: 225 us for 32 lists of 65536; a cluster 29, of which the first reads of the weights take 5 to 10, the
-// passes 3 each.) Items of up to 4096 positions take one block, those of up to 16384 four. evict_copy_kernel copies the listed rows of K, V and weights, a block 32 of them
-// (rows looked up and read two or four at a time by a thread: slower, 83 and 89 us).
+// passes 3 each.) Items of up to 4096 positions take one block, those of up to 16384 four. evict_copy_kernel
+// copies the listed rows of K, V and weights, a block 32 of them (rows looked up and read two or four at a time by
+// a thread: slower, 83 and 89 us).
 // Bound by memory: weights are read once, what stays is read and written once. 4 sequences of up to 65536 keys of
-// 8 heads of 128 down to 8192, bf16: 79.7 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
+// 8 heads of 128 down to 8192, bf16: 79 us, 44 of them the copy at 6.2 TB/s; six layers of 16 windows
 // of 448 keys down to 112: 18.9 us, latency of the two kernels.
 #include <algorithm>
 

@@ -27,7 +27,8 @@
 // Bound by the products, 2 latent operations a value; the values written (2 bytes each) take nearly as long. 32768
 // positions, 20 heads of 128, 512 + 64 channels: 109 us, 1180 TFLOP/s and 3.5 TB/s (main loop alone 67 at
 // cuBLAS's rate; without the stores 85). 24 sequences of up to 1500 positions, 8 heads of 64, 256 + 32: 24 us, of
-// which the floor of bytes is 9.5: start, and two or three products a pair.
+// which the floor of bytes is 9.5: start (barriers, tensor memory and maps are set up behind the wait for the kernel
+// before), and 408 products over 76 pairs, so that pairs with six set the end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 

@@ -3,12 +3,12 @@
 //   out[r] = sum_j p_rj c_j / sum_j p_rj,  p_rj = 2^(s_rj - m_r),  s_rj = scale log2(e) q_r . [c_j | r_j]
 //
 // for 16 query rows (tokens times heads) of a sequence at a time, each key's row read once for all of
-// them, in one pass with the running reference m_r. fp32 has no tensor-core product of its precision,
-// and 16 rows of 2 latent + rope products a key are what binds: 17,400 of them for 512 + 64 channels,
-// 136 clocks of an SM, against 98 for reading the key's 2304 bytes. 5 tokens in each of 16 sequences of up to 1500
-// keys, 8 heads, 128 + 32 channels: 32 us with the merge, of which the products alone take 4: a block has five steps,
-// each a chain of three barriers, behind the start and before the merge. 16 tokens of 20 heads over up to 4000 keys of
-// 512 + 64: 99 us, 18 TFLOP/s.
+// them, in one pass with the running reference m_r. (Products of three bf16 parts on the tensor cores, as the
+// few-rows kernel of the K/V pages has them, have not been tried here.) On the CUDA cores the 16 rows of 2 latent +
+// rope products a key are what binds: 17,400 of them for 512 + 64 channels, 136 clocks of an SM, against 98 for reading the key's 2304 bytes. 5 tokens in each of 16 sequences of up to 1500
+// keys, 8 heads, 128 + 32 channels: 32 us with the merge, of which the products alone take 4: a block has at most four
+// steps, each a chain of three barriers, and 46 % of the issue slots are taken (fragments, exchanges and masks beside
+// the products). 16 tokens of 20 heads over up to 4000 keys of 512 + 64: 100 us, 14.8 TFLOP/s.
 //
 // A step is 32 keys, copied into shared memory a step ahead (cp.async). Scores: a warp has four keys
 // in registers, a 32nd of the channels in each lane, and takes a row of q after the other from shared

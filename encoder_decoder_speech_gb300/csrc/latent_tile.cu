@@ -14,7 +14,7 @@
 //    rotated part took a unit: 84 us for 64 heads over 262,144 keys, 72 so.) It also copies an item's
 //    queries, where tokens' rows stand one behind the other (the softmax warps do, otherwise).
 //  * warps 4 and 5 issue the products, one the scores, as units come, the other P.V: each waits for what it
-//    needs alone (one warp for both, scores first: 112 us for 64 single tokens over 287,000 keys of 20 heads).
+//    needs alone (one warp for both, scores first: 112 us for 64 single tokens over 276,698 keys of 20 heads).
 //  * warps 0 to 3 do the softmax, 16 keys each; a thread has two keys and a quarter of the rows. A row's
 //    reference m moves, and O^T is rescaled, only when a score passes it by more than 2^8 (agreed on by one barrier a
 //    step). Sums stay in each thread and meet at an item's end.

@@ -249,8 +249,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank)
                : "memory");
 }
 
-// The same without a release: for an arrival that hands over nothing in memory (tensor memory that has
-// been read, say). A release at cluster scope waits until this thread's earlier global stores are performed.
+// The same without a release: for an arrival that hands over nothing in memory. A release at cluster scope waits
+// until this thread's earlier global stores are performed. Tensor memory that has been read may be handed back so:
+// its order does not rest on the memory model but on tcgen05.wait::ld (the loads have returned their values) and
+// tcgen05.fence::before_thread_sync before the arrival, and tcgen05.fence::after_thread_sync behind the wait for it.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, rank))
                : "memory");

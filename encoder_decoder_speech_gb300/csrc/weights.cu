@@ -12,7 +12,7 @@ constexpr double kSplitChunks = 8192;
 
 // A tile of 128 rows holds whole tokens, so G query heads have to fit into it.
 bool on_tiles(int G, bool bf16) { return bf16 && G <= 128; }
-// (16 single tokens over up to 4000 keys of 8 heads of 64 in fp32: 194 us the way of many rows, 27 this.)
+// (16 single tokens over up to 4000 keys of 8 heads of 64 in fp32: 194 us the way of many rows, 31 this.)
 bool few_in_fp32(int G, int max_new, bool bf16) { return !bf16 && static_cast<long long>(G) * max_new <= kFewRows16; }
 
 }  // namespace
@@ -20,7 +20,7 @@ bool few_in_fp32(int G, int max_new, bool bf16) { return !bf16 && static_cast<lo
 // All have few rows, where no sequence can have more than a product's 16; otherwise those of one or two
 // tokens (more would take room for scores that hardly any use), if their scores can be kept, there is more than
 // one sequence, and the keys are many enough to pay for two more launches. (20 single tokens beside 4 chunks of a
-// prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 237 so; 5 tokens in each of 16 sequences of
+// prompt, up to 8191 keys of 20 heads each: 534 us all with the many, 236 so; 5 tokens in each of 16 sequences of
 // up to 1500 keys of 8 heads: 39 us and 45.) Whether the keys are enough goes by the table's width: where they are not,
 // in a wide table, the launches cost 13 us (24 sequences, 300 tokens, up to 500 keys: 35 us and 48). Asked of
 // the device, the kernels that then find nothing to do cost more: 52 us, and 248 in place of 241 where they have.

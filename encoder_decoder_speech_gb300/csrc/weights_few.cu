@@ -6,8 +6,8 @@
 // weights_few_rows_kernel is bound by reading K: chunks of 128 keys come by cp.async two ahead, a thread takes
 // one key's row from shared memory and the rows' queries as broadcasts, up to four rows at a time (always four:
 // 2 us and 19 more of the two calls below), and stores the scores (4 bytes a row and key, against 4 dh bytes
-// of the key itself). 16 single tokens over up to 4000 keys of 8 heads of 64: 27 us; 32 over up to 8000 keys of 8 heads
-// of 128: 121 us, 4.5 TB/s.
+// of the key itself). 16 single tokens over up to 4000 keys of 8 heads of 64: 31 us; 32 over up to 8000 keys of 8 heads
+// of 128: 122 us, 4.5 TB/s.
 // weights_add_kernel reads them back, mostly from L2, and adds the weights to W.
 #include "ptx.cuh"
 #include "weights_few.cuh"

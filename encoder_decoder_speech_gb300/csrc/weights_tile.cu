@@ -10,7 +10,7 @@
 //                        over all tiles of 128 query rows that see them. A thread adds up its own key's weights,
 //                        so that every W is written once and in one order.
 // Both are bound by the exponentials, 32 a clock of an SM: 512 clocks for 128 x 128 scores, against 256 (64
-// channels) or 512 (128) for their product. 2048 tokens over 8192 keys of 20 heads of 64: 145 us, the exponential
+// channels) or 512 (128) for their product. 2048 tokens over 8192 keys of 20 heads of 64: 144 us, the exponential
 // units busy 44 and 41 % of the two passes: two warps a scheduler do not cover each other's waits and reads of
 // tensor memory (registers alone: 82 %). Tried: a second warp for the products and 16 softmax warps, no gain; 64
 // columns at a time with the next ones on their way, 183 us; sums with a reference that seldom moves, 170 us.
@@ -21,7 +21,7 @@
 //                        references and sums of its own until the item's end, and stores the scores (4 bytes a row
 //                        and key, against 2 dh bytes of the key itself).
 //   weights_add_kernel   (weights_few.cu) reads the scores back and adds the weights to W.
-// 64 single tokens, 32 heads on 8 of 128, over 287,000 keys: 124 us, 104 of them the first at 5.7 TB/s.
+// 64 single tokens, 32 heads on 8 of 128, over 282,119 keys: 124 us, 104 of them the first at 5.7 TB/s.
 // Where the scores have no room, the second pass is weights_sum_kernel, which reads K once more (ScoreRule).
 //
 // Products of bf16 values are exact; sums, references and weights are fp32.
