@@ -68,8 +68,8 @@ struct WeightsLaunch {
 struct WeightsWorkspace {
   size_t least, most;
 };
-WeightsWorkspace weights_workspace(int B, int n_tokens, int width, int page_shift, int Hq, int Hkv, int max_new,
-                                   bool bf16);
+WeightsWorkspace weights_workspace(int B, int n_tokens, int width, int page_shift, int num_pages, int Hq, int Hkv,
+                                   int max_new, bool bf16);
 // Whether the work of all its kernels can be numbered in 31 bits.
 bool weights_countable(const PagedBatch& bt, int page_shift, int Hkv, int G, bool bf16);
 cudaError_t launch_weights(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t stream, std::string* msg);

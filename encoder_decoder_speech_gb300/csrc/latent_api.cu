@@ -64,7 +64,7 @@ cxa::WeightsWorkspace weights_workspace_of(const cxa_pages* pages, int B, int n_
       static_cast<long long>(max_pages) << pages->page_shift > (1LL << 30) || Hq < 1 || Hq > 65535 ||
       Hq % pages->Hkv != 0)
     return {0, 0};
-  return cxa::weights_workspace(B, n_tokens, max_pages, pages->page_shift, Hq, pages->Hkv, max_new,
+  return cxa::weights_workspace(B, n_tokens, max_pages, pages->page_shift, pages->num_pages, Hq, pages->Hkv, max_new,
                                 pages->dtype == CXA_BF16);
 }
 

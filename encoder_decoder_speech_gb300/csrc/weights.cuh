@@ -30,6 +30,10 @@ struct ScoreRule {
 
 // Chunks of 128 keys that a call can have, as far as the host knows, and the bytes of a chunk's scores.
 constexpr size_t kMaxScoreBytes = 256u << 20;      // that are kept at most
+// (sequences of a batch share no page, so that the pool bounds them too; against that, chunks are counted all the same)
+inline double weights_pool_chunks(int B, int num_pages, int page_shift, int Hkv) {
+  return static_cast<double>(Hkv) * (((static_cast<long long>(num_pages) << page_shift) + 127) / 128 + B);
+}
 inline double weights_chunks(int B, int width, int page_shift, int Hkv) {
   return static_cast<double>(B) * Hkv * ((static_cast<long long>(width) << page_shift >> 7) + 1);
 }
@@ -62,8 +66,9 @@ struct WeightsSplit {
   int few_rows;       // 0: none do
   bool many;          // whether there can be others
   double chunks;      // that the call can have
+  size_t most;        // bytes of scores that it makes use of
 };
-WeightsSplit weights_split(int B, int width, int page_shift, int Hkv, int G, int max_new);
+WeightsSplit weights_split(int B, int width, int page_shift, int num_pages, int Hkv, int G, int max_new);
 ScoreRule score_rule(const WeightsSplit& s, const WeightsPlaces& at);
 
 // fp32, sequences of at most 16 query rows a K/V head (weights_few.cu).

@@ -234,7 +234,8 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.layer = a.layer;
   p.shape.G = a.Hq / a.layer.Hkv;
   p.rule = score_rule(
-      weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, p.shape.G, a.max_new), at);
+      weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.num_pages, a.layer.Hkv, p.shape.G, a.max_new),
+      at);
   p.shape.rows = kScoreRows;
   p.shape.chunk_shift = kFewChunkShift;
   p.shape.coarse = false;

@@ -868,7 +868,7 @@ cudaError_t launch(const WeightsLaunch& a, const DeviceInfo& dev, cudaStream_t s
   p.ref = at.ref;
   p.part = at.part;
   p.scores = at.scores;
-  WeightsSplit split = weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.Hkv, G, a.max_new);
+  WeightsSplit split = weights_split(a.batch.B, a.batch.width, a.layer.page_shift, a.layer.num_pages, a.layer.Hkv, G, a.max_new);
   p.rule = score_rule(split, at);
   if (split.many && !p.rule.kept && !p.rule.ask) split.few_rows = 0;      // (no room at all)
   p.status = dev.status_word;

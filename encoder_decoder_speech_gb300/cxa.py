@@ -1055,7 +1055,7 @@ class PagedCache(_Paged):
         had gathered before counts decay times, and new tokens' entries start at zero. No page may be two
         sequences' of the batch. max_new and workspace as for attend, but a sequence with more new tokens
         than max_new may be left out (cxa_device_status then says CXA_EINVAL). The kept workspace has room for the scores
-        of single tokens, 256 MB of them at most, as far as the table may need it; one of the caller's needs
+        of single tokens, 256 MB of them at most, as far as the table and the pool may need it; one of the caller's needs
         cxa_paged_weights_workspace_bytes, and without that room keys are read twice. Returns weights."""
         tc = _torch_calls or _calls()
         at, dh, dt = self._at, self.dh, q.dtype

@@ -493,9 +493,9 @@ CXA_API int cxa_paged_attention(const cxa_pages* pages, int layer, int B, int n_
  *              CXA_PAGED_COUNTER_BYTES are the same counters). Sequences of few new tokens leave their scores in it,
  *              4 bytes for each key (in chunks of 128), K/V head and query row: the least size has room for them if
  *              a table of that width can need 256 MB at most. In wider tables what a call needs goes by its keys:
- *              the scores are kept if what there is beyond the least size, 256 MB of it at most, holds them, and
- *              K is read twice otherwise (the weights then differ by their rounding).
- *              cxa_paged_weights_room_bytes() is the size with all the room that a call makes use of.
+ *              the scores are kept if what there is beyond the least size holds them, and K is read twice
+ *              otherwise (the weights then differ by their rounding). cxa_paged_weights_room_bytes() is the size
+ *              with all the room that a call makes use of: for as many keys as the pool has, 256 MB at most.
  * Work is counted in 31 bits: with G = Hq / Hkv, t = max_pages * page_size, and r = 2 * (128 / G * G) rows (128 / G
  * rounded down) and k = 128 keys for CXA_BF16 and G <= 128, r = 32 and k = 64 otherwise,
  * Hkv * (B + n_tokens * G / r) * (t / k + 1) must be below 2^31.

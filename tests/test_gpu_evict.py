@@ -702,3 +702,16 @@ def test_scores_that_a_workspace_has_room_for_or_not(pool, n, more):
         b.accumulate(workspace=ws[:size])
         b.close(before, b.W)
         assert bool((ws[size:] == 255).all())
+
+
+@pytest.mark.parametrize("Hq, Hkv", [(8, 2), (5, 1), (12, 1), (16, 1), (20, 1)])
+def test_single_tokens_beside_prompts_in_a_large_pool(Hq, Hkv):
+    """A table and a pool that can hold so many keys that sequences of few query rows go a way of their own."""
+    b = Batch([1, 70, 2, 0, 1, 3, 40], [70000, 300, 66000, 100, 1, 9000, 40], 256, Hq, Hkv, 64, "bf16", seed=Hq,
+              spare=(1 << 20) // 256 // Hkv).fill()
+    b.d["page_table"] = torch.cat([b.table, torch.full((7, 2000), -1, dtype=torch.int32)], 1).cuda()
+    before = b.W.clone()
+    first = b.accumulate().clone()
+    b.close(before, first)
+    b.W.copy_(before)
+    assert torch.equal(b.accumulate(), first)

@@ -286,7 +286,11 @@ def test_room_for_scores(pages):
     """The least workspace has room for the scores of tables that can need 256 MB; in wider ones room is the caller's."""
     least, room = cxa.cxa_paged_weights_workspace_bytes, cxa.cxa_paged_weights_room_bytes
     assert room(pages, 2, 2, 1, 80, 8) == least(pages, 2, 2, 1, 80, 8)
-    assert room(pages, 64, 64, 1, 1 << 16, 8) == least(pages, 64, 64, 1, 1 << 16, 8) + (256 << 20)
+    # (160 positions of the pool, in 64 sequences: 66 chunks of 128 keys a head)
+    assert room(pages, 64, 64, 1, 1 << 16, 8) == least(pages, 64, 64, 1, 1 << 16, 8) + 66 * 4 * 2 * 512
+    big = make_pages(num_pages=1 << 24)[1]
+    assert room(big, 64, 64, 1, 1 << 16, 8) == least(big, 64, 64, 1, 1 << 16, 8) + (256 << 20)
+    cxa.cxa_pages_destroy(big)
     assert room(pages, 1, 2000, 2000, 1 << 16, 8) == least(pages, 1, 2000, 2000, 1 << 16, 8)      # no sequence of few rows
     assert room(pages, 1, 1, 1, 3, 6) == 0 and room(None, 1, 1, 1, 3, 8) == 0
 
